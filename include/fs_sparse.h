@@ -69,10 +69,13 @@ extern "C" {
 #define FS_MAX_RANKS 1024    /* virtual ranks = shards, W */
 #define FS_MAX_TABLES 8
 #define FS_MAX_UIH 65535
+#define FS_MAX_TOKEN_DIM 65536 /* columns of a token embedding */
+#define FS_MAX_HEADS 1024      /* query heads of a jagged attention */
 
 /* enums */
 #define FS_F32 0
 #define FS_BF16 1
+#define FS_F16 2 /* token embedding and jagged attention only */
 #define FS_SGD 0
 #define FS_RW_ADAGRAD 1
 #define FS_ALL (-1)
@@ -437,6 +440,134 @@ int fs_grad_reduce_update_noalloc(const fs_table* tables, int32_t T, int32_t W,
                                   const uint8_t* cls, int32_t which, int32_t rows,
                                   int32_t optim, float lr, float eps, float* const* reduced_out,
                                   hipStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Token embedding -- a vocabulary's table looked up by token, without the   */
+/* batch's balancing, sharding and dedup: the lookup with scaling and an     */
+/* output type of its own, the tokens sorted by row, and the gradient of the */
+/* whole table by the sorted tokens (for any optimizer). Element types are   */
+/* FS_F32, FS_BF16 and FS_F16, dim is 1 .. FS_MAX_TOKEN_DIM.                 */
+/*                                                                          */
+/* fs_token_lookup: out[i][d] = round(scale * w[ids[i]][d]), the product in  */
+/* fp32 and rounded once more (to nearest even) to the output's type.        */
+/*  table    host, one table: weights, rows, dim, dtype and stride are read; */
+/*           weights and stride need only be aligned to an element (fastest   */
+/*           where rows and stride are multiples of 16 bytes).               */
+/*  ids      device [n]; an ID outside [0, rows) gives a row of zeros and    */
+/*           flags FS_EF_ID_RANGE.                                           */
+/*  out      device [n][dim] of out_dtype, rows out_stride bytes apart       */
+/*           (0: dense); not aliasing the table.                             */
+/*  err      sticky flags (may be NULL).                                     */
+int fs_token_lookup(const fs_table* table, const int64_t* ids, int64_t n, float scale, void* out,
+                    int32_t out_dtype, int64_t out_stride, int32_t* err, hipStream_t stream);
+
+/* fs_token_sort: the tokens grouped by row, rows ascending, each row's       */
+/* tokens in their order. The padding ID's tokens take no part; IDs outside  */
+/* [0, rows) neither, and flag FS_EF_ID_RANGE.                               */
+/*  padding_id  an ID without a gradient; outside [0, rows) (e.g. -1): none  */
+/*              inside, and its tokens are dropped without a flag.           */
+/*  unique .. occ_uid, counts: as fs_unique_collision_split writes them for  */
+/*              one table and W = 1 (capacities n, seg_offsets n + 1,        */
+/*              unique_offsets 2, counts 4), so fs_grad_reduce_update and    */
+/*              fs_jagged_lookup take them with T = W = 1; item k of that    */
+/*              batch is token k. Entries past the last row and the last     */
+/*              token (seg_offsets[U]) are unspecified.                      */
+/*  rows < 2^32 - 1; n < 2^31.                                               */
+int fs_token_sort(const int64_t* ids, int64_t n, int64_t rows, int64_t padding_id,
+                  int64_t* unique, int64_t* unique_offsets, int32_t* seg_offsets, int32_t* occ_bm,
+                  int32_t* occ_uid, int64_t* counts, int32_t* err, void* ws, size_t ws_bytes,
+                  hipStream_t stream);
+
+size_t fs_token_sort_workspace_size(int64_t n);
+
+/* fs_token_grad: grad[v][d] = round(scale * the sum of dout[i][d] over the  */
+/* tokens i of row v), summed in 64 bits; with accumulate the sum is added   */
+/* to what grad[v][d] holds before the one rounding. Equal calls give equal   */
+/* bits.                                                                    */
+/*  unique .. occ_uid  fs_token_sort's outputs (W = 1), or a dedup call's of  */
+/*           one table and W shards. n: their capacity.                      */
+/*  dout     device [n][dim] of dout_dtype, rows dout_stride bytes apart     */
+/*           (0: dense), indexed by occ_bm. Rows of dropped tokens are not   */
+/*           read.                                                           */
+/*  grad     device [rows][dim] of grad_dtype, rows grad_stride bytes apart. */
+/*  accumulate  0: every row is written, zeros where a row has no token;     */
+/*           else only rows with tokens are read and written.                */
+int fs_token_grad(const int64_t* unique, const int64_t* unique_offsets, int32_t W,
+                  const int32_t* seg_offsets, const int32_t* occ_bm, const int32_t* occ_uid,
+                  int64_t n, const void* dout, int32_t dout_dtype, int64_t dout_stride,
+                  float scale, int64_t rows, int32_t dim, void* grad, int32_t grad_dtype,
+                  int64_t grad_stride, int32_t accumulate, void* ws, size_t ws_bytes,
+                  hipStream_t stream);
+
+size_t fs_token_grad_workspace_size(int64_t n, int32_t dim);
+
+/* ------------------------------------------------------------------------ */
+/* Jagged attention -- the operator between the batch-major rows a lookup    */
+/* writes and the batch-major gradients an update reads. Sample s owns the   */
+/* tokens [offsets[s], offsets[s+1]) (e.g. fs_bucketize_permute's            */
+/* bal_offsets); its last n_cand[s] tokens are candidates, the ones before   */
+/* them its history of h tokens. Token i of the sample sees token j of it    */
+/*   where valid_i and valid_j and                                          */
+/*         ((j < h and (j <= i or not causal)) or j == i):                   */
+/* a candidate sees the history and itself. With S_ij = scale q_i . k_j over  */
+/* the tokens j that i sees,                                                 */
+/*   lse_i = log(sum_j exp S_ij),  P_ij = exp(S_ij - lse_i),                 */
+/*   out_i = sum_j P_ij v_j;  a token that sees nothing has out 0, lse -inf. */
+/* The backward call recomputes P; with D_i = dout_i . out_i and              */
+/*   dS_ij = P_ij (dout_i . v_j - D_i):                                      */
+/*   dq_i = scale sum_j dS_ij k_j, dk_j = scale sum_i dS_ij q_i,             */
+/*   dv_j = sum_i P_ij dout_i,                                               */
+/* dk and dv summed over the query heads of the key head. Scores, statistics */
+/* and sums are fp32; P and dS are rounded to the inputs' type before the    */
+/* products that sum them (half a step each, as the outputs), and equal      */
+/* calls give equal bits.                                                    */
+/*  q, out, dout, dq  host: [n_tok][heads][dim] arrays of dtype (FS_BF16 or  */
+/*           FS_F16, else FS_ERR_UNSUPPORTED); k, v, dk, dv: kv_heads heads. */
+/*           Strides in bytes, multiples of 16, data 16-byte aligned; 0:     */
+/*           dense. q, k and v may be views of one projection's output.      */
+/*           heads is a multiple of kv_heads, query heads h group .. h group */
+/*           + group - 1 share key head h. heads <= FS_MAX_HEADS; dim a      */
+/*           multiple of 8 up to 128 (else FS_ERR_UNSUPPORTED).              */
+/*  offsets  device [n+1], rising inside [0, n_tok], else FS_EF_SHAPE is     */
+/*           flagged and nothing is computed. Tokens of no sample (behind the */
+/*           last one) are neither read nor written.                         */
+/*  n_cand   device int32 [n], or NULL: no candidates. Values outside        */
+/*           [0, length] are clamped and flag FS_EF_SHAPE.                   */
+/*  valid    device uint8 [n_tok], 0: the token takes no part (its rows are  */
+/*           not read, its out, dq, dk and dv are zeros, its lse -inf); NULL: */
+/*           all are valid.                                                  */
+/*  lse      device fp32 [heads][n_tok]: written by the forward call, read by */
+/*           the backward call, as is out.                                   */
+/*  ws, ws_bytes  at least the workspace query's bytes, else FS_ERR_WORKSPACE. */
+/* A NaN or an infinity in a valid token's rows may reach every row of its    */
+/* sample, also those that do not see it (0 times NaN in a sum of products), */
+/* and none of another sample. scale is finite, of any sign.                 */
+/* Outputs must not alias inputs or each other. n <= FS_MAX_SAMPLES,         */
+/* n_tok < 2^31 - 1.                                                         */
+typedef struct fs_heads {
+  void* data;
+  int64_t token_stride; /* bytes between tokens; 0: heads * dim elements */
+  int64_t head_stride;  /* bytes between heads; 0: dim elements */
+} fs_heads;
+
+int fs_jagged_attention(const fs_heads* q, const fs_heads* k, const fs_heads* v,
+                        const int64_t* offsets, int32_t n, int64_t n_tok, const int32_t* n_cand,
+                        const uint8_t* valid, int32_t heads, int32_t kv_heads, int32_t dim,
+                        int32_t dtype, int32_t causal, float scale, const fs_heads* out,
+                        float* lse, int32_t* err, void* ws, size_t ws_bytes, hipStream_t stream);
+
+size_t fs_jagged_attention_workspace_size(int64_t n_tok, int32_t n);
+
+int fs_jagged_attention_backward(const fs_heads* q, const fs_heads* k, const fs_heads* v,
+                                 const fs_heads* out, const float* lse, const fs_heads* dout,
+                                 const int64_t* offsets, int32_t n, int64_t n_tok,
+                                 const int32_t* n_cand, const uint8_t* valid, int32_t heads,
+                                 int32_t kv_heads, int32_t dim, int32_t dtype, int32_t causal,
+                                 float scale, const fs_heads* dq, const fs_heads* dk,
+                                 const fs_heads* dv, int32_t* err, void* ws, size_t ws_bytes,
+                                 hipStream_t stream);
+
+size_t fs_jagged_attention_backward_workspace_size(int64_t n_tok, int32_t n, int32_t heads);
 
 /* ------------------------------------------------------------------------ */
 const char* fs_strerror(int code);

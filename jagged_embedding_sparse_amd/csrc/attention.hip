@@ -1,0 +1,267 @@
+// Jagged softmax attention, forward, and the tile table both directions use.
+//
+// Sample s owns the tokens [offsets[s], offsets[s+1]); its last n_cand[s] are
+// candidates. With S = scale q k^T over the keys a row sees,
+//   out = softmax(S) v,   lse = log(sum exp S).
+// The scores are never written: a workgroup holds 32 query rows per wave and
+// passes over the keys once, in tiles of 64, with the running maximum m and
+// sum l of each row (base 2):
+//   m' = max(m, max S),  l = l 2^(m - m') + sum 2^(S - m'),  O = O 2^(m - m') + 2^(S - m') v.
+#include <cmath>
+
+#include "attention.hpp"
+
+namespace fs {
+namespace attn {
+namespace {
+
+constexpr int kTableThreads = 1024;
+
+// One workgroup: counts each sample's tiles and writes one descriptor per
+// tile, samples in order. Offsets that do not rise inside [0, n_tok] would let
+// samples overlap (and outgrow the table): then there are no tiles.
+__global__ void __launch_bounds__(kTableThreads)
+k_attn_tiles(const int64_t* __restrict__ offsets, int32_t n, int64_t n_tok,
+             const int32_t* __restrict__ n_cand, int32_t rows, Tile* __restrict__ tiles,
+             int32_t* __restrict__ n_tiles, int32_t* __restrict__ err) {
+  __shared__ int32_t tmp[17];
+  int32_t base = 0;
+  bool bad = false, order = true;
+  for (int32_t s = threadIdx.x; s < n; s += kTableThreads)
+    order &= offsets[s] >= 0 && offsets[s] <= offsets[s + 1] && offsets[s + 1] <= n_tok;
+  if (__syncthreads_or(!order)) {
+    flag_err(err, !order, FS_EF_SHAPE);
+    if (threadIdx.x == 0) *n_tiles = 0;
+    return;
+  }
+  for (int32_t s0 = 0; s0 < n; s0 += kTableThreads) {  // uniform
+    const int32_t s = s0 + threadIdx.x;
+    int32_t lo = 0, len = 0, cand = 0;
+    if (s < n) {
+      lo = (int32_t)offsets[s];
+      len = (int32_t)(offsets[s + 1] - lo);
+      cand = n_cand ? n_cand[s] : 0;
+      bad |= cand < 0 || cand > len;
+      cand = min(max(cand, 0), len);
+    }
+    const int32_t cnt = (int32_t)cdiv(len, rows);
+    int32_t total;
+    const int32_t at = base + block_excl_scan<int32_t>(cnt, tmp, &total);
+    for (int32_t k = 0; k < cnt; ++k) tiles[at + k] = Tile{lo, len, len - cand, k * rows};
+    base += total;
+  }
+  flag_err(err, bad, FS_EF_SHAPE);
+  if (threadIdx.x == 0) *n_tiles = base;
+}
+
+struct FwdArgs {
+  Shape s;
+  View q, k, v, o;
+  float* lse;
+};
+
+constexpr int kKeys = 64;  // keys per step
+
+template <typename T, int DP, int NW>
+__global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
+  constexpr int NT = NW * kWave;
+  __shared__ uint16_t sk[2][kKeys * DP], sv[2][kKeys * DP];
+  if ((int32_t)blockIdx.x >= *a.s.n_tiles) return;
+  const Tile t = a.s.tiles[blockIdx.x];
+  const int head = blockIdx.y, kvh = head / a.s.group;
+  const char* kp = a.k.p + kvh * a.k.head;
+  const char* vp = a.v.p + kvh * a.v.head;
+  const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
+  const int t1 = min(t.t0 + 32 * NW, t.len);  // the workgroup's rows: [t0, t1)
+  const int i0 = t.t0 + 32 * w, i = i0 + (l & 31);
+  const bool on = live_row(a.s, t, i);
+  const bool causal = a.s.causal != 0;
+
+  u32x4 qf[DP / 16];
+  load_scaled_columns<DP>(qf, a.q.p + head * a.q.head, a.q.tok, a.s, t, i, on);
+  f32x16 o[DP / 32];
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d) o[d] = zero16();
+  // finite, so that a row that sees nothing keeps 2^(-inf - m) = 0
+  float m = -1e30f, sum = 0.f;
+  const float c = log2_scale(a.s);
+
+  // key tiles: the history, then the workgroup's own candidates
+  const int hist_end = (int)cdiv(causal ? min(t.hist, t1) : t.hist, kKeys);
+  const int own_lo = max(hist_end, max(t.t0, t.hist) / kKeys);
+  const int own_end = t1 > t.hist ? (int)cdiv(t1, kKeys) : 0;
+  const int steps = hist_end + max(0, own_end - own_lo);
+  auto key0 = [&](int step) { return (step < hist_end ? step : own_lo + step - hist_end) * kKeys; };
+
+  Staged<DP, kKeys, NT> ks, vs;
+  if (steps > 0) {
+    ks.load(kp, a.k.tok, a.s, t, key0(0));
+    vs.load(vp, a.v.tok, a.s, t, key0(0));
+  }
+  for (int step = 0; step < steps; ++step) {
+    const int j0 = key0(step), b = step & 1;
+    ks.store(sk[b]);
+    vs.store(sv[b]);
+    __syncthreads();
+    if (step + 1 < steps) {
+      ks.load(kp, a.k.tok, a.s, t, key0(step + 1));
+      vs.load(vp, a.v.tok, a.s, t, key0(step + 1));
+    }
+    // tiles that none of this wave's rows sees
+    const bool past = causal ? j0 > i0 + 31 : j0 >= t.hist;
+    if (i0 >= t1 || (past && (j0 > i0 + 31 || j0 + kKeys <= i0))) continue;
+    const uint64_t keys = live_rows(a.s, t, j0);
+    const bool whole = keys == ~0ull && j0 + kKeys <= t.hist && (!causal || j0 + kKeys <= i0 + 1);
+    f32x16 s[2];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      s[kb] = zero16();
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk)
+        s[kb] = Elem<T>::mfma(rows_operand<DP>(sk[b], 32 * kb, kk), qf[kk], s[kb]);
+    }
+    if (!whole || !__all(on)) {
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        uint32_t see = on ? seen_keys(i, j0 + 32 * kb, t.hist, causal) & (uint32_t)(keys >> (32 * kb))
+                          : 0u;
+        see >>= 4 * g;
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (!((see >> (8 * (x >> 2) + (x & 3))) & 1u)) s[kb][x] = -INFINITY;
+      }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) top = fmaxf(top, s[kb][x]);
+    top = fmaxf(max_halves(top) * c, m);
+    if (__any(top > m)) {
+      const float f = __builtin_amdgcn_exp2f(m - top);
+      m = top;
+      sum *= f;
+#pragma unroll
+      for (int d = 0; d < DP / 32; ++d) o[d] *= f;
+    }
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        s[kb][x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][x], c, -m));
+        sum += s[kb][x];
+      }
+    // probabilities are rounded to the operand's type (half a step each)
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        const u32x4 p = to_operand<T>(s[kb], ch);
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+          o[d] = Elem<T>::mfma(cols_operand<DP>(sv[b], 32 * kb + 16 * ch, 32 * d), p, o[d]);
+      }
+  }
+  if (i >= t.len) return;
+  sum = add_halves(sum);
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a sum that is NaN stays NaN
+  char* op = a.o.p + head * a.o.head + ((int64_t)t.lo + i) * a.o.tok;
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int col = 32 * d + 8 * x + 4 * g;
+      if (col < a.s.dim) {
+        u32x2 v;
+        v[0] = Elem<T>::pack(o[d][4 * x] * inv, o[d][4 * x + 1] * inv);
+        v[1] = Elem<T>::pack(o[d][4 * x + 2] * inv, o[d][4 * x + 3] * inv);
+        *(u32x2*)(op + 2 * col) = v;
+      }
+    }
+  if (g == 0)
+    a.lse[(int64_t)head * a.s.n_tok + t.lo + i] =
+        sum == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * kLn2;
+}
+
+template <typename T>
+void launch_fwd(const FwdArgs& a, dim3 grid, hipStream_t stream) {
+  constexpr int NW = 4;
+  if (a.s.dim <= 32)
+    hipLaunchKernelGGL((k_attn_fwd<T, 32, NW>), grid, dim3(NW * kWave), 0, stream, a);
+  else if (a.s.dim <= 64)
+    hipLaunchKernelGGL((k_attn_fwd<T, 64, NW>), grid, dim3(NW * kWave), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_attn_fwd<T, 128, NW>), grid, dim3(NW * kWave), 0, stream, a);
+}
+
+}  // namespace
+
+int make_view(const fs_heads* x, int32_t heads, int32_t dim, View* v) {
+  if (!x) return FS_ERR_INVALID_ARG;
+  const int64_t row = (int64_t)dim * 2;
+  v->p = (char*)x->data;
+  v->head = x->head_stride ? x->head_stride : row;
+  v->tok = x->token_stride ? x->token_stride : row * heads;
+  if (v->head < 0 || v->tok < 0 || (v->head & 15) || (v->tok & 15) || ((uintptr_t)v->p & 15))
+    return FS_ERR_INVALID_ARG;
+  if (v->tok < row || (heads > 1 && v->head < row)) return FS_ERR_INVALID_ARG;
+  return FS_OK;
+}
+
+int launch_tiles(const int64_t* offsets, int32_t n, int64_t n_tok, const int32_t* n_cand,
+                 int32_t rows, Tile* tiles, int32_t* n_tiles, int32_t* err, hipStream_t stream) {
+  hipLaunchKernelGGL(k_attn_tiles, dim3(1), dim3(kTableThreads), 0, stream, offsets, n, n_tok,
+                     n_cand, rows, tiles, n_tiles, err);
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
+}  // namespace attn
+}  // namespace fs
+
+using namespace fs;
+using namespace fs::attn;
+
+extern "C" size_t fs_jagged_attention_workspace_size(int64_t n_tok, int32_t n) {
+  if (n_tok < 0 || n < 0) return 0;
+  Carve c(nullptr);
+  c.take<int32_t>(1);
+  c.take<Tile>((size_t)tile_cap(n_tok, n, 32));
+  return c.used + 256;
+}
+
+extern "C" int fs_jagged_attention(const fs_heads* q, const fs_heads* k, const fs_heads* v,
+                                   const int64_t* offsets, int32_t n, int64_t n_tok,
+                                   const int32_t* n_cand, const uint8_t* valid, int32_t heads,
+                                   int32_t kv_heads, int32_t dim, int32_t dtype, int32_t causal,
+                                   float scale, const fs_heads* out, float* lse, int32_t* err,
+                                   void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (n < 0 || n > FS_MAX_SAMPLES || n_tok < 0 || n_tok >= (int64_t)INT32_MAX || heads < 1 ||
+      kv_heads < 1 || heads % kv_heads || !offsets || !std::isfinite(scale))
+    return FS_ERR_INVALID_ARG;
+  if (!type_ok(dtype) || dim < 8 || dim > 128 || dim % 8 || heads > FS_MAX_HEADS)
+    return FS_ERR_UNSUPPORTED;
+  FwdArgs a;
+  int rc;
+  if ((rc = make_view(q, heads, dim, &a.q)) || (rc = make_view(k, kv_heads, dim, &a.k)) ||
+      (rc = make_view(v, kv_heads, dim, &a.v)) || (rc = make_view(out, heads, dim, &a.o)))
+    return rc;
+  if (n_tok > 0 && n > 0 && (!a.q.p || !a.k.p || !a.v.p || !a.o.p || !lse))
+    return FS_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < fs_jagged_attention_workspace_size(n_tok, n)) return FS_ERR_WORKSPACE;
+  if (n == 0 || n_tok == 0) return FS_OK;
+  constexpr int32_t rows = 128;
+  Carve c(ws);
+  int32_t* n_tiles = c.take<int32_t>(1);
+  Tile* tiles = c.take<Tile>((size_t)tile_cap(n_tok, n, rows));
+  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, rows, tiles, n_tiles, err, stream))) return rc;
+  a.s = Shape{tiles, n_tiles, valid, n_tok, heads / kv_heads, dim, causal, scale};
+  a.lse = lse;
+  const dim3 grid((unsigned)tile_cap(n_tok, n, rows), (unsigned)heads);
+  if (dtype == FS_BF16)
+    launch_fwd<__bf16>(a, grid, stream);
+  else
+    launch_fwd<_Float16>(a, grid, stream);
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}

@@ -1,0 +1,276 @@
+// Tiles, masks and matrix-core fragments shared by the jagged attention's
+// forward and backward kernels.
+//
+// Fragments of v_mfma_f32_32x32x16 (lane = 32 g + c, g in {0, 1}):
+//   A  row c,    k = 8 g + e,  e = 0..7      (16 bytes of one row)
+//   B  column c, k = 8 g + e
+//   C  column c, row 8 (i / 4) + 4 g + i % 4, i = 0..15
+// A product's C holds, for a fixed column, rows 4 g .. 4 g + 3 of every
+// group of 8. Read as the B operand of a second product over those rows,
+// accumulators 8 s .. 8 s + 7 are k-slots of chunk s in the order
+//   k-slot (g, e)  <->  row 16 s + 8 (e / 4) + 4 g + e % 4,
+// and the sum over k does not care about the order as long as A uses the same.
+// So probabilities go from the first product's accumulators to the second
+// product's operand by rounding alone, with no shared memory and no shuffles,
+// and A is read from a row-major tile with the transposing 8-byte LDS read
+// (16 lanes read 4 rows x 16 columns, lane c receives column c's 4 rows).
+#pragma once
+
+#include "common.hpp"
+
+namespace fs {
+namespace attn {
+
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 8 elements of either type travel as four 32-bit registers.
+template <typename T>
+struct Elem;
+template <>
+struct Elem<__bf16> {
+  static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {  // to nearest even
+    const f32x2 v = {x, y};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
+  }
+  static __device__ __forceinline__ f32x2 unpack(uint32_t u) {
+    return __builtin_convertvector(__builtin_bit_cast(bf16x2, u), f32x2);
+  }
+};
+template <>
+struct Elem<_Float16> {
+  static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  }
+  static __device__ __forceinline__ uint32_t pack(float x, float y) {
+    const f32x2 v = {x, y};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2));
+  }
+  static __device__ __forceinline__ f32x2 unpack(uint32_t u) {
+    return __builtin_convertvector(__builtin_bit_cast(f16x2, u), f32x2);
+  }
+};
+
+__device__ __forceinline__ f32x16 zero16() {
+  f32x16 z;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) z[i] = 0.f;
+  return z;
+}
+
+// accumulators 8 s .. 8 s + 7 as the B operand of chunk s
+template <typename T>
+__device__ __forceinline__ u32x4 to_operand(const f32x16& x, int s) {
+  u32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = Elem<T>::pack(x[8 * s + 2 * e], x[8 * s + 2 * e + 1]);
+  return r;
+}
+
+// the two lanes that hold one column's rows (c and c + 32): both get both
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float add_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false,
+                                                  false);
+  return __uint_as_float(r[0]) + __uint_as_float(r[1]);
+}
+
+// ---------------------------------------------------------------- LDS tiles
+// A tile of rows of DP elements (2 bytes each; DP = 32, 64 or 128) without
+// padding. The 16-byte pieces of a row are permuted by the row so that both
+// reads below touch every bank equally often: piece p of row r lies at
+// p ^ swz(r). Rows of 128 bytes or more start at the same bank, so the eight
+// rows r..r+7 take eight different pieces; the lowest row bit goes to the
+// piece's highest, which puts two of four neighbouring rows into each half of
+// the banks (the transposing read takes four neighbouring rows at a time).
+// 64-byte rows alternate between the two halves by themselves.
+template <int DP>
+__device__ __forceinline__ int swz(int r) {
+  if constexpr (DP == 32) return (r >> 1) & 3;
+  return ((r & 1) << 2) | ((r >> 1) & 3);
+}
+
+// piece p (8 elements) of row r, as an element offset
+template <int DP>
+__device__ __forceinline__ int piece(int r, int p) {
+  return r * DP + ((p ^ swz<DP>(r)) << 3);
+}
+
+// A operand: rows r0 .. r0 + 31, elements 16 kk .. 16 kk + 15
+template <int DP>
+__device__ __forceinline__ u32x4 rows_operand(const uint16_t* tile, int r0, int kk) {
+  const int l = lane();
+  return *(const u32x4*)(tile + piece<DP>(r0 + (l & 31), 2 * kk + (l >> 5)));
+}
+
+// A operand of the transposed tile: its rows are the tile's columns
+// c0 .. c0 + 31, its k-slots the tile's rows r0 .. r0 + 15 in the order of
+// to_operand
+template <int DP>
+__device__ __forceinline__ u32x4 cols_operand(const uint16_t* tile, int r0, int c0) {
+  const int l = lane(), g = l >> 5, j = l & 15;
+  const int col = c0 + (l & 16) + 4 * (j & 3);
+  const int row = r0 + 4 * g + (j >> 2);
+  const uint16_t* a = tile + piece<DP>(row, col >> 3) + (col & 7);
+  const uint16_t* b = tile + piece<DP>(row + 8, col >> 3) + (col & 7);
+  const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a));
+  const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)b));
+  return u32x4{lo[0], lo[1], hi[0], hi[1]};
+}
+
+// ---------------------------------------------------------------- samples
+// One tile of rows of one sample: rows t0 .. of the sample whose tokens start
+// at lo; len tokens, of which the first hist are history.
+struct Tile {
+  int32_t lo, len, hist, t0;
+};
+
+// A [n_tok, heads, D] array: bytes between tokens and between heads
+struct View {
+  char* p;
+  int64_t tok, head;
+};
+
+struct Shape {
+  const Tile* tiles;
+  const int32_t* n_tiles;
+  const uint8_t* valid;  // nullable
+  int64_t n_tok;
+  int32_t group;         // query heads per key head
+  int32_t dim;           // elements of a head, at most DP
+  int32_t causal;
+  float scale;           // of the scores
+};
+
+// bits of the rows r0 .. r0 + 63 of a sample that exist and are valid
+__device__ __forceinline__ uint64_t live_rows(const Shape& a, const Tile& t, int r0) {
+  const int r = r0 + lane();
+  bool on = r >= 0 && r < t.len;
+  if (a.valid != nullptr && on) on = a.valid[(int64_t)t.lo + r] != 0;
+  return __ballot(on);
+}
+
+__device__ __forceinline__ bool live_row(const Shape& a, const Tile& t, int r) {
+  if (r >= t.len) return false;
+  return a.valid == nullptr || a.valid[(int64_t)t.lo + r] != 0;
+}
+
+// the lowest n bits (n may lie outside 0..32)
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? ~0u : ((1u << n) - 1u));
+}
+__device__ __forceinline__ uint32_t one_bit(int n) { return n >= 0 && n < 32 ? 1u << n : 0u; }
+
+// keys j0 .. j0 + 31 that row i sees: the history, up to itself where causal,
+// and itself
+__device__ __forceinline__ uint32_t seen_keys(int i, int j0, int hist, bool causal) {
+  const int lim = causal ? min(hist, i + 1) : hist;
+  return low_bits(lim - j0) | one_bit(i - j0);
+}
+// rows i0 .. i0 + 31 that see key j
+__device__ __forceinline__ uint32_t seeing_rows(int j, int i0, int hist, bool causal) {
+  const uint32_t self = one_bit(j - i0);
+  if (j >= hist) return self;
+  return causal ? ~low_bits(j - i0) : ~0u;
+}
+
+// 16 bytes of row r of one head, elements 8 p .. 8 p + 7; zeros past the
+// head's width and for rows that do not exist or are not valid, so that what
+// lies there (NaN among it) never meets a product
+__device__ __forceinline__ u32x4 load_piece(const char* head, int64_t tok_bytes, const Shape& a,
+                                            const Tile& t, int r, int p, bool on) {
+  u32x4 v = {0, 0, 0, 0};
+  if (on && 8 * p < a.dim) v = *(const u32x4*)(head + ((int64_t)t.lo + r) * tok_bytes + 16 * p);
+  return v;
+}
+
+// A tile of ROWS rows on its way from memory to LDS, NT threads: load() fills
+// registers, store() writes them to LDS.
+template <int DP, int ROWS, int NT>
+struct Staged {
+  static constexpr int kPieces = DP / 8;
+  static constexpr int kPer = ROWS * kPieces / NT;
+  static_assert(kPer >= 1 && ROWS * kPieces % NT == 0, "whole pieces per thread");
+  u32x4 v[kPer];
+
+  __device__ __forceinline__ void load(const char* head, int64_t tok_bytes, const Shape& a,
+                                       const Tile& t, int r0) {
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int id = x * NT + threadIdx.x;
+      const int r = r0 + id / kPieces;
+      v[x] = load_piece(head, tok_bytes, a, t, r, id % kPieces, live_row(a, t, r));
+    }
+  }
+  __device__ __forceinline__ void store(uint16_t* tile) const {
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int id = x * NT + threadIdx.x;
+      *(u32x4*)(tile + piece<DP>(id / kPieces, id % kPieces)) = v[x];
+    }
+  }
+};
+
+// B operands of 32 rows of one head: column c = row r0 + c
+template <int DP>
+__device__ __forceinline__ void load_columns(u32x4 (&f)[DP / 16], const char* head,
+                                             int64_t tok_bytes, const Shape& a, const Tile& t,
+                                             int r, bool on) {
+#pragma unroll
+  for (int kk = 0; kk < DP / 16; ++kk)
+    f[kk] = load_piece(head, tok_bytes, a, t, r, 2 * kk + (lane() >> 5), on);
+}
+
+// The kernels scale scores by a positive number (a maximum may be scaled
+// after it is taken, and a masked score stays -inf). The sign of `scale` goes
+// into one operand of S, and a scale of 0 makes that operand zero.
+template <int DP>
+__device__ __forceinline__ void load_scaled_columns(u32x4 (&f)[DP / 16], const char* head,
+                                                    int64_t tok_bytes, const Shape& a,
+                                                    const Tile& t, int r, bool on) {
+  load_columns<DP>(f, head, tok_bytes, a, t, r, on && a.scale != 0.f);
+  if (a.scale < 0.f) {
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) f[kk] ^= 0x80008000u;
+  }
+}
+__device__ __forceinline__ float log2_scale(const Shape& a) {
+  return a.scale == 0.f ? 1.f : fabsf(a.scale) * kLog2e;
+}
+
+// ---------------------------------------------------------------- host side
+__host__ inline bool type_ok(int32_t dtype) { return dtype == FS_BF16 || dtype == FS_F16; }
+
+// tiles of `rows` rows that n samples of n_tok tokens can need
+__host__ inline int64_t tile_cap(int64_t n_tok, int32_t n, int32_t rows) { return n_tok / rows + n; }
+
+// checks of one argument array; dense strides filled in
+__host__ int make_view(const fs_heads* x, int32_t heads, int32_t dim, View* v);
+
+// Launches the tile table of `rows`-row tiles (see attention.hip).
+int launch_tiles(const int64_t* offsets, int32_t n, int64_t n_tok, const int32_t* n_cand,
+                 int32_t rows, Tile* tiles, int32_t* n_tiles, int32_t* err, hipStream_t stream);
+
+}  // namespace attn
+}  // namespace fs

@@ -1,0 +1,331 @@
+// Jagged softmax attention, backward. The probabilities are recomputed from
+// the forward pass's log-sum-exp:
+//   P = exp(S - lse),  delta_i = sum_d dO_id O_id,  dP = dO v^T,
+//   dS = P (dP - delta),  dV = P^T dO,  dQ = scale dS k,  dK = scale dS^T q.
+//
+// Two kernels, because dQ sums over keys and dK, dV over rows: each keeps its
+// sums in registers and recomputes S and dP (7 products instead of the least
+// 5), so no sum crosses workgroups, nothing is added atomically and equal
+// calls give equal bits. The first writes delta for the second.
+#include <cmath>
+
+#include "attention.hpp"
+
+namespace fs {
+namespace attn {
+namespace {
+
+constexpr int kStep = 64;  // rows or keys per step
+
+struct BwdArgs {
+  Shape s;
+  View q, k, v, o, d_o, dq, dk, dv;
+  const float* lse;  // [heads][n_tok]
+  float* delta;      // [heads][n_tok]
+};
+
+// 32 columns x DP rows of sums to one row of memory per lane, scaled
+template <typename T, int DP>
+__device__ __forceinline__ void store_rows(char* row, const f32x16 (&x)[DP / 32], int dim,
+                                           float f) {
+  const int g = lane() >> 5;
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int col = 32 * d + 8 * y + 4 * g;
+      if (col < dim) {
+        u32x2 v;
+        v[0] = Elem<T>::pack(x[d][4 * y] * f, x[d][4 * y + 1] * f);
+        v[1] = Elem<T>::pack(x[d][4 * y + 2] * f, x[d][4 * y + 3] * f);
+        *(u32x2*)(row + 2 * col) = v;
+      }
+    }
+}
+
+// dQ: 32 rows per wave, keys in steps. S^T = k q^T and dP^T = v dO^T have one
+// row per lane, so lse and delta are one register each and dS^T is the operand
+// of dQ^T = k^T dS^T.
+template <typename T, int DP, int NW>
+__global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
+  constexpr int NT = NW * kWave;
+  __shared__ uint16_t sk[2][kStep * DP], sv[2][kStep * DP];
+  if ((int32_t)blockIdx.x >= *a.s.n_tiles) return;
+  const Tile t = a.s.tiles[blockIdx.x];
+  const int head = blockIdx.y, kvh = head / a.s.group;
+  const char* kp = a.k.p + kvh * a.k.head;
+  const char* vp = a.v.p + kvh * a.v.head;
+  const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
+  const int t1 = min(t.t0 + 32 * NW, t.len);
+  const int i0 = t.t0 + 32 * w, i = i0 + (l & 31);
+  const bool on = live_row(a.s, t, i);
+  const bool causal = a.s.causal != 0;
+
+  u32x4 qf[DP / 16], df[DP / 16];
+  load_scaled_columns<DP>(qf, a.q.p + head * a.q.head, a.q.tok, a.s, t, i, on);
+  load_columns<DP>(df, a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i, on);
+  // delta: each half of the wave holds half of a row's columns
+  float delta = 0.f;
+  {
+    const char* op = a.o.p + head * a.o.head;
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+      const u32x4 x = load_piece(op, a.o.tok, a.s, t, i, 2 * kk + g, on);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const f32x2 u = Elem<T>::unpack(x[e]), y = Elem<T>::unpack(df[kk][e]);
+        delta = __builtin_fmaf(u[0], y[0], delta);
+        delta = __builtin_fmaf(u[1], y[1], delta);
+      }
+    }
+    delta = add_halves(delta);
+  }
+  // a row that sees nothing has lse = -inf: 2^(S - inf) = 0
+  float lse = INFINITY;
+  if (i < t.len) {
+    const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
+    if (g == 0) a.delta[at] = delta;
+    if (on) lse = a.lse[at];
+    lse = lse == -INFINITY ? INFINITY : lse * kLog2e;
+  }
+  f32x16 dq[DP / 32];
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d) dq[d] = zero16();
+  const float c = log2_scale(a.s);
+
+  const int hist_end = (int)cdiv(causal ? min(t.hist, t1) : t.hist, kStep);
+  const int own_lo = max(hist_end, max(t.t0, t.hist) / kStep);
+  const int own_end = t1 > t.hist ? (int)cdiv(t1, kStep) : 0;
+  const int steps = hist_end + max(0, own_end - own_lo);
+  auto key0 = [&](int step) { return (step < hist_end ? step : own_lo + step - hist_end) * kStep; };
+
+  Staged<DP, kStep, NT> ks, vs;
+  if (steps > 0) {
+    ks.load(kp, a.k.tok, a.s, t, key0(0));
+    vs.load(vp, a.v.tok, a.s, t, key0(0));
+  }
+  for (int step = 0; step < steps; ++step) {
+    const int j0 = key0(step), b = step & 1;
+    ks.store(sk[b]);
+    vs.store(sv[b]);
+    __syncthreads();
+    if (step + 1 < steps) {
+      ks.load(kp, a.k.tok, a.s, t, key0(step + 1));
+      vs.load(vp, a.v.tok, a.s, t, key0(step + 1));
+    }
+    const bool past = causal ? j0 > i0 + 31 : j0 >= t.hist;
+    if (i0 >= t1 || (past && (j0 > i0 + 31 || j0 + kStep <= i0))) continue;
+    const uint64_t keys = live_rows(a.s, t, j0);
+    const bool whole = keys == ~0ull && j0 + kStep <= t.hist && (!causal || j0 + kStep <= i0 + 1) &&
+                       __all(on);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        s = Elem<T>::mfma(rows_operand<DP>(sk[b], 32 * kb, kk), qf[kk], s);
+        dp = Elem<T>::mfma(rows_operand<DP>(sv[b], 32 * kb, kk), df[kk], dp);
+      }
+      uint32_t see = ~0u;
+      if (!whole)
+        see = on ? seen_keys(i, j0 + 32 * kb, t.hist, causal) & (uint32_t)(keys >> (32 * kb)) : 0u;
+      see >>= 4 * g;
+#pragma unroll
+      for (int x = 0; x < 16; ++x) {
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], c, -lse));
+        s[x] = whole || ((see >> (8 * (x >> 2) + (x & 3))) & 1u) ? p * (dp[x] - delta) : 0.f;
+      }
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        const u32x4 ds = to_operand<T>(s, ch);
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+          dq[d] = Elem<T>::mfma(cols_operand<DP>(sk[b], 32 * kb + 16 * ch, 32 * d), ds, dq[d]);
+      }
+    }
+  }
+  if (i < t.len)
+    store_rows<T, DP>(a.dq.p + head * a.dq.head + ((int64_t)t.lo + i) * a.dq.tok, dq, a.s.dim,
+                      a.s.scale);
+}
+
+// dK and dV: 32 keys per wave, the rows of every query head of the key head
+// in steps. S = q k^T and dP = dO v^T have one key per lane, so P and dS are
+// the operands of dV^T = dO^T P and dK^T = q^T dS.
+template <typename T, int DP, int NW>
+__global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
+  constexpr int NT = NW * kWave;
+  __shared__ uint16_t sq[2][kStep * DP], sd[2][kStep * DP];
+  __shared__ __attribute__((aligned(16))) float s_lse[2][kStep], s_delta[2][kStep];
+  if ((int32_t)blockIdx.x >= *a.s.n_tiles) return;
+  const Tile t = a.s.tiles[blockIdx.x];
+  const int kvh = blockIdx.y;
+  const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
+  const int t1 = min(t.t0 + 32 * NW, t.len);
+  const int j0 = t.t0 + 32 * w, j = j0 + (l & 31);
+  const bool on = live_row(a.s, t, j);
+  const bool causal = a.s.causal != 0;
+
+  u32x4 kf[DP / 16], vf[DP / 16];
+  load_scaled_columns<DP>(kf, a.k.p + kvh * a.k.head, a.k.tok, a.s, t, j, on);
+  load_columns<DP>(vf, a.v.p + kvh * a.v.head, a.v.tok, a.s, t, j, on);
+  f32x16 dk[DP / 32], dv[DP / 32];
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = zero16();
+  const float c = log2_scale(a.s);
+
+  // rows that see a key of this tile: from the tile on where causal, all of
+  // them otherwise; only its own where it holds candidates alone
+  const bool own = t.t0 >= t.hist;
+  const int first = (own || causal ? t.t0 : 0) / kStep;
+  const int last = (int)cdiv(own ? t1 : t.len, kStep);
+  const int per = last - first, steps = per * a.s.group;
+
+  Staged<DP, kStep, NT> qs, ds;
+  float st_lse = INFINITY, st_delta = 0.f;  // threads 0 .. 63: one row each
+  auto load = [&](int step) {
+    const int head = kvh * a.s.group + step / per, i0 = (first + step % per) * kStep;
+    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
+    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
+    if (threadIdx.x < kStep) {
+      const int i = i0 + threadIdx.x;
+      st_lse = INFINITY;
+      st_delta = 0.f;
+      if (live_row(a.s, t, i)) {
+        const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
+        const float x = a.lse[at];
+        st_lse = x == -INFINITY ? INFINITY : x * kLog2e;
+        st_delta = a.delta[at];
+      }
+    }
+  };
+  if (steps > 0) load(0);
+  for (int step = 0; step < steps; ++step) {
+    const int i0 = (first + step % per) * kStep, b = step & 1;
+    qs.store(sq[b]);
+    ds.store(sd[b]);
+    if (threadIdx.x < kStep) {
+      s_lse[b][threadIdx.x] = st_lse;
+      s_delta[b][threadIdx.x] = st_delta;
+    }
+    __syncthreads();
+    if (step + 1 < steps) load(step + 1);
+    // steps whose rows see none of this wave's keys
+    if (j0 >= t1 || (causal && i0 + kStep <= j0)) continue;
+    if (j0 >= t.hist && (i0 + kStep <= j0 || i0 > j0 + 31)) continue;
+    const uint64_t rows = live_rows(a.s, t, i0);
+    const bool whole = rows == ~0ull && j0 + 32 <= t.hist && (!causal || i0 >= j0 + 31) && __all(on);
+#pragma unroll
+    for (int ib = 0; ib < 2; ++ib) {
+      f32x16 s = zero16(), dp = zero16();
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        s = Elem<T>::mfma(rows_operand<DP>(sq[b], 32 * ib, kk), kf[kk], s);
+        dp = Elem<T>::mfma(rows_operand<DP>(sd[b], 32 * ib, kk), vf[kk], dp);
+      }
+      uint32_t see = ~0u;
+      if (!whole)
+        see = on ? seeing_rows(j, i0 + 32 * ib, t.hist, causal) & (uint32_t)(rows >> (32 * ib)) : 0u;
+      see >>= 4 * g;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const f32x4 ls = *(const f32x4*)&s_lse[b][32 * ib + 8 * y + 4 * g];
+        const f32x4 de = *(const f32x4*)&s_delta[b][32 * ib + 8 * y + 4 * g];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int z = 4 * y + x;
+          const bool in = whole || ((see >> (8 * y + x)) & 1u);
+          const float p = in ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], c, -ls[x])) : 0.f;
+          s[z] = p;
+          dp[z] = in ? p * (dp[z] - de[x]) : 0.f;
+        }
+      }
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        const u32x4 pb = to_operand<T>(s, ch), db = to_operand<T>(dp, ch);
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d) {
+          dv[d] = Elem<T>::mfma(cols_operand<DP>(sd[b], 32 * ib + 16 * ch, 32 * d), pb, dv[d]);
+          dk[d] = Elem<T>::mfma(cols_operand<DP>(sq[b], 32 * ib + 16 * ch, 32 * d), db, dk[d]);
+        }
+      }
+    }
+  }
+  if (j >= t.len) return;
+  const int64_t tok = (int64_t)t.lo + j;
+  store_rows<T, DP>(a.dk.p + kvh * a.dk.head + tok * a.dk.tok, dk, a.s.dim, a.s.scale);
+  store_rows<T, DP>(a.dv.p + kvh * a.dv.head + tok * a.dv.tok, dv, a.s.dim, 1.f);
+}
+
+template <typename T, int DP>
+int launch_bwd(const BwdArgs& a, int32_t heads, int64_t cap, hipStream_t stream) {
+  constexpr int NW = 4;
+  hipLaunchKernelGGL((k_attn_dq<T, DP, NW>), dim3((unsigned)cap, (unsigned)heads),
+                     dim3(NW * kWave), 0, stream, a);
+  FS_LAUNCH_CHECK();
+  hipLaunchKernelGGL((k_attn_dkv<T, DP, NW>), dim3((unsigned)cap, (unsigned)(heads / a.s.group)),
+                     dim3(NW * kWave), 0, stream, a);
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
+template <typename T>
+int launch_bwd(const BwdArgs& a, int32_t heads, int64_t cap, hipStream_t stream) {
+  if (a.s.dim <= 32) return launch_bwd<T, 32>(a, heads, cap, stream);
+  if (a.s.dim <= 64) return launch_bwd<T, 64>(a, heads, cap, stream);
+  return launch_bwd<T, 128>(a, heads, cap, stream);
+}
+
+}  // namespace
+}  // namespace attn
+}  // namespace fs
+
+using namespace fs;
+using namespace fs::attn;
+
+extern "C" size_t fs_jagged_attention_backward_workspace_size(int64_t n_tok, int32_t n,
+                                                              int32_t heads) {
+  if (n_tok < 0 || n < 0 || heads < 0) return 0;
+  Carve c(nullptr);
+  c.take<int32_t>(1);
+  c.take<Tile>((size_t)tile_cap(n_tok, n, 32));
+  c.take<float>((size_t)heads * (size_t)n_tok);
+  return c.used + 256;
+}
+
+extern "C" int fs_jagged_attention_backward(
+    const fs_heads* q, const fs_heads* k, const fs_heads* v, const fs_heads* out,
+    const float* lse, const fs_heads* dout, const int64_t* offsets, int32_t n, int64_t n_tok,
+    const int32_t* n_cand, const uint8_t* valid, int32_t heads, int32_t kv_heads, int32_t dim,
+    int32_t dtype, int32_t causal, float scale, const fs_heads* dq, const fs_heads* dk,
+    const fs_heads* dv, int32_t* err, void* ws, size_t ws_bytes, hipStream_t stream) {
+  if (n < 0 || n > FS_MAX_SAMPLES || n_tok < 0 || n_tok >= (int64_t)INT32_MAX || heads < 1 ||
+      kv_heads < 1 || heads % kv_heads || !offsets || !std::isfinite(scale))
+    return FS_ERR_INVALID_ARG;
+  if (!type_ok(dtype) || dim < 8 || dim > 128 || dim % 8 || heads > FS_MAX_HEADS)
+    return FS_ERR_UNSUPPORTED;
+  BwdArgs a;
+  int rc;
+  if ((rc = make_view(q, heads, dim, &a.q)) || (rc = make_view(k, kv_heads, dim, &a.k)) ||
+      (rc = make_view(v, kv_heads, dim, &a.v)) || (rc = make_view(out, heads, dim, &a.o)) ||
+      (rc = make_view(dout, heads, dim, &a.d_o)) || (rc = make_view(dq, heads, dim, &a.dq)) ||
+      (rc = make_view(dk, kv_heads, dim, &a.dk)) || (rc = make_view(dv, kv_heads, dim, &a.dv)))
+    return rc;
+  if (n_tok > 0 && n > 0 &&
+      (!a.q.p || !a.k.p || !a.v.p || !a.o.p || !a.d_o.p || !a.dq.p || !a.dk.p || !a.dv.p || !lse))
+    return FS_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < fs_jagged_attention_backward_workspace_size(n_tok, n, heads))
+    return FS_ERR_WORKSPACE;
+  if (n == 0 || n_tok == 0) return FS_OK;
+  constexpr int32_t rows = 128;
+  Carve c(ws);
+  int32_t* n_tiles = c.take<int32_t>(1);
+  Tile* tiles = c.take<Tile>((size_t)tile_cap(n_tok, n, 32));
+  a.lse = lse;
+  a.delta = c.take<float>((size_t)heads * (size_t)n_tok);
+  const int64_t cap = tile_cap(n_tok, n, rows);
+  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, rows, tiles, n_tiles, err, stream))) return rc;
+  a.s = Shape{tiles, n_tiles, valid, n_tok, heads / kv_heads, dim, causal, scale};
+  return dtype == FS_BF16 ? launch_bwd<__bf16>(a, heads, cap, stream)
+                          : launch_bwd<_Float16>(a, heads, cap, stream);
+}

@@ -21,11 +21,12 @@ FS_OK, FS_ERR_INVALID_ARG, FS_ERR_WORKSPACE, FS_ERR_HIP, FS_ERR_UNSUPPORTED = 0,
 FS_ERR_TOO_LARGE = -5
 FS_NOALLOC_SCRATCH_BYTES = 64 << 20
 FS_EF_ID_RANGE, FS_EF_SHAPE, FS_EF_LEN_RANGE = 1, 2, 4
-FS_F32, FS_BF16 = 0, 1
+FS_F32, FS_BF16, FS_F16 = 0, 1, 2
 FS_SGD, FS_RW_ADAGRAD = 0, 1
 FS_ALL, FS_EXCLUSIVE, FS_COLLISION = -1, 0, 1
 FS_ROWS_FEW, FS_ROWS_MANY, FS_ROWS_ALL = 1, 2, 3
 FS_MAX_SAMPLES, FS_MAX_RANKS, FS_MAX_TABLES, FS_MAX_UIH = 16384, 1024, 8, 65535
+FS_MAX_TOKEN_DIM, FS_MAX_HEADS = 65536, 1024
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built: run `python __graft_entry__.py build` "
@@ -38,9 +39,13 @@ class FsTable(C.Structure):
                 ("state_stride", C.c_int64)]
 
 
+class FsHeads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("token_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
 _L = C.CDLL(LIB_PATH)
 _P, _i32, _i64, _sz, _f = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
-_TP = C.POINTER(FsTable)
+_TP, _HP = C.POINTER(FsTable), C.POINTER(FsHeads)
 
 
 def _sig(name, res, *args):
@@ -80,6 +85,20 @@ _c_reduce_ws = _sig("fs_grad_reduce_update_workspace_size", _sz, _i64, _i32, _i3
 _c_reduce_noalloc = _sig("fs_grad_reduce_update_noalloc", C.c_int, _TP, _i32, _i32,
                          C.POINTER(_P), _i64, _P, _P, _P, _P, _P, _P, _i32, _i32, _i32, _f, _f,
                          C.POINTER(_P), _P)
+_c_token_lookup = _sig("fs_token_lookup", C.c_int, _TP, _P, _i64, _f, _P, _i32, _i64, _P, _P)
+_c_token_sort = _sig("fs_token_sort", C.c_int, _P, _i64, _i64, _i64, _P, _P, _P, _P, _P, _P, _P,
+                     _P, _sz, _P)
+_c_token_sort_ws = _sig("fs_token_sort_workspace_size", _sz, _i64)
+_c_token_grad = _sig("fs_token_grad", C.c_int, _P, _P, _i32, _P, _P, _P, _i64, _P, _i32, _i64, _f,
+                     _i64, _i32, _P, _i32, _i64, _i32, _P, _sz, _P)
+_c_token_grad_ws = _sig("fs_token_grad_workspace_size", _sz, _i64, _i32)
+_c_attention = _sig("fs_jagged_attention", C.c_int, _HP, _HP, _HP, _P, _i32, _i64, _P, _P, _i32,
+                    _i32, _i32, _i32, _i32, _f, _HP, _P, _P, _P, _sz, _P)
+_c_attention_ws = _sig("fs_jagged_attention_workspace_size", _sz, _i64, _i32)
+_c_attention_bwd = _sig("fs_jagged_attention_backward", C.c_int, _HP, _HP, _HP, _HP, _P, _HP, _P,
+                        _i32, _i64, _P, _P, _i32, _i32, _i32, _i32, _i32, _f, _HP, _HP, _HP, _P,
+                        _P, _sz, _P)
+_c_attention_bwd_ws = _sig("fs_jagged_attention_backward_workspace_size", _sz, _i64, _i32, _i32)
 _c_strerror = _sig("fs_strerror", C.c_char_p, C.c_int)
 _c_version = _sig("fs_version", C.c_int)
 
@@ -90,7 +109,11 @@ EXPORTED = ["fs_balance_fbs", "fs_balance_vbs", "fs_balance_workspace_size",
             "fs_jagged_lookup", "fs_ranged_combine",
             "fs_keyed_transpose", "fs_keyed_transpose_workspace_size",
             "fs_grad_reduce_update", "fs_grad_reduce_update_noalloc",
-            "fs_grad_reduce_update_workspace_size", "fs_strerror", "fs_version"]
+            "fs_grad_reduce_update_workspace_size", "fs_token_lookup", "fs_token_sort",
+            "fs_token_sort_workspace_size", "fs_token_grad", "fs_token_grad_workspace_size",
+            "fs_jagged_attention", "fs_jagged_attention_workspace_size",
+            "fs_jagged_attention_backward", "fs_jagged_attention_backward_workspace_size",
+            "fs_strerror", "fs_version"]
 
 
 class FsError(RuntimeError):
@@ -459,6 +482,170 @@ def fs_grad_reduce_update_noalloc(weights, states, W, grads, n_tok, uq, optim, l
                              _ptr(cls) if which != FS_ALL else None, which, rows,
                              FS_RW_ADAGRAD if optim in ("rw_adagrad", FS_RW_ADAGRAD) else FS_SGD,
                              float(lr), float(eps), red, _stream(stream)))
+
+
+# ---------------------------------------------------------------------------- token embedding
+
+_DTYPES = {torch.float32: FS_F32, torch.bfloat16: FS_BF16, torch.float16: FS_F16}
+
+
+def _dtype(dt):
+    if dt not in _DTYPES:
+        raise FsError("dtype", FS_ERR_UNSUPPORTED)
+    return _DTYPES[dt]
+
+
+def fs_token_lookup(weight, ids, scale=1.0, dtype=None, out=None, err=None, stream=None):
+    """out[i] = scale * weight[ids[i]] in `dtype` (the table's by default):
+    weight [rows, dim] (fp32, bf16 or fp16, rows contiguous, any row stride),
+    ids int64 [n]. IDs outside the table give zeros and flag FS_EF_ID_RANGE."""
+    assert weight.dim() == 2 and ids.dtype == torch.int64
+    n, dim = ids.numel(), weight.shape[1]
+    if out is None:
+        out = torch.empty((n, dim), dtype=dtype or weight.dtype, device=_dev())
+    assert out.shape == (n, dim)
+    tab = FsTable()
+    tab.weights, tab.stride = _rows_ptr(weight)
+    tab.rows, tab.dim, tab.dtype = weight.shape[0], dim, _dtype(weight.dtype)
+    optr, ostride = _rows_ptr(out)
+    _check("fs_token_lookup",
+           _c_token_lookup(C.byref(tab), _ptr(ids), n, float(scale), optr, _dtype(out.dtype),
+                           ostride, _ptr(err), _stream(stream)))
+    return out
+
+
+def token_sort_workspace_size(n):
+    return int(_c_token_sort_ws(n))
+
+
+def fs_token_sort(ids, rows, padding_id=-1, out=None, err=None, ws=None, stream=None):
+    """ids: int64 [n]. Returns the tokens sorted by row as the dedup's outputs
+    of one table and W = 1 (unique, unique_offsets, seg_offsets, occ_bm,
+    occ_uid, counts): fs_token_grad, fs_grad_reduce_update and
+    fs_jagged_lookup take them."""
+    assert ids.dtype == torch.int64
+    d, n = _dev(), ids.numel()
+    cap = max(n, 1)
+    o = out or {}
+    uq = _get(o, "unique", lambda: torch.empty(cap, dtype=torch.int64, device=d))
+    uo = _get(o, "unique_offsets", lambda: torch.empty(2, dtype=torch.int64, device=d))
+    seg = _get(o, "seg_offsets", lambda: torch.empty(cap + 1, dtype=torch.int32, device=d))
+    bm = _get(o, "occ_bm", lambda: torch.empty(cap, dtype=torch.int32, device=d))
+    uid = _get(o, "occ_uid", lambda: torch.empty(cap, dtype=torch.int32, device=d))
+    counts = _get(o, "counts", lambda: torch.empty(4, dtype=torch.int64, device=d))
+    ws = _ws(token_sort_workspace_size(n), ws)
+    _check("fs_token_sort",
+           _c_token_sort(_ptr(ids), n, int(rows), int(padding_id), _ptr(uq), _ptr(uo), _ptr(seg),
+                         _ptr(bm), _ptr(uid), _ptr(counts), _ptr(err), _ptr(ws), ws.numel(),
+                         _stream(stream)))
+    return dict(unique=uq, unique_offsets=uo, seg_offsets=seg, occ_bm=bm, occ_uid=uid,
+                counts=counts)
+
+
+def token_grad_workspace_size(n, dim):
+    return int(_c_token_grad_ws(n, dim))
+
+
+def fs_token_grad(uq, dout, rows, scale=1.0, dtype=torch.float32, grad=None, accumulate=False,
+                  W=1, ws=None, stream=None):
+    """The table's gradient [rows, dim] in `dtype` from the tokens' gradients
+    dout [n, dim] and their sort `uq` (fs_token_sort's outputs, or a dedup's
+    of one table and W shards). With accumulate it is added to `grad`."""
+    assert dout.dim() == 2
+    n, dim = dout.shape
+    if grad is None:
+        assert not accumulate, "accumulate adds to a given grad"
+        grad = torch.empty((rows, dim), dtype=dtype, device=_dev())
+    assert grad.shape == (rows, dim)
+    ws = _ws(token_grad_workspace_size(n, dim), ws)
+    dptr, dstride = _rows_ptr(dout)
+    gptr, gstride = _rows_ptr(grad)
+    _check("fs_token_grad",
+           _c_token_grad(_ptr(uq["unique"]), _ptr(uq["unique_offsets"]), W,
+                         _ptr(uq["seg_offsets"]), _ptr(uq["occ_bm"]), _ptr(uq["occ_uid"]), n, dptr,
+                         _dtype(dout.dtype), dstride, float(scale), int(rows), dim, gptr,
+                         _dtype(grad.dtype), gstride, int(bool(accumulate)), _ptr(ws),
+                         ws.numel(), _stream(stream)))
+    return grad
+
+
+# ---------------------------------------------------------------------------- jagged attention
+
+
+def _heads_arg(t, shape, dtype):
+    """fs_heads of a [n_tok, heads, dim] tensor with contiguous rows (an axis
+    of one entry has no stride of its own: 0, dense)."""
+    assert t.is_cuda and t.dim() == 3 and t.shape == shape and t.dtype == dtype
+    assert t.stride(2) == 1, "a head's elements must be contiguous"
+    e = t.element_size()
+    return FsHeads(t.data_ptr(), t.stride(0) * e if shape[0] > 1 else 0,
+                   t.stride(1) * e if shape[1] > 1 else 0)
+
+
+def _attention_args(q, k, v, offsets, n_cand, valid, scale):
+    n_tok, heads, dim = q.shape
+    kv = (n_tok, k.shape[1], dim)
+    n = offsets.numel() - 1
+    assert offsets.dtype == torch.int64
+    assert n_cand is None or (n_cand.dtype == torch.int32 and n_cand.numel() == n)
+    assert valid is None or (valid.dtype in (torch.uint8, torch.bool) and valid.numel() == n_tok)
+    return (n_tok, heads, dim, kv, n, dim ** -0.5 if scale is None else float(scale),
+            [_heads_arg(q, q.shape, q.dtype), _heads_arg(k, kv, q.dtype),
+             _heads_arg(v, kv, q.dtype)])
+
+
+def attention_workspace_size(n_tok, n):
+    return int(_c_attention_ws(n_tok, n))
+
+
+def fs_jagged_attention(q, k, v, offsets, n_cand=None, valid=None, causal=True, scale=None,
+                        out=None, lse=None, err=None, ws=None, stream=None):
+    """Softmax attention inside every sample of a jagged batch: q [n_tok,
+    heads, dim], k and v [n_tok, kv_heads, dim] (bf16 or fp16, views allowed),
+    offsets int64 [n + 1], n_cand int32 [n] (candidates at each sample's end),
+    valid uint8 or bool [n_tok]. scale: 1 / sqrt(dim) by default. Returns out
+    like q (dense) and lse fp32 [heads, n_tok]; rows of tokens behind the last
+    sample are not written."""
+    n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale)
+    if out is None:
+        out = torch.empty((n_tok, heads, dim), dtype=q.dtype, device=_dev())
+    if lse is None:
+        lse = torch.empty((heads, n_tok), dtype=torch.float32, device=_dev())
+    assert lse.dtype == torch.float32 and lse.shape == (heads, n_tok)
+    ws = _ws(attention_workspace_size(n_tok, n), ws)
+    _check("fs_jagged_attention",
+           _c_attention(hs[0], hs[1], hs[2], _ptr(offsets), n, n_tok, _ptr(n_cand), _ptr(valid),
+                        heads, kv[1], dim, _dtype(q.dtype), int(bool(causal)), scale,
+                        _heads_arg(out, q.shape, q.dtype), _ptr(lse), _ptr(err), _ptr(ws),
+                        ws.numel(), _stream(stream)))
+    return out, lse
+
+
+def attention_backward_workspace_size(n_tok, n, heads):
+    return int(_c_attention_bwd_ws(n_tok, n, heads))
+
+
+def fs_jagged_attention_backward(q, k, v, out, lse, dout, offsets, n_cand=None, valid=None,
+                                 causal=True, scale=None, dq=None, dk=None, dv=None, err=None,
+                                 ws=None, stream=None):
+    """Gradients (dq, dk, dv) of fs_jagged_attention from its outputs out and
+    lse and the gradient dout of out; the other arguments are the forward
+    call's. Outputs may be views (e.g. of one projection's gradient)."""
+    n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale)
+    assert lse.dtype == torch.float32 and lse.shape == (heads, n_tok)
+    d = _dev()
+    dq = dq if dq is not None else torch.empty((n_tok, heads, dim), dtype=q.dtype, device=d)
+    dk = dk if dk is not None else torch.empty(kv, dtype=q.dtype, device=d)
+    dv = dv if dv is not None else torch.empty(kv, dtype=q.dtype, device=d)
+    ws = _ws(attention_backward_workspace_size(n_tok, n, heads), ws)
+    _check("fs_jagged_attention_backward",
+           _c_attention_bwd(hs[0], hs[1], hs[2], _heads_arg(out, q.shape, q.dtype), _ptr(lse),
+                            _heads_arg(dout, q.shape, q.dtype), _ptr(offsets), n, n_tok,
+                            _ptr(n_cand), _ptr(valid), heads, kv[1], dim, _dtype(q.dtype),
+                            int(bool(causal)), scale, _heads_arg(dq, q.shape, q.dtype),
+                            _heads_arg(dk, kv, q.dtype), _heads_arg(dv, kv, q.dtype), _ptr(err),
+                            _ptr(ws), ws.numel(), _stream(stream)))
+    return dq, dk, dv
 
 
 # ---------------------------------------------------------------------------- prepared calls
