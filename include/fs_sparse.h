@@ -524,7 +524,8 @@ size_t fs_token_grad_workspace_size(int64_t n, int32_t dim);
 /*  q, out, dout, dq  host: [n_tok][heads][dim] arrays of dtype (FS_BF16 or  */
 /*           FS_F16, else FS_ERR_UNSUPPORTED); k, v, dk, dv: kv_heads heads. */
 /*           Strides in bytes, multiples of 16, data 16-byte aligned; 0:     */
-/*           dense. q, k and v may be views of one projection's output.      */
+/*           dense; at most 2^26 between tokens (else FS_ERR_UNSUPPORTED).   */
+/*           q, k and v may be views of one projection's output.              */
 /*           heads is a multiple of kv_heads, query heads h group .. h group */
 /*           + group - 1 share key head h. heads <= FS_MAX_HEADS; dim a      */
 /*           multiple of 8 up to 128 (else FS_ERR_UNSUPPORTED).              */
@@ -533,9 +534,9 @@ size_t fs_token_grad_workspace_size(int64_t n, int32_t dim);
 /*           last one) are neither read nor written.                         */
 /*  n_cand   device int32 [n], or NULL: no candidates. Values outside        */
 /*           [0, length] are clamped and flag FS_EF_SHAPE.                   */
-/*  valid    device uint8 [n_tok], 0: the token takes no part (its rows are  */
-/*           not read, its out, dq, dk and dv are zeros, its lse -inf); NULL: */
-/*           all are valid.                                                  */
+/*  valid    device uint8 [n_tok], 0: the token takes no part (whatever its   */
+/*           rows hold, its out, dq, dk and dv are zeros, its lse -inf);      */
+/*           NULL: all are valid.                                            */
 /*  lse      device fp32 [heads][n_tok]: written by the forward call, read by */
 /*           the backward call, as is out.                                   */
 /*  ws, ws_bytes  at least the workspace query's bytes, else FS_ERR_WORKSPACE. */

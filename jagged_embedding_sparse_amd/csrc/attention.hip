@@ -16,17 +16,23 @@ namespace attn {
 namespace {
 
 constexpr int kTableThreads = 1024;
+constexpr int kBuckets = 256;
 
-// One workgroup: counts each sample's tiles and writes one descriptor per
-// tile, samples in order. Offsets that do not rise inside [0, n_tok] would let
+// One workgroup: one descriptor per tile of each sample, those with the most
+// steps first, so that the last ones to start are short and the workgroups
+// end together. A tile's steps are what a causal pass over rows t0 + rows - 1
+// and before, or t0 and after, takes (tile_by_end turns one into the other);
+// without causal every tile of a sample takes as many as its sample has.
+// Tiles with equally many (or kBuckets and more) come in any order, which
+// changes no result. Offsets that do not rise inside [0, n_tok] would let
 // samples overlap (and outgrow the table): then there are no tiles.
 __global__ void __launch_bounds__(kTableThreads)
 k_attn_tiles(const int64_t* __restrict__ offsets, int32_t n, int64_t n_tok,
-             const int32_t* __restrict__ n_cand, int32_t rows, Tile* __restrict__ tiles,
-             int32_t* __restrict__ n_tiles, int32_t* __restrict__ err) {
-  __shared__ int32_t tmp[17];
-  int32_t base = 0;
+             const int32_t* __restrict__ n_cand, int32_t rows, int32_t causal,
+             Tile* __restrict__ tiles, int32_t* __restrict__ n_tiles, int32_t* __restrict__ err) {
+  __shared__ int32_t first[kBuckets], tmp[17];
   bool bad = false, order = true;
+  if (threadIdx.x < kBuckets) first[threadIdx.x] = 0;
   for (int32_t s = threadIdx.x; s < n; s += kTableThreads)
     order &= offsets[s] >= 0 && offsets[s] <= offsets[s + 1] && offsets[s + 1] <= n_tok;
   if (__syncthreads_or(!order)) {
@@ -34,24 +40,31 @@ k_attn_tiles(const int64_t* __restrict__ offsets, int32_t n, int64_t n_tok,
     if (threadIdx.x == 0) *n_tiles = 0;
     return;
   }
-  for (int32_t s0 = 0; s0 < n; s0 += kTableThreads) {  // uniform
-    const int32_t s = s0 + threadIdx.x;
-    int32_t lo = 0, len = 0, cand = 0;
-    if (s < n) {
-      lo = (int32_t)offsets[s];
-      len = (int32_t)(offsets[s + 1] - lo);
-      cand = n_cand ? n_cand[s] : 0;
+  // pass 0 counts the tiles of each bucket, pass 1 places them
+  for (int pass = 0; pass < 2; ++pass) {
+    for (int32_t s = threadIdx.x; s < n; s += kTableThreads) {
+      const int32_t lo = (int32_t)offsets[s], len = (int32_t)(offsets[s + 1] - lo);
+      int32_t cand = n_cand ? n_cand[s] : 0;
       bad |= cand < 0 || cand > len;
       cand = min(max(cand, 0), len);
+      const int32_t cnt = (int32_t)cdiv(len, rows);
+      for (int32_t k = 0; k < cnt; ++k) {
+        const int32_t b = kBuckets - min(causal ? cnt - k : cnt, kBuckets);
+        const int32_t at = atomicAdd(&first[b], 1);
+        if (pass) tiles[at] = Tile{lo, len, len - cand, k * rows};
+      }
     }
-    const int32_t cnt = (int32_t)cdiv(len, rows);
-    int32_t total;
-    const int32_t at = base + block_excl_scan<int32_t>(cnt, tmp, &total);
-    for (int32_t k = 0; k < cnt; ++k) tiles[at + k] = Tile{lo, len, len - cand, k * rows};
-    base += total;
+    __syncthreads();
+    if (pass == 0) {
+      int32_t total;
+      const int32_t x = threadIdx.x < kBuckets ? first[threadIdx.x] : 0;
+      const int32_t ex = block_excl_scan<int32_t>(x, tmp, &total);
+      if (threadIdx.x < kBuckets) first[threadIdx.x] = ex;
+      if (threadIdx.x == 0) *n_tiles = total;
+      __syncthreads();
+    }
   }
   flag_err(err, bad, FS_EF_SHAPE);
-  if (threadIdx.x == 0) *n_tiles = base;
 }
 
 struct FwdArgs {
@@ -66,9 +79,10 @@ template <typename T, int DP, int NW>
 __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sk[2][kKeys * DP], sv[2][kKeys * DP];
-  if ((int32_t)blockIdx.x >= *a.s.n_tiles) return;
-  const Tile t = a.s.tiles[blockIdx.x];
-  const int head = blockIdx.y, kvh = head / a.s.group;
+  const int at = blockIdx.x / a.s.heads, head = blockIdx.x % a.s.heads;
+  if (at >= *a.s.n_tiles) return;
+  const Tile t = tile_by_end(a.s.tiles[at], 32 * NW);
+  const int kvh = head / a.s.group;
   const char* kp = a.k.p + kvh * a.k.head;
   const char* vp = a.v.p + kvh * a.v.head;
   const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
@@ -93,25 +107,33 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   const int steps = hist_end + max(0, own_end - own_lo);
   auto key0 = [&](int step) { return (step < hist_end ? step : own_lo + step - hist_end) * kKeys; };
 
-  Staged<DP, kKeys, NT> ks, vs;
+  Staged<DP, NT> ks, vs;
+  uint64_t keys = 0;
+  uint32_t ahead = 0;
+  bool full = false;
+  auto load = [&](int step) {
+    const int j = key0(step);
+    keys = live_bits(ahead);
+    full = keys == ~0ull && a.s.dim == DP;
+    ks.load(kp, a.k.tok, a.s, t, j, full);
+    vs.load(vp, a.v.tok, a.s, t, j, full);
+    if (step + 1 < steps) ahead = live_byte(a.s, t, key0(step + 1));
+  };
   if (steps > 0) {
-    ks.load(kp, a.k.tok, a.s, t, key0(0));
-    vs.load(vp, a.v.tok, a.s, t, key0(0));
+    ahead = live_byte(a.s, t, key0(0));
+    load(0);
   }
   for (int step = 0; step < steps; ++step) {
     const int j0 = key0(step), b = step & 1;
-    ks.store(sk[b]);
-    vs.store(sv[b]);
+    const uint64_t live = keys;
+    ks.store(sk[b], a.s, live, full);
+    vs.store(sv[b], a.s, live, full);
     __syncthreads();
-    if (step + 1 < steps) {
-      ks.load(kp, a.k.tok, a.s, t, key0(step + 1));
-      vs.load(vp, a.v.tok, a.s, t, key0(step + 1));
-    }
+    if (step + 1 < steps) load(step + 1);
     // tiles that none of this wave's rows sees
     const bool past = causal ? j0 > i0 + 31 : j0 >= t.hist;
     if (i0 >= t1 || (past && (j0 > i0 + 31 || j0 + kKeys <= i0))) continue;
-    const uint64_t keys = live_rows(a.s, t, j0);
-    const bool whole = keys == ~0ull && j0 + kKeys <= t.hist && (!causal || j0 + kKeys <= i0 + 1);
+    const bool whole = live == ~0ull && j0 + kKeys <= t.hist && (!causal || j0 + kKeys <= i0 + 1);
     f32x16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -123,7 +145,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
     if (!whole || !__all(on)) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        uint32_t see = on ? seen_keys(i, j0 + 32 * kb, t.hist, causal) & (uint32_t)(keys >> (32 * kb))
+        uint32_t see = on ? seen_keys(i, j0 + 32 * kb, t.hist, causal) & (uint32_t)(live >> (32 * kb))
                           : 0u;
         see >>= 4 * g;
 #pragma unroll
@@ -202,6 +224,7 @@ int make_view(const fs_heads* x, int32_t heads, int32_t dim, View* v) {
   v->p = (char*)x->data;
   v->head = x->head_stride ? x->head_stride : row;
   v->tok = x->token_stride ? x->token_stride : row * heads;
+  if (v->tok > kMaxStride || v->head > ((int64_t)1 << 40)) return FS_ERR_UNSUPPORTED;
   if (v->head < 0 || v->tok < 0 || (v->head & 15) || (v->tok & 15) || ((uintptr_t)v->p & 15))
     return FS_ERR_INVALID_ARG;
   if (v->tok < row || (heads > 1 && v->head < row)) return FS_ERR_INVALID_ARG;
@@ -209,9 +232,10 @@ int make_view(const fs_heads* x, int32_t heads, int32_t dim, View* v) {
 }
 
 int launch_tiles(const int64_t* offsets, int32_t n, int64_t n_tok, const int32_t* n_cand,
-                 int32_t rows, Tile* tiles, int32_t* n_tiles, int32_t* err, hipStream_t stream) {
+                 int32_t rows, int32_t causal, Tile* tiles, int32_t* n_tiles, int32_t* err,
+                 hipStream_t stream) {
   hipLaunchKernelGGL(k_attn_tiles, dim3(1), dim3(kTableThreads), 0, stream, offsets, n, n_tok,
-                     n_cand, rows, tiles, n_tiles, err);
+                     n_cand, rows, causal, tiles, n_tiles, err);
   FS_LAUNCH_CHECK();
   return FS_OK;
 }
@@ -251,13 +275,14 @@ extern "C" int fs_jagged_attention(const fs_heads* q, const fs_heads* k, const f
   if (!ws || ws_bytes < fs_jagged_attention_workspace_size(n_tok, n)) return FS_ERR_WORKSPACE;
   if (n == 0 || n_tok == 0) return FS_OK;
   constexpr int32_t rows = 128;
+  if (tile_cap(n_tok, n, rows) * heads >= (int64_t)INT32_MAX) return FS_ERR_UNSUPPORTED;
   Carve c(ws);
   int32_t* n_tiles = c.take<int32_t>(1);
   Tile* tiles = c.take<Tile>((size_t)tile_cap(n_tok, n, rows));
-  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, rows, tiles, n_tiles, err, stream))) return rc;
-  a.s = Shape{tiles, n_tiles, valid, n_tok, heads / kv_heads, dim, causal, scale};
+  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, rows, causal, tiles, n_tiles, err, stream))) return rc;
+  a.s = Shape{tiles, n_tiles, valid, n_tok, heads, heads / kv_heads, dim, causal, scale};
   a.lse = lse;
-  const dim3 grid((unsigned)tile_cap(n_tok, n, rows), (unsigned)heads);
+  const dim3 grid((unsigned)(tile_cap(n_tok, n, rows) * heads));
   if (dtype == FS_BF16)
     launch_fwd<__bf16>(a, grid, stream);
   else

@@ -146,6 +146,18 @@ struct Tile {
   int32_t lo, len, hist, t0;
 };
 
+// The table lists a sample's tiles by their rows to the sample's end (most
+// first). The kernels that pass over the tokens before their rows take the
+// mirrored tile: as many rows from the start.
+__device__ __forceinline__ Tile tile_by_end(Tile t, int rows) {
+  t.t0 = (t.len - 1) / rows * rows - t.t0;
+  return t;
+}
+
+// A thread's rows of a staged tile lie less than 64 tokens behind a uniform
+// address, so 32 bits hold their distance.
+constexpr int64_t kMaxStride = (int64_t)1 << 26;
+
 // A [n_tok, heads, D] array: bytes between tokens and between heads
 struct View {
   char* p;
@@ -157,19 +169,12 @@ struct Shape {
   const int32_t* n_tiles;
   const uint8_t* valid;  // nullable
   int64_t n_tok;
+  int32_t heads;         // query heads
   int32_t group;         // query heads per key head
   int32_t dim;           // elements of a head, at most DP
   int32_t causal;
   float scale;           // of the scores
 };
-
-// bits of the rows r0 .. r0 + 63 of a sample that exist and are valid
-__device__ __forceinline__ uint64_t live_rows(const Shape& a, const Tile& t, int r0) {
-  const int r = r0 + lane();
-  bool on = r >= 0 && r < t.len;
-  if (a.valid != nullptr && on) on = a.valid[(int64_t)t.lo + r] != 0;
-  return __ballot(on);
-}
 
 __device__ __forceinline__ bool live_row(const Shape& a, const Tile& t, int r) {
   if (r >= t.len) return false;
@@ -205,29 +210,55 @@ __device__ __forceinline__ u32x4 load_piece(const char* head, int64_t tok_bytes,
   return v;
 }
 
-// A tile of ROWS rows on its way from memory to LDS, NT threads: load() fills
-// registers, store() writes them to LDS.
-template <int DP, int ROWS, int NT>
+// Which rows r0 .. r0 + 63 of a sample exist and are valid, one row per lane:
+// read one step before it is needed (live_bits), so that no wait stands
+// between a step's products.
+__device__ __forceinline__ uint32_t live_byte(const Shape& a, const Tile& t, int r0) {
+  const int r = r0 + lane();
+  if (r >= t.len) return 0;
+  return a.valid == nullptr ? 1 : a.valid[(int64_t)t.lo + r];
+}
+__device__ __forceinline__ uint64_t live_bits(uint32_t byte) { return __ballot(byte != 0); }
+
+// A tile of 64 rows on its way from memory to LDS, NT threads: load() fills
+// registers, store() writes them to LDS, zeros in the place of what is not
+// live or lies past the head's width. Rows past the sample load its last one
+// and pieces past the width the first, so every load is in bounds and none is
+// conditional; tiles that are live throughout skip all of that.
+template <int DP, int NT>
 struct Staged {
+  static constexpr int kRows = 64;
   static constexpr int kPieces = DP / 8;
-  static constexpr int kPer = ROWS * kPieces / NT;
-  static_assert(kPer >= 1 && ROWS * kPieces % NT == 0, "whole pieces per thread");
+  static constexpr int kPer = kRows * kPieces / NT;
+  static constexpr int kStepRows = NT / kPieces;  // rows between a thread's pieces
+  static_assert(kPer >= 1 && kRows * kPieces % NT == 0, "whole pieces per thread");
   u32x4 v[kPer];
 
   __device__ __forceinline__ void load(const char* head, int64_t tok_bytes, const Shape& a,
-                                       const Tile& t, int r0) {
+                                       const Tile& t, int r0, bool whole) {
+    const int row = threadIdx.x / kPieces, p = threadIdx.x % kPieces;
+    const char* base = head + ((int64_t)t.lo + r0) * tok_bytes;  // uniform
+    if (whole) {
+      const uint32_t at = (uint32_t)row * (uint32_t)tok_bytes + 16 * p;
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const int id = x * NT + threadIdx.x;
-      const int r = r0 + id / kPieces;
-      v[x] = load_piece(head, tok_bytes, a, t, r, id % kPieces, live_row(a, t, r));
+      for (int x = 0; x < kPer; ++x)
+        v[x] = *(const u32x4*)(base + (int64_t)x * kStepRows * tok_bytes + at);
+    } else {
+      const int last = t.len - 1 - r0, pc = 8 * p < a.dim ? 16 * p : 0;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x)
+        v[x] = *(const u32x4*)(base + (int64_t)min(row + x * kStepRows, last) * tok_bytes + pc);
     }
   }
-  __device__ __forceinline__ void store(uint16_t* tile) const {
+  __device__ __forceinline__ void store(uint16_t* tile, const Shape& a, uint64_t live,
+                                        bool whole) const {
+    const int row = threadIdx.x / kPieces, p = threadIdx.x % kPieces;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
-      const int id = x * NT + threadIdx.x;
-      *(u32x4*)(tile + piece<DP>(id / kPieces, id % kPieces)) = v[x];
+      const int r = row + x * kStepRows;
+      u32x4 y = v[x];
+      if (!whole && (!((live >> r) & 1) || 8 * p >= a.dim)) y = u32x4{0, 0, 0, 0};
+      *(u32x4*)(tile + piece<DP>(r, p)) = y;
     }
   }
 };
@@ -270,7 +301,8 @@ __host__ int make_view(const fs_heads* x, int32_t heads, int32_t dim, View* v);
 
 // Launches the tile table of `rows`-row tiles (see attention.hip).
 int launch_tiles(const int64_t* offsets, int32_t n, int64_t n_tok, const int32_t* n_cand,
-                 int32_t rows, Tile* tiles, int32_t* n_tiles, int32_t* err, hipStream_t stream);
+                 int32_t rows, int32_t causal, Tile* tiles, int32_t* n_tiles, int32_t* err,
+                 hipStream_t stream);
 
 }  // namespace attn
 }  // namespace fs

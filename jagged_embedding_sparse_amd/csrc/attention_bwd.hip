@@ -50,9 +50,10 @@ template <typename T, int DP, int NW>
 __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sk[2][kStep * DP], sv[2][kStep * DP];
-  if ((int32_t)blockIdx.x >= *a.s.n_tiles) return;
-  const Tile t = a.s.tiles[blockIdx.x];
-  const int head = blockIdx.y, kvh = head / a.s.group;
+  const int at = blockIdx.x / a.s.heads, head = blockIdx.x % a.s.heads;
+  if (at >= *a.s.n_tiles) return;
+  const Tile t = tile_by_end(a.s.tiles[at], 32 * NW);
+  const int kvh = head / a.s.group;
   const char* kp = a.k.p + kvh * a.k.head;
   const char* vp = a.v.p + kvh * a.v.head;
   const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
@@ -99,24 +100,32 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
   const int steps = hist_end + max(0, own_end - own_lo);
   auto key0 = [&](int step) { return (step < hist_end ? step : own_lo + step - hist_end) * kStep; };
 
-  Staged<DP, kStep, NT> ks, vs;
+  Staged<DP, NT> ks, vs;
+  uint64_t keys = 0;
+  uint32_t ahead = 0;
+  bool full = false;
+  auto load = [&](int step) {
+    const int j = key0(step);
+    keys = live_bits(ahead);
+    full = keys == ~0ull && a.s.dim == DP;
+    ks.load(kp, a.k.tok, a.s, t, j, full);
+    vs.load(vp, a.v.tok, a.s, t, j, full);
+    if (step + 1 < steps) ahead = live_byte(a.s, t, key0(step + 1));
+  };
   if (steps > 0) {
-    ks.load(kp, a.k.tok, a.s, t, key0(0));
-    vs.load(vp, a.v.tok, a.s, t, key0(0));
+    ahead = live_byte(a.s, t, key0(0));
+    load(0);
   }
   for (int step = 0; step < steps; ++step) {
     const int j0 = key0(step), b = step & 1;
-    ks.store(sk[b]);
-    vs.store(sv[b]);
+    const uint64_t live = keys;
+    ks.store(sk[b], a.s, live, full);
+    vs.store(sv[b], a.s, live, full);
     __syncthreads();
-    if (step + 1 < steps) {
-      ks.load(kp, a.k.tok, a.s, t, key0(step + 1));
-      vs.load(vp, a.v.tok, a.s, t, key0(step + 1));
-    }
+    if (step + 1 < steps) load(step + 1);
     const bool past = causal ? j0 > i0 + 31 : j0 >= t.hist;
     if (i0 >= t1 || (past && (j0 > i0 + 31 || j0 + kStep <= i0))) continue;
-    const uint64_t keys = live_rows(a.s, t, j0);
-    const bool whole = keys == ~0ull && j0 + kStep <= t.hist && (!causal || j0 + kStep <= i0 + 1) &&
+    const bool whole = live == ~0ull && j0 + kStep <= t.hist && (!causal || j0 + kStep <= i0 + 1) &&
                        __all(on);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
@@ -128,7 +137,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
       }
       uint32_t see = ~0u;
       if (!whole)
-        see = on ? seen_keys(i, j0 + 32 * kb, t.hist, causal) & (uint32_t)(keys >> (32 * kb)) : 0u;
+        see = on ? seen_keys(i, j0 + 32 * kb, t.hist, causal) & (uint32_t)(live >> (32 * kb)) : 0u;
       see >>= 4 * g;
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
@@ -157,9 +166,10 @@ __global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sq[2][kStep * DP], sd[2][kStep * DP];
   __shared__ __attribute__((aligned(16))) float s_lse[2][kStep], s_delta[2][kStep];
-  if ((int32_t)blockIdx.x >= *a.s.n_tiles) return;
-  const Tile t = a.s.tiles[blockIdx.x];
-  const int kvh = blockIdx.y;
+  const int kv_heads = a.s.heads / a.s.group;
+  const int at = blockIdx.x / kv_heads, kvh = blockIdx.x % kv_heads;
+  if (at >= *a.s.n_tiles) return;
+  const Tile t = a.s.tiles[at];
   const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
   const int t1 = min(t.t0 + 32 * NW, t.len);
   const int j0 = t.t0 + 32 * w, j = j0 + (l & 31);
@@ -181,40 +191,46 @@ __global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
   const int last = (int)cdiv(own ? t1 : t.len, kStep);
   const int per = last - first, steps = per * a.s.group;
 
-  Staged<DP, kStep, NT> qs, ds;
+  Staged<DP, NT> qs, ds;
+  uint64_t rows = 0;
+  uint32_t ahead = 0;
+  bool full = false;
   float st_lse = INFINITY, st_delta = 0.f;  // threads 0 .. 63: one row each
+  auto row0 = [&](int step) { return (first + step % per) * kStep; };
   auto load = [&](int step) {
-    const int head = kvh * a.s.group + step / per, i0 = (first + step % per) * kStep;
-    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
-    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
+    const int head = kvh * a.s.group + step / per, i0 = row0(step);
+    rows = live_bits(ahead);
+    full = rows == ~0ull && a.s.dim == DP;
+    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0, full);
+    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0, full);
     if (threadIdx.x < kStep) {
-      const int i = i0 + threadIdx.x;
-      st_lse = INFINITY;
-      st_delta = 0.f;
-      if (live_row(a.s, t, i)) {
-        const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
-        const float x = a.lse[at];
-        st_lse = x == -INFINITY ? INFINITY : x * kLog2e;
-        st_delta = a.delta[at];
-      }
+      const int i = min(i0 + (int)threadIdx.x, t.len - 1);
+      const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
+      st_lse = a.lse[at];
+      st_delta = a.delta[at];
     }
+    if (step + 1 < steps) ahead = live_byte(a.s, t, row0(step + 1));
   };
-  if (steps > 0) load(0);
+  if (steps > 0) {
+    ahead = live_byte(a.s, t, row0(0));
+    load(0);
+  }
   for (int step = 0; step < steps; ++step) {
-    const int i0 = (first + step % per) * kStep, b = step & 1;
-    qs.store(sq[b]);
-    ds.store(sd[b]);
+    const int i0 = row0(step), b = step & 1;
+    const uint64_t live = rows;
+    qs.store(sq[b], a.s, live, full);
+    ds.store(sd[b], a.s, live, full);
     if (threadIdx.x < kStep) {
-      s_lse[b][threadIdx.x] = st_lse;
-      s_delta[b][threadIdx.x] = st_delta;
+      const bool in = (live >> threadIdx.x) & 1;
+      s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e;
+      s_delta[b][threadIdx.x] = in ? st_delta : 0.f;
     }
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
     // steps whose rows see none of this wave's keys
     if (j0 >= t1 || (causal && i0 + kStep <= j0)) continue;
     if (j0 >= t.hist && (i0 + kStep <= j0 || i0 > j0 + 31)) continue;
-    const uint64_t rows = live_rows(a.s, t, i0);
-    const bool whole = rows == ~0ull && j0 + 32 <= t.hist && (!causal || i0 >= j0 + 31) && __all(on);
+    const bool whole = live == ~0ull && j0 + 32 <= t.hist && (!causal || i0 >= j0 + 31) && __all(on);
 #pragma unroll
     for (int ib = 0; ib < 2; ++ib) {
       f32x16 s = zero16(), dp = zero16();
@@ -225,7 +241,7 @@ __global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
       }
       uint32_t see = ~0u;
       if (!whole)
-        see = on ? seeing_rows(j, i0 + 32 * ib, t.hist, causal) & (uint32_t)(rows >> (32 * ib)) : 0u;
+        see = on ? seeing_rows(j, i0 + 32 * ib, t.hist, causal) & (uint32_t)(live >> (32 * ib)) : 0u;
       see >>= 4 * g;
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
@@ -260,10 +276,10 @@ __global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
 template <typename T, int DP>
 int launch_bwd(const BwdArgs& a, int32_t heads, int64_t cap, hipStream_t stream) {
   constexpr int NW = 4;
-  hipLaunchKernelGGL((k_attn_dq<T, DP, NW>), dim3((unsigned)cap, (unsigned)heads),
+  hipLaunchKernelGGL((k_attn_dq<T, DP, NW>), dim3((unsigned)(cap * heads)),
                      dim3(NW * kWave), 0, stream, a);
   FS_LAUNCH_CHECK();
-  hipLaunchKernelGGL((k_attn_dkv<T, DP, NW>), dim3((unsigned)cap, (unsigned)(heads / a.s.group)),
+  hipLaunchKernelGGL((k_attn_dkv<T, DP, NW>), dim3((unsigned)(cap * (heads / a.s.group))),
                      dim3(NW * kWave), 0, stream, a);
   FS_LAUNCH_CHECK();
   return FS_OK;
@@ -324,8 +340,9 @@ extern "C" int fs_jagged_attention_backward(
   a.lse = lse;
   a.delta = c.take<float>((size_t)heads * (size_t)n_tok);
   const int64_t cap = tile_cap(n_tok, n, rows);
-  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, rows, tiles, n_tiles, err, stream))) return rc;
-  a.s = Shape{tiles, n_tiles, valid, n_tok, heads / kv_heads, dim, causal, scale};
+  if (cap * heads >= (int64_t)INT32_MAX) return FS_ERR_UNSUPPORTED;
+  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, rows, causal, tiles, n_tiles, err, stream))) return rc;
+  a.s = Shape{tiles, n_tiles, valid, n_tok, heads, heads / kv_heads, dim, causal, scale};
   return dtype == FS_BF16 ? launch_bwd<__bf16>(a, heads, cap, stream)
                           : launch_bwd<_Float16>(a, heads, cap, stream);
 }
