@@ -568,7 +568,8 @@ int fs_jagged_attention_backward(const fs_heads* q, const fs_heads* k, const fs_
                                  const fs_heads* dv, int32_t* err, void* ws, size_t ws_bytes,
                                  hipStream_t stream);
 
-size_t fs_jagged_attention_backward_workspace_size(int64_t n_tok, int32_t n, int32_t heads);
+size_t fs_jagged_attention_backward_workspace_size(int64_t n_tok, int32_t n, int32_t heads,
+                                                   int32_t kv_heads, int32_t dim);
 
 /* ------------------------------------------------------------------------ */
 const char* fs_strerror(int code);

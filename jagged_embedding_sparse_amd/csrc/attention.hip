@@ -208,9 +208,9 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
 template <typename T>
 void launch_fwd(const FwdArgs& a, dim3 grid, hipStream_t stream) {
   constexpr int NW = 4;
-  if (a.s.dim <= 32)
+  if (padded(a.s.dim) == 32)
     hipLaunchKernelGGL((k_attn_fwd<T, 32, NW>), grid, dim3(NW * kWave), 0, stream, a);
-  else if (a.s.dim <= 64)
+  else if (padded(a.s.dim) == 64)
     hipLaunchKernelGGL((k_attn_fwd<T, 64, NW>), grid, dim3(NW * kWave), 0, stream, a);
   else
     hipLaunchKernelGGL((k_attn_fwd<T, 128, NW>), grid, dim3(NW * kWave), 0, stream, a);

@@ -293,6 +293,9 @@ __device__ __forceinline__ float log2_scale(const Shape& a) {
 // ---------------------------------------------------------------- host side
 __host__ inline bool type_ok(int32_t dtype) { return dtype == FS_BF16 || dtype == FS_F16; }
 
+// the width of the kernel's rows for heads of dim elements
+__host__ inline int32_t padded(int32_t dim) { return dim <= 32 ? 32 : (dim <= 64 ? 64 : 128); }
+
 // tiles of `rows` rows that n samples of n_tok tokens can need
 __host__ inline int64_t tile_cap(int64_t n_tok, int32_t n, int32_t rows) { return n_tok / rows + n; }
 

@@ -7,6 +7,7 @@
 // sums in registers and recomputes S and dP (7 products instead of the least
 // 5), so no sum crosses workgroups, nothing is added atomically and equal
 // calls give equal bits. The first writes delta for the second.
+#include <algorithm>
 #include <cmath>
 
 #include "attention.hpp"
@@ -22,7 +23,31 @@ struct BwdArgs {
   View q, k, v, o, d_o, dq, dk, dv;
   const float* lse;  // [heads][n_tok]
   float* delta;      // [heads][n_tok]
+  float* part;       // [splits][2][kv_heads][n_tok][DP]: dK (unscaled) and dV
+  int32_t splits;
 };
+
+// The grid of the dK / dV kernel is one workgroup per 128 keys and key head.
+// Causal tiles differ in length by up to the sample's, so with fewer than
+// about two workgroups per CU the longest one decides; then each tile's steps
+// are cut into equal parts, whose sums a second kernel adds in order. Measured
+// at 2 x 8192 tokens, 8/2 heads of 128 (256 tiles): 2028 us whole, SPLIT_US in
+// two parts and their sum; at 54790 tokens, 8/2 heads of 64 (about 980 tiles)
+// parts only add their traffic.
+constexpr int64_t kParts = 512;   // workgroups to reach
+constexpr int64_t kSplitMax = 8;  // parts of one tile
+__host__ inline int32_t splits_of(int64_t n_tok, int32_t kv_heads) {
+  const int64_t tiles = std::max<int64_t>(1, n_tok / 128 * kv_heads);
+  return (int32_t)std::min(kSplitMax, cdiv(kParts, tiles));
+}
+// The most tokens times splits of any call with at most n_tok tokens: a call
+// has s splits or more while its tiles are at most (kParts - 1) / (s - 1).
+__host__ inline int64_t split_tokens(int64_t n_tok, int32_t kv_heads) {
+  int64_t most = 0;
+  for (int64_t s = 2; s <= kSplitMax; ++s)
+    most = std::max(most, s * std::min(n_tok, ((kParts - 1) / (s - 1) / kv_heads + 1) * 128 - 1));
+  return most;
+}
 
 // 32 columns x DP rows of sums to one row of memory per lane, scaled
 template <typename T, int DP>
@@ -167,7 +192,8 @@ __global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
   __shared__ uint16_t sq[2][kStep * DP], sd[2][kStep * DP];
   __shared__ __attribute__((aligned(16))) float s_lse[2][kStep], s_delta[2][kStep];
   const int kv_heads = a.s.heads / a.s.group;
-  const int at = blockIdx.x / kv_heads, kvh = blockIdx.x % kv_heads;
+  const int kvh = blockIdx.x % kv_heads, part = blockIdx.x / kv_heads % a.splits;
+  const int at = blockIdx.x / kv_heads / a.splits;
   if (at >= *a.s.n_tiles) return;
   const Tile t = a.s.tiles[at];
   const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
@@ -189,7 +215,9 @@ __global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
   const bool own = t.t0 >= t.hist;
   const int first = (own || causal ? t.t0 : 0) / kStep;
   const int last = (int)cdiv(own ? t1 : t.len, kStep);
-  const int per = last - first, steps = per * a.s.group;
+  const int per = last - first, all = per * a.s.group;
+  const int step0 = (int)((int64_t)all * part / a.splits);
+  const int steps = (int)((int64_t)all * (part + 1) / a.splits);
 
   Staged<DP, NT> qs, ds;
   uint64_t rows = 0;
@@ -211,11 +239,11 @@ __global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
     }
     if (step + 1 < steps) ahead = live_byte(a.s, t, row0(step + 1));
   };
-  if (steps > 0) {
-    ahead = live_byte(a.s, t, row0(0));
-    load(0);
+  if (step0 < steps) {
+    ahead = live_byte(a.s, t, row0(step0));
+    load(step0);
   }
-  for (int step = 0; step < steps; ++step) {
+  for (int step = step0; step < steps; ++step) {
     const int i0 = row0(step), b = step & 1;
     const uint64_t live = rows;
     qs.store(sq[b], a.s, live, full);
@@ -269,27 +297,71 @@ __global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
   }
   if (j >= t.len) return;
   const int64_t tok = (int64_t)t.lo + j;
+  if (a.splits > 1) {
+    float* to = a.part + (((int64_t)part * 2 * kv_heads + kvh) * a.s.n_tok + tok) * DP;
+    const int64_t dv_at = (int64_t)kv_heads * a.s.n_tok * DP;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int col = 32 * d + 8 * y + 4 * g;
+        *(f32x4*)(to + col) = f32x4{dk[d][4 * y], dk[d][4 * y + 1], dk[d][4 * y + 2], dk[d][4 * y + 3]};
+        *(f32x4*)(to + dv_at + col) = f32x4{dv[d][4 * y], dv[d][4 * y + 1], dv[d][4 * y + 2], dv[d][4 * y + 3]};
+      }
+    return;
+  }
   store_rows<T, DP>(a.dk.p + kvh * a.dk.head + tok * a.dk.tok, dk, a.s.dim, a.s.scale);
   store_rows<T, DP>(a.dv.p + kvh * a.dv.head + tok * a.dv.tok, dv, a.s.dim, 1.f);
 }
 
+// Sums of the parts, part by part: one thread per 4 columns of dK or dV.
 template <typename T, int DP>
-int launch_bwd(const BwdArgs& a, int32_t heads, int64_t cap, hipStream_t stream) {
+__global__ void __launch_bounds__(256) k_attn_join(BwdArgs a, const int64_t* __restrict__ offsets,
+                                                   int32_t n) {
+  constexpr int kPer = DP / 4;
+  if (*a.s.n_tiles == 0) return;  // no samples, or offsets that do not rise
+  const int kv_heads = a.s.heads / a.s.group;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int col = (int)(id % kPer) * 4;
+  const int64_t tok = id / kPer % a.s.n_tok;
+  const int64_t row = id / kPer / a.s.n_tok;  // which * kv_heads + key head
+  if (row >= 2 * kv_heads || col >= a.s.dim || tok < offsets[0] || tok >= offsets[n]) return;
+  f32x4 s = {0, 0, 0, 0};
+  for (int p = 0; p < a.splits; ++p)
+    s += *(const f32x4*)(a.part + (((int64_t)p * 2 * kv_heads + row) * a.s.n_tok + tok) * DP + col);
+  const bool is_v = row >= kv_heads;
+  const View& o = is_v ? a.dv : a.dk;
+  if (!is_v) s *= a.s.scale;
+  *(u32x2*)(o.p + (row - (is_v ? kv_heads : 0)) * o.head + tok * o.tok + 2 * col) =
+      u32x2{Elem<T>::pack(s[0], s[1]), Elem<T>::pack(s[2], s[3])};
+}
+
+template <typename T, int DP>
+int launch_bwd(const BwdArgs& a, const int64_t* offsets, int32_t n, int64_t cap,
+               hipStream_t stream) {
   constexpr int NW = 4;
-  hipLaunchKernelGGL((k_attn_dq<T, DP, NW>), dim3((unsigned)(cap * heads)),
+  const int64_t kv_heads = a.s.heads / a.s.group;
+  hipLaunchKernelGGL((k_attn_dq<T, DP, NW>), dim3((unsigned)(cap * a.s.heads)),
                      dim3(NW * kWave), 0, stream, a);
   FS_LAUNCH_CHECK();
-  hipLaunchKernelGGL((k_attn_dkv<T, DP, NW>), dim3((unsigned)(cap * (heads / a.s.group))),
+  hipLaunchKernelGGL((k_attn_dkv<T, DP, NW>), dim3((unsigned)(cap * kv_heads * a.splits)),
                      dim3(NW * kWave), 0, stream, a);
   FS_LAUNCH_CHECK();
+  if (a.splits > 1) {
+    const int64_t threads = 2 * kv_heads * a.s.n_tok * (DP / 4);
+    hipLaunchKernelGGL((k_attn_join<T, DP>), dim3((unsigned)cdiv(threads, 256)), dim3(256), 0, stream,
+                       a, offsets, n);
+    FS_LAUNCH_CHECK();
+  }
   return FS_OK;
 }
 
 template <typename T>
-int launch_bwd(const BwdArgs& a, int32_t heads, int64_t cap, hipStream_t stream) {
-  if (a.s.dim <= 32) return launch_bwd<T, 32>(a, heads, cap, stream);
-  if (a.s.dim <= 64) return launch_bwd<T, 64>(a, heads, cap, stream);
-  return launch_bwd<T, 128>(a, heads, cap, stream);
+int launch_bwd(const BwdArgs& a, const int64_t* offsets, int32_t n, int64_t cap,
+               hipStream_t stream) {
+  if (padded(a.s.dim) == 32) return launch_bwd<T, 32>(a, offsets, n, cap, stream);
+  if (padded(a.s.dim) == 64) return launch_bwd<T, 64>(a, offsets, n, cap, stream);
+  return launch_bwd<T, 128>(a, offsets, n, cap, stream);
 }
 
 }  // namespace
@@ -300,12 +372,14 @@ using namespace fs;
 using namespace fs::attn;
 
 extern "C" size_t fs_jagged_attention_backward_workspace_size(int64_t n_tok, int32_t n,
-                                                              int32_t heads) {
-  if (n_tok < 0 || n < 0 || heads < 0) return 0;
+                                                              int32_t heads, int32_t kv_heads,
+                                                              int32_t dim) {
+  if (n_tok < 0 || n < 0 || heads < 0 || kv_heads < 1 || dim < 0) return 0;
   Carve c(nullptr);
   c.take<int32_t>(1);
   c.take<Tile>((size_t)tile_cap(n_tok, n, 32));
   c.take<float>((size_t)heads * (size_t)n_tok);
+  c.take<float>((size_t)split_tokens(n_tok, kv_heads) * 2 * kv_heads * padded(dim));
   return c.used + 256;
 }
 
@@ -330,7 +404,7 @@ extern "C" int fs_jagged_attention_backward(
   if (n_tok > 0 && n > 0 &&
       (!a.q.p || !a.k.p || !a.v.p || !a.o.p || !a.d_o.p || !a.dq.p || !a.dk.p || !a.dv.p || !lse))
     return FS_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < fs_jagged_attention_backward_workspace_size(n_tok, n, heads))
+  if (!ws || ws_bytes < fs_jagged_attention_backward_workspace_size(n_tok, n, heads, kv_heads, dim))
     return FS_ERR_WORKSPACE;
   if (n == 0 || n_tok == 0) return FS_OK;
   constexpr int32_t rows = 128;
@@ -339,10 +413,12 @@ extern "C" int fs_jagged_attention_backward(
   Tile* tiles = c.take<Tile>((size_t)tile_cap(n_tok, n, 32));
   a.lse = lse;
   a.delta = c.take<float>((size_t)heads * (size_t)n_tok);
+  a.splits = splits_of(n_tok, kv_heads);
+  a.part = c.take<float>((size_t)split_tokens(n_tok, kv_heads) * 2 * kv_heads * padded(dim));
   const int64_t cap = tile_cap(n_tok, n, rows);
-  if (cap * heads >= (int64_t)INT32_MAX) return FS_ERR_UNSUPPORTED;
+  if (cap * heads >= (int64_t)INT32_MAX || cap * kv_heads * a.splits >= (int64_t)INT32_MAX) return FS_ERR_UNSUPPORTED;
   if ((rc = launch_tiles(offsets, n, n_tok, n_cand, rows, causal, tiles, n_tiles, err, stream))) return rc;
   a.s = Shape{tiles, n_tiles, valid, n_tok, heads, heads / kv_heads, dim, causal, scale};
-  return dtype == FS_BF16 ? launch_bwd<__bf16>(a, heads, cap, stream)
-                          : launch_bwd<_Float16>(a, heads, cap, stream);
+  return dtype == FS_BF16 ? launch_bwd<__bf16>(a, offsets, n, cap, stream)
+                          : launch_bwd<_Float16>(a, offsets, n, cap, stream);
 }

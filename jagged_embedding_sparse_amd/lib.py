@@ -98,7 +98,8 @@ _c_attention_ws = _sig("fs_jagged_attention_workspace_size", _sz, _i64, _i32)
 _c_attention_bwd = _sig("fs_jagged_attention_backward", C.c_int, _HP, _HP, _HP, _HP, _P, _HP, _P,
                         _i32, _i64, _P, _P, _i32, _i32, _i32, _i32, _i32, _f, _HP, _HP, _HP, _P,
                         _P, _sz, _P)
-_c_attention_bwd_ws = _sig("fs_jagged_attention_backward_workspace_size", _sz, _i64, _i32, _i32)
+_c_attention_bwd_ws = _sig("fs_jagged_attention_backward_workspace_size", _sz, _i64, _i32, _i32,
+                            _i32, _i32)
 _c_strerror = _sig("fs_strerror", C.c_char_p, C.c_int)
 _c_version = _sig("fs_version", C.c_int)
 
@@ -621,8 +622,8 @@ def fs_jagged_attention(q, k, v, offsets, n_cand=None, valid=None, causal=True, 
     return out, lse
 
 
-def attention_backward_workspace_size(n_tok, n, heads):
-    return int(_c_attention_bwd_ws(n_tok, n, heads))
+def attention_backward_workspace_size(n_tok, n, heads, kv_heads, dim):
+    return int(_c_attention_bwd_ws(n_tok, n, heads, kv_heads, dim))
 
 
 def fs_jagged_attention_backward(q, k, v, out, lse, dout, offsets, n_cand=None, valid=None,
@@ -637,7 +638,7 @@ def fs_jagged_attention_backward(q, k, v, out, lse, dout, offsets, n_cand=None, 
     dq = dq if dq is not None else torch.empty((n_tok, heads, dim), dtype=q.dtype, device=d)
     dk = dk if dk is not None else torch.empty(kv, dtype=q.dtype, device=d)
     dv = dv if dv is not None else torch.empty(kv, dtype=q.dtype, device=d)
-    ws = _ws(attention_backward_workspace_size(n_tok, n, heads), ws)
+    ws = _ws(attention_backward_workspace_size(n_tok, n, heads, kv[1], dim), ws)
     _check("fs_jagged_attention_backward",
            _c_attention_bwd(hs[0], hs[1], hs[2], _heads_arg(out, q.shape, q.dtype), _ptr(lse),
                             _heads_arg(dout, q.shape, q.dtype), _ptr(offsets), n, n_tok,

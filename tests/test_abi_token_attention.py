@@ -101,7 +101,7 @@ def attention(L, request):
         ok = [h, h, h, FAKE, 4, 50, None, None, 8, 2, 64, L.FS_BF16, 1, 0.1, h, FAKE, None, FAKE,
               need, None]
         return _caller(L._c_attention, NAMES, ok), ["q", "k", "v", "out"], need
-    need = L.attention_backward_workspace_size(50, 4, 8)
+    need = L.attention_backward_workspace_size(50, 4, 8, 2, 64)
     ok = [h, h, h, h, FAKE, h, FAKE, 4, 50, None, None, 8, 2, 64, L.FS_BF16, 1, 0.1, h, h, h, None,
           FAKE, need, None]
     return _caller(L._c_attention_bwd, NAMES_BWD, ok), \
@@ -133,11 +133,17 @@ def test_workspace_queries_never_decrease(L):
     prev = [0] * 4
     for n in list(range(0, 300)) + [4095, 4096, 4097, 5000, 65_535, 65_536, 65_537, 70_000, 1 << 20]:
         now = [L.token_sort_workspace_size(n), L.token_grad_workspace_size(n, 100),
-               L.attention_workspace_size(n, 16), L.attention_backward_workspace_size(n, 16, 4)]
+               L.attention_workspace_size(n, 16), L.attention_backward_workspace_size(n, 16, 4, 2, 64)]
         assert all(a >= b for a, b in zip(now, prev)), n
         prev = now
     for dim in range(1, 1100):
         assert L.token_grad_workspace_size(1000, dim) <= L.token_grad_workspace_size(1000, dim + 1)
     assert L.attention_workspace_size(100, 5) <= L.attention_workspace_size(100, 6)
-    assert L.attention_backward_workspace_size(100, 5, 2) <= \
-        L.attention_backward_workspace_size(100, 5, 3)
+    assert L.attention_backward_workspace_size(100, 5, 2, 2, 64) <= \
+        L.attention_backward_workspace_size(100, 5, 4, 2, 64)
+    for kv in (1, 3, 8):  # the parts of long tiles: fewer as the batch grows
+        prev = 0
+        for n in list(range(0, 70_000, 97)) + [1 << 17, 1 << 20]:
+            now = L.attention_backward_workspace_size(n, 4, 8, kv, 128)
+            assert now >= prev, (kv, n)
+            prev = now

@@ -251,7 +251,7 @@ def test_capture_replay_and_streams(L):
     do = c.dout.cuda()
     n = len(c.off) - 1
     ws = torch.empty(L.attention_workspace_size(c.n, n), dtype=torch.uint8, device="cuda")
-    wb = torch.empty(L.attention_backward_workspace_size(c.n, n, 4), dtype=torch.uint8,
+    wb = torch.empty(L.attention_backward_workspace_size(c.n, n, 4, 2, 64), dtype=torch.uint8,
                      device="cuda")
 
     def work(a, do, outs=None, ws=None, wb=None, stream=None):
