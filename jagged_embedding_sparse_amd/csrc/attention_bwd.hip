@@ -187,7 +187,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
 // in steps. S = q k^T and dP = dO v^T have one key per lane, so P and dS are
 // the operands of dV^T = dO^T P and dK^T = q^T dS.
 template <typename T, int DP, int NW>
-__global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
+__global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)) k_attn_dkv(BwdArgs a) {
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sq[2][kStep * DP], sd[2][kStep * DP];
   __shared__ __attribute__((aligned(16))) float s_lse[2][kStep], s_delta[2][kStep];
@@ -314,6 +314,161 @@ __global__ void __launch_bounds__(NW * kWave, 1) k_attn_dkv(BwdArgs a) {
   store_rows<T, DP>(a.dv.p + kvh * a.dv.head + tok * a.dv.tok, dv, a.s.dim, 1.f);
 }
 
+// dK and dV of heads wider than 64: the sums alone take 128 registers per
+// lane, which leaves one wave per SIMD. So two waves share 32 keys: of each
+// step's 64 rows, each computes P and dS of 32, then one sums dV over all 64
+// and the other dK, each with its own operand and its partner's, which travels
+// through LDS as rounded operands (2 KB a step). The sums of a step are taken
+// one step later, beside the next step's scores: their products do not wait
+// for the exponentials, and one barrier per step serves both the tiles (three
+// in turn) and the exchange.
+template <typename T, int DP>
+__global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
+  constexpr int NT = 512;
+  __shared__ uint16_t sq[3][kStep * DP], sd[3][kStep * DP];
+  __shared__ u32x4 ex[2][8][2][kWave];
+  __shared__ __attribute__((aligned(16))) float s_lse[3][kStep], s_delta[3][kStep];
+  const int kv_heads = a.s.heads / a.s.group;
+  const int kvh = blockIdx.x % kv_heads, part = blockIdx.x / kv_heads % a.splits;
+  const int at = blockIdx.x / kv_heads / a.splits;
+  if (at >= *a.s.n_tiles) return;
+  const Tile t = a.s.tiles[at];
+  const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
+  const int half = w >> 2;  // which 32 rows of a step, and dV (0) or dK (1)
+  const int t1 = min(t.t0 + 128, t.len);
+  const int j0 = t.t0 + 32 * (w & 3), j = j0 + (l & 31);
+  const bool on = live_row(a.s, t, j);
+  const bool causal = a.s.causal != 0;
+
+  u32x4 kf[DP / 16], vf[DP / 16];
+  load_scaled_columns<DP>(kf, a.k.p + kvh * a.k.head, a.k.tok, a.s, t, j, on);
+  load_columns<DP>(vf, a.v.p + kvh * a.v.head, a.v.tok, a.s, t, j, on);
+  f32x16 sum[DP / 32];
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d) sum[d] = zero16();
+  const float c = log2_scale(a.s);
+
+  const bool own = t.t0 >= t.hist;
+  const int first = (own || causal ? t.t0 : 0) / kStep;
+  const int last = (int)cdiv(own ? t1 : t.len, kStep);
+  const int per = last - first, all = per * a.s.group;
+  const int step0 = (int)((int64_t)all * part / a.splits);
+  const int steps = (int)((int64_t)all * (part + 1) / a.splits);
+
+  Staged<DP, NT> qs, ds;
+  uint64_t rows = 0;
+  uint32_t ahead = 0;
+  bool full = false;
+  float st_lse = INFINITY, st_delta = 0.f;  // threads 0 .. 63: one row each
+  auto row0 = [&](int step) { return (first + step % per) * kStep; };
+  auto load = [&](int step) {
+    const int head = kvh * a.s.group + step / per, i0 = row0(step);
+    rows = live_bits(ahead);
+    full = rows == ~0ull && a.s.dim == DP;
+    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0, full);
+    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0, full);
+    if (threadIdx.x < kStep) {
+      const int i = min(i0 + (int)threadIdx.x, t.len - 1);
+      const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
+      st_lse = a.lse[at];
+      st_delta = a.delta[at];
+    }
+    if (step + 1 < steps) ahead = live_byte(a.s, t, row0(step + 1));
+  };
+  if (step0 < steps) {
+    ahead = live_byte(a.s, t, row0(step0));
+    load(step0);
+  }
+  bool have = false;       // the last step's operands wait to be summed
+  u32x4 mine[2];           // this wave's own of them
+  int b = 0, before = 2;   // this step's tiles, the last step's
+  for (int step = step0; step <= steps; ++step) {  // one more, for the last sums
+    const int e = step & 1;
+    const uint64_t live = rows;
+    if (step < steps) {
+      qs.store(sq[b], a.s, live, full);
+      ds.store(sd[b], a.s, live, full);
+      if (threadIdx.x < kStep) {
+        const bool in = (live >> threadIdx.x) & 1;
+        s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e;
+        s_delta[b][threadIdx.x] = in ? st_delta : 0.f;
+      }
+    }
+    __syncthreads();
+    if (step + 1 < steps) load(step + 1);
+    const int i0 = row0(step), r0 = i0 + 32 * half;
+    // steps whose rows see none of these keys (the same for both waves)
+    const bool none = step >= steps || j0 >= t1 || (causal && i0 + kStep <= j0) ||
+                      (j0 >= t.hist && (i0 + kStep <= j0 || i0 > j0 + 31));
+    f32x16 s, dp;
+    if (!none) {
+      s = dp = zero16();
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        s = Elem<T>::mfma(rows_operand<DP>(sq[b], 32 * half, kk), kf[kk], s);
+        dp = Elem<T>::mfma(rows_operand<DP>(sd[b], 32 * half, kk), vf[kk], dp);
+      }
+      const uint32_t half_live = (uint32_t)(live >> (32 * half));
+      if (half_live != ~0u || j0 + 32 > t.hist || (causal && r0 < j0 + 31) || !__all(on)) {
+        const uint32_t see =
+            (on ? seeing_rows(j, r0, t.hist, causal) & half_live : 0u) >> (4 * g);
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (!((see >> (8 * (x >> 2) + (x & 3))) & 1u)) s[x] = -INFINITY;
+      }
+    }
+    if (have) {
+      const uint16_t* tile = half ? sq[before] : sd[before];
+#pragma unroll
+      for (int ib = 0; ib < 2; ++ib)
+#pragma unroll
+        for (int ch = 0; ch < 2; ++ch) {
+          const u32x4 x = ib == half ? mine[ch] : ex[e ^ 1][w ^ 4][ch][l];
+#pragma unroll
+          for (int d = 0; d < DP / 32; ++d)
+            sum[d] = Elem<T>::mfma(cols_operand<DP>(tile, 32 * ib + 16 * ch, 32 * d), x, sum[d]);
+        }
+    }
+    if (!none) {
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const f32x4 ls = *(const f32x4*)&s_lse[b][32 * half + 8 * y + 4 * g];
+        const f32x4 de = *(const f32x4*)&s_delta[b][32 * half + 8 * y + 4 * g];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int z = 4 * y + x;
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], c, -ls[x]));
+          s[z] = p;
+          dp[z] = p * (dp[z] - de[x]);
+        }
+      }
+#pragma unroll
+      for (int ch = 0; ch < 2; ++ch) {
+        const u32x4 pb = to_operand<T>(s, ch), db = to_operand<T>(dp, ch);
+        mine[ch] = half ? db : pb;
+        ex[e][w][ch][l] = half ? pb : db;
+      }
+    }
+    have = !none;
+    before = b;
+    b = b == 2 ? 0 : b + 1;
+  }
+  if (j >= t.len) return;
+  const int64_t tok = (int64_t)t.lo + j;
+  if (a.splits > 1) {
+    float* to = a.part + (((int64_t)part * 2 + 1 - half) * kv_heads + kvh) * a.s.n_tok * DP + tok * DP;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        *(f32x4*)(to + 32 * d + 8 * y + 4 * g) =
+            f32x4{sum[d][4 * y], sum[d][4 * y + 1], sum[d][4 * y + 2], sum[d][4 * y + 3]};
+    return;
+  }
+  const View& o = half ? a.dk : a.dv;
+  store_rows<T, DP>(o.p + kvh * o.head + tok * o.tok, sum, a.s.dim, half ? a.s.scale : 1.f);
+}
+
 // Sums of the parts, part by part: one thread per 4 columns of dK or dV.
 template <typename T, int DP>
 __global__ void __launch_bounds__(256) k_attn_join(BwdArgs a, const int64_t* __restrict__ offsets,
@@ -344,8 +499,11 @@ int launch_bwd(const BwdArgs& a, const int64_t* offsets, int32_t n, int64_t cap,
   hipLaunchKernelGGL((k_attn_dq<T, DP, NW>), dim3((unsigned)(cap * a.s.heads)),
                      dim3(NW * kWave), 0, stream, a);
   FS_LAUNCH_CHECK();
-  hipLaunchKernelGGL((k_attn_dkv<T, DP, NW>), dim3((unsigned)(cap * kv_heads * a.splits)),
-                     dim3(NW * kWave), 0, stream, a);
+  const dim3 grid((unsigned)(cap * kv_heads * a.splits));
+  if constexpr (DP >= 64)
+    hipLaunchKernelGGL((k_attn_dkv2<T, DP>), grid, dim3(512), 0, stream, a);
+  else
+    hipLaunchKernelGGL((k_attn_dkv<T, DP, NW>), grid, dim3(NW * kWave), 0, stream, a);
   FS_LAUNCH_CHECK();
   if (a.splits > 1) {
     const int64_t threads = 2 * kv_heads * a.s.n_tok * (DP / 4);
