@@ -79,6 +79,7 @@ template <typename T, int DP, int NW>
 __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sk[2][kKeys * DP], sv[2][kKeys * DP];
+  __shared__ __attribute__((aligned(16))) float s_off[2][kKeys];
   const int at = blockIdx.x / a.s.heads, head = blockIdx.x % a.s.heads;
   if (at >= *a.s.n_tiles) return;
   const Tile t = tile_by_end(a.s.tiles[at], 32 * NW);
@@ -128,26 +129,25 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
     const uint64_t live = keys;
     ks.store(sk[b], a.s, live, full);
     vs.store(sv[b], a.s, live, full);
+    store_off(s_off[b], live);
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
     // tiles that none of this wave's rows sees
     const bool past = causal ? j0 > i0 + 31 : j0 >= t.hist;
     if (i0 >= t1 || (past && (j0 > i0 + 31 || j0 + kKeys <= i0))) continue;
-    const bool whole = live == ~0ull && j0 + kKeys <= t.hist && (!causal || j0 + kKeys <= i0 + 1);
+    const bool whole = j0 + kKeys <= t.hist && (!causal || j0 + kKeys <= i0 + 1);
     f32x16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      s[kb] = zero16();
+      s[kb] = live == ~0ull ? zero16() : load_off(s_off[b], 32 * kb);
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk)
         s[kb] = Elem<T>::mfma(rows_operand<DP>(sk[b], 32 * kb, kk), qf[kk], s[kb]);
     }
-    if (!whole || !__all(on)) {
+    if (!whole) {
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb) {
-        uint32_t see = on ? seen_keys(i, j0 + 32 * kb, t.hist, causal) & (uint32_t)(live >> (32 * kb))
-                          : 0u;
-        see >>= 4 * g;
+        const uint32_t see = seen_keys(i, j0 + 32 * kb, t.hist, causal) >> (4 * g);
 #pragma unroll
         for (int x = 0; x < 16; ++x)
           if (!((see >> (8 * (x >> 2) + (x & 3))) & 1u)) s[kb][x] = -INFINITY;
@@ -186,6 +186,11 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   }
   if (i >= t.len) return;
   sum = add_halves(sum);
+  if (!on) {  // a row that is not live has summed what it does not see
+    sum = 0.f;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d) o[d] = zero16();
+  }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a sum that is NaN stays NaN
   char* op = a.o.p + head * a.o.head + ((int64_t)t.lo + i) * a.o.tok;
 #pragma unroll

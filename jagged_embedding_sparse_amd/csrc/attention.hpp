@@ -263,6 +263,24 @@ struct Staged {
   }
 };
 
+// What a score of each key of a tile starts from: 0, or -inf for keys that
+// are not live. In the scores' accumulators keys run down the rows, so both
+// halves of the wave read theirs as they are, and no score is masked later.
+__device__ __forceinline__ void store_off(float* off, uint64_t live) {
+  if (threadIdx.x < 64) off[threadIdx.x] = (live >> threadIdx.x) & 1 ? 0.f : -INFINITY;
+}
+__device__ __forceinline__ f32x16 load_off(const float* off, int k0) {
+  const int g = lane() >> 5;
+  f32x16 r;
+#pragma unroll
+  for (int y = 0; y < 4; ++y) {
+    const f32x4 x = *(const f32x4*)(off + k0 + 8 * y + 4 * g);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) r[4 * y + z] = x[z];
+  }
+  return r;
+}
+
 // B operands of 32 rows of one head: column c = row r0 + c
 template <int DP>
 __device__ __forceinline__ void load_columns(u32x4 (&f)[DP / 16], const char* head,

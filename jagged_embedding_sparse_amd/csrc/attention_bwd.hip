@@ -75,6 +75,7 @@ template <typename T, int DP, int NW>
 __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sk[2][kStep * DP], sv[2][kStep * DP];
+  __shared__ __attribute__((aligned(16))) float s_off[2][kStep];
   const int at = blockIdx.x / a.s.heads, head = blockIdx.x % a.s.heads;
   if (at >= *a.s.n_tiles) return;
   const Tile t = tile_by_end(a.s.tiles[at], 32 * NW);
@@ -146,29 +147,29 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
     const uint64_t live = keys;
     ks.store(sk[b], a.s, live, full);
     vs.store(sv[b], a.s, live, full);
+    store_off(s_off[b], live);
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
     const bool past = causal ? j0 > i0 + 31 : j0 >= t.hist;
     if (i0 >= t1 || (past && (j0 > i0 + 31 || j0 + kStep <= i0))) continue;
-    const bool whole = live == ~0ull && j0 + kStep <= t.hist && (!causal || j0 + kStep <= i0 + 1) &&
-                       __all(on);
+    const bool whole = j0 + kStep <= t.hist && (!causal || j0 + kStep <= i0 + 1);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      f32x16 s = zero16(), dp = zero16();
+      f32x16 s = live == ~0ull ? zero16() : load_off(s_off[b], 32 * kb), dp = zero16();
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
         s = Elem<T>::mfma(rows_operand<DP>(sk[b], 32 * kb, kk), qf[kk], s);
         dp = Elem<T>::mfma(rows_operand<DP>(sv[b], 32 * kb, kk), df[kk], dp);
       }
-      uint32_t see = ~0u;
-      if (!whole)
-        see = on ? seen_keys(i, j0 + 32 * kb, t.hist, causal) & (uint32_t)(live >> (32 * kb)) : 0u;
-      see >>= 4 * g;
+      if (!whole) {
+        const uint32_t see = seen_keys(i, j0 + 32 * kb, t.hist, causal) >> (4 * g);
 #pragma unroll
-      for (int x = 0; x < 16; ++x) {
-        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], c, -lse));
-        s[x] = whole || ((see >> (8 * (x >> 2) + (x & 3))) & 1u) ? p * (dp[x] - delta) : 0.f;
+        for (int x = 0; x < 16; ++x)
+          if (!((see >> (8 * (x >> 2) + (x & 3))) & 1u)) s[x] = -INFINITY;
       }
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        s[x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], c, -lse)) * (dp[x] - delta);
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
         const u32x4 ds = to_operand<T>(s, ch);
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
       }
     }
   }
+  // a row that is not live has lse = inf, so dq = 0
   if (i < t.len)
     store_rows<T, DP>(a.dq.p + head * a.dq.head + ((int64_t)t.lo + i) * a.dq.tok, dq, a.s.dim,
                       a.s.scale);
@@ -258,7 +260,9 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
     // steps whose rows see none of this wave's keys
     if (j0 >= t1 || (causal && i0 + kStep <= j0)) continue;
     if (j0 >= t.hist && (i0 + kStep <= j0 || i0 > j0 + 31)) continue;
-    const bool whole = live == ~0ull && j0 + 32 <= t.hist && (!causal || i0 >= j0 + 31) && __all(on);
+    // rows that are not live have lse = inf, so P = 0; keys that are not live
+    // spoil only their own column, which is not stored
+    const bool whole = j0 + 32 <= t.hist && (!causal || i0 >= j0 + 31);
 #pragma unroll
     for (int ib = 0; ib < 2; ++ib) {
       f32x16 s = zero16(), dp = zero16();
@@ -267,10 +271,12 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
         s = Elem<T>::mfma(rows_operand<DP>(sq[b], 32 * ib, kk), kf[kk], s);
         dp = Elem<T>::mfma(rows_operand<DP>(sd[b], 32 * ib, kk), vf[kk], dp);
       }
-      uint32_t see = ~0u;
-      if (!whole)
-        see = on ? seeing_rows(j, i0 + 32 * ib, t.hist, causal) & (uint32_t)(live >> (32 * ib)) : 0u;
-      see >>= 4 * g;
+      if (!whole) {
+        const uint32_t see = seeing_rows(j, i0 + 32 * ib, t.hist, causal) >> (4 * g);
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          if (!((see >> (8 * (x >> 2) + (x & 3))) & 1u)) s[x] = -INFINITY;
+      }
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const f32x4 ls = *(const f32x4*)&s_lse[b][32 * ib + 8 * y + 4 * g];
@@ -278,10 +284,9 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
           const int z = 4 * y + x;
-          const bool in = whole || ((see >> (8 * y + x)) & 1u);
-          const float p = in ? __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], c, -ls[x])) : 0.f;
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], c, -ls[x]));
           s[z] = p;
-          dp[z] = in ? p * (dp[z] - de[x]) : 0.f;
+          dp[z] = p * (dp[z] - de[x]);
         }
       }
 #pragma unroll
@@ -296,6 +301,10 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
     }
   }
   if (j >= t.len) return;
+  if (!on) {
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = zero16();
+  }
   const int64_t tok = (int64_t)t.lo + j;
   if (a.splits > 1) {
     float* to = a.part + (((int64_t)part * 2 * kv_heads + kvh) * a.s.n_tok + tok) * DP;
@@ -408,10 +417,10 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
         s = Elem<T>::mfma(rows_operand<DP>(sq[b], 32 * half, kk), kf[kk], s);
         dp = Elem<T>::mfma(rows_operand<DP>(sd[b], 32 * half, kk), vf[kk], dp);
       }
-      const uint32_t half_live = (uint32_t)(live >> (32 * half));
-      if (half_live != ~0u || j0 + 32 > t.hist || (causal && r0 < j0 + 31) || !__all(on)) {
-        const uint32_t see =
-            (on ? seeing_rows(j, r0, t.hist, causal) & half_live : 0u) >> (4 * g);
+      // rows that are not live have lse = inf, so P = 0; keys that are not
+      // live spoil only their own column, which is not stored
+      if (j0 + 32 > t.hist || (causal && r0 < j0 + 31)) {
+        const uint32_t see = seeing_rows(j, r0, t.hist, causal) >> (4 * g);
 #pragma unroll
         for (int x = 0; x < 16; ++x)
           if (!((see >> (8 * (x >> 2) + (x & 3))) & 1u)) s[x] = -INFINITY;
@@ -454,6 +463,10 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
     b = b == 2 ? 0 : b + 1;
   }
   if (j >= t.len) return;
+  if (!on) {
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d) sum[d] = zero16();
+  }
   const int64_t tok = (int64_t)t.lo + j;
   if (a.splits > 1) {
     float* to = a.part + (((int64_t)part * 2 + 1 - half) * kv_heads + kvh) * a.s.n_tok * DP + tok * DP;
@@ -500,7 +513,7 @@ int launch_bwd(const BwdArgs& a, const int64_t* offsets, int32_t n, int64_t cap,
                      dim3(NW * kWave), 0, stream, a);
   FS_LAUNCH_CHECK();
   const dim3 grid((unsigned)(cap * kv_heads * a.splits));
-  if constexpr (DP >= 64)
+  if constexpr (DP == 128)
     hipLaunchKernelGGL((k_attn_dkv2<T, DP>), grid, dim3(512), 0, stream, a);
   else
     hipLaunchKernelGGL((k_attn_dkv<T, DP, NW>), grid, dim3(NW * kWave), 0, stream, a);
