@@ -73,7 +73,8 @@ struct FwdArgs {
   float* lse;
 };
 
-constexpr int kKeys = 64;  // keys per step
+constexpr int kKeys = 64;    // keys per step
+constexpr float kLazy = 8.f;  // 2^(S - m) stays at most 2^8, well inside either type
 
 template <typename T, int DP, int NW>
 __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
@@ -98,8 +99,9 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) o[d] = zero16();
   // finite, so that a row that sees nothing keeps 2^(-inf - m) = 0
-  float m = -1e30f, sum = 0.f;
+  float m = -3e38f, sum = 0.f;
   const float c = log2_scale(a.s);
+  const Operands<DP> op;
 
   // key tiles: the history, then the workgroup's own candidates
   const int hist_end = (int)cdiv(causal ? min(t.hist, t1) : t.hist, kKeys);
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
       s[kb] = live == ~0ull ? zero16() : load_off(s_off[b], 32 * kb);
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk)
-        s[kb] = Elem<T>::mfma(rows_operand<DP>(sk[b], 32 * kb, kk), qf[kk], s[kb]);
+        s[kb] = Elem<T>::mfma(op.rows(sk[b], 32 * kb, kk), qf[kk], s[kb]);
     }
     if (!whole) {
 #pragma unroll
@@ -158,21 +160,26 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int x = 0; x < 16; ++x) top = fmaxf(top, s[kb][x]);
-    top = fmaxf(max_halves(top) * c, m);
-    if (__any(top > m)) {
-      const float f = __builtin_amdgcn_exp2f(m - top);
-      m = top;
+    top = max_halves(top) * c;
+    // The running maximum only has to keep 2^(S - m) in range: it moves when a
+    // row passes it by more than kLazy, so the sums are rescaled in few steps
+    // instead of nearly all (some of 32 rows has a new maximum in most).
+    if (__any(top > m + kLazy)) {
+      const float to = fmaxf(top, m), f = __builtin_amdgcn_exp2f(m - to);
+      m = to;
       sum *= f;
 #pragma unroll
       for (int d = 0; d < DP / 32; ++d) o[d] *= f;
     }
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
       for (int x = 0; x < 16; ++x) {
         s[kb][x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][x], c, -m));
-        sum += s[kb][x];
+        part[x & 3] += s[kb][x];
       }
+    sum += (part[0] + part[1]) + (part[2] + part[3]);
     // probabilities are rounded to the operand's type (half a step each)
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
@@ -181,7 +188,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
         const u32x4 p = to_operand<T>(s[kb], ch);
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
-          o[d] = Elem<T>::mfma(cols_operand<DP>(sv[b], 32 * kb + 16 * ch, 32 * d), p, o[d]);
+          o[d] = Elem<T>::mfma(op.cols(sv[b], 32 * kb + 16 * ch, 32 * d), p, o[d]);
       }
   }
   if (i >= t.len) return;
@@ -192,7 +199,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
     for (int d = 0; d < DP / 32; ++d) o[d] = zero16();
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;  // a sum that is NaN stays NaN
-  char* op = a.o.p + head * a.o.head + ((int64_t)t.lo + i) * a.o.tok;
+  char* dst = a.o.p + head * a.o.head + ((int64_t)t.lo + i) * a.o.tok;
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
@@ -202,7 +209,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
         u32x2 v;
         v[0] = Elem<T>::pack(o[d][4 * x] * inv, o[d][4 * x + 1] * inv);
         v[1] = Elem<T>::pack(o[d][4 * x + 2] * inv, o[d][4 * x + 3] * inv);
-        *(u32x2*)(op + 2 * col) = v;
+        *(u32x2*)(dst + 2 * col) = v;
       }
     }
   if (g == 0)

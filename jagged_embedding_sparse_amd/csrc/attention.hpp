@@ -98,17 +98,21 @@ __device__ __forceinline__ float add_halves(float x) {
 
 // ---------------------------------------------------------------- LDS tiles
 // A tile of rows of DP elements (2 bytes each; DP = 32, 64 or 128) without
-// padding. The 16-byte pieces of a row are permuted by the row so that both
-// reads below touch every bank equally often: piece p of row r lies at
-// p ^ swz(r). Rows of 128 bytes or more start at the same bank, so the eight
-// rows r..r+7 take eight different pieces; the lowest row bit goes to the
-// piece's highest, which puts two of four neighbouring rows into each half of
-// the banks (the transposing read takes four neighbouring rows at a time).
-// 64-byte rows alternate between the two halves by themselves.
+// padding. The 16-byte pieces of a row are permuted by the row, so that both
+// reads below meet every bank equally often (a row of 256 bytes spans the
+// banks once): piece p of row r lies at p ^ swz(r).
+//  - A read of one piece of 16 neighbouring rows should find 16 different
+//    places in 256 bytes. Rows are 1, 2 or 4 to 256 bytes; the row's higher
+//    bits choose among the pieces of its part.
+//  - The transposing read takes 64 bytes of 4 neighbouring rows, which should
+//    lie in 4 different quarters: the row's lowest bits go to the piece's
+//    highest.
+// Measured on this card with the counters of bank conflicts: see the kernels.
 template <int DP>
 __device__ __forceinline__ int swz(int r) {
-  if constexpr (DP == 32) return (r >> 1) & 3;
-  return ((r & 1) << 2) | ((r >> 1) & 3);
+  if constexpr (DP == 32) return (r >> 2) & 3;
+  if constexpr (DP == 64) return (r & 2) << 1 | ((r >> 2) & 3);
+  return (r & 3) << 2 | ((r >> 2) & 3);
 }
 
 // piece p (8 elements) of row r, as an element offset
@@ -117,27 +121,33 @@ __device__ __forceinline__ int piece(int r, int p) {
   return r * DP + ((p ^ swz<DP>(r)) << 3);
 }
 
-// A operand: rows r0 .. r0 + 31, elements 16 kk .. 16 kk + 15
+// The two operand reads. Rows enter as multiples of 16, which do not change
+// the permutation, so what depends on the lane is one offset, and pieces
+// differ from it by exclusive-or with constants.
 template <int DP>
-__device__ __forceinline__ u32x4 rows_operand(const uint16_t* tile, int r0, int kk) {
-  const int l = lane();
-  return *(const u32x4*)(tile + piece<DP>(r0 + (l & 31), 2 * kk + (l >> 5)));
-}
-
-// A operand of the transposed tile: its rows are the tile's columns
-// c0 .. c0 + 31, its k-slots the tile's rows r0 .. r0 + 15 in the order of
-// to_operand
-template <int DP>
-__device__ __forceinline__ u32x4 cols_operand(const uint16_t* tile, int r0, int c0) {
-  const int l = lane(), g = l >> 5, j = l & 15;
-  const int col = c0 + (l & 16) + 4 * (j & 3);
-  const int row = r0 + 4 * g + (j >> 2);
-  const uint16_t* a = tile + piece<DP>(row, col >> 3) + (col & 7);
-  const uint16_t* b = tile + piece<DP>(row + 8, col >> 3) + (col & 7);
-  const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a));
-  const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)b));
-  return u32x4{lo[0], lo[1], hi[0], hi[1]};
-}
+struct Operands {
+  int rows_at, cols_at;
+  __device__ __forceinline__ Operands() {
+    const int l = lane(), g = l >> 5, j = l & 15;
+    rows_at = piece<DP>(l & 31, g);
+    const int col = (l & 16) + 4 * (j & 3);
+    cols_at = piece<DP>(4 * g + (j >> 2), col >> 3) + (col & 7);
+  }
+  // A operand: rows r0 .. r0 + 31 (r0 a multiple of 32), elements 16 kk .. + 15
+  __device__ __forceinline__ u32x4 rows(const uint16_t* tile, int r0, int kk) const {
+    return *(const u32x4*)(tile + (rows_at ^ (16 * kk)) + r0 * DP);
+  }
+  // A operand of the transposed tile: its rows are the tile's columns c0 ..
+  // c0 + 31, its k-slots the tile's rows r0 .. r0 + 15 in the order of
+  // to_operand. Rows 8 apart differ in bit 1 of the permutation alone.
+  __device__ __forceinline__ u32x4 cols(const uint16_t* tile, int r0, int c0) const {
+    const uint16_t* a = tile + (cols_at ^ c0) + r0 * DP;
+    const uint16_t* b = tile + (cols_at ^ c0 ^ 16) + (r0 + 8) * DP;
+    const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a));
+    const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)b));
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+  }
+};
 
 // ---------------------------------------------------------------- samples
 // One tile of rows of one sample: rows t0 .. of the sample whose tokens start

@@ -94,10 +94,10 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
   // delta: each half of the wave holds half of a row's columns
   float delta = 0.f;
   {
-    const char* op = a.o.p + head * a.o.head;
+    const char* outp = a.o.p + head * a.o.head;
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
-      const u32x4 x = load_piece(op, a.o.tok, a.s, t, i, 2 * kk + g, on);
+      const u32x4 x = load_piece(outp, a.o.tok, a.s, t, i, 2 * kk + g, on);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const f32x2 u = Elem<T>::unpack(x[e]), y = Elem<T>::unpack(df[kk][e]);
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) dq[d] = zero16();
   const float c = log2_scale(a.s);
+  const Operands<DP> op;
 
   const int hist_end = (int)cdiv(causal ? min(t.hist, t1) : t.hist, kStep);
   const int own_lo = max(hist_end, max(t.t0, t.hist) / kStep);
@@ -158,8 +159,8 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
       f32x16 s = live == ~0ull ? zero16() : load_off(s_off[b], 32 * kb), dp = zero16();
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
-        s = Elem<T>::mfma(rows_operand<DP>(sk[b], 32 * kb, kk), qf[kk], s);
-        dp = Elem<T>::mfma(rows_operand<DP>(sv[b], 32 * kb, kk), df[kk], dp);
+        s = Elem<T>::mfma(op.rows(sk[b], 32 * kb, kk), qf[kk], s);
+        dp = Elem<T>::mfma(op.rows(sv[b], 32 * kb, kk), df[kk], dp);
       }
       if (!whole) {
         const uint32_t see = seen_keys(i, j0 + 32 * kb, t.hist, causal) >> (4 * g);
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
         const u32x4 ds = to_operand<T>(s, ch);
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d)
-          dq[d] = Elem<T>::mfma(cols_operand<DP>(sk[b], 32 * kb + 16 * ch, 32 * d), ds, dq[d]);
+          dq[d] = Elem<T>::mfma(op.cols(sk[b], 32 * kb + 16 * ch, 32 * d), ds, dq[d]);
       }
     }
   }
@@ -211,6 +212,7 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = zero16();
   const float c = log2_scale(a.s);
+  const Operands<DP> op;
 
   // rows that see a key of this tile: from the tile on where causal, all of
   // them otherwise; only its own where it holds candidates alone
@@ -268,8 +270,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
       f32x16 s = zero16(), dp = zero16();
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
-        s = Elem<T>::mfma(rows_operand<DP>(sq[b], 32 * ib, kk), kf[kk], s);
-        dp = Elem<T>::mfma(rows_operand<DP>(sd[b], 32 * ib, kk), vf[kk], dp);
+        s = Elem<T>::mfma(op.rows(sq[b], 32 * ib, kk), kf[kk], s);
+        dp = Elem<T>::mfma(op.rows(sd[b], 32 * ib, kk), vf[kk], dp);
       }
       if (!whole) {
         const uint32_t see = seeing_rows(j, i0 + 32 * ib, t.hist, causal) >> (4 * g);
@@ -294,8 +296,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
         const u32x4 pb = to_operand<T>(s, ch), db = to_operand<T>(dp, ch);
 #pragma unroll
         for (int d = 0; d < DP / 32; ++d) {
-          dv[d] = Elem<T>::mfma(cols_operand<DP>(sd[b], 32 * ib + 16 * ch, 32 * d), pb, dv[d]);
-          dk[d] = Elem<T>::mfma(cols_operand<DP>(sq[b], 32 * ib + 16 * ch, 32 * d), db, dk[d]);
+          dv[d] = Elem<T>::mfma(op.cols(sd[b], 32 * ib + 16 * ch, 32 * d), pb, dv[d]);
+          dk[d] = Elem<T>::mfma(op.cols(sq[b], 32 * ib + 16 * ch, 32 * d), db, dk[d]);
         }
       }
     }
@@ -356,6 +358,7 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) sum[d] = zero16();
   const float c = log2_scale(a.s);
+  const Operands<DP> op;
 
   const bool own = t.t0 >= t.hist;
   const int first = (own || causal ? t.t0 : 0) / kStep;
@@ -414,8 +417,8 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
       s = dp = zero16();
 #pragma unroll
       for (int kk = 0; kk < DP / 16; ++kk) {
-        s = Elem<T>::mfma(rows_operand<DP>(sq[b], 32 * half, kk), kf[kk], s);
-        dp = Elem<T>::mfma(rows_operand<DP>(sd[b], 32 * half, kk), vf[kk], dp);
+        s = Elem<T>::mfma(op.rows(sq[b], 32 * half, kk), kf[kk], s);
+        dp = Elem<T>::mfma(op.rows(sd[b], 32 * half, kk), vf[kk], dp);
       }
       // rows that are not live have lse = inf, so P = 0; keys that are not
       // live spoil only their own column, which is not stored
@@ -435,7 +438,7 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
           const u32x4 x = ib == half ? mine[ch] : ex[e ^ 1][w ^ 4][ch][l];
 #pragma unroll
           for (int d = 0; d < DP / 32; ++d)
-            sum[d] = Elem<T>::mfma(cols_operand<DP>(tile, 32 * ib + 16 * ch, 32 * d), x, sum[d]);
+            sum[d] = Elem<T>::mfma(op.cols(tile, 32 * ib + 16 * ch, 32 * d), x, sum[d]);
         }
     }
     if (!none) {
