@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
     const uint64_t live = keys;
     ks.store(sk[b], a.s, live, full);
     vs.store(sv[b], a.s, live, full);
-    store_off(s_off[b], live);
+    if (live != ~0ull) store_off(s_off[b], live);
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
     // tiles that none of this wave's rows sees
@@ -141,9 +141,13 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
     f32x16 s[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      s[kb] = live == ~0ull ? zero16() : load_off(s_off[b], 32 * kb);
+      // both start a product, the first with a zero that takes no registers
+      if (live == ~0ull)
+        s[kb] = Elem<T>::mfma(op.rows(sk[b], 32 * kb, 0), qf[0], zero16());
+      else
+        s[kb] = Elem<T>::mfma(op.rows(sk[b], 32 * kb, 0), qf[0], load_off(s_off[b], 32 * kb));
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk)
+      for (int kk = 1; kk < DP / 16; ++kk)
         s[kb] = Elem<T>::mfma(op.rows(sk[b], 32 * kb, kk), qf[kk], s[kb]);
     }
     if (!whole) {

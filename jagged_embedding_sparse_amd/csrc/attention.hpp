@@ -263,12 +263,20 @@ struct Staged {
   __device__ __forceinline__ void store(uint16_t* tile, const Shape& a, uint64_t live,
                                         bool whole) const {
     const int row = threadIdx.x / kPieces, p = threadIdx.x % kPieces;
+    if (whole) {
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) {
-      const int r = row + x * kStepRows;
-      u32x4 y = v[x];
-      if (!whole && (!((live >> r) & 1) || 8 * p >= a.dim)) y = u32x4{0, 0, 0, 0};
-      *(u32x4*)(tile + piece<DP>(r, p)) = y;
+      for (int x = 0; x < kPer; ++x) *(u32x4*)(tile + piece<DP>(row + x * kStepRows, p)) = v[x];
+    } else {
+      const bool in = 8 * p < a.dim;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x) {
+        const int r = row + x * kStepRows;
+        const bool keep = in & (((live >> r) & 1) != 0);
+        u32x4 y;
+#pragma unroll
+        for (int z = 0; z < 4; ++z) y[z] = keep ? v[x][z] : 0u;
+        *(u32x4*)(tile + piece<DP>(r, p)) = y;
+      }
     }
   }
 };

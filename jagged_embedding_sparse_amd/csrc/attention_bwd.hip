@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
     const uint64_t live = keys;
     ks.store(sk[b], a.s, live, full);
     vs.store(sv[b], a.s, live, full);
-    store_off(s_off[b], live);
+    if (live != ~0ull) store_off(s_off[b], live);
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
     const bool past = causal ? j0 > i0 + 31 : j0 >= t.hist;
