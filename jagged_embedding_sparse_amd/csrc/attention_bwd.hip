@@ -72,7 +72,7 @@ __device__ __forceinline__ void store_rows(char* row, const f32x16 (&x)[DP / 32]
 // row per lane, so lse and delta are one register each and dS^T is the operand
 // of dQ^T = k^T dS^T.
 template <typename T, int DP, int NW>
-__global__ void __launch_bounds__(NW * kWave, 2) k_attn_dq(BwdArgs a) {
+__global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdArgs a) {
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sk[2][kStep * DP], sv[2][kStep * DP];
   __shared__ __attribute__((aligned(16))) float s_off[2][kStep];
