@@ -18,49 +18,73 @@ namespace {
 constexpr int kTableThreads = 1024;
 constexpr int kBuckets = 256;
 
-// One workgroup: one descriptor per tile of each sample, those with the most
-// steps first, so that the last ones to start are short and the workgroups
-// end together. A tile's steps are what a causal pass over rows t0 + rows - 1
-// and before, or t0 and after, takes (tile_by_end turns one into the other);
-// without causal every tile of a sample takes as many as its sample has.
-// Tiles with equally many (or kBuckets and more) come in any order, which
-// changes no result. Offsets that do not rise inside [0, n_tok] would let
-// samples overlap (and outgrow the table): then there are no tiles.
+// One workgroup per table: one descriptor per tile of each sample, those with
+// the most steps first, so that the last ones to start are short and the
+// workgroups end together. A tile's steps are what a causal pass over rows t0
+// + rows - 1 and before, or t0 and after, takes (tile_by_end turns one into
+// the other); without causal every tile of a sample takes as many as its
+// sample has. Tiles with equally many (or kBuckets and more) come in any
+// order, which changes no result. Offsets that do not rise inside [0, n_tok]
+// would let samples overlap (and outgrow the table): then there are no tiles.
+// Threads run over tiles, not samples, so one long sample takes no longer
+// than many short ones.
 __global__ void __launch_bounds__(kTableThreads)
 k_attn_tiles(const int64_t* __restrict__ offsets, int32_t n, int64_t n_tok,
-             const int32_t* __restrict__ n_cand, int32_t rows, int32_t causal,
-             Tile* __restrict__ tiles, int32_t* __restrict__ n_tiles, int32_t* __restrict__ err) {
+             const int32_t* __restrict__ n_cand, int32_t causal, TileTable t0, TileTable t1,
+             int32_t* __restrict__ err) {
   __shared__ int32_t first[kBuckets], tmp[17];
+  __shared__ int32_t s_lo[kTableThreads], s_len[kTableThreads], s_cand[kTableThreads];
+  __shared__ int32_t s_at[kTableThreads + 1];
+  const TileTable t = blockIdx.x ? t1 : t0;
   bool bad = false, order = true;
   if (threadIdx.x < kBuckets) first[threadIdx.x] = 0;
   for (int32_t s = threadIdx.x; s < n; s += kTableThreads)
     order &= offsets[s] >= 0 && offsets[s] <= offsets[s + 1] && offsets[s + 1] <= n_tok;
   if (__syncthreads_or(!order)) {
     flag_err(err, !order, FS_EF_SHAPE);
-    if (threadIdx.x == 0) *n_tiles = 0;
+    if (threadIdx.x == 0) *t.n = 0;
     return;
   }
   // pass 0 counts the tiles of each bucket, pass 1 places them
   for (int pass = 0; pass < 2; ++pass) {
-    for (int32_t s = threadIdx.x; s < n; s += kTableThreads) {
-      const int32_t lo = (int32_t)offsets[s], len = (int32_t)(offsets[s + 1] - lo);
-      int32_t cand = n_cand ? n_cand[s] : 0;
-      bad |= cand < 0 || cand > len;
-      cand = min(max(cand, 0), len);
-      const int32_t cnt = (int32_t)cdiv(len, rows);
-      for (int32_t k = 0; k < cnt; ++k) {
-        const int32_t b = kBuckets - min(causal ? cnt - k : cnt, kBuckets);
-        const int32_t at = atomicAdd(&first[b], 1);
-        if (pass) tiles[at] = Tile{lo, len, len - cand, k * rows};
+    for (int32_t c0 = 0; c0 < n; c0 += kTableThreads) {  // uniform
+      const int32_t s = c0 + threadIdx.x, left = min(n - c0, kTableThreads);
+      if (n > kTableThreads || pass == 0) {  // one chunk stays in LDS for the second pass
+        int32_t lo = 0, len = 0, cand = 0;
+        if (s < n) {
+          lo = (int32_t)offsets[s];
+          len = (int32_t)(offsets[s + 1] - lo);
+          cand = n_cand ? n_cand[s] : 0;
+          bad |= cand < 0 || cand > len;
+          cand = min(max(cand, 0), len);
+        }
+        int32_t total;
+        const int32_t at = block_excl_scan<int32_t>((int32_t)cdiv(len, t.rows), tmp, &total);
+        s_lo[threadIdx.x] = lo;
+        s_len[threadIdx.x] = len;
+        s_cand[threadIdx.x] = cand;
+        s_at[threadIdx.x] = at;
+        if (threadIdx.x == 0) s_at[kTableThreads] = total;
+        __syncthreads();
       }
+      for (int32_t e = threadIdx.x; e < s_at[kTableThreads]; e += kTableThreads) {
+        int32_t a = 0, b = left - 1;  // the last sample that starts at or before tile e
+        while (a < b) {
+          const int32_t mid = (a + b + 1) >> 1;
+          if (s_at[mid] <= e) a = mid; else b = mid - 1;
+        }
+        const int32_t len = s_len[a], k = e - s_at[a], cnt = (int32_t)cdiv(len, t.rows);
+        const int32_t at = atomicAdd(&first[kBuckets - min(causal ? cnt - k : cnt, kBuckets)], 1);
+        if (pass) t.tiles[at] = Tile{s_lo[a], len, len - s_cand[a], k * t.rows};
+      }
+      __syncthreads();
     }
-    __syncthreads();
     if (pass == 0) {
       int32_t total;
       const int32_t x = threadIdx.x < kBuckets ? first[threadIdx.x] : 0;
       const int32_t ex = block_excl_scan<int32_t>(x, tmp, &total);
       if (threadIdx.x < kBuckets) first[threadIdx.x] = ex;
-      if (threadIdx.x == 0) *n_tiles = total;
+      if (threadIdx.x == 0) *t.n = total;
       __syncthreads();
     }
   }
@@ -81,15 +105,16 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sk[2][kKeys * DP], sv[2][kKeys * DP];
   __shared__ __attribute__((aligned(16))) float s_off[2][kKeys];
-  const int at = blockIdx.x / a.s.heads, head = blockIdx.x % a.s.heads;
-  if (at >= *a.s.n_tiles) return;
-  const Tile t = tile_by_end(a.s.tiles[at], 32 * NW);
+  const int l = lane(), w = wave_id(), g = l >> 5;
+  const int rows = 32 * NW / a.s.pack, packs = a.s.heads / a.s.pack;  // see pack_of
+  const int at = blockIdx.x / packs, head = blockIdx.x % packs * a.s.pack + w % a.s.pack;
+  if (at >= *a.s.tab.n) return;
+  const Tile t = tile_by_end(a.s.tab.tiles[at], rows);
   const int kvh = head / a.s.group;
   const char* kp = a.k.p + kvh * a.k.head;
   const char* vp = a.v.p + kvh * a.v.head;
-  const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
-  const int t1 = min(t.t0 + 32 * NW, t.len);  // the workgroup's rows: [t0, t1)
-  const int i0 = t.t0 + 32 * w, i = i0 + (l & 31);
+  const int t1 = min(t.t0 + rows, t.len);  // the workgroup's rows: [t0, t1)
+  const int i0 = t.t0 + 32 * (w / a.s.pack), i = i0 + (l & 31);
   const bool on = live_row(a.s, t, i);
   const bool causal = a.s.causal != 0;
 
@@ -248,10 +273,10 @@ int make_view(const fs_heads* x, int32_t heads, int32_t dim, View* v) {
 }
 
 int launch_tiles(const int64_t* offsets, int32_t n, int64_t n_tok, const int32_t* n_cand,
-                 int32_t rows, int32_t causal, Tile* tiles, int32_t* n_tiles, int32_t* err,
+                 int32_t causal, const TileTable* t, int32_t tables, int32_t* err,
                  hipStream_t stream) {
-  hipLaunchKernelGGL(k_attn_tiles, dim3(1), dim3(kTableThreads), 0, stream, offsets, n, n_tok,
-                     n_cand, rows, causal, tiles, n_tiles, err);
+  hipLaunchKernelGGL(k_attn_tiles, dim3((unsigned)tables), dim3(kTableThreads), 0, stream, offsets,
+                     n, n_tok, n_cand, causal, t[0], t[tables - 1], err);
   FS_LAUNCH_CHECK();
   return FS_OK;
 }
@@ -290,19 +315,21 @@ extern "C" int fs_jagged_attention(const fs_heads* q, const fs_heads* k, const f
     return FS_ERR_INVALID_ARG;
   if (!ws || ws_bytes < fs_jagged_attention_workspace_size(n_tok, n)) return FS_ERR_WORKSPACE;
   if (n == 0 || n_tok == 0) return FS_OK;
-  constexpr int32_t rows = 128;
-  if (tile_cap(n_tok, n, rows) * heads >= (int64_t)INT32_MAX) return FS_ERR_UNSUPPORTED;
+  const int32_t pack = pack_of(heads / kv_heads), rows = 128 / pack;
+  const int64_t cap = tile_cap(n_tok, n, rows), grid = cap * (heads / pack);
+  if (grid >= (int64_t)INT32_MAX) return FS_ERR_UNSUPPORTED;
   Carve c(ws);
-  int32_t* n_tiles = c.take<int32_t>(1);
-  Tile* tiles = c.take<Tile>((size_t)tile_cap(n_tok, n, rows));
-  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, rows, causal, tiles, n_tiles, err, stream))) return rc;
-  a.s = Shape{tiles, n_tiles, valid, n_tok, heads, heads / kv_heads, dim, causal, scale};
+  TileTable tab;
+  tab.rows = rows;
+  tab.n = c.take<int32_t>(1);
+  tab.tiles = c.take<Tile>((size_t)cap);
+  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, causal, &tab, 1, err, stream))) return rc;
+  a.s = Shape{tab, valid, n_tok, heads, heads / kv_heads, pack, dim, causal, scale};
   a.lse = lse;
-  const dim3 grid((unsigned)(tile_cap(n_tok, n, rows) * heads));
   if (dtype == FS_BF16)
-    launch_fwd<__bf16>(a, grid, stream);
+    launch_fwd<__bf16>(a, dim3((unsigned)grid), stream);
   else
-    launch_fwd<_Float16>(a, grid, stream);
+    launch_fwd<_Float16>(a, dim3((unsigned)grid), stream);
   FS_LAUNCH_CHECK();
   return FS_OK;
 }

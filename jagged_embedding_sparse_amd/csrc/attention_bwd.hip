@@ -21,6 +21,7 @@ constexpr int kStep = 64;  // rows or keys per step
 struct BwdArgs {
   Shape s;
   View q, k, v, o, d_o, dq, dk, dv;
+  TileTable keys;    // 128 keys each
   const float* lse;  // [heads][n_tok]
   float* delta;      // [heads][n_tok]
   float* part;       // [splits][2][kv_heads][n_tok][DP]: dK (unscaled) and dV
@@ -76,15 +77,16 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sk[2][kStep * DP], sv[2][kStep * DP];
   __shared__ __attribute__((aligned(16))) float s_off[2][kStep];
-  const int at = blockIdx.x / a.s.heads, head = blockIdx.x % a.s.heads;
-  if (at >= *a.s.n_tiles) return;
-  const Tile t = tile_by_end(a.s.tiles[at], 32 * NW);
+  const int l = lane(), w = wave_id(), g = l >> 5;
+  const int rows = 32 * NW / a.s.pack, packs = a.s.heads / a.s.pack;  // see pack_of
+  const int at = blockIdx.x / packs, head = blockIdx.x % packs * a.s.pack + w % a.s.pack;
+  if (at >= *a.s.tab.n) return;
+  const Tile t = tile_by_end(a.s.tab.tiles[at], rows);
   const int kvh = head / a.s.group;
   const char* kp = a.k.p + kvh * a.k.head;
   const char* vp = a.v.p + kvh * a.v.head;
-  const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
-  const int t1 = min(t.t0 + 32 * NW, t.len);
-  const int i0 = t.t0 + 32 * w, i = i0 + (l & 31);
+  const int t1 = min(t.t0 + rows, t.len);
+  const int i0 = t.t0 + 32 * (w / a.s.pack), i = i0 + (l & 31);
   const bool on = live_row(a.s, t, i);
   const bool causal = a.s.causal != 0;
 
@@ -197,9 +199,9 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
   const int kv_heads = a.s.heads / a.s.group;
   const int kvh = blockIdx.x % kv_heads, part = blockIdx.x / kv_heads % a.splits;
   const int at = blockIdx.x / kv_heads / a.splits;
-  if (at >= *a.s.n_tiles) return;
-  const Tile t = a.s.tiles[at];
-  const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
+  if (at >= *a.keys.n) return;
+  const Tile t = a.keys.tiles[at];
+  const int l = lane(), w = wave_id(), g = l >> 5;
   const int t1 = min(t.t0 + 32 * NW, t.len);
   const int j0 = t.t0 + 32 * w, j = j0 + (l & 31);
   const bool on = live_row(a.s, t, j);
@@ -342,9 +344,9 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
   const int kv_heads = a.s.heads / a.s.group;
   const int kvh = blockIdx.x % kv_heads, part = blockIdx.x / kv_heads % a.splits;
   const int at = blockIdx.x / kv_heads / a.splits;
-  if (at >= *a.s.n_tiles) return;
-  const Tile t = a.s.tiles[at];
-  const int l = lane(), w = threadIdx.x / kWave, g = l >> 5;
+  if (at >= *a.keys.n) return;
+  const Tile t = a.keys.tiles[at];
+  const int l = lane(), w = wave_id(), g = l >> 5;
   const int half = w >> 2;  // which 32 rows of a step, and dV (0) or dK (1)
   const int t1 = min(t.t0 + 128, t.len);
   const int j0 = t.t0 + 32 * (w & 3), j = j0 + (l & 31);
@@ -490,7 +492,7 @@ template <typename T, int DP>
 __global__ void __launch_bounds__(256) k_attn_join(BwdArgs a, const int64_t* __restrict__ offsets,
                                                    int32_t n) {
   constexpr int kPer = DP / 4;
-  if (*a.s.n_tiles == 0) return;  // no samples, or offsets that do not rise
+  if (*a.keys.n == 0) return;  // no samples, or offsets that do not rise
   const int kv_heads = a.s.heads / a.s.group;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int col = (int)(id % kPer) * 4;
@@ -508,14 +510,14 @@ __global__ void __launch_bounds__(256) k_attn_join(BwdArgs a, const int64_t* __r
 }
 
 template <typename T, int DP>
-int launch_bwd(const BwdArgs& a, const int64_t* offsets, int32_t n, int64_t cap,
+int launch_bwd(const BwdArgs& a, const int64_t* offsets, int32_t n, int64_t row_cap, int64_t key_cap,
                hipStream_t stream) {
   constexpr int NW = 4;
   const int64_t kv_heads = a.s.heads / a.s.group;
-  hipLaunchKernelGGL((k_attn_dq<T, DP, NW>), dim3((unsigned)(cap * a.s.heads)),
+  hipLaunchKernelGGL((k_attn_dq<T, DP, NW>), dim3((unsigned)(row_cap * (a.s.heads / a.s.pack))),
                      dim3(NW * kWave), 0, stream, a);
   FS_LAUNCH_CHECK();
-  const dim3 grid((unsigned)(cap * kv_heads * a.splits));
+  const dim3 grid((unsigned)(key_cap * kv_heads * a.splits));
   if constexpr (DP == 128)
     hipLaunchKernelGGL((k_attn_dkv2<T, DP>), grid, dim3(512), 0, stream, a);
   else
@@ -531,11 +533,11 @@ int launch_bwd(const BwdArgs& a, const int64_t* offsets, int32_t n, int64_t cap,
 }
 
 template <typename T>
-int launch_bwd(const BwdArgs& a, const int64_t* offsets, int32_t n, int64_t cap,
+int launch_bwd(const BwdArgs& a, const int64_t* offsets, int32_t n, int64_t row_cap, int64_t key_cap,
                hipStream_t stream) {
-  if (padded(a.s.dim) == 32) return launch_bwd<T, 32>(a, offsets, n, cap, stream);
-  if (padded(a.s.dim) == 64) return launch_bwd<T, 64>(a, offsets, n, cap, stream);
-  return launch_bwd<T, 128>(a, offsets, n, cap, stream);
+  if (padded(a.s.dim) == 32) return launch_bwd<T, 32>(a, offsets, n, row_cap, key_cap, stream);
+  if (padded(a.s.dim) == 64) return launch_bwd<T, 64>(a, offsets, n, row_cap, key_cap, stream);
+  return launch_bwd<T, 128>(a, offsets, n, row_cap, key_cap, stream);
 }
 
 }  // namespace
@@ -552,6 +554,8 @@ extern "C" size_t fs_jagged_attention_backward_workspace_size(int64_t n_tok, int
   Carve c(nullptr);
   c.take<int32_t>(1);
   c.take<Tile>((size_t)tile_cap(n_tok, n, 32));
+  c.take<int32_t>(1);
+  c.take<Tile>((size_t)tile_cap(n_tok, n, 128));
   c.take<float>((size_t)heads * (size_t)n_tok);
   c.take<float>((size_t)split_tokens(n_tok, kv_heads) * 2 * kv_heads * padded(dim));
   return c.used + 256;
@@ -581,18 +585,26 @@ extern "C" int fs_jagged_attention_backward(
   if (!ws || ws_bytes < fs_jagged_attention_backward_workspace_size(n_tok, n, heads, kv_heads, dim))
     return FS_ERR_WORKSPACE;
   if (n == 0 || n_tok == 0) return FS_OK;
-  constexpr int32_t rows = 128;
+  const int32_t pack = pack_of(heads / kv_heads), rows = 128 / pack;
+  const int64_t row_cap = tile_cap(n_tok, n, rows), key_cap = tile_cap(n_tok, n, 128);
+  a.splits = splits_of(n_tok, kv_heads);
+  if (row_cap * (heads / pack) >= (int64_t)INT32_MAX ||
+      key_cap * kv_heads * a.splits >= (int64_t)INT32_MAX)
+    return FS_ERR_UNSUPPORTED;
   Carve c(ws);
-  int32_t* n_tiles = c.take<int32_t>(1);
-  Tile* tiles = c.take<Tile>((size_t)tile_cap(n_tok, n, 32));
+  TileTable tabs[2];
+  tabs[0].rows = rows;
+  tabs[0].n = c.take<int32_t>(1);
+  tabs[0].tiles = c.take<Tile>((size_t)tile_cap(n_tok, n, 32));
+  tabs[1].rows = 128;
+  tabs[1].n = c.take<int32_t>(1);
+  tabs[1].tiles = c.take<Tile>((size_t)key_cap);
   a.lse = lse;
   a.delta = c.take<float>((size_t)heads * (size_t)n_tok);
-  a.splits = splits_of(n_tok, kv_heads);
   a.part = c.take<float>((size_t)split_tokens(n_tok, kv_heads) * 2 * kv_heads * padded(dim));
-  const int64_t cap = tile_cap(n_tok, n, rows);
-  if (cap * heads >= (int64_t)INT32_MAX || cap * kv_heads * a.splits >= (int64_t)INT32_MAX) return FS_ERR_UNSUPPORTED;
-  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, rows, causal, tiles, n_tiles, err, stream))) return rc;
-  a.s = Shape{tiles, n_tiles, valid, n_tok, heads, heads / kv_heads, dim, causal, scale};
-  return dtype == FS_BF16 ? launch_bwd<__bf16>(a, offsets, n, cap, stream)
-                          : launch_bwd<_Float16>(a, offsets, n, cap, stream);
+  if ((rc = launch_tiles(offsets, n, n_tok, n_cand, causal, tabs, 2, err, stream))) return rc;
+  a.s = Shape{tabs[0], valid, n_tok, heads, heads / kv_heads, pack, dim, causal, scale};
+  a.keys = tabs[1];
+  return dtype == FS_BF16 ? launch_bwd<__bf16>(a, offsets, n, row_cap, key_cap, stream)
+                          : launch_bwd<_Float16>(a, offsets, n, row_cap, key_cap, stream);
 }
