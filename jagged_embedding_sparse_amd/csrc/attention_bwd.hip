@@ -111,15 +111,9 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   }
   // a row that sees nothing has lse = -inf: 2^(S - inf) = 0
   float lse = INFINITY;
-  if (i < t.len) {
-    const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
-    if (g == 0) a.delta[at] = delta;
-    if (on) lse = a.lse[at];
-    lse = lse == -INFINITY ? INFINITY : lse * kLog2e;
-  }
-  f32x16 dq[DP / 32];
-#pragma unroll
-  for (int d = 0; d < DP / 32; ++d) dq[d] = zero16();
+  const int64_t lse_at = (int64_t)head * a.s.n_tok + t.lo + i;
+  if (on) lse = a.lse[lse_at];
+  lse = lse == -INFINITY ? INFINITY : lse * kLog2e;
   const float c = log2_scale(a.s);
   const Operands<DP> op;
 
@@ -128,8 +122,56 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   const int own_end = t1 > t.hist ? (int)cdiv(t1, kStep) : 0;
   const int steps = hist_end + max(0, own_end - own_lo);
   auto key0 = [&](int step) { return (step < hist_end ? step : own_lo + step - hist_end) * kStep; };
+  // The scores of 32 keys of a staged tile and their dP, masked
+  auto scores = [&](int j0, int b, int kb, uint64_t live, f32x16& s, f32x16& dp) {
+    s = live == ~0ull ? zero16() : load_off(s_off[b], 32 * kb);
+    dp = zero16();
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+      s = Elem<T>::mfma(op.rows(sk[b], 32 * kb, kk), qf[kk], s);
+      dp = Elem<T>::mfma(op.rows(sv[b], 32 * kb, kk), df[kk], dp);
+    }
+    if (j0 + kStep > t.hist || (causal && j0 + kStep > i0 + 1)) {
+      const uint32_t see = seen_keys(i, j0 + 32 * kb, t.hist, causal) >> (4 * g);
+#pragma unroll
+      for (int x = 0; x < 16; ++x)
+        if (!((see >> (8 * (x >> 2) + (x & 3))) & 1u)) s[x] = -INFINITY;
+    }
+  };
 
   Staged<DP, NT> ks, vs;
+  // delta comes with the rounding of out to 16 bits. Where a row sees few keys,
+  // out is as large as v and that is as much as all of dS's own rounding: rows
+  // of at most two steps sum delta = sum_j P_ij dP_ij first, in fp32.
+  if (steps <= 2) {
+    delta = 0.f;
+    for (int step = 0; step < steps; ++step) {
+      const int j0 = key0(step);
+      const uint64_t live = live_bits(live_byte(a.s, t, j0));
+      const bool full = live == ~0ull && a.s.dim == DP;
+      ks.load(kp, a.k.tok, a.s, t, j0, full);
+      vs.load(vp, a.v.tok, a.s, t, j0, full);
+      ks.store(sk[0], a.s, live, full);
+      vs.store(sv[0], a.s, live, full);
+      if (live != ~0ull) store_off(s_off[0], live);
+      __syncthreads();
+#pragma unroll 1
+      for (int kb = 0; kb < 2; ++kb) {
+        f32x16 s, dp;
+        scores(j0, 0, kb, live, s, dp);
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          delta = __builtin_fmaf(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x], c, -lse)), dp[x], delta);
+      }
+      __syncthreads();
+    }
+    delta = add_halves(delta);
+  }
+  if (g == 0 && i < t.len) a.delta[lse_at] = delta;
+  f32x16 dq[DP / 32];
+#pragma unroll
+  for (int d = 0; d < DP / 32; ++d) dq[d] = zero16();
+
   uint64_t keys = 0;
   uint32_t ahead = 0;
   bool full = false;
@@ -155,21 +197,10 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
     if (step + 1 < steps) load(step + 1);
     const bool past = causal ? j0 > i0 + 31 : j0 >= t.hist;
     if (i0 >= t1 || (past && (j0 > i0 + 31 || j0 + kStep <= i0))) continue;
-    const bool whole = j0 + kStep <= t.hist && (!causal || j0 + kStep <= i0 + 1);
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      f32x16 s = live == ~0ull ? zero16() : load_off(s_off[b], 32 * kb), dp = zero16();
-#pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
-        s = Elem<T>::mfma(op.rows(sk[b], 32 * kb, kk), qf[kk], s);
-        dp = Elem<T>::mfma(op.rows(sv[b], 32 * kb, kk), df[kk], dp);
-      }
-      if (!whole) {
-        const uint32_t see = seen_keys(i, j0 + 32 * kb, t.hist, causal) >> (4 * g);
-#pragma unroll
-        for (int x = 0; x < 16; ++x)
-          if (!((see >> (8 * (x >> 2) + (x & 3))) & 1u)) s[x] = -INFINITY;
-      }
+      f32x16 s, dp;
+      scores(j0, b, kb, live, s, dp);
 #pragma unroll
       for (int x = 0; x < 16; ++x)
         s[x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], c, -lse)) * (dp[x] - delta);
