@@ -133,13 +133,13 @@ struct TokGradArgs {
   const int32_t* occ_uid;
   const char* dout;
   char* grad;
-  double* part;  // [chunks][2][cols]
+  double* part;  // [workgroups][2][cols]
   int64_t n, rows, in_stride, out_stride;
   float scale;
   int32_t W, dim, accumulate;
   int32_t lanes;       // lanes per chunk, a power of two
   int32_t chunk;       // sorted tokens per chunk
-  int32_t chunks;      // of all n tokens
+  int32_t spans;       // workgroups' shares of all n tokens
   int32_t col_tiles;
   int32_t cols;        // col_tiles * lanes * N
   int64_t sum_blocks;  // workgroups that sum; the rest clear rows
@@ -163,8 +163,12 @@ __device__ __forceinline__ void put_row(const TokGradArgs& a, int64_t row, int32
   *p = y;
 }
 
-constexpr int kAhead = 8;  // tokens whose gradients are in flight
+constexpr int kAhead = 8;   // tokens whose gradients are in flight
+constexpr int kShort = 64;  // rows of at most this many tokens are summed whole
 constexpr int kClearMax = 1024;
+constexpr int kMinLanes = 8;    // lanes of a chunk, at least
+constexpr int kChunkMax = 64;   // tokens of a chunk, at most
+constexpr int kStage = kThreads / kMinLanes * kChunkMax + kShort;  // tokens of a workgroup
 
 // rows of [row0, row0 + clear_rows) that no token names
 template <typename TO>
@@ -192,91 +196,216 @@ __device__ void clear_rows(const TokGradArgs& a, int64_t row0, int64_t U) {
   }
 }
 
-// A lane group takes a chunk of the sorted tokens and N columns per lane,
-// sums row after row in 64 bits, and writes the rows that begin and end in
-// the chunk; the sums of rows that cross a chunk's bound go to `part`: [0] of
-// the row that came in, [1] of the row that goes on.
+// A lane group takes a chunk of the sorted tokens and N columns per lane and
+// sums row after row in 64 bits. Rows of at most kShort tokens belong whole to
+// the chunk they begin in, which reads on past its end for the last one, so
+// nearly every row is written at once. Of a longer row each chunk sums its own
+// tokens: the workgroup adds its chunks' sums in LDS and writes the rows that
+// begin and end in it; the rest goes to `part` ([0] of a row that came in, [1]
+// of one that goes on), which k_token_join adds. A workgroup's tokens and rows
+// are read together into LDS first: between its start and its first gradient
+// stand two dependent reads (row index, row), not one per token.
+struct TokStage {
+  int32_t bm[kStage], uid[kStage];
+  uint32_t row[kStage];
+};
+
+// What a lane group leaves of its long rows
+constexpr int32_t kCame = 1;     // [0]: of a row that came in and ends here
+constexpr int32_t kGoes = 2;     // [1]: of a row that begins here and goes on
+constexpr int32_t kThrough = 4;  // [0]: of a row that came in and goes on
+
 template <typename TI, typename TO, int N>
 __global__ void __launch_bounds__(kThreads) k_token_grad(TokGradArgs a) {
-  const int64_t U = max((int64_t)0, min(a.unique_offsets[a.W], a.n));
+  // the sums take the place of the tokens when these are done with
+  constexpr size_t kSums = (size_t)2 * kThreads * N * sizeof(double);
+  __shared__ __attribute__((aligned(16))) char
+      lds[kSums > sizeof(TokStage) ? kSums : sizeof(TokStage)];
+  __shared__ int32_t s_has[kThreads / kMinLanes];
+  __shared__ uint32_t s_last[kThreads / kMinLanes];
+  __shared__ int32_t s_any;
   if ((int64_t)blockIdx.x >= a.sum_blocks) {
+    const int64_t U = max((int64_t)0, min(a.unique_offsets[a.W], a.n));
     clear_rows<TO>(a, ((int64_t)blockIdx.x - a.sum_blocks) * a.clear_rows, U);
     return;
   }
-  const int32_t n = min(a.seg[U], (int32_t)a.n);
-  const int32_t groups = kThreads / a.lanes;
+  TokStage& st = *(TokStage*)lds;
+  const int32_t groups = kThreads / a.lanes, gi = threadIdx.x / a.lanes;
+  const int32_t li = threadIdx.x % a.lanes;
   const int32_t tile = (int32_t)(blockIdx.x % a.col_tiles);
-  const int64_t c = (int64_t)(blockIdx.x / a.col_tiles) * groups + threadIdx.x / a.lanes;
-  const int32_t col = (tile * a.lanes + (int32_t)(threadIdx.x % a.lanes)) * N;
-  const int64_t e0 = c * a.chunk;
-  if (e0 >= n || col >= a.dim) return;
-  const int32_t e1 = (int32_t)min((int64_t)n, e0 + a.chunk);
-  double s[N];
+  const int64_t wg = blockIdx.x / a.col_tiles;
+  const int64_t base = wg * groups * a.chunk;  // the workgroup's first token
+  const int32_t staged = groups * a.chunk + kShort;
+  const int64_t U = max((int64_t)0, min(a.unique_offsets[a.W], a.n));
+  for (int32_t x = threadIdx.x; x < staged; x += kThreads) {
+    const bool in = base + x < a.n;
+    // past the last sorted token the arrays hold anything: clamped to be read
+    const int32_t u = in ? a.occ_uid[base + x] : 0;
+    st.uid[x] = u;
+    st.bm[x] = in ? a.occ_bm[base + x] : 0;
+    st.row[x] = (uint32_t)a.unique[min(max(u, 0), (int32_t)a.n - 1)];
+  }
+  if (threadIdx.x == 0) s_any = 0;
+  if (threadIdx.x < kThreads / kMinLanes) s_has[threadIdx.x] = 0;
+  const int32_t n = min(a.seg[U], (int32_t)a.n);
+  __syncthreads();
+  const int32_t off = gi * a.chunk;
+  const int64_t e0 = base + off;
+  const int32_t col = (tile * a.lanes + li) * N;
+  double s[N], came_sum[N];
 #pragma unroll
-  for (int x = 0; x < N; ++x) s[x] = 0;
-  const char* base = a.dout + (int64_t)col * (int64_t)sizeof(TI);
-  int32_t u = a.occ_uid[e0];
-  auto close = [&](bool goes_on) {  // row u ends here, or at the chunk's end
-    if (a.seg[u] < (int32_t)e0 || goes_on) {
-      double* p = a.part + ((int64_t)c * 2 + (a.seg[u] < (int32_t)e0 ? 0 : 1)) * a.cols + col;
+  for (int x = 0; x < N; ++x) s[x] = came_sum[x] = 0;
+  int32_t has = 0;
+  uint32_t row = 0;
+  if (e0 < n && col < a.dim) {
+    const int32_t e1 = (int32_t)min((int64_t)n, e0 + a.chunk);
+    // the rows at the chunk's two ends
+    const int32_t uf = st.uid[off], ul = st.uid[off + (e1 - (int32_t)e0) - 1];
+    const int32_t f0 = a.seg[uf], f1 = a.seg[uf + 1], l0 = a.seg[ul], l1 = a.seg[ul + 1];
+    const bool came = f0 < (int32_t)e0, goes = l1 > e1;
+    const bool long_f = f1 - f0 > kShort, long_l = l1 - l0 > kShort;
+    const int32_t p0 = came && !long_f ? f1 : (int32_t)e0;  // its chunk sums it
+    const int32_t p1 = goes && !long_l ? (l0 < (int32_t)e0 ? e1 : l1) : e1;
+    const char* src = a.dout + (int64_t)col * (int64_t)sizeof(TI);
+    int32_t at = p0 - (int32_t)base;
+    const int32_t stop = p1 - (int32_t)base;
+    bool first = came && long_f;  // the row being summed came in
+    if (at < stop) {
+      row = st.row[at];
+      for (; at < stop; at += kAhead) {
+        Pack<TI, N> v[kAhead];
+        uint32_t r[kAhead];
 #pragma unroll
-      for (int x = 0; x < N; ++x) p[x] = s[x];
-    } else {
-      put_row<TO, N>(a, a.unique[u], col, s);
-    }
-#pragma unroll
-    for (int x = 0; x < N; ++x) s[x] = 0;
-  };
-  for (int32_t e = (int32_t)e0; e < e1; e += kAhead) {
-    Pack<TI, N> v[kAhead];
-    int32_t uid[kAhead];
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int32_t x = min(e + k, e1 - 1);
-      uid[k] = a.occ_uid[x];
-      v[k] = *(const Pack<TI, N>*)(base + (int64_t)a.occ_bm[x] * a.in_stride);
-    }
-#pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      if (e + k < e1) {
-        if (uid[k] != u) {
-          close(false);
-          u = uid[k];
+        for (int k = 0; k < kAhead; ++k) {
+          const int32_t x = min(at + k, stop - 1);
+          r[k] = st.row[x];
+          v[k] = *(const Pack<TI, N>*)(src + (int64_t)st.bm[x] * a.in_stride);
         }
 #pragma unroll
-        for (int x = 0; x < N; ++x) s[x] += (double)Num<TI>::up(v[k].v[x]);
+        for (int k = 0; k < kAhead; ++k) {
+          if (at + k < stop) {
+            if (r[k] != row) {
+              if (first) {
+                has = kCame;
+#pragma unroll
+                for (int x = 0; x < N; ++x) came_sum[x] = s[x];
+              } else {
+                put_row<TO, N>(a, row, col, s);
+              }
+              first = false;
+              row = r[k];
+#pragma unroll
+              for (int x = 0; x < N; ++x) s[x] = 0;
+            }
+#pragma unroll
+            for (int x = 0; x < N; ++x) s[x] += (double)Num<TI>::up(v[k].v[x]);
+          }
+        }
+      }
+      if (first) {
+        has = goes ? kThrough : kCame;
+#pragma unroll
+        for (int x = 0; x < N; ++x) came_sum[x] = s[x];
+      } else if (goes && long_l) {
+        has |= kGoes;
+      } else {
+        put_row<TO, N>(a, row, col, s);
       }
     }
   }
-  close(a.seg[u + 1] > e1);
+  if (has) s_any = 1;  // the same for every lane of a group that has a column
+  __syncthreads();
+  if (!s_any) return;
+  // the groups' sums, then each column's in the order of the groups
+  double* sums = (double*)lds;
+  if (col < a.dim) {
+    if (li == 0) {
+      s_has[gi] = has;
+      s_last[gi] = row;
+    }
+#pragma unroll
+    for (int x = 0; x < N; ++x) {
+      sums[(gi * 2 + 0) * a.lanes * N + li * N + x] = came_sum[x];
+      sums[(gi * 2 + 1) * a.lanes * N + li * N + x] = s[x];
+    }
+  }
+  __syncthreads();
+  if (gi != 0 || col >= a.dim) return;
+#pragma unroll
+  for (int x = 0; x < N; ++x) s[x] = 0;
+  auto keep = [&](int32_t which) {
+    double* p = a.part + (wg * 2 + which) * a.cols + col;
+#pragma unroll
+    for (int x = 0; x < N; ++x) p[x] = s[x];
+  };
+  bool open = false, began = false;  // a row is being added; it began in this workgroup
+  uint32_t open_row = 0;
+  for (int32_t y = 0; y < groups; ++y) {
+    const int32_t h = s_has[y];
+    const double* p = sums + y * 2 * a.lanes * N + li * N;
+    if (h & (kCame | kThrough)) {
+      open = true;
+#pragma unroll
+      for (int x = 0; x < N; ++x) s[x] += p[x];
+    }
+    if (h & kCame) {
+      if (began) put_row<TO, N>(a, open_row, col, s); else keep(0);
+      open = began = false;
+#pragma unroll
+      for (int x = 0; x < N; ++x) s[x] = 0;
+    }
+    if (h & kGoes) {
+      open = began = true;
+      open_row = s_last[y];
+#pragma unroll
+      for (int x = 0; x < N; ++x) s[x] = p[a.lanes * N + x];
+    }
+  }
+  if (open) keep(began ? 1 : 0);
 }
 
-// Rows over several chunks: the workgroup of the chunk where a row begins
-// adds the chunks' sums, each lane group every groups-th one, then the groups
-// in order.
+// Rows of more than kShort tokens over several workgroups: that of the
+// workgroup where such a row begins adds the workgroups' sums, every lane
+// group a run of them, then the groups in order.
 template <typename TO, int N>
 __global__ void __launch_bounds__(kThreads) k_token_join(TokGradArgs a) {
   __shared__ double stage[kThreads][N];
   const int64_t U = max((int64_t)0, min(a.unique_offsets[a.W], a.n));
-  const int32_t n = min(a.seg[U], (int32_t)a.n);
   const int32_t tile = (int32_t)(blockIdx.x % a.col_tiles);
-  const int64_t c = blockIdx.x / a.col_tiles;
-  const int64_t end = (c + 1) * a.chunk;
-  if (end >= n) return;
-  const int32_t u = a.occ_uid[end - 1];
-  if (a.seg[u] < c * a.chunk || a.seg[u + 1] <= end) return;  // uniform
-  const int64_t last = (a.seg[u + 1] - 1) / a.chunk;
   const int32_t groups = kThreads / a.lanes, gi = threadIdx.x / a.lanes;
+  const int32_t span = groups * a.chunk;  // tokens of a workgroup
+  const int32_t c = (int32_t)(blockIdx.x / a.col_tiles);
+  const int64_t end = ((int64_t)c + 1) * span;  // below n: see the grid
+  const int32_t u = min(max(a.occ_uid[end - 1], 0), (int32_t)a.n - 1);
+  if (end >= a.seg[U]) return;
+  const int32_t l0 = a.seg[u], l1 = a.seg[u + 1];
+  if (l0 < (int64_t)c * span || l1 <= end || l1 - l0 <= kShort) return;  // uniform
+  const int32_t last = (l1 - 1) / span;
   const int32_t li = threadIdx.x % a.lanes;
   const int32_t col = (tile * a.lanes + li) * N;
   double s[N];
 #pragma unroll
   for (int x = 0; x < N; ++x) s[x] = 0;
   if (col < a.dim) {
-    for (int64_t k = c + gi; k <= last; k += groups) {
-      const double* p = a.part + (k * 2 + (k == c ? 1 : 0)) * a.cols + col;
+    const double* p = a.part + col;
+    if (gi == 0) {
 #pragma unroll
-      for (int x = 0; x < N; ++x) s[x] += p[x];
+      for (int x = 0; x < N; ++x) s[x] = p[((int64_t)c * 2 + 1) * a.cols + x];
+    }
+    const int32_t all = last - c;
+    const int32_t k0 = c + 1 + (int32_t)((int64_t)all * gi / groups);
+    const int32_t k1 = c + 1 + (int32_t)((int64_t)all * (gi + 1) / groups);
+    for (int32_t k = k0; k < k1; k += kAhead) {
+      double v[kAhead][N];
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y)
+#pragma unroll
+        for (int x = 0; x < N; ++x) v[y][x] = p[(int64_t)min(k + y, k1 - 1) * 2 * a.cols + x];
+#pragma unroll
+      for (int y = 0; y < kAhead; ++y)
+        if (k + y < k1)
+#pragma unroll
+          for (int x = 0; x < N; ++x) s[x] += v[y][x];
     }
   }
 #pragma unroll
@@ -309,7 +438,10 @@ int32_t piece_elems(int32_t dim, int32_t most, const void* a, int64_t a_stride, 
 template <typename TI, typename TO>
 void launch_lookup(const TokLookupArgs& a, int32_t elems, unsigned grid, hipStream_t stream) {
   switch (elems) {
-    case 8: hipLaunchKernelGGL((k_token_lookup<TI, TO, 8>), dim3(grid), dim3(kThreads), 0, stream, a); break;
+    case 8:
+      if constexpr (sizeof(TI) + sizeof(TO) < 8)  // 16 bytes of a 2-byte type
+        hipLaunchKernelGGL((k_token_lookup<TI, TO, 8>), dim3(grid), dim3(kThreads), 0, stream, a);
+      break;
     case 4: hipLaunchKernelGGL((k_token_lookup<TI, TO, 4>), dim3(grid), dim3(kThreads), 0, stream, a); break;
     case 2: hipLaunchKernelGGL((k_token_lookup<TI, TO, 2>), dim3(grid), dim3(kThreads), 0, stream, a); break;
     default: hipLaunchKernelGGL((k_token_lookup<TI, TO, 1>), dim3(grid), dim3(kThreads), 0, stream, a);
@@ -330,8 +462,8 @@ int launch_grad(const TokGradArgs& a, int64_t blocks, hipStream_t stream) {
     hipLaunchKernelGGL((k_token_grad<TI, TO, N>), dim3((unsigned)blocks), dim3(kThreads), 0, stream, a);
     FS_LAUNCH_CHECK();
   }
-  if (a.chunks > 1) {
-    hipLaunchKernelGGL((k_token_join<TO, N>), dim3((unsigned)(a.chunks * a.col_tiles)),
+  if (a.n > kShort && a.spans > 1) {
+    hipLaunchKernelGGL((k_token_join<TO, N>), dim3((unsigned)((a.spans - 1) * a.col_tiles)),
                        dim3(kThreads), 0, stream, a);
     FS_LAUNCH_CHECK();
   }
@@ -341,7 +473,9 @@ int launch_grad(const TokGradArgs& a, int64_t blocks, hipStream_t stream) {
 template <typename TI, typename TO>
 int launch_grad(const TokGradArgs& a, int32_t elems, int64_t blocks, hipStream_t stream) {
   switch (elems) {
-    case 8: return launch_grad<TI, TO, 8>(a, blocks, stream);
+    case 8:
+      if constexpr (sizeof(TI) == 2) return launch_grad<TI, TO, 8>(a, blocks, stream);
+      break;
     case 4: return launch_grad<TI, TO, 4>(a, blocks, stream);
     case 2: return launch_grad<TI, TO, 2>(a, blocks, stream);
   }
@@ -356,14 +490,20 @@ int launch_grad(const TokGradArgs& a, int32_t elems, int32_t out_dtype, int64_t 
   return launch_grad<TI, _Float16>(a, elems, blocks, stream);
 }
 
-// Sorted tokens per chunk of a gradient call: a rule on the token count alone,
-// so that the workspace query and every alignment agree.
-int32_t grad_chunk(int64_t n) { return n <= 4096 ? 8 : (n <= 65536 ? 16 : 64); }
-// chunks of any call with at most n tokens
-int64_t grad_chunks_cap(int64_t n) {
-  int64_t most = cdiv(n, grad_chunk(n));
-  if (n > 4096) most = std::max(most, cdiv((int64_t)4096, (int64_t)8));
-  if (n > 65536) most = std::max(most, cdiv((int64_t)65536, (int64_t)16));
+// Sorted tokens per chunk of a gradient call: as long as about 4096 waves of
+// 512 columns each still share the work.
+int32_t grad_chunk(int64_t n, int32_t dim) {
+  int32_t c = 8;
+  while (c < kChunkMax && n * dim >= (int64_t)c * 2 * 512 * 4096) c *= 2;
+  return c;
+}
+// the most chunks of any call of at most n tokens
+int64_t grad_chunks_cap(int64_t n, int32_t dim) {
+  int64_t most = cdiv(n, grad_chunk(n, dim));
+  for (int32_t c = 8; c < kChunkMax; c *= 2) {  // the largest call of each chunk size
+    const int64_t last = std::min(n, ((int64_t)c * 2 * 512 * 4096 - 1) / dim);
+    most = std::max(most, cdiv(last, c));
+  }
   return most;
 }
 
@@ -452,9 +592,10 @@ extern "C" int fs_token_sort(const int64_t* ids, int64_t n, int64_t rows, int64_
 }
 
 extern "C" size_t fs_token_grad_workspace_size(int64_t n, int32_t dim) {
-  if (n < 0 || dim < 0) return 0;
+  if (n < 0 || dim < 1) return 0;
   Carve c(nullptr);
-  c.take<double>((size_t)grad_chunks_cap(n) * 2 * align_up((size_t)dim, 512));
+  // a workgroup has at least four chunks, and fewer columns where it has more
+  c.take<double>((size_t)cdiv(grad_chunks_cap(n, dim), kThreads / kWave) * 2 * align_up((size_t)dim, 512));
   return c.used + 256;
 }
 
@@ -495,18 +636,18 @@ extern "C" int fs_token_grad(const int64_t* unique, const int64_t* unique_offset
   const int32_t elems = piece_elems(dim, ei == 4 ? 4 : 8, dout, a.in_stride, ei, grad,
                                     a.out_stride, eo);
   const int32_t pieces = dim / elems;
-  a.lanes = 1;
+  a.lanes = kMinLanes;
   while (a.lanes < kWave && a.lanes < pieces) a.lanes *= 2;
-  a.chunk = grad_chunk(n);
-  a.chunks = (int32_t)cdiv(n, a.chunk);
+  a.chunk = grad_chunk(n, dim);
+  a.spans = (int32_t)cdiv(n, (int64_t)a.chunk * (kThreads / a.lanes));
   a.col_tiles = (int32_t)cdiv(pieces, a.lanes);
   a.cols = a.col_tiles * a.lanes * elems;
-  a.sum_blocks = cdiv(a.chunks, kThreads / a.lanes) * a.col_tiles;
+  a.sum_blocks = (int64_t)a.spans * a.col_tiles;
   const int64_t row_bytes = (int64_t)dim * eo;
   a.clear_rows = (int32_t)std::min<int64_t>(kClearMax, std::max<int64_t>(4, 32768 / row_bytes));
   const int64_t clear_blocks = a.accumulate ? 0 : cdiv(rows, a.clear_rows);
   const int64_t blocks = a.sum_blocks + clear_blocks;
-  if (blocks >= (int64_t)INT32_MAX || (int64_t)a.chunks * a.col_tiles >= (int64_t)INT32_MAX)
+  if (blocks >= (int64_t)INT32_MAX)
     return FS_ERR_UNSUPPORTED;
   if (dout_dtype == FS_F32) return launch_grad<float>(a, elems, grad_dtype, blocks, stream);
   if (dout_dtype == FS_BF16) return launch_grad<__bf16>(a, elems, grad_dtype, blocks, stream);
