@@ -1,5 +1,5 @@
-// Token embedding: scaled lookup of a vocabulary's rows, the tokens sorted by
-// row, and the gradient of the rows by the sorted tokens.
+// Token embedding: scaled lookup of a vocabulary's rows, and the gradient of
+// the rows by the sorted tokens (token_sort.hip).
 //
 //   out[i] = scale w[ids[i]]        g[v] = scale sum over i with ids[i] = v of dout[i]
 #include <algorithm>
@@ -88,39 +88,6 @@ __global__ void __launch_bounds__(kThreads) k_token_lookup(TokLookupArgs a) {
       for (int e = 0; e < N; ++e) y.v[e] = Num<TO>::down(Num<TI>::up(x[u].v[e]) * a.scale);
       *(Pack<TO, N>*)(a.out + to[u]) = y;
     }
-  }
-}
-
-// ---------------------------------------------------------------- sort
-// The tokens as the items of a one-shard batch: dropped ones (padding, outside
-// the table) go to one more row behind the last, which the sort puts last.
-__global__ void __launch_bounds__(kThreads)
-k_token_items(const int64_t* __restrict__ ids, int64_t n, int64_t rows, int64_t padding,
-              int64_t* __restrict__ keys, int32_t* __restrict__ bm, int64_t* __restrict__ bounds,
-              int32_t* __restrict__ err) {
-  const int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-  bool bad = false;
-  if (i < n) {
-    const int64_t id = ids[i];
-    bad = id != padding && (id < 0 || id >= rows);
-    keys[i] = id == padding || bad ? rows : id;
-    bm[i] = (int32_t)i;
-  }
-  flag_err(err, bad, FS_EF_ID_RANGE);
-  if (i == 0) {
-    bounds[0] = 0;
-    bounds[1] = n;
-  }
-}
-
-// takes the row of the dropped tokens off the end
-__global__ void k_token_drop(const int64_t* __restrict__ unique, int64_t rows, int64_t n,
-                             int64_t* __restrict__ unique_offsets, int64_t* __restrict__ counts) {
-  const int64_t u = counts[0];
-  if (threadIdx.x == 0 && u > 0 && u <= n && unique[u - 1] >= rows) {
-    counts[0] = u - 1;
-    counts[2] = u - 1;
-    unique_offsets[1] = u - 1;
   }
 }
 
@@ -544,49 +511,6 @@ extern "C" int fs_token_lookup(const fs_table* table, const int64_t* ids, int64_
   if (table->dtype == FS_F32) launch_lookup<float>(a, elems, out_dtype, grid, stream);
   else if (table->dtype == FS_BF16) launch_lookup<__bf16>(a, elems, out_dtype, grid, stream);
   else launch_lookup<_Float16>(a, elems, out_dtype, grid, stream);
-  FS_LAUNCH_CHECK();
-  return FS_OK;
-}
-
-extern "C" size_t fs_token_sort_workspace_size(int64_t n) {
-  if (n < 0) return 0;
-  const size_t cap = (size_t)(n > 0 ? n : 1);
-  Carve c(nullptr);
-  c.take<int64_t>(cap);
-  c.take<int32_t>(cap);
-  c.take<int64_t>(2);
-  c.take<uint8_t>(cap);
-  return c.used + 256 + fs_unique_workspace_size(n, 0, 1, 1);
-}
-
-extern "C" int fs_token_sort(const int64_t* ids, int64_t n, int64_t rows, int64_t padding_id,
-                             int64_t* unique, int64_t* unique_offsets, int32_t* seg_offsets,
-                             int32_t* occ_bm, int32_t* occ_uid, int64_t* counts, int32_t* err,
-                             void* ws, size_t ws_bytes, hipStream_t stream) {
-  if (n < 0 || n >= (int64_t)INT32_MAX || rows < 1 || !unique_offsets || !seg_offsets || !counts)
-    return FS_ERR_INVALID_ARG;
-  if (rows >= (int64_t)UINT32_MAX) return FS_ERR_UNSUPPORTED;
-  if (n > 0 && (!ids || !unique || !occ_bm || !occ_uid)) return FS_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < fs_token_sort_workspace_size(n)) return FS_ERR_WORKSPACE;
-  const size_t cap = (size_t)(n > 0 ? n : 1);
-  Carve c(ws);
-  int64_t* keys = c.take<int64_t>(cap);
-  int32_t* bm = c.take<int32_t>(cap);
-  int64_t* bounds = c.take<int64_t>(2);
-  uint8_t* cls = c.take<uint8_t>(cap);
-  char* rest = (char*)ws + align_up(c.used, 256);
-  hipLaunchKernelGGL(k_token_items, dim3((unsigned)cdiv((int64_t)cap, kThreads)), dim3(kThreads), 0,
-                     stream, ids, n, rows, padding_id, keys, bm, bounds, err);
-  FS_LAUNCH_CHECK();
-  fs_table tab = {};
-  tab.rows = rows + 1;
-  const int rc = fs_unique_collision_split(
-      keys, bm, bounds, n, &tab, 1, 1, nullptr, nullptr, nullptr, 0, unique, unique_offsets,
-      seg_offsets, occ_bm, occ_uid, cls, nullptr, counts, rest,
-      fs_unique_workspace_size(n, 0, 1, 1), stream);
-  if (rc) return rc;
-  hipLaunchKernelGGL(k_token_drop, dim3(1), dim3(kWave), 0, stream, unique, rows, n,
-                     unique_offsets, counts);
   FS_LAUNCH_CHECK();
   return FS_OK;
 }
