@@ -10,6 +10,8 @@
 namespace fs {
 namespace {
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
 constexpr int kThreads = 256;
 
 // ---------------------------------------------------------------- elements
@@ -111,6 +113,9 @@ struct TokGradArgs {
   int32_t cols;        // col_tiles * lanes * N
   int64_t sum_blocks;  // workgroups that sum; the rest clear rows
   int32_t clear_rows;  // rows per clearing workgroup
+  int32_t clear_pieces;  // 16-byte pieces of a row
+  int32_t clear_wide;    // which are aligned, and whole
+  DivU32 by_clear_pieces;
 };
 
 template <typename TO, int N>
@@ -149,16 +154,18 @@ __device__ void clear_rows(const TokGradArgs& a, int64_t row0, int64_t U) {
   for (int64_t u = u0 + threadIdx.x; u < U && unique[u] < row1; u += kThreads)
     atomicOr(&named[(unique[u] - row0) >> 5], 1u << ((unique[u] - row0) & 31));
   __syncthreads();
-  const int64_t bytes = (int64_t)a.dim * (int64_t)sizeof(TO);
-  const bool wide = (bytes & 15) == 0 && (a.out_stride & 15) == 0 && ((uintptr_t)a.grad & 15) == 0;
-  const int w = threadIdx.x / kWave;
-  for (int64_t r = row0 + w; r < row1; r += kThreads / kWave) {
-    if ((named[(r - row0) >> 5] >> ((r - row0) & 31)) & 1u) continue;
-    char* p = a.grad + r * a.out_stride;
-    if (wide) {
-      for (int64_t x = lane() * 16; x < bytes; x += kWave * 16) *(uint4*)(p + x) = uint4{0, 0, 0, 0};
+  // 16 bytes per thread, rows one after the other
+  const uint32_t pieces = (uint32_t)a.clear_pieces, total = (uint32_t)(row1 - row0) * pieces;
+  for (uint32_t x = threadIdx.x; x < total; x += kThreads) {
+    const uint32_t r = divu32(x, a.by_clear_pieces), p = x - r * pieces;
+    if ((named[r >> 5] >> (r & 31)) & 1u) continue;
+    char* row = a.grad + (row0 + r) * a.out_stride;
+    if (a.clear_wide) {
+      __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, (u32x4*)row + p);
     } else {
-      for (int64_t x = lane(); x < a.dim; x += kWave) ((TO*)p)[x] = Num<TO>::down(0.f);
+      constexpr int kPer = 16 / sizeof(TO);
+      for (int32_t y = p * kPer; y < min((int32_t)(p + 1) * kPer, a.dim); ++y)
+        ((TO*)row)[y] = Num<TO>::down(0.f);
     }
   }
 }
@@ -563,11 +570,18 @@ extern "C" int fs_token_grad(const int64_t* unique, const int64_t* unique_offset
   a.lanes = kMinLanes;
   while (a.lanes < kWave && a.lanes < pieces) a.lanes *= 2;
   a.chunk = grad_chunk(n, dim);
-  a.spans = (int32_t)cdiv(n, (int64_t)a.chunk * (kThreads / a.lanes));
+  // few tokens in one workgroup need no second launch (about 4 us); beyond 32
+  // tokens one after the other a group takes as long itself
+  const int32_t groups = kThreads / a.lanes;
+  while (a.chunk < 32 && (int64_t)a.chunk * groups < n && n <= (int64_t)32 * groups) a.chunk *= 2;
+  a.spans = (int32_t)cdiv(n, (int64_t)a.chunk * groups);
   a.col_tiles = (int32_t)cdiv(pieces, a.lanes);
   a.cols = a.col_tiles * a.lanes * elems;
   a.sum_blocks = (int64_t)a.spans * a.col_tiles;
   const int64_t row_bytes = (int64_t)dim * eo;
+  a.clear_pieces = (int32_t)cdiv(row_bytes, 16);
+  a.clear_wide = row_bytes % 16 == 0 && a.out_stride % 16 == 0 && (uintptr_t)grad % 16 == 0;
+  a.by_clear_pieces = make_divu32((uint32_t)a.clear_pieces);
   a.clear_rows = (int32_t)std::min<int64_t>(kClearMax, std::max<int64_t>(4, 32768 / row_bytes));
   const int64_t clear_blocks = a.accumulate ? 0 : cdiv(rows, a.clear_rows);
   const int64_t blocks = a.sum_blocks + clear_blocks;

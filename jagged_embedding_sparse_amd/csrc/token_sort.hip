@@ -320,6 +320,7 @@ k_token_csr(const uint32_t* __restrict__ keys, int32_t n, uint32_t rows,
   if (heads) {
     if (threadIdx.x < blockIdx.x) mine = heads[threadIdx.x];
   } else {
+#pragma unroll 4
     for (uint32_t t = 0; t < blockIdx.x; ++t)
       mine += popc(heads_of(keys, t * kMidTile + threadIdx.x * kRounds, n, rows, &live));
   }

@@ -139,8 +139,10 @@ def _ptr(t):
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return s.cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    # the current stream's handle without a Stream object (2.8 us of a call's host time)
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(fn, rc):
@@ -525,20 +527,23 @@ def fs_token_sort(ids, rows, padding_id=-1, out=None, err=None, ws=None, stream=
     occ_uid, counts): fs_token_grad, fs_grad_reduce_update and
     fs_jagged_lookup take them."""
     assert ids.dtype == torch.int64
-    d, n = _dev(), ids.numel()
-    cap = max(n, 1)
-    o = out or {}
-    uq = _get(o, "unique", lambda: torch.empty(cap, dtype=torch.int64, device=d))
-    uo = _get(o, "unique_offsets", lambda: torch.empty(2, dtype=torch.int64, device=d))
-    seg = _get(o, "seg_offsets", lambda: torch.empty(cap + 1, dtype=torch.int32, device=d))
-    bm = _get(o, "occ_bm", lambda: torch.empty(cap, dtype=torch.int32, device=d))
-    uid = _get(o, "occ_uid", lambda: torch.empty(cap, dtype=torch.int32, device=d))
-    counts = _get(o, "counts", lambda: torch.empty(4, dtype=torch.int64, device=d))
-    ws = _ws(token_sort_workspace_size(n), ws)
+    n = ids.numel()
+    cap, nb = max(n, 1), token_sort_workspace_size(n)
+    if out is None:  # two allocations for the six outputs and the workspace
+        d, nw = _dev(), 0 if ws is not None else -(-nb // 8)
+        w64, uq, uo, counts = torch.empty(nw + cap + 6, dtype=torch.int64,
+                                          device=d).split_with_sizes((nw, cap, 2, 4))
+        seg, bm, uid = torch.empty(3 * cap + 1, dtype=torch.int32,
+                                   device=d).split_with_sizes((cap + 1, cap, cap))
+        ws = w64 if ws is None else ws
+    else:
+        uq, uo, seg, bm, uid, counts = (out[k] for k in ("unique", "unique_offsets", "seg_offsets",
+                                                         "occ_bm", "occ_uid", "counts"))
+    ws = _ws(nb, ws)
     _check("fs_token_sort",
            _c_token_sort(_ptr(ids), n, int(rows), int(padding_id), _ptr(uq), _ptr(uo), _ptr(seg),
-                         _ptr(bm), _ptr(uid), _ptr(counts), _ptr(err), _ptr(ws), ws.numel(),
-                         _stream(stream)))
+                         _ptr(bm), _ptr(uid), _ptr(counts), _ptr(err), _ptr(ws),
+                         ws.numel() * ws.element_size(), _stream(stream)))
     return dict(unique=uq, unique_offsets=uo, seg_offsets=seg, occ_bm=bm, occ_uid=uid,
                 counts=counts)
 
