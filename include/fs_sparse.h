@@ -451,8 +451,7 @@ int fs_grad_reduce_update_noalloc(const fs_table* tables, int32_t T, int32_t W,
 /* fs_token_lookup: out[i][d] = round(scale * w[ids[i]][d]), the product in  */
 /* fp32 and rounded once more (to nearest even) to the output's type.        */
 /*  table    host, one table: weights, rows, dim, dtype and stride are read; */
-/*           weights and stride need only be aligned to an element (fastest   */
-/*           where rows and stride are multiples of 16 bytes).               */
+/*           weights and stride need only be aligned to an element.          */
 /*  ids      device [n]; an ID outside [0, rows) gives a row of zeros and    */
 /*           flags FS_EF_ID_RANGE.                                           */
 /*  out      device [n][dim] of out_dtype, rows out_stride bytes apart       */
