@@ -189,12 +189,12 @@ k_token_sort_small(const int64_t* __restrict__ ids, int32_t n, int64_t rows, int
 }
 
 // ---------------------------------------------------------------- tiles
-constexpr int kMidThreads = 1024;
-constexpr int kMidTile = kMidThreads * kRounds;  // 4096
+// Workgroups of 256 threads up to 64 tiles of 1024 tokens, of 1024 beyond.
 constexpr int kMidBits = 9;
 constexpr int kMidBins = 1 << kMidBits;
-constexpr int64_t kMidTiles = 64;      // 262144 tokens
+constexpr int64_t kMidTiles = 64;
 constexpr int64_t kRecountTiles = 16;  // up to here the CSR counts the rows before a tile itself
+constexpr int64_t kMidMax = kMidTiles * 1024 * kRounds;  // 262144 tokens
 
 template <bool kFirst>
 __device__ __forceinline__ uint32_t load_key(const int64_t* ids, const uint32_t* keys, int32_t i,
@@ -203,40 +203,41 @@ __device__ __forceinline__ uint32_t load_key(const int64_t* ids, const uint32_t*
   return keys[i];
 }
 
-template <bool kFirst>
-__global__ void __launch_bounds__(kMidThreads)
+template <int NT, bool kFirst>
+__global__ void __launch_bounds__(NT)
 k_token_hist(const int64_t* __restrict__ ids, const uint32_t* __restrict__ keys, int32_t n,
              int64_t rows, int64_t padding, int shift, int bits, uint32_t* __restrict__ hist,
              int32_t* __restrict__ err) {
   __shared__ uint32_t h[kMidBins];
-  if (threadIdx.x < kMidBins) h[threadIdx.x] = 0;
+  for (int b = threadIdx.x; b < kMidBins; b += NT) h[b] = 0;
   __syncthreads();
   const uint32_t mask = (1u << bits) - 1;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < kRounds; ++i) {
-    const int32_t x = blockIdx.x * kMidTile + i * kMidThreads + threadIdx.x;
+    const int32_t x = (blockIdx.x * kRounds + i) * NT + threadIdx.x;
     if (x < n)
       atomicAdd(&h[(load_key<kFirst>(ids, keys, x, rows, padding, bad) >> shift) & mask], 1u);
   }
   if (kFirst) flag_err(err, bad, FS_EF_ID_RANGE);
   __syncthreads();
-  if (threadIdx.x <= mask) hist[blockIdx.x * kMidBins + threadIdx.x] = h[threadIdx.x];
+  for (uint32_t b = threadIdx.x; b <= mask; b += NT) hist[blockIdx.x * kMidBins + b] = h[b];
 }
 
-template <bool kFirst>
-__global__ void __launch_bounds__(kMidThreads)
+template <int NT, bool kFirst>
+__global__ void __launch_bounds__(NT)
 k_token_scatter(const int64_t* __restrict__ ids, const uint32_t* __restrict__ keys,
                 const int32_t* __restrict__ vals, int32_t n, int64_t rows, int64_t padding,
                 int shift, int bits, const uint32_t* __restrict__ hist, uint32_t* __restrict__ kout,
                 int32_t* __restrict__ vout) {
-  constexpr int kWaves = kMidThreads / kWave;
+  constexpr int kWaves = NT / kWave;
+  constexpr int kParts = NT > kMidBins ? NT / kMidBins : 1;  // threads per digit
   __shared__ uint32_t count[kWaves][kMidBins];
   __shared__ uint64_t peers[kWaves][kMidBins];
-  __shared__ uint32_t before[2][kMidBins], total[2][kMidBins];
+  __shared__ uint32_t before[kParts][kMidBins], total[kParts][kMidBins];
   __shared__ uint32_t tmp[17];
   const int w = threadIdx.x / kWave, l = lane();
-  const int32_t t0 = blockIdx.x * kMidTile, tiles = gridDim.x;
+  const int32_t t0 = blockIdx.x * NT * kRounds, tiles = gridDim.x;
   uint32_t key[kRounds], place[kRounds];
   int32_t val[kRounds];
   bool bad = false;
@@ -247,32 +248,40 @@ k_token_scatter(const int64_t* __restrict__ ids, const uint32_t* __restrict__ ke
     val[i] = kFirst ? x : vals[x];
   }
   for (int b = l; b < kMidBins; b += kWave) peers[w][b] = 0;
-  {  // each half of the threads sums every second tile's counts
-    const int b = threadIdx.x % kMidBins, half = threadIdx.x / kMidBins;
+  // each digit's counts in the tiles before this one and in all of them
+  for (int b = threadIdx.x % kMidBins; b < 1 << bits; b += NT) {
+    const int part = threadIdx.x / kMidBins;
     uint32_t pre = 0, all = 0;
-    if (b < 1 << bits) {
-      for (int32_t t = half; t < tiles; t += 16) {
-        uint32_t v[8];
+    for (int32_t t = part; t < tiles; t += 8 * kParts) {
+      uint32_t v[8];
 #pragma unroll
-        for (int y = 0; y < 8; ++y) v[y] = t + 2 * y < tiles ? hist[(t + 2 * y) * kMidBins + b] : 0u;
+      for (int y = 0; y < 8; ++y)
+        v[y] = t + kParts * y < tiles ? hist[(t + kParts * y) * kMidBins + b] : 0u;
 #pragma unroll
-        for (int y = 0; y < 8; ++y) {
-          all += v[y];
-          if (t + 2 * y < (int32_t)blockIdx.x) pre += v[y];
-        }
+      for (int y = 0; y < 8; ++y) {
+        all += v[y];
+        if (t + kParts * y < (int32_t)blockIdx.x) pre += v[y];
       }
     }
-    before[half][b] = pre;
-    total[half][b] = all;
+    before[part][b] = pre;
+    total[part][b] = all;
   }
   __syncthreads();
+  uint32_t carry = 0;  // of the digits before this round's
   auto start = [&](int b, uint32_t) {
-    const uint32_t tot = b < kMidBins ? total[0][b] + total[1][b] : 0u;
-    uint32_t all;
-    const uint32_t ex = block_excl_scan<uint32_t>(tot, tmp, &all);
-    return b < kMidBins ? ex + before[0][b] + before[1][b] : 0u;
+    uint32_t tot = 0, pre = 0, all;
+    if (b < 1 << bits) {
+#pragma unroll
+      for (int y = 0; y < kParts; ++y) {
+        tot += total[y][b];
+        pre += before[y][b];
+      }
+    }
+    const uint32_t ex = carry + block_excl_scan<uint32_t>(tot, tmp, &all);
+    carry += all;
+    return ex + pre;
   };
-  digit_places<kMidThreads, kMidBits>(key, n - t0, shift, bits, count, peers, start, place);
+  digit_places<NT, kMidBits>(key, n - t0, shift, bits, count, peers, start, place);
 #pragma unroll
   for (int i = 0; i < kRounds; ++i)
     if (t0 + w * kWaveItems + i * kWave + l < n) {
@@ -281,18 +290,24 @@ k_token_scatter(const int64_t* __restrict__ ids, const uint32_t* __restrict__ ke
     }
 }
 
-// Heads of sorted places p0 .. p0 + 3 (bits), of them those below n that are
-// rows; *live: places that hold a token that was not dropped
+// Heads of sorted places p0 .. p0 + 3 (bits), p0 a multiple of 4 that grows by
+// 4 from lane to lane; *live: the places that hold a token that was not dropped
 __device__ __forceinline__ uint32_t heads_of(const uint32_t* keys, int32_t p0, int32_t n,
                                              uint32_t rows, uint32_t* live) {
   uint32_t k[kRounds], bits = 0, in = 0;
-  uint32_t last = p0 > 0 && p0 - 1 < n ? keys[p0 - 1] : 0;
+  if (p0 + kRounds <= n) {
+    const uint4 v = *(const uint4*)(keys + p0);
+    k[0] = v.x, k[1] = v.y, k[2] = v.z, k[3] = v.w;
+  } else {
 #pragma unroll
-  for (int y = 0; y < kRounds; ++y) k[y] = p0 + y < n ? keys[p0 + y] : rows;
+    for (int y = 0; y < kRounds; ++y) k[y] = p0 + y < n ? keys[p0 + y] : rows;
+  }
+  uint32_t last = __shfl_up(k[kRounds - 1], 1, kWave);
+  if (lane() == 0) last = p0 > 0 && p0 - 1 < n ? keys[p0 - 1] : rows;  // rows: no key of a row
 #pragma unroll
   for (int y = 0; y < kRounds; ++y) {
     const bool ok = k[y] < rows;
-    if (ok && (p0 + y == 0 || last != k[y])) bits |= 1u << y;
+    if (ok && last != k[y]) bits |= 1u << y;
     in += ok;
     last = k[y];
   }
@@ -300,36 +315,67 @@ __device__ __forceinline__ uint32_t heads_of(const uint32_t* keys, int32_t p0, i
   return bits;
 }
 
-__global__ void __launch_bounds__(kMidThreads)
+template <int NT>
+__global__ void __launch_bounds__(NT)
 k_token_heads(const uint32_t* __restrict__ keys, int32_t n, uint32_t rows,
               uint32_t* __restrict__ heads) {
   __shared__ uint32_t tmp[17];
   uint32_t live, tot;
-  const uint32_t b = heads_of(keys, blockIdx.x * kMidTile + threadIdx.x * kRounds, n, rows, &live);
+  const uint32_t b = heads_of(keys, (blockIdx.x * NT + threadIdx.x) * kRounds, n, rows, &live);
   block_excl_scan<uint32_t>((uint32_t)popc(b), tmp, &tot);
   if (threadIdx.x == 0) heads[blockIdx.x] = tot;
 }
 
+// This thread's share of the heads in tiles 0 .. tiles - 1 (which are whole),
+// eight tiles' keys in flight
+template <int NT>
+__device__ __forceinline__ uint32_t heads_before(const uint32_t* keys, uint32_t tiles,
+                                                 uint32_t rows) {
+  uint32_t sum = 0;
+  for (uint32_t t = 0; t < tiles; t += 8) {
+    uint4 v[8];
+    uint32_t last[8];
+#pragma unroll
+    for (int y = 0; y < 8; ++y) {
+      const uint32_t p = ((t + y) * NT + threadIdx.x) * kRounds;
+      v[y] = uint4{rows, rows, rows, rows};
+      last[y] = rows;
+      if (t + y < tiles) {
+        v[y] = *(const uint4*)(keys + p);
+        if (p > 0) last[y] = keys[p - 1];
+      }
+    }
+#pragma unroll
+    for (int y = 0; y < 8; ++y)
+      sum += (uint32_t)(v[y].x < rows && v[y].x != last[y]) + (v[y].y < rows && v[y].y != v[y].x) +
+             (v[y].z < rows && v[y].z != v[y].y) + (v[y].w < rows && v[y].w != v[y].z);
+  }
+  return sum;
+}
+
 // The CSR of one tile. `heads`: rows that begin in each tile; NULL: counted
 // here over the tiles before this one.
-__global__ void __launch_bounds__(kMidThreads)
+template <int NT>
+__global__ void __launch_bounds__(NT)
 k_token_csr(const uint32_t* __restrict__ keys, int32_t n, uint32_t rows,
             const uint32_t* __restrict__ heads, SortOut o) {
-  __shared__ uint32_t tmp[17];
-  uint32_t mine = 0, live, before;
+  __shared__ uint64_t tmp64[17];
+  uint32_t mine = 0, live;
+  const int32_t p0 = (blockIdx.x * NT + threadIdx.x) * kRounds;
+  const uint32_t b = heads_of(keys, p0, n, rows, &live);
   if (heads) {
     if (threadIdx.x < blockIdx.x) mine = heads[threadIdx.x];
   } else {
-#pragma unroll 4
-    for (uint32_t t = 0; t < blockIdx.x; ++t)
-      mine += popc(heads_of(keys, t * kMidTile + threadIdx.x * kRounds, n, rows, &live));
+    mine = heads_before<NT>(keys, blockIdx.x, rows);
   }
-  block_excl_scan<uint32_t>(mine, tmp, &before);
-  const int32_t p0 = blockIdx.x * kMidTile + threadIdx.x * kRounds;
-  const uint32_t b = heads_of(keys, p0, n, rows, &live);
-  uint32_t tot, live_all;
-  uint32_t u = before + block_excl_scan<uint32_t>((uint32_t)popc(b), tmp, &tot);
-  block_excl_scan<uint32_t>(live, tmp, &live_all);
+  // three sums in one scan: heads before the tile (its total), heads and live
+  // places before the thread (a tile has at most 4096 of each)
+  uint64_t all;
+  const uint64_t ex =
+      block_excl_scan<uint64_t>((uint64_t)mine << 32 | (uint64_t)popc(b) << 16 | live, tmp64, &all);
+  const uint32_t before = (uint32_t)(all >> 32), live_all = (uint32_t)all & 0xffffu;
+  uint32_t u = before + ((uint32_t)(ex >> 16) & 0xffffu);
+  const uint32_t tot = (uint32_t)(all >> 16) & 0xffffu;
 #pragma unroll
   for (int y = 0; y < kRounds; ++y) {
     if (y >= (int)live) break;
@@ -342,9 +388,11 @@ k_token_csr(const uint32_t* __restrict__ keys, int32_t n, uint32_t rows,
     o.uid[p] = (int32_t)u - 1;
   }
   // the tile that holds the last token's place, or the first one if none is left
-  const int32_t t0 = blockIdx.x * kMidTile, end = t0 + (int32_t)live_all;
-  const bool last = live_all > 0 ? (end == n || keys[end] >= rows) : blockIdx.x == 0;
-  if (threadIdx.x == 0 && last) write_totals(o, before + tot, end);
+  const int32_t t0 = blockIdx.x * NT * kRounds, end = t0 + (int32_t)live_all;
+  if (threadIdx.x == 0) {
+    const bool last = live_all > 0 ? (end == n || keys[end] >= rows) : blockIdx.x == 0;
+    if (last) write_totals(o, before + tot, end);
+  }
 }
 
 // ---------------------------------------------------------------- large
@@ -397,6 +445,53 @@ size_t mid_bytes(int64_t n) {
   return c.used + 256;
 }
 
+template <int NT>
+int sort_mid(const int64_t* ids, int32_t n, int64_t rows, int64_t padding, int kbits,
+             const SortOut& o, int32_t* err, void* ws, hipStream_t stream) {
+  const int64_t tiles = cdiv(n, NT * kRounds);
+  Carve c(ws);
+  uint32_t* kbuf[2];
+  int32_t* vbuf[2];
+  for (auto& k : kbuf) k = c.take<uint32_t>((size_t)n);
+  for (auto& v : vbuf) v = c.take<int32_t>((size_t)n);
+  uint32_t* hist = c.take<uint32_t>((size_t)(kMidTiles * kMidBins));
+  uint32_t* heads = c.take<uint32_t>((size_t)kMidTiles);
+  const dim3 grid((unsigned)tiles), block(NT);
+  const int passes = (kbits + kMidBits - 1) / kMidBits;
+  for (int p = 0, shift = 0; p < passes; ++p) {
+    const int bits = (kbits - shift + passes - p - 1) / (passes - p);
+    const uint32_t* kin = kbuf[(p + 1) & 1];
+    const int32_t* vin = vbuf[(p + 1) & 1];
+    uint32_t* kout = kbuf[p & 1];
+    int32_t* vout = p == passes - 1 ? o.bm : vbuf[p & 1];
+    if (p == 0) {
+      hipLaunchKernelGGL((k_token_hist<NT, true>), grid, block, 0, stream, ids, nullptr, n, rows,
+                         padding, shift, bits, hist, err);
+      FS_LAUNCH_CHECK();
+      hipLaunchKernelGGL((k_token_scatter<NT, true>), grid, block, 0, stream, ids, nullptr, nullptr,
+                         n, rows, padding, shift, bits, hist, kout, vout);
+    } else {
+      hipLaunchKernelGGL((k_token_hist<NT, false>), grid, block, 0, stream, nullptr, kin, n, rows,
+                         padding, shift, bits, hist, nullptr);
+      FS_LAUNCH_CHECK();
+      hipLaunchKernelGGL((k_token_scatter<NT, false>), grid, block, 0, stream, nullptr, kin, vin, n,
+                         rows, padding, shift, bits, hist, kout, vout);
+    }
+    FS_LAUNCH_CHECK();
+    shift += bits;
+  }
+  const uint32_t* sorted = kbuf[(passes + 1) & 1];
+  const bool recount = tiles <= kRecountTiles;
+  if (!recount) {
+    hipLaunchKernelGGL(k_token_heads<NT>, grid, block, 0, stream, sorted, n, (uint32_t)rows, heads);
+    FS_LAUNCH_CHECK();
+  }
+  hipLaunchKernelGGL(k_token_csr<NT>, grid, block, 0, stream, sorted, n, (uint32_t)rows,
+                     recount ? nullptr : heads, o);
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
 }  // namespace
 }  // namespace fs
 
@@ -404,8 +499,8 @@ using namespace fs;
 
 extern "C" size_t fs_token_sort_workspace_size(int64_t n) {
   if (n <= kSmall) return 256;  // all in LDS
-  const size_t mid = mid_bytes(std::min(n, kMidTiles * kMidTile));
-  if (n <= kMidTiles * kMidTile) return mid;
+  const size_t mid = mid_bytes(std::min(n, kMidMax));
+  if (n <= kMidMax) return mid;
   Carve c(nullptr);
   c.take<int64_t>((size_t)n);
   c.take<int32_t>((size_t)n);
@@ -437,50 +532,10 @@ extern "C" int fs_token_sort(const int64_t* ids, int64_t n, int64_t rows, int64_
     return FS_OK;
   }
 
-  const int64_t tiles = cdiv(n, kMidTile);
-  if (tiles <= kMidTiles) {
-    Carve c(ws);
-    uint32_t* kbuf[2];
-    int32_t* vbuf[2];
-    for (auto& k : kbuf) k = c.take<uint32_t>((size_t)n);
-    for (auto& v : vbuf) v = c.take<int32_t>((size_t)n);
-    uint32_t* hist = c.take<uint32_t>((size_t)(kMidTiles * kMidBins));
-    uint32_t* heads = c.take<uint32_t>((size_t)kMidTiles);
-    const dim3 grid((unsigned)tiles), block(kMidThreads);
-    const int passes = (kbits + kMidBits - 1) / kMidBits;
-    for (int p = 0, shift = 0; p < passes; ++p) {
-      const int bits = (kbits - shift + passes - p - 1) / (passes - p);
-      const uint32_t* kin = kbuf[(p + 1) & 1];
-      const int32_t* vin = vbuf[(p + 1) & 1];
-      uint32_t* kout = kbuf[p & 1];
-      int32_t* vout = p == passes - 1 ? occ_bm : vbuf[p & 1];
-      if (p == 0) {
-        hipLaunchKernelGGL(k_token_hist<true>, grid, block, 0, stream, ids, nullptr, (int32_t)n,
-                           rows, padding_id, shift, bits, hist, err);
-        FS_LAUNCH_CHECK();
-        hipLaunchKernelGGL(k_token_scatter<true>, grid, block, 0, stream, ids, nullptr, nullptr,
-                           (int32_t)n, rows, padding_id, shift, bits, hist, kout, vout);
-      } else {
-        hipLaunchKernelGGL(k_token_hist<false>, grid, block, 0, stream, nullptr, kin, (int32_t)n,
-                           rows, padding_id, shift, bits, hist, nullptr);
-        FS_LAUNCH_CHECK();
-        hipLaunchKernelGGL(k_token_scatter<false>, grid, block, 0, stream, nullptr, kin, vin,
-                           (int32_t)n, rows, padding_id, shift, bits, hist, kout, vout);
-      }
-      FS_LAUNCH_CHECK();
-      shift += bits;
-    }
-    const uint32_t* sorted = kbuf[(passes + 1) & 1];
-    if (tiles > kRecountTiles) {
-      hipLaunchKernelGGL(k_token_heads, grid, block, 0, stream, sorted, (int32_t)n, (uint32_t)rows,
-                         heads);
-      FS_LAUNCH_CHECK();
-    }
-    hipLaunchKernelGGL(k_token_csr, grid, block, 0, stream, sorted, (int32_t)n, (uint32_t)rows,
-                       tiles > kRecountTiles ? heads : nullptr, o);
-    FS_LAUNCH_CHECK();
-    return FS_OK;
-  }
+  if (n <= kMidTiles * 256 * kRounds)
+    return sort_mid<256>(ids, (int32_t)n, rows, padding_id, kbits, o, err, ws, stream);
+  if (n <= kMidMax)
+    return sort_mid<1024>(ids, (int32_t)n, rows, padding_id, kbits, o, err, ws, stream);
 
   Carve c(ws);
   int64_t* keys = c.take<int64_t>((size_t)n);
