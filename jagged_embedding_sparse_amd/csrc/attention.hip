@@ -15,7 +15,6 @@ namespace fs {
 namespace attn {
 namespace {
 
-constexpr int kTableThreads = 1024;
 constexpr int kBuckets = 256;
 
 // One workgroup per table: one descriptor per tile of each sample, those with
@@ -28,17 +27,19 @@ constexpr int kBuckets = 256;
 // would let samples overlap (and outgrow the table): then there are no tiles.
 // Threads run over tiles, not samples, so one long sample takes no longer
 // than many short ones.
-__global__ void __launch_bounds__(kTableThreads)
+template <int NT>
+__global__ void __launch_bounds__(NT)
 k_attn_tiles(const int64_t* __restrict__ offsets, int32_t n, int64_t n_tok,
              const int32_t* __restrict__ n_cand, int32_t causal, TileTable t0, TileTable t1,
              int32_t* __restrict__ err) {
   __shared__ int32_t first[kBuckets], tmp[17];
-  __shared__ int32_t s_lo[kTableThreads], s_len[kTableThreads], s_cand[kTableThreads];
-  __shared__ int32_t s_at[kTableThreads + 1];
+  __shared__ int32_t s_lo[NT], s_len[NT], s_cand[NT];
+  __shared__ int32_t s_at[NT + 1];
   const TileTable t = blockIdx.x ? t1 : t0;
   bool bad = false, order = true;
+  static_assert(NT >= kBuckets, "a thread per bucket");
   if (threadIdx.x < kBuckets) first[threadIdx.x] = 0;
-  for (int32_t s = threadIdx.x; s < n; s += kTableThreads)
+  for (int32_t s = threadIdx.x; s < n; s += NT)
     order &= offsets[s] >= 0 && offsets[s] <= offsets[s + 1] && offsets[s + 1] <= n_tok;
   if (__syncthreads_or(!order)) {
     flag_err(err, !order, FS_EF_SHAPE);
@@ -47,9 +48,9 @@ k_attn_tiles(const int64_t* __restrict__ offsets, int32_t n, int64_t n_tok,
   }
   // pass 0 counts the tiles of each bucket, pass 1 places them
   for (int pass = 0; pass < 2; ++pass) {
-    for (int32_t c0 = 0; c0 < n; c0 += kTableThreads) {  // uniform
-      const int32_t s = c0 + threadIdx.x, left = min(n - c0, kTableThreads);
-      if (n > kTableThreads || pass == 0) {  // one chunk stays in LDS for the second pass
+    for (int32_t c0 = 0; c0 < n; c0 += NT) {  // uniform
+      const int32_t s = c0 + threadIdx.x, left = min(n - c0, NT);
+      if (n > NT || pass == 0) {  // one chunk stays in LDS for the second pass
         int32_t lo = 0, len = 0, cand = 0;
         if (s < n) {
           lo = (int32_t)offsets[s];
@@ -64,10 +65,10 @@ k_attn_tiles(const int64_t* __restrict__ offsets, int32_t n, int64_t n_tok,
         s_len[threadIdx.x] = len;
         s_cand[threadIdx.x] = cand;
         s_at[threadIdx.x] = at;
-        if (threadIdx.x == 0) s_at[kTableThreads] = total;
+        if (threadIdx.x == 0) s_at[NT] = total;
         __syncthreads();
       }
-      for (int32_t e = threadIdx.x; e < s_at[kTableThreads]; e += kTableThreads) {
+      for (int32_t e = threadIdx.x; e < s_at[NT]; e += NT) {
         int32_t a = 0, b = left - 1;  // the last sample that starts at or before tile e
         while (a < b) {
           const int32_t mid = (a + b + 1) >> 1;
@@ -275,8 +276,13 @@ int make_view(const fs_heads* x, int32_t heads, int32_t dim, View* v) {
 int launch_tiles(const int64_t* offsets, int32_t n, int64_t n_tok, const int32_t* n_cand,
                  int32_t causal, const TileTable* t, int32_t tables, int32_t* err,
                  hipStream_t stream) {
-  hipLaunchKernelGGL(k_attn_tiles, dim3((unsigned)tables), dim3(kTableThreads), 0, stream, offsets,
-                     n, n_tok, n_cand, causal, t[0], t[tables - 1], err);
+  // few samples and tiles: barriers of four waves instead of sixteen
+  if (n <= 256 && tile_cap(n_tok, n, t[0].rows) <= 1024)
+    hipLaunchKernelGGL(k_attn_tiles<256>, dim3((unsigned)tables), dim3(256), 0, stream, offsets, n,
+                       n_tok, n_cand, causal, t[0], t[tables - 1], err);
+  else
+    hipLaunchKernelGGL(k_attn_tiles<1024>, dim3((unsigned)tables), dim3(1024), 0, stream, offsets, n,
+                       n_tok, n_cand, causal, t[0], t[tables - 1], err);
   FS_LAUNCH_CHECK();
   return FS_OK;
 }

@@ -37,9 +37,11 @@ struct BwdArgs {
 // parts only add their traffic.
 constexpr int64_t kParts = 512;   // workgroups to reach
 constexpr int64_t kSplitMax = 8;  // parts of one tile
-__host__ inline int32_t splits_of(int64_t n_tok, int32_t kv_heads) {
+constexpr int64_t kPartSteps = 4;  // steps that a part of a tile of average length has, at least
+__host__ inline int32_t splits_of(int64_t n_tok, int32_t n, int32_t kv_heads, int32_t group) {
   const int64_t tiles = std::max<int64_t>(1, n_tok / 128 * kv_heads);
-  return (int32_t)std::min(kSplitMax, cdiv(kParts, tiles));
+  const int64_t steps = n_tok / n * group / kStep;
+  return (int32_t)std::max<int64_t>(1, std::min({kSplitMax, cdiv(kParts, tiles), steps / kPartSteps}));
 }
 // The most tokens times splits of any call with at most n_tok tokens: a call
 // has s splits or more while its tiles are at most (kParts - 1) / (s - 1).
@@ -618,7 +620,7 @@ extern "C" int fs_jagged_attention_backward(
   if (n == 0 || n_tok == 0) return FS_OK;
   const int32_t pack = pack_of(heads / kv_heads), rows = 128 / pack;
   const int64_t row_cap = tile_cap(n_tok, n, rows), key_cap = tile_cap(n_tok, n, 128);
-  a.splits = splits_of(n_tok, kv_heads);
+  a.splits = splits_of(n_tok, n, kv_heads, heads / kv_heads);
   if (row_cap * (heads / pack) >= (int64_t)INT32_MAX ||
       key_cap * kv_heads * a.splits >= (int64_t)INT32_MAX)
     return FS_ERR_UNSUPPORTED;

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes as C
 import os
+import struct
 
 import torch
 
@@ -45,7 +46,8 @@ class FsHeads(C.Structure):
 
 _L = C.CDLL(LIB_PATH)
 _P, _i32, _i64, _sz, _f = C.c_void_p, C.c_int32, C.c_int64, C.c_size_t, C.c_float
-_TP, _HP = C.POINTER(FsTable), C.POINTER(FsHeads)
+_TP = C.POINTER(FsTable)
+_HP = C.c_void_p  # const fs_heads*
 
 
 def _sig(name, res, *args):
@@ -498,14 +500,24 @@ def _dtype(dt):
     return _DTYPES[dt]
 
 
+def _here(t):
+    """The device of a call's first tensor, which has to be the current one: the
+    call's stream, its other tensors and what it allocates belong to that."""
+    d = t.device
+    if d.type != "cuda" or d.index != torch.cuda.current_device():
+        raise FsError(f"a tensor on {d} with cuda:{torch.cuda.current_device()} current",
+                      FS_ERR_INVALID_ARG)
+    return d
+
+
 def fs_token_lookup(weight, ids, scale=1.0, dtype=None, out=None, err=None, stream=None):
     """out[i] = scale * weight[ids[i]] in `dtype` (the table's by default):
     weight [rows, dim] (fp32, bf16 or fp16, rows contiguous, any row stride),
     ids int64 [n]. IDs outside the table give zeros and flag FS_EF_ID_RANGE."""
     assert weight.dim() == 2 and ids.dtype == torch.int64
-    n, dim = ids.numel(), weight.shape[1]
+    n, dim, d = ids.numel(), weight.shape[1], _here(weight)
     if out is None:
-        out = torch.empty((n, dim), dtype=dtype or weight.dtype, device=_dev())
+        out = torch.empty((n, dim), dtype=dtype or weight.dtype, device=d)
     assert out.shape == (n, dim)
     tab = FsTable()
     tab.weights, tab.stride = _rows_ptr(weight)
@@ -527,10 +539,10 @@ def fs_token_sort(ids, rows, padding_id=-1, out=None, err=None, ws=None, stream=
     occ_uid, counts): fs_token_grad, fs_grad_reduce_update and
     fs_jagged_lookup take them."""
     assert ids.dtype == torch.int64
-    n = ids.numel()
+    n, d = ids.numel(), _here(ids)
     cap, nb = max(n, 1), token_sort_workspace_size(n)
     if out is None:  # two allocations for the six outputs and the workspace
-        d, nw = _dev(), 0 if ws is not None else -(-nb // 8)
+        nw = 0 if ws is not None else -(-nb // 8)
         w64, uq, uo, counts = torch.empty(nw + cap + 6, dtype=torch.int64,
                                           device=d).split_with_sizes((nw, cap, 2, 4))
         seg, bm, uid = torch.empty(3 * cap + 1, dtype=torch.int32,
@@ -558,10 +570,10 @@ def fs_token_grad(uq, dout, rows, scale=1.0, dtype=torch.float32, grad=None, acc
     dout [n, dim] and their sort `uq` (fs_token_sort's outputs, or a dedup's
     of one table and W shards). With accumulate it is added to `grad`."""
     assert dout.dim() == 2
-    n, dim = dout.shape
+    (n, dim), d = dout.shape, _here(dout)
     if grad is None:
         assert not accumulate, "accumulate adds to a given grad"
-        grad = torch.empty((rows, dim), dtype=dtype, device=_dev())
+        grad = torch.empty((rows, dim), dtype=dtype, device=d)
     assert grad.shape == (rows, dim)
     ws = _ws(token_grad_workspace_size(n, dim), ws)
     dptr, dstride = _rows_ptr(dout)
@@ -578,14 +590,17 @@ def fs_token_grad(uq, dout, rows, scale=1.0, dtype=torch.float32, grad=None, acc
 # ---------------------------------------------------------------------------- jagged attention
 
 
+_PACK_HEADS = struct.Struct("Pqq").pack  # fs_heads, in a tenth of a ctypes structure's time
+
+
 def _heads_arg(t, shape, dtype):
     """fs_heads of a [n_tok, heads, dim] tensor with contiguous rows (an axis
     of one entry has no stride of its own: 0, dense)."""
-    assert t.is_cuda and t.dim() == 3 and t.shape == shape and t.dtype == dtype
-    assert t.stride(2) == 1, "a head's elements must be contiguous"
+    assert t.is_cuda and t.shape == shape and t.dtype == dtype
+    tok, head, one = t.stride()
+    assert one == 1, "a head's elements must be contiguous"
     e = t.element_size()
-    return FsHeads(t.data_ptr(), t.stride(0) * e if shape[0] > 1 else 0,
-                   t.stride(1) * e if shape[1] > 1 else 0)
+    return _PACK_HEADS(t.data_ptr(), tok * e if shape[0] > 1 else 0, head * e if shape[1] > 1 else 0)
 
 
 def _attention_args(q, k, v, offsets, n_cand, valid, scale):
@@ -595,9 +610,9 @@ def _attention_args(q, k, v, offsets, n_cand, valid, scale):
     assert offsets.dtype == torch.int64
     assert n_cand is None or (n_cand.dtype == torch.int32 and n_cand.numel() == n)
     assert valid is None or (valid.dtype in (torch.uint8, torch.bool) and valid.numel() == n_tok)
-    return (n_tok, heads, dim, kv, n, dim ** -0.5 if scale is None else float(scale),
-            [_heads_arg(q, q.shape, q.dtype), _heads_arg(k, kv, q.dtype),
-             _heads_arg(v, kv, q.dtype)])
+    return (_here(q), n_tok, heads, dim, kv, n, dim ** -0.5 if scale is None else float(scale),
+            (_heads_arg(q, q.shape, q.dtype), _heads_arg(k, kv, q.dtype),
+             _heads_arg(v, kv, q.dtype)))
 
 
 def attention_workspace_size(n_tok, n):
@@ -612,11 +627,11 @@ def fs_jagged_attention(q, k, v, offsets, n_cand=None, valid=None, causal=True, 
     valid uint8 or bool [n_tok]. scale: 1 / sqrt(dim) by default. Returns out
     like q (dense) and lse fp32 [heads, n_tok]; rows of tokens behind the last
     sample are not written."""
-    n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale)
+    d, n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale)
     if out is None:
-        out = torch.empty((n_tok, heads, dim), dtype=q.dtype, device=_dev())
+        out = torch.empty((n_tok, heads, dim), dtype=q.dtype, device=d)
     if lse is None:
-        lse = torch.empty((heads, n_tok), dtype=torch.float32, device=_dev())
+        lse = torch.empty((heads, n_tok), dtype=torch.float32, device=d)
     assert lse.dtype == torch.float32 and lse.shape == (heads, n_tok)
     ws = _ws(attention_workspace_size(n_tok, n), ws)
     _check("fs_jagged_attention",
@@ -637,9 +652,8 @@ def fs_jagged_attention_backward(q, k, v, out, lse, dout, offsets, n_cand=None, 
     """Gradients (dq, dk, dv) of fs_jagged_attention from its outputs out and
     lse and the gradient dout of out; the other arguments are the forward
     call's. Outputs may be views (e.g. of one projection's gradient)."""
-    n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale)
+    d, n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale)
     assert lse.dtype == torch.float32 and lse.shape == (heads, n_tok)
-    d = _dev()
     dq = dq if dq is not None else torch.empty((n_tok, heads, dim), dtype=q.dtype, device=d)
     dk = dk if dk is not None else torch.empty(kv, dtype=q.dtype, device=d)
     dv = dv if dv is not None else torch.empty(kv, dtype=q.dtype, device=d)
