@@ -139,13 +139,11 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   Staged<DP, NT> ks, vs;
   uint64_t keys = 0;
   uint32_t ahead = 0;
-  bool full = false;
   auto load = [&](int step) {
     const int j = key0(step);
     keys = live_bits(ahead);
-    full = keys == ~0ull && a.s.dim == DP;
-    ks.load(kp, a.k.tok, a.s, t, j, full);
-    vs.load(vp, a.v.tok, a.s, t, j, full);
+    ks.load(kp, a.k.tok, a.s, t, j);
+    vs.load(vp, a.v.tok, a.s, t, j);
     if (step + 1 < steps) ahead = live_byte(a.s, t, key0(step + 1));
   };
   if (steps > 0) {
@@ -155,8 +153,8 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   for (int step = 0; step < steps; ++step) {
     const int j0 = key0(step), b = step & 1;
     const uint64_t live = keys;
-    ks.store(sk[b], a.s, live, full);
-    vs.store(sv[b], a.s, live, full);
+    ks.store(sk[b], a.s, live);
+    vs.store(sv[b], a.s, live);
     if (live != ~0ull) store_off(s_off[b], live);
     __syncthreads();
     if (step + 1 < steps) load(step + 1);

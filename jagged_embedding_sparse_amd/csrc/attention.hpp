@@ -246,7 +246,8 @@ __device__ __forceinline__ uint64_t live_bits(uint32_t byte) { return __ballot(b
 // registers, store() writes them to LDS, zeros in the place of what is not
 // live or lies past the head's width. Rows past the sample load its last one
 // and pieces past the width the first, so every load is in bounds and none is
-// conditional; tiles that are live throughout skip all of that.
+// conditional; tiles inside the sample (of heads as wide as the tile) skip
+// that, and tiles that are live throughout the zeros.
 template <int DP, int NT>
 struct Staged {
   static constexpr int kRows = 64;
@@ -257,10 +258,10 @@ struct Staged {
   u32x4 v[kPer];
 
   __device__ __forceinline__ void load(const char* head, int64_t tok_bytes, const Shape& a,
-                                       const Tile& t, int r0, bool whole) {
+                                       const Tile& t, int r0) {
     const int row = threadIdx.x / kPieces, p = threadIdx.x % kPieces;
     const char* base = head + ((int64_t)t.lo + r0) * tok_bytes;  // uniform
-    if (whole) {
+    if (r0 + kRows <= t.len && a.dim == DP) {
       const uint32_t at = (uint32_t)row * (uint32_t)tok_bytes + 16 * p;
 #pragma unroll
       for (int x = 0; x < kPer; ++x)
@@ -272,10 +273,9 @@ struct Staged {
         v[x] = *(const u32x4*)(base + (int64_t)min(row + x * kStepRows, last) * tok_bytes + pc);
     }
   }
-  __device__ __forceinline__ void store(uint16_t* tile, const Shape& a, uint64_t live,
-                                        bool whole) const {
+  __device__ __forceinline__ void store(uint16_t* tile, const Shape& a, uint64_t live) const {
     const int row = threadIdx.x / kPieces, p = threadIdx.x % kPieces;
-    if (whole) {
+    if (live == ~0ull && a.dim == DP) {
 #pragma unroll
       for (int x = 0; x < kPer; ++x) *(u32x4*)(tile + piece<DP>(row + x * kStepRows, p)) = v[x];
     } else {

@@ -150,11 +150,10 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
     for (int step = 0; step < steps; ++step) {
       const int j0 = key0(step);
       const uint64_t live = live_bits(live_byte(a.s, t, j0));
-      const bool full = live == ~0ull && a.s.dim == DP;
-      ks.load(kp, a.k.tok, a.s, t, j0, full);
-      vs.load(vp, a.v.tok, a.s, t, j0, full);
-      ks.store(sk[0], a.s, live, full);
-      vs.store(sv[0], a.s, live, full);
+      ks.load(kp, a.k.tok, a.s, t, j0);
+      vs.load(vp, a.v.tok, a.s, t, j0);
+      ks.store(sk[0], a.s, live);
+      vs.store(sv[0], a.s, live);
       if (live != ~0ull) store_off(s_off[0], live);
       __syncthreads();
 #pragma unroll 1
@@ -176,13 +175,11 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
 
   uint64_t keys = 0;
   uint32_t ahead = 0;
-  bool full = false;
   auto load = [&](int step) {
     const int j = key0(step);
     keys = live_bits(ahead);
-    full = keys == ~0ull && a.s.dim == DP;
-    ks.load(kp, a.k.tok, a.s, t, j, full);
-    vs.load(vp, a.v.tok, a.s, t, j, full);
+    ks.load(kp, a.k.tok, a.s, t, j);
+    vs.load(vp, a.v.tok, a.s, t, j);
     if (step + 1 < steps) ahead = live_byte(a.s, t, key0(step + 1));
   };
   if (steps > 0) {
@@ -192,8 +189,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   for (int step = 0; step < steps; ++step) {
     const int j0 = key0(step), b = step & 1;
     const uint64_t live = keys;
-    ks.store(sk[b], a.s, live, full);
-    vs.store(sv[b], a.s, live, full);
+    ks.store(sk[b], a.s, live);
+    vs.store(sv[b], a.s, live);
     if (live != ~0ull) store_off(s_off[b], live);
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
@@ -261,15 +258,13 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
   Staged<DP, NT> qs, ds;
   uint64_t rows = 0;
   uint32_t ahead = 0;
-  bool full = false;
   float st_lse = INFINITY, st_delta = 0.f;  // threads 0 .. 63: one row each
   auto row0 = [&](int step) { return (first + step % per) * kStep; };
   auto load = [&](int step) {
     const int head = kvh * a.s.group + step / per, i0 = row0(step);
     rows = live_bits(ahead);
-    full = rows == ~0ull && a.s.dim == DP;
-    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0, full);
-    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0, full);
+    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
+    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
     if (threadIdx.x < kStep) {
       const int i = min(i0 + (int)threadIdx.x, t.len - 1);
       const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
@@ -285,8 +280,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
   for (int step = step0; step < steps; ++step) {
     const int i0 = row0(step), b = step & 1;
     const uint64_t live = rows;
-    qs.store(sq[b], a.s, live, full);
-    ds.store(sd[b], a.s, live, full);
+    qs.store(sq[b], a.s, live);
+    ds.store(sd[b], a.s, live);
     if (threadIdx.x < kStep) {
       const bool in = (live >> threadIdx.x) & 1;
       s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e;
@@ -405,15 +400,13 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
   Staged<DP, NT> qs, ds;
   uint64_t rows = 0;
   uint32_t ahead = 0;
-  bool full = false;
   float st_lse = INFINITY, st_delta = 0.f;  // threads 0 .. 63: one row each
   auto row0 = [&](int step) { return (first + step % per) * kStep; };
   auto load = [&](int step) {
     const int head = kvh * a.s.group + step / per, i0 = row0(step);
     rows = live_bits(ahead);
-    full = rows == ~0ull && a.s.dim == DP;
-    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0, full);
-    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0, full);
+    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
+    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
     if (threadIdx.x < kStep) {
       const int i = min(i0 + (int)threadIdx.x, t.len - 1);
       const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
@@ -433,8 +426,8 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
     const int e = step & 1;
     const uint64_t live = rows;
     if (step < steps) {
-      qs.store(sq[b], a.s, live, full);
-      ds.store(sd[b], a.s, live, full);
+      qs.store(sq[b], a.s, live);
+      ds.store(sd[b], a.s, live);
       if (threadIdx.x < kStep) {
         const bool in = (live >> threadIdx.x) & 1;
         s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e;
