@@ -136,14 +136,14 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   const int steps = hist_end + max(0, own_end - own_lo);
   auto key0 = [&](int step) { return (step < hist_end ? step : own_lo + step - hist_end) * kKeys; };
 
-  Staged<DP, NT> ks, vs;
+  using Tiles = Direct<DP, NT>;
   uint64_t keys = 0;
   uint32_t ahead = 0;
   auto load = [&](int step) {
     const int j = key0(step);
     keys = live_bits(ahead);
-    ks.load(kp, a.k.tok, a.s, t, j);
-    vs.load(vp, a.v.tok, a.s, t, j);
+    Tiles::load(sk[step & 1], kp, a.k.tok, a.s, t, j);
+    Tiles::load(sv[step & 1], vp, a.v.tok, a.s, t, j);
     if (step + 1 < steps) ahead = live_byte(a.s, t, key0(step + 1));
   };
   if (steps > 0) {
@@ -153,8 +153,9 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   for (int step = 0; step < steps; ++step) {
     const int j0 = key0(step), b = step & 1;
     const uint64_t live = keys;
-    ks.store(sk[b], a.s, live);
-    vs.store(sv[b], a.s, live);
+    Tiles::wait();
+    Tiles::finish(sk[b], a.s, live);
+    Tiles::finish(sv[b], a.s, live);
     if (live != ~0ull) store_off(s_off[b], live);
     __syncthreads();
     if (step + 1 < steps) load(step + 1);

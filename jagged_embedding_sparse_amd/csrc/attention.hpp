@@ -73,6 +73,13 @@ __device__ __forceinline__ int wave_id() {
   return __builtin_amdgcn_readfirstlane((int)threadIdx.x / kWave);
 }
 
+__device__ __forceinline__ const char* uniform(const char* p) {
+  const uint64_t x = (uint64_t)p;
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)x);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((uint32_t)(x >> 32));
+  return (const char*)((uint64_t)hi << 32 | lo);
+}
+
 __device__ __forceinline__ f32x16 zero16() {
   f32x16 z;
 #pragma unroll
@@ -291,6 +298,67 @@ struct Staged {
       }
     }
   }
+};
+
+// The same tile without registers: load() lets memory write to LDS as it
+// arrives, finish() clears what is not live. A wave's load fills 1024 bytes of
+// LDS in the order of its lanes, so a lane loads the piece that belongs at its
+// place. The instruction is written out because the compiler otherwise waits
+// for it before the next read of any LDS, which is where the other tile's
+// products start: wait() is the one wait, before the barrier that lets the
+// tile be read, and nothing reads or writes the tile between load() and that.
+template <int DP, int NT>
+struct Direct {
+  static constexpr int kRows = 64;
+  static constexpr int kPieces = DP / 8;
+  static constexpr int kPer = kRows * kPieces / NT;
+  static constexpr int kStepRows = NT / kPieces;
+  static_assert(kPer >= 1 && kRows * kPieces % NT == 0, "whole pieces per thread");
+  static_assert(kStepRows % 16 == 0, "a thread's rows share the permutation");
+
+  static __device__ __forceinline__ int piece_of() {
+    return ((int)threadIdx.x % kPieces) ^ swz<DP>(threadIdx.x / kPieces);
+  }
+  // 16 bytes per lane from base + at to LDS address `to` + 16 lane; base and
+  // `to` are uniform. The instruction takes `to` from M0 (which nothing else in
+  // these kernels uses), one idle cycle after it is written.
+  static __device__ __forceinline__ void load16(const char* base, uint32_t at, uint32_t to) {
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :
+                 : "s"(to), "v"(at), "s"(base)
+                 : "memory");
+  }
+  static __device__ __forceinline__ void load(uint16_t* tile, const char* head, int64_t tok_bytes,
+                                              const Shape& a, const Tile& t, int r0) {
+    typedef __attribute__((address_space(3))) uint16_t* lds_ptr;
+    const int row = threadIdx.x / kPieces, p = piece_of();
+    const char* base = uniform(head + ((int64_t)t.lo + r0) * tok_bytes);
+    const uint32_t to = __builtin_amdgcn_readfirstlane(
+        (uint32_t)(uintptr_t)(lds_ptr)tile + threadIdx.x / kWave * (kWave * 16));
+    if (r0 + kRows <= t.len && a.dim == DP) {
+      const uint32_t at = (uint32_t)row * (uint32_t)tok_bytes + 16 * p;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x)
+        load16(uniform(base + (int64_t)x * kStepRows * tok_bytes), at, to + x * NT * 16);
+    } else {
+      const int last = t.len - 1 - r0, pc = 8 * p < a.dim ? 16 * p : 0;
+#pragma unroll
+      for (int x = 0; x < kPer; ++x)
+        load16(base, (uint32_t)min(row + x * kStepRows, last) * (uint32_t)tok_bytes + pc,
+               to + x * NT * 16);
+    }
+  }
+  // before the barrier that lets the tile be read, after wait()
+  static __device__ __forceinline__ void finish(uint16_t* tile, const Shape& a, uint64_t live) {
+    if (live == ~0ull && a.dim == DP) return;
+    const int row = threadIdx.x / kPieces;
+    const bool in = 8 * piece_of() < a.dim;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x)
+      if (!in || !((live >> (row + x * kStepRows)) & 1))
+        *(u32x4*)(tile + (x * NT + threadIdx.x) * 8) = u32x4{0, 0, 0, 0};
+  }
+  static __device__ __forceinline__ void wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 };
 
 // What a score of each key of a tile starts from: 0, or -inf for keys that

@@ -141,7 +141,7 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
     }
   };
 
-  Staged<DP, NT> ks, vs;
+  using Tiles = Direct<DP, NT>;
   // delta comes with the rounding of out to 16 bits. Where a row sees few keys,
   // out is as large as v and that is as much as all of dS's own rounding: rows
   // of at most two steps sum delta = sum_j P_ij dP_ij first, in fp32.
@@ -150,10 +150,11 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
     for (int step = 0; step < steps; ++step) {
       const int j0 = key0(step);
       const uint64_t live = live_bits(live_byte(a.s, t, j0));
-      ks.load(kp, a.k.tok, a.s, t, j0);
-      vs.load(vp, a.v.tok, a.s, t, j0);
-      ks.store(sk[0], a.s, live);
-      vs.store(sv[0], a.s, live);
+      Tiles::load(sk[0], kp, a.k.tok, a.s, t, j0);
+      Tiles::load(sv[0], vp, a.v.tok, a.s, t, j0);
+      Tiles::wait();
+      Tiles::finish(sk[0], a.s, live);
+      Tiles::finish(sv[0], a.s, live);
       if (live != ~0ull) store_off(s_off[0], live);
       __syncthreads();
 #pragma unroll 1
@@ -178,8 +179,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   auto load = [&](int step) {
     const int j = key0(step);
     keys = live_bits(ahead);
-    ks.load(kp, a.k.tok, a.s, t, j);
-    vs.load(vp, a.v.tok, a.s, t, j);
+    Tiles::load(sk[step & 1], kp, a.k.tok, a.s, t, j);
+    Tiles::load(sv[step & 1], vp, a.v.tok, a.s, t, j);
     if (step + 1 < steps) ahead = live_byte(a.s, t, key0(step + 1));
   };
   if (steps > 0) {
@@ -189,8 +190,9 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   for (int step = 0; step < steps; ++step) {
     const int j0 = key0(step), b = step & 1;
     const uint64_t live = keys;
-    ks.store(sk[b], a.s, live);
-    vs.store(sv[b], a.s, live);
+    Tiles::wait();
+    Tiles::finish(sk[b], a.s, live);
+    Tiles::finish(sv[b], a.s, live);
     if (live != ~0ull) store_off(s_off[b], live);
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
@@ -255,7 +257,7 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
   const int step0 = (int)((int64_t)all * part / a.splits);
   const int steps = (int)((int64_t)all * (part + 1) / a.splits);
 
-  Staged<DP, NT> qs, ds;
+  using Tiles = Direct<DP, NT>;
   uint64_t rows = 0;
   uint32_t ahead = 0;
   float st_lse = INFINITY, st_delta = 0.f;  // threads 0 .. 63: one row each
@@ -263,8 +265,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
   auto load = [&](int step) {
     const int head = kvh * a.s.group + step / per, i0 = row0(step);
     rows = live_bits(ahead);
-    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
-    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
+    Tiles::load(sq[step & 1], a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
+    Tiles::load(sd[step & 1], a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
     if (threadIdx.x < kStep) {
       const int i = min(i0 + (int)threadIdx.x, t.len - 1);
       const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
@@ -280,8 +282,9 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)
   for (int step = step0; step < steps; ++step) {
     const int i0 = row0(step), b = step & 1;
     const uint64_t live = rows;
-    qs.store(sq[b], a.s, live);
-    ds.store(sd[b], a.s, live);
+    Tiles::wait();
+    Tiles::finish(sq[b], a.s, live);
+    Tiles::finish(sd[b], a.s, live);
     if (threadIdx.x < kStep) {
       const bool in = (live >> threadIdx.x) & 1;
       s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e;
