@@ -400,16 +400,16 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
   const int step0 = (int)((int64_t)all * part / a.splits);
   const int steps = (int)((int64_t)all * (part + 1) / a.splits);
 
-  Staged<DP, NT> qs, ds;
+  using Tiles = Direct<DP, NT>;
   uint64_t rows = 0;
   uint32_t ahead = 0;
   float st_lse = INFINITY, st_delta = 0.f;  // threads 0 .. 63: one row each
   auto row0 = [&](int step) { return (first + step % per) * kStep; };
-  auto load = [&](int step) {
+  auto load = [&](int step, int to) {
     const int head = kvh * a.s.group + step / per, i0 = row0(step);
     rows = live_bits(ahead);
-    qs.load(a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
-    ds.load(a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
+    Tiles::load(sq[to], a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
+    Tiles::load(sd[to], a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
     if (threadIdx.x < kStep) {
       const int i = min(i0 + (int)threadIdx.x, t.len - 1);
       const int64_t at = (int64_t)head * a.s.n_tok + t.lo + i;
@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
   };
   if (step0 < steps) {
     ahead = live_byte(a.s, t, row0(step0));
-    load(step0);
+    load(step0, 0);
   }
   bool have = false;       // the last step's operands wait to be summed
   u32x4 mine[2];           // this wave's own of them
@@ -429,8 +429,9 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
     const int e = step & 1;
     const uint64_t live = rows;
     if (step < steps) {
-      qs.store(sq[b], a.s, live);
-      ds.store(sd[b], a.s, live);
+      Tiles::wait();
+      Tiles::finish(sq[b], a.s, live);
+      Tiles::finish(sd[b], a.s, live);
       if (threadIdx.x < kStep) {
         const bool in = (live >> threadIdx.x) & 1;
         s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e;
@@ -438,7 +439,7 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
       }
     }
     __syncthreads();
-    if (step + 1 < steps) load(step + 1);
+    if (step + 1 < steps) load(step + 1, b == 2 ? 0 : b + 1);
     const int i0 = row0(step), r0 = i0 + 32 * half;
     // steps whose rows see none of these keys (the same for both waves)
     const bool none = step >= steps || j0 >= t1 || (causal && i0 + kStep <= j0) ||
