@@ -224,7 +224,7 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
 // in steps. S = q k^T and dP = dO v^T have one key per lane, so P and dS are
 // the operands of dV^T = dO^T P and dK^T = q^T dS.
 template <typename T, int DP, int NW>
-__global__ void __launch_bounds__(NW * kWave, DP == 128 ? 1 : (DP == 64 ? 2 : 3)) k_attn_dkv(BwdArgs a) {
+__global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdArgs a) {
   constexpr int NT = NW * kWave;
   __shared__ uint16_t sq[2][kStep * DP], sd[2][kStep * DP];
   __shared__ __attribute__((aligned(16))) float s_lse[2][kStep], s_delta[2][kStep];

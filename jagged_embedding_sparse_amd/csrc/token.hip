@@ -167,6 +167,7 @@ __device__ __forceinline__ Cols cols_of(const TokGradArgs& a, int32_t tile, int3
 template <typename TO, int N>
 __device__ __forceinline__ void put_row(const TokGradArgs& a, int64_t row, const Cols& c,
                                         const double (&s)[N]) {
+  if (row < 0 || row >= a.rows) return;  // the sort of a larger table
   Pack<TO, N>* p = (Pack<TO, N>*)(a.grad + row * a.out_stride + c.at * (int64_t)sizeof(TO));
   Pack<TO, N> y;
   if (a.accumulate) {
@@ -267,7 +268,7 @@ __global__ void __launch_bounds__(kThreads) k_token_grad(TokGradArgs a) {
     // past the last sorted token the arrays hold anything: clamped to be read
     const int32_t u = in ? a.occ_uid[base + x] : 0;
     st.uid[x] = u;
-    st.bm[x] = in ? a.occ_bm[base + x] : 0;
+    st.bm[x] = in ? min(max(a.occ_bm[base + x], 0), (int32_t)a.n - 1) : 0;
     st.row[x] = (uint32_t)a.unique[min(max(u, 0), (int32_t)a.n - 1)];
   }
   if (threadIdx.x == 0) s_any = 0;

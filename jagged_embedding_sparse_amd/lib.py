@@ -510,6 +510,15 @@ def _here(t):
     return d
 
 
+def _own_rows_ptr(t):
+    """_rows_ptr of rows that lie apart: a stride of 0 (one row expanded to
+    many) would read as dense in the C call."""
+    if t.shape[0] > 1 and t.stride(0) == 0:
+        raise FsError("rows expanded from one", FS_ERR_INVALID_ARG)
+    p, stride = _rows_ptr(t)
+    return p, stride if t.shape[0] > 1 else 0
+
+
 def fs_token_lookup(weight, ids, scale=1.0, dtype=None, out=None, err=None, stream=None):
     """out[i] = scale * weight[ids[i]] in `dtype` (the table's by default):
     weight [rows, dim] (fp32, bf16 or fp16, rows contiguous, any row stride),
@@ -520,9 +529,9 @@ def fs_token_lookup(weight, ids, scale=1.0, dtype=None, out=None, err=None, stre
         out = torch.empty((n, dim), dtype=dtype or weight.dtype, device=d)
     assert out.shape == (n, dim)
     tab = FsTable()
-    tab.weights, tab.stride = _rows_ptr(weight)
+    tab.weights, tab.stride = _own_rows_ptr(weight)
     tab.rows, tab.dim, tab.dtype = weight.shape[0], dim, _dtype(weight.dtype)
-    optr, ostride = _rows_ptr(out)
+    optr, ostride = _own_rows_ptr(out)
     _check("fs_token_lookup",
            _c_token_lookup(C.byref(tab), _ptr(ids), n, float(scale), optr, _dtype(out.dtype),
                            ostride, _ptr(err), _stream(stream)))
@@ -551,6 +560,8 @@ def fs_token_sort(ids, rows, padding_id=-1, out=None, err=None, ws=None, stream=
     else:
         uq, uo, seg, bm, uid, counts = (out[k] for k in ("unique", "unique_offsets", "seg_offsets",
                                                          "occ_bm", "occ_uid", "counts"))
+        assert uo.numel() >= 2 and counts.numel() >= 4 and seg.numel() > cap and \
+            min(uq.numel(), bm.numel(), uid.numel()) >= cap, "outputs smaller than the batch"
     ws = _ws(nb, ws)
     _check("fs_token_sort",
            _c_token_sort(_ptr(ids), n, int(rows), int(padding_id), _ptr(uq), _ptr(uo), _ptr(seg),
@@ -567,17 +578,20 @@ def token_grad_workspace_size(n, dim):
 def fs_token_grad(uq, dout, rows, scale=1.0, dtype=torch.float32, grad=None, accumulate=False,
                   W=1, ws=None, stream=None):
     """The table's gradient [rows, dim] in `dtype` from the tokens' gradients
-    dout [n, dim] and their sort `uq` (fs_token_sort's outputs, or a dedup's
-    of one table and W shards). With accumulate it is added to `grad`."""
+    dout [n, dim] and their sort `uq` (fs_token_sort's outputs for these n
+    tokens and rows, or a dedup's of one table and W shards). With accumulate
+    it is added to `grad`."""
     assert dout.dim() == 2
     (n, dim), d = dout.shape, _here(dout)
     if grad is None:
         assert not accumulate, "accumulate adds to a given grad"
         grad = torch.empty((rows, dim), dtype=dtype, device=d)
     assert grad.shape == (rows, dim)
+    assert min(uq[k].numel() for k in ("unique", "occ_bm", "occ_uid")) >= n and \
+        uq["seg_offsets"].numel() > n and uq["unique_offsets"].numel() > W, "the sort of fewer tokens"
     ws = _ws(token_grad_workspace_size(n, dim), ws)
-    dptr, dstride = _rows_ptr(dout)
-    gptr, gstride = _rows_ptr(grad)
+    dptr, dstride = _own_rows_ptr(dout)
+    gptr, gstride = _own_rows_ptr(grad)
     _check("fs_token_grad",
            _c_token_grad(_ptr(uq["unique"]), _ptr(uq["unique_offsets"]), W,
                          _ptr(uq["seg_offsets"]), _ptr(uq["occ_bm"]), _ptr(uq["occ_uid"]), n, dptr,
@@ -599,6 +613,8 @@ def _heads_arg(t, shape, dtype):
     assert t.is_cuda and t.shape == shape and t.dtype == dtype
     tok, head, one = t.stride()
     assert one == 1, "a head's elements must be contiguous"
+    if (tok == 0 and shape[0] > 1) or (head == 0 and shape[1] > 1):
+        raise FsError("heads or tokens expanded from one", FS_ERR_INVALID_ARG)  # 0 means dense
     e = t.element_size()
     return _PACK_HEADS(t.data_ptr(), tok * e if shape[0] > 1 else 0, head * e if shape[1] > 1 else 0)
 

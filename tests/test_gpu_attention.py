@@ -170,6 +170,79 @@ def test_long_sample(L):
     Case([1500, 3], 2, 1, 128, HF, False, cand=[70, 1], seed=6).run(L)
 
 
+def test_split_tiles_with_masks(L):
+    """Few key tiles, whose steps are shared by several workgroups."""
+    Case([1400], 4, 1, 40, BF, True, cand=[9], masked=0.2, fused=True, seed=2).run(L)
+    Case([900, 0, 700], 2, 2, 128, HF, False, cand=[0, 0, 90], masked=0.1, seed=3, behind=70).run(L)
+
+
+def test_more_tiles_than_the_tables_buckets(L):
+    """9000 tokens: 282 tiles of 32 rows; equal keys make every sum easy."""
+    n = 9000
+    q = torch.zeros(n, 4, 16, dtype=BF, device="cuda")
+    v = (torch.arange(n, device="cuda") % 64).to(BF)[:, None, None].expand(n, 1, 16).contiguous()
+    out, lse = L.fs_jagged_attention(q, q[:, :1].contiguous(), v, torch.tensor([0, n], device="cuda"))
+    mean = torch.cumsum(v[:, 0, 0].double(), 0) / torch.arange(1, n + 1, device="cuda")
+    assert ((out[:, :, 0].double() - mean[:, None]).abs() <= 2 * P.u(BF) * mean[:, None]).all()
+    ref = torch.arange(1, n + 1, device="cuda").double().log()
+    assert ((lse.double() - ref).abs() <= 1e-5).all()
+
+
+@pytest.mark.parametrize("d", [32, 128])
+def test_heads_first_layout(L, d):
+    """[heads, n_tok, dim] memory: tokens close together, heads far apart."""
+    c = Case([100, 37], 4, 2, d, BF, True, cand=[3, 0], seed=6)
+    a = c.dev()
+    for x in "qkv":
+        a[x] = a[x].transpose(0, 1).contiguous().transpose(0, 1)
+    out = torch.empty(4, c.n, d, dtype=BF, device="cuda").transpose(0, 1)
+    lse = L.fs_jagged_attention(**a, out=out)[1]
+    plain, lse2 = L.fs_jagged_attention(**c.dev())
+    assert torch.equal(out, plain) and torch.equal(lse, lse2)
+    q, k, v = a.pop("q"), a.pop("k"), a.pop("v")
+    grads = L.fs_jagged_attention_backward(q, k, v, out, lse, c.dout.cuda(), **a)
+    b = c.dev()
+    q, k, v = b.pop("q"), b.pop("k"), b.pop("v")
+    for x, y in zip(grads, L.fs_jagged_attention_backward(q, k, v, plain, lse, c.dout.cuda(), **b)):
+        assert torch.equal(x, y)
+
+
+def test_expanded_heads_and_other_devices_are_refused(L):
+    q = torch.zeros(9, 4, 32, dtype=BF, device="cuda")
+    off = torch.tensor([0, 9], device="cuda")
+    for k in (q[:, :1].expand(9, 4, 32), q[:1].expand(9, 4, 32)):
+        with pytest.raises(L.FsError):
+            L.fs_jagged_attention(q, k, q, off)
+    with pytest.raises(L.FsError):
+        L.fs_jagged_attention(q.cpu(), q, q, off)
+
+
+def test_two_calls_at_once(L):
+    """Forward and backward of two batches on two streams, each with its own
+    workspaces, against the same calls one after the other."""
+    cases = [Case([300, 20], 4, 2, 64, BF, seed=1), Case([64, 500], 4, 4, 128, HF, False, seed=2)]
+    args = [c.dev() for c in cases]
+    dos = [c.dout.cuda() for c in cases]
+
+    def work(i, stream=None):
+        a = dict(args[i])
+        out, lse = L.fs_jagged_attention(**a, stream=stream)
+        q, k, v = a.pop("q"), a.pop("k"), a.pop("v")
+        return [out, lse, *L.fs_jagged_attention_backward(q, k, v, out, lse, dos[i], **a,
+                                                          stream=stream)]
+    alone = [work(0), work(1)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(3):
+        both = []
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                both.append(work(i))
+        torch.cuda.synchronize()
+        for x, y in zip(alone, both):
+            assert all(torch.equal(u, w) for u, w in zip(x, y))
+
+
 def test_many_short_samples(L):
     g = torch.Generator().manual_seed(1)
     lens = torch.randint(0, 9, (2500,), generator=g).tolist()

@@ -101,7 +101,8 @@ def _sorted_lists(uq):
         uq["occ_uid"][:seg[-1]].tolist()
 
 
-@pytest.mark.parametrize("n", [0, 1, 2, 63, 64, 65, 1000, 4095, 4096, 4097, 20_000, 70_001])
+@pytest.mark.parametrize("n", [0, 1, 2, 63, 64, 65, 1000, 1024, 1025, 4095, 4096, 4097, 16_384,
+                               16_385, 20_000, 65_536, 65_537, 70_001, 262_144, 262_145])
 @pytest.mark.parametrize("rows,pad", [(1, -1), (1, 0), (300, 0), (50_000, 17), (3_000_000, -1)])
 def test_sort(L, n, rows, pad):
     ids = _ids(n, rows, n + rows, skew=3.0, bad=0.05 if n % 2 else 0.0)
@@ -122,6 +123,25 @@ def test_sort_nothing_left_and_one_row(L, n):
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     L.fs_token_sort(ids.cuda(), 9, padding_id=9, err=err)
     assert int(err) == 0
+
+
+@pytest.mark.parametrize("n", [3000, 9000, 100_000, 300_000])
+@pytest.mark.parametrize("rows", [255, 256, 511, 512, 2 ** 18 - 1, 2 ** 18, 2 ** 32 - 2])
+def test_sort_at_the_bounds_of_digits(L, n, rows):
+    ids = torch.randint(0, rows, (n,), generator=_gen(n))
+    ids[::3] = rows - 1 - ids[::3] % 5
+    assert _sorted_lists(L.fs_token_sort(ids.cuda(), rows, padding_id=rows - 2)) == \
+        P.token_sort(ids, rows, rows - 2)
+
+
+@pytest.mark.parametrize("n", [4097, 66_000])
+def test_sort_drops_whole_tiles(L, n):
+    ids = torch.arange(n)
+    ids[5:] = -1
+    assert _sorted_lists(L.fs_token_sort(ids.cuda(), n)) == \
+        ([0, 1, 2, 3, 4], [0, 1, 2, 3, 4, 5], [0, 1, 2, 3, 4], [0, 1, 2, 3, 4])
+    ids[:] = 7
+    assert _sorted_lists(L.fs_token_sort(ids.cuda(), n, padding_id=7)) == ([], [0], [], [])
 
 
 def test_sort_large_rows(L):
@@ -146,7 +166,9 @@ def _check_grad(got, ids, dout, rows, pad, scale, base=None):
 @pytest.mark.parametrize("to", TYPES)
 @pytest.mark.parametrize("n,rows,dim,pad", [(1, 1, 1, -1), (7, 3, 5, 0), (300, 700, 64, 0),
                                             (4097, 90, 40, 3), (5000, 20_000, 136, -1),
-                                            (70_000, 2500, 24, 1), (200, 33, 2050, 0)])
+                                            (70_000, 2500, 24, 1), (200, 33, 2050, 0),
+                                            (9000, 12, 2, -1), (3000, 5, 7, -1), (6000, 30, 9, 2),
+                                            (2500, 400, 515, 0), (64, 3, 33, -1), (65, 1, 33, -1)])
 def test_grad(L, ti, to, n, rows, dim, pad):
     ids = _ids(n, rows, dim, skew=4.0, bad=0.02)
     dout = torch.randn(n, dim, generator=_gen(n)).to(ti)
@@ -158,7 +180,8 @@ def test_grad(L, ti, to, n, rows, dim, pad):
 
 
 @pytest.mark.parametrize("to", TYPES)
-@pytest.mark.parametrize("n,rows,dim", [(0, 5, 8), (50, 9, 16), (9000, 100, 72)])
+@pytest.mark.parametrize("n,rows,dim", [(0, 5, 8), (50, 9, 16), (9000, 100, 72), (700, 11, 3),
+                                        (5000, 40, 13), (300, 20, 517)])
 def test_grad_accumulates(L, to, n, rows, dim):
     ids = _ids(n, rows, 5)
     dout = torch.randn(n, dim, generator=_gen(2)).to(torch.bfloat16)
@@ -205,6 +228,40 @@ def test_grad_one_hot_row_of_many_tokens(L):
     got = L.fs_token_grad(L.fs_token_sort(ids.cuda(), 5), dout.cuda(), 5).cpu()
     for r in range(5):
         assert torch.equal(got[r], dout[ids == r].double().sum(0).float())
+
+
+@pytest.mark.parametrize("length", [63, 64, 65, 128, 129, 200, 513])
+def test_grad_rows_at_the_bounds_of_whole_and_shared_sums(L, length):
+    """Rows of equal length around the bound of rows summed whole, at every
+    offset from a chunk's start; sums of multiples of 2^-10 are exact."""
+    for lead in (0, 1, 7, 8, 31):
+        n = lead + 9 * length + 5
+        ids = torch.cat([torch.arange(lead), lead + torch.arange(n - lead) // length])
+        rows = int(ids[-1]) + 2
+        dout = torch.randint(-1000, 1000, (n, 40), generator=_gen(lead)).float() / 1024
+        got = L.fs_token_grad(L.fs_token_sort(ids.cuda(), rows), dout.cuda(), rows).cpu()
+        ref = torch.zeros(rows, 40, dtype=torch.float64).index_add_(0, ids, dout.double())
+        assert torch.equal(got, ref.float()), lead
+
+
+def test_expanded_tensors_and_short_sorts_are_refused(L):
+    ids = torch.arange(8, device="cuda")
+    one = torch.ones(1, 16, device="cuda")
+    for call in (lambda: L.fs_token_lookup(one.expand(8, 16), ids),
+                 lambda: L.fs_token_lookup(torch.ones(8, 16, device="cuda"), ids,
+                                           out=one.clone().expand(8, 16)),
+                 lambda: L.fs_token_grad(L.fs_token_sort(ids, 8), one.expand(8, 16), 8)):
+        with pytest.raises(L.FsError):
+            call()
+    with pytest.raises(AssertionError):
+        L.fs_token_grad(L.fs_token_sort(ids[:4], 8), torch.ones(8, 16, device="cuda"), 8)
+    with pytest.raises(AssertionError):
+        L.fs_token_sort(ids, 8, out=L.fs_token_sort(ids[:4], 8))
+    with pytest.raises(L.FsError):
+        L.fs_token_lookup(torch.ones(8, 16), ids)
+    # a table smaller than the sort's: rows past it are left out
+    got = L.fs_token_grad(L.fs_token_sort(ids, 8), torch.ones(8, 16, device="cuda"), 5)
+    assert got.shape == (5, 16) and (got == 1).all()
 
 
 def test_grad_takes_the_dedup_of_a_step(L):
