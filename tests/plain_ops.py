@@ -71,9 +71,11 @@ def _sample(q, k, v, see, scale):
     return p, lse
 
 
-def attention(q, k, v, offsets, cand, valid, causal, scale, dout=None):
+def attention(q, k, v, offsets, cand, valid, causal, scale, dout=None, own_out=False):
     """Per-token results in 64 bits and their bounds for a result in q's type:
-    dict of (value, bound) by name. Tokens of no sample hold NaN."""
+    dict of (value, bound) by name. Tokens of no sample hold NaN. own_out: the
+    backward pass was given an out within the forward's bound, not the exact
+    one rounded."""
     n_tok, hq, d = q.shape
     hk, t = k.shape[1], q.dtype
     group = hq // hk
@@ -115,7 +117,8 @@ def attention(q, k, v, offsets, cand, valid, causal, scale, dout=None):
         ov = p @ vd.abs()
         # the forward pass rounds 2^(S - m) with a maximum of 1 over the row, sum at least 1
         low = (see * (tiny(t) / 2)).double() @ vd.abs()
-        put("out", lo, hi, out, (ut + 2 * rel) * ov + low + ut * out.abs() + tiny(t))
+        b_out = (ut + 2 * rel) * ov + low + ut * out.abs() + tiny(t)
+        put("out", lo, hi, out, b_out)
         fin = lse.masked_fill(torch.isinf(lse), 0.0).abs()
         put("lse", lo, hi, lse, rel[..., 0] + 4 * U32 * fin)
         if dout is None:
@@ -125,12 +128,13 @@ def attention(q, k, v, offsets, cand, valid, causal, scale, dout=None):
         dsize = do.abs() @ vd.abs().transpose(1, 2)
         delta = (do * out).sum(2, keepdim=True)
         d_out = (do.abs() * out.abs()).sum(2, keepdim=True)
+        off_out = (do.abs() * b_out).sum(2, keepdim=True) if own_out else ut * d_out
         ds = p * (dp - delta)
         # dP and delta in d fp32 steps, out rounded once (the backward's input);
         # P and dS are rounded to t, where they lie below t's normal range (fp16:
         # 2^-14) to a multiple of tiny(t), off by at most half of it each
         under = see * (tiny(t) / 2)
-        e_ds = (ut + 2 * rel) * ds.abs() + p * ((d + 4) * U32 * (dsize + d_out) + ut * d_out
+        e_ds = (ut + 2 * rel) * ds.abs() + p * ((d + 4) * U32 * (dsize + d_out) + off_out
                                                 + tiny(t) * do.abs().sum(2, keepdim=True)) + under
         e_p = (ut + 2 * rel) * p + under
 
