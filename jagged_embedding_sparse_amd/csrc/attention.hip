@@ -109,8 +109,9 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   const int l = lane(), w = wave_id(), g = l >> 5;
   const int rows = 32 * NW / a.s.pack, packs = a.s.heads / a.s.pack;  // see pack_of
   const int at = blockIdx.x / packs, head = blockIdx.x % packs * a.s.pack + w % a.s.pack;
+  const Tile entry = a.s.tab.tiles[at];  // in the table's memory, beside the count
   if (at >= *a.s.tab.n) return;
-  const Tile t = tile_by_end(a.s.tab.tiles[at], rows);
+  const Tile t = tile_by_end(entry, rows);
   const int kvh = head / a.s.group;
   const char* kp = a.k.p + kvh * a.k.head;
   const char* vp = a.v.p + kvh * a.v.head;
@@ -120,7 +121,7 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   const bool causal = a.s.causal != 0;
 
   u32x4 qf[DP / 16];
-  load_scaled_columns<DP>(qf, a.q.p + head * a.q.head, a.q.tok, a.s, t, i, on);
+  load_scaled_columns<DP>(qf, a.q.p + head * a.q.head, a.q.tok, a.s, t, i);
   f32x16 o[DP / 32];
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) o[d] = zero16();
@@ -137,6 +138,10 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   auto key0 = [&](int step) { return (step < hist_end ? step : own_lo + step - hist_end) * kKeys; };
 
   using Tiles = Direct<DP, NT>;
+  // The bytes that say which keys are live are read two steps ahead and made
+  // bits one step ahead, before the next tiles are asked for: made after the
+  // tiles' wait, as in the backward pass, they cost this kernel 5% (302 against
+  // 318 us on 4 x 8192 tokens, 4 heads of 128).
   uint64_t keys = 0;
   uint32_t ahead = 0;
   auto load = [&](int step) {
@@ -194,7 +199,8 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
     // row passes it by more than kLazy, so the sums are rescaled in few steps
     // instead of nearly all (some of 32 rows has a new maximum in most).
     if (__any(top > m + kLazy)) {
-      const float to = fmaxf(top, m), f = __builtin_amdgcn_exp2f(m - to);
+      // rows that need not move keep theirs: a row's bits depend on no other row
+      const float to = top > m + kLazy ? top : m, f = __builtin_amdgcn_exp2f(m - to);
       m = to;
       sum *= f;
 #pragma unroll

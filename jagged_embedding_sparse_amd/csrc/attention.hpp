@@ -229,19 +229,17 @@ __device__ __forceinline__ uint32_t seeing_rows(int j, int i0, int hist, bool ca
   return causal ? ~low_bits(j - i0) : ~0u;
 }
 
-// 16 bytes of row r of one head, elements 8 p .. 8 p + 7; zeros past the
-// head's width and for rows that do not exist or are not valid, so that what
-// lies there (NaN among it) never meets a product
+// 16 bytes of row r of one head, elements 8 p .. 8 p + 7. A row past the
+// sample loads its last one and a piece past the head's width the first, so
+// that no load waits for a condition.
 __device__ __forceinline__ u32x4 load_piece(const char* head, int64_t tok_bytes, const Shape& a,
-                                            const Tile& t, int r, int p, bool on) {
-  u32x4 v = {0, 0, 0, 0};
-  if (on && 8 * p < a.dim) v = *(const u32x4*)(head + ((int64_t)t.lo + r) * tok_bytes + 16 * p);
-  return v;
+                                            const Tile& t, int r, int p) {
+  return *(const u32x4*)(head + ((int64_t)t.lo + min(r, t.len - 1)) * tok_bytes +
+                         (8 * p < a.dim ? 16 * p : 0));
 }
 
-// Which rows r0 .. r0 + 63 of a sample exist and are valid, one row per lane:
-// read one step before it is needed (live_bits), so that no wait stands
-// between a step's products.
+// Which rows r0 .. r0 + 63 of a sample exist and are valid, one row per lane,
+// and as bits.
 __device__ __forceinline__ uint32_t live_byte(const Shape& a, const Tile& t, int r0) {
   const int r = r0 + lane();
   if (r >= t.len) return 0;
@@ -333,14 +331,17 @@ __device__ __forceinline__ f32x16 load_off(const float* off, int k0) {
   return r;
 }
 
-// B operands of 32 rows of one head: column c = row r0 + c
+// B operands of 32 rows of one head: column c = row r0 + c. Rows that are not
+// live bring whatever memory holds: a column of a product depends on no other
+// column, and those of such rows are cleared before they are stored. Pieces
+// past the width meet zeros of the staged tile.
 template <int DP>
 __device__ __forceinline__ void load_columns(u32x4 (&f)[DP / 16], const char* head,
                                              int64_t tok_bytes, const Shape& a, const Tile& t,
-                                             int r, bool on) {
+                                             int r) {
 #pragma unroll
   for (int kk = 0; kk < DP / 16; ++kk)
-    f[kk] = load_piece(head, tok_bytes, a, t, r, 2 * kk + (lane() >> 5), on);
+    f[kk] = load_piece(head, tok_bytes, a, t, r, 2 * kk + (lane() >> 5));
 }
 
 // The kernels scale scores by a positive number (a maximum may be scaled
@@ -349,11 +350,11 @@ __device__ __forceinline__ void load_columns(u32x4 (&f)[DP / 16], const char* he
 template <int DP>
 __device__ __forceinline__ void load_scaled_columns(u32x4 (&f)[DP / 16], const char* head,
                                                     int64_t tok_bytes, const Shape& a,
-                                                    const Tile& t, int r, bool on) {
-  load_columns<DP>(f, head, tok_bytes, a, t, r, on && a.scale != 0.f);
-  if (a.scale < 0.f) {
+                                                    const Tile& t, int r) {
+  load_columns<DP>(f, head, tok_bytes, a, t, r);
+  if (a.scale <= 0.f) {
 #pragma unroll
-    for (int kk = 0; kk < DP / 16; ++kk) f[kk] ^= 0x80008000u;
+    for (int kk = 0; kk < DP / 16; ++kk) f[kk] = a.scale < 0.f ? f[kk] ^ 0x80008000u : f[kk] & 0u;
   }
 }
 __device__ __forceinline__ float log2_scale(const Shape& a) {

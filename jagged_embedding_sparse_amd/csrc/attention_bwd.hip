@@ -82,8 +82,9 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   const int l = lane(), w = wave_id(), g = l >> 5;
   const int rows = 32 * NW / a.s.pack, packs = a.s.heads / a.s.pack;  // see pack_of
   const int at = blockIdx.x / packs, head = blockIdx.x % packs * a.s.pack + w % a.s.pack;
+  const Tile entry = a.s.tab.tiles[at];  // in the table's memory, beside the count
   if (at >= *a.s.tab.n) return;
-  const Tile t = tile_by_end(a.s.tab.tiles[at], rows);
+  const Tile t = tile_by_end(entry, rows);
   const int kvh = head / a.s.group;
   const char* kp = a.k.p + kvh * a.k.head;
   const char* vp = a.v.p + kvh * a.v.head;
@@ -93,15 +94,16 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   const bool causal = a.s.causal != 0;
 
   u32x4 qf[DP / 16], df[DP / 16];
-  load_scaled_columns<DP>(qf, a.q.p + head * a.q.head, a.q.tok, a.s, t, i, on);
-  load_columns<DP>(df, a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i, on);
+  load_scaled_columns<DP>(qf, a.q.p + head * a.q.head, a.q.tok, a.s, t, i);
+  load_columns<DP>(df, a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i);
   // delta: each half of the wave holds half of a row's columns
   float delta = 0.f;
   {
     const char* outp = a.o.p + head * a.o.head;
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
-      const u32x4 x = load_piece(outp, a.o.tok, a.s, t, i, 2 * kk + g, on);
+      if (8 * (2 * kk + g) >= a.s.dim) continue;
+      const u32x4 x = load_piece(outp, a.o.tok, a.s, t, i, 2 * kk + g);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const f32x2 u = Elem<T>::unpack(x[e]), y = Elem<T>::unpack(df[kk][e]);
@@ -149,10 +151,11 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
     delta = 0.f;
     for (int step = 0; step < steps; ++step) {
       const int j0 = key0(step);
-      const uint64_t live = live_bits(live_byte(a.s, t, j0));
       Tiles::load(sk[0], kp, a.k.tok, a.s, t, j0);
       Tiles::load(sv[0], vp, a.v.tok, a.s, t, j0);
+      const uint32_t byte = live_byte(a.s, t, j0);
       Tiles::wait();
+      const uint64_t live = live_bits(byte);
       Tiles::finish(sk[0], a.s, live);
       Tiles::finish(sv[0], a.s, live);
       if (live != ~0ull) store_off(s_off[0], live);
@@ -174,23 +177,18 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) dq[d] = zero16();
 
-  uint64_t keys = 0;
-  uint32_t ahead = 0;
+  uint32_t live_of = 0;
   auto load = [&](int step) {
     const int j = key0(step);
-    keys = live_bits(ahead);
     Tiles::load(sk[step & 1], kp, a.k.tok, a.s, t, j);
     Tiles::load(sv[step & 1], vp, a.v.tok, a.s, t, j);
-    if (step + 1 < steps) ahead = live_byte(a.s, t, key0(step + 1));
+    live_of = live_byte(a.s, t, j);
   };
-  if (steps > 0) {
-    ahead = live_byte(a.s, t, key0(0));
-    load(0);
-  }
+  if (steps > 0) load(0);
   for (int step = 0; step < steps; ++step) {
     const int j0 = key0(step), b = step & 1;
-    const uint64_t live = keys;
     Tiles::wait();
+    const uint64_t live = live_bits(live_of);
     Tiles::finish(sk[b], a.s, live);
     Tiles::finish(sv[b], a.s, live);
     if (live != ~0ull) store_off(s_off[b], live);
@@ -214,10 +212,13 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
       }
     }
   }
-  // a row that is not live has lse = inf, so dq = 0
-  if (i < t.len)
-    store_rows<T, DP>(a.dq.p + head * a.dq.head + ((int64_t)t.lo + i) * a.dq.tok, dq, a.s.dim,
-                      a.s.scale);
+  if (i >= t.len) return;
+  if (!on) {
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d) dq[d] = zero16();
+  }
+  store_rows<T, DP>(a.dq.p + head * a.dq.head + ((int64_t)t.lo + i) * a.dq.tok, dq, a.s.dim,
+                    a.s.scale);
 }
 
 // dK and dV: 32 keys per wave, the rows of every query head of the key head
@@ -231,8 +232,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
   const int kv_heads = a.s.heads / a.s.group;
   const int kvh = blockIdx.x % kv_heads, part = blockIdx.x / kv_heads % a.splits;
   const int at = blockIdx.x / kv_heads / a.splits;
-  if (at >= *a.keys.n) return;
   const Tile t = a.keys.tiles[at];
+  if (at >= *a.keys.n) return;
   const int l = lane(), w = wave_id(), g = l >> 5;
   const int t1 = min(t.t0 + 32 * NW, t.len);
   const int j0 = t.t0 + 32 * w, j = j0 + (l & 31);
@@ -240,8 +241,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
   const bool causal = a.s.causal != 0;
 
   u32x4 kf[DP / 16], vf[DP / 16];
-  load_scaled_columns<DP>(kf, a.k.p + kvh * a.k.head, a.k.tok, a.s, t, j, on);
-  load_columns<DP>(vf, a.v.p + kvh * a.v.head, a.v.tok, a.s, t, j, on);
+  load_scaled_columns<DP>(kf, a.k.p + kvh * a.k.head, a.k.tok, a.s, t, j);
+  load_columns<DP>(vf, a.v.p + kvh * a.v.head, a.v.tok, a.s, t, j);
   f32x16 dk[DP / 32], dv[DP / 32];
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = zero16();
@@ -258,13 +259,11 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
   const int steps = (int)((int64_t)all * (part + 1) / a.splits);
 
   using Tiles = Direct<DP, NT>;
-  uint64_t rows = 0;
-  uint32_t ahead = 0;
+  uint32_t live_of = 0;
   float st_lse = INFINITY, st_delta = 0.f;  // threads 0 .. 63: one row each
   auto row0 = [&](int step) { return (first + step % per) * kStep; };
   auto load = [&](int step) {
     const int head = kvh * a.s.group + step / per, i0 = row0(step);
-    rows = live_bits(ahead);
     Tiles::load(sq[step & 1], a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
     Tiles::load(sd[step & 1], a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
     if (threadIdx.x < kStep) {
@@ -273,16 +272,13 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
       st_lse = a.lse[at];
       st_delta = a.delta[at];
     }
-    if (step + 1 < steps) ahead = live_byte(a.s, t, row0(step + 1));
+    live_of = live_byte(a.s, t, i0);
   };
-  if (step0 < steps) {
-    ahead = live_byte(a.s, t, row0(step0));
-    load(step0);
-  }
+  if (step0 < steps) load(step0);
   for (int step = step0; step < steps; ++step) {
     const int i0 = row0(step), b = step & 1;
-    const uint64_t live = rows;
     Tiles::wait();
+    const uint64_t live = live_bits(live_of);
     Tiles::finish(sq[b], a.s, live);
     Tiles::finish(sd[b], a.s, live);
     if (threadIdx.x < kStep) {
@@ -375,8 +371,8 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
   const int kv_heads = a.s.heads / a.s.group;
   const int kvh = blockIdx.x % kv_heads, part = blockIdx.x / kv_heads % a.splits;
   const int at = blockIdx.x / kv_heads / a.splits;
-  if (at >= *a.keys.n) return;
   const Tile t = a.keys.tiles[at];
+  if (at >= *a.keys.n) return;
   const int l = lane(), w = wave_id(), g = l >> 5;
   const int half = w >> 2;  // which 32 rows of a step, and dV (0) or dK (1)
   const int t1 = min(t.t0 + 128, t.len);
@@ -385,8 +381,8 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
   const bool causal = a.s.causal != 0;
 
   u32x4 kf[DP / 16], vf[DP / 16];
-  load_scaled_columns<DP>(kf, a.k.p + kvh * a.k.head, a.k.tok, a.s, t, j, on);
-  load_columns<DP>(vf, a.v.p + kvh * a.v.head, a.v.tok, a.s, t, j, on);
+  load_scaled_columns<DP>(kf, a.k.p + kvh * a.k.head, a.k.tok, a.s, t, j);
+  load_columns<DP>(vf, a.v.p + kvh * a.v.head, a.v.tok, a.s, t, j);
   f32x16 sum[DP / 32];
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) sum[d] = zero16();
@@ -401,13 +397,11 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
   const int steps = (int)((int64_t)all * (part + 1) / a.splits);
 
   using Tiles = Direct<DP, NT>;
-  uint64_t rows = 0;
-  uint32_t ahead = 0;
+  uint32_t live_of = 0;
   float st_lse = INFINITY, st_delta = 0.f;  // threads 0 .. 63: one row each
   auto row0 = [&](int step) { return (first + step % per) * kStep; };
   auto load = [&](int step, int to) {
     const int head = kvh * a.s.group + step / per, i0 = row0(step);
-    rows = live_bits(ahead);
     Tiles::load(sq[to], a.q.p + head * a.q.head, a.q.tok, a.s, t, i0);
     Tiles::load(sd[to], a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i0);
     if (threadIdx.x < kStep) {
@@ -416,20 +410,17 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
       st_lse = a.lse[at];
       st_delta = a.delta[at];
     }
-    if (step + 1 < steps) ahead = live_byte(a.s, t, row0(step + 1));
+    live_of = live_byte(a.s, t, i0);
   };
-  if (step0 < steps) {
-    ahead = live_byte(a.s, t, row0(step0));
-    load(step0, 0);
-  }
+  if (step0 < steps) load(step0, 0);
   bool have = false;       // the last step's operands wait to be summed
   u32x4 mine[2];           // this wave's own of them
   int b = 0, before = 2;   // this step's tiles, the last step's
   for (int step = step0; step <= steps; ++step) {  // one more, for the last sums
-    const int e = step & 1;
-    const uint64_t live = rows;
+    const int e = step & 1, i0 = row0(step), r0 = i0 + 32 * half;
     if (step < steps) {
       Tiles::wait();
+      const uint64_t live = live_bits(live_of);
       Tiles::finish(sq[b], a.s, live);
       Tiles::finish(sd[b], a.s, live);
       if (threadIdx.x < kStep) {
@@ -440,7 +431,6 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
     }
     __syncthreads();
     if (step + 1 < steps) load(step + 1, b == 2 ? 0 : b + 1);
-    const int i0 = row0(step), r0 = i0 + 32 * half;
     // steps whose rows see none of these keys (the same for both waves)
     const bool none = step >= steps || j0 >= t1 || (causal && i0 + kStep <= j0) ||
                       (j0 >= t.hist && (i0 + kStep <= j0 || i0 > j0 + 31));
