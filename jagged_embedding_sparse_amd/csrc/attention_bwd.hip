@@ -32,9 +32,9 @@ struct BwdArgs {
 // Causal tiles differ in length by up to the sample's, so with fewer than
 // about two workgroups per CU the longest one decides; then each tile's steps
 // are cut into equal parts, whose sums a second kernel adds in order. Measured
-// at 2 x 8192 tokens, 8/2 heads of 128 (256 tiles): 2028 us whole, SPLIT_US in
-// two parts and their sum; at 54790 tokens, 8/2 heads of 64 (about 980 tiles)
-// parts only add their traffic.
+// at 2 x 8192 tokens, 8/2 heads of 128 (256 tiles): 2028 us whole, 1103 and 16
+// for the sum in two parts; in 64 short samples (5644 tokens, one key head)
+// eight parts take 15 and 6 us, one 20, and a launch less.
 constexpr int64_t kParts = 512;   // workgroups to reach
 constexpr int64_t kSplitMax = 8;  // parts of one tile
 constexpr int64_t kPartSteps = 4;  // steps that a part of a tile of average length has, at least
