@@ -6,7 +6,11 @@
 // Two kernels, because dQ sums over keys and dK, dV over rows: each keeps its
 // sums in registers and recomputes S and dP (7 products instead of the least
 // 5), so no sum crosses workgroups, nothing is added atomically and equal
-// calls give equal bits. The first writes delta for the second.
+// calls give equal bits. The first writes delta for the second. Bound as the
+// forward pass is: at 2 x 8192 tokens, 8/2 heads of 128, causal, 1036 to 1068
+// us for both (the seven products would take 777 at a library product's rate);
+// in 128 samples of 428 tokens on average, 8/2 heads of 64, 110 us for dQ and
+// 128 for dK and dV.
 #include <algorithm>
 #include <cmath>
 
