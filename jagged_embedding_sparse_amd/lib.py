@@ -10,6 +10,8 @@ the library is missing, importing this module raises.
 from __future__ import annotations
 
 import ctypes as C
+import functools
+import inspect
 import os
 import struct
 
@@ -147,6 +149,40 @@ def _stream(stream):
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
+def _used_on(out, stream):
+    """Records on `stream` the use of every tensor in a call's result."""
+    if torch.is_tensor(out):
+        out.record_stream(stream)
+    elif out is not None:
+        for t in out.values() if isinstance(out, dict) else out:
+            _used_on(t, stream)
+
+
+def _allocates(call):
+    """A call that allocates what its caller did not pass. The caching allocator
+    orders a block's next use behind the work of the stream that was current
+    when the block was handed out, and of no other. So with stream= given, that
+    stream is the current one (and its device the current device) inside the
+    call: the workspace that the call drops goes to nobody before the kernels on
+    that stream are done with it, and no block comes in that another stream's
+    pending work still uses. The results, which the caller has on the stream that
+    was current, are recorded there."""
+    at = list(inspect.signature(call).parameters).index("stream")
+
+    @functools.wraps(call)
+    def run(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return call(*args, **kw)
+        caller = torch.cuda.current_stream(stream.device)
+        with torch.cuda.stream(stream):
+            out = call(*args, **kw)
+        _used_on(out, caller)
+        return out
+
+    return run
+
+
 def _check(fn, rc):
     if rc != FS_OK:
         raise FsError(fn, rc)
@@ -231,6 +267,7 @@ def balance_workspace_size(n, W):
     return int(_c_balance_ws(n, W))
 
 
+@_allocates
 def fs_balance_fbs(uih_len, W, perm=None, rank_offsets=None, err=None, ws=None, stream=None):
     n = uih_len.numel()
     perm = perm if perm is not None else torch.empty(n, dtype=torch.int32, device=_dev())
@@ -242,6 +279,7 @@ def fs_balance_fbs(uih_len, W, perm=None, rank_offsets=None, err=None, ws=None, 
     return perm, ro
 
 
+@_allocates
 def fs_balance_vbs(uih_len, W, alpha=(3, 2), perm=None, rank_offsets=None, rank_weight=None,
                    err=None, ws=None, stream=None):
     n = uih_len.numel()
@@ -258,6 +296,7 @@ def fs_balance_vbs(uih_len, W, alpha=(3, 2), perm=None, rank_offsets=None, rank_
     return perm, ro, rw
 
 
+@_allocates
 def fs_balance_vbs_shares(uih_len, W, shares, alpha=(3, 2), perm=None, rank_offsets=None,
                           rank_weight=None, err=None, ws=None, stream=None):
     """VBS cut at per-rank shares (device int64 [W]) of the weight."""
@@ -276,6 +315,7 @@ def fs_balance_vbs_shares(uih_len, W, shares, alpha=(3, 2), perm=None, rank_offs
     return perm, ro, rw
 
 
+@_allocates
 def fs_rank_cost(uih_len, perm, rank_offsets, coef=(1, 0, 0), cost=None, stream=None):
     """Modelled per-rank time: sum of c2 L^2 + c1 L + c0 over each rank's samples."""
     W = rank_offsets.numel() - 1
@@ -302,6 +342,7 @@ def bucketize_workspace_size(n_tok, n, T, W):
     return int(_c_bucketize_ws(n_tok, n, T, W))
 
 
+@_allocates
 def fs_bucketize_permute(ids, sample_offsets, rows, perm, rank_offsets, W, out=None, err=None,
                          ws=None, stream=None):
     """ids: int64 [T, n_tok]. Returns dict of bal_offsets, shard_keys, shard_bm, splits,
@@ -328,6 +369,7 @@ def unique_workspace_size(n_cap, T, W, prev_cap=None):
     return int(_c_unique_ws(n_cap, n_cap if prev_cap is None else prev_cap, T, W))
 
 
+@_allocates
 def fs_unique_collision_split(shard_keys, shard_bm, shard_offsets, n_cap, rows, W,
                               prev_unique=None, prev_counts=None, prev_cap=0, out=None, ws=None,
                               stream=None, prev_unique_offsets=None):
@@ -362,6 +404,7 @@ def collision_workspace_size(n_cap, T, W):
     return int(_c_collide_ws(n_cap, T, W))
 
 
+@_allocates
 def fs_collision_split(uq, n_cap, T, W, prev_unique=None, prev_unique_offsets=None,
                        prev_counts=None, prev_cap=0, prev_cls=None, ws=None, stream=None):
     """The collision split alone on a dedup call's outputs `uq` (its cls and
@@ -388,6 +431,7 @@ def _ptr_array(ts):
     return arr
 
 
+@_allocates
 def fs_jagged_lookup(weights, W, uq, n_tok, which=FS_ALL, cls=None, out=None, stream=None):
     """weights: list of [rows, dim] tensors; uq: the split call's outputs."""
     d = _dev()
@@ -404,6 +448,7 @@ def fs_jagged_lookup(weights, W, uq, n_tok, which=FS_ALL, cls=None, out=None, st
     return out
 
 
+@_allocates
 def fs_ranged_combine(src, bucket, W, dims, dtypes, rows, n_tok, out=None, stream=None):
     """src: device uint8 [n_items, stride] rows in the dispatch's shard-major
     order; bucket: fs_bucketize_permute's outputs; dims / dtypes / rows: per
@@ -431,6 +476,7 @@ def keyed_transpose_workspace_size(F, B):
     return int(_c_kt_ws(F, B))
 
 
+@_allocates
 def fs_keyed_transpose(values, lengths, out=None, out_offsets=None, err=None, ws=None,
                        stream=None):
     """values: device 1-D tensor of 4- or 8-byte elements, the feature-major
@@ -456,6 +502,7 @@ def reduce_workspace_size(n_tok, max_dim, T=1):
     return int(_c_reduce_ws(n_tok, T, max_dim))
 
 
+@_allocates
 def fs_grad_reduce_update(weights, states, W, grads, n_tok, uq, optim, lr, eps=0.0,
                           which=FS_ALL, cls=None, reduced_out=None, ws=None, stream=None,
                           rows=FS_ROWS_ALL):
@@ -519,6 +566,7 @@ def _own_rows_ptr(t):
     return p, stride if t.shape[0] > 1 else 0
 
 
+@_allocates
 def fs_token_lookup(weight, ids, scale=1.0, dtype=None, out=None, err=None, stream=None):
     """out[i] = scale * weight[ids[i]] in `dtype` (the table's by default):
     weight [rows, dim] (fp32, bf16 or fp16, rows contiguous, any row stride),
@@ -542,6 +590,7 @@ def token_sort_workspace_size(n):
     return int(_c_token_sort_ws(n))
 
 
+@_allocates
 def fs_token_sort(ids, rows, padding_id=-1, out=None, err=None, ws=None, stream=None):
     """ids: int64 [n]. Returns the tokens sorted by row as the dedup's outputs
     of one table and W = 1 (unique, unique_offsets, seg_offsets, occ_bm,
@@ -575,6 +624,7 @@ def token_grad_workspace_size(n, dim):
     return int(_c_token_grad_ws(n, dim))
 
 
+@_allocates
 def fs_token_grad(uq, dout, rows, scale=1.0, dtype=torch.float32, grad=None, accumulate=False,
                   W=1, ws=None, stream=None):
     """The table's gradient [rows, dim] in `dtype` from the tokens' gradients
@@ -635,6 +685,7 @@ def attention_workspace_size(n_tok, n):
     return int(_c_attention_ws(n_tok, n))
 
 
+@_allocates
 def fs_jagged_attention(q, k, v, offsets, n_cand=None, valid=None, causal=True, scale=None,
                         out=None, lse=None, err=None, ws=None, stream=None):
     """Softmax attention inside every sample of a jagged batch: q [n_tok,
@@ -662,6 +713,7 @@ def attention_backward_workspace_size(n_tok, n, heads, kv_heads, dim):
     return int(_c_attention_bwd_ws(n_tok, n, heads, kv_heads, dim))
 
 
+@_allocates
 def fs_jagged_attention_backward(q, k, v, out, lse, dout, offsets, n_cand=None, valid=None,
                                  causal=True, scale=None, dq=None, dk=None, dv=None, err=None,
                                  ws=None, stream=None):
