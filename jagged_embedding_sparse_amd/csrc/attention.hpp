@@ -41,6 +41,7 @@ template <typename T>
 struct Elem;
 template <>
 struct Elem<__bf16> {
+  static constexpr bool kNarrow = false;  // of fewer exponents than fp32
   static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a),
                                                    __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -55,6 +56,7 @@ struct Elem<__bf16> {
 };
 template <>
 struct Elem<_Float16> {
+  static constexpr bool kNarrow = true;
   static __device__ __forceinline__ f32x16 mfma(u32x4 a, u32x4 b, f32x16 c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a),
                                                   __builtin_bit_cast(f16x8, b), c, 0, 0, 0);

@@ -28,6 +28,7 @@ struct BwdArgs {
   TileTable keys;    // 128 keys each
   const float* lse;  // [heads][n_tok]
   float* delta;      // [heads][n_tok]
+  float* factor;     // [heads][n_tok], fp16: of every 32 rows of a sample, see kDsTop
   float* part;       // [splits][2][kv_heads][n_tok][DP]: dK (unscaled) and dV
   int32_t splits;
 };
@@ -54,6 +55,52 @@ __host__ inline int64_t split_tokens(int64_t n_tok, int32_t kv_heads) {
   for (int64_t s = 2; s <= kSplitMax; ++s)
     most = std::max(most, s * std::min(n_tok, ((kParts - 1) / (s - 1) / kv_heads + 1) * 128 - 1));
   return most;
+}
+
+// fp16 has 5 bits of exponent, and P and dS leave its range where inputs and
+// outputs do not: P is about 1 / length, dS = P (dP - delta) that times the size
+// of a gradient. So both are rounded times a power of two that the sums lose
+// again (bf16 has fp32's exponents and needs none):
+//  - P of dV times 2^kPUp;
+//  - dS of dQ times a row's own factor, which is a lane's: it takes the largest
+//    of the row's dS so far to 2^(kDsTop - 2) .. 2^kDsTop, and moves (with the
+//    sums) where one passes 2^kDsMost. It starts from delta, so that a row
+//    whose dS cancel to rounding errors of delta has a factor for these too;
+//  - dS of dK and dV's kernel times one factor per tile of keys, from the
+//    smallest of the rows that meet it, which the dQ kernel leaves for every 32
+//    rows: dS is at most 2^kDsMost over that factor, up to the two kernels'
+//    rounding of P, which has three bits here.
+// What is too small for fp16 even so is rounded to a multiple of 2^-24, off by
+// at most 2^-25: 2^-37 of P's 1, of dS 2^-36 of the row's largest (dQ) or 2^-34
+// of the largest of the rows that the tile meets (dK). Measured against dS and
+// P rounded as they are, which at gradients of 1e-4 over 8192 tokens are off by
+// several percent: 240 us instead of 229 on the ordinary batch, 1094 instead of
+// 1051 on the long one, 36 instead of 34 on the short one (a row's largest dS
+// is looked for at every step).
+constexpr int kPUp = 12, kDsTop = 13, kDsMost = 15;
+constexpr int kFactorMost = 60;  // bits of a factor: products with dP stay inside fp32
+
+__device__ __forceinline__ int factor_bits(int bits) {
+  return min(max(bits, -kFactorMost), kFactorMost);
+}
+__device__ __forceinline__ float wave_min(float x) {
+#pragma unroll
+  for (int d = kWave / 2; d > 0; d >>= 1) x = fminf(x, __shfl_xor(x, d, kWave));
+  return x;
+}
+
+// The factor of dS for the rows [r0, r1) of a sample (r0 a multiple of 32) and a
+// key head's query heads
+__device__ __forceinline__ float rows_factor(const BwdArgs& a, const Tile& t, int kvh, int r0,
+                                             int r1) {
+  const int per = (int)cdiv(r1 - r0, 32);
+  float f = INFINITY;
+#pragma unroll 4
+  for (int x = lane(); x < per * a.s.group; x += kWave)
+    f = fminf(f, a.factor[(int64_t)(kvh * a.s.group + x / per) * a.s.n_tok + t.lo + r0 + x % per * 32]);
+  f = wave_min(f);
+  // times 2^kPUp, which comes with P
+  return f == INFINITY ? 1.f : ldexpf(f, kDsTop - kDsMost - kPUp);
 }
 
 // 32 columns x DP rows of sums to one row of memory per lane, scaled
@@ -180,6 +227,14 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   f32x16 dq[DP / 32];
 #pragma unroll
   for (int d = 0; d < DP / 32; ++d) dq[d] = zero16();
+  // fp16: the row's factor 2^up, and whether no dS other than 0 has come yet
+  int up = 0;
+  bool fresh = true;
+  if (Elem<T>::kNarrow && delta != 0.f) {
+    up = factor_bits(kDsMost + kDsTop - 1 - __builtin_amdgcn_frexp_expf(delta));
+    fresh = false;
+  }
+  float factor = ldexpf(1.f, up), scaled_delta = delta * factor;
 
   uint32_t live_of = 0;
   auto load = [&](int step) {
@@ -206,7 +261,26 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
       scores(j0, b, kb, live, s, dp);
 #pragma unroll
       for (int x = 0; x < 16; ++x)
-        s[x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], c, -lse)) * (dp[x] - delta);
+        s[x] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[x], c, -lse)) *
+               (Elem<T>::kNarrow ? __builtin_fmaf(dp[x], factor, -scaled_delta) : dp[x] - delta);
+      if constexpr (Elem<T>::kNarrow) {
+        float top = 0.f;
+#pragma unroll
+        for (int x = 0; x < 16; ++x) top = fmaxf(top, fabsf(s[x]));
+        top = max_halves(top);
+        const bool move = top > (float)(1 << kDsMost) || (fresh && top > 0.f);
+        if (__any(move)) {
+          const int to = move ? factor_bits(up + kDsTop - __builtin_amdgcn_frexp_expf(top)) : up;
+          const float by = ldexpf(1.f, to - up);
+          s *= by;
+#pragma unroll
+          for (int d = 0; d < DP / 32; ++d) dq[d] *= by;
+          up = to;
+          factor = ldexpf(1.f, up);
+          scaled_delta = delta * factor;
+          fresh = fresh && !move;
+        }
+      }
 #pragma unroll
       for (int ch = 0; ch < 2; ++ch) {
         const u32x4 ds = to_operand<T>(s, ch);
@@ -216,13 +290,17 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
       }
     }
   }
+  if constexpr (Elem<T>::kNarrow) {
+    const float least = wave_min(on && !fresh ? factor : INFINITY);
+    if (l == 0 && i0 < t.len) a.factor[(int64_t)head * a.s.n_tok + t.lo + i0] = least;
+  }
   if (i >= t.len) return;
   if (!on) {
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) dq[d] = zero16();
   }
   store_rows<T, DP>(a.dq.p + head * a.dq.head + ((int64_t)t.lo + i) * a.dq.tok, dq, a.s.dim,
-                    a.s.scale);
+                    ldexpf(a.s.scale, -up));
 }
 
 // dK and dV: 32 keys per wave, the rows of every query head of the key head
@@ -279,6 +357,10 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
     live_of = live_byte(a.s, t, i0);
   };
   if (step0 < steps) load(step0);
+  // beside the first tiles' way
+  const float factor =
+      Elem<T>::kNarrow ? rows_factor(a, t, kvh, first * kStep, own ? t1 : t.len) : 1.f;
+  constexpr float p_up = Elem<T>::kNarrow ? kPUp : 0;
   for (int step = step0; step < steps; ++step) {
     const int i0 = row0(step), b = step & 1;
     Tiles::wait();
@@ -287,8 +369,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
     Tiles::finish(sd[b], a.s, live);
     if (threadIdx.x < kStep) {
       const bool in = (live >> threadIdx.x) & 1;
-      s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e;
-      s_delta[b][threadIdx.x] = in ? st_delta : 0.f;
+      s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e - p_up;
+      s_delta[b][threadIdx.x] = in ? st_delta * factor : 0.f;
     }
     __syncthreads();
     if (step + 1 < steps) load(step + 1);
@@ -321,7 +403,7 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
           const int z = 4 * y + x;
           const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], c, -ls[x]));
           s[z] = p;
-          dp[z] = p * (dp[z] - de[x]);
+          dp[z] = p * (Elem<T>::kNarrow ? __builtin_fmaf(dp[z], factor, -de[x]) : dp[z] - de[x]);
         }
       }
 #pragma unroll
@@ -340,8 +422,17 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) dk[d] = dv[d] = zero16();
   }
+  // what takes the powers of two out again: exact in fp32
+  const float dv_by = ldexpf(1.f, Elem<T>::kNarrow ? -kPUp : 0), dk_by = dv_by / factor;
   const int64_t tok = (int64_t)t.lo + j;
   if (a.splits > 1) {
+    if constexpr (Elem<T>::kNarrow) {
+#pragma unroll
+      for (int d = 0; d < DP / 32; ++d) {
+        dk[d] *= dk_by;
+        dv[d] *= dv_by;
+      }
+    }
     float* to = a.part + (((int64_t)part * 2 * kv_heads + kvh) * a.s.n_tok + tok) * DP;
     const int64_t dv_at = (int64_t)kv_heads * a.s.n_tok * DP;
 #pragma unroll
@@ -354,8 +445,9 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
       }
     return;
   }
-  store_rows<T, DP>(a.dk.p + kvh * a.dk.head + tok * a.dk.tok, dk, a.s.dim, a.s.scale);
-  store_rows<T, DP>(a.dv.p + kvh * a.dv.head + tok * a.dv.tok, dv, a.s.dim, 1.f);
+  store_rows<T, DP>(a.dk.p + kvh * a.dk.head + tok * a.dk.tok, dk, a.s.dim,
+                    a.s.scale * dk_by);
+  store_rows<T, DP>(a.dv.p + kvh * a.dv.head + tok * a.dv.tok, dv, a.s.dim, dv_by);
 }
 
 // dK and dV of heads wider than 64: the sums alone take 128 registers per
@@ -417,6 +509,10 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
     live_of = live_byte(a.s, t, i0);
   };
   if (step0 < steps) load(step0, 0);
+  // beside the first tiles' way
+  const float factor =
+      Elem<T>::kNarrow ? rows_factor(a, t, kvh, first * kStep, own ? t1 : t.len) : 1.f;
+  constexpr float p_up = Elem<T>::kNarrow ? kPUp : 0;
   bool have = false;       // the last step's operands wait to be summed
   u32x4 mine[2];           // this wave's own of them
   int b = 0, before = 2;   // this step's tiles, the last step's
@@ -429,8 +525,8 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
       Tiles::finish(sd[b], a.s, live);
       if (threadIdx.x < kStep) {
         const bool in = (live >> threadIdx.x) & 1;
-        s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e;
-        s_delta[b][threadIdx.x] = in ? st_delta : 0.f;
+        s_lse[b][threadIdx.x] = !in || st_lse == -INFINITY ? INFINITY : st_lse * kLog2e - p_up;
+        s_delta[b][threadIdx.x] = in ? st_delta * factor : 0.f;
       }
     }
     __syncthreads();
@@ -477,7 +573,7 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
           const int z = 4 * y + x;
           const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[z], c, -ls[x]));
           s[z] = p;
-          dp[z] = p * (dp[z] - de[x]);
+          dp[z] = p * (Elem<T>::kNarrow ? __builtin_fmaf(dp[z], factor, -de[x]) : dp[z] - de[x]);
         }
       }
 #pragma unroll
@@ -496,8 +592,14 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d) sum[d] = zero16();
   }
+  // what takes the powers of two out again: exact in fp32
+  const float dv_by = ldexpf(1.f, Elem<T>::kNarrow ? -kPUp : 0), by = half ? dv_by / factor : dv_by;
   const int64_t tok = (int64_t)t.lo + j;
   if (a.splits > 1) {
+    if constexpr (Elem<T>::kNarrow) {
+#pragma unroll
+      for (int d = 0; d < DP / 32; ++d) sum[d] *= by;
+    }
     float* to = a.part + (((int64_t)part * 2 + 1 - half) * kv_heads + kvh) * a.s.n_tok * DP + tok * DP;
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
@@ -508,7 +610,8 @@ __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
     return;
   }
   const View& o = half ? a.dk : a.dv;
-  store_rows<T, DP>(o.p + kvh * o.head + tok * o.tok, sum, a.s.dim, half ? a.s.scale : 1.f);
+  store_rows<T, DP>(o.p + kvh * o.head + tok * o.tok, sum, a.s.dim,
+                    half ? a.s.scale * by : by);
 }
 
 // Sums of the parts, part by part: one thread per 4 columns of dK or dV.
@@ -581,6 +684,7 @@ extern "C" size_t fs_jagged_attention_backward_workspace_size(int64_t n_tok, int
   c.take<int32_t>(1);
   c.take<Tile>((size_t)tile_cap(n_tok, n, 128));
   c.take<float>((size_t)heads * (size_t)n_tok);
+  c.take<float>((size_t)heads * (size_t)n_tok);
   c.take<float>((size_t)split_tokens(n_tok, kv_heads) * 2 * kv_heads * padded(dim));
   return c.used + 256;
 }
@@ -625,6 +729,7 @@ extern "C" int fs_jagged_attention_backward(
   tabs[1].tiles = c.take<Tile>((size_t)key_cap);
   a.lse = lse;
   a.delta = c.take<float>((size_t)heads * (size_t)n_tok);
+  a.factor = c.take<float>((size_t)heads * (size_t)n_tok);
   a.part = c.take<float>((size_t)split_tokens(n_tok, kv_heads) * 2 * kv_heads * padded(dim));
   if ((rc = launch_tiles(offsets, n, n_tok, n_cand, causal, tabs, 2, err, stream))) return rc;
   a.s = Shape{tabs[0], valid, n_tok, heads, heads / kv_heads, pack, dim, causal, scale};
