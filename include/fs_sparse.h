@@ -519,10 +519,11 @@ size_t fs_token_grad_workspace_size(int64_t n, int32_t dim);
 /* dk and dv summed over the query heads of the key head. Scores, statistics */
 /* and sums are fp32; P and dS are rounded to the inputs' type before the    */
 /* products that sum them (half a step each, as the outputs), and equal      */
-/* calls give equal bits. In fp16 the backward call rounds P and dS times    */
-/* powers of two, which the sums lose again: none of them overflows, and a   */
-/* step ends only at 2^-36 of P's 1, of dS at 2^-36 of the row's largest in   */
-/* dq and at 2^-34 of the largest of a key head's rows of the sample in dk.   */
+/* calls give equal bits. In fp16 P and dS are rounded times powers of two,   */
+/* which the sums lose again: none of them overflows, and a step ends only at */
+/* 2^-32 of the row's largest P in out, at 2^-36 in dv, of dS at 2^-36 of the */
+/* row's largest in dq and at 2^-34 of the largest of a key head's rows of    */
+/* the sample in dk.                                                         */
 /*  q, out, dout, dq  host: [n_tok][heads][dim] arrays of dtype (FS_BF16 or  */
 /*           FS_F16, else FS_ERR_UNSUPPORTED); k, v, dk, dv: kv_heads heads. */
 /*           Strides in bytes, multiples of 16, data 16-byte aligned; 0:     */

@@ -104,7 +104,14 @@ struct FwdArgs {
 };
 
 constexpr int kKeys = 64;    // keys per step
-constexpr float kLazy = 8.f;  // 2^(S - m) stays at most 2^8, well inside either type
+// A row's running maximum m moves where 2^(S - m) would pass 2^kMost, to where
+// its largest is 2^kTo. fp16's largest value is just below 2^16 and its smallest
+// step 2^-24, so there the largest stays in 2^8 .. 2^15: what lies 2^22 below it
+// and more is rounded to a multiple of 2^-32 of it, not to one of 2^-24.
+template <typename T>
+constexpr float kMost = Elem<T>::kNarrow ? 15.f : 8.f;
+template <typename T>
+constexpr float kTo = Elem<T>::kNarrow ? 8.f : 0.f;
 
 template <typename T, int DP, int NW>
 __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
@@ -201,11 +208,11 @@ __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
       for (int x = 0; x < 16; ++x) top = fmaxf(top, s[kb][x]);
     top = max_halves(top) * c;
     // The running maximum only has to keep 2^(S - m) in range: it moves when a
-    // row passes it by more than kLazy, so the sums are rescaled in few steps
+    // row passes it by more than kMost, so the sums are rescaled in few steps
     // instead of nearly all (some of 32 rows has a new maximum in most).
-    if (__any(top > m + kLazy)) {
+    if (__any(top > m + kMost<T>)) {
       // rows that need not move keep theirs: a row's bits depend on no other row
-      const float to = top > m + kLazy ? top : m, f = __builtin_amdgcn_exp2f(m - to);
+      const float to = top > m + kMost<T> ? top - kTo<T> : m, f = __builtin_amdgcn_exp2f(m - to);
       m = to;
       sum *= f;
 #pragma unroll

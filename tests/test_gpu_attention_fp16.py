@@ -1,4 +1,4 @@
-"""The attention's backward pass in fp16 where P and dS leave fp16's range and the inputs and
+"""The attention in fp16 where P and dS leave fp16's range and the inputs and
 outputs do not: long samples, small gradients, gradients scaled up against
 underflow. Against 64 bits, with bounds that allow a result its own rounding
 and P and dS half a step each, which ends only far below the largest of them."""
@@ -167,3 +167,29 @@ def test_infinities_and_nan_stay_in_their_sample(L):
             o, s = L.fs_jagged_attention(*y[:3], off)
             for a, b in zip(L.fs_jagged_attention_backward(*y[:3], o, s, y[3], off), want):
                 assert torch.equal(a[:70], b[:70]) and torch.equal(a[370:], b[370:])
+
+
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("causal", [True, False])
+def test_many_keys_far_below_the_rows_largest(L, d, causal):
+    """One key takes nearly all of every row, and thousands of keys of 2^-25 of
+    it bring all of the output."""
+    n, g = 4000, torch.Generator().manual_seed(d)
+    q, k = torch.zeros(n, 1, d), torch.zeros(n, 1, d)
+    q[:, 0, 0] = 4.0
+    k[1:, 0, 0] = -4.3 - 0.1 * torch.rand(n - 1, generator=g)  # exp(4 k) = 2^-24.8 .. 2^-25.4
+    v = 1 + torch.rand(n, 1, d, generator=g)
+    v[0] = 0
+    q, k, v = (x.to(HF) for x in (q, k, v))
+    off = torch.tensor([0, n])
+    out, lse = L.fs_jagged_attention(q.cuda(), k.cuda(), v.cuda(), off.cuda(), causal=causal, scale=1.0)
+    see = P.sees(n, 0, causal)
+    a = (q[:, 0].double() @ k[:, 0].double().T).masked_fill(~see, -math.inf)
+    p = torch.softmax(a, 1)
+    ref = p @ v[:, 0].double()
+    # S is exact but for its product with log2 e (18 2^-24); n terms are summed
+    rel = (4 * 18 + 24 + n) * U32
+    e = (UT + 2 * rel) * p + see * 2.0 ** -32 * p.amax(1, keepdim=True)
+    P.check(out[:, 0], (ref, e @ v[:, 0].double().abs() + UT * ref.abs() + TINY))
+    ref = torch.logsumexp(a, 1)
+    P.check(lse[0], (ref, rel + 4 * U32 * ref.abs()))
