@@ -34,6 +34,23 @@ struct Num<_Float16> {
   static __device__ __forceinline__ _Float16 down(float x) { return (_Float16)x; }
 };
 
+// A 64-bit sum to a table's type in one rounding. To 16 bits it goes by way of
+// fp32 rounded to odd: where fp32 is not exact, its last bit is set, 13 bits or
+// more below the 16-bit type's, so that a sum beside a midpoint stays on its side
+// of it. Infinities and NaN stay.
+template <typename T>
+__device__ __forceinline__ T round_sum(double x) {
+  const float f = (float)x;
+  if constexpr (sizeof(T) == 4) {
+    return f;
+  } else {
+    const double back = fabs((double)f), size = fabs(x);
+    uint32_t u = __float_as_uint(f);
+    if (!(u & 1)) u += size > back ? 1 : (size < back ? -1 : 0);
+    return Num<T>::down(__uint_as_float(u));
+  }
+}
+
 template <typename T>
 struct Pair {
   T a, b;
@@ -176,10 +193,10 @@ __device__ __forceinline__ void put_row(const TokGradArgs& a, int64_t row, const
     y = *p;
 #pragma unroll
     for (int e = 0; e < N; ++e)
-      y.v[e] = Num<TO>::down((float)((double)Num<TO>::up(y.v[e]) + (double)a.scale * s[e]));
+      y.v[e] = round_sum<TO>((double)Num<TO>::up(y.v[e]) + (double)a.scale * s[e]);
   } else {
 #pragma unroll
-    for (int e = 0; e < N; ++e) y.v[e] = Num<TO>::down((float)((double)a.scale * s[e]));
+    for (int e = 0; e < N; ++e) y.v[e] = round_sum<TO>((double)a.scale * s[e]);
   }
   if (c.skip == 0) {
     put_through(p, y);
