@@ -197,9 +197,13 @@ def _get(o, key, make):
     return o[key] if key in o and o[key] is not None else make()
 
 
+def _nbytes(t):
+    return t.numel() * t.element_size()
+
+
 def _ws(nbytes, ws):
     if ws is not None:
-        assert ws.numel() * ws.element_size() >= nbytes
+        assert _nbytes(ws) >= nbytes
         return ws
     return torch.empty(max(int(nbytes), 1), dtype=torch.uint8, device=_dev())
 
@@ -275,7 +279,7 @@ def fs_balance_fbs(uih_len, W, perm=None, rank_offsets=None, err=None, ws=None, 
                                                                    device=_dev())
     ws = _ws(balance_workspace_size(n, W), ws)
     _check("fs_balance_fbs", _c_balance_fbs(_ptr(uih_len), n, W, _ptr(perm), _ptr(ro), _ptr(err),
-                                            _ptr(ws), ws.numel(), _stream(stream)))
+                                            _ptr(ws), _nbytes(ws), _stream(stream)))
     return perm, ro
 
 
@@ -292,7 +296,7 @@ def fs_balance_vbs(uih_len, W, alpha=(3, 2), perm=None, rank_offsets=None, rank_
     ws = _ws(nb, ws)
     _check("fs_balance_vbs", _c_balance_vbs(_ptr(uih_len), n, W, int(alpha[0]), int(alpha[1]),
                                             _ptr(perm), _ptr(ro), _ptr(rw), _ptr(err), _ptr(ws),
-                                            ws.numel(), _stream(stream)))
+                                            _nbytes(ws), _stream(stream)))
     return perm, ro, rw
 
 
@@ -310,7 +314,7 @@ def fs_balance_vbs_shares(uih_len, W, shares, alpha=(3, 2), perm=None, rank_offs
     ws = _ws(balance_workspace_size(n, W), ws)
     _check("fs_balance_vbs_shares",
            _c_balance_shares(_ptr(uih_len), n, W, int(alpha[0]), int(alpha[1]), _ptr(shares),
-                             _ptr(perm), _ptr(ro), _ptr(rw), _ptr(err), _ptr(ws), ws.numel(),
+                             _ptr(perm), _ptr(ro), _ptr(rw), _ptr(err), _ptr(ws), _nbytes(ws),
                              _stream(stream)))
     return perm, ro, rw
 
@@ -361,7 +365,7 @@ def fs_bucketize_permute(ids, sample_offsets, rows, perm, rank_offsets, W, out=N
     _check("fs_bucketize_permute",
            _c_bucketize(_ptr(ids), n_tok, _ptr(sample_offsets), n, tabs, T, _ptr(perm),
                         _ptr(rank_offsets), W, _ptr(bal), _ptr(keys), _ptr(bm), _ptr(splits),
-                        _ptr(sho), _ptr(err), _ptr(ws), ws.numel(), _stream(stream)))
+                        _ptr(sho), _ptr(err), _ptr(ws), _nbytes(ws), _stream(stream)))
     return dict(bal_offsets=bal, shard_keys=keys, shard_bm=bm, splits=splits, shard_offsets=sho)
 
 
@@ -395,7 +399,7 @@ def fs_unique_collision_split(shard_keys, shard_bm, shard_offsets, n_cap, rows, 
                      int(prev_cap) if prev_unique
                      is not None else 0, _ptr(uq), _ptr(uo), _ptr(seg), _ptr(occ_bm),
                      _ptr(occ_uid), _ptr(cls), _ptr(pcls) if prev_unique is not None else None,
-                     _ptr(counts), _ptr(ws), ws.numel(), _stream(stream)))
+                     _ptr(counts), _ptr(ws), _nbytes(ws), _stream(stream)))
     return dict(unique=uq, unique_offsets=uo, seg_offsets=seg, occ_bm=occ_bm, occ_uid=occ_uid,
                 cls=cls, prev_cls=pcls, counts=counts)
 
@@ -419,7 +423,7 @@ def fs_collision_split(uq, n_cap, T, W, prev_unique=None, prev_unique_offsets=No
            _c_collide(_ptr(uq["unique"]), _ptr(uq["unique_offsets"]), int(n_cap), T, W,
                       _ptr(prev_unique), _ptr(prev_unique_offsets), _ptr(prev_counts),
                       int(prev_cap) if has else 0, _ptr(uq["cls"]),
-                      _ptr(prev_cls) if has else None, _ptr(uq["counts"]), _ptr(ws), ws.numel(),
+                      _ptr(prev_cls) if has else None, _ptr(uq["counts"]), _ptr(ws), _nbytes(ws),
                       _stream(stream)))
     return prev_cls
 
@@ -494,7 +498,7 @@ def fs_keyed_transpose(values, lengths, out=None, out_offsets=None, err=None, ws
     _check("fs_keyed_transpose",
            _c_kt(_ptr(values) if n else None, n, values.element_size(), _ptr(lengths), F, B,
                  _ptr(out) if n else None, _ptr(out_offsets), _ptr(err), _ptr(ws),
-                 ws.numel() * ws.element_size(), _stream(stream)))
+                 _nbytes(ws), _stream(stream)))
     return out, out_offsets
 
 
@@ -516,7 +520,7 @@ def fs_grad_reduce_update(weights, states, W, grads, n_tok, uq, optim, lr, eps=0
                      _ptr(uq["unique_offsets"]), _ptr(uq["seg_offsets"]), _ptr(uq["occ_bm"]),
                      _ptr(uq["occ_uid"]), _ptr(cls) if which != FS_ALL else None, which, rows,
                      FS_RW_ADAGRAD if optim in ("rw_adagrad", FS_RW_ADAGRAD) else FS_SGD,
-                     float(lr), float(eps), red, _ptr(ws), ws.numel(), _stream(stream)))
+                     float(lr), float(eps), red, _ptr(ws), _nbytes(ws), _stream(stream)))
 
 
 def fs_grad_reduce_update_noalloc(weights, states, W, grads, n_tok, uq, optim, lr, eps=0.0,
@@ -615,7 +619,7 @@ def fs_token_sort(ids, rows, padding_id=-1, out=None, err=None, ws=None, stream=
     _check("fs_token_sort",
            _c_token_sort(_ptr(ids), n, int(rows), int(padding_id), _ptr(uq), _ptr(uo), _ptr(seg),
                          _ptr(bm), _ptr(uid), _ptr(counts), _ptr(err), _ptr(ws),
-                         ws.numel() * ws.element_size(), _stream(stream)))
+                         _nbytes(ws), _stream(stream)))
     return dict(unique=uq, unique_offsets=uo, seg_offsets=seg, occ_bm=bm, occ_uid=uid,
                 counts=counts)
 
@@ -647,7 +651,7 @@ def fs_token_grad(uq, dout, rows, scale=1.0, dtype=torch.float32, grad=None, acc
                          _ptr(uq["seg_offsets"]), _ptr(uq["occ_bm"]), _ptr(uq["occ_uid"]), n, dptr,
                          _dtype(dout.dtype), dstride, float(scale), int(rows), dim, gptr,
                          _dtype(grad.dtype), gstride, int(bool(accumulate)), _ptr(ws),
-                         ws.numel(), _stream(stream)))
+                         _nbytes(ws), _stream(stream)))
     return grad
 
 
@@ -705,7 +709,7 @@ def fs_jagged_attention(q, k, v, offsets, n_cand=None, valid=None, causal=True, 
            _c_attention(hs[0], hs[1], hs[2], _ptr(offsets), n, n_tok, _ptr(n_cand), _ptr(valid),
                         heads, kv[1], dim, _dtype(q.dtype), int(bool(causal)), scale,
                         _heads_arg(out, q.shape, q.dtype), _ptr(lse), _ptr(err), _ptr(ws),
-                        ws.numel(), _stream(stream)))
+                        _nbytes(ws), _stream(stream)))
     return out, lse
 
 
@@ -732,7 +736,7 @@ def fs_jagged_attention_backward(q, k, v, out, lse, dout, offsets, n_cand=None, 
                             _ptr(n_cand), _ptr(valid), heads, kv[1], dim, _dtype(q.dtype),
                             int(bool(causal)), scale, _heads_arg(dq, q.shape, q.dtype),
                             _heads_arg(dk, kv, q.dtype), _heads_arg(dv, kv, q.dtype), _ptr(err),
-                            _ptr(ws), ws.numel(), _stream(stream)))
+                            _ptr(ws), _nbytes(ws), _stream(stream)))
     return dq, dk, dv
 
 
@@ -766,17 +770,17 @@ class Prepared:
 def prepare_balance(balancer, W, alpha, perm, rank_offsets, rank_weight, err, ws):
     """fs_balance_fbs / fs_balance_vbs; call with uih=, n=, stream=."""
     if balancer == "fbs":
-        args = [None, 0, W, _ptr(perm), _ptr(rank_offsets), _ptr(err), _ptr(ws), ws.numel(), None]
+        args = [None, 0, W, _ptr(perm), _ptr(rank_offsets), _ptr(err), _ptr(ws), _nbytes(ws), None]
         return Prepared("fs_balance_fbs", _c_balance_fbs, args, dict(uih=0, n=1, stream=8))
     args = [None, 0, W, int(alpha[0]), int(alpha[1]), _ptr(perm), _ptr(rank_offsets),
-            _ptr(rank_weight), _ptr(err), _ptr(ws), ws.numel(), None]
+            _ptr(rank_weight), _ptr(err), _ptr(ws), _nbytes(ws), None]
     return Prepared("fs_balance_vbs", _c_balance_vbs, args, dict(uih=0, n=1, stream=11))
 
 
 def prepare_balance_shares(W, alpha, shares, perm, rank_offsets, rank_weight, err, ws):
     """fs_balance_vbs_shares; call with uih=, n=, stream=."""
     args = [None, 0, W, int(alpha[0]), int(alpha[1]), _ptr(shares), _ptr(perm),
-            _ptr(rank_offsets), _ptr(rank_weight), _ptr(err), _ptr(ws), ws.numel(), None]
+            _ptr(rank_offsets), _ptr(rank_weight), _ptr(err), _ptr(ws), _nbytes(ws), None]
     return Prepared("fs_balance_vbs_shares", _c_balance_shares, args, dict(uih=0, n=1, stream=12))
 
 
@@ -801,7 +805,7 @@ def prepare_bucketize(rows, perm, rank_offsets, W, out, err, ws):
     tabs = make_row_tables(rows)
     args = [None, 0, None, 0, tabs, len(rows), _ptr(perm), _ptr(rank_offsets), W,
             _ptr(out["bal_offsets"]), _ptr(out["shard_keys"]), _ptr(out["shard_bm"]),
-            _ptr(out["splits"]), _ptr(out["shard_offsets"]), _ptr(err), _ptr(ws), ws.numel(), None]
+            _ptr(out["splits"]), _ptr(out["shard_offsets"]), _ptr(err), _ptr(ws), _nbytes(ws), None]
     return Prepared("fs_bucketize_permute", _c_bucketize, args,
                     dict(ids=0, n_tok=1, so=2, n=3, stream=17))
 
@@ -817,7 +821,7 @@ def prepare_unique(bucket, rows, W, uq, prev_uq, prev_cls, ws):
             _ptr(prev_uq["counts"]) if has else None, 0, _ptr(uq["unique"]),
             _ptr(uq["unique_offsets"]), _ptr(uq["seg_offsets"]), _ptr(uq["occ_bm"]),
             _ptr(uq["occ_uid"]), _ptr(uq["cls"]), _ptr(prev_cls) if has else None,
-            _ptr(uq["counts"]), _ptr(ws), ws.numel(), None]
+            _ptr(uq["counts"]), _ptr(ws), _nbytes(ws), None]
     return Prepared("fs_unique_collision_split", _c_unique, args,
                     dict(n_cap=3, prev_cap=10, stream=21))
 
@@ -830,7 +834,7 @@ def prepare_collision(uq, T, W, prev_uq, prev_cls, ws):
             _ptr(prev_uq["unique"]) if has else None,
             _ptr(prev_uq["unique_offsets"]) if has else None,
             _ptr(prev_uq["counts"]) if has else None, 0, _ptr(uq["cls"]),
-            _ptr(prev_cls) if has else None, _ptr(uq["counts"]), _ptr(ws), ws.numel(), None]
+            _ptr(prev_cls) if has else None, _ptr(uq["counts"]), _ptr(ws), _nbytes(ws), None]
     return Prepared("fs_collision_split", _c_collide, args, dict(n_cap=2, prev_cap=8, stream=14))
 
 
@@ -853,6 +857,6 @@ def prepare_update(weights, states, W, uq, optim, lr, eps, which, cls, ws):
             _ptr(uq["unique_offsets"]), _ptr(uq["seg_offsets"]), _ptr(uq["occ_bm"]),
             _ptr(uq["occ_uid"]), _ptr(cls) if which != FS_ALL else None, which, FS_ROWS_ALL,
             FS_RW_ADAGRAD if optim in ("rw_adagrad", FS_RW_ADAGRAD) else FS_SGD, float(lr),
-            float(eps), None, _ptr(ws), ws.numel(), None]
+            float(eps), None, _ptr(ws), _nbytes(ws), None]
     return Prepared("fs_grad_reduce_update", _c_reduce, args, dict(n_tok=4, rows=12, stream=19),
                     arrays=dict(grads=grads))

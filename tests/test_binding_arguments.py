@@ -1,0 +1,63 @@
+"""What the binding makes of its arguments, without a GPU (the stubs of
+test_binding_streams)."""
+
+import pytest
+import torch
+
+from test_binding_streams import calls  # noqa: F401  (a fixture)
+
+
+def _with_workspace(L):
+    """Every call that takes a workspace: its C function, the bytes it needs and
+    the call with one given. By name."""
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    i64 = lambda *x: torch.tensor(x, dtype=torch.int64)  # noqa: E731
+    lens, perm, ro, so = i32(1, 2), i32(0, 1), i32(0, 2), i64(0, 1, 3)
+    uq = dict(unique=i64(0, 1, 2), unique_offsets=i64(0, 3), seg_offsets=i32(0, 1, 2, 3),
+              occ_bm=i32(0, 1, 2), occ_uid=i32(0, 1, 2), counts=i64(3, 0, 3, 0),
+              cls=torch.tensor([0, 0, 0], dtype=torch.uint8))
+    w = torch.tensor([[1.0] * 16] * 3)
+    q = torch.tensor([[[1.0] * 8] * 2] * 3, dtype=torch.bfloat16)
+    lse = torch.tensor([[0.0] * 3] * 2)
+    bucket = dict(shard_keys=i64(0, 1, 2), shard_bm=i32(0, 1, 2), shard_offsets=i64(0, 3))
+    balance = L.balance_workspace_size(2, 1)
+    return dict(
+        fs_balance_fbs=("_c_balance_fbs", balance, lambda ws: L.fs_balance_fbs(lens, 1, ws=ws)),
+        fs_balance_vbs=("_c_balance_vbs", balance, lambda ws: L.fs_balance_vbs(lens, 1, ws=ws)),
+        fs_balance_vbs_shares=("_c_balance_shares", balance,
+                               lambda ws: L.fs_balance_vbs_shares(lens, 1, i64(1), ws=ws)),
+        fs_bucketize_permute=("_c_bucketize", L.bucketize_workspace_size(3, 2, 1, 1),
+                              lambda ws: L.fs_bucketize_permute(i64(0, 1, 2)[None], so, [3], perm, ro, 1, ws=ws)),
+        fs_unique_collision_split=("_c_unique", L.unique_workspace_size(3, 1, 1),
+                                   lambda ws: L.fs_unique_collision_split(
+                                       bucket["shard_keys"], bucket["shard_bm"], bucket["shard_offsets"], 3,
+                                       [3], 1, ws=ws)),
+        fs_collision_split=("_c_collide", L.collision_workspace_size(3, 1, 1),
+                            lambda ws: L.fs_collision_split(uq, 3, 1, 1, ws=ws)),
+        fs_keyed_transpose=("_c_kt", L.keyed_transpose_workspace_size(1, 2),
+                            lambda ws: L.fs_keyed_transpose(i64(1, 2, 3), i32(1, 2)[None], ws=ws)),
+        fs_grad_reduce_update=("_c_reduce", L.reduce_workspace_size(3, 16),
+                               lambda ws: L.fs_grad_reduce_update([w], [None], 1, [w], 3, uq, "sgd", 0.1, ws=ws)),
+        fs_token_sort=("_c_token_sort", L.token_sort_workspace_size(2),
+                       lambda ws: L.fs_token_sort(i64(0, 1), 3, ws=ws)),
+        fs_token_grad=("_c_token_grad", L.token_grad_workspace_size(3, 16),
+                       lambda ws: L.fs_token_grad(uq, w, 3, ws=ws)),
+        fs_jagged_attention=("_c_attention", L.attention_workspace_size(3, 2),
+                             lambda ws: L.fs_jagged_attention(q, q, q, so, ws=ws)),
+        fs_jagged_attention_backward=("_c_attention_bwd", L.attention_backward_workspace_size(3, 2, 2, 2, 8),
+                                      lambda ws: L.fs_jagged_attention_backward(q, q, q, q, lse, q, so, ws=ws)))
+
+
+@pytest.mark.parametrize("dtype", [torch.uint8, torch.int64, torch.float32])
+def test_a_workspace_counts_in_bytes(calls, monkeypatch, dtype):  # noqa: F811
+    """The C calls get a workspace's bytes whatever its elements are."""
+    L, _ = calls
+    for name, (fn, need, call) in _with_workspace(L).items():
+        got = []
+        monkeypatch.setattr(L, fn, lambda *a: got.append(a[-2]) or L.FS_OK)
+        size = -(-need // dtype.itemsize)
+        call(torch.zeros(size, dtype=dtype))
+        assert got == [size * dtype.itemsize] and got[0] >= need, name
+        with pytest.raises(AssertionError):
+            call(torch.zeros(max(need // dtype.itemsize - 1, 0), dtype=dtype))
+        assert len(got) == 1, name
