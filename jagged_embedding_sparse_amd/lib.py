@@ -551,14 +551,14 @@ def _dtype(dt):
     return _DTYPES[dt]
 
 
-def _here(t):
-    """The device of a call's first tensor, which has to be the current one: the
-    call's stream, its other tensors and what it allocates belong to that."""
-    d = t.device
-    if d.type != "cuda" or d.index != torch.cuda.current_device():
-        raise FsError(f"a tensor on {d} with cuda:{torch.cuda.current_device()} current",
-                      FS_ERR_INVALID_ARG)
-    return d
+def _here(*tensors):
+    """The device of a call's tensors, which has to be the current one: the
+    call's stream and what it allocates belong to that. None may be among them."""
+    now = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != now:
+            raise FsError(f"a tensor on {t.device} with cuda:{now} current", FS_ERR_INVALID_ARG)
+    return tensors[0].device
 
 
 def _own_rows_ptr(t):
@@ -576,7 +576,7 @@ def fs_token_lookup(weight, ids, scale=1.0, dtype=None, out=None, err=None, stre
     weight [rows, dim] (fp32, bf16 or fp16, rows contiguous, any row stride),
     ids int64 [n]. IDs outside the table give zeros and flag FS_EF_ID_RANGE."""
     assert weight.dim() == 2 and ids.dtype == torch.int64
-    n, dim, d = ids.numel(), weight.shape[1], _here(weight)
+    n, dim, d = ids.numel(), weight.shape[1], _here(weight, ids, out, err)
     if out is None:
         out = torch.empty((n, dim), dtype=dtype or weight.dtype, device=d)
     assert out.shape == (n, dim)
@@ -590,6 +590,9 @@ def fs_token_lookup(weight, ids, scale=1.0, dtype=None, out=None, err=None, stre
     return out
 
 
+_SORT = ("unique", "unique_offsets", "seg_offsets", "occ_bm", "occ_uid")
+
+
 def token_sort_workspace_size(n):
     return int(_c_token_sort_ws(n))
 
@@ -601,7 +604,7 @@ def fs_token_sort(ids, rows, padding_id=-1, out=None, err=None, ws=None, stream=
     occ_uid, counts): fs_token_grad, fs_grad_reduce_update and
     fs_jagged_lookup take them."""
     assert ids.dtype == torch.int64
-    n, d = ids.numel(), _here(ids)
+    n, d = ids.numel(), _here(ids, err, ws)
     cap, nb = max(n, 1), token_sort_workspace_size(n)
     if out is None:  # two allocations for the six outputs and the workspace
         nw = 0 if ws is not None else -(-nb // 8)
@@ -613,6 +616,7 @@ def fs_token_sort(ids, rows, padding_id=-1, out=None, err=None, ws=None, stream=
     else:
         uq, uo, seg, bm, uid, counts = (out[k] for k in ("unique", "unique_offsets", "seg_offsets",
                                                          "occ_bm", "occ_uid", "counts"))
+        _here(uq, uo, seg, bm, uid, counts)
         assert uo.numel() >= 2 and counts.numel() >= 4 and seg.numel() > cap and \
             min(uq.numel(), bm.numel(), uid.numel()) >= cap, "outputs smaller than the batch"
     ws = _ws(nb, ws)
@@ -636,7 +640,7 @@ def fs_token_grad(uq, dout, rows, scale=1.0, dtype=torch.float32, grad=None, acc
     tokens and rows, or a dedup's of one table and W shards). With accumulate
     it is added to `grad`."""
     assert dout.dim() == 2
-    (n, dim), d = dout.shape, _here(dout)
+    (n, dim), d = dout.shape, _here(dout, grad, ws, *(uq[k] for k in _SORT))
     if grad is None:
         assert not accumulate, "accumulate adds to a given grad"
         grad = torch.empty((rows, dim), dtype=dtype, device=d)
@@ -673,14 +677,14 @@ def _heads_arg(t, shape, dtype):
     return _PACK_HEADS(t.data_ptr(), tok * e if shape[0] > 1 else 0, head * e if shape[1] > 1 else 0)
 
 
-def _attention_args(q, k, v, offsets, n_cand, valid, scale):
+def _attention_args(q, k, v, offsets, n_cand, valid, scale, *others):
     n_tok, heads, dim = q.shape
     kv = (n_tok, k.shape[1], dim)
     n = offsets.numel() - 1
     assert offsets.dtype == torch.int64
     assert n_cand is None or (n_cand.dtype == torch.int32 and n_cand.numel() == n)
     assert valid is None or (valid.dtype in (torch.uint8, torch.bool) and valid.numel() == n_tok)
-    return (_here(q), n_tok, heads, dim, kv, n, dim ** -0.5 if scale is None else float(scale),
+    return (_here(q, k, v, offsets, n_cand, valid, *others), n_tok, heads, dim, kv, n, dim ** -0.5 if scale is None else float(scale),
             (_heads_arg(q, q.shape, q.dtype), _heads_arg(k, kv, q.dtype),
              _heads_arg(v, kv, q.dtype)))
 
@@ -698,7 +702,8 @@ def fs_jagged_attention(q, k, v, offsets, n_cand=None, valid=None, causal=True, 
     valid uint8 or bool [n_tok]. scale: 1 / sqrt(dim) by default. Returns out
     like q (dense) and lse fp32 [heads, n_tok]; rows of tokens behind the last
     sample are not written."""
-    d, n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale)
+    d, n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale,
+                                                             out, lse, err, ws)
     if out is None:
         out = torch.empty((n_tok, heads, dim), dtype=q.dtype, device=d)
     if lse is None:
@@ -724,7 +729,8 @@ def fs_jagged_attention_backward(q, k, v, out, lse, dout, offsets, n_cand=None, 
     """Gradients (dq, dk, dv) of fs_jagged_attention from its outputs out and
     lse and the gradient dout of out; the other arguments are the forward
     call's. Outputs may be views (e.g. of one projection's gradient)."""
-    d, n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale)
+    d, n_tok, heads, dim, kv, n, scale, hs = _attention_args(q, k, v, offsets, n_cand, valid, scale,
+                                                             out, lse, dout, dq, dk, dv, err, ws)
     assert lse.dtype == torch.float32 and lse.shape == (heads, n_tok)
     dq = dq if dq is not None else torch.empty((n_tok, heads, dim), dtype=q.dtype, device=d)
     dk = dk if dk is not None else torch.empty(kv, dtype=q.dtype, device=d)

@@ -61,3 +61,60 @@ def test_a_workspace_counts_in_bytes(calls, monkeypatch, dtype):  # noqa: F811
         with pytest.raises(AssertionError):
             call(torch.zeros(max(need // dtype.itemsize - 1, 0), dtype=dtype))
         assert len(got) == 1, name
+
+
+class _On:
+    """A tensor of which only the device is asked."""
+
+    def __init__(self, *device):
+        self.device = torch.device(*device)
+
+    def get_device(self):
+        return -1 if self.device.type == "cpu" else self.device.index
+
+
+def test_tensors_belong_to_the_current_device(monkeypatch):
+    from jagged_embedding_sparse_amd import lib as L
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    here, other, cpu = _On("cuda", 1), _On("cuda", 0), _On("cpu")
+    assert L._here(here, None, here) == torch.device("cuda", 1)
+    for bad in ((other,), (cpu,), (here, other), (here, None, cpu), (here, here, here, other)):
+        with pytest.raises(L.FsError) as e:
+            L._here(*bad)
+        assert e.value.code == L.FS_ERR_INVALID_ARG
+
+
+def test_every_tensor_of_a_call_is_checked(calls, monkeypatch):  # noqa: F811
+    """Inputs, outputs, flags and workspaces of the token embedding's and the
+    attention's calls, all of them given."""
+    L, _ = calls
+    seen = []
+    monkeypatch.setattr(L, "_here", lambda *ts: seen.extend(ts) or torch.device("cpu"))
+    i32 = lambda *x: torch.tensor(x, dtype=torch.int32)  # noqa: E731
+    i64 = lambda *x: torch.tensor(x, dtype=torch.int64)  # noqa: E731
+    w = lambda: torch.ones(3, 16)  # noqa: E731
+    h = lambda: torch.ones(3, 2, 8, dtype=torch.bfloat16)  # noqa: E731
+    ws = lambda: torch.ones(1 << 16, dtype=torch.uint8)  # noqa: E731
+    uq = lambda: dict(unique=i64(0, 1, 2), unique_offsets=i64(0, 3), seg_offsets=i32(0, 1, 2, 3),  # noqa: E731
+                      occ_bm=i32(0, 1, 2), occ_uid=i32(0, 1, 2), counts=i64(3, 0, 3, 0))
+    side = dict(offsets=i64(0, 1, 3), n_cand=i32(0, 1), valid=torch.ones(3, dtype=torch.uint8))
+    sort, grad = uq(), uq()
+    del grad["counts"]  # fs_token_grad does not read them
+    given = [
+        (L.fs_token_lookup, dict(weight=w(), ids=i64(0, 1, 2), out=w(), err=i32(0))),
+        (L.fs_token_sort, dict(ids=i64(0, 1, 2), rows=3, out=sort, err=i32(0), ws=ws())),
+        (L.fs_token_grad, dict(uq=grad, dout=w(), rows=3, grad=w(), ws=ws())),
+        (L.fs_jagged_attention, dict(q=h(), k=h(), v=h(), out=h(), lse=torch.ones(2, 3), err=i32(0),
+                                     ws=ws(), **side)),
+        (L.fs_jagged_attention_backward, dict(q=h(), k=h(), v=h(), out=h(), lse=torch.ones(2, 3),
+                                              dout=h(), dq=h(), dk=h(), dv=h(), err=i32(0), ws=ws(),
+                                              **side))]
+    for fn, kw in given:
+        seen.clear()
+        fn(**kw)
+        tensors = []
+        for x in kw.values():
+            tensors += list(x.values()) if isinstance(x, dict) else [x]
+        for x in tensors:
+            if torch.is_tensor(x):
+                assert any(x is y for y in seen), (fn.__name__, [k for k, v in kw.items() if v is x])
