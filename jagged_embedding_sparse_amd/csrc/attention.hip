@@ -116,7 +116,8 @@ constexpr float kTo = Elem<T>::kNarrow ? 8.f : 0.f;
 template <typename T, int DP, int NW>
 __global__ void __launch_bounds__(NW * kWave, 2) k_attn_fwd(FwdArgs a) {
   constexpr int NT = NW * kWave;
-  __shared__ uint16_t sk[2][kKeys * DP], sv[2][kKeys * DP];
+  __shared__ __attribute__((aligned(kTileAlign))) uint16_t sk[2][kKeys * DP], sv[2][kKeys * DP];
+  static_assert(__alignof__(sk) >= kTileAlign && __alignof__(sv) >= kTileAlign, "16-byte pieces");
   __shared__ __attribute__((aligned(16))) float s_off[2][kKeys];
   const int l = lane(), w = wave_id(), g = l >> 5;
   const int rows = 32 * NW / a.s.pack, packs = a.s.heads / a.s.pack;  // see pack_of

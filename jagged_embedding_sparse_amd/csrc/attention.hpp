@@ -33,6 +33,10 @@ typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
 
+// LDS tiles are filled and read in pieces of 16 bytes, their addresses formed
+// by exclusive-or below that
+constexpr int kTileAlign = 16;
+
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 

@@ -128,7 +128,8 @@ __device__ __forceinline__ void store_rows(char* row, const f32x16 (&x)[DP / 32]
 template <typename T, int DP, int NW>
 __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdArgs a) {
   constexpr int NT = NW * kWave;
-  __shared__ uint16_t sk[2][kStep * DP], sv[2][kStep * DP];
+  __shared__ __attribute__((aligned(kTileAlign))) uint16_t sk[2][kStep * DP], sv[2][kStep * DP];
+  static_assert(__alignof__(sk) >= kTileAlign && __alignof__(sv) >= kTileAlign, "16-byte pieces");
   __shared__ __attribute__((aligned(16))) float s_off[2][kStep];
   const int l = lane(), w = wave_id(), g = l >> 5;
   const int rows = 32 * NW / a.s.pack, packs = a.s.heads / a.s.pack;  // see pack_of
@@ -309,7 +310,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
 template <typename T, int DP, int NW>
 __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdArgs a) {
   constexpr int NT = NW * kWave;
-  __shared__ uint16_t sq[2][kStep * DP], sd[2][kStep * DP];
+  __shared__ __attribute__((aligned(kTileAlign))) uint16_t sq[2][kStep * DP], sd[2][kStep * DP];
+  static_assert(__alignof__(sq) >= kTileAlign && __alignof__(sd) >= kTileAlign, "16-byte pieces");
   __shared__ __attribute__((aligned(16))) float s_lse[2][kStep], s_delta[2][kStep];
   const int kv_heads = a.s.heads / a.s.group;
   const int kvh = blockIdx.x % kv_heads, part = blockIdx.x / kv_heads % a.splits;
@@ -461,7 +463,8 @@ __global__ void __launch_bounds__(NW * kWave, DP == 64 ? 2 : 3) k_attn_dkv(BwdAr
 template <typename T, int DP>
 __global__ void __launch_bounds__(512, 2) k_attn_dkv2(BwdArgs a) {
   constexpr int NT = 512;
-  __shared__ uint16_t sq[3][kStep * DP], sd[3][kStep * DP];
+  __shared__ __attribute__((aligned(kTileAlign))) uint16_t sq[3][kStep * DP], sd[3][kStep * DP];
+  static_assert(__alignof__(sq) >= kTileAlign && __alignof__(sd) >= kTileAlign, "16-byte pieces");
   __shared__ u32x4 ex[2][8][2][kWave];
   __shared__ __attribute__((aligned(16))) float s_lse[3][kStep], s_delta[3][kStep];
   const int kv_heads = a.s.heads / a.s.group;
