@@ -279,13 +279,17 @@ struct Direct {
     return ((int)threadIdx.x % kPieces) ^ swz<DP>(threadIdx.x / kPieces);
   }
   // 16 bytes per lane from base + at to LDS address `to` + 16 lane; base and
-  // `to` are uniform. The instruction takes `to` from M0 (which nothing else in
-  // these kernels uses), one idle cycle after it is written.
+  // `to` are uniform. The instruction takes `to` from M0, one idle cycle after it
+  // is written. The compiler does not let an asm declare that it changes M0, so
+  // what was there is put back.
   static __device__ __forceinline__ void load16(const char* base, uint32_t at, uint32_t to) {
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :
-                 : "s"(to), "v"(at), "s"(base)
-                 : "memory");
+    uint32_t m0;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(m0)
+        : "s"(to), "v"(at), "s"(base)
+        : "memory");
   }
   static __device__ __forceinline__ void load(uint16_t* tile, const char* head, int64_t tok_bytes,
                                               const Shape& a, const Tile& t, int r0) {
