@@ -547,7 +547,9 @@ size_t fs_token_grad_workspace_size(int64_t n, int32_t dim);
 /* sample, also those that do not see it (0 times NaN in a sum of products), */
 /* and none of another sample. scale is finite, of any sign.                 */
 /* Outputs must not alias inputs or each other. n <= FS_MAX_SAMPLES,         */
-/* n_tok < 2^31 - 1.                                                         */
+/* n_tok < 2^31 - 1; (n_tok + 128 n) heads is at most about 2^31, in the      */
+/* backward call also 2^30 key heads of more than 64 (else                   */
+/* FS_ERR_UNSUPPORTED).                                                      */
 typedef struct fs_heads {
   void* data;
   int64_t token_stride; /* bytes between tokens; 0: heads * dim elements */

@@ -341,7 +341,7 @@ extern "C" int fs_jagged_attention(const fs_heads* q, const fs_heads* k, const f
   if (n == 0 || n_tok == 0) return FS_OK;
   const int32_t pack = pack_of(heads / kv_heads), rows = 128 / pack;
   const int64_t cap = tile_cap(n_tok, n, rows), grid = cap * (heads / pack);
-  if (grid >= (int64_t)INT32_MAX) return FS_ERR_UNSUPPORTED;
+  if (!grid_fits(grid, 256)) return FS_ERR_UNSUPPORTED;
   Carve c(ws);
   TileTable tab;
   tab.rows = rows;

@@ -719,8 +719,8 @@ extern "C" int fs_jagged_attention_backward(
   const int32_t pack = pack_of(heads / kv_heads), rows = 128 / pack;
   const int64_t row_cap = tile_cap(n_tok, n, rows), key_cap = tile_cap(n_tok, n, 128);
   a.splits = splits_of(n_tok, n, kv_heads, heads / kv_heads);
-  if (row_cap * (heads / pack) >= (int64_t)INT32_MAX ||
-      key_cap * kv_heads * a.splits >= (int64_t)INT32_MAX)
+  if (!grid_fits(row_cap * (heads / pack), 256) ||
+      !grid_fits(key_cap * kv_heads * a.splits, padded(dim) == 128 ? 512 : 256))
     return FS_ERR_UNSUPPORTED;
   Carve c(ws);
   TileTable tabs[2];

@@ -179,6 +179,11 @@ __host__ __device__ __forceinline__ size_t align_up(size_t x, size_t a) {
   return (x + a - 1) / a * a;
 }
 
+// A grid's threads in one dimension are fewer than 2^32.
+__host__ inline bool grid_fits(int64_t blocks, int64_t threads) {
+  return blocks < ((int64_t)1 << 32) / threads;
+}
+
 // bump allocator over a caller workspace
 struct Carve {
   char* base;

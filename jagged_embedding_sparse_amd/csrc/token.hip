@@ -99,6 +99,7 @@ struct TokLookupArgs {
 };
 
 constexpr int kLookupPer = 4;  // pieces per thread
+constexpr int64_t kLookupBlocks = (int64_t)1 << 23;
 
 // A workgroup takes rows_per_block tokens; its threads run over the pieces
 // (N elements) of their rows, all of a thread's pieces in flight. Bound by HBM:
@@ -584,7 +585,9 @@ extern "C" int fs_token_lookup(const fs_table* table, const int64_t* ids, int64_
   const int32_t elems = piece_elems(table->dim, ei == 4 && eo == 4 ? 4 : 8);
   a.dim = table->dim;
   a.pieces = (int32_t)cdiv(table->dim, elems);
-  a.rows_per_block = std::max(1, kThreads * kLookupPer / a.pieces);
+  // more rows than fill a workgroup where the grid would pass 2^32 threads
+  a.rows_per_block = (int32_t)std::max<int64_t>({1, kThreads * kLookupPer / a.pieces,
+                                                 cdiv(n, kLookupBlocks)});
   a.by_pieces = make_divu32((uint32_t)a.pieces);
   const unsigned grid = (unsigned)cdiv(n, a.rows_per_block);
   if (table->dtype == FS_F32) launch_lookup<float>(a, elems, out_dtype, grid, stream);
@@ -655,8 +658,7 @@ extern "C" int fs_token_grad(const int64_t* unique, const int64_t* unique_offset
   a.clear_rows = (int32_t)std::min<int64_t>(kClearMax, std::max<int64_t>(4, 32768 / row_bytes));
   const int64_t clear_blocks = a.accumulate ? 0 : cdiv(rows, a.clear_rows);
   const int64_t blocks = a.sum_blocks + clear_blocks;
-  if (blocks >= (int64_t)INT32_MAX)
-    return FS_ERR_UNSUPPORTED;
+  if (!grid_fits(blocks, kThreads)) return FS_ERR_UNSUPPORTED;
   if (dout_dtype == FS_F32) return launch_grad<float>(a, elems, grad_dtype, blocks, stream);
   if (dout_dtype == FS_BF16) return launch_grad<__bf16>(a, elems, grad_dtype, blocks, stream);
   return launch_grad<_Float16>(a, elems, grad_dtype, blocks, stream);

@@ -118,3 +118,25 @@ def test_every_tensor_of_a_call_is_checked(calls, monkeypatch):  # noqa: F811
         for x in tensors:
             if torch.is_tensor(x):
                 assert any(x is y for y in seen), (fn.__name__, [k for k, v in kw.items() if v is x])
+
+
+FAKE = 1 << 20  # an aligned address that no call below gets to read
+
+
+def test_grids_of_too_many_threads_are_refused():
+    """A grid has fewer than 2^32 threads in one dimension: attention calls of
+    more tokens times heads are refused before any launch."""
+    import ctypes as C
+    from jagged_embedding_sparse_amd import lib as L
+    h, n = C.byref(L.FsHeads(FAKE, 0, 0)), 4
+    for n_tok, heads, kv, dim, back in ((1 << 28, 8, 8, 8, 0), (1 << 28, 8, 2, 64, 0),
+                                        ((1 << 31) - 2, 1, 1, 8, 0), (1 << 26, 32, 8, 128, 0),
+                                        (1 << 28, 8, 8, 8, 1), (1 << 27, 8, 8, 128, 1)):
+        big = 1 << 62
+        if back:
+            rc = L._c_attention_bwd(h, h, h, h, FAKE, h, FAKE, n, n_tok, None, None, heads, kv, dim,
+                                    L.FS_BF16, 1, 0.1, h, h, h, None, FAKE, big, None)
+        else:
+            rc = L._c_attention(h, h, h, FAKE, n, n_tok, None, None, heads, kv, dim, L.FS_BF16, 1, 0.1,
+                                h, FAKE, None, FAKE, big, None)
+        assert rc == L.FS_ERR_UNSUPPORTED, (n_tok, heads, kv, dim, back)
