@@ -545,7 +545,7 @@ size_t fs_token_grad_workspace_size(int64_t n, int32_t dim);
 /*  ws, ws_bytes  at least the workspace query's bytes, else FS_ERR_WORKSPACE. */
 /* A NaN or an infinity in a valid token's rows may reach every row of its    */
 /* sample, also those that do not see it (0 times NaN in a sum of products), */
-/* and none of another sample. scale is finite, of any sign.                 */
+/* and none of another sample. scale is of any sign, below 2.3e38 in size.   */
 /* Outputs must not alias inputs or each other. n <= FS_MAX_SAMPLES,         */
 /* n_tok < 2^31 - 1; (n_tok + 128 n) heads is at most about 2^31, in the      */
 /* backward call also 2^30 key heads of more than 64 (else                   */

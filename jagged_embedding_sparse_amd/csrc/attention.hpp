@@ -16,6 +16,8 @@
 // (16 lanes read 4 rows x 16 columns, lane c receives column c's 4 rows).
 #pragma once
 
+#include <cmath>
+
 #include "common.hpp"
 
 namespace fs {
@@ -374,6 +376,10 @@ __device__ __forceinline__ float log2_scale(const Shape& a) {
 
 // ---------------------------------------------------------------- host side
 __host__ inline bool type_ok(int32_t dtype) { return dtype == FS_BF16 || dtype == FS_F16; }
+
+// Exponents are scaled by scale log2(e), which has to be finite too: 0 times an
+// infinity is no score.
+__host__ inline bool scale_ok(float scale) { return std::isfinite(scale * kLog2e); }
 
 // the width of the kernel's rows for heads of dim elements
 __host__ inline int32_t padded(int32_t dim) { return dim <= 32 ? 32 : (dim <= 64 ? 64 : 128); }

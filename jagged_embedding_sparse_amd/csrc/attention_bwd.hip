@@ -699,7 +699,7 @@ extern "C" int fs_jagged_attention_backward(
     int32_t dtype, int32_t causal, float scale, const fs_heads* dq, const fs_heads* dk,
     const fs_heads* dv, int32_t* err, void* ws, size_t ws_bytes, hipStream_t stream) {
   if (n < 0 || n > FS_MAX_SAMPLES || n_tok < 0 || n_tok >= (int64_t)INT32_MAX || heads < 1 ||
-      kv_heads < 1 || heads % kv_heads || !offsets || !std::isfinite(scale))
+      kv_heads < 1 || heads % kv_heads || !offsets || !scale_ok(scale))
     return FS_ERR_INVALID_ARG;
   if (!type_ok(dtype) || dim < 8 || dim > 128 || dim % 8 || heads > FS_MAX_HEADS)
     return FS_ERR_UNSUPPORTED;

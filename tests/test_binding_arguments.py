@@ -140,3 +140,18 @@ def test_grids_of_too_many_threads_are_refused():
             rc = L._c_attention(h, h, h, FAKE, n, n_tok, None, None, heads, kv, dim, L.FS_BF16, 1, 0.1,
                                 h, FAKE, None, FAKE, big, None)
         assert rc == L.FS_ERR_UNSUPPORTED, (n_tok, heads, kv, dim, back)
+
+
+def test_scales_whose_exponents_are_not_finite_are_refused():
+    """3e38 is finite, 3e38 log2(e) is not, and 0 times it would be no score."""
+    import ctypes as C
+    from jagged_embedding_sparse_amd import lib as L
+    h, n, n_tok, big = C.byref(L.FsHeads(FAKE, 0, 0)), 4, 50, 1 << 40
+    for scale, want in ((3e38, L.FS_ERR_INVALID_ARG), (-2.4e38, L.FS_ERR_INVALID_ARG)):
+        assert L._c_attention(h, h, h, FAKE, n, n_tok, None, None, 2, 2, 64, L.FS_BF16, 1, scale, h, FAKE,
+                              None, FAKE, big, None) == want
+        assert L._c_attention_bwd(h, h, h, h, FAKE, h, FAKE, n, n_tok, None, None, 2, 2, 64, L.FS_BF16, 1,
+                                  scale, h, h, h, None, FAKE, big, None) == want
+    # nothing launched, nothing refused
+    assert L._c_attention(h, h, h, FAKE, n, 0, None, None, 2, 2, 64, L.FS_BF16, 1, 2.3e38, h, FAKE, None,
+                          FAKE, big, None) == L.FS_OK
