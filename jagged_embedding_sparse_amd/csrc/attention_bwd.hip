@@ -148,21 +148,22 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   u32x4 qf[DP / 16], df[DP / 16];
   load_scaled_columns<DP>(qf, a.q.p + head * a.q.head, a.q.tok, a.s, t, i);
   load_columns<DP>(df, a.d_o.p + head * a.d_o.head, a.d_o.tok, a.s, t, i);
-  // delta: each half of the wave holds half of a row's columns
+  // delta, the diagonal of out dO^T: by the product that makes dP, in its order,
+  // so that a row that sees itself alone, whose out is its v, has delta = dP to
+  // the bit and dS = 0, whatever its P of about 1 is
   float delta = 0.f;
   {
     const char* outp = a.o.p + head * a.o.head;
+    f32x16 x = zero16();
 #pragma unroll
     for (int kk = 0; kk < DP / 16; ++kk) {
-      if (8 * (2 * kk + g) >= a.s.dim) continue;
-      const u32x4 x = load_piece(outp, a.o.tok, a.s, t, i, 2 * kk + g);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const f32x2 u = Elem<T>::unpack(x[e]), y = Elem<T>::unpack(df[kk][e]);
-        delta = __builtin_fmaf(u[0], y[0], delta);
-        delta = __builtin_fmaf(u[1], y[1], delta);
-      }
+      u32x4 o = load_piece(outp, a.o.tok, a.s, t, i, 2 * kk + g);
+      if (8 * (2 * kk + g) >= a.s.dim) o = u32x4{0, 0, 0, 0};
+      x = Elem<T>::mfma(o, df[kk], x);
     }
+#pragma unroll
+    for (int y = 0; y < 16; ++y)  // row l & 31 of the diagonal is in one of the halves
+      if ((l & 31) == 8 * (y >> 2) + 4 * g + (y & 3)) delta = x[y];
     delta = add_halves(delta);
   }
   // a row that sees nothing has lse = -inf: 2^(S - inf) = 0
@@ -198,9 +199,11 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
   using Tiles = Direct<DP, NT>;
   // delta comes with the rounding of out to 16 bits. Where a row sees few keys,
   // out is as large as v and that is as much as all of dS's own rounding: rows
-  // of at most two steps sum delta = sum_j P_ij dP_ij first, in fp32.
+  // of at most two steps sum delta = sum_j P_ij dP_ij first, in fp32, unless they
+  // see one key.
   if (steps <= 2) {
-    delta = 0.f;
+    float sum = 0.f;
+    int seen = 0;
     for (int step = 0; step < steps; ++step) {
       const int j0 = key0(step);
       Tiles::load(sk[0], kp, a.k.tok, a.s, t, j0);
@@ -218,11 +221,13 @@ __global__ void __launch_bounds__(NW * kWave, DP == 128 ? 2 : 3) k_attn_dq(BwdAr
         scores(j0, 0, kb, live, s, dp);
 #pragma unroll
         for (int x = 0; x < 16; ++x)
-          delta = __builtin_fmaf(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x], c, -lse)), dp[x], delta);
+          sum = __builtin_fmaf(__builtin_amdgcn_exp2f(__builtin_fmaf(s[x], c, -lse)), dp[x], sum);
+        seen += __popc(seen_keys(i, j0 + 32 * kb, t.hist, causal) & (uint32_t)(live >> (32 * kb)));
       }
       __syncthreads();
     }
-    delta = add_halves(delta);
+    sum = add_halves(sum);
+    if (seen != 1) delta = sum;
   }
   if (g == 0 && i < t.len) a.delta[lse_at] = delta;
   f32x16 dq[DP / 32];
