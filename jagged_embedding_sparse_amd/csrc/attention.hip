@@ -8,10 +8,11 @@
 // sum l of each row (base 2):
 //   m' = max(m, max S),  l = l 2^(m - m') + sum 2^(S - m'),  O = O 2^(m - m') + 2^(S - m') v.
 // Bound by how far one wave's exponentials overlap another's products: at 4 x
-// 8192 tokens, 4 heads of 128, causal, 291 us (944 TFLOP/s; a library product
-// of 8192^3 reaches 1239), matrix units busy 35% and vector units 45% of the
-// time at two waves per SIMD. In 128 samples of 428 tokens on average, 8/2
-// heads of 64, 75 us, where loads and joins of short samples weigh as much.
+// 8192 tokens, 4 heads of 128, causal, the kernel takes 289 us (952 TFLOP/s; a
+// library product of 8192^3 reaches 1239), matrix units busy 43% and vector
+// units 43% of the time at two waves per SIMD. In 128 samples of 428 tokens on
+// average, 8/2 heads of 64, 67 us (22% and 56%), where loads and joins of short
+// samples weigh as much.
 #include <cmath>
 
 #include "attention.hpp"

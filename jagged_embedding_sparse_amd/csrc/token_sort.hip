@@ -4,7 +4,7 @@
 // Dropped tokens (padding, IDs outside the table) take the row number behind
 // the last one, which sorts last and is left out of the result. At these sizes
 // launches cost more than the data: the dedup's path for the same items takes
-// eleven dependent launches (about 60 us from 4097 to 262144 tokens). Here
+// eleven dependent launches (about 60 us up to 262144 tokens). Here
 //  - up to kSmall tokens one workgroup sorts in LDS and writes the CSR;
 //  - up to kMidTiles tiles a pass is two launches (digit counts per tile; a
 //    scatter in which every workgroup sums the counts before it itself instead
@@ -196,9 +196,15 @@ k_token_sort_small(const int64_t* __restrict__ ids, int32_t n, int64_t rows, int
 constexpr int kMidBits = 9;
 constexpr int kMidBins = 1 << kMidBits;
 constexpr int64_t kMidTiles = 64;
-// Up to here the CSR counts the rows before a tile itself (16 tiles: 6.2 us; a
-// launch that counts them first and the CSR 4.7 + 5.1 us).
+// Up to here the CSR counts the rows before a tile itself, beyond it a launch
+// counts them first. Whole sorts with the recount / with the launch, of 32000
+// rows: 8 tiles of 1024 22.7 / 23.2 us, 16 tiles 24.9 / 24.8, 24 tiles 26.4 /
+// 25.9, 32 tiles 28.9 / 26.6, 64 tiles 38.3 / 31.4; 17 tiles of 4096 38.9 / 36.3,
+// 64 tiles 59.5 / 41.0.
 constexpr int64_t kRecountTiles = 16;
+// Beyond this the dedup's passes sort. They take 58 to 62 us at 262144 tokens
+// (32000 to 1000000 rows) where the tiles here take 41 to 58, and 80 to 85 at
+// 1000000 tokens.
 constexpr int64_t kMidMax = kMidTiles * 1024 * kRounds;  // 262144 tokens
 
 template <bool kFirst>
