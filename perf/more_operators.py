@@ -36,37 +36,37 @@ def _bytes(name):
 def listed():
     return [
         # one token at serving time: latency only
-        dict(name="norm, one token", op="norm", n=1, dim=2048, x="bf16", out="bf16", param="bf16"),
+        dict(name="norm: one token", op="norm", n=1, dim=2048, x="bf16", out="bf16", param="bf16"),
         # a training batch's fp32 residual stream, normed into bf16 activations
-        dict(name="norm, a batch", op="norm", n=32_768, dim=1024, x="f32", out="bf16", param="f32"),
+        dict(name="norm: a batch", op="norm", n=32_768, dim=1024, x="f32", out="bf16", param="f32"),
         # a few samples' tokens, narrow rows
-        dict(name="norm back, few tokens", op="norm back", n=300, dim=64, x="f32", out="f32",
+        dict(name="norm back: few tokens", op="norm back", n=300, dim=64, x="f32", out="f32",
              param="f32"),
         # a large batch, odd sizes, everything in 16 bits
-        dict(name="norm back, large", op="norm back", n=65_537, dim=1000, x="bf16", out="bf16",
+        dict(name="norm back: large", op="norm back", n=65_537, dim=1000, x="bf16", out="bf16",
              param="bf16"),
         # the samples' last tokens scored against a vocabulary: one pass over its rows
-        dict(name="loss, few tokens", op="loss", n=17, rows=100_000, dim=256, type="bf16", zipf=1.05,
+        dict(name="loss: few tokens", op="loss", n=17, rows=100_000, dim=256, type="bf16", zipf=1.05,
              masked=0.0, scale=1.0),
         # a training batch, a tenth of its tokens without a label
-        dict(name="loss, a batch", op="loss", n=16_384, rows=100_000, dim=1024, type="bf16",
+        dict(name="loss: a batch", op="loss", n=16_384, rows=100_000, dim=1024, type="bf16",
              zipf=1.05, masked=0.1, scale=1.0),
         # a small batch, fp16
-        dict(name="loss back, few tokens", op="loss back", n=64, rows=32_000, dim=64, type="f16",
+        dict(name="loss back: few tokens", op="loss back", n=64, rows=32_000, dim=64, type="f16",
              zipf=1.05, masked=0.2, scale=1.0),
         # the largest: a training batch against a large vocabulary
-        dict(name="loss back, large", op="loss back", n=16_384, rows=131_072, dim=1024, type="bf16",
+        dict(name="loss back: large", op="loss back", n=16_384, rows=131_072, dim=1024, type="bf16",
              zipf=1.05, masked=0.0, scale=1.0),
         # a short batch with a few entries for each token, temperature 2
-        dict(name="distill, short", op="distill", n=128, rows=50_000, dim=256, type="f16", zipf=1.1,
+        dict(name="distill: short", op="distill", n=128, rows=50_000, dim=256, type="f16", zipf=1.1,
              masked=0.0, top=16, teacher="f16", scale=0.5),
         # an ordinary batch
-        dict(name="distill, a batch", op="distill", n=8192, rows=32_000, dim=1024, type="bf16",
+        dict(name="distill: a batch", op="distill", n=8192, rows=32_000, dim=1024, type="bf16",
              zipf=1.05, masked=0.05, top=64, teacher="bf16", scale=1.0),
         # odd sizes, some entries missing
-        dict(name="distill back, short", op="distill back", n=499, rows=10_007, dim=200, type="f16",
+        dict(name="distill back: short", op="distill back", n=499, rows=10_007, dim=200, type="f16",
              zipf=1.1, masked=0.1, top=8, teacher="f32", scale=0.5),
-        dict(name="distill back, a batch", op="distill back", n=8192, rows=65_536, dim=768,
+        dict(name="distill back: a batch", op="distill back", n=8192, rows=65_536, dim=768,
              type="bf16", zipf=1.05, masked=0.05, top=32, teacher="f32", scale=1.0),
     ]
 
