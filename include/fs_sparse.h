@@ -71,11 +71,12 @@ extern "C" {
 #define FS_MAX_UIH 65535
 #define FS_MAX_TOKEN_DIM 65536 /* columns of a token embedding */
 #define FS_MAX_HEADS 1024      /* query heads of a jagged attention */
+#define FS_MAX_NORM_DIM 16384  /* columns of a layer norm */
 
 /* enums */
 #define FS_F32 0
 #define FS_BF16 1
-#define FS_F16 2 /* token embedding and jagged attention only */
+#define FS_F16 2 /* token embedding, attention, norm and losses only */
 #define FS_SGD 0
 #define FS_RW_ADAGRAD 1
 #define FS_ALL (-1)
@@ -575,6 +576,39 @@ int fs_jagged_attention_backward(const fs_heads* q, const fs_heads* k, const fs_
 
 size_t fs_jagged_attention_backward_workspace_size(int64_t n_tok, int32_t n, int32_t heads,
                                                    int32_t kv_heads, int32_t dim);
+
+/* ------------------------------------------------------------------------ */
+/* Layer norm -- over the rows of [n][dim], dim 1 .. FS_MAX_NORM_DIM (else    */
+/* FS_ERR_UNSUPPORTED):                                                      */
+/*   mean = sum x / dim,  rstd = (sum (x - mean)^2 / dim + eps)^-1/2,        */
+/*   h = (x - mean) rstd,  out = h weight + bias.                            */
+/* The backward call takes mean and rstd as the forward call left them:      */
+/*   g = dout weight,  dx = rstd (g - sum g / dim - h sum (g h) / dim),      */
+/*   dweight = sum over the rows of dout h,  dbias = of dout.                */
+/* Everything is computed in fp32 and rounded once, to nearest even, to the  */
+/* output's type; equal calls give equal bits.                               */
+/*  x, out, dout, dx  device [n][dim], each FS_F32, FS_BF16 or FS_F16 (dx in  */
+/*           x's type), rows the given bytes apart (0: dense), aligned to an */
+/*           element.                                                        */
+/*  weight, bias  device [dim] of param_dtype, dense; NULL: ones, zeros.     */
+/*  mean, rstd  device fp32 [n]; the forward call takes NULL for either.     */
+/*  dweight, dbias  device [dim] of param_dtype; NULL: not computed. With    */
+/*           n = 0 they are zeros.                                           */
+/*  eps      finite and not negative.                                        */
+/*  ws, ws_bytes  at least the workspace query's bytes, else FS_ERR_WORKSPACE. */
+/* Outputs must not alias inputs or each other. n < 2^31 - 1.                */
+int fs_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, int64_t n, int32_t dim,
+                  const void* weight, const void* bias, int32_t param_dtype, float eps, void* out,
+                  int32_t out_dtype, int64_t out_stride, float* mean, float* rstd,
+                  hipStream_t stream);
+
+int fs_layer_norm_backward(const void* x, int32_t x_dtype, int64_t x_stride, int64_t n, int32_t dim,
+                           const float* mean, const float* rstd, const void* dout,
+                           int32_t dout_dtype, int64_t dout_stride, const void* weight,
+                           int32_t param_dtype, void* dx, int64_t dx_stride, void* dweight,
+                           void* dbias, void* ws, size_t ws_bytes, hipStream_t stream);
+
+size_t fs_layer_norm_backward_workspace_size(int64_t n, int32_t dim);
 
 /* ------------------------------------------------------------------------ */
 const char* fs_strerror(int code);

@@ -1,0 +1,481 @@
+// Layer norm over the rows of [n, dim], forward and backward.
+//
+//   mean = sum x / dim,  rstd = (sum (x - mean)^2 / dim + eps)^-1/2,
+//   h = (x - mean) rstd,  out = h weight + bias
+//   g = dout weight,  dx = rstd (g - sum g / dim - h sum (g h) / dim),
+//   dweight = sum over the rows of dout h,  dbias = of dout
+//
+// A row stays in the registers of the lanes that share it, so memory is read
+// once and the variance is that of the centred values. Both directions are
+// bound by memory.
+#include <algorithm>
+#include <cmath>
+
+#include "common.hpp"
+
+namespace fs {
+namespace {
+
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+template <typename T, int N>
+struct Pack {  // anywhere an element may be: wide accesses need no alignment here
+  T v[N];
+};
+
+struct NormRows {
+  char* p;
+  int64_t stride;
+  int32_t type;
+};
+
+// A lane's share of a row: C pieces of E elements, L lanes apart. The last piece
+// of a row may overlap the one before it and pieces past the row are its last
+// one again, so that no access waits for a condition; `first` is the piece's
+// first element that is this lane's own (E: none). Only sums ask for it: what
+// two lanes compute of one element is the same, and so is what they store.
+template <int E, int L, int C>
+struct Share {
+  int32_t at[C], first[C], dim;
+  __device__ __forceinline__ Share(int32_t l, int32_t dim_) : dim(dim_) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int32_t col = (c * L + l) * E;
+      at[c] = max(min(col, dim - E), 0);
+      first[c] = col < dim ? col - at[c] : E;
+    }
+  }
+  // this lane's element, counted once (rows of fewer than E elements have one piece)
+  __device__ __forceinline__ bool mine(int c, int e) const { return e >= first[c] && at[c] + e < dim; }
+
+  template <typename T>
+  __device__ __forceinline__ void load_as(float (&v)[C][E], const char* row) const {
+    if (dim >= E) {  // uniform
+      Pack<T, E> x[C];
+#pragma unroll
+      for (int c = 0; c < C; ++c) x[c] = *(const Pack<T, E>*)(row + at[c] * (int)sizeof(T));
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[c][e] = (float)x[c].v[e];
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[c][e] = mine(c, e) ? (float)((const T*)row)[at[c] + e] : 0.f;
+    }
+  }
+  __device__ __forceinline__ void load(float (&v)[C][E], const char* row, int32_t type) const {
+    if (type == FS_F32) load_as<float>(v, row);
+    else if (type == FS_BF16) load_as<__bf16>(v, row);
+    else load_as<_Float16>(v, row);
+  }
+
+  template <typename T>
+  __device__ __forceinline__ void store_as(const float (&v)[C][E], char* row) const {
+    if (dim >= E) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        Pack<T, E> y;
+#pragma unroll
+        for (int e = 0; e < E; ++e) y.v[e] = (T)v[c][e];
+        if (first[c] < E) *(Pack<T, E>*)(row + at[c] * (int)sizeof(T)) = y;
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (mine(c, e)) ((T*)row)[at[c] + e] = (T)v[c][e];
+    }
+  }
+  __device__ __forceinline__ void store(const float (&v)[C][E], char* row, int32_t type) const {
+    if (type == FS_F32) store_as<float>(v, row);
+    else if (type == FS_BF16) store_as<__bf16>(v, row);
+    else store_as<_Float16>(v, row);
+  }
+};
+
+// Two sums over the L lanes of a row; with more than a wave the whole
+// workgroup shares the row. `tmp` holds 2 x 16 pairs, taken in turn: a pair is
+// written again only behind the other's barrier.
+template <int L>
+__device__ __forceinline__ void row_sums(float& a, float& b, float (*tmp)[2], int turn) {
+  constexpr int W = L < kWave ? L : kWave;
+#pragma unroll
+  for (int d = W / 2; d > 0; d >>= 1) {
+    a += __shfl_xor(a, d, kWave);
+    b += __shfl_xor(b, d, kWave);
+  }
+  if constexpr (L > kWave) {
+    float(*t)[2] = tmp + 16 * turn;
+    const int w = threadIdx.x / kWave;
+    if (lane() == 0) {
+      t[w][0] = a;
+      t[w][1] = b;
+    }
+    __syncthreads();
+    a = b = 0.f;
+#pragma unroll
+    for (int i = 0; i < L / kWave; ++i) {
+      a += t[i][0];
+      b += t[i][1];
+    }
+  }
+}
+
+struct NormArgs {
+  NormRows x, out;  // backward: out is dout
+  char* dx;
+  int64_t dx_stride, n;
+  const char *weight, *bias;
+  float *mean, *rstd;
+  float* part;               // backward: [workgroups][2][dim], or null: one workgroup writes
+  char *dweight, *dbias;
+  int32_t dim, param;        // type of weight, bias and their gradients
+  float inv_dim, eps;
+};
+
+template <int E, int L, int C>
+__global__ void __launch_bounds__(L > 256 ? L : 256) k_norm(NormArgs a) {
+  __shared__ float tmp[32][2];
+  const Share<E, L, C> s(threadIdx.x % L, a.dim);
+  float w[C][E], b[C][E];
+  if (a.weight) {
+    s.load(w, a.weight, a.param);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[c][e] = 1.f;
+  }
+  if (a.bias) {
+    s.load(b, a.bias, a.param);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) b[c][e] = 0.f;
+  }
+  const int per = blockDim.x / L;
+  for (int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / L; r < a.n; r += (int64_t)gridDim.x * per) {
+    float v[C][E];
+    s.load(v, a.x.p + r * a.x.stride, a.x.type);
+    float sum = 0.f, none = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) sum += s.mine(c, e) ? v[c][e] : 0.f;
+    row_sums<L>(sum, none, tmp, 0);
+    const float mean = sum * a.inv_dim;
+    float sq = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        v[c][e] -= mean;
+        sq += s.mine(c, e) ? v[c][e] * v[c][e] : 0.f;
+      }
+    row_sums<L>(sq, none, tmp, 1);
+    const float rstd = 1.f / sqrtf(sq * a.inv_dim + a.eps);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[c][e] = v[c][e] * rstd * w[c][e] + b[c][e];
+    s.store(v, a.out.p + r * a.out.stride, a.out.type);
+    if (threadIdx.x % L == 0) {
+      if (a.mean) a.mean[r] = mean;
+      if (a.rstd) a.rstd[r] = rstd;
+    }
+  }
+}
+
+__device__ __forceinline__ void put_param(char* p, int32_t type, int64_t i, float v) {
+  if (type == FS_F32) ((float*)p)[i] = v;
+  else if (type == FS_BF16) ((__bf16*)p)[i] = (__bf16)v;
+  else ((_Float16*)p)[i] = (_Float16)v;
+}
+
+// The sums of a workgroup's groups of L lanes, in order, in the first group's
+// registers. `join` holds C E floats for every thread.
+template <int E, int L, int C>
+__device__ __forceinline__ void join_groups(float (&v)[C][E], float* join) {
+  const int T = blockDim.x, l = threadIdx.x % L, per = T / L;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < E; ++e) join[(c * E + e) * T + threadIdx.x] = v[c][e];
+  __syncthreads();
+  // the groups take a lane's C E sums in turn
+  for (int k = threadIdx.x / L; k < C * E; k += per) {
+    float sum = 0.f;
+    for (int g = 0; g < per; ++g) sum += join[k * T + g * L + l];
+    join[k * T + l] = sum;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[c][e] = join[(c * E + e) * T + l];
+  __syncthreads();
+}
+
+// Each group of L lanes adds its rows' parts of dweight and dbias in registers;
+// a workgroup's groups are joined in LDS, in order, and the workgroups' sums by
+// k_norm_params, in order: equal calls give equal bits.
+template <int E, int L, int C>
+__global__ void __launch_bounds__(1024) k_norm_back(NormArgs a) {
+  extern __shared__ float join[];  // [C E][threads], where a workgroup has more groups than one
+  __shared__ float tmp[32][2];
+  const int l = threadIdx.x % L, per = blockDim.x / L;
+  const Share<E, L, C> s(l, a.dim);
+  float w[C][E], dw[C][E], db[C][E];
+  if (a.weight) {
+    s.load(w, a.weight, a.param);
+  } else {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[c][e] = 1.f;
+  }
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < E; ++e) dw[c][e] = db[c][e] = 0.f;
+  int turn = 0;
+  for (int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / L; r < a.n; r += (int64_t)gridDim.x * per) {
+    float h[C][E], g[C][E];
+    s.load(h, a.x.p + r * a.x.stride, a.x.type);
+    s.load(g, a.out.p + r * a.out.stride, a.out.type);
+    const float mean = a.mean[r], rstd = a.rstd[r];
+    float sg = 0.f, sgh = 0.f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        h[c][e] = (h[c][e] - mean) * rstd;
+        dw[c][e] += g[c][e] * h[c][e];
+        db[c][e] += g[c][e];
+        g[c][e] *= w[c][e];
+        sg += s.mine(c, e) ? g[c][e] : 0.f;
+        sgh += s.mine(c, e) ? g[c][e] * h[c][e] : 0.f;
+      }
+    row_sums<L>(sg, sgh, tmp, turn);
+    turn ^= 1;
+    sg *= a.inv_dim;
+    sgh *= a.inv_dim;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+      for (int e = 0; e < E; ++e) g[c][e] = rstd * (g[c][e] - sg - h[c][e] * sgh);
+    s.store(g, a.dx + r * a.dx_stride, a.x.type);
+  }
+  if (!a.dweight && !a.dbias) return;
+  if (per > 1) {
+    join_groups<E, L, C>(dw, join);
+    join_groups<E, L, C>(db, join);
+    if (threadIdx.x >= L) return;
+  }
+  float* part = a.part ? a.part + (int64_t)blockIdx.x * 2 * a.dim : nullptr;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (s.mine(c, e)) {
+        const int32_t col = s.at[c] + e;
+        if (part) {
+          part[col] = dw[c][e];
+          part[a.dim + col] = db[c][e];
+        } else {
+          if (a.dweight) put_param(a.dweight, a.param, col, dw[c][e]);
+          if (a.dbias) put_param(a.dbias, a.param, col, db[c][e]);
+        }
+      }
+}
+
+constexpr int kParamCols = 64;
+
+// dweight and dbias: the workgroups' sums, added in order by 16 threads a column.
+__global__ void __launch_bounds__(1024)
+k_norm_params(const float* __restrict__ part, int32_t parts, int32_t dim, char* dweight, char* dbias,
+              int32_t type) {
+  __shared__ float sh[16][kParamCols];
+  const int x = threadIdx.x % kParamCols, y = threadIdx.x / kParamCols;
+  const int32_t col = blockIdx.x * kParamCols + x, width = 2 * dim;
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (col < width) {
+    int32_t i = y;
+    for (; i + 48 < parts; i += 64)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) s[u] += part[(int64_t)(i + 16 * u) * width + col];
+    for (; i < parts; i += 16) s[0] += part[(int64_t)i * width + col];
+  }
+  sh[y][x] = (s[0] + s[1]) + (s[2] + s[3]);
+  __syncthreads();
+  if (y || col >= width) return;
+  float sum = 0.f;
+  for (int i = 0; i < 16; ++i) sum += sh[i][x];
+  if (col < dim) {
+    if (dweight) put_param(dweight, type, col, sum);
+  } else if (dbias) {
+    put_param(dbias, type, col - dim, sum);
+  }
+}
+
+// ---------------------------------------------------------------- host
+int32_t elem_bytes(int32_t type) { return type == FS_F32 ? 4 : 2; }
+bool type_known(int32_t type) { return type == FS_F32 || type == FS_BF16 || type == FS_F16; }
+
+// strides filled in, null pointers and layouts refused
+int rows_of(const void* p, int32_t type, int64_t stride, int32_t dim, NormRows* r) {
+  const int32_t e = elem_bytes(type);
+  r->p = (char*)p;
+  r->type = type;
+  r->stride = stride ? stride : (int64_t)dim * e;
+  if (!p || r->stride < (int64_t)dim * e || r->stride % e || (uintptr_t)p % e) return FS_ERR_INVALID_ARG;
+  return FS_OK;
+}
+
+constexpr int32_t kMaxParts = 1024;     // workgroups that sum dweight and dbias
+
+// Lanes and pieces of a row by its width in pieces, calls launch.template go<E, L, C>().
+template <int E, typename F>
+void by_width(int32_t dim, const F& launch) {
+  const int32_t q = (int32_t)cdiv(dim, E);
+  if (q <= 8) launch.template go<E, 8, 1>();
+  else if (q <= 16) launch.template go<E, 16, 1>();
+  else if (q <= 32) launch.template go<E, 32, 1>();
+  else if (q <= 64) launch.template go<E, 64, 1>();
+  else if (q <= 128) launch.template go<E, 64, 2>();
+  else if (q <= 256) launch.template go<E, 256, 1>();
+  else if (q <= 512) launch.template go<E, 256, 2>();
+  else if (q <= 1024) launch.template go<E, 1024, 1>();
+  else if (q <= 2048) launch.template go<E, 1024, 2>();
+  else launch.template go<4, 1024, 4>();  // fp32 alone: 16 bits have half as many pieces
+}
+
+template <typename F>
+void by_type(const NormArgs& a, const F& launch) {
+  if (a.x.type == FS_F32) by_width<4>(a.dim, launch);
+  else by_width<8>(a.dim, launch);
+}
+
+struct Forward {
+  const NormArgs& a;
+  hipStream_t stream;
+  template <int E, int L, int C>
+  void go() const {
+    constexpr int T = L > 256 ? L : 256;
+    const int64_t blocks = std::min<int64_t>(cdiv(a.n, T / L), 4096);
+    hipLaunchKernelGGL((k_norm<E, L, C>), dim3((unsigned)blocks), dim3(T), 0, stream, a);
+  }
+};
+
+struct Backward {
+  NormArgs& a;
+  float* part;
+  int32_t* parts;
+  hipStream_t stream;
+  template <int E, int L, int C>
+  void go() const {
+    int T = L > 256 ? L : 256;
+    int64_t blocks = std::min<int64_t>(cdiv(a.n, T / L), kMaxParts);
+    constexpr int Wide = C * E > 8 ? 512 : 1024;
+    if (L < 256 && cdiv(a.n, Wide / L) <= 8) {  // few rows: one workgroup, one launch
+      T = Wide;
+      blocks = 1;
+    }
+    blocks = std::max<int64_t>(blocks, 1);
+    a.part = blocks > 1 ? part : nullptr;
+    *parts = (int32_t)blocks;
+    const size_t lds = T > L ? sizeof(float) * C * E * T : 0;
+    hipLaunchKernelGGL((k_norm_back<E, L, C>), dim3((unsigned)blocks), dim3(T), lds, stream, a);
+  }
+};
+
+}  // namespace
+}  // namespace fs
+
+using namespace fs;
+
+extern "C" int fs_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, int64_t n, int32_t dim,
+                             const void* weight, const void* bias, int32_t param_dtype, float eps,
+                             void* out, int32_t out_dtype, int64_t out_stride, float* mean,
+                             float* rstd, hipStream_t stream) {
+  if (n < 0 || n >= (int64_t)INT32_MAX || dim < 1 || !type_known(x_dtype) || !type_known(out_dtype) ||
+      !type_known(param_dtype) || !std::isfinite(eps) || eps < 0.f)
+    return FS_ERR_INVALID_ARG;
+  if (dim > FS_MAX_NORM_DIM) return FS_ERR_UNSUPPORTED;
+  if (n == 0) return FS_OK;
+  NormArgs a = {};
+  int rc;
+  if ((rc = rows_of(x, x_dtype, x_stride, dim, &a.x)) || (rc = rows_of(out, out_dtype, out_stride, dim, &a.out)))
+    return rc;
+  const int32_t e = elem_bytes(param_dtype);
+  if ((uintptr_t)weight % e || (uintptr_t)bias % e) return FS_ERR_INVALID_ARG;
+  a.n = n;
+  a.weight = (const char*)weight;
+  a.bias = (const char*)bias;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.dim = dim;
+  a.param = param_dtype;
+  a.inv_dim = 1.f / (float)dim;
+  a.eps = eps;
+  by_type(a, Forward{a, stream});
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
+extern "C" size_t fs_layer_norm_backward_workspace_size(int64_t n, int32_t dim) {
+  if (n < 0 || dim < 1) return 0;
+  return sizeof(float) * 2 * (size_t)dim * (size_t)std::min<int64_t>(n, kMaxParts) + 256;
+}
+
+extern "C" int fs_layer_norm_backward(const void* x, int32_t x_dtype, int64_t x_stride, int64_t n,
+                                      int32_t dim, const float* mean, const float* rstd,
+                                      const void* dout, int32_t dout_dtype, int64_t dout_stride,
+                                      const void* weight, int32_t param_dtype, void* dx,
+                                      int64_t dx_stride, void* dweight, void* dbias, void* ws,
+                                      size_t ws_bytes, hipStream_t stream) {
+  if (n < 0 || n >= (int64_t)INT32_MAX || dim < 1 || !type_known(x_dtype) || !type_known(dout_dtype) ||
+      !type_known(param_dtype))
+    return FS_ERR_INVALID_ARG;
+  if (dim > FS_MAX_NORM_DIM) return FS_ERR_UNSUPPORTED;
+  NormArgs a = {};
+  NormRows to = {};
+  int rc;
+  if (n > 0 && ((rc = rows_of(x, x_dtype, x_stride, dim, &a.x)) ||
+                (rc = rows_of(dout, dout_dtype, dout_stride, dim, &a.out)) ||
+                (rc = rows_of(dx, x_dtype, dx_stride, dim, &to))))
+    return rc;
+  const int32_t e = elem_bytes(param_dtype);
+  if ((n > 0 && (!mean || !rstd)) || (uintptr_t)weight % e || (uintptr_t)dweight % e || (uintptr_t)dbias % e)
+    return FS_ERR_INVALID_ARG;
+  if (!ws || ws_bytes < fs_layer_norm_backward_workspace_size(n, dim)) return FS_ERR_WORKSPACE;
+  if (n == 0 && !dweight && !dbias) return FS_OK;
+  a.dx = to.p;
+  a.dx_stride = to.stride;
+  a.n = n;
+  a.weight = (const char*)weight;
+  a.mean = (float*)mean;
+  a.rstd = (float*)rstd;
+  a.dweight = (char*)dweight;
+  a.dbias = (char*)dbias;
+  a.dim = dim;
+  a.param = param_dtype;
+  a.inv_dim = 1.f / (float)dim;
+  a.x.type = x_dtype;
+  float* part = Carve(ws).take<float>(1);
+  part = (float*)align_up((size_t)part, 256);
+  int32_t parts = 1;
+  by_type(a, Backward{a, part, &parts, stream});
+  FS_LAUNCH_CHECK();
+  if (parts > 1 && (dweight || dbias)) {
+    hipLaunchKernelGGL(k_norm_params, dim3((unsigned)cdiv(2 * (int64_t)dim, kParamCols)), dim3(1024), 0,
+                       stream, part, parts, dim, (char*)dweight, (char*)dbias, param_dtype);
+    FS_LAUNCH_CHECK();
+  }
+  return FS_OK;
+}

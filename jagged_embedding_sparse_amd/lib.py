@@ -29,7 +29,7 @@ FS_SGD, FS_RW_ADAGRAD = 0, 1
 FS_ALL, FS_EXCLUSIVE, FS_COLLISION = -1, 0, 1
 FS_ROWS_FEW, FS_ROWS_MANY, FS_ROWS_ALL = 1, 2, 3
 FS_MAX_SAMPLES, FS_MAX_RANKS, FS_MAX_TABLES, FS_MAX_UIH = 16384, 1024, 8, 65535
-FS_MAX_TOKEN_DIM, FS_MAX_HEADS = 65536, 1024
+FS_MAX_TOKEN_DIM, FS_MAX_HEADS, FS_MAX_NORM_DIM = 65536, 1024, 16384
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built: run `python __graft_entry__.py build` "
@@ -104,6 +104,11 @@ _c_attention_bwd = _sig("fs_jagged_attention_backward", C.c_int, _HP, _HP, _HP, 
                         _P, _sz, _P)
 _c_attention_bwd_ws = _sig("fs_jagged_attention_backward_workspace_size", _sz, _i64, _i32, _i32,
                             _i32, _i32)
+_c_layer_norm = _sig("fs_layer_norm", C.c_int, _P, _i32, _i64, _i64, _i32, _P, _P, _i32, _f, _P,
+                     _i32, _i64, _P, _P, _P)
+_c_layer_norm_bwd = _sig("fs_layer_norm_backward", C.c_int, _P, _i32, _i64, _i64, _i32, _P, _P, _P,
+                         _i32, _i64, _P, _i32, _P, _i64, _P, _P, _P, _sz, _P)
+_c_layer_norm_bwd_ws = _sig("fs_layer_norm_backward_workspace_size", _sz, _i64, _i32)
 _c_strerror = _sig("fs_strerror", C.c_char_p, C.c_int)
 _c_version = _sig("fs_version", C.c_int)
 
@@ -118,6 +123,7 @@ EXPORTED = ["fs_balance_fbs", "fs_balance_vbs", "fs_balance_workspace_size",
             "fs_token_sort_workspace_size", "fs_token_grad", "fs_token_grad_workspace_size",
             "fs_jagged_attention", "fs_jagged_attention_workspace_size",
             "fs_jagged_attention_backward", "fs_jagged_attention_backward_workspace_size",
+            "fs_layer_norm", "fs_layer_norm_backward", "fs_layer_norm_backward_workspace_size",
             "fs_strerror", "fs_version"]
 
 
@@ -744,6 +750,79 @@ def fs_jagged_attention_backward(q, k, v, out, lse, dout, offsets, n_cand=None, 
                             _heads_arg(dk, kv, q.dtype), _heads_arg(dv, kv, q.dtype), _ptr(err),
                             _ptr(ws), _nbytes(ws), _stream(stream)))
     return dq, dk, dv
+
+
+# ---------------------------------------------------------------------------- layer norm
+
+
+def _out(t, shape, dtype, d):
+    """An output of a call: the caller's, of this shape and type, or a fresh one."""
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=d)
+    assert tuple(t.shape) == tuple(shape) and t.dtype == dtype, "an output of another shape or type"
+    return t
+
+
+def _space(nbytes, ws):
+    """A call's workspace: the caller's, or a fresh one."""
+    return _ws(nbytes, ws)
+
+
+def _params(*tensors, dim):
+    """The one type of a norm's parameters (fp32 where there are none)."""
+    types = {t.dtype for t in tensors if t is not None}
+    assert len(types) < 2, "a norm's weight and bias have one type"
+    assert all(t.shape == (dim,) for t in tensors if t is not None)
+    return types.pop() if types else torch.float32
+
+
+@_allocates
+def fs_layer_norm(x, weight=None, bias=None, eps=1e-5, dtype=None, out=None, mean=None, rstd=None,
+                  stream=None):
+    """Layer norm of the rows of x [n, dim] (fp32, bf16 or fp16, rows contiguous,
+    any row stride) with weight and bias [dim] (of one type; None: ones, zeros),
+    in `dtype` (x's by default). Returns out, mean [n] and rstd [n] (fp32)."""
+    assert x.dim() == 2
+    (n, dim), d = x.shape, _here(x, weight, bias, out, mean, rstd)
+    param = _params(weight, bias, dim=dim)
+    out = _out(out, (n, dim), dtype or (x.dtype if out is None else out.dtype), d)
+    mean, rstd = (_out(t, (n,), torch.float32, d) for t in (mean, rstd))
+    xptr, xstride = _own_rows_ptr(x)
+    optr, ostride = _own_rows_ptr(out)
+    _check("fs_layer_norm",
+           _c_layer_norm(xptr, _dtype(x.dtype), xstride, n, dim, _ptr(weight), _ptr(bias),
+                         _dtype(param), float(eps), optr, _dtype(out.dtype), ostride, _ptr(mean),
+                         _ptr(rstd), _stream(stream)))
+    return out, mean, rstd
+
+
+def layer_norm_backward_workspace_size(n, dim):
+    return int(_c_layer_norm_bwd_ws(n, dim))
+
+
+@_allocates
+def fs_layer_norm_backward(x, mean, rstd, dout, weight=None, dx=None, dweight=None, dbias=None,
+                           ws=None, stream=None):
+    """Gradients (dx, dweight, dbias) of fs_layer_norm from its mean and rstd and
+    the gradient dout of its output (any of the three types). dx is in x's type,
+    dweight and dbias are in weight's; without a weight those two are computed
+    only into tensors given for them (None otherwise)."""
+    assert x.dim() == 2 and dout.shape == x.shape
+    (n, dim), d = x.shape, _here(x, mean, rstd, dout, weight, dx, dweight, dbias, ws)
+    assert mean.dtype == rstd.dtype == torch.float32 and mean.shape == rstd.shape == (n,)
+    param = _params(weight, dweight, dbias, dim=dim)
+    dx = _out(dx, (n, dim), x.dtype, d)
+    if weight is not None:
+        dweight, dbias = (_out(t, (dim,), param, d) for t in (dweight, dbias))
+    ws = _space(layer_norm_backward_workspace_size(n, dim), ws)
+    xptr, xstride = _own_rows_ptr(x)
+    optr, ostride = _own_rows_ptr(dout)
+    gptr, gstride = _own_rows_ptr(dx)
+    _check("fs_layer_norm_backward",
+           _c_layer_norm_bwd(xptr, _dtype(x.dtype), xstride, n, dim, _ptr(mean), _ptr(rstd), optr,
+                             _dtype(dout.dtype), ostride, _ptr(weight), _dtype(param), gptr, gstride,
+                             _ptr(dweight), _ptr(dbias), _ptr(ws), _nbytes(ws), _stream(stream)))
+    return dx, dweight, dbias
 
 
 # ---------------------------------------------------------------------------- prepared calls
