@@ -72,6 +72,7 @@ extern "C" {
 #define FS_MAX_TOKEN_DIM 65536 /* columns of a token embedding */
 #define FS_MAX_HEADS 1024      /* query heads of a jagged attention */
 #define FS_MAX_NORM_DIM 16384  /* columns of a layer norm */
+#define FS_MAX_TOP 256         /* entries of a teacher's token */
 
 /* enums */
 #define FS_F32 0
@@ -609,6 +610,87 @@ int fs_layer_norm_backward(const void* x, int32_t x_dtype, int64_t x_stride, int
                            void* dbias, void* ws, size_t ws_bytes, hipStream_t stream);
 
 size_t fs_layer_norm_backward_workspace_size(int64_t n, int32_t dim);
+
+/* ------------------------------------------------------------------------ */
+/* Token losses -- the softmax of tokens over a vocabulary's table, against  */
+/* a label or a teacher's top logits, without the tokens' logits. With       */
+/* z_iv = scale x_i . w_v over all rows v of the table,                      */
+/*   lse_i = log(sum_v exp z_iv)                                             */
+/* fs_token_loss: loss_i = lse_i - z_i,labels[i]; a token takes part where    */
+/* its label is not padding_id and inside [0, rows) (outside: FS_EF_ID_RANGE */
+/* is flagged).                                                             */
+/* fs_token_distill: entry k of token i takes part where ids[i][k] is not    */
+/* padding_id and inside [0, rows) (outside: FS_EF_ID_RANGE) and             */
+/* teacher[i][k] is not -inf; q_i is the softmax of scale teacher_i over the  */
+/* entries that do, and                                                     */
+/*   loss_i = sum_k q_ik (log q_ik - z_i,ids[i][k] + lse_i);                 */
+/* a token takes part where an entry does. One id may stand in more entries. */
+/* Tokens that take no part have loss 0 and lse 0, whatever their rows hold. */
+/* The backward calls compute the scores again and, for the gradients        */
+/* dloss_i of the losses,                                                   */
+/*   e_iv = dloss_i scale (exp(z_iv - lse_i) - t_iv),                        */
+/*   dx_i = sum_v e_iv w_v,  dweight_v = sum_i e_iv x_i,                     */
+/* t_iv being 1 at the label, or the sum of the q_ik of entries with id v.   */
+/* Tokens that take no part have dx 0 and bring nothing to dweight. Scores,   */
+/* statistics and sums are fp32; e is rounded to x's type (half a step)      */
+/* before the products that sum it, and equal calls give equal bits. In fp16  */
+/* e is rounded times a power of two, which the sums lose again: a step ends  */
+/* only at 2^-37 of the largest |dloss scale|.                              */
+/*  x        device [n][dim] of the table's type, rows x_stride bytes apart   */
+/*           (0: dense).                                                     */
+/*  table    host, one table: weights, rows, dim, dtype (FS_BF16 or FS_F16,   */
+/*           else FS_ERR_UNSUPPORTED) and stride are read. Rows of x and of  */
+/*           the table need only be aligned to an element; table rows 16-byte */
+/*           aligned and of a multiple of 8 columns are read as they lie,    */
+/*           others are laid out in the workspace first, piece by piece.      */
+/*  labels   device int64 [n]. ids: device int64 [n][top], teacher: device    */
+/*           [n][top] of teacher_dtype (any of the three), dense; top 1 ..    */
+/*           FS_MAX_TOP (more: FS_ERR_UNSUPPORTED).                          */
+/*  loss, lse  device fp32 [n]; logits: device fp32 [n][top], z at the entries */
+/*           (0 where one takes no part). The backward calls read lse and     */
+/*           logits as the forward call left them.                          */
+/*  dx       device [n][dim] of x's type, rows dx_stride bytes apart;        */
+/*  dweight  device [rows][dim] of dweight_dtype (any of the three), rows     */
+/*           dweight_stride bytes apart: every row is written. Either may be  */
+/*           NULL (not computed), not both.                                  */
+/*  err      sticky flags (may be NULL).                                     */
+/*  ws, ws_bytes  at least the query's bytes (the same for both losses), else */
+/*           FS_ERR_WORKSPACE: the tokens' rows once more and, forward, 8     */
+/*           bytes per token and 256 table rows; backward, e for a piece of  */
+/*           the table (2^29 bytes, or 512 bytes per token where that is     */
+/*           more) and the sums of cut products (2^28 bytes each, or one dx  */
+/*           in fp32 where that is more), all of them less where the sizes   */
+/*           need less.                                                     */
+/* A NaN or an infinity in a row of a token that takes part, in its dloss, or */
+/* in the table may reach every output of tokens that take part and all of    */
+/* dweight. scale is of any sign, below 2.3e38 in size. Outputs must not     */
+/* alias inputs or each other. n < 2^26, n rows < 2^37 about (else            */
+/* FS_ERR_UNSUPPORTED), dim at most FS_MAX_TOKEN_DIM.                       */
+int fs_token_loss(const void* x, int64_t x_stride, int64_t n, const fs_table* table,
+                  const int64_t* labels, float scale, int64_t padding_id, float* loss, float* lse,
+                  int32_t* err, void* ws, size_t ws_bytes, hipStream_t stream);
+
+int fs_token_loss_backward(const void* x, int64_t x_stride, int64_t n, const fs_table* table,
+                           const int64_t* labels, const float* lse, const float* dloss, float scale,
+                           int64_t padding_id, void* dx, int64_t dx_stride, void* dweight,
+                           int32_t dweight_dtype, int64_t dweight_stride, int32_t* err, void* ws,
+                           size_t ws_bytes, hipStream_t stream);
+
+int fs_token_distill(const void* x, int64_t x_stride, int64_t n, const fs_table* table,
+                     const int64_t* ids, int32_t top, const void* teacher, int32_t teacher_dtype,
+                     float scale, int64_t padding_id, float* loss, float* lse, float* logits,
+                     int32_t* err, void* ws, size_t ws_bytes, hipStream_t stream);
+
+int fs_token_distill_backward(const void* x, int64_t x_stride, int64_t n, const fs_table* table,
+                              const int64_t* ids, int32_t top, const void* teacher,
+                              int32_t teacher_dtype, const float* lse, const float* logits,
+                              const float* dloss, float scale, int64_t padding_id, void* dx,
+                              int64_t dx_stride, void* dweight, int32_t dweight_dtype,
+                              int64_t dweight_stride, int32_t* err, void* ws, size_t ws_bytes,
+                              hipStream_t stream);
+
+size_t fs_token_loss_workspace_size(int64_t n, int64_t rows, int32_t dim);
+size_t fs_token_loss_backward_workspace_size(int64_t n, int64_t rows, int32_t dim);
 
 /* ------------------------------------------------------------------------ */
 const char* fs_strerror(int code);

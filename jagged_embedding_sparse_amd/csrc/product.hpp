@@ -1,0 +1,302 @@
+// Tile products of 16-bit matrices on the matrix cores: a workgroup of eight
+// waves computes out[n][m] = sum over k of A(m, k) B(n, k) for BM columns m and
+// BN rows n of the output, with fp32 sums in registers.
+//
+// An operand lies in memory in one of two ways: Rows, its row m (or n) holding
+// the k's one after another, or Cols, its row k holding the m's. Either travels
+// to LDS as it lies, 64 k's a step, without registers, and is read into the
+// layout of v_mfma_f32_32x32x16 (see attention.hpp): a row's 16 bytes for Rows,
+// two transposing 8-byte reads for Cols. Pieces of 16 bytes are permuted by
+// exclusive-or with bits of the row so that neither read meets a bank twice.
+//
+// The pipeline: two stages in LDS. A step has four chunks of 16 k's; the next
+// chunk's operands are read while this one's products run, and the one barrier
+// of a step stands before its last chunk's products, which cover the first reads
+// of the next stage. Loads are asked for right behind the barrier, a whole step
+// before they are waited for.
+#pragma once
+
+#include "attention.hpp"
+
+namespace fs {
+namespace prod {
+
+using attn::Elem;
+using attn::f32x16;
+using attn::f32x4;
+using attn::u32x2;
+using attn::u32x4;
+
+constexpr int kK = 64;        // k's of a step
+constexpr int kWaves = 8;
+constexpr int kThreads = kWaves * kWave;
+
+typedef __attribute__((address_space(3))) uint16_t* lds_ptr;
+
+// 16 bytes per lane from base + at to LDS address `to` + 16 lane, for N loads
+// whose LDS addresses are `step` apart. M0 is put back: the compiler does not let
+// an asm declare that it changes it.
+template <int N>
+__device__ __forceinline__ void load_pieces(const char* base, const uint32_t (&at)[N], uint32_t to,
+                                            uint32_t step) {
+#pragma unroll
+  for (int x = 0; x < N; ++x) {
+    uint32_t m0;
+    asm volatile(
+        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\t"
+        "s_mov_b32 m0, %0"
+        : "=&s"(m0)
+        : "s"(to + x * step), "v"(at[x]), "s"(base)
+        : "memory");
+  }
+}
+
+// k's together: a tile of R rows and 64 k's, rows of 128 bytes.
+template <int R>
+struct Rows {
+  static constexpr int kElems = R * kK;
+  static constexpr int kPer = R * 8 / kThreads;  // loads of a thread
+  static_assert(kPer >= 1 && R * 8 % kThreads == 0, "whole pieces per thread");
+  const char* base;  // of the tile's first row, at the next step's first k
+  uint32_t at[kPer];
+  uint32_t row_bytes;
+  int32_t last;
+
+  static __device__ __forceinline__ int row_of(int x) { return x * (kThreads / 8) + (int)threadIdx.x / 8; }
+  static __device__ __forceinline__ int piece_of() {
+    return ((int)threadIdx.x % 8) ^ attn::swz<kK>((int)threadIdx.x / 8);
+  }
+  // rows row0 .. of `rows` rows; rows past the last load it again
+  __device__ __forceinline__ Rows(const char* p, int64_t stride, int64_t row0, int64_t rows, int64_t k0) {
+    base = attn::uniform(p + row0 * stride + k0 * 2);
+    row_bytes = (uint32_t)stride;
+    last = (int32_t)min((int64_t)R, rows - row0) - 1;
+    limit(kK);
+  }
+  // pieces of k's past `left` load the step's first
+  __device__ __forceinline__ void limit(int left) {
+    const int p = 8 * piece_of() < left ? piece_of() : 0;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) at[x] = (uint32_t)min(row_of(x), last) * row_bytes + 16 * p;
+  }
+  __device__ __forceinline__ void load(uint32_t tile) {
+    load_pieces(base, at, tile + attn::wave_id() * (kWave * 16), kThreads * 16);
+    base = attn::uniform(base + kK * 2);
+  }
+  // rows r0 .. r0 + 31 (a multiple of 32), k's 16 kk ..
+  struct Read {
+    int rows_at;
+    __device__ __forceinline__ Read() { rows_at = attn::piece<kK>(lane() & 31, lane() >> 5); }
+    __device__ __forceinline__ u32x4 operator()(const uint16_t* tile, int r0, int kk) const {
+      return *(const u32x4*)(tile + (rows_at ^ (16 * kk)) + r0 * kK);
+    }
+  };
+};
+
+// k's apart: a tile of 64 k's, rows of R elements. Piece p of row r lies at
+// p ^ ((r & 3) << 2 | (r >> 2) & 3): see attention.hpp.
+template <int R>
+struct Cols {
+  static constexpr int kElems = R * kK;
+  static constexpr int kPieces = R / 8;
+  static constexpr int kPer = R * 8 / kThreads;
+  static constexpr int kStepRows = kThreads / kPieces;
+  static_assert(kPer >= 1 && R * 8 % kThreads == 0 && kStepRows % 16 == 0, "a thread's rows share the permutation");
+  const char* base;  // of the next step's first row, at the tile's first column
+  uint32_t at[kPer];
+  uint32_t row_bytes;
+  int32_t cols;
+
+  static __device__ __forceinline__ int row_of(int x) { return x * kStepRows + (int)threadIdx.x / kPieces; }
+  static __device__ __forceinline__ int piece_of() {
+    return ((int)threadIdx.x % kPieces) ^ attn::swz<128>((int)threadIdx.x / kPieces);
+  }
+  // columns col0 .. of `cols_` (a multiple of 8); pieces past the last load the tile's first
+  __device__ __forceinline__ Cols(const char* p, int64_t stride, int64_t col0, int64_t cols_, int64_t k0) {
+    base = attn::uniform(p + k0 * stride + col0 * 2);
+    row_bytes = (uint32_t)stride;
+    cols = (int32_t)min((int64_t)R, cols_ - col0);
+    limit(kK);
+  }
+  // rows past `left` load the step's first
+  __device__ __forceinline__ void limit(int left) {
+    const int p = 8 * piece_of() < cols ? piece_of() : 0;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x)
+      at[x] = (row_of(x) < left ? (uint32_t)row_of(x) * row_bytes : 0u) + 16 * p;
+  }
+  __device__ __forceinline__ void load(uint32_t tile) {
+    load_pieces(base, at, tile + attn::wave_id() * (kWave * 16), kThreads * 16);
+    base = attn::uniform(base + (int64_t)kK * row_bytes);
+  }
+  struct Read {
+    int cols_at;
+    __device__ __forceinline__ Read() {
+      const int l = lane(), g = l >> 5, j = l & 15, col = (l & 16) + 4 * (j & 3);
+      const int p = (col >> 3) ^ ((j >> 2) << 2 | 2 * g);
+      cols_at = (8 * g + (j >> 2)) * R + 8 * p + (col & 7);
+    }
+    // columns c0 .. c0 + 31 (a multiple of 32), k's 16 kk + 8 g ..
+    __device__ __forceinline__ u32x4 operator()(const uint16_t* tile, int c0, int kk) const {
+      const uint16_t* a = tile + (cols_at ^ c0) + 16 * kk * R;
+      const uint16_t* b = tile + (cols_at ^ c0 ^ 8) + (16 * kk + 4) * R;
+      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn::lds_s16x4*)a));
+      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn::lds_s16x4*)b));
+      return u32x4{lo[0], lo[1], hi[0], hi[1]};
+    }
+  };
+};
+
+// WM x WN waves, each of MI x NI blocks of 32 x 32. Register i of a lane's block
+// (mi, ni) is column m = m_of(mi) + 8 (i / 4) + i % 4 of row n = n_of(ni).
+template <typename T, typename A, typename B, int BM, int BN, int WM, int WN>
+struct Tile {
+  static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
+  static constexpr int kStage = (BM + BN) * kK;  // elements
+  static_assert(WM * WN == kWaves && MI >= 1 && NI >= 1, "eight waves");
+  f32x16 acc[MI][NI];
+
+  static __device__ __forceinline__ int m_of(int mi) {
+    return (attn::wave_id() % WM * MI + mi) * 32 + 4 * (lane() >> 5);
+  }
+  static __device__ __forceinline__ int n_of(int ni) {
+    return (attn::wave_id() / WM * NI + ni) * 32 + (lane() & 31);
+  }
+
+  struct Operands {
+    u32x4 a[MI], b[NI];
+  };
+  __device__ __forceinline__ void read(Operands& o, const typename A::Read& ra, const typename B::Read& rb,
+                                       const uint16_t* stage, int kk) const {
+    const int w = attn::wave_id();
+#pragma unroll
+    for (int i = 0; i < NI; ++i) o.b[i] = rb(stage + BM * kK, (w / WM * NI + i) * 32, kk);
+#pragma unroll
+    for (int i = 0; i < MI; ++i) o.a[i] = ra(stage, (w % WM * MI + i) * 32, kk);
+  }
+  __device__ __forceinline__ void multiply(const Operands& o) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = Elem<T>::mfma(o.a[i], o.b[j], acc[i][j]);
+  }
+
+  // `k` k's from where a and b stand, in steps of 64; in the last step the
+  // operands are told how many are left where LIM says so. lds: 2 kStage elements.
+  // The stages are free again when it returns.
+  template <bool LimA, bool LimB>
+  __device__ __forceinline__ void run(A& a, B& b, int64_t k, uint16_t* lds) {
+    const typename A::Read ra;
+    const typename B::Read rb;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)lds);
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = attn::zero16();
+    const int steps = (int)cdiv(k, (int64_t)kK);
+    if (steps <= 0) return;
+    auto load = [&](int step, int buf) {
+      if ((LimA || LimB) && (step + 1) * (int64_t)kK > k) {
+        if (LimA) a.limit((int)(k - step * (int64_t)kK));
+        if (LimB) b.limit((int)(k - step * (int64_t)kK));
+      }
+      a.load(lds0 + buf * (kStage * 2));
+      b.load(lds0 + buf * (kStage * 2) + BM * kK * 2);
+    };
+    load(0, 0);
+    landed();
+    if (steps > 1) load(1, 1);
+    Operands o[2];
+    read(o[0], ra, rb, lds, 0);
+    // one step on stage `buf`; the other one holds the next step's tiles
+    auto step = [&](int t, int buf) {
+      const uint16_t* here = lds + buf * kStage;
+#pragma unroll
+      for (int kk = 0; kk < 3; ++kk) {
+        read(o[(kk + 1) & 1], ra, rb, here, kk + 1);
+        multiply(o[kk & 1]);
+      }
+      // the last chunk's operands are here (the compiler waits for them before
+      // the barrier's fence), so this stage may be written behind the barrier
+      landed();
+      if (t + 1 < steps) {
+        if (t + 2 < steps) load(t + 2, buf);
+        read(o[0], ra, rb, lds + (buf ^ 1) * kStage, 0);
+      }
+      multiply(o[1]);
+    };
+    int t = 0;
+    for (; t + 1 < steps; t += 2) {
+      step(t, 0);
+      step(t + 1, 1);
+    }
+    if (t < steps) step(t, 0);
+  }
+
+  // every wave's loads have landed and every wave's reads of LDS are done
+  static __device__ __forceinline__ void landed() {
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+  }
+};
+
+// ---------------------------------------------------------------- output
+// Rows of a tile pass through LDS so that memory sees whole rows: 4 neighbouring
+// columns of a lane are 8 (16-bit) or 16 bytes (fp32), and a row's 16-byte pieces
+// are permuted by the row, so neither side meets a bank twice.
+//
+// put(n, m, v): columns m .. m + 3 of row n of the staged rows; at: a thread's
+// pieces in turn.
+template <int BM>
+struct Stage16 {  // rows of BM elements of 2 bytes
+  static constexpr int kPieces = BM / 8;
+  static __device__ __forceinline__ void put(uint16_t* lds, int n, int m, u32x2 v) {
+    const int p = (m >> 3) ^ (n & (kPieces - 1));
+    *(u32x2*)(lds + n * BM + 8 * p + (m & 7)) = v;
+  }
+  static __device__ __forceinline__ u32x4 get(const uint16_t* lds, int n, int piece) {
+    return *(const u32x4*)(lds + n * BM + 8 * (piece ^ (n & (kPieces - 1))));
+  }
+};
+template <int BM>
+struct Stage32 {  // rows of BM floats
+  static constexpr int kPieces = BM / 4;
+  static __device__ __forceinline__ void put(float* lds, int n, int m, f32x4 v) {
+    *(f32x4*)(lds + n * BM + 4 * ((m >> 2) ^ (n & (kPieces - 1)))) = v;
+  }
+  static __device__ __forceinline__ f32x4 get(const float* lds, int n, int piece) {
+    return *(const f32x4*)(lds + n * BM + 4 * (piece ^ (n & (kPieces - 1))));
+  }
+};
+
+// Elements at any alignment, 16 bytes at a time where they are whole.
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+// Order of a grid's tiles: XCD x runs an eighth of them in a row, and inside
+// that blocks of `group` row tiles go by column tile, so that the tiles of an XCD
+// at one time share operands in its L2.
+struct Order {
+  int32_t rows, cols;  // tiles
+  __device__ __forceinline__ void at(int32_t id, int32_t group, int32_t* row, int32_t* col) const {
+    const int32_t whole = rows / group * group * cols;
+    if (id < whole) {
+      const int32_t block = group * cols, b = id / block, r = id % block;
+      *row = b * group + r % group;
+      *col = r / group;
+    } else {
+      const int32_t left = rows % group, r = id - whole;
+      *row = rows / group * group + r % left;
+      *col = r / left;
+    }
+  }
+};
+// workgroup to position: neighbours in order on one XCD
+__device__ __forceinline__ int32_t in_order(int32_t bid, int32_t n) {
+  const int32_t per = n / kXcd, cut = n % kXcd, x = bid % kXcd, i = bid / kXcd;
+  return x < cut ? x * (per + 1) + i : cut * (per + 1) + (x - cut) * per + i;
+}
+
+}  // namespace prod
+}  // namespace fs

@@ -1,0 +1,1175 @@
+// Softmax losses of tokens against a vocabulary's table, without their logits.
+//
+//   z_iv = scale x_i . w_v,  lse_i = log sum_v exp z_iv
+//   loss:     loss_i = lse_i - z_i,label(i)
+//   distill:  q_i = softmax of scale teacher_i over the token's entries,
+//             loss_i = sum_k q_ik (log q_ik - z_i,id(k) + lse_i)
+//   back:     e_iv = dloss_i scale (exp(z_iv - lse_i) - target_iv),  dx = e w,  dw = e^T x
+//             target: 1 at the label; the sum of the q of the entries with id v
+//
+// Tokens that take part are first packed together (k_head_pack). The forward
+// pass is one product whose tiles keep a maximum and a sum per token instead of
+// scores. The backward pass goes over the table in pieces: scores again, e in 16
+// bits, and the two products that sum it; what it holds of a piece is bounded
+// whatever the vocabulary's size.
+#include <algorithm>
+#include <cmath>
+
+#include "product.hpp"
+
+namespace fs {
+namespace {
+
+using namespace prod;
+
+constexpr float kLog2e = attn::kLog2e, kLn2 = attn::kLn2;
+constexpr int kV = 256;                           // table rows of a tile
+constexpr int kD = 256;                           // columns of a gradient's tile
+constexpr int64_t kPieceBytes = (int64_t)1 << 29;  // e of one piece of the table
+constexpr int64_t kPackBytes = (int64_t)1 << 26;   // a piece of a table that has to be laid out
+constexpr int64_t kPartBytes = (int64_t)1 << 28;   // sums of a cut product
+constexpr int kMostParts = 32;
+
+// What the kernels of one call share, in its workspace.
+struct Head {
+  int32_t* n_live;  // tokens that take part
+  float* mul;       // [2]: e is rounded times mul[0], sums of it come times mul[1]
+  int32_t* pos;     // [n] a token's place among them, or -1
+  int32_t* label;   // [npad] by place, as are lse2 and coef
+  float* lse2;      // lse log2(e)
+  float* coef;      // dloss scale
+  char* x;          // [npad][dp] 16 bits: their rows, zeros past dim and past n_live
+  int64_t n, npad;
+  int32_t dim, dp;
+};
+
+// 8 elements of a row of `dim`, zeros past it, from any alignment
+__device__ __forceinline__ u32x4 row_piece(const char* row, int32_t col, int32_t dim) {
+  if (col + 8 <= dim) return *(const u32x4_any*)(row + 2 * (int64_t)col);
+  uint16_t v[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = col + e < dim ? ((const uint16_t*)row)[col + e] : (uint16_t)0;
+  u32x4 r;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) r[e] = v[2 * e] | (uint32_t)v[2 * e + 1] << 16;
+  return r;
+}
+
+// ---------------------------------------------------------------- packing
+struct PackArgs {
+  Head h;
+  const char* x;
+  int64_t x_stride;
+  const int64_t* labels;  // or null: live says which tokens take part
+  const uint8_t* live;
+  int64_t rows, pad;
+  const float *lse, *dloss;  // backward
+  int32_t back;
+  float scale;
+  int32_t per;     // tokens of a workgroup
+  int32_t pad_to;  // zero rows up to a multiple of this
+  int32_t narrow;  // fp16
+  int32_t* err;
+};
+
+constexpr int kPackThreads = 256;
+
+__device__ __forceinline__ bool takes_part(const PackArgs& a, int64_t i, bool* bad) {
+  if (!a.labels) return a.live[i] != 0;
+  const int64_t v = a.labels[i];
+  const bool in = v >= 0 && v < a.rows;
+  *bad = !in && v != a.pad;
+  return in && v != a.pad;
+}
+
+// Each workgroup counts the tokens before its own that take part (labels are few
+// bytes beside the rows), so one launch does it without waiting for another
+// workgroup. The last workgroup writes the count and the zero rows behind it.
+__global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
+  __shared__ int32_t tmp[17], s_row[kPackThreads];
+  __shared__ float s_max[kPackThreads / kWave];
+  const int64_t i0 = (int64_t)blockIdx.x * a.per, i1 = min(a.h.n, i0 + a.per);
+  int32_t count = 0;
+  bool bad = false;
+  for (int64_t i = threadIdx.x; i < i0; i += kPackThreads) count += takes_part(a, i, &bad);
+  int32_t base;
+  block_excl_scan<int32_t>(count, tmp, &base);
+  const int32_t pieces = a.h.dp / 8;
+  for (int64_t c = i0; c < i1; c += kPackThreads) {  // uniform
+    const int64_t i = c + threadIdx.x;
+    bad = false;
+    const bool on = i < i1 && takes_part(a, i, &bad);
+    flag_err(a.err, bad, FS_EF_ID_RANGE);
+    int32_t total;
+    const int32_t at = block_excl_scan<int32_t>(on ? 1 : 0, tmp, &total);
+    if (i < i1) a.h.pos[i] = on ? base + at : -1;
+    if (on) {
+      s_row[at] = (int32_t)(i - i0);
+      a.h.label[base + at] = a.labels ? (int32_t)a.labels[i] : -1;
+      if (a.back) {
+        a.h.lse2[base + at] = a.lse[i] * kLog2e;
+        a.h.coef[base + at] = a.dloss[i] * a.scale;
+      }
+    }
+    __syncthreads();
+    for (int32_t u = threadIdx.x; u < total * pieces; u += kPackThreads) {
+      const int32_t r = u / pieces, p = u - r * pieces;
+      *(u32x4*)(a.h.x + ((int64_t)(base + r) * a.h.dp + 8 * p) * 2) =
+          row_piece(a.x + (i0 + s_row[r]) * a.x_stride, 8 * p, a.h.dim);
+    }
+    base += total;
+    __syncthreads();
+  }
+  if (blockIdx.x == gridDim.x - 1) {
+    const int32_t end = (int32_t)cdiv(base, a.pad_to) * a.pad_to, rest = end - base;
+    if (threadIdx.x == 0) *a.h.n_live = base;
+    for (int32_t r = base + threadIdx.x; r < end; r += kPackThreads) {
+      a.h.label[r] = -1;
+      a.h.lse2[r] = a.h.coef[r] = 0.f;
+    }
+    for (int32_t u = threadIdx.x; u < rest * pieces; u += kPackThreads)
+      *(u32x4*)(a.h.x + ((int64_t)base * a.h.dp + 8 * (int64_t)u) * 2) = u32x4{0, 0, 0, 0};
+  }
+  if (blockIdx.x == 0 && a.back) {
+    // fp16's exponents end where e's do not: e is rounded times a power of two
+    // that takes the largest coefficient to 2^13 .. 2^14, and the sums lose it again
+    float top = 0.f;
+    if (a.narrow) {
+      for (int64_t i = threadIdx.x; i < a.h.n; i += kPackThreads)
+        if (takes_part(a, i, &bad)) top = fmaxf(top, fabsf(a.dloss[i] * a.scale));
+#pragma unroll
+      for (int d = kWave / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+      if (lane() == 0) s_max[threadIdx.x / kWave] = top;
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) {
+      float m = 1.f, back = 1.f;
+      if (a.narrow) {
+        for (int w = 0; w < kPackThreads / kWave; ++w) top = fmaxf(top, s_max[w]);
+        int ex = 0;
+        if (top > 0.f && top < INFINITY) frexpf(top, &ex);
+        // powers of two that fp32 has on both sides
+        const int s = min(max(14 - ex, -120), 120);
+        m = ldexpf(1.f, s);
+        back = ldexpf(1.f, -s);
+      }
+      a.h.mul[0] = m;
+      a.h.mul[1] = back;
+    }
+  }
+}
+
+// Table rows that the tiles cannot load as they lie, [rows][dp] with zeros past dim.
+__global__ void __launch_bounds__(kPackThreads)
+k_table_pack(const char* w, int64_t stride, int64_t rows, int32_t dim, int32_t dp, char* to) {
+  const int32_t pieces = dp / 8;
+  for (int64_t u = (int64_t)blockIdx.x * kPackThreads + threadIdx.x; u < rows * pieces;
+       u += (int64_t)gridDim.x * kPackThreads) {
+    const int64_t r = u / pieces;
+    *(u32x4*)(to + u * 16) = row_piece(w + r * stride, 8 * (int32_t)(u - r * pieces), dim);
+  }
+}
+
+// ---------------------------------------------------------------- scores
+struct ScoreArgs {
+  Head h;
+  const char* w;     // the piece's first row
+  int64_t w_stride;
+  int64_t v0;        // its number in the table
+  int64_t rows;      // rows of the piece
+  int32_t k;         // elements of a row
+  int32_t v_tile0;   // forward: tiles of the pieces before
+  Order order;
+  float scale2;      // scale log2(e)
+  float2* part;      // forward: [tiles of the table][npad] maximum and sum, base 2
+  float* at_label;   // forward: [npad] the label's score, base 2
+  char* e;           // backward: [npad][e_cols] 16 bits
+  int64_t e_cols;
+};
+
+constexpr int kGroup = 8;  // token tiles that go by a table tile together
+
+// One tile of scores. Columns of the product are table rows, its rows tokens:
+// a lane's registers hold one token's scores, so their maximum and sum need one
+// exchange between two lanes and one between waves.
+template <typename T, int BN, int WM, int WN, bool Back>
+__global__ void __launch_bounds__(kThreads) k_scores(ScoreArgs a) {
+  using P = Tile<T, Rows<kV>, Rows<BN>, kV, BN, WM, WN>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
+  static_assert(2 * P::kStage >= BN * kV, "the stages hold a tile of e");
+  int32_t tn, tv;
+  a.order.at(in_order(blockIdx.x, gridDim.x), kGroup, &tn, &tv);
+  const int32_t live = *a.h.n_live;
+  const int64_t n0 = (int64_t)tn * BN, v0 = (int64_t)tv * kV;
+  if (n0 >= live) return;
+  Rows<kV> w(a.w, a.w_stride, v0, a.rows, 0);
+  Rows<BN> x(a.h.x, 2 * (int64_t)a.h.dp, n0, a.h.npad, 0);
+  P p;
+  p.template run<true, false>(w, x, a.k, lds);
+  const int left = (int)min((int64_t)kV, a.rows - v0);  // rows of this tile
+  if constexpr (!Back) {
+    float2(*s_part)[BN] = (float2(*)[BN])lds;  // the stages are done with
+    static_assert(4 * P::kStage >= WM * BN * 8, "");
+#pragma unroll
+    for (int j = 0; j < P::NI; ++j) {
+      const int n = P::n_of(j);
+      const int64_t lab = (int64_t)a.h.label[n0 + n] - a.v0 - v0;
+      float top = -3e38f;  // finite, so that scores of -inf add 0
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int m = P::m_of(i) + 8 * (r >> 2) + (r & 3);
+          p.acc[i][j][r] *= a.scale2;
+          if (left < kV && m >= left) p.acc[i][j][r] = -INFINITY;
+          top = fmaxf(top, p.acc[i][j][r]);
+        }
+      top = attn::max_halves(top);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum[r & 3] += __builtin_amdgcn_exp2f(p.acc[i][j][r] - top);
+      const float total = attn::add_halves((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      if (lab >= 0 && lab < kV) {
+#pragma unroll
+        for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (P::m_of(i) + 8 * (r >> 2) + (r & 3) == lab) a.at_label[n0 + n] = p.acc[i][j][r];
+      }
+      if (lane() < 32) s_part[attn::wave_id() % WM][n] = make_float2(top, total);
+    }
+    __syncthreads();
+    for (int n = threadIdx.x; n < BN; n += kThreads) {
+      float top = s_part[0][n].x;
+#pragma unroll
+      for (int i = 1; i < WM; ++i) top = fmaxf(top, s_part[i][n].x);
+      float sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < WM; ++i) sum += s_part[i][n].y * __builtin_amdgcn_exp2f(s_part[i][n].x - top);
+      a.part[(int64_t)(a.v_tile0 + tv) * a.h.npad + n0 + n] = make_float2(top, sum);
+    }
+  } else {
+    const float mul = a.h.mul[0];
+#pragma unroll
+    for (int j = 0; j < P::NI; ++j) {
+      const int n = P::n_of(j);
+      const int64_t lab = (int64_t)a.h.label[n0 + n] - a.v0 - v0;
+      const int label = lab >= 0 && lab < kV ? (int)lab : -1;
+      const float lse2 = a.h.lse2[n0 + n], c = a.h.coef[n0 + n] * mul;
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int m = P::m_of(i) + 8 * q;
+          float v[4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            v[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][4 * q + r], a.scale2, -lse2));
+            if (m + r == label) v[r] -= 1.f;
+            v[r] *= c;
+            if (left < kV && m + r >= left) v[r] = 0.f;
+          }
+          u32x2 y;
+          y[0] = Elem<T>::pack(v[0], v[1]);
+          y[1] = Elem<T>::pack(v[2], v[3]);
+          Stage16<kV>::put(lds, n, m, y);
+        }
+    }
+    __syncthreads();
+    constexpr int kPieces = kV / 8;
+#pragma unroll 4
+    for (int u = threadIdx.x; u < BN * kPieces; u += kThreads) {
+      const int n = u / kPieces, piece = u % kPieces;
+      *(u32x4*)(a.e + ((n0 + n) * a.e_cols + v0 + 8 * piece) * 2) = Stage16<kV>::get(lds, n, piece);
+    }
+  }
+}
+
+// ---------------------------------------------------------------- gradients
+struct SumArgs {
+  Head h;
+  const char* w;     // dx: the piece's first row
+  int64_t w_stride;
+  int64_t rows;      // rows of the piece
+  int32_t w_cols;
+  const char* e;
+  int64_t e_cols;
+  Order order;       // of the output's tiles
+  int32_t parts;     // of the sum
+  int32_t steps;     // of 64, of a part (dx)
+  int32_t add;       // to what the parts hold
+  float* part;       // [parts][rows of the output][dp], or
+  char* out;         // the output itself
+  int64_t out_stride, out_rows;
+  int32_t out_type;
+};
+
+// A tile's sums, fp32, to [row][dp] floats or to an output of any type.
+template <typename T, typename P, int BN, int WM>
+__device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, float* part, int64_t row0,
+                                         int64_t rows, int32_t col0) {
+  const int32_t cols = part ? a.h.dp : a.h.dim;
+  if (part || a.out_type == FS_F32) {
+    const float back = part ? 1.f : a.h.mul[1];
+    constexpr int kRows = kWaves / WM * 32, kPieces = kD / 4;
+    float* f = (float*)lds;
+#pragma unroll
+    for (int j = 0; j < P::NI; ++j) {
+      if (j) __syncthreads();
+      const int n = attn::wave_id() / WM * 32 + (lane() & 31);
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          Stage32<kD>::put(f, n, P::m_of(i) + 8 * q,
+                           f32x4{p.acc[i][j][4 * q] * back, p.acc[i][j][4 * q + 1] * back,
+                                 p.acc[i][j][4 * q + 2] * back, p.acc[i][j][4 * q + 3] * back});
+      __syncthreads();
+#pragma unroll 4
+      for (int u = threadIdx.x; u < kRows * kPieces; u += kThreads) {
+        const int s = u / kPieces, piece = u % kPieces;
+        const int64_t row = row0 + (s / 32 * P::NI + j) * 32 + s % 32;
+        const int32_t col = col0 + 4 * piece;
+        if (row >= rows || col >= cols) continue;
+        f32x4 v = Stage32<kD>::get(f, s, piece);
+        if (part) {
+          f32x4* to = (f32x4*)(part + row * a.h.dp + col);
+          if (a.add) v += *to;
+          *to = v;
+        } else {
+          float* to = (float*)(a.out + row * a.out_stride) + col;
+          if (col + 4 <= cols) {
+            *(f32x4_any*)to = v;
+          } else {
+            for (int e = 0; e < cols - col; ++e) to[e] = v[e];
+          }
+        }
+      }
+    }
+    return;
+  }
+  const float back = a.h.mul[1];
+  constexpr int kPieces = kD / 8;
+#pragma unroll
+  for (int j = 0; j < P::NI; ++j)
+#pragma unroll
+    for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = p.acc[i][j][4 * q + r] * back;
+        u32x2 y;
+        if (a.out_type == FS_BF16) {
+          y[0] = Elem<__bf16>::pack(v[0], v[1]);
+          y[1] = Elem<__bf16>::pack(v[2], v[3]);
+        } else {
+          y[0] = Elem<_Float16>::pack(v[0], v[1]);
+          y[1] = Elem<_Float16>::pack(v[2], v[3]);
+        }
+        Stage16<kD>::put(lds, P::n_of(j), P::m_of(i) + 8 * q, y);
+      }
+  __syncthreads();
+#pragma unroll 4
+  for (int u = threadIdx.x; u < BN * kPieces; u += kThreads) {
+    const int n = u / kPieces, piece = u % kPieces;
+    const int64_t row = row0 + n;
+    const int32_t col = col0 + 8 * piece;
+    if (row >= rows || col >= cols) continue;
+    const u32x4 v = Stage16<kD>::get(lds, n, piece);
+    uint16_t* to = (uint16_t*)(a.out + row * a.out_stride) + col;
+    if (col + 8 <= cols) {
+      *(u32x4_any*)to = v;
+    } else {
+      for (int e = 0; e < cols - col; ++e) to[e] = (uint16_t)(v[e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
+
+// dx = e w over a part of the piece's rows, by tokens' places.
+template <typename T, int BN, int WM, int WN>
+__global__ void __launch_bounds__(kThreads) k_grad_x(SumArgs a) {
+  using P = Tile<T, Cols<kD>, Rows<BN>, kD, BN, WM, WN>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
+  static_assert(4 * P::kStage >= kWaves / WM * 32 * kD * 4, "the stages hold rows of sums");
+  const int32_t tiles = a.order.rows * a.order.cols, id = in_order(blockIdx.x, gridDim.x);
+  int32_t tn, td;
+  // parts of one tile run apart, tiles of one part together
+  a.order.at(id % tiles, kGroup, &tn, &td);
+  const int32_t part = id / tiles;
+  const int64_t n0 = (int64_t)tn * BN;
+  if (n0 >= *a.h.n_live) return;
+  const int64_t k0 = (int64_t)part * a.steps * kK, k1 = min(a.rows, k0 + (int64_t)a.steps * kK);
+  P p;
+  Cols<kD> w(a.w, a.w_stride, td * kD, a.w_cols, k0);
+  Rows<BN> e(a.e, 2 * a.e_cols, n0, a.h.npad, k0);
+  p.template run<true, false>(w, e, k1 - k0, lds);
+  put_sums<T, P, BN, WM>(p, lds, a, a.part + (int64_t)part * a.h.npad * a.h.dp, n0, a.h.npad, td * kD);
+}
+
+// dw = e^T x over a part of the tokens.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) k_grad_w(SumArgs a) {
+  constexpr int WM = 2, WN = 4;
+  using P = Tile<T, Cols<kD>, Cols<kV>, kD, kV, WM, WN>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
+  const int32_t tiles = a.order.rows * a.order.cols, id = in_order(blockIdx.x, gridDim.x);
+  int32_t tv, td;
+  a.order.at(id % tiles, kGroup, &tv, &td);
+  const int32_t part = id / tiles;
+  // rows of e and x are zeros from n_live to the next multiple of 64
+  const int64_t steps = cdiv(*a.h.n_live, kK), per = cdiv(steps, a.parts);
+  const int64_t s0 = min(steps, part * per), s1 = min(steps, s0 + per);
+  P p;
+  Cols<kD> x(a.h.x, 2 * (int64_t)a.h.dp, td * kD, a.h.dp, s0 * kK);
+  Cols<kV> e(a.e, 2 * a.e_cols, (int64_t)tv * kV, a.e_cols, s0 * kK);
+  p.template run<false, false>(x, e, (s1 - s0) * kK, lds);
+  float* to = a.part ? a.part + (int64_t)part * a.out_rows * a.h.dp : nullptr;
+  put_sums<T, P, kV, WM>(p, lds, a, to, (int64_t)tv * kV, a.out_rows, td * kD);
+}
+
+// The parts of a sum, added in order and rounded once. Rows of pos < 0 are zeros.
+struct JoinArgs {
+  const float* part;
+  int64_t part_rows;
+  int32_t parts, dp, dim;
+  const int32_t* pos;  // null: every row is its own
+  int64_t rows;
+  const float* mul;
+  char* out;
+  int64_t out_stride;
+};
+template <typename T>
+__global__ void __launch_bounds__(256) k_join(JoinArgs a) {
+  const int32_t pieces = (int32_t)cdiv(a.dim, 4);
+  const float back = a.mul[1];
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < a.rows * pieces; u += (int64_t)gridDim.x * 256) {
+    const int64_t row = u / pieces;
+    const int32_t col = 4 * (int32_t)(u - row * pieces);
+    const int64_t r = a.pos ? a.pos[row] : row;
+    f32x4 s = {0.f, 0.f, 0.f, 0.f};
+    if (r >= 0) {
+      const f32x4* p = (const f32x4*)(a.part + r * a.dp + col);
+      const int64_t step = a.part_rows * a.dp / 4;
+      for (int i = 0; i < a.parts; ++i) s += p[i * step];
+      s *= back;
+    }
+    T* to = (T*)(a.out + row * a.out_stride) + col;
+    struct __attribute__((packed, aligned(sizeof(T)))) Four {
+      T v[4];
+    };
+    if (col + 4 <= a.dim) {
+      *(Four*)to = Four{{(T)s[0], (T)s[1], (T)s[2], (T)s[3]}};
+    } else {
+      for (int e = 0; e < a.dim - col; ++e) to[e] = (T)s[e];
+    }
+  }
+}
+
+// ---------------------------------------------------------------- losses
+struct LossArgs {
+  Head h;
+  const float2* part;
+  int64_t tiles;
+  const float* at_label;  // null: no loss here
+  float *loss, *lse;
+};
+
+// A token's tiles joined: R tokens a workgroup, 256 / R threads each.
+template <int R>
+__global__ void __launch_bounds__(256) k_loss(LossArgs a) {
+  constexpr int Q = 256 / R;
+  __shared__ float2 sh[Q][R];
+  const int r = threadIdx.x % R, q = threadIdx.x / R;
+  const int64_t i = (int64_t)blockIdx.x * R + r;
+  const int32_t pos = i < a.h.n ? a.h.pos[i] : -1;
+  float top = -3e38f, sum = 0.f;
+  if (pos >= 0) {
+    int64_t t = q;
+    for (; t + 3 * Q < a.tiles; t += 4 * Q) {
+      float2 x[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) x[u] = a.part[(t + u * Q) * a.h.npad + pos];
+      const float m = fmaxf(fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x)), top);
+      sum *= __builtin_amdgcn_exp2f(top - m);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) sum += x[u].y * __builtin_amdgcn_exp2f(x[u].x - m);
+      top = m;
+    }
+    for (; t < a.tiles; t += Q) {
+      const float2 x = a.part[t * a.h.npad + pos];
+      const float m = fmaxf(x.x, top);
+      sum = sum * __builtin_amdgcn_exp2f(top - m) + x.y * __builtin_amdgcn_exp2f(x.x - m);
+      top = m;
+    }
+  }
+  sh[q][r] = make_float2(top, sum);
+  __syncthreads();
+  if (q || i >= a.h.n) return;
+  float m = top;
+  for (int u = 1; u < Q; ++u) m = fmaxf(m, sh[u][r].x);
+  sum = 0.f;
+  for (int u = 0; u < Q; ++u) sum += sh[u][r].y * __builtin_amdgcn_exp2f(sh[u][r].x - m);
+  const float log = __builtin_amdgcn_logf(sum);  // base 2
+  a.lse[i] = pos >= 0 ? (m + log) * kLn2 : 0.f;
+  // the label's score is among those of the maximum, so a loss is not negative
+  if (a.at_label) a.loss[i] = pos >= 0 ? ((m - a.at_label[pos]) + log) * kLn2 : 0.f;
+}
+
+// ---------------------------------------------------------------- distillation
+struct TeacherArgs {
+  Head h;
+  const int64_t* ids;  // [n][top]
+  const char* teacher;
+  int32_t type, top;
+  int64_t rows, pad;
+  float scale;
+  uint8_t* live;
+  int32_t* err;
+  // forward
+  const char* w;
+  int64_t w_stride;
+  float *loss, *logits;
+  const float* lse;
+  // backward
+  const float* logits_in;
+  char* e;
+  int64_t e_cols, v0, piece_rows;
+};
+
+constexpr int kRowsPerGroup = 4;  // tokens of a workgroup, a wave each
+
+__device__ __forceinline__ float teacher_at(const TeacherArgs& a, int64_t i) {
+  if (a.type == FS_F32) return ((const float*)a.teacher)[i];
+  if (a.type == FS_BF16) return (float)((const __bf16*)a.teacher)[i];
+  return (float)((const _Float16*)a.teacher)[i];
+}
+// An entry takes part where its id is a row of the table and not the padding,
+// and its logit is not -inf.
+__device__ __forceinline__ bool entry_on(const TeacherArgs& a, int64_t id, float t) {
+  return id >= 0 && id < a.rows && id != a.pad && t != -INFINITY;
+}
+
+__global__ void __launch_bounds__(kRowsPerGroup * kWave) k_teacher_live(TeacherArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * kRowsPerGroup + threadIdx.x / kWave;
+  if (i >= a.h.n) return;
+  bool on = false, bad = false;
+  for (int k = lane(); k < a.top; k += kWave) {
+    const int64_t id = a.ids[i * a.top + k];
+    bad |= (id < 0 || id >= a.rows) && id != a.pad;
+    on |= entry_on(a, id, teacher_at(a, i * a.top + k));
+  }
+  flag_err(a.err, bad, FS_EF_ID_RANGE);
+  const bool any = __any(on);
+  if (lane() == 0) a.live[i] = any;
+}
+
+constexpr int kPerLane = FS_MAX_TOP / kWave;
+
+// The teacher's distribution over a token's entries, one wave: q and log q of
+// entry lane + 64 u (0 where it takes no part).
+struct Teacher {
+  float q[kPerLane], logq[kPerLane];
+  int64_t id[kPerLane];
+  bool on[kPerLane];
+  __device__ __forceinline__ Teacher(const TeacherArgs& a, int64_t i) {
+    float t[kPerLane], top = -INFINITY, sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < kPerLane; ++u) {
+      const int k = lane() + kWave * u;
+      on[u] = false;
+      id[u] = -1;
+      t[u] = 0.f;
+      if (k < a.top) {
+        id[u] = a.ids[i * a.top + k];
+        const float x = teacher_at(a, i * a.top + k);
+        on[u] = entry_on(a, id[u], x);
+        t[u] = x * a.scale;
+      }
+      if (on[u]) top = fmaxf(top, t[u]);
+    }
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+#pragma unroll
+    for (int u = 0; u < kPerLane; ++u) {
+      t[u] -= top;
+      q[u] = on[u] ? expf(t[u]) : 0.f;
+      sum += q[u];
+    }
+    sum = wave_sum(sum);
+    const float log = logf(sum);
+#pragma unroll
+    for (int u = 0; u < kPerLane; ++u) {
+      logq[u] = on[u] ? t[u] - log : 0.f;
+      q[u] = on[u] ? q[u] / sum : 0.f;
+    }
+  }
+};
+
+// Scores of a token's entries, and its loss. A wave's lanes share the elements
+// of a row; four rows are in flight.
+template <typename T>
+__global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a) {
+  __shared__ float s_z[kRowsPerGroup][FS_MAX_TOP];
+  const int w = threadIdx.x / kWave;
+  const int64_t i = (int64_t)blockIdx.x * kRowsPerGroup + w;
+  if (i >= a.h.n) return;
+  const int32_t pos = a.h.pos[i];
+  const int l = lane();
+  if (pos < 0) {
+    for (int k = l; k < a.top; k += kWave) a.logits[i * a.top + k] = 0.f;
+    if (l == 0) a.loss[i] = 0.f;
+    return;
+  }
+  const Teacher t(a, i);
+  const char* x = a.h.x + (int64_t)pos * a.h.dp * 2;
+  for (int k0 = 0; k0 < a.top; k0 += 4) {
+    const char* row[4];
+    float sum[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const int k = min(k0 + u, a.top - 1);
+      int64_t id = 0;
+      bool on = false;
+#pragma unroll
+      for (int y = 0; y < kPerLane; ++y)
+        if (k / kWave == y) {
+          id = __shfl(t.id[y], k % kWave, kWave);
+          on = __shfl((int)t.on[y], k % kWave, kWave);
+        }
+      row[u] = on ? a.w + id * a.w_stride : nullptr;
+      sum[u] = 0.f;
+    }
+    for (int c = 8 * l; c < a.h.dim; c += 8 * kWave) {
+      const u32x4 xv = *(const u32x4*)(x + 2 * c);
+      u32x4 wv[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) wv[u] = row[u] ? row_piece(row[u], c, a.h.dim) : u32x4{0, 0, 0, 0};
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const auto p = Elem<T>::unpack(xv[e]), y = Elem<T>::unpack(wv[u][e]);
+          sum[u] += p[0] * y[0];
+          sum[u] += p[1] * y[1];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float z = row[u] ? wave_sum(sum[u]) * a.scale : 0.f;
+      if (l == 0 && k0 + u < a.top) s_z[w][k0 + u] = z;
+    }
+  }
+  __builtin_amdgcn_wave_barrier();
+  __threadfence_block();
+  const float lse = a.lse[i];
+  float loss = 0.f;
+#pragma unroll
+  for (int u = 0; u < kPerLane; ++u) {
+    const int k = l + kWave * u;
+    if (k < a.top) {
+      const float z = s_z[w][k];
+      a.logits[i * a.top + k] = z;
+      if (t.on[u] && t.q[u] != 0.f) loss += t.q[u] * (t.logq[u] - z + lse);
+    }
+  }
+  loss = wave_sum(loss);
+  if (l == 0) a.loss[i] = loss;
+}
+
+// The entries' places of e in a piece: target off the softmax before the one
+// rounding. Entries of one id write the same value.
+template <typename T>
+__global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill_entries(TeacherArgs a) {
+  __shared__ int64_t s_id[kRowsPerGroup][FS_MAX_TOP];
+  __shared__ float s_q[kRowsPerGroup][FS_MAX_TOP];
+  const int w = threadIdx.x / kWave, l = lane();
+  const int64_t i = (int64_t)blockIdx.x * kRowsPerGroup + w;
+  if (i >= a.h.n) return;
+  const int32_t pos = a.h.pos[i];
+  if (pos < 0) return;
+  const Teacher t(a, i);
+#pragma unroll
+  for (int u = 0; u < kPerLane; ++u) {
+    s_id[w][l + kWave * u] = t.on[u] ? t.id[u] : -1;
+    s_q[w][l + kWave * u] = t.q[u];
+  }
+  __builtin_amdgcn_wave_barrier();
+  __threadfence_block();
+  const float c = a.h.coef[pos] * a.h.mul[0], lse2 = a.h.lse2[pos];
+#pragma unroll
+  for (int u = 0; u < kPerLane; ++u) {
+    const int64_t v = t.id[u] - a.v0;
+    if (!t.on[u] || v < 0 || v >= a.piece_rows) continue;
+    float q = 0.f;
+    for (int k = 0; k < a.top; ++k) q += s_id[w][k] == t.id[u] ? s_q[w][k] : 0.f;
+    const float z = a.logits_in[i * a.top + l + kWave * u];
+    const float e = (__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -lse2)) - q) * c;
+    ((T*)a.e)[pos * a.e_cols + v] = (T)e;
+  }
+}
+
+// ---------------------------------------------------------------- host
+struct Sizes {
+  int64_t n, rows, npad, vpad, piece, pack_rows, pack_bytes, e_bytes, dx_part, dw_part, tiles;
+  int32_t dim, dp, bn;
+};
+
+int64_t most_parts(int64_t steps) { return std::min<int64_t>(kMostParts, std::max<int64_t>(1, steps / 4)); }
+
+// A product's tiles and steps say in how many parts it is cut: few tiles leave
+// CUs idle, so sums over many steps are cut until about two workgroups a CU are
+// there, at least four steps each, as far as the sums' space goes.
+int32_t parts_of(int64_t tiles, int64_t steps, int64_t bytes_each, int64_t bytes) {
+  const int64_t p = std::min(std::max<int64_t>(1, 512 / std::max<int64_t>(tiles, 1)), most_parts(steps));
+  return (int32_t)std::max<int64_t>(1, std::min(p, bytes / std::max<int64_t>(bytes_each, 1)));
+}
+
+Sizes sizes_of(int64_t n, int64_t rows, int32_t dim) {
+  Sizes s;
+  s.n = n;
+  s.rows = rows;
+  s.dim = dim;
+  s.dp = (int32_t)align_up((size_t)dim, kK);
+  // Tiles of 64 tokens where those of 256 would be few or mostly empty
+  s.bn = n > 128 && cdiv(n, 256) * cdiv(rows, kV) >= 512 ? 256 : 64;
+  s.npad = (int64_t)align_up((size_t)std::max<int64_t>(n, 1), n > 128 ? 256 : 64);
+  s.vpad = (int64_t)align_up((size_t)rows, kV);
+  s.tiles = s.vpad / kV;
+  // e: all of it, or pieces of kPieceBytes, or of one tile's width
+  s.e_bytes = s.npad <= kPieceBytes / 2 / s.vpad ? s.npad * s.vpad * 2 : std::max(kPieceBytes, s.npad * kV * 2);
+  s.piece = std::min(s.vpad, std::max<int64_t>(kV, s.e_bytes / (s.npad * 2) / kV * kV));
+  s.pack_bytes = std::max(std::min(s.vpad * s.dp * 2, kPackBytes), (int64_t)kV * s.dp * 2);
+  s.pack_rows = std::min(s.vpad, std::max<int64_t>(kV, s.pack_bytes / (s.dp * 2) / kV * kV));
+  const int64_t dx = s.npad * s.dp * 4, dw = s.vpad * s.dp * 4;
+  const int64_t x_most = most_parts(s.vpad / kK), w_most = most_parts(s.npad / kK);
+  s.dx_part = std::max(dx, std::min(dx * x_most, kPartBytes));
+  s.dw_part = w_most > 1 ? std::min(dw * w_most, kPartBytes) : 0;
+  return s;
+}
+
+struct Space {
+  Head h;
+  uint8_t* live;
+  char* pack;
+  float2* part;      // forward
+  float* at_label;
+  char* e;           // backward
+  float *dx_part, *dw_part;
+};
+
+size_t carve(void* ws, const Sizes& s, bool back, Space* o) {
+  Carve c(ws);
+  Head& h = o->h;
+  h.n_live = c.take<int32_t>(1);
+  h.mul = c.take<float>(2);
+  h.pos = c.take<int32_t>((size_t)s.npad);
+  h.label = c.take<int32_t>((size_t)s.npad);
+  h.lse2 = c.take<float>((size_t)s.npad);
+  h.coef = c.take<float>((size_t)s.npad);
+  h.x = c.take<char>((size_t)(s.npad * s.dp * 2));
+  o->live = c.take<uint8_t>((size_t)s.npad);
+  o->pack = c.take<char>((size_t)s.pack_bytes);
+  if (back) {
+    o->e = c.take<char>((size_t)s.e_bytes);
+    o->dx_part = c.take<float>((size_t)s.dx_part / 4);
+    o->dw_part = c.take<float>((size_t)s.dw_part / 4);
+  } else {
+    o->part = c.take<float2>((size_t)(s.tiles * s.npad));
+    o->at_label = c.take<float>((size_t)s.npad);
+  }
+  h.n = s.n;
+  h.npad = s.npad;
+  h.dim = s.dim;
+  h.dp = s.dp;
+  return c.used + 512;
+}
+
+void* aligned(void* ws) { return (void*)align_up((size_t)ws, 256); }
+
+// The table as the tiles load it: rows that lie 16-byte aligned as they are.
+struct Table {
+  const char* w;
+  int64_t stride;
+  bool direct;
+};
+
+bool loads_directly(const char* w, int64_t stride, int32_t dim) {
+  return dim % 8 == 0 && stride % 16 == 0 && (uintptr_t)w % 16 == 0 && stride <= ((int64_t)1 << 23);
+}
+
+// rows v0 .. of a table, laid out in `pack` where the tiles cannot load them
+int piece_of(const Table& t, const Sizes& s, int64_t v0, int64_t rows, char* pack, const char** w,
+             int64_t* stride, int32_t* k, hipStream_t stream) {
+  *w = t.w + v0 * t.stride;
+  *stride = t.stride;
+  *k = s.dim;
+  if (t.direct) return FS_OK;
+  const int64_t blocks = std::min<int64_t>(cdiv(rows * (s.dp / 8), kPackThreads), 8192);
+  hipLaunchKernelGGL(k_table_pack, dim3((unsigned)blocks), dim3(kPackThreads), 0, stream, *w, t.stride, rows,
+                     s.dim, s.dp, pack);
+  FS_LAUNCH_CHECK();
+  *w = pack;
+  *stride = 2 * (int64_t)s.dp;
+  *k = s.dp;
+  return FS_OK;
+}
+
+int pack_tokens(PackArgs a, hipStream_t stream) {
+  const int64_t per = std::max<int64_t>(64, cdiv(a.h.n, 256));
+  a.per = (int32_t)per;
+  const int64_t blocks = std::max<int64_t>(1, cdiv(a.h.n, per));
+  hipLaunchKernelGGL(k_head_pack, dim3((unsigned)blocks), dim3(kPackThreads), 0, stream, a);
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
+template <bool Back>
+int launch_scores(const ScoreArgs& a, const Sizes& s, int32_t dtype, hipStream_t stream) {
+  const int64_t grid = (int64_t)a.order.rows * a.order.cols;
+  if (!grid_fits(grid, kThreads)) return FS_ERR_UNSUPPORTED;
+  const dim3 g((unsigned)grid), b(kThreads);
+  if (dtype == FS_BF16) {
+    if (s.bn == 256) hipLaunchKernelGGL((k_scores<__bf16, 256, 2, 4, Back>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((k_scores<__bf16, 64, 8, 1, Back>), g, b, 0, stream, a);
+  } else {
+    if (s.bn == 256) hipLaunchKernelGGL((k_scores<_Float16, 256, 2, 4, Back>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((k_scores<_Float16, 64, 8, 1, Back>), g, b, 0, stream, a);
+  }
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
+template <typename T>
+void launch_grad_x(const SumArgs& a, const Sizes& s, dim3 g, hipStream_t stream) {
+  if (s.bn == 256) hipLaunchKernelGGL((k_grad_x<T, 256, 2, 4>), g, dim3(kThreads), 0, stream, a);
+  else hipLaunchKernelGGL((k_grad_x<T, 64, 8, 1>), g, dim3(kThreads), 0, stream, a);
+}
+
+int launch_join(const JoinArgs& a, int32_t type, hipStream_t stream) {
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(cdiv(a.rows * cdiv(a.dim, 4), 256), 16384));
+  const dim3 g((unsigned)blocks), b(256);
+  if (type == FS_F32) hipLaunchKernelGGL(k_join<float>, g, b, 0, stream, a);
+  else if (type == FS_BF16) hipLaunchKernelGGL(k_join<__bf16>, g, b, 0, stream, a);
+  else hipLaunchKernelGGL(k_join<_Float16>, g, b, 0, stream, a);
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
+// What both losses' calls are checked for alike.
+int check(const void* x, int64_t* x_stride, int64_t n, const fs_table* table, float scale, Table* t) {
+  if (!table || n < 0 || n >= (int64_t)INT32_MAX - 256 || table->rows < 1 || table->dim < 1 ||
+      !attn::scale_ok(scale))
+    return FS_ERR_INVALID_ARG;
+  if ((table->dtype != FS_BF16 && table->dtype != FS_F16) || table->dim > FS_MAX_TOKEN_DIM ||
+      table->rows >= (int64_t)INT32_MAX - 256)
+    return FS_ERR_UNSUPPORTED;
+  const int64_t row = 2 * (int64_t)table->dim;
+  if (!*x_stride) *x_stride = row;
+  t->w = (const char*)table->weights;
+  t->stride = table->stride ? table->stride : row;
+  if (*x_stride < row || *x_stride % 2 || t->stride < row || t->stride % 2 || !t->w || (uintptr_t)t->w % 2 ||
+      (n > 0 && (!x || (uintptr_t)x % 2)))
+    return FS_ERR_INVALID_ARG;
+  t->direct = loads_directly(t->w, t->stride, table->dim);
+  return FS_OK;
+}
+
+// lse (and the losses of labels) of the packed tokens
+int forward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float scale, bool labels,
+            float* loss, float* lse, hipStream_t stream) {
+  int rc;
+  const int64_t step = t.direct ? s.vpad : s.pack_rows;
+  for (int64_t v0 = 0; v0 < s.rows; v0 += step) {
+    ScoreArgs a = {};
+    a.h = o.h;
+    a.v0 = v0;
+    a.rows = std::min(step, s.rows - v0);
+    a.v_tile0 = (int32_t)(v0 / kV);
+    if ((rc = piece_of(t, s, v0, a.rows, o.pack, &a.w, &a.w_stride, &a.k, stream))) return rc;
+    a.order = Order{(int32_t)cdiv(s.n, s.bn), (int32_t)cdiv(a.rows, kV)};
+    a.scale2 = scale * kLog2e;
+    a.part = o.part;
+    a.at_label = o.at_label;
+    if ((rc = launch_scores<false>(a, s, dtype, stream))) return rc;
+  }
+  const LossArgs l{o.h, o.part, s.tiles, labels ? o.at_label : nullptr, loss, lse};
+  if (s.n < 2048) hipLaunchKernelGGL(k_loss<4>, dim3((unsigned)cdiv(s.n, 4)), dim3(256), 0, stream, l);
+  else hipLaunchKernelGGL(k_loss<16>, dim3((unsigned)cdiv(s.n, 16)), dim3(256), 0, stream, l);
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
+struct Grads {
+  void* dx;
+  int64_t dx_stride;
+  void* dw;
+  int32_t dw_type;
+  int64_t dw_stride;
+};
+
+int check_grads(Grads* g, int64_t n, int32_t dim) {
+  if (g->dw_type != FS_F32 && g->dw_type != FS_BF16 && g->dw_type != FS_F16) return FS_ERR_INVALID_ARG;
+  const int32_t e = g->dw_type == FS_F32 ? 4 : 2;
+  if (!g->dx_stride) g->dx_stride = 2 * (int64_t)dim;
+  if (!g->dw_stride) g->dw_stride = e * (int64_t)dim;
+  if (g->dx_stride < 2 * (int64_t)dim || g->dx_stride % 2 || (uintptr_t)g->dx % 2 ||
+      g->dw_stride < e * (int64_t)dim || g->dw_stride % e || (uintptr_t)g->dw % e || (!g->dx && !g->dw))
+    return FS_ERR_INVALID_ARG;
+  return FS_OK;
+}
+
+int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float scale, const Grads& g,
+             TeacherArgs* entries, hipStream_t stream) {
+  int rc;
+  const int64_t step = t.direct ? s.piece : std::min(s.piece, s.pack_rows);
+  const int32_t token_tiles = (int32_t)cdiv(s.n, s.bn), col_tiles = (int32_t)cdiv(s.dim, kD);
+  const int32_t x_parts = parts_of((int64_t)token_tiles * col_tiles, cdiv(std::min(step, s.rows), kK),
+                                   s.npad * s.dp * 4, s.dx_part);
+  for (int64_t v0 = 0; v0 < s.rows; v0 += step) {
+    ScoreArgs a = {};
+    a.h = o.h;
+    a.v0 = v0;
+    a.rows = std::min(step, s.rows - v0);
+    a.e = o.e;
+    a.e_cols = (int64_t)align_up((size_t)a.rows, kV);
+    if ((rc = piece_of(t, s, v0, a.rows, o.pack, &a.w, &a.w_stride, &a.k, stream))) return rc;
+    const int32_t table_tiles = (int32_t)cdiv(a.rows, kV);
+    a.order = Order{token_tiles, table_tiles};
+    a.scale2 = scale * kLog2e;
+    if (s.n > 0) {
+      if ((rc = launch_scores<true>(a, s, dtype, stream))) return rc;
+      if (entries) {
+        entries->e = a.e;
+        entries->e_cols = a.e_cols;
+        entries->v0 = v0;
+        entries->piece_rows = a.rows;
+        const dim3 grid((unsigned)cdiv(s.n, kRowsPerGroup)), block(kRowsPerGroup * kWave);
+        if (dtype == FS_BF16) hipLaunchKernelGGL(k_distill_entries<__bf16>, grid, block, 0, stream, *entries);
+        else hipLaunchKernelGGL(k_distill_entries<_Float16>, grid, block, 0, stream, *entries);
+        FS_LAUNCH_CHECK();
+      }
+    }
+    SumArgs b = {};
+    b.h = o.h;
+    b.w = a.w;
+    b.w_stride = a.w_stride;
+    b.rows = a.rows;
+    b.w_cols = a.k;
+    b.e = a.e;
+    b.e_cols = a.e_cols;
+    if (g.dx && s.n > 0) {
+      b.order = Order{token_tiles, col_tiles};
+      b.parts = x_parts;
+      b.steps = (int32_t)cdiv(cdiv(a.rows, kK), x_parts);
+      b.add = v0 > 0;
+      b.part = o.dx_part;
+      const int64_t grid = (int64_t)token_tiles * col_tiles * x_parts;
+      if (!grid_fits(grid, kThreads)) return FS_ERR_UNSUPPORTED;
+      if (dtype == FS_BF16) launch_grad_x<__bf16>(b, s, dim3((unsigned)grid), stream);
+      else launch_grad_x<_Float16>(b, s, dim3((unsigned)grid), stream);
+      FS_LAUNCH_CHECK();
+    }
+    if (g.dw) {
+      const int64_t tiles = (int64_t)table_tiles * col_tiles;
+      const int32_t parts = parts_of(tiles, cdiv(s.n, kK), a.rows * s.dp * 4, s.dw_part);
+      b.order = Order{table_tiles, col_tiles};
+      b.parts = parts;
+      b.add = 0;
+      b.part = parts > 1 ? o.dw_part : nullptr;
+      b.out = (char*)g.dw + v0 * g.dw_stride;
+      b.out_stride = g.dw_stride;
+      b.out_rows = a.rows;
+      b.out_type = g.dw_type;
+      if (!grid_fits(tiles * parts, kThreads)) return FS_ERR_UNSUPPORTED;
+      const dim3 grid((unsigned)(tiles * parts)), block(kThreads);
+      if (dtype == FS_BF16) hipLaunchKernelGGL(k_grad_w<__bf16>, grid, block, 0, stream, b);
+      else hipLaunchKernelGGL(k_grad_w<_Float16>, grid, block, 0, stream, b);
+      FS_LAUNCH_CHECK();
+      if (parts > 1) {
+        const JoinArgs j{o.dw_part, a.rows, parts, s.dp, s.dim, nullptr, a.rows, o.h.mul, b.out, g.dw_stride};
+        if ((rc = launch_join(j, g.dw_type, stream))) return rc;
+      }
+    }
+  }
+  if (g.dx && s.n > 0) {
+    const JoinArgs j{o.dx_part, s.npad, x_parts, s.dp, s.dim, o.h.pos, s.n, o.h.mul, (char*)g.dx, g.dx_stride};
+    if ((rc = launch_join(j, dtype, stream))) return rc;
+  }
+  return FS_OK;
+}
+
+// a grid of any launch of a call, by its sizes
+bool too_many(const Sizes& s) {
+  return !grid_fits(cdiv(s.npad, 64) * s.tiles, kThreads) || !grid_fits(s.npad, 64);
+}
+
+PackArgs pack_args(const Space& o, const Sizes& s, const void* x, int64_t x_stride, const int64_t* labels,
+                   int64_t padding_id, float scale, int32_t dtype, int32_t* err) {
+  PackArgs p = {};
+  p.h = o.h;
+  p.x = (const char*)x;
+  p.x_stride = x_stride;
+  p.labels = labels;
+  p.live = o.live;
+  p.rows = s.rows;
+  p.pad = padding_id;
+  p.scale = scale;
+  p.pad_to = s.bn;
+  p.narrow = dtype == FS_F16;
+  p.err = err;
+  return p;
+}
+
+bool top_ok(int32_t top, int32_t type) {
+  return top >= 1 && (type == FS_F32 || type == FS_BF16 || type == FS_F16);
+}
+
+TeacherArgs teacher_args(const Space& o, const Sizes& s, const int64_t* ids, int32_t top, const void* teacher,
+                         int32_t type, float scale, int64_t padding_id, int32_t* err) {
+  TeacherArgs t = {};
+  t.h = o.h;
+  t.ids = ids;
+  t.teacher = (const char*)teacher;
+  t.type = type;
+  t.top = top;
+  t.rows = s.rows;
+  t.pad = padding_id;
+  t.scale = scale;
+  t.live = o.live;
+  t.err = err;
+  return t;
+}
+
+int teacher_live(const TeacherArgs& t, hipStream_t stream) {
+  hipLaunchKernelGGL(k_teacher_live, dim3((unsigned)cdiv(t.h.n, kRowsPerGroup)), dim3(kRowsPerGroup * kWave), 0,
+                     stream, t);
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
+}  // namespace
+}  // namespace fs
+
+using namespace fs;
+
+extern "C" size_t fs_token_loss_workspace_size(int64_t n, int64_t rows, int32_t dim) {
+  if (n < 0 || rows < 1 || dim < 1) return 0;
+  Space o;
+  return carve(nullptr, sizes_of(n, rows, dim), false, &o);
+}
+
+extern "C" size_t fs_token_loss_backward_workspace_size(int64_t n, int64_t rows, int32_t dim) {
+  if (n < 0 || rows < 1 || dim < 1) return 0;
+  Space o;
+  return carve(nullptr, sizes_of(n, rows, dim), true, &o);
+}
+
+extern "C" int fs_token_loss(const void* x, int64_t x_stride, int64_t n, const fs_table* table,
+                             const int64_t* labels, float scale, int64_t padding_id, float* loss,
+                             float* lse, int32_t* err, void* ws, size_t ws_bytes, hipStream_t stream) {
+  Table t;
+  int rc;
+  if ((rc = check(x, &x_stride, n, table, scale, &t))) return rc;
+  if (n > 0 && (!labels || !loss || !lse)) return FS_ERR_INVALID_ARG;
+  const Sizes s = sizes_of(n, table->rows, table->dim);
+  if (too_many(s)) return FS_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < fs_token_loss_workspace_size(n, table->rows, table->dim)) return FS_ERR_WORKSPACE;
+  if (n == 0) return FS_OK;
+  Space o;
+  carve(aligned(ws), s, false, &o);
+  if ((rc = pack_tokens(pack_args(o, s, x, x_stride, labels, padding_id, scale, table->dtype, err), stream)))
+    return rc;
+  return forward(s, o, t, table->dtype, scale, true, loss, lse, stream);
+}
+
+extern "C" int fs_token_loss_backward(const void* x, int64_t x_stride, int64_t n, const fs_table* table,
+                                      const int64_t* labels, const float* lse, const float* dloss,
+                                      float scale, int64_t padding_id, void* dx, int64_t dx_stride,
+                                      void* dweight, int32_t dweight_dtype, int64_t dweight_stride,
+                                      int32_t* err, void* ws, size_t ws_bytes, hipStream_t stream) {
+  Table t;
+  int rc;
+  Grads g{dx, dx_stride, dweight, dweight_dtype, dweight_stride};
+  if ((rc = check(x, &x_stride, n, table, scale, &t)) || (rc = check_grads(&g, n, table->dim))) return rc;
+  if (n > 0 && (!labels || !lse || !dloss)) return FS_ERR_INVALID_ARG;
+  const Sizes s = sizes_of(n, table->rows, table->dim);
+  if (too_many(s)) return FS_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < fs_token_loss_backward_workspace_size(n, table->rows, table->dim))
+    return FS_ERR_WORKSPACE;
+  Space o;
+  carve(aligned(ws), s, true, &o);
+  PackArgs p = pack_args(o, s, x, x_stride, labels, padding_id, scale, table->dtype, err);
+  p.lse = lse;
+  p.dloss = dloss;
+  p.back = 1;
+  if ((rc = pack_tokens(p, stream))) return rc;
+  return backward(s, o, t, table->dtype, scale, g, nullptr, stream);
+}
+
+extern "C" int fs_token_distill(const void* x, int64_t x_stride, int64_t n, const fs_table* table,
+                                const int64_t* ids, int32_t top, const void* teacher,
+                                int32_t teacher_dtype, float scale, int64_t padding_id, float* loss,
+                                float* lse, float* logits, int32_t* err, void* ws, size_t ws_bytes,
+                                hipStream_t stream) {
+  Table t;
+  int rc;
+  if ((rc = check(x, &x_stride, n, table, scale, &t))) return rc;
+  if (!top_ok(top, teacher_dtype)) return FS_ERR_INVALID_ARG;
+  if (top > FS_MAX_TOP) return FS_ERR_UNSUPPORTED;
+  if (n > 0 && (!ids || !teacher || !loss || !lse || !logits)) return FS_ERR_INVALID_ARG;
+  const Sizes s = sizes_of(n, table->rows, table->dim);
+  if (too_many(s)) return FS_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < fs_token_loss_workspace_size(n, table->rows, table->dim)) return FS_ERR_WORKSPACE;
+  if (n == 0) return FS_OK;
+  Space o;
+  carve(aligned(ws), s, false, &o);
+  TeacherArgs a = teacher_args(o, s, ids, top, teacher, teacher_dtype, scale, padding_id, err);
+  if ((rc = teacher_live(a, stream)) ||
+      (rc = pack_tokens(pack_args(o, s, x, x_stride, nullptr, padding_id, scale, table->dtype, err), stream)) ||
+      (rc = forward(s, o, t, table->dtype, scale, false, loss, lse, stream)))
+    return rc;
+  a.w = t.w;
+  a.w_stride = t.stride;
+  a.loss = loss;
+  a.logits = logits;
+  a.lse = lse;
+  const dim3 grid((unsigned)cdiv(n, kRowsPerGroup)), block(kRowsPerGroup * kWave);
+  if (table->dtype == FS_BF16) hipLaunchKernelGGL(k_distill<__bf16>, grid, block, 0, stream, a);
+  else hipLaunchKernelGGL(k_distill<_Float16>, grid, block, 0, stream, a);
+  FS_LAUNCH_CHECK();
+  return FS_OK;
+}
+
+extern "C" int fs_token_distill_backward(const void* x, int64_t x_stride, int64_t n, const fs_table* table,
+                                         const int64_t* ids, int32_t top, const void* teacher,
+                                         int32_t teacher_dtype, const float* lse, const float* logits,
+                                         const float* dloss, float scale, int64_t padding_id, void* dx,
+                                         int64_t dx_stride, void* dweight, int32_t dweight_dtype,
+                                         int64_t dweight_stride, int32_t* err, void* ws,
+                                         size_t ws_bytes, hipStream_t stream) {
+  Table t;
+  int rc;
+  Grads g{dx, dx_stride, dweight, dweight_dtype, dweight_stride};
+  if ((rc = check(x, &x_stride, n, table, scale, &t)) || (rc = check_grads(&g, n, table->dim))) return rc;
+  if (!top_ok(top, teacher_dtype)) return FS_ERR_INVALID_ARG;
+  if (top > FS_MAX_TOP) return FS_ERR_UNSUPPORTED;
+  if (n > 0 && (!ids || !teacher || !lse || !logits || !dloss)) return FS_ERR_INVALID_ARG;
+  const Sizes s = sizes_of(n, table->rows, table->dim);
+  if (too_many(s)) return FS_ERR_UNSUPPORTED;
+  if (!ws || ws_bytes < fs_token_loss_backward_workspace_size(n, table->rows, table->dim))
+    return FS_ERR_WORKSPACE;
+  Space o;
+  carve(aligned(ws), s, true, &o);
+  TeacherArgs a = teacher_args(o, s, ids, top, teacher, teacher_dtype, scale, padding_id, err);
+  a.logits_in = logits;
+  if (n > 0 && (rc = teacher_live(a, stream))) return rc;
+  PackArgs p = pack_args(o, s, x, x_stride, nullptr, padding_id, scale, table->dtype, err);
+  p.lse = lse;
+  p.dloss = dloss;
+  p.back = 1;
+  if ((rc = pack_tokens(p, stream))) return rc;
+  return backward(s, o, t, table->dtype, scale, g, &a, stream);
+}

@@ -29,7 +29,7 @@ FS_SGD, FS_RW_ADAGRAD = 0, 1
 FS_ALL, FS_EXCLUSIVE, FS_COLLISION = -1, 0, 1
 FS_ROWS_FEW, FS_ROWS_MANY, FS_ROWS_ALL = 1, 2, 3
 FS_MAX_SAMPLES, FS_MAX_RANKS, FS_MAX_TABLES, FS_MAX_UIH = 16384, 1024, 8, 65535
-FS_MAX_TOKEN_DIM, FS_MAX_HEADS, FS_MAX_NORM_DIM = 65536, 1024, 16384
+FS_MAX_TOKEN_DIM, FS_MAX_HEADS, FS_MAX_NORM_DIM, FS_MAX_TOP = 65536, 1024, 16384, 256
 
 if not os.path.exists(LIB_PATH):
     raise ImportError(f"{LIB_PATH} is not built: run `python __graft_entry__.py build` "
@@ -109,6 +109,16 @@ _c_layer_norm = _sig("fs_layer_norm", C.c_int, _P, _i32, _i64, _i64, _i32, _P, _
 _c_layer_norm_bwd = _sig("fs_layer_norm_backward", C.c_int, _P, _i32, _i64, _i64, _i32, _P, _P, _P,
                          _i32, _i64, _P, _i32, _P, _i64, _P, _P, _P, _sz, _P)
 _c_layer_norm_bwd_ws = _sig("fs_layer_norm_backward_workspace_size", _sz, _i64, _i32)
+_c_token_loss = _sig("fs_token_loss", C.c_int, _P, _i64, _i64, _TP, _P, _f, _i64, _P, _P, _P, _P, _sz,
+                     _P)
+_c_token_loss_bwd = _sig("fs_token_loss_backward", C.c_int, _P, _i64, _i64, _TP, _P, _P, _P, _f, _i64,
+                         _P, _i64, _P, _i32, _i64, _P, _P, _sz, _P)
+_c_token_distill = _sig("fs_token_distill", C.c_int, _P, _i64, _i64, _TP, _P, _i32, _P, _i32, _f, _i64,
+                        _P, _P, _P, _P, _P, _sz, _P)
+_c_token_distill_bwd = _sig("fs_token_distill_backward", C.c_int, _P, _i64, _i64, _TP, _P, _i32, _P,
+                            _i32, _P, _P, _P, _f, _i64, _P, _i64, _P, _i32, _i64, _P, _P, _sz, _P)
+_c_token_loss_ws = _sig("fs_token_loss_workspace_size", _sz, _i64, _i64, _i32)
+_c_token_loss_bwd_ws = _sig("fs_token_loss_backward_workspace_size", _sz, _i64, _i64, _i32)
 _c_strerror = _sig("fs_strerror", C.c_char_p, C.c_int)
 _c_version = _sig("fs_version", C.c_int)
 
@@ -124,6 +134,8 @@ EXPORTED = ["fs_balance_fbs", "fs_balance_vbs", "fs_balance_workspace_size",
             "fs_jagged_attention", "fs_jagged_attention_workspace_size",
             "fs_jagged_attention_backward", "fs_jagged_attention_backward_workspace_size",
             "fs_layer_norm", "fs_layer_norm_backward", "fs_layer_norm_backward_workspace_size",
+            "fs_token_loss", "fs_token_loss_backward", "fs_token_distill", "fs_token_distill_backward",
+            "fs_token_loss_workspace_size", "fs_token_loss_backward_workspace_size",
             "fs_strerror", "fs_version"]
 
 
@@ -823,6 +835,136 @@ def fs_layer_norm_backward(x, mean, rstd, dout, weight=None, dx=None, dweight=No
                              _dtype(dout.dtype), ostride, _ptr(weight), _dtype(param), gptr, gstride,
                              _ptr(dweight), _ptr(dbias), _ptr(ws), _nbytes(ws), _stream(stream)))
     return dx, dweight, dbias
+
+
+# ---------------------------------------------------------------------------- token losses
+
+
+def token_loss_workspace_size(n, rows, dim):
+    return int(_c_token_loss_ws(n, rows, dim))
+
+
+def token_loss_backward_workspace_size(n, rows, dim):
+    return int(_c_token_loss_bwd_ws(n, rows, dim))
+
+
+def _scored(x, weight):
+    """(pointer and stride of x's rows, n, fs_table of the weight)"""
+    assert x.dim() == 2 and weight.dim() == 2 and x.shape[1] == weight.shape[1]
+    assert x.dtype == weight.dtype, "the tokens are in the table's type"
+    tab = FsTable()
+    tab.weights, tab.stride = _own_rows_ptr(weight)
+    tab.rows, tab.dim, tab.dtype = weight.shape[0], weight.shape[1], _dtype(weight.dtype)
+    return _own_rows_ptr(x), x.shape[0], tab
+
+
+def _targets(ids, teacher, n):
+    assert ids.dtype == torch.int64 and ids.dim() == 2 and ids.shape[0] == n
+    assert teacher.shape == ids.shape
+    return ids.shape[1]
+
+
+def _loss_grads(x, weight, dtype, dx, dweight, d):
+    """The gradients of a loss and their C arguments: False in the place of one
+    leaves it out."""
+    if dweight is not None and dweight is not False:
+        dtype = dtype or dweight.dtype
+    dx = None if dx is False else _out(dx, x.shape, x.dtype, d)
+    dweight = None if dweight is False else _out(dweight, weight.shape, dtype or weight.dtype, d)
+    xptr, xstride = (None, 0) if dx is None else _own_rows_ptr(dx)
+    wptr, wstride = (None, 0) if dweight is None else _own_rows_ptr(dweight)
+    return dx, dweight, (xptr, xstride, wptr, FS_F32 if dweight is None else _dtype(dweight.dtype), wstride)
+
+
+def _per_token(n, *tensors):
+    for t in tensors:
+        assert t.dtype == torch.float32 and t.shape == (n,), "one fp32 number a token"
+
+
+@_allocates
+def fs_token_loss(x, weight, labels, scale=1.0, padding_id=-1, loss=None, lse=None, err=None, ws=None,
+                  stream=None):
+    """Softmax cross entropy of the tokens x [n, dim] against the table weight
+    [rows, dim] (both bf16 or fp16, rows contiguous, any row stride): with z =
+    scale x weight^T, lse = logsumexp(z), loss = lse - z[labels]. labels: int64
+    [n]; tokens with padding_id take no part (loss and lse 0), nor do those whose
+    label is outside the table (FS_EF_ID_RANGE). Returns loss and lse, fp32 [n].
+    The logits are never stored."""
+    d = _here(x, weight, labels, loss, lse, err, ws)
+    (xptr, xstride), n, tab = _scored(x, weight)
+    assert labels.dtype == torch.int64 and labels.shape == (n,)
+    loss, lse = (_out(t, (n,), torch.float32, d) for t in (loss, lse))
+    ws = _space(token_loss_workspace_size(n, tab.rows, tab.dim), ws)
+    _check("fs_token_loss",
+           _c_token_loss(xptr, xstride, n, C.byref(tab), _ptr(labels), float(scale), int(padding_id),
+                         _ptr(loss), _ptr(lse), _ptr(err), _ptr(ws), _nbytes(ws), _stream(stream)))
+    return loss, lse
+
+
+@_allocates
+def fs_token_loss_backward(x, weight, labels, lse, dloss, scale=1.0, padding_id=-1, dtype=None, dx=None,
+                           dweight=None, err=None, ws=None, stream=None):
+    """Gradients (dx, dweight) of fs_token_loss from its lse and the gradients
+    dloss (fp32 [n]) of its losses; the other arguments are the forward call's.
+    dx is in x's type, dweight in `dtype` (weight's by default). dx=False or
+    dweight=False leaves that one out (None is returned for it)."""
+    given = [t for t in (dx, dweight) if t is not False]
+    d = _here(x, weight, labels, lse, dloss, *given, err, ws)
+    (xptr, xstride), n, tab = _scored(x, weight)
+    assert labels.dtype == torch.int64 and labels.shape == (n,)
+    _per_token(n, lse, dloss)
+    dx, dweight, grads = _loss_grads(x, weight, dtype, dx, dweight, d)
+    ws = _space(token_loss_backward_workspace_size(n, tab.rows, tab.dim), ws)
+    _check("fs_token_loss_backward",
+           _c_token_loss_bwd(xptr, xstride, n, C.byref(tab), _ptr(labels), _ptr(lse), _ptr(dloss),
+                             float(scale), int(padding_id), *grads, _ptr(err), _ptr(ws), _nbytes(ws),
+                             _stream(stream)))
+    return dx, dweight
+
+
+@_allocates
+def fs_token_distill(x, weight, ids, teacher, scale=1.0, padding_id=-1, loss=None, lse=None, logits=None,
+                     err=None, ws=None, stream=None):
+    """Distillation of the tokens x [n, dim] (as fs_token_loss takes them) from a
+    teacher's top logits: teacher [n, top] (fp32, bf16 or fp16) at the rows ids
+    (int64 [n, top]). With z = scale x weight^T (scale: one over the temperature)
+    and q the softmax of scale teacher over a token's entries, loss = sum q (log q
+    - z[ids] + lse). Entries with padding_id or a logit of -inf take no part, nor
+    do those outside the table (FS_EF_ID_RANGE). Returns loss and lse, fp32 [n],
+    and logits, fp32 [n, top], z at the entries."""
+    d = _here(x, weight, ids, teacher, loss, lse, logits, err, ws)
+    (xptr, xstride), n, tab = _scored(x, weight)
+    top = _targets(ids, teacher, n)
+    loss, lse = (_out(t, (n,), torch.float32, d) for t in (loss, lse))
+    logits = _out(logits, (n, top), torch.float32, d)
+    ws = _space(token_loss_workspace_size(n, tab.rows, tab.dim), ws)
+    _check("fs_token_distill",
+           _c_token_distill(xptr, xstride, n, C.byref(tab), _ptr(ids), top, _ptr(teacher),
+                            _dtype(teacher.dtype), float(scale), int(padding_id), _ptr(loss), _ptr(lse),
+                            _ptr(logits), _ptr(err), _ptr(ws), _nbytes(ws), _stream(stream)))
+    return loss, lse, logits
+
+
+@_allocates
+def fs_token_distill_backward(x, weight, ids, teacher, lse, logits, dloss, scale=1.0, padding_id=-1,
+                              dtype=None, dx=None, dweight=None, err=None, ws=None, stream=None):
+    """Gradients (dx, dweight) of fs_token_distill from its lse and logits and the
+    gradients dloss (fp32 [n]) of its losses, as fs_token_loss_backward returns
+    them; the other arguments are the forward call's."""
+    given = [t for t in (dx, dweight) if t is not False]
+    d = _here(x, weight, ids, teacher, lse, logits, dloss, *given, err, ws)
+    (xptr, xstride), n, tab = _scored(x, weight)
+    top = _targets(ids, teacher, n)
+    _per_token(n, lse, dloss)
+    assert logits.dtype == torch.float32 and logits.shape == ids.shape
+    dx, dweight, grads = _loss_grads(x, weight, dtype, dx, dweight, d)
+    ws = _space(token_loss_backward_workspace_size(n, tab.rows, tab.dim), ws)
+    _check("fs_token_distill_backward",
+           _c_token_distill_bwd(xptr, xstride, n, C.byref(tab), _ptr(ids), top, _ptr(teacher),
+                                _dtype(teacher.dtype), _ptr(lse), _ptr(logits), _ptr(dloss), float(scale),
+                                int(padding_id), *grads, _ptr(err), _ptr(ws), _nbytes(ws),
+                                _stream(stream)))
+    return dx, dweight
 
 
 # ---------------------------------------------------------------------------- prepared calls
