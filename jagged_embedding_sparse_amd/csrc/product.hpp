@@ -16,6 +16,8 @@
 // before they are waited for.
 #pragma once
 
+#include <type_traits>
+
 #include "attention.hpp"
 
 namespace fs {
@@ -28,41 +30,33 @@ using attn::u32x2;
 using attn::u32x4;
 
 constexpr int kK = 64;        // k's of a step
-constexpr int kWaves = 8;
-constexpr int kThreads = kWaves * kWave;
 
 typedef __attribute__((address_space(3))) uint16_t* lds_ptr;
 
-// 16 bytes per lane from base + at to LDS address `to` + 16 lane, for N loads
-// whose LDS addresses are `step` apart. M0 is put back: the compiler does not let
-// an asm declare that it changes it.
-template <int N>
-__device__ __forceinline__ void load_pieces(const char* base, const uint32_t (&at)[N], uint32_t to,
-                                            uint32_t step) {
-#pragma unroll
-  for (int x = 0; x < N; ++x) {
-    uint32_t m0;
-    asm volatile(
-        "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\t"
-        "s_mov_b32 m0, %0"
-        : "=&s"(m0)
-        : "s"(to + x * step), "v"(at[x]), "s"(base)
-        : "memory");
-  }
+// 16 bytes per lane from base + at to LDS address `to` + 16 lane. M0 is put back:
+// the compiler does not let an asm declare that it changes it.
+__device__ __forceinline__ void load_piece(const char* base, uint32_t at, uint32_t to) {
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %2, %3\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(to), "v"(at), "s"(base)
+      : "memory");
 }
 
 // k's together: a tile of R rows and 64 k's, rows of 128 bytes.
-template <int R>
+template <int R, int NT>
 struct Rows {
   static constexpr int kElems = R * kK;
-  static constexpr int kPer = R * 8 / kThreads;  // loads of a thread
-  static_assert(kPer >= 1 && R * 8 % kThreads == 0, "whole pieces per thread");
+  static constexpr int kPer = R * 8 / NT;  // loads of a thread
+  static_assert(kPer >= 1 && R * 8 % NT == 0, "whole pieces per thread");
   const char* base;  // of the tile's first row, at the next step's first k
   uint32_t at[kPer];
   uint32_t row_bytes;
   int32_t last;
 
-  static __device__ __forceinline__ int row_of(int x) { return x * (kThreads / 8) + (int)threadIdx.x / 8; }
+  static __device__ __forceinline__ int row_of(int x) { return x * (NT / 8) + (int)threadIdx.x / 8; }
   static __device__ __forceinline__ int piece_of() {
     return ((int)threadIdx.x % 8) ^ attn::swz<kK>((int)threadIdx.x / 8);
   }
@@ -79,10 +73,11 @@ struct Rows {
 #pragma unroll
     for (int x = 0; x < kPer; ++x) at[x] = (uint32_t)min(row_of(x), last) * row_bytes + 16 * p;
   }
-  __device__ __forceinline__ void load(uint32_t tile) {
-    load_pieces(base, at, tile + attn::wave_id() * (kWave * 16), kThreads * 16);
-    base = attn::uniform(base + kK * 2);
+  // piece x of the next step's tile; then the step after it
+  __device__ __forceinline__ void load(uint32_t tile, int x) const {
+    load_piece(base, at[x], tile + attn::wave_id() * (kWave * 16) + x * NT * 16);
   }
+  __device__ __forceinline__ void advance() { base = attn::uniform(base + kK * 2); }
   // rows r0 .. r0 + 31 (a multiple of 32), k's 16 kk ..
   struct Read {
     int rows_at;
@@ -95,21 +90,21 @@ struct Rows {
 
 // k's apart: a tile of 64 k's, rows of R elements. Piece p of row r lies at
 // p ^ ((r & 3) << 2 | (r >> 2) & 3): see attention.hpp.
-template <int R>
+template <int R, int NT>
 struct Cols {
   static constexpr int kElems = R * kK;
   static constexpr int kPieces = R / 8;
-  static constexpr int kPer = R * 8 / kThreads;
-  static constexpr int kStepRows = kThreads / kPieces;
-  static_assert(kPer >= 1 && R * 8 % kThreads == 0 && kStepRows % 16 == 0, "a thread's rows share the permutation");
+  static constexpr int kPer = R * 8 / NT;
+  static constexpr int kStepRows = NT / kPieces;
+  static_assert(kPer >= 1 && R * 8 % NT == 0 && NT % kPieces == 0, "whole rows per step");
   const char* base;  // of the next step's first row, at the tile's first column
   uint32_t at[kPer];
   uint32_t row_bytes;
   int32_t cols;
 
   static __device__ __forceinline__ int row_of(int x) { return x * kStepRows + (int)threadIdx.x / kPieces; }
-  static __device__ __forceinline__ int piece_of() {
-    return ((int)threadIdx.x % kPieces) ^ attn::swz<128>((int)threadIdx.x / kPieces);
+  static __device__ __forceinline__ int piece_of(int x) {
+    return ((int)threadIdx.x % kPieces) ^ attn::swz<128>(row_of(x));
   }
   // columns col0 .. of `cols_` (a multiple of 8); pieces past the last load the tile's first
   __device__ __forceinline__ Cols(const char* p, int64_t stride, int64_t col0, int64_t cols_, int64_t k0) {
@@ -120,15 +115,15 @@ struct Cols {
   }
   // rows past `left` load the step's first
   __device__ __forceinline__ void limit(int left) {
-    const int p = 8 * piece_of() < cols ? piece_of() : 0;
 #pragma unroll
     for (int x = 0; x < kPer; ++x)
-      at[x] = (row_of(x) < left ? (uint32_t)row_of(x) * row_bytes : 0u) + 16 * p;
+      at[x] = (row_of(x) < left ? (uint32_t)row_of(x) * row_bytes : 0u) +
+              (8 * piece_of(x) < cols ? 16 * piece_of(x) : 0);
   }
-  __device__ __forceinline__ void load(uint32_t tile) {
-    load_pieces(base, at, tile + attn::wave_id() * (kWave * 16), kThreads * 16);
-    base = attn::uniform(base + (int64_t)kK * row_bytes);
+  __device__ __forceinline__ void load(uint32_t tile, int x) const {
+    load_piece(base, at[x], tile + attn::wave_id() * (kWave * 16) + x * NT * 16);
   }
+  __device__ __forceinline__ void advance() { base = attn::uniform(base + (int64_t)kK * row_bytes); }
   struct Read {
     int cols_at;
     __device__ __forceinline__ Read() {
@@ -151,9 +146,10 @@ struct Cols {
 // (mi, ni) is column m = m_of(mi) + 8 (i / 4) + i % 4 of row n = n_of(ni).
 template <typename T, typename A, typename B, int BM, int BN, int WM, int WN>
 struct Tile {
+  static constexpr int kThreads = WM * WN * kWave;
   static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
   static constexpr int kStage = (BM + BN) * kK;  // elements
-  static_assert(WM * WN == kWaves && MI >= 1 && NI >= 1, "eight waves");
+  static_assert(MI >= 1 && NI >= 1, "whole blocks");
   f32x16 acc[MI][NI];
 
   static __device__ __forceinline__ int m_of(int mi) {
@@ -166,24 +162,25 @@ struct Tile {
   struct Operands {
     u32x4 a[MI], b[NI];
   };
+  // operand x of a chunk, in the order in which the products ask for them
+  static constexpr int kOperands = MI + NI, kProducts = MI * NI, kLoads = A::kPer + B::kPer;
   __device__ __forceinline__ void read(Operands& o, const typename A::Read& ra, const typename B::Read& rb,
-                                       const uint16_t* stage, int kk) const {
+                                       const uint16_t* stage, int kk, int x) const {
     const int w = attn::wave_id();
-#pragma unroll
-    for (int i = 0; i < NI; ++i) o.b[i] = rb(stage + BM * kK, (w / WM * NI + i) * 32, kk);
-#pragma unroll
-    for (int i = 0; i < MI; ++i) o.a[i] = ra(stage, (w % WM * MI + i) * 32, kk);
+    if (x > 0 && x <= NI) o.b[x - 1] = rb(stage + BM * kK, (w / WM * NI + x - 1) * 32, kk);
+    else o.a[x ? x - NI : 0] = ra(stage, (w % WM * MI + (x ? x - NI : 0)) * 32, kk);
   }
-  __device__ __forceinline__ void multiply(const Operands& o) {
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j) acc[i][j] = Elem<T>::mfma(o.a[i], o.b[j], acc[i][j]);
+  __device__ __forceinline__ void multiply(const Operands& o, int x) {
+    acc[x / NI][x % NI] = Elem<T>::mfma(o.a[x / NI], o.b[x % NI], acc[x / NI][x % NI]);
   }
 
   // `k` k's from where a and b stand, in steps of 64; in the last step the
-  // operands are told how many are left where LIM says so. lds: 2 kStage elements.
+  // operands are told how many are left where Lim says so. lds: 2 kStage elements.
   // The stages are free again when it returns.
+  //
+  // Products, reads and loads are issued in this order and no other (left to
+  // itself the compiler reads a chunk's operands right before its products and
+  // waits for them there).
   template <bool LimA, bool LimB>
   __device__ __forceinline__ void run(A& a, B& b, int64_t k, uint16_t* lds) {
     const typename A::Read ra;
@@ -195,42 +192,65 @@ struct Tile {
       for (int j = 0; j < NI; ++j) acc[i][j] = attn::zero16();
     const int steps = (int)cdiv(k, (int64_t)kK);
     if (steps <= 0) return;
-    auto load = [&](int step, int buf) {
+    auto limit = [&](int step) {
       if ((LimA || LimB) && (step + 1) * (int64_t)kK > k) {
         if (LimA) a.limit((int)(k - step * (int64_t)kK));
         if (LimB) b.limit((int)(k - step * (int64_t)kK));
       }
-      a.load(lds0 + buf * (kStage * 2));
-      b.load(lds0 + buf * (kStage * 2) + BM * kK * 2);
     };
-    load(0, 0);
-    landed();
-    if (steps > 1) load(1, 1);
-    Operands o[2];
-    read(o[0], ra, rb, lds, 0);
-    // one step on stage `buf`; the other one holds the next step's tiles
-    auto step = [&](int t, int buf) {
-      const uint16_t* here = lds + buf * kStage;
+    auto load = [&](int x, int buf) {
+      if (x < A::kPer) a.load(lds0 + buf * (kStage * 2), x);
+      else b.load(lds0 + buf * (kStage * 2) + BM * kK * 2, x - A::kPer);
+    };
+    auto advance = [&] {
+      a.advance();
+      b.advance();
+    };
+    for (int s = 0; s < 2; ++s) {
+      if (s < steps) {
+        limit(s);
 #pragma unroll
-      for (int kk = 0; kk < 3; ++kk) {
-        read(o[(kk + 1) & 1], ra, rb, here, kk + 1);
-        multiply(o[kk & 1]);
+        for (int x = 0; x < kLoads; ++x) load(x, s);
+        advance();
       }
-      // the last chunk's operands are here (the compiler waits for them before
-      // the barrier's fence), so this stage may be written behind the barrier
+      if (s == 0) landed();
+    }
+    Operands o[2];
+#pragma unroll
+    for (int x = 0; x < kOperands; ++x) read(o[0], ra, rb, lds, 0, x);
+    constexpr int kMost = kProducts > kOperands ? kProducts : kOperands;
+    // one step on stage `buf`; the other one holds the next step's tiles
+    int buf = 0;
+    auto step = [&](auto more) {
+      const uint16_t* here = lds + buf * kStage;
+      const uint16_t* next = lds + (buf ^ 1) * kStage;
+#pragma unroll
+      for (int kk = 0; kk < 3; ++kk)
+#pragma unroll
+        for (int x = 0; x < kMost; ++x) {
+          if (x < kOperands) read(o[(kk + 1) & 1], ra, rb, here, kk + 1, x);
+          if (x < kProducts) multiply(o[kk & 1], x);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      // the last chunk's operands are here, so this stage may be written again
       landed();
-      if (t + 1 < steps) {
-        if (t + 2 < steps) load(t + 2, buf);
-        read(o[0], ra, rb, lds + (buf ^ 1) * kStage, 0);
+#pragma unroll
+      for (int x = 0; x < kLoads || x < kMost; ++x) {
+        if (x < kOperands) read(o[0], ra, rb, next, 0, x);  // behind the last step: of no use
+        if (more && x < kLoads) load(x, buf);
+        if (x < kProducts) multiply(o[1], x);
+        __builtin_amdgcn_sched_barrier(0);
       }
-      multiply(o[1]);
+      if (more) advance();
+      buf ^= 1;
     };
     int t = 0;
-    for (; t + 1 < steps; t += 2) {
-      step(t, 0);
-      step(t + 1, 1);
+    for (; t + 2 < steps; ++t) {
+      limit(t + 2);
+      step(std::true_type());
     }
-    if (t < steps) step(t, 0);
+    for (; t < steps; ++t) step(std::false_type());
+    landed();
   }
 
   // every wave's loads have landed and every wave's reads of LDS are done

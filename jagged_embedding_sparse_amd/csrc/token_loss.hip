@@ -187,14 +187,22 @@ struct ScoreArgs {
   int64_t e_cols;
 };
 
+// waves of a tile: 256 x 256 and 256 x 64
+#ifndef W_M
+#define W_M 2
+#define W_N 4
+#endif
+constexpr int kWM = W_M, kWN = W_N;
+constexpr int kMostThreads = 512;
 constexpr int kGroup = 8;  // token tiles that go by a table tile together
 
 // One tile of scores. Columns of the product are table rows, its rows tokens:
 // a lane's registers hold one token's scores, so their maximum and sum need one
 // exchange between two lanes and one between waves.
 template <typename T, int BN, int WM, int WN, bool Back>
-__global__ void __launch_bounds__(kThreads) k_scores(ScoreArgs a) {
-  using P = Tile<T, Rows<kV>, Rows<BN>, kV, BN, WM, WN>;
+__global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
+  constexpr int NT = WM * WN * kWave;
+  using P = Tile<T, Rows<kV, NT>, Rows<BN, NT>, kV, BN, WM, WN>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
   static_assert(2 * P::kStage >= BN * kV, "the stages hold a tile of e");
   int32_t tn, tv;
@@ -202,8 +210,8 @@ __global__ void __launch_bounds__(kThreads) k_scores(ScoreArgs a) {
   const int32_t live = *a.h.n_live;
   const int64_t n0 = (int64_t)tn * BN, v0 = (int64_t)tv * kV;
   if (n0 >= live) return;
-  Rows<kV> w(a.w, a.w_stride, v0, a.rows, 0);
-  Rows<BN> x(a.h.x, 2 * (int64_t)a.h.dp, n0, a.h.npad, 0);
+  Rows<kV, NT> w(a.w, a.w_stride, v0, a.rows, 0);
+  Rows<BN, NT> x(a.h.x, 2 * (int64_t)a.h.dp, n0, a.h.npad, 0);
   P p;
   p.template run<true, false>(w, x, a.k, lds);
   const int left = (int)min((int64_t)kV, a.rows - v0);  // rows of this tile
@@ -241,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) k_scores(ScoreArgs a) {
       if (lane() < 32) s_part[attn::wave_id() % WM][n] = make_float2(top, total);
     }
     __syncthreads();
-    for (int n = threadIdx.x; n < BN; n += kThreads) {
+    for (int n = threadIdx.x; n < BN; n += NT) {
       float top = s_part[0][n].x;
 #pragma unroll
       for (int i = 1; i < WM; ++i) top = fmaxf(top, s_part[i][n].x);
@@ -280,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) k_scores(ScoreArgs a) {
     __syncthreads();
     constexpr int kPieces = kV / 8;
 #pragma unroll 4
-    for (int u = threadIdx.x; u < BN * kPieces; u += kThreads) {
+    for (int u = threadIdx.x; u < BN * kPieces; u += NT) {
       const int n = u / kPieces, piece = u % kPieces;
       *(u32x4*)(a.e + ((n0 + n) * a.e_cols + v0 + 8 * piece) * 2) = Stage16<kV>::get(lds, n, piece);
     }
@@ -313,7 +321,7 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
   const int32_t cols = part ? a.h.dp : a.h.dim;
   if (part || a.out_type == FS_F32) {
     const float back = part ? 1.f : a.h.mul[1];
-    constexpr int kRows = kWaves / WM * 32, kPieces = kD / 4;
+    constexpr int kRows = P::kThreads / kWave / WM * 32, kPieces = kD / 4;
     float* f = (float*)lds;
 #pragma unroll
     for (int j = 0; j < P::NI; ++j) {
@@ -328,7 +336,7 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
                                  p.acc[i][j][4 * q + 2] * back, p.acc[i][j][4 * q + 3] * back});
       __syncthreads();
 #pragma unroll 4
-      for (int u = threadIdx.x; u < kRows * kPieces; u += kThreads) {
+      for (int u = threadIdx.x; u < kRows * kPieces; u += P::kThreads) {
         const int s = u / kPieces, piece = u % kPieces;
         const int64_t row = row0 + (s / 32 * P::NI + j) * 32 + s % 32;
         const int32_t col = col0 + 4 * piece;
@@ -373,7 +381,7 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
       }
   __syncthreads();
 #pragma unroll 4
-  for (int u = threadIdx.x; u < BN * kPieces; u += kThreads) {
+  for (int u = threadIdx.x; u < BN * kPieces; u += P::kThreads) {
     const int n = u / kPieces, piece = u % kPieces;
     const int64_t row = row0 + n;
     const int32_t col = col0 + 8 * piece;
@@ -390,10 +398,11 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
 
 // dx = e w over a part of the piece's rows, by tokens' places.
 template <typename T, int BN, int WM, int WN>
-__global__ void __launch_bounds__(kThreads) k_grad_x(SumArgs a) {
-  using P = Tile<T, Cols<kD>, Rows<BN>, kD, BN, WM, WN>;
+__global__ void __launch_bounds__(WM * WN * kWave) k_grad_x(SumArgs a) {
+  constexpr int NT = WM * WN * kWave;
+  using P = Tile<T, Cols<kD, NT>, Rows<BN, NT>, kD, BN, WM, WN>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
-  static_assert(4 * P::kStage >= kWaves / WM * 32 * kD * 4, "the stages hold rows of sums");
+  static_assert(4 * P::kStage >= WN * 32 * kD * 4, "the stages hold rows of sums");
   const int32_t tiles = a.order.rows * a.order.cols, id = in_order(blockIdx.x, gridDim.x);
   int32_t tn, td;
   // parts of one tile run apart, tiles of one part together
@@ -403,17 +412,17 @@ __global__ void __launch_bounds__(kThreads) k_grad_x(SumArgs a) {
   if (n0 >= *a.h.n_live) return;
   const int64_t k0 = (int64_t)part * a.steps * kK, k1 = min(a.rows, k0 + (int64_t)a.steps * kK);
   P p;
-  Cols<kD> w(a.w, a.w_stride, td * kD, a.w_cols, k0);
-  Rows<BN> e(a.e, 2 * a.e_cols, n0, a.h.npad, k0);
+  Cols<kD, NT> w(a.w, a.w_stride, td * kD, a.w_cols, k0);
+  Rows<BN, NT> e(a.e, 2 * a.e_cols, n0, a.h.npad, k0);
   p.template run<true, false>(w, e, k1 - k0, lds);
   put_sums<T, P, BN, WM>(p, lds, a, a.part + (int64_t)part * a.h.npad * a.h.dp, n0, a.h.npad, td * kD);
 }
 
 // dw = e^T x over a part of the tokens.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_grad_w(SumArgs a) {
-  constexpr int WM = 2, WN = 4;
-  using P = Tile<T, Cols<kD>, Cols<kV>, kD, kV, WM, WN>;
+__global__ void __launch_bounds__(kWM * kWN * kWave) k_grad_w(SumArgs a) {
+  constexpr int WM = kWM, WN = kWN, NT = WM * WN * kWave;
+  using P = Tile<T, Cols<kD, NT>, Cols<kV, NT>, kD, kV, WM, WN>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
   const int32_t tiles = a.order.rows * a.order.cols, id = in_order(blockIdx.x, gridDim.x);
   int32_t tv, td;
@@ -423,8 +432,8 @@ __global__ void __launch_bounds__(kThreads) k_grad_w(SumArgs a) {
   const int64_t steps = cdiv(*a.h.n_live, kK), per = cdiv(steps, a.parts);
   const int64_t s0 = min(steps, part * per), s1 = min(steps, s0 + per);
   P p;
-  Cols<kD> x(a.h.x, 2 * (int64_t)a.h.dp, td * kD, a.h.dp, s0 * kK);
-  Cols<kV> e(a.e, 2 * a.e_cols, (int64_t)tv * kV, a.e_cols, s0 * kK);
+  Cols<kD, NT> x(a.h.x, 2 * (int64_t)a.h.dp, td * kD, a.h.dp, s0 * kK);
+  Cols<kV, NT> e(a.e, 2 * a.e_cols, (int64_t)tv * kV, a.e_cols, s0 * kK);
   p.template run<false, false>(x, e, (s1 - s0) * kK, lds);
   float* to = a.part ? a.part + (int64_t)part * a.out_rows * a.h.dp : nullptr;
   put_sums<T, P, kV, WM>(p, lds, a, to, (int64_t)tv * kV, a.out_rows, td * kD);
@@ -829,13 +838,13 @@ int pack_tokens(PackArgs a, hipStream_t stream) {
 template <bool Back>
 int launch_scores(const ScoreArgs& a, const Sizes& s, int32_t dtype, hipStream_t stream) {
   const int64_t grid = (int64_t)a.order.rows * a.order.cols;
-  if (!grid_fits(grid, kThreads)) return FS_ERR_UNSUPPORTED;
-  const dim3 g((unsigned)grid), b(kThreads);
+  if (!grid_fits(grid, kMostThreads)) return FS_ERR_UNSUPPORTED;
+  const dim3 g((unsigned)grid), b((s.bn == 256 ? kWM * kWN : 8) * kWave);
   if (dtype == FS_BF16) {
-    if (s.bn == 256) hipLaunchKernelGGL((k_scores<__bf16, 256, 2, 4, Back>), g, b, 0, stream, a);
+    if (s.bn == 256) hipLaunchKernelGGL((k_scores<__bf16, 256, kWM, kWN, Back>), g, b, 0, stream, a);
     else hipLaunchKernelGGL((k_scores<__bf16, 64, 8, 1, Back>), g, b, 0, stream, a);
   } else {
-    if (s.bn == 256) hipLaunchKernelGGL((k_scores<_Float16, 256, 2, 4, Back>), g, b, 0, stream, a);
+    if (s.bn == 256) hipLaunchKernelGGL((k_scores<_Float16, 256, kWM, kWN, Back>), g, b, 0, stream, a);
     else hipLaunchKernelGGL((k_scores<_Float16, 64, 8, 1, Back>), g, b, 0, stream, a);
   }
   FS_LAUNCH_CHECK();
@@ -844,8 +853,8 @@ int launch_scores(const ScoreArgs& a, const Sizes& s, int32_t dtype, hipStream_t
 
 template <typename T>
 void launch_grad_x(const SumArgs& a, const Sizes& s, dim3 g, hipStream_t stream) {
-  if (s.bn == 256) hipLaunchKernelGGL((k_grad_x<T, 256, 2, 4>), g, dim3(kThreads), 0, stream, a);
-  else hipLaunchKernelGGL((k_grad_x<T, 64, 8, 1>), g, dim3(kThreads), 0, stream, a);
+  if (s.bn == 256) hipLaunchKernelGGL((k_grad_x<T, 256, kWM, kWN>), g, dim3(kWM * kWN * kWave), 0, stream, a);
+  else hipLaunchKernelGGL((k_grad_x<T, 64, 8, 1>), g, dim3(8 * kWave), 0, stream, a);
 }
 
 int launch_join(const JoinArgs& a, int32_t type, hipStream_t stream) {
@@ -967,7 +976,7 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
       b.add = v0 > 0;
       b.part = o.dx_part;
       const int64_t grid = (int64_t)token_tiles * col_tiles * x_parts;
-      if (!grid_fits(grid, kThreads)) return FS_ERR_UNSUPPORTED;
+      if (!grid_fits(grid, kMostThreads)) return FS_ERR_UNSUPPORTED;
       if (dtype == FS_BF16) launch_grad_x<__bf16>(b, s, dim3((unsigned)grid), stream);
       else launch_grad_x<_Float16>(b, s, dim3((unsigned)grid), stream);
       FS_LAUNCH_CHECK();
@@ -983,8 +992,8 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
       b.out_stride = g.dw_stride;
       b.out_rows = a.rows;
       b.out_type = g.dw_type;
-      if (!grid_fits(tiles * parts, kThreads)) return FS_ERR_UNSUPPORTED;
-      const dim3 grid((unsigned)(tiles * parts)), block(kThreads);
+      if (!grid_fits(tiles * parts, kMostThreads)) return FS_ERR_UNSUPPORTED;
+      const dim3 grid((unsigned)(tiles * parts)), block(kWM * kWN * kWave);
       if (dtype == FS_BF16) hipLaunchKernelGGL(k_grad_w<__bf16>, grid, block, 0, stream, b);
       else hipLaunchKernelGGL(k_grad_w<_Float16>, grid, block, 0, stream, b);
       FS_LAUNCH_CHECK();
@@ -1003,7 +1012,7 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
 
 // a grid of any launch of a call, by its sizes
 bool too_many(const Sizes& s) {
-  return !grid_fits(cdiv(s.npad, 64) * s.tiles, kThreads) || !grid_fits(s.npad, 64);
+  return !grid_fits(cdiv(s.npad, 64) * s.tiles, kMostThreads) || !grid_fits(s.npad, 64);
 }
 
 PackArgs pack_args(const Space& o, const Sizes& s, const void* x, int64_t x_stride, const int64_t* labels,
