@@ -45,6 +45,33 @@ __device__ __forceinline__ void load_piece(const char* base, uint32_t at, uint32
       : "memory");
 }
 
+// A operand reads of a tile in LDS: rows r0 .. r0 + 31 (a multiple of 32), k's
+// 16 kk + 8 g .. of a tile of rows of 64 k's;
+struct ReadRows {
+  int rows_at;
+  __device__ __forceinline__ ReadRows() { rows_at = attn::piece<kK>(lane() & 31, lane() >> 5); }
+  __device__ __forceinline__ u32x4 operator()(const uint16_t* tile, int r0, int kk) const {
+    return *(const u32x4*)(tile + (rows_at ^ (16 * kk)) + r0 * kK);
+  }
+};
+// columns c0 .. c0 + 31 (a multiple of 32) of a tile of 64 rows of R elements.
+template <int R>
+struct ReadCols {
+  int cols_at;
+  __device__ __forceinline__ ReadCols() {
+    const int l = lane(), g = l >> 5, j = l & 15, col = (l & 16) + 4 * (j & 3);
+    const int p = (col >> 3) ^ ((j >> 2) << 2 | 2 * g);
+    cols_at = (8 * g + (j >> 2)) * R + 8 * p + (col & 7);
+  }
+  __device__ __forceinline__ u32x4 operator()(const uint16_t* tile, int c0, int kk) const {
+    const uint16_t* a = tile + (cols_at ^ c0) + 16 * kk * R;
+    const uint16_t* b = tile + (cols_at ^ c0 ^ 8) + (16 * kk + 4) * R;
+    const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn::lds_s16x4*)a));
+    const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn::lds_s16x4*)b));
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+  }
+};
+
 // k's together: a tile of R rows and 64 k's, rows of 128 bytes.
 template <int R, int NT>
 struct Rows {
@@ -79,13 +106,7 @@ struct Rows {
   }
   __device__ __forceinline__ void advance() { base = attn::uniform(base + kK * 2); }
   // rows r0 .. r0 + 31 (a multiple of 32), k's 16 kk ..
-  struct Read {
-    int rows_at;
-    __device__ __forceinline__ Read() { rows_at = attn::piece<kK>(lane() & 31, lane() >> 5); }
-    __device__ __forceinline__ u32x4 operator()(const uint16_t* tile, int r0, int kk) const {
-      return *(const u32x4*)(tile + (rows_at ^ (16 * kk)) + r0 * kK);
-    }
-  };
+  using Read = ReadRows;
 };
 
 // k's apart: a tile of 64 k's, rows of R elements. Piece p of row r lies at
@@ -124,22 +145,70 @@ struct Cols {
     load_piece(base, at[x], tile + attn::wave_id() * (kWave * 16) + x * NT * 16);
   }
   __device__ __forceinline__ void advance() { base = attn::uniform(base + (int64_t)kK * row_bytes); }
-  struct Read {
-    int cols_at;
-    __device__ __forceinline__ Read() {
-      const int l = lane(), g = l >> 5, j = l & 15, col = (l & 16) + 4 * (j & 3);
-      const int p = (col >> 3) ^ ((j >> 2) << 2 | 2 * g);
-      cols_at = (8 * g + (j >> 2)) * R + 8 * p + (col & 7);
+  using Read = ReadCols<R>;
+};
+
+// Matrices of this library's own making lie in blocks of 64 x 64, a block's rows
+// one after another, so that what a step loads is a few runs of 8 KiB: whole rows
+// of a power of two apart would meet the same memory channels. Both kinds of tile
+// load from blocks; rows and columns are padded to whole blocks.
+constexpr int kBlock = kK * kK;  // elements
+
+__host__ __device__ __forceinline__ int64_t blocked(int64_t row, int64_t col, int64_t cols) {
+  return (row / kK * (cols / kK) + col / kK) * kBlock + row % kK * kK + col % kK;
+}
+
+template <int R, int NT>
+struct BlockRows {
+  static constexpr int kElems = R * kK;
+  static constexpr int kPer = R * 8 / NT;
+  static_assert(kPer >= 1 && R * 8 % NT == 0, "whole pieces per thread");
+  const char* base;
+  uint32_t at[kPer];
+  // row0 and k0: multiples of 64
+  __device__ __forceinline__ BlockRows(const char* p, int64_t cols, int64_t row0, int64_t k0) {
+    base = attn::uniform(p + 2 * blocked(row0, k0, cols));
+    const int piece = ((int)threadIdx.x % 8) ^ attn::swz<kK>((int)threadIdx.x / 8);
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int row = x * (NT / 8) + (int)threadIdx.x / 8;
+      at[x] = (uint32_t)(row / kK) * (uint32_t)(cols * kK * 2) + row % kK * (kK * 2) + 16 * piece;
     }
-    // columns c0 .. c0 + 31 (a multiple of 32), k's 16 kk + 8 g ..
-    __device__ __forceinline__ u32x4 operator()(const uint16_t* tile, int c0, int kk) const {
-      const uint16_t* a = tile + (cols_at ^ c0) + 16 * kk * R;
-      const uint16_t* b = tile + (cols_at ^ c0 ^ 8) + (16 * kk + 4) * R;
-      const u32x2 lo = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn::lds_s16x4*)a));
-      const u32x2 hi = __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((attn::lds_s16x4*)b));
-      return u32x4{lo[0], lo[1], hi[0], hi[1]};
+  }
+  __device__ __forceinline__ void limit(int) {}
+  __device__ __forceinline__ void load(uint32_t tile, int x) const {
+    load_piece(base, at[x], tile + attn::wave_id() * (kWave * 16) + x * NT * 16);
+  }
+  __device__ __forceinline__ void advance() { base = attn::uniform(base + kBlock * 2); }
+  using Read = ReadRows;
+};
+
+template <int R, int NT>
+struct BlockCols {
+  static constexpr int kElems = R * kK;
+  static constexpr int kPieces = R / 8, kPer = R * 8 / NT;
+  static_assert(kPer >= 1 && R * 8 % NT == 0 && NT % kPieces == 0, "whole rows per step");
+  const char* base;
+  uint32_t at[kPer];
+  int64_t step;
+  // col0 and k0: multiples of 64; columns past `cols` are the tile's first block again
+  __device__ __forceinline__ BlockCols(const char* p, int64_t cols, int64_t col0, int64_t k0) {
+    base = attn::uniform(p + 2 * blocked(k0, col0, cols));
+    step = cols * kK * 2;
+#pragma unroll
+    for (int x = 0; x < kPer; ++x) {
+      const int row = x * (NT / kPieces) + (int)threadIdx.x / kPieces;
+      const int piece = ((int)threadIdx.x % kPieces) ^ attn::swz<128>(row);
+      const int block = col0 + 8 * piece < cols ? piece / 8 : 0;
+      at[x] = block * (kBlock * 2) + row * (kK * 2) + 16 * (piece % 8);
     }
-  };
+  }
+  __device__ __forceinline__ void limit(int) {}
+  __device__ __forceinline__ void load(uint32_t tile, int x) const {
+    load_piece(base, at[x], tile + attn::wave_id() * (kWave * 16) + x * NT * 16);
+  }
+  __device__ __forceinline__ void advance() { base = attn::uniform(base + step); }
+  using Read = ReadCols<R>;
 };
 
 // WM x WN waves, each of MI x NI blocks of 32 x 32. Register i of a lane's block
@@ -152,11 +221,11 @@ struct Tile {
   static_assert(MI >= 1 && NI >= 1, "whole blocks");
   f32x16 acc[MI][NI];
 
-  static __device__ __forceinline__ int m_of(int mi) {
-    return (attn::wave_id() % WM * MI + mi) * 32 + 4 * (lane() >> 5);
+  static __device__ __forceinline__ int m_of(int mi, int l = lane()) {
+    return (attn::wave_id() % WM * MI + mi) * 32 + 4 * (l >> 5);
   }
-  static __device__ __forceinline__ int n_of(int ni) {
-    return (attn::wave_id() / WM * NI + ni) * 32 + (lane() & 31);
+  static __device__ __forceinline__ int n_of(int ni, int l = lane()) {
+    return (attn::wave_id() / WM * NI + ni) * 32 + (l & 31);
   }
 
   struct Operands {
@@ -174,9 +243,16 @@ struct Tile {
     acc[x / NI][x % NI] = Elem<T>::mfma(o.a[x / NI], o.b[x % NI], acc[x / NI][x % NI]);
   }
 
-  // `k` k's from where a and b stand, in steps of 64; in the last step the
+  // Asks for the first 64 of `k` k's, from where a and b stand. The first stage
+  // must be free; run() may follow after other work that leaves it alone.
+  template <bool LimA, bool LimB>
+  static __device__ __forceinline__ void ask(A& a, B& b, int64_t k, uint16_t* lds) {
+    if (k > 0) ask_step<LimA, LimB>(a, b, k, 0, lds_address(lds));
+  }
+
+  // The product over `k` k's in steps of 64, behind ask(); in the last step the
   // operands are told how many are left where Lim says so. lds: 2 kStage elements.
-  // The stages are free again when it returns.
+  // The stages are free again when it returns, the second one before it begins.
   //
   // Products, reads and loads are issued in this order and no other (left to
   // itself the compiler reads a chunk's operands right before its products and
@@ -185,36 +261,15 @@ struct Tile {
   __device__ __forceinline__ void run(A& a, B& b, int64_t k, uint16_t* lds) {
     const typename A::Read ra;
     const typename B::Read rb;
-    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)lds);
+    const uint32_t lds0 = lds_address(lds);
 #pragma unroll
     for (int i = 0; i < MI; ++i)
 #pragma unroll
       for (int j = 0; j < NI; ++j) acc[i][j] = attn::zero16();
     const int steps = (int)cdiv(k, (int64_t)kK);
     if (steps <= 0) return;
-    auto limit = [&](int step) {
-      if ((LimA || LimB) && (step + 1) * (int64_t)kK > k) {
-        if (LimA) a.limit((int)(k - step * (int64_t)kK));
-        if (LimB) b.limit((int)(k - step * (int64_t)kK));
-      }
-    };
-    auto load = [&](int x, int buf) {
-      if (x < A::kPer) a.load(lds0 + buf * (kStage * 2), x);
-      else b.load(lds0 + buf * (kStage * 2) + BM * kK * 2, x - A::kPer);
-    };
-    auto advance = [&] {
-      a.advance();
-      b.advance();
-    };
-    for (int s = 0; s < 2; ++s) {
-      if (s < steps) {
-        limit(s);
-#pragma unroll
-        for (int x = 0; x < kLoads; ++x) load(x, s);
-        advance();
-      }
-      if (s == 0) landed();
-    }
+    landed();
+    if (steps > 1) ask_step<LimA, LimB>(a, b, k, 1, lds0 + kStage * 2);
     Operands o[2];
 #pragma unroll
     for (int x = 0; x < kOperands; ++x) read(o[0], ra, rb, lds, 0, x);
@@ -237,20 +292,46 @@ struct Tile {
 #pragma unroll
       for (int x = 0; x < kLoads || x < kMost; ++x) {
         if (x < kOperands) read(o[0], ra, rb, next, 0, x);  // behind the last step: of no use
-        if (more && x < kLoads) load(x, buf);
+        if (more && x < kLoads) load(a, b, lds0 + buf * (kStage * 2), x);
         if (x < kProducts) multiply(o[1], x);
         __builtin_amdgcn_sched_barrier(0);
       }
-      if (more) advance();
+      if (more) {
+        a.advance();
+        b.advance();
+      }
       buf ^= 1;
     };
     int t = 0;
     for (; t + 2 < steps; ++t) {
-      limit(t + 2);
+      limit<LimA, LimB>(a, b, k, t + 2);
       step(std::true_type());
     }
     for (; t < steps; ++t) step(std::false_type());
     landed();
+  }
+
+  static __device__ __forceinline__ uint32_t lds_address(uint16_t* lds) {
+    return __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_ptr)lds);
+  }
+  template <bool LimA, bool LimB>
+  static __device__ __forceinline__ void limit(A& a, B& b, int64_t k, int step) {
+    if ((LimA || LimB) && (step + 1) * (int64_t)kK > k) {
+      if (LimA) a.limit((int)(k - step * (int64_t)kK));
+      if (LimB) b.limit((int)(k - step * (int64_t)kK));
+    }
+  }
+  static __device__ __forceinline__ void load(const A& a, const B& b, uint32_t stage, int x) {
+    if (x < A::kPer) a.load(stage, x);
+    else b.load(stage + BM * kK * 2, x - A::kPer);
+  }
+  template <bool LimA, bool LimB>
+  static __device__ __forceinline__ void ask_step(A& a, B& b, int64_t k, int step, uint32_t stage) {
+    limit<LimA, LimB>(a, b, k, step);
+#pragma unroll
+    for (int x = 0; x < kLoads; ++x) load(a, b, stage, x);
+    a.advance();
+    b.advance();
   }
 
   // every wave's loads have landed and every wave's reads of LDS are done
@@ -260,6 +341,13 @@ struct Tile {
     asm volatile("" ::: "memory");
   }
 };
+
+// LDS written before it is read behind it; loads in flight stay in flight
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
 
 // ---------------------------------------------------------------- output
 // Rows of a tile pass through LDS so that memory sees whole rows: 4 neighbouring
@@ -274,6 +362,9 @@ struct Stage16 {  // rows of BM elements of 2 bytes
   static __device__ __forceinline__ void put(uint16_t* lds, int n, int m, u32x2 v) {
     const int p = (m >> 3) ^ (n & (kPieces - 1));
     *(u32x2*)(lds + n * BM + 8 * p + (m & 7)) = v;
+  }
+  static __device__ __forceinline__ void put1(uint16_t* lds, int n, int m, uint32_t v) {
+    lds[n * BM + 8 * ((m >> 3) ^ (n & (kPieces - 1))) + (m & 7)] = (uint16_t)v;
   }
   static __device__ __forceinline__ u32x4 get(const uint16_t* lds, int n, int piece) {
     return *(const u32x4*)(lds + n * BM + 8 * (piece ^ (n & (kPieces - 1))));

@@ -25,10 +25,13 @@ using namespace prod;
 constexpr float kLog2e = attn::kLog2e, kLn2 = attn::kLn2;
 constexpr int kV = 256;                           // table rows of a tile
 constexpr int kD = 256;                           // columns of a gradient's tile
-constexpr int64_t kPieceBytes = (int64_t)1 << 29;  // e of one piece of the table
+#ifndef PB
+#define PB 30
+#endif
+constexpr int64_t kPieceBytes = (int64_t)1 << PB;  // e of one piece of the table
 constexpr int64_t kPackBytes = (int64_t)1 << 26;   // a piece of a table that has to be laid out
 constexpr int64_t kPartBytes = (int64_t)1 << 28;   // sums of a cut product
-constexpr int kMostParts = 32;
+constexpr int kMostParts = 64;
 
 // What the kernels of one call share, in its workspace.
 struct Head {
@@ -38,7 +41,7 @@ struct Head {
   int32_t* label;   // [npad] by place, as are lse2 and coef
   float* lse2;      // lse log2(e)
   float* coef;      // dloss scale
-  char* x;          // [npad][dp] 16 bits: their rows, zeros past dim and past n_live
+  char* x;          // [npad][dp] 16 bits in blocks: their rows, zeros past dim and n_live
   int64_t n, npad;
   int32_t dim, dp;
 };
@@ -114,7 +117,7 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
     __syncthreads();
     for (int32_t u = threadIdx.x; u < total * pieces; u += kPackThreads) {
       const int32_t r = u / pieces, p = u - r * pieces;
-      *(u32x4*)(a.h.x + ((int64_t)(base + r) * a.h.dp + 8 * p) * 2) =
+      *(u32x4*)(a.h.x + 2 * blocked(base + r, 8 * p, a.h.dp)) =
           row_piece(a.x + (i0 + s_row[r]) * a.x_stride, 8 * p, a.h.dim);
     }
     base += total;
@@ -128,7 +131,7 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
       a.h.lse2[r] = a.h.coef[r] = 0.f;
     }
     for (int32_t u = threadIdx.x; u < rest * pieces; u += kPackThreads)
-      *(u32x4*)(a.h.x + ((int64_t)base * a.h.dp + 8 * (int64_t)u) * 2) = u32x4{0, 0, 0, 0};
+      *(u32x4*)(a.h.x + 2 * blocked(base + u / pieces, 8 * (u % pieces), a.h.dp)) = u32x4{0, 0, 0, 0};
   }
   if (blockIdx.x == 0 && a.back) {
     // fp16's exponents end where e's do not: e is rounded times a power of two
@@ -183,7 +186,7 @@ struct ScoreArgs {
   float scale2;      // scale log2(e)
   float2* part;      // forward: [tiles of the table][npad] maximum and sum, base 2
   float* at_label;   // forward: [npad] the label's score, base 2
-  char* e;           // backward: [npad][e_cols] 16 bits
+  char* e;           // backward: [npad][e_cols] 16 bits in blocks
   int64_t e_cols;
 };
 
@@ -194,62 +197,72 @@ struct ScoreArgs {
 #endif
 constexpr int kWM = W_M, kWN = W_N;
 constexpr int kMostThreads = 512;
+constexpr int kCus = 256;
 constexpr int kGroup = 8;  // token tiles that go by a table tile together
 
-// One tile of scores. Columns of the product are table rows, its rows tokens:
-// a lane's registers hold one token's scores, so their maximum and sum need one
-// exchange between two lanes and one between waves.
-template <typename T, int BN, int WM, int WN, bool Back>
-__global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
+// A value that the compiler takes for new each time, so that what follows from it
+// is not kept in registers over a loop.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
+// What a tile's scores leave behind, by way of the stage that the next tile's
+// first loads do not write.
+template <typename T, int BN, int WM, int WN, bool Back, typename P>
+__device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t* lds, int64_t n0, int64_t v0,
+                                              int32_t tv) {
   constexpr int NT = WM * WN * kWave;
-  using P = Tile<T, Rows<kV, NT>, Rows<BN, NT>, kV, BN, WM, WN>;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
-  static_assert(2 * P::kStage >= BN * kV, "the stages hold a tile of e");
-  int32_t tn, tv;
-  a.order.at(in_order(blockIdx.x, gridDim.x), kGroup, &tn, &tv);
-  const int32_t live = *a.h.n_live;
-  const int64_t n0 = (int64_t)tn * BN, v0 = (int64_t)tv * kV;
-  if (n0 >= live) return;
-  Rows<kV, NT> w(a.w, a.w_stride, v0, a.rows, 0);
-  Rows<BN, NT> x(a.h.x, 2 * (int64_t)a.h.dp, n0, a.h.npad, 0);
-  P p;
-  p.template run<true, false>(w, x, a.k, lds);
+  const int l = here(lane()), tid = here(threadIdx.x);
   const int left = (int)min((int64_t)kV, a.rows - v0);  // rows of this tile
+  // from here on the scale is positive, so the largest product's score is the
+  // largest (a scale of 0 makes the products zeros)
+  if (a.scale2 <= 0.f) {
+#pragma unroll
+    for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < P::NI; ++j) p.acc[i][j] = a.scale2 < 0.f ? -p.acc[i][j] : attn::zero16();
+  }
+  const float scale2 = a.scale2 == 0.f ? 1.f : fabsf(a.scale2);
   if constexpr (!Back) {
-    float2(*s_part)[BN] = (float2(*)[BN])lds;  // the stages are done with
-    static_assert(4 * P::kStage >= WM * BN * 8, "");
+    float2(*s_part)[BN] = (float2(*)[BN])lds;
+    static_assert(2 * P::kStage >= WM * BN * 8, "a stage holds them");
 #pragma unroll
     for (int j = 0; j < P::NI; ++j) {
-      const int n = P::n_of(j);
+      const int n = P::n_of(j, l);
       const int64_t lab = (int64_t)a.h.label[n0 + n] - a.v0 - v0;
-      float top = -3e38f;  // finite, so that scores of -inf add 0
-#pragma unroll
-      for (int i = 0; i < P::MI; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int m = P::m_of(i) + 8 * (r >> 2) + (r & 3);
-          p.acc[i][j][r] *= a.scale2;
-          if (left < kV && m >= left) p.acc[i][j][r] = -INFINITY;
-          top = fmaxf(top, p.acc[i][j][r]);
-        }
-      top = attn::max_halves(top);
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int i = 0; i < P::MI; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sum[r & 3] += __builtin_amdgcn_exp2f(p.acc[i][j][r] - top);
-      const float total = attn::add_halves((sum[0] + sum[1]) + (sum[2] + sum[3]));
       if (lab >= 0 && lab < kV) {
 #pragma unroll
         for (int i = 0; i < P::MI; ++i)
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            if (P::m_of(i) + 8 * (r >> 2) + (r & 3) == lab) a.at_label[n0 + n] = p.acc[i][j][r];
+            if (P::m_of(i, l) + 8 * (r >> 2) + (r & 3) == lab) a.at_label[n0 + n] = p.acc[i][j][r] * scale2;
       }
-      if (lane() < 32) s_part[attn::wave_id() % WM][n] = make_float2(top, total);
+      if (left < kV) {
+#pragma unroll
+        for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (P::m_of(i, l) + 8 * (r >> 2) + (r & 3) >= left) p.acc[i][j][r] = -INFINITY;
+      }
+      float top = p.acc[0][j][0];
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, p.acc[i][j][r]);
+      // finite, so that scores of -inf add 0
+      top = fmaxf(attn::max_halves(top) * scale2, -3e38f);
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          sum[r & 3] += __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][r], scale2, -top));
+      const float total = attn::add_halves((sum[0] + sum[1]) + (sum[2] + sum[3]));
+      if (l < 32) s_part[attn::wave_id() % WM][n] = make_float2(top, total);
     }
-    __syncthreads();
-    for (int n = threadIdx.x; n < BN; n += NT) {
+    lds_barrier();
+    for (int n = tid; n < BN; n += NT) {
       float top = s_part[0][n].x;
 #pragma unroll
       for (int i = 1; i < WM; ++i) top = fmaxf(top, s_part[i][n].x);
@@ -260,38 +273,97 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
     }
   } else {
     const float mul = a.h.mul[0];
+    constexpr int kRows = WN * 32;
+    static_assert(P::kStage >= kRows * kV, "a stage holds a pass of e");
 #pragma unroll
     for (int j = 0; j < P::NI; ++j) {
-      const int n = P::n_of(j);
+      if (j) lds_barrier();
+      const int n = P::n_of(j, l), s = attn::wave_id() / WM * 32 + (l & 31);
       const int64_t lab = (int64_t)a.h.label[n0 + n] - a.v0 - v0;
-      const int label = lab >= 0 && lab < kV ? (int)lab : -1;
       const float lse2 = a.h.lse2[n0 + n], c = a.h.coef[n0 + n] * mul;
+      // c exp2(s) = exp2(s + log2 c): the factor costs no instruction of its own
+      const float at = __builtin_amdgcn_logf(fabsf(c)) - lse2;
+      const uint32_t sign = c < 0.f ? 0x80008000u : 0u;
 #pragma unroll
       for (int i = 0; i < P::MI; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int m = P::m_of(i) + 8 * q;
+          const int m = P::m_of(i, l) + 8 * q;
           float v[4];
 #pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            v[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][4 * q + r], a.scale2, -lse2));
-            if (m + r == label) v[r] -= 1.f;
-            v[r] *= c;
-            if (left < kV && m + r >= left) v[r] = 0.f;
-          }
+          for (int r = 0; r < 4; ++r)
+            v[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][4 * q + r], scale2, at));
           u32x2 y;
-          y[0] = Elem<T>::pack(v[0], v[1]);
-          y[1] = Elem<T>::pack(v[2], v[3]);
-          Stage16<kV>::put(lds, n, m, y);
+          y[0] = Elem<T>::pack(v[0], v[1]) ^ sign;
+          y[1] = Elem<T>::pack(v[2], v[3]) ^ sign;
+          Stage16<kV>::put(lds, s, m, y);
         }
-    }
-    __syncthreads();
-    constexpr int kPieces = kV / 8;
+      // the label's place, from the difference; places past the table
+      if (lab >= 0 && lab < kV) {
+#pragma unroll
+        for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (P::m_of(i, l) + 8 * (r >> 2) + (r & 3) == lab) {
+              const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][r], scale2, -lse2)) - 1.f;
+              Stage16<kV>::put1(lds, s, (int)lab, Elem<T>::pack(v * c, 0.f));
+            }
+      }
+      if (left < kV) {
+#pragma unroll
+        for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int m = P::m_of(i, l) + 8 * (r >> 2) + (r & 3);
+            if (m >= left) Stage16<kV>::put1(lds, s, m, 0);
+          }
+      }
+      lds_barrier();
+      constexpr int kPieces = kV / 8;
 #pragma unroll 4
-    for (int u = threadIdx.x; u < BN * kPieces; u += NT) {
-      const int n = u / kPieces, piece = u % kPieces;
-      *(u32x4*)(a.e + ((n0 + n) * a.e_cols + v0 + 8 * piece) * 2) = Stage16<kV>::get(lds, n, piece);
+      for (int u = tid; u < kRows * kPieces; u += NT) {  // block by block
+        const int r = u / 8 % kRows, piece = u / (8 * kRows) * 8 + u % 8;
+        // past the caches, which hold the operands of the tiles beside this one
+        // (597 -> 565 us, and the product that reads e 503 -> 479)
+        __builtin_nontemporal_store(
+            Stage16<kV>::get(lds, r, piece),
+            (u32x4*)(a.e + 2 * blocked(n0 + (r / 32 * P::NI + j) * 32 + r % 32, v0 + 8 * piece, a.e_cols)));
+      }
     }
+  }
+}
+
+// One tile of scores. Columns of the product are table rows, its rows tokens:
+// a lane's registers hold one token's scores, so their maximum and sum need one
+// exchange between two lanes and one between waves.
+template <typename T, int BN, int WM, int WN, bool Back>
+__global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
+  constexpr int NT = WM * WN * kWave;
+  using P = Tile<T, Rows<kV, NT>, BlockRows<BN, NT>, kV, BN, WM, WN>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
+  uint16_t* const second = lds + P::kStage;
+  const int32_t live = *a.h.n_live;
+  // tiles of tokens that take part, dealt to all XCDs alike
+  const Order order{(int32_t)cdiv(live, BN), a.order.cols};
+  const int32_t tiles = order.rows * order.cols;
+  if ((int32_t)blockIdx.x >= tiles) return;
+  int32_t tn, tv;
+  order.at(in_order(blockIdx.x, tiles), kGroup, &tn, &tv);
+  Rows<kV, NT> w(a.w, a.w_stride, (int64_t)tv * kV, a.rows, 0);
+  BlockRows<BN, NT> x(a.h.x, a.h.dp, (int64_t)tn * BN, 0);
+  P::template ask<true, false>(w, x, a.k, lds);
+  for (int32_t id = blockIdx.x; id < tiles; id += gridDim.x) {  // uniform
+    const int64_t n0 = (int64_t)tn * BN, v0 = (int64_t)tv * kV;
+    const int32_t tile = tv;
+    P p;
+    p.template run<true, false>(w, x, a.k, lds);
+    if (id + (int32_t)gridDim.x < tiles) {  // the next tile's first loads, behind this one's scores
+      order.at(in_order(id + gridDim.x, tiles), kGroup, &tn, &tv);
+      w = Rows<kV, NT>(a.w, a.w_stride, (int64_t)tv * kV, a.rows, 0);
+      x = BlockRows<BN, NT>(a.h.x, a.h.dp, (int64_t)tn * BN, 0);
+      P::template ask<true, false>(w, x, a.k, lds);
+    }
+    finish_scores<T, BN, WM, WN, Back>(a, p, second, n0, v0, tile);
   }
 }
 
@@ -400,20 +472,23 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
 template <typename T, int BN, int WM, int WN>
 __global__ void __launch_bounds__(WM * WN * kWave) k_grad_x(SumArgs a) {
   constexpr int NT = WM * WN * kWave;
-  using P = Tile<T, Cols<kD, NT>, Rows<BN, NT>, kD, BN, WM, WN>;
+  using P = Tile<T, Cols<kD, NT>, BlockRows<BN, NT>, kD, BN, WM, WN>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
   static_assert(4 * P::kStage >= WN * 32 * kD * 4, "the stages hold rows of sums");
-  const int32_t tiles = a.order.rows * a.order.cols, id = in_order(blockIdx.x, gridDim.x);
+  const Order order{(int32_t)cdiv(*a.h.n_live, BN), a.order.cols};
+  const int32_t tiles = order.rows * order.cols;
+  if ((int64_t)blockIdx.x >= (int64_t)tiles * a.parts) return;
+  const int32_t id = in_order(blockIdx.x, tiles * a.parts);
   int32_t tn, td;
   // parts of one tile run apart, tiles of one part together
-  a.order.at(id % tiles, kGroup, &tn, &td);
+  order.at(id % tiles, kGroup, &tn, &td);
   const int32_t part = id / tiles;
   const int64_t n0 = (int64_t)tn * BN;
-  if (n0 >= *a.h.n_live) return;
   const int64_t k0 = (int64_t)part * a.steps * kK, k1 = min(a.rows, k0 + (int64_t)a.steps * kK);
   P p;
   Cols<kD, NT> w(a.w, a.w_stride, td * kD, a.w_cols, k0);
-  Rows<BN, NT> e(a.e, 2 * a.e_cols, n0, a.h.npad, k0);
+  BlockRows<BN, NT> e(a.e, a.e_cols, n0, k0);
+  P::template ask<true, false>(w, e, k1 - k0, lds);
   p.template run<true, false>(w, e, k1 - k0, lds);
   put_sums<T, P, BN, WM>(p, lds, a, a.part + (int64_t)part * a.h.npad * a.h.dp, n0, a.h.npad, td * kD);
 }
@@ -422,7 +497,7 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_grad_x(SumArgs a) {
 template <typename T>
 __global__ void __launch_bounds__(kWM * kWN * kWave) k_grad_w(SumArgs a) {
   constexpr int WM = kWM, WN = kWN, NT = WM * WN * kWave;
-  using P = Tile<T, Cols<kD, NT>, Cols<kV, NT>, kD, kV, WM, WN>;
+  using P = Tile<T, BlockCols<kD, NT>, BlockCols<kV, NT>, kD, kV, WM, WN>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
   const int32_t tiles = a.order.rows * a.order.cols, id = in_order(blockIdx.x, gridDim.x);
   int32_t tv, td;
@@ -432,8 +507,9 @@ __global__ void __launch_bounds__(kWM * kWN * kWave) k_grad_w(SumArgs a) {
   const int64_t steps = cdiv(*a.h.n_live, kK), per = cdiv(steps, a.parts);
   const int64_t s0 = min(steps, part * per), s1 = min(steps, s0 + per);
   P p;
-  Cols<kD, NT> x(a.h.x, 2 * (int64_t)a.h.dp, td * kD, a.h.dp, s0 * kK);
-  Cols<kV, NT> e(a.e, 2 * a.e_cols, (int64_t)tv * kV, a.e_cols, s0 * kK);
+  BlockCols<kD, NT> x(a.h.x, a.h.dp, td * kD, s0 * kK);
+  BlockCols<kV, NT> e(a.e, a.e_cols, (int64_t)tv * kV, s0 * kK);
+  P::template ask<false, false>(x, e, (s1 - s0) * kK, lds);
   p.template run<false, false>(x, e, (s1 - s0) * kK, lds);
   float* to = a.part ? a.part + (int64_t)part * a.out_rows * a.h.dp : nullptr;
   put_sums<T, P, kV, WM>(p, lds, a, to, (int64_t)tv * kV, a.out_rows, td * kD);
@@ -633,7 +709,6 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
     return;
   }
   const Teacher t(a, i);
-  const char* x = a.h.x + (int64_t)pos * a.h.dp * 2;
   for (int k0 = 0; k0 < a.top; k0 += 4) {
     const char* row[4];
     float sum[4];
@@ -652,7 +727,7 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
       sum[u] = 0.f;
     }
     for (int c = 8 * l; c < a.h.dim; c += 8 * kWave) {
-      const u32x4 xv = *(const u32x4*)(x + 2 * c);
+      const u32x4 xv = *(const u32x4*)(a.h.x + 2 * blocked(pos, c, a.h.dp));
       u32x4 wv[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) wv[u] = row[u] ? row_piece(row[u], c, a.h.dim) : u32x4{0, 0, 0, 0};
@@ -716,7 +791,7 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill_entries(Teach
     for (int k = 0; k < a.top; ++k) q += s_id[w][k] == t.id[u] ? s_q[w][k] : 0.f;
     const float z = a.logits_in[i * a.top + l + kWave * u];
     const float e = (__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -lse2)) - q) * c;
-    ((T*)a.e)[pos * a.e_cols + v] = (T)e;
+    ((T*)a.e)[blocked(pos, v, a.e_cols)] = (T)e;
   }
 }
 
@@ -728,12 +803,25 @@ struct Sizes {
 
 int64_t most_parts(int64_t steps) { return std::min<int64_t>(kMostParts, std::max<int64_t>(1, steps / 4)); }
 
-// A product's tiles and steps say in how many parts it is cut: few tiles leave
-// CUs idle, so sums over many steps are cut until about two workgroups a CU are
-// there, at least four steps each, as far as the sums' space goes.
+// In how many parts a product is cut, so that few tiles do not leave CUs idle: the
+// number for which its rounds of workgroups (a CU each) take the least time, with
+// the sums that every part writes and somebody reads. A step of 64 takes a
+// workgroup 1.8 us, its start and end about 6, and memory 5 bytes in a ps.
+// (256 tiles of 256 steps in two parts 503 us, in one @@; 96 tiles of 1024 in one part
+// @@, in 8 @@.)
 int32_t parts_of(int64_t tiles, int64_t steps, int64_t bytes_each, int64_t bytes) {
-  const int64_t p = std::min(std::max<int64_t>(1, 512 / std::max<int64_t>(tiles, 1)), most_parts(steps));
-  return (int32_t)std::max<int64_t>(1, std::min(p, bytes / std::max<int64_t>(bytes_each, 1)));
+  const int64_t most = std::min(most_parts(steps), std::max<int64_t>(1, bytes / std::max<int64_t>(bytes_each, 1)));
+  int32_t best = 1;
+  double least = 1e300;
+  for (int64_t p = 1; p <= most; ++p) {
+    const double us = (double)cdiv(tiles * p, kCus) * ((double)cdiv(steps, p) * 1.8 + 6.0) +
+                      (p > 1 ? 4.0 : 0.0) + 2e-6 * (double)(p * bytes_each) / 5.0;
+    if (us < least) {
+      least = us;
+      best = (int32_t)p;
+    }
+  }
+  return best;
 }
 
 Sizes sizes_of(int64_t n, int64_t rows, int32_t dim) {
@@ -839,7 +927,7 @@ template <bool Back>
 int launch_scores(const ScoreArgs& a, const Sizes& s, int32_t dtype, hipStream_t stream) {
   const int64_t grid = (int64_t)a.order.rows * a.order.cols;
   if (!grid_fits(grid, kMostThreads)) return FS_ERR_UNSUPPORTED;
-  const dim3 g((unsigned)grid), b((s.bn == 256 ? kWM * kWN : 8) * kWave);
+  const dim3 g((unsigned)(s.bn == 256 ? std::min<int64_t>(grid, kCus) : grid)), b((s.bn == 256 ? kWM * kWN : 8) * kWave);
   if (dtype == FS_BF16) {
     if (s.bn == 256) hipLaunchKernelGGL((k_scores<__bf16, 256, kWM, kWN, Back>), g, b, 0, stream, a);
     else hipLaunchKernelGGL((k_scores<__bf16, 64, 8, 1, Back>), g, b, 0, stream, a);

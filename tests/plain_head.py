@@ -117,8 +117,10 @@ def loss_gradients(x, w, lse, dloss, dtype, scale=1.0, pad=-1, labels=None, ids=
     c = torch.where(live, dloss.double() * scale, 0.0)[:, None]
     p = torch.exp(z - lse)
     e = c * (p - target)
-    # p: its exponent's argument and exp2; the difference and the factor in one rounding each
-    off = c.abs() * (p * (2 * e_z + 6 * U32 * (z.abs() + lse.abs()) + 4 * U32) + 4 * U32 * (p + target))
+    # p: its exponent's argument (the factor's logarithm in it) and exp2; the
+    # difference and the factor in one rounding each
+    log = torch.where(c == 0, 0.0, c.abs().clamp_min(1e-300).log().abs()) + 40
+    off = c.abs() * (p * (2 * e_z + 6 * U32 * (z.abs() + lse.abs() + log) + 4 * U32) + 4 * U32 * (p + target))
     if ids is not None:
         s = (teacher.double() * scale).abs().masked_fill(teacher == -math.inf, 0.0).amax(1, keepdim=True)
         off = off + c.abs() * target * (16 * s + 2 * 280) * U32
