@@ -45,6 +45,17 @@ __device__ __forceinline__ void load_piece(const char* base, uint32_t at, uint32
       : "memory");
 }
 
+// the same for 4 bytes per lane
+__device__ __forceinline__ void load_words(const void* base, uint32_t at, uint32_t to) {
+  uint32_t m0;
+  asm volatile(
+      "s_mov_b32 %0, m0\n\ts_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dword %2, %3\n\t"
+      "s_mov_b32 m0, %0"
+      : "=&s"(m0)
+      : "s"(to), "v"(at), "s"(base)
+      : "memory");
+}
+
 // A operand reads of a tile in LDS: rows r0 .. r0 + 31 (a multiple of 32), k's
 // 16 kk + 8 g .. of a tile of rows of 64 k's;
 struct ReadRows {
@@ -253,12 +264,15 @@ struct Tile {
   // The product over `k` k's in steps of 64, behind ask(); in the last step the
   // operands are told how many are left where Lim says so. lds: 2 kStage elements.
   // The stages are free again when it returns, the second one before it begins.
+  // Since ask() the wave has issued `After` memory operations or more (of which
+  // none has to be waited for at the start: they complete in order), or none
+  // where `fresh`.
   //
   // Products, reads and loads are issued in this order and no other (left to
   // itself the compiler reads a chunk's operands right before its products and
   // waits for them there).
-  template <bool LimA, bool LimB>
-  __device__ __forceinline__ void run(A& a, B& b, int64_t k, uint16_t* lds) {
+  template <bool LimA, bool LimB, int After = 0>
+  __device__ __forceinline__ void run(A& a, B& b, int64_t k, uint16_t* lds, bool fresh = true) {
     const typename A::Read ra;
     const typename B::Read rb;
     const uint32_t lds0 = lds_address(lds);
@@ -268,7 +282,8 @@ struct Tile {
       for (int j = 0; j < NI; ++j) acc[i][j] = attn::zero16();
     const int steps = (int)cdiv(k, (int64_t)kK);
     if (steps <= 0) return;
-    landed();
+    if (After == 0 || fresh) landed();
+    else landed<After>();
     if (steps > 1) ask_step<LimA, LimB>(a, b, k, 1, lds0 + kStage * 2);
     Operands o[2];
 #pragma unroll
@@ -335,8 +350,9 @@ struct Tile {
   }
 
   // every wave's loads have landed and every wave's reads of LDS are done
+  template <int But = 0>  // all but the latest operations
   static __device__ __forceinline__ void landed() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(But) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }

@@ -207,11 +207,41 @@ __device__ __forceinline__ int here(int x) {
   return x;
 }
 
+// label, lse2 and coef of a tile's tokens, to LDS without registers: a wait for
+// them would wait for the next tile's loads as well
+template <int BN, int NW, bool Back>
+__device__ __forceinline__ void ask_info(const Head& h, int64_t n0, float (*info)[BN]) {
+  const uint32_t to = __builtin_amdgcn_readfirstlane(
+      (uint32_t)(uintptr_t)(__attribute__((address_space(3))) float*)&info[0][0]);
+  constexpr int kGroups = BN / kWave;
+#pragma unroll
+  for (int t0 = 0; t0 < (Back ? 3 : 1) * kGroups; t0 += NW) {
+    const int t = t0 + attn::wave_id(), which = t / kGroups, g = t % kGroups;
+    if (which >= (Back ? 3 : 1)) break;
+    const char* from = (const char*)(which == 0 ? (const void*)h.label : which == 1 ? h.lse2 : h.coef);
+    load_words(attn::uniform(from + 4 * (n0 + g * kWave)), 4 * lane(), to + 4 * (which * BN + g * kWave));
+  }
+}
+
+// Where a tile's tokens' label, lse2 and coef are read: LDS, or memory where a
+// workgroup has one tile.
+template <int BN>
+struct TokenInfo {
+  const float (*lds)[BN];
+  const Head& h;
+  int64_t n0;
+  __device__ __forceinline__ int32_t label(int n) const {
+    return BN == 256 ? __float_as_int(lds[0][n]) : h.label[n0 + n];
+  }
+  __device__ __forceinline__ float lse2(int n) const { return BN == 256 ? lds[1][n] : h.lse2[n0 + n]; }
+  __device__ __forceinline__ float coef(int n) const { return BN == 256 ? lds[2][n] : h.coef[n0 + n]; }
+};
+
 // What a tile's scores leave behind, by way of the stage that the next tile's
 // first loads do not write.
 template <typename T, int BN, int WM, int WN, bool Back, typename P>
 __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t* lds, int64_t n0, int64_t v0,
-                                              int32_t tv) {
+                                              int32_t tv, const TokenInfo<BN>& info, float mul) {
   constexpr int NT = WM * WN * kWave;
   const int l = here(lane()), tid = here(threadIdx.x);
   const int left = (int)min((int64_t)kV, a.rows - v0);  // rows of this tile
@@ -230,7 +260,7 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
 #pragma unroll
     for (int j = 0; j < P::NI; ++j) {
       const int n = P::n_of(j, l);
-      const int64_t lab = (int64_t)a.h.label[n0 + n] - a.v0 - v0;
+      const int64_t lab = (int64_t)info.label(n) - a.v0 - v0;
       if (lab >= 0 && lab < kV) {
 #pragma unroll
         for (int i = 0; i < P::MI; ++i)
@@ -272,15 +302,14 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
       a.part[(int64_t)(a.v_tile0 + tv) * a.h.npad + n0 + n] = make_float2(top, sum);
     }
   } else {
-    const float mul = a.h.mul[0];
     constexpr int kRows = WN * 32;
     static_assert(P::kStage >= kRows * kV, "a stage holds a pass of e");
 #pragma unroll
     for (int j = 0; j < P::NI; ++j) {
       if (j) lds_barrier();
       const int n = P::n_of(j, l), s = attn::wave_id() / WM * 32 + (l & 31);
-      const int64_t lab = (int64_t)a.h.label[n0 + n] - a.v0 - v0;
-      const float lse2 = a.h.lse2[n0 + n], c = a.h.coef[n0 + n] * mul;
+      const int64_t lab = (int64_t)info.label(n) - a.v0 - v0;
+      const float lse2 = info.lse2(n), c = info.coef(n) * mul;
       // c exp2(s) = exp2(s + log2 c): the factor costs no instruction of its own
       const float at = __builtin_amdgcn_logf(fabsf(c)) - lse2;
       const uint32_t sign = c < 0.f ? 0x80008000u : 0u;
@@ -321,8 +350,8 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
       lds_barrier();
       constexpr int kPieces = kV / 8;
 #pragma unroll 4
-      for (int u = tid; u < kRows * kPieces; u += NT) {  // block by block
-        const int r = u / 8 % kRows, piece = u / (8 * kRows) * 8 + u % 8;
+      for (int y = 0; y < kRows * kPieces / NT; ++y) {  // block by block
+        const int u = y * NT + tid, r = u / 8 % kRows, piece = u / (8 * kRows) * 8 + u % 8;
         // past the caches, which hold the operands of the tiles beside this one
         // (597 -> 565 us, and the product that reads e 503 -> 479)
         __builtin_nontemporal_store(
@@ -351,19 +380,30 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
   order.at(in_order(blockIdx.x, tiles), kGroup, &tn, &tv);
   Rows<kV, NT> w(a.w, a.w_stride, (int64_t)tv * kV, a.rows, 0);
   BlockRows<BN, NT> x(a.h.x, a.h.dp, (int64_t)tn * BN, 0);
+  // tiles of 64 tokens are one to a workgroup, and LDS holds two such
+  constexpr bool kMany = BN == 256;
+  __shared__ float info[kMany ? 2 : 1][kMany ? (Back ? 3 : 1) : 1][kMany ? BN : 1];
+  if constexpr (kMany) ask_info<BN, WM * WN, Back>(a.h, (int64_t)tn * BN, info[0]);
+  const float mul = Back ? __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(a.h.mul[0]))) : 1.f;
   P::template ask<true, false>(w, x, a.k, lds);
+  // a thread's stores of e behind the next tile's loads
+  constexpr int kAfter = Back ? P::NI * WN * 32 * kV / 8 / NT : 0;
+  int turn = 0;
   for (int32_t id = blockIdx.x; id < tiles; id += gridDim.x) {  // uniform
     const int64_t n0 = (int64_t)tn * BN, v0 = (int64_t)tv * kV;
     const int32_t tile = tv;
     P p;
-    p.template run<true, false>(w, x, a.k, lds);
+    p.template run<true, false, kAfter>(w, x, a.k, lds, id == (int32_t)blockIdx.x);
     if (id + (int32_t)gridDim.x < tiles) {  // the next tile's first loads, behind this one's scores
       order.at(in_order(id + gridDim.x, tiles), kGroup, &tn, &tv);
       w = Rows<kV, NT>(a.w, a.w_stride, (int64_t)tv * kV, a.rows, 0);
       x = BlockRows<BN, NT>(a.h.x, a.h.dp, (int64_t)tn * BN, 0);
+      if constexpr (kMany) ask_info<BN, WM * WN, Back>(a.h, (int64_t)tn * BN, info[turn ^ 1]);
       P::template ask<true, false>(w, x, a.k, lds);
     }
-    finish_scores<T, BN, WM, WN, Back>(a, p, second, n0, v0, tile);
+    const TokenInfo<BN> its{kMany ? (const float(*)[BN])info[turn] : nullptr, a.h, n0};
+    finish_scores<T, BN, WM, WN, Back>(a, p, second, n0, v0, tile, its, mul);
+    if (kMany) turn ^= 1;
   }
 }
 
