@@ -10,6 +10,7 @@
 // bound by memory.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "common.hpp"
 
@@ -72,6 +73,56 @@ struct Share {
     else load_as<_Float16>(v, row);
   }
 
+  // A row as it lies, B bytes an element, for a later look at it: the loads of the
+  // next row are in flight while this one is worked on.
+  template <int B>
+  struct Raw {
+    Pack<uint32_t, E * B / 4> v[C];
+  };
+  template <int B>
+  __device__ __forceinline__ void load_raw(Raw<B>& r, const char* row) const {
+    struct __attribute__((packed, aligned(2))) Any {
+      uint32_t v[E * B / 4];
+    };
+    if (dim >= E) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) {
+        const Any x = *(const Any*)(row + at[c] * B);
+        r.v[c] = __builtin_bit_cast(Pack<uint32_t, E * B / 4>, x);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < E * B / 4; ++e) {
+          if constexpr (B == 4) r.v[c].v[e] = mine(c, e) ? ((const uint32_t*)row)[at[c] + e] : 0u;
+          else
+            r.v[c].v[e] = (mine(c, 2 * e) ? ((const uint16_t*)row)[at[c] + 2 * e] : 0u) |
+                          (mine(c, 2 * e + 1) ? (uint32_t)((const uint16_t*)row)[at[c] + 2 * e + 1] << 16 : 0u);
+        }
+    }
+  }
+  template <int B>
+  __device__ __forceinline__ void values(float (&v)[C][E], const Raw<B>& r, int32_t type) const {
+    if constexpr (B == 4) {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[c][e] = __uint_as_float(r.v[c].v[e]);
+    } else if (type == FS_BF16) {  // uniform
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[c][e] = bf16_bits_to_f32(e & 1 ? r.v[c].v[e / 2] >> 16 : r.v[c].v[e / 2] & 0xffffu);
+    } else {
+#pragma unroll
+      for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          v[c][e] = (float)__builtin_bit_cast(_Float16, (uint16_t)(r.v[c].v[e / 2] >> (16 * (e & 1))));
+    }
+  }
+
   template <typename T>
   __device__ __forceinline__ void store_as(const float (&v)[C][E], char* row) const {
     if (dim >= E) {
@@ -97,30 +148,47 @@ struct Share {
   }
 };
 
-// Two sums over the L lanes of a row; with more than a wave the whole
-// workgroup shares the row. `tmp` holds 2 x 16 pairs, taken in turn: a pair is
-// written again only behind the other's barrier.
-template <int L>
-__device__ __forceinline__ void row_sums(float& a, float& b, float (*tmp)[2], int turn) {
-  constexpr int W = L < kWave ? L : kWave;
-#pragma unroll
-  for (int d = W / 2; d > 0; d >>= 1) {
-    a += __shfl_xor(a, d, kWave);
-    b += __shfl_xor(b, d, kWave);
+// Sum over groups of W lanes (8 to 64), the same bits in each of them: exchanges
+// inside 16 lanes cost no instruction of their own, the two wider ones one each.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float x) {
+  auto dpp = [](float v, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value, 0xf, 0xf, true));
+  };
+  x += dpp(x, std::integral_constant<int, 0xb1>());   // lanes 1 0 3 2
+  x += dpp(x, std::integral_constant<int, 0x4e>());   // lanes 2 3 0 1
+  x += dpp(x, std::integral_constant<int, 0x141>());  // 8 lanes mirrored
+  if constexpr (W >= 16) x += dpp(x, std::integral_constant<int, 0x140>());  // 16 lanes mirrored
+  if constexpr (W >= 32) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
   }
+  if constexpr (W >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(r[0]) + __uint_as_float(r[1]);
+  }
+  return x;
+}
+
+// N sums over the L lanes of a row; with more than a wave the whole workgroup
+// shares the row. `tmp` holds 2 x 16 pairs, taken in turn: a pair is written again
+// only behind the other's barrier.
+template <int L, int N>
+__device__ __forceinline__ void row_sums(float (&s)[N], float (*tmp)[2], int turn) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) s[k] = lanes_sum<L < kWave ? L : kWave>(s[k]);
   if constexpr (L > kWave) {
     float(*t)[2] = tmp + 16 * turn;
-    const int w = threadIdx.x / kWave;
     if (lane() == 0) {
-      t[w][0] = a;
-      t[w][1] = b;
+#pragma unroll
+      for (int k = 0; k < N; ++k) t[threadIdx.x / kWave][k] = s[k];
     }
     __syncthreads();
-    a = b = 0.f;
 #pragma unroll
-    for (int i = 0; i < L / kWave; ++i) {
-      a += t[i][0];
-      b += t[i][1];
+    for (int k = 0; k < N; ++k) {
+      s[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < L / kWave; ++i) s[k] += t[i][k];
     }
   }
 }
@@ -162,23 +230,23 @@ __global__ void __launch_bounds__(L > 256 ? L : 256) k_norm(NormArgs a) {
   for (int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / L; r < a.n; r += (int64_t)gridDim.x * per) {
     float v[C][E];
     s.load(v, a.x.p + r * a.x.stride, a.x.type);
-    float sum = 0.f, none = 0.f;
+    float sum[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += s.mine(c, e) ? v[c][e] : 0.f;
-    row_sums<L>(sum, none, tmp, 0);
-    const float mean = sum * a.inv_dim;
-    float sq = 0.f;
+      for (int e = 0; e < E; ++e) sum[0] += s.mine(c, e) ? v[c][e] : 0.f;
+    row_sums<L>(sum, tmp, 0);
+    const float mean = sum[0] * a.inv_dim;
+    float sq[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         v[c][e] -= mean;
-        sq += s.mine(c, e) ? v[c][e] * v[c][e] : 0.f;
+        sq[0] += s.mine(c, e) ? v[c][e] * v[c][e] : 0.f;
       }
-    row_sums<L>(sq, none, tmp, 1);
-    const float rstd = 1.f / sqrtf(sq * a.inv_dim + a.eps);
+    row_sums<L>(sq, tmp, 1);
+    const float rstd = 1.f / sqrtf(sq[0] * a.inv_dim + a.eps);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -224,10 +292,11 @@ __device__ __forceinline__ void join_groups(float (&v)[C][E], float* join) {
 // Each group of L lanes adds its rows' parts of dweight and dbias in registers;
 // a workgroup's groups are joined in LDS, in order, and the workgroups' sums by
 // k_norm_params, in order: equal calls give equal bits.
-template <int E, int L, int C>
-__global__ void __launch_bounds__(1024) k_norm_back(NormArgs a) {
+template <int E, int L, int C, int B>
+__global__ void __launch_bounds__(L > 256 ? L : C * E > 8 ? 512 : 1024) k_norm_back(NormArgs a) {
   extern __shared__ float join[];  // [C E][threads], where a workgroup has more groups than one
   __shared__ float tmp[32][2];
+  constexpr int BX = 16 / E;  // bytes of an element of x; B: of dout
   const int l = threadIdx.x % L, per = blockDim.x / L;
   const Share<E, L, C> s(l, a.dim);
   float w[C][E], dw[C][E], db[C][E];
@@ -244,12 +313,26 @@ __global__ void __launch_bounds__(1024) k_norm_back(NormArgs a) {
 #pragma unroll
     for (int e = 0; e < E; ++e) dw[c][e] = db[c][e] = 0.f;
   int turn = 0;
-  for (int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / L; r < a.n; r += (int64_t)gridDim.x * per) {
+  const int64_t step = (int64_t)gridDim.x * per;
+  int64_t r = (int64_t)blockIdx.x * per + threadIdx.x / L;
+  typename Share<E, L, C>::template Raw<BX> xr;
+  typename Share<E, L, C>::template Raw<B> gr;
+  float mean_r = 0.f, rstd_r = 0.f;
+  auto ask = [&](int64_t row) {
+    s.load_raw(xr, a.x.p + row * a.x.stride);
+    s.load_raw(gr, a.out.p + row * a.out.stride);
+    mean_r = a.mean[row];
+    rstd_r = a.rstd[row];
+  };
+  if (r < a.n) ask(r);
+  for (; r < a.n; r += step) {
     float h[C][E], g[C][E];
-    s.load(h, a.x.p + r * a.x.stride, a.x.type);
-    s.load(g, a.out.p + r * a.out.stride, a.out.type);
-    const float mean = a.mean[r], rstd = a.rstd[r];
-    float sg = 0.f, sgh = 0.f;
+    s.values(h, xr, a.x.type);
+    s.values(g, gr, a.out.type);
+    const float mean = mean_r, rstd = rstd_r;
+    constexpr bool kAhead = L < 1024 || C == 1;  // as registers allow
+    if (kAhead) ask(min(r + step, a.n - 1));
+    float sum[2] = {0.f, 0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -258,18 +341,18 @@ __global__ void __launch_bounds__(1024) k_norm_back(NormArgs a) {
         dw[c][e] += g[c][e] * h[c][e];
         db[c][e] += g[c][e];
         g[c][e] *= w[c][e];
-        sg += s.mine(c, e) ? g[c][e] : 0.f;
-        sgh += s.mine(c, e) ? g[c][e] * h[c][e] : 0.f;
+        sum[0] += s.mine(c, e) ? g[c][e] : 0.f;
+        sum[1] += s.mine(c, e) ? g[c][e] * h[c][e] : 0.f;
       }
-    row_sums<L>(sg, sgh, tmp, turn);
+    row_sums<L>(sum, tmp, turn);
     turn ^= 1;
-    sg *= a.inv_dim;
-    sgh *= a.inv_dim;
+    const float sg = sum[0] * a.inv_dim, sgh = sum[1] * a.inv_dim;
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
       for (int e = 0; e < E; ++e) g[c][e] = rstd * (g[c][e] - sg - h[c][e] * sgh);
     s.store(g, a.dx + r * a.dx_stride, a.x.type);
+    if (!kAhead) ask(min(r + step, a.n - 1));
   }
   if (!a.dweight && !a.dbias) return;
   if (per > 1) {
@@ -390,7 +473,10 @@ struct Backward {
     a.part = blocks > 1 ? part : nullptr;
     *parts = (int32_t)blocks;
     const size_t lds = T > L ? sizeof(float) * C * E * T : 0;
-    hipLaunchKernelGGL((k_norm_back<E, L, C>), dim3((unsigned)blocks), dim3(T), lds, stream, a);
+    if (a.out.type == FS_F32)
+      hipLaunchKernelGGL((k_norm_back<E, L, C, 4>), dim3((unsigned)blocks), dim3(T), lds, stream, a);
+    else
+      hipLaunchKernelGGL((k_norm_back<E, L, C, 2>), dim3((unsigned)blocks), dim3(T), lds, stream, a);
   }
 };
 
@@ -467,6 +553,7 @@ extern "C" int fs_layer_norm_backward(const void* x, int32_t x_dtype, int64_t x_
   a.param = param_dtype;
   a.inv_dim = 1.f / (float)dim;
   a.x.type = x_dtype;
+  a.out.type = dout_dtype;
   float* part = Carve(ws).take<float>(1);
   part = (float*)align_up((size_t)part, 256);
   int32_t parts = 1;

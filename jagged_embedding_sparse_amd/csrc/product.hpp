@@ -67,12 +67,14 @@ struct ReadRows {
 };
 // columns c0 .. c0 + 31 (a multiple of 32) of a tile of 64 rows of R elements.
 template <int R>
+constexpr int kColsSwz = R == 64 ? 64 : 128;
+template <int R>
 struct ReadCols {
   int cols_at;
   __device__ __forceinline__ ReadCols() {
-    const int l = lane(), g = l >> 5, j = l & 15, col = (l & 16) + 4 * (j & 3);
-    const int p = (col >> 3) ^ ((j >> 2) << 2 | 2 * g);
-    cols_at = (8 * g + (j >> 2)) * R + 8 * p + (col & 7);
+    // rows 8 g + j / 4 and 4 more (the permutation of those differs in bit 0)
+    const int l = lane(), g = l >> 5, j = l & 15, col = (l & 16) + 4 * (j & 3), row = 8 * g + (j >> 2);
+    cols_at = row * R + 8 * ((col >> 3) ^ attn::swz<kColsSwz<R>>(row)) + (col & 7);
   }
   __device__ __forceinline__ u32x4 operator()(const uint16_t* tile, int c0, int kk) const {
     const uint16_t* a = tile + (cols_at ^ c0) + 16 * kk * R;
@@ -121,7 +123,8 @@ struct Rows {
 };
 
 // k's apart: a tile of 64 k's, rows of R elements. Piece p of row r lies at
-// p ^ ((r & 3) << 2 | (r >> 2) & 3): see attention.hpp.
+// p ^ ((r & 3) << 2 | (r >> 2) & 3), of rows of 128 bytes at p ^ ((r & 2) << 1 |
+// (r >> 2) & 3): see attention.hpp.
 template <int R, int NT>
 struct Cols {
   static constexpr int kElems = R * kK;
@@ -136,7 +139,7 @@ struct Cols {
 
   static __device__ __forceinline__ int row_of(int x) { return x * kStepRows + (int)threadIdx.x / kPieces; }
   static __device__ __forceinline__ int piece_of(int x) {
-    return ((int)threadIdx.x % kPieces) ^ attn::swz<128>(row_of(x));
+    return ((int)threadIdx.x % kPieces) ^ attn::swz<kColsSwz<R>>(row_of(x));
   }
   // columns col0 .. of `cols_` (a multiple of 8); pieces past the last load the tile's first
   __device__ __forceinline__ Cols(const char* p, int64_t stride, int64_t col0, int64_t cols_, int64_t k0) {
@@ -209,7 +212,7 @@ struct BlockCols {
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
       const int row = x * (NT / kPieces) + (int)threadIdx.x / kPieces;
-      const int piece = ((int)threadIdx.x % kPieces) ^ attn::swz<128>(row);
+      const int piece = ((int)threadIdx.x % kPieces) ^ attn::swz<kColsSwz<R>>(row);
       const int block = col0 + 8 * piece < cols ? piece / 8 : 0;
       at[x] = block * (kBlock * 2) + row * (kK * 2) + 16 * (piece % 8);
     }

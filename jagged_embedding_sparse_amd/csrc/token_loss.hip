@@ -84,6 +84,27 @@ __device__ __forceinline__ bool takes_part(const PackArgs& a, int64_t i, bool* b
   *bad = !in && v != a.pad;
   return in && v != a.pad;
 }
+// Which of tokens i, i + 256, .. take part, eight with their loads in flight
+// together; tokens from `end` on do not.
+constexpr int kAtOnce = 8;
+__device__ __forceinline__ uint32_t take_part(const PackArgs& a, int64_t i, int64_t end) {
+  uint32_t on = 0;
+  if (a.labels) {
+    int64_t v[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) v[u] = a.labels[min(i + u * kPackThreads, end - 1)];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) on |= (uint32_t)(v[u] >= 0 && v[u] < a.rows && v[u] != a.pad) << u;
+  } else {
+    uint8_t v[kAtOnce];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) v[u] = a.live[min(i + u * kPackThreads, end - 1)];
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) on |= (uint32_t)(v[u] != 0) << u;
+  }
+  const int64_t left = cdiv(end - i, kPackThreads);
+  return left < kAtOnce ? on & ((1u << left) - 1) : on;
+}
 
 // Each workgroup counts the tokens before its own that take part (labels are few
 // bytes beside the rows), so one launch does it without waiting for another
@@ -94,10 +115,11 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
   const int64_t i0 = (int64_t)blockIdx.x * a.per, i1 = min(a.h.n, i0 + a.per);
   int32_t count = 0;
   bool bad = false;
-  for (int64_t i = threadIdx.x; i < i0; i += kPackThreads) count += takes_part(a, i, &bad);
+  for (int64_t i = threadIdx.x; i < i0; i += kAtOnce * kPackThreads) count += __popc(take_part(a, i, i0));
   int32_t base;
   block_excl_scan<int32_t>(count, tmp, &base);
   const int32_t pieces = a.h.dp / 8;
+  const bool whole = a.h.dim % 8 == 0;
   for (int64_t c = i0; c < i1; c += kPackThreads) {  // uniform
     const int64_t i = c + threadIdx.x;
     bad = false;
@@ -115,10 +137,23 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
       }
     }
     __syncthreads();
-    for (int32_t u = threadIdx.x; u < total * pieces; u += kPackThreads) {
-      const int32_t r = u / pieces, p = u - r * pieces;
-      *(u32x4*)(a.h.x + 2 * blocked(base + r, 8 * p, a.h.dp)) =
-          row_piece(a.x + (i0 + s_row[r]) * a.x_stride, 8 * p, a.h.dim);
+    const int32_t all = total * pieces;
+    for (int32_t u0 = 0; u0 < all; u0 += 4 * kPackThreads) {  // four pieces of a thread in flight
+      u32x4 v[4];
+      int32_t r[4], p[4];
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int32_t u = min(u0 + y * kPackThreads + (int32_t)threadIdx.x, all - 1);
+        r[y] = u / pieces;
+        p[y] = u - r[y] * pieces;
+        const char* row = a.x + (i0 + s_row[r[y]]) * a.x_stride;
+        if (whole) v[y] = *(const u32x4_any*)(row + 16 * (8 * p[y] < a.h.dim ? p[y] : 0));
+        else v[y] = row_piece(row, 8 * p[y], a.h.dim);
+      }
+#pragma unroll
+      for (int y = 0; y < 4; ++y)
+        *(u32x4*)(a.h.x + 2 * blocked(base + r[y], 8 * p[y], a.h.dp)) =
+            8 * p[y] < a.h.dim ? v[y] : u32x4{0, 0, 0, 0};
     }
     base += total;
     __syncthreads();
@@ -138,8 +173,14 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
     // that takes the largest coefficient to 2^13 .. 2^14, and the sums lose it again
     float top = 0.f;
     if (a.narrow) {
-      for (int64_t i = threadIdx.x; i < a.h.n; i += kPackThreads)
-        if (takes_part(a, i, &bad)) top = fmaxf(top, fabsf(a.dloss[i] * a.scale));
+      for (int64_t i = threadIdx.x; i < a.h.n; i += kAtOnce * kPackThreads) {
+        float d[kAtOnce];
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) d[u] = a.dloss[min(i + u * kPackThreads, a.h.n - 1)];
+        const uint32_t on = take_part(a, i, a.h.n);
+#pragma unroll
+        for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, on >> u & 1 ? fabsf(d[u] * a.scale) : 0.f);
+      }
 #pragma unroll
       for (int d = kWave / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
       if (lane() == 0) s_max[threadIdx.x / kWave] = top;
@@ -534,10 +575,10 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_grad_x(SumArgs a) {
 }
 
 // dw = e^T x over a part of the tokens.
-template <typename T>
-__global__ void __launch_bounds__(kWM * kWN * kWave) k_grad_w(SumArgs a) {
-  constexpr int WM = kWM, WN = kWN, NT = WM * WN * kWave;
-  using P = Tile<T, BlockCols<kD, NT>, BlockCols<kV, NT>, kD, kV, WM, WN>;
+template <typename T, int BV, int WM, int WN>
+__global__ void __launch_bounds__(WM * WN * kWave) k_grad_w(SumArgs a) {
+  constexpr int NT = WM * WN * kWave;
+  using P = Tile<T, BlockCols<kD, NT>, BlockCols<BV, NT>, kD, BV, WM, WN>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
   const int32_t tiles = a.order.rows * a.order.cols, id = in_order(blockIdx.x, gridDim.x);
   int32_t tv, td;
@@ -548,11 +589,11 @@ __global__ void __launch_bounds__(kWM * kWN * kWave) k_grad_w(SumArgs a) {
   const int64_t s0 = min(steps, part * per), s1 = min(steps, s0 + per);
   P p;
   BlockCols<kD, NT> x(a.h.x, a.h.dp, td * kD, s0 * kK);
-  BlockCols<kV, NT> e(a.e, a.e_cols, (int64_t)tv * kV, s0 * kK);
+  BlockCols<BV, NT> e(a.e, a.e_cols, (int64_t)tv * BV, s0 * kK);
   P::template ask<false, false>(x, e, (s1 - s0) * kK, lds);
   p.template run<false, false>(x, e, (s1 - s0) * kK, lds);
   float* to = a.part ? a.part + (int64_t)part * a.out_rows * a.h.dp : nullptr;
-  put_sums<T, P, kV, WM>(p, lds, a, to, (int64_t)tv * kV, a.out_rows, td * kD);
+  put_sums<T, P, BV, WM>(p, lds, a, to, (int64_t)tv * BV, a.out_rows, td * kD);
 }
 
 // The parts of a sum, added in order and rounded once. Rows of pos < 0 are zeros.
@@ -566,21 +607,41 @@ struct JoinArgs {
   char* out;
   int64_t out_stride;
 };
-template <typename T>
+// PL lanes share the parts of 4 columns of a row.
+template <typename T, int PL>
 __global__ void __launch_bounds__(256) k_join(JoinArgs a) {
+  constexpr int kPer = 256 / PL;
+  __shared__ f32x4 sh[PL][kPer];
   const int32_t pieces = (int32_t)cdiv(a.dim, 4);
   const float back = a.mul[1];
-  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < a.rows * pieces; u += (int64_t)gridDim.x * 256) {
-    const int64_t row = u / pieces;
+  const int x = threadIdx.x % kPer, y = threadIdx.x / kPer;
+  for (int64_t u0 = (int64_t)blockIdx.x * kPer; u0 < a.rows * pieces; u0 += (int64_t)gridDim.x * kPer) {  // uniform
+    const int64_t u = u0 + x, row = u / pieces;
+    const bool in = u < a.rows * pieces;
     const int32_t col = 4 * (int32_t)(u - row * pieces);
-    const int64_t r = a.pos ? a.pos[row] : row;
+    const int64_t r = !in ? -1 : a.pos ? a.pos[row] : row;
     f32x4 s = {0.f, 0.f, 0.f, 0.f};
     if (r >= 0) {
       const f32x4* p = (const f32x4*)(a.part + r * a.dp + col);
       const int64_t step = a.part_rows * a.dp / 4;
-      for (int i = 0; i < a.parts; ++i) s += p[i * step];
-      s *= back;
+      int i = y;
+      for (; i + 3 * PL < a.parts; i += 4 * PL) {
+        f32x4 v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = p[(i + k * PL) * step];
+        s += (v[0] + v[1]) + (v[2] + v[3]);
+      }
+      for (; i < a.parts; i += PL) s += p[i * step];
     }
+    if constexpr (PL > 1) {
+      __syncthreads();
+      sh[y][x] = s;
+      __syncthreads();
+      if (y || !in) continue;
+      for (int i = 1; i < PL; ++i) s += sh[i][x];
+    }
+    if (!in) continue;
+    s *= back;
     T* to = (T*)(a.out + row * a.out_stride) + col;
     struct __attribute__((packed, aligned(sizeof(T)))) Four {
       T v[4];
@@ -733,46 +794,45 @@ struct Teacher {
   }
 };
 
-// Scores of a token's entries, and its loss. A wave's lanes share the elements
-// of a row; four rows are in flight.
+// Scores of a token's entries, and its loss. A workgroup's waves take the entries
+// in turn, eight of their rows in flight, a row's elements shared by the lanes.
 template <typename T>
 __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a) {
-  __shared__ float s_z[kRowsPerGroup][FS_MAX_TOP];
-  const int w = threadIdx.x / kWave;
-  const int64_t i = (int64_t)blockIdx.x * kRowsPerGroup + w;
-  if (i >= a.h.n) return;
+  __shared__ int64_t s_id[FS_MAX_TOP];
+  __shared__ float s_z[FS_MAX_TOP];
+  const int w = attn::wave_id(), l = lane();
+  const int64_t i = blockIdx.x;
   const int32_t pos = a.h.pos[i];
-  const int l = lane();
   if (pos < 0) {
-    for (int k = l; k < a.top; k += kWave) a.logits[i * a.top + k] = 0.f;
-    if (l == 0) a.loss[i] = 0.f;
+    for (int k = threadIdx.x; k < a.top; k += kRowsPerGroup * kWave) a.logits[i * a.top + k] = 0.f;
+    if (threadIdx.x == 0) a.loss[i] = 0.f;
     return;
   }
-  const Teacher t(a, i);
-  for (int k0 = 0; k0 < a.top; k0 += 4) {
-    const char* row[4];
-    float sum[4];
+  for (int k = threadIdx.x; k < a.top; k += kRowsPerGroup * kWave) {
+    const int64_t id = a.ids[i * a.top + k];
+    s_id[k] = entry_on(a, id, teacher_at(a, i * a.top + k)) ? id : -1;
+  }
+  __syncthreads();
+  constexpr int kRows = 8;
+  for (int k0 = w; k0 < a.top; k0 += kRows * kRowsPerGroup) {  // uniform in a wave
+    int64_t id[kRows];
+    float sum[kRows];
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int k = min(k0 + u, a.top - 1);
-      int64_t id = 0;
-      bool on = false;
-#pragma unroll
-      for (int y = 0; y < kPerLane; ++y)
-        if (k / kWave == y) {
-          id = __shfl(t.id[y], k % kWave, kWave);
-          on = __shfl((int)t.on[y], k % kWave, kWave);
-        }
-      row[u] = on ? a.w + id * a.w_stride : nullptr;
+    for (int u = 0; u < kRows; ++u) {
+      const int k = k0 + u * kRowsPerGroup;
+      id[u] = k < a.top ? s_id[k] : -1;
       sum[u] = 0.f;
     }
     for (int c = 8 * l; c < a.h.dim; c += 8 * kWave) {
       const u32x4 xv = *(const u32x4*)(a.h.x + 2 * blocked(pos, c, a.h.dp));
-      u32x4 wv[4];
+      u32x4 wv[kRows];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) wv[u] = row[u] ? row_piece(row[u], c, a.h.dim) : u32x4{0, 0, 0, 0};
+      for (int u = 0; u < kRows; ++u) {
+        wv[u] = u32x4{0, 0, 0, 0};
+        if (id[u] >= 0) wv[u] = row_piece(a.w + id[u] * a.w_stride, c, a.h.dim);
+      }
 #pragma unroll
-      for (int u = 0; u < 4; ++u)
+      for (int u = 0; u < kRows; ++u)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const auto p = Elem<T>::unpack(xv[e]), y = Elem<T>::unpack(wv[u][e]);
@@ -781,20 +841,22 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
         }
     }
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const float z = row[u] ? wave_sum(sum[u]) * a.scale : 0.f;
-      if (l == 0 && k0 + u < a.top) s_z[w][k0 + u] = z;
+    for (int u = 0; u < kRows; ++u) {
+      const float z = wave_sum(sum[u]) * a.scale;
+      const int k = k0 + u * kRowsPerGroup;
+      if (l == 0 && k < a.top) s_z[k] = id[u] >= 0 ? z : 0.f;
     }
   }
-  __builtin_amdgcn_wave_barrier();
-  __threadfence_block();
+  __syncthreads();
+  if (w) return;
+  const Teacher t(a, i);
   const float lse = a.lse[i];
   float loss = 0.f;
 #pragma unroll
   for (int u = 0; u < kPerLane; ++u) {
     const int k = l + kWave * u;
     if (k < a.top) {
-      const float z = s_z[w][k];
+      const float z = s_z[k];
       a.logits[i * a.top + k] = z;
       if (t.on[u] && t.q[u] != 0.f) loss += t.q[u] * (t.logq[u] - z + lse);
     }
@@ -844,18 +906,20 @@ struct Sizes {
 int64_t most_parts(int64_t steps) { return std::min<int64_t>(kMostParts, std::max<int64_t>(1, steps / 4)); }
 
 // In how many parts a product is cut, so that few tiles do not leave CUs idle: the
-// number for which its rounds of workgroups (a CU each) take the least time, with
-// the sums that every part writes and somebody reads. A step of 64 takes a
-// workgroup 1.8 us, its start and end about 6, and memory 5 bytes in a ps.
-// (256 tiles of 256 steps in two parts 503 us, in one @@; 96 tiles of 1024 in one part
-// @@, in 8 @@.)
-int32_t parts_of(int64_t tiles, int64_t steps, int64_t bytes_each, int64_t bytes) {
+// number for which its rounds of workgroups take the least time, with the sums that
+// every part writes and somebody reads. Measured: a step of 64 takes a workgroup 1.8
+// us in tiles of 256 x 256 (one to a CU) and 0.9 in tiles of 64 rows (two to a CU),
+// its start and end about 6, memory gives 5 bytes in a ps. 256 tiles of 256 steps:
+// in two parts 479 us, in one 453.
+int32_t parts_of(int64_t tiles, int64_t steps, int32_t rows, int64_t bytes_each, int64_t bytes) {
   const int64_t most = std::min(most_parts(steps), std::max<int64_t>(1, bytes / std::max<int64_t>(bytes_each, 1)));
+  const int64_t at_once = rows == 64 ? 2 * kCus : kCus;
+  const double step = rows == 64 ? 0.9 : 1.8;
   int32_t best = 1;
   double least = 1e300;
   for (int64_t p = 1; p <= most; ++p) {
-    const double us = (double)cdiv(tiles * p, kCus) * ((double)cdiv(steps, p) * 1.8 + 6.0) +
-                      (p > 1 ? 4.0 : 0.0) + 2e-6 * (double)(p * bytes_each) / 5.0;
+    const double us = (double)cdiv(tiles * p, at_once) * ((double)cdiv(steps, p) * step + 6.0) +
+                      (p > 1 ? 5.0 : 0.0) + 2e-6 * (double)(p * bytes_each) / 5.0;
     if (us < least) {
       least = us;
       best = (int32_t)p;
@@ -955,7 +1019,7 @@ int piece_of(const Table& t, const Sizes& s, int64_t v0, int64_t rows, char* pac
 }
 
 int pack_tokens(PackArgs a, hipStream_t stream) {
-  const int64_t per = std::max<int64_t>(64, cdiv(a.h.n, 256));
+  const int64_t per = std::max<int64_t>(16, cdiv(a.h.n, 1024));
   a.per = (int32_t)per;
   const int64_t blocks = std::max<int64_t>(1, cdiv(a.h.n, per));
   hipLaunchKernelGGL(k_head_pack, dim3((unsigned)blocks), dim3(kPackThreads), 0, stream, a);
@@ -985,12 +1049,27 @@ void launch_grad_x(const SumArgs& a, const Sizes& s, dim3 g, hipStream_t stream)
   else hipLaunchKernelGGL((k_grad_x<T, 64, 8, 1>), g, dim3(8 * kWave), 0, stream, a);
 }
 
+template <typename T>
+void launch_grad_w(const SumArgs& a, int32_t bv, dim3 g, hipStream_t stream) {
+  if (bv == 256) hipLaunchKernelGGL((k_grad_w<T, 256, kWM, kWN>), g, dim3(kWM * kWN * kWave), 0, stream, a);
+  else hipLaunchKernelGGL((k_grad_w<T, 64, 8, 1>), g, dim3(8 * kWave), 0, stream, a);
+}
+
+template <typename T>
+void launch_join_as(const JoinArgs& a, hipStream_t stream) {
+  // many parts, few rows: 8 lanes share them (63 parts of 64 x 64: 19 -> 4.6 us; 8
+  // parts of 8192 x 768: 38 by one lane, 53 by eight)
+  const bool share = a.parts >= 8 && a.rows * a.dim <= ((int64_t)1 << 19);
+  const int64_t per = share ? 32 : 256, work = cdiv(a.rows * cdiv(a.dim, 4), per);
+  const dim3 g((unsigned)std::max<int64_t>(1, std::min<int64_t>(work, 16384))), b(256);
+  if (share) hipLaunchKernelGGL((k_join<T, 8>), g, b, 0, stream, a);
+  else hipLaunchKernelGGL((k_join<T, 1>), g, b, 0, stream, a);
+}
+
 int launch_join(const JoinArgs& a, int32_t type, hipStream_t stream) {
-  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>(cdiv(a.rows * cdiv(a.dim, 4), 256), 16384));
-  const dim3 g((unsigned)blocks), b(256);
-  if (type == FS_F32) hipLaunchKernelGGL(k_join<float>, g, b, 0, stream, a);
-  else if (type == FS_BF16) hipLaunchKernelGGL(k_join<__bf16>, g, b, 0, stream, a);
-  else hipLaunchKernelGGL(k_join<_Float16>, g, b, 0, stream, a);
+  if (type == FS_F32) launch_join_as<float>(a, stream);
+  else if (type == FS_BF16) launch_join_as<__bf16>(a, stream);
+  else launch_join_as<_Float16>(a, stream);
   FS_LAUNCH_CHECK();
   return FS_OK;
 }
@@ -1064,7 +1143,7 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
   const int64_t step = t.direct ? s.piece : std::min(s.piece, s.pack_rows);
   const int32_t token_tiles = (int32_t)cdiv(s.n, s.bn), col_tiles = (int32_t)cdiv(s.dim, kD);
   const int32_t x_parts = parts_of((int64_t)token_tiles * col_tiles, cdiv(std::min(step, s.rows), kK),
-                                   s.npad * s.dp * 4, s.dx_part);
+                                   s.bn, s.npad * s.dp * 4, s.dx_part);
   for (int64_t v0 = 0; v0 < s.rows; v0 += step) {
     ScoreArgs a = {};
     a.h = o.h;
@@ -1110,9 +1189,12 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
       FS_LAUNCH_CHECK();
     }
     if (g.dw) {
-      const int64_t tiles = (int64_t)table_tiles * col_tiles;
-      const int32_t parts = parts_of(tiles, cdiv(s.n, kK), a.rows * s.dp * 4, s.dw_part);
-      b.order = Order{table_tiles, col_tiles};
+      // tiles of 64 rows where those of 256 would leave CUs idle
+      const int32_t bv = (int64_t)table_tiles * col_tiles < kCus ? 64 : kV;
+      const int32_t row_tiles = (int32_t)cdiv(a.rows, bv);
+      const int64_t tiles = (int64_t)row_tiles * col_tiles;
+      const int32_t parts = parts_of(tiles, cdiv(s.n, kK), bv, a.rows * s.dp * 4, s.dw_part);
+      b.order = Order{row_tiles, col_tiles};
       b.parts = parts;
       b.add = 0;
       b.part = parts > 1 ? o.dw_part : nullptr;
@@ -1121,9 +1203,9 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
       b.out_rows = a.rows;
       b.out_type = g.dw_type;
       if (!grid_fits(tiles * parts, kMostThreads)) return FS_ERR_UNSUPPORTED;
-      const dim3 grid((unsigned)(tiles * parts)), block(kWM * kWN * kWave);
-      if (dtype == FS_BF16) hipLaunchKernelGGL(k_grad_w<__bf16>, grid, block, 0, stream, b);
-      else hipLaunchKernelGGL(k_grad_w<_Float16>, grid, block, 0, stream, b);
+      const dim3 grid((unsigned)(tiles * parts));
+      if (dtype == FS_BF16) launch_grad_w<__bf16>(b, bv, grid, stream);
+      else launch_grad_w<_Float16>(b, bv, grid, stream);
       FS_LAUNCH_CHECK();
       if (parts > 1) {
         const JoinArgs j{o.dw_part, a.rows, parts, s.dp, s.dim, nullptr, a.rows, o.h.mul, b.out, g.dw_stride};
@@ -1140,7 +1222,7 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
 
 // a grid of any launch of a call, by its sizes
 bool too_many(const Sizes& s) {
-  return !grid_fits(cdiv(s.npad, 64) * s.tiles, kMostThreads) || !grid_fits(s.npad, 64);
+  return !grid_fits(cdiv(s.npad, 64) * s.tiles, kMostThreads) || !grid_fits(s.npad, kRowsPerGroup * kWave);
 }
 
 PackArgs pack_args(const Space& o, const Sizes& s, const void* x, int64_t x_stride, const int64_t* labels,
@@ -1273,7 +1355,7 @@ extern "C" int fs_token_distill(const void* x, int64_t x_stride, int64_t n, cons
   a.loss = loss;
   a.logits = logits;
   a.lse = lse;
-  const dim3 grid((unsigned)cdiv(n, kRowsPerGroup)), block(kRowsPerGroup * kWave);
+  const dim3 grid((unsigned)n), block(kRowsPerGroup * kWave);
   if (table->dtype == FS_BF16) hipLaunchKernelGGL(k_distill<__bf16>, grid, block, 0, stream, a);
   else hipLaunchKernelGGL(k_distill<_Float16>, grid, block, 0, stream, a);
   FS_LAUNCH_CHECK();
