@@ -33,6 +33,13 @@ constexpr int kK = 64;        // k's of a step
 
 typedef __attribute__((address_space(3))) uint16_t* lds_ptr;
 
+// A value that the compiler takes for new each time, so that what follows from it
+// is not kept in registers over a loop.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // 16 bytes per lane from base + at to LDS address `to` + 16 lane. M0 is put back:
 // the compiler does not let an asm declare that it changes it.
 __device__ __forceinline__ void load_piece(const char* base, uint32_t at, uint32_t to) {
@@ -96,10 +103,8 @@ struct Rows {
   uint32_t row_bytes;
   int32_t last;
 
-  static __device__ __forceinline__ int row_of(int x) { return x * (NT / 8) + (int)threadIdx.x / 8; }
-  static __device__ __forceinline__ int piece_of() {
-    return ((int)threadIdx.x % 8) ^ attn::swz<kK>((int)threadIdx.x / 8);
-  }
+  static __device__ __forceinline__ int row_of(int x, int t) { return x * (NT / 8) + t / 8; }
+  static __device__ __forceinline__ int piece_of(int t) { return (t % 8) ^ attn::swz<kK>(t / 8); }
   // rows row0 .. of `rows` rows; rows past the last load it again
   __device__ __forceinline__ Rows(const char* p, int64_t stride, int64_t row0, int64_t rows, int64_t k0) {
     base = attn::uniform(p + row0 * stride + k0 * 2);
@@ -109,9 +114,9 @@ struct Rows {
   }
   // pieces of k's past `left` load the step's first
   __device__ __forceinline__ void limit(int left) {
-    const int p = 8 * piece_of() < left ? piece_of() : 0;
+    const int t = here(threadIdx.x), p = 8 * piece_of(t) < left ? piece_of(t) : 0;
 #pragma unroll
-    for (int x = 0; x < kPer; ++x) at[x] = (uint32_t)min(row_of(x), last) * row_bytes + 16 * p;
+    for (int x = 0; x < kPer; ++x) at[x] = (uint32_t)min(row_of(x, t), last) * row_bytes + 16 * p;
   }
   // piece x of the next step's tile; then the step after it
   __device__ __forceinline__ void load(uint32_t tile, int x) const {
@@ -235,6 +240,12 @@ struct Tile {
   static_assert(MI >= 1 && NI >= 1, "whole blocks");
   f32x16 acc[MI][NI];
 
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NI; ++j) acc[i][j] = attn::zero16();
+  }
   static __device__ __forceinline__ int m_of(int mi, int l = lane()) {
     return (attn::wave_id() % WM * MI + mi) * 32 + 4 * (l >> 5);
   }
@@ -264,7 +275,7 @@ struct Tile {
     if (k > 0) ask_step<LimA, LimB>(a, b, k, 0, lds_address(lds));
   }
 
-  // The product over `k` k's in steps of 64, behind ask(); in the last step the
+  // Adds the product over `k` k's in steps of 64, behind ask(); in the last step the
   // operands are told how many are left where Lim says so. lds: 2 kStage elements.
   // The stages are free again when it returns, the second one before it begins.
   // Since ask() the wave has issued `After` memory operations or more (of which
@@ -279,10 +290,6 @@ struct Tile {
     const typename A::Read ra;
     const typename B::Read rb;
     const uint32_t lds0 = lds_address(lds);
-#pragma unroll
-    for (int i = 0; i < MI; ++i)
-#pragma unroll
-      for (int j = 0; j < NI; ++j) acc[i][j] = attn::zero16();
     const int steps = (int)cdiv(k, (int64_t)kK);
     if (steps <= 0) return;
     if (After == 0 || fresh) landed();

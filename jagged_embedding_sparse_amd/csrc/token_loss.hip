@@ -32,6 +32,8 @@ constexpr int64_t kPieceBytes = (int64_t)1 << PB;  // e of one piece of the tabl
 constexpr int64_t kPackBytes = (int64_t)1 << 26;   // a piece of a table that has to be laid out
 constexpr int64_t kPartBytes = (int64_t)1 << 28;   // sums of a cut product
 constexpr int kMostParts = 64;
+constexpr int64_t kFew = 256;
+constexpr int64_t kCacheBytes = (int64_t)1 << 27;  // half of the last level
 
 // What the kernels of one call share, in its workspace.
 struct Head {
@@ -227,8 +229,14 @@ struct ScoreArgs {
   float scale2;      // scale log2(e)
   float2* part;      // forward: [tiles of the table][npad] maximum and sum, base 2
   float* at_label;   // forward: [npad] the label's score, base 2
-  char* e;           // backward: [npad][e_cols] 16 bits in blocks
-  int64_t e_cols;
+  // backward: [npad][e_cols] 16 bits in blocks. Up to kFew tokens e is two numbers,
+  // rounded and what the rounding left, the second e_half bytes behind: few
+  // tokens' gradients have few terms to average a rounding over (64 tokens: dx off
+  // by 3.2e-4 of its size in one number, fp16, where its own rounding is 2.1e-4),
+  // and their time goes elsewhere.
+  char* e;
+  int64_t e_cols, e_half;
+  int32_t past;
 };
 
 // waves of a tile: 256 x 256 and 256 x 64
@@ -240,13 +248,6 @@ constexpr int kWM = W_M, kWN = W_N;
 constexpr int kMostThreads = 512;
 constexpr int kCus = 256;
 constexpr int kGroup = 8;  // token tiles that go by a table tile together
-
-// A value that the compiler takes for new each time, so that what follows from it
-// is not kept in registers over a loop.
-__device__ __forceinline__ int here(int x) {
-  asm volatile("" : "+v"(x));
-  return x;
-}
 
 // label, lse2 and coef of a tile's tokens, to LDS without registers: a wait for
 // them would wait for the next tile's loads as well
@@ -280,7 +281,7 @@ struct TokenInfo {
 
 // What a tile's scores leave behind, by way of the stage that the next tile's
 // first loads do not write.
-template <typename T, int BN, int WM, int WN, bool Back, typename P>
+template <typename T, int BN, int WM, int WN, int Halves, typename P>
 __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t* lds, int64_t n0, int64_t v0,
                                               int32_t tv, const TokenInfo<BN>& info, float mul) {
   constexpr int NT = WM * WN * kWave;
@@ -295,27 +296,37 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
       for (int j = 0; j < P::NI; ++j) p.acc[i][j] = a.scale2 < 0.f ? -p.acc[i][j] : attn::zero16();
   }
   const float scale2 = a.scale2 == 0.f ? 1.f : fabsf(a.scale2);
-  if constexpr (!Back) {
+  if (left < kV) {  // rows past the table: exp 0
+    const int d = left - P::m_of(0, l);
+#pragma unroll
+    for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+      for (int j = 0; j < P::NI; ++j)
+#pragma unroll
+        for (int r = 0; r < 16; ++r)
+          if (32 * i + 8 * (r >> 2) + (r & 3) >= d) p.acc[i][j][r] = -INFINITY;
+  }
+  // the product at column m of a lane's row, where the lane has it
+  auto product_at = [&](int j, int m) {
+    const int d = here(m - P::m_of(0, l));
+    float v = 0.f;
+#pragma unroll
+    for (int i = 0; i < P::MI; ++i)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) v = 32 * i + 8 * (r >> 2) + (r & 3) == d ? p.acc[i][j][r] : v;
+    return v;
+  };
+  auto has = [&](int m) {  // m of the tile
+    return m / 32 / P::MI == attn::wave_id() % WM && (m >> 2 & 1) == l >> 5;
+  };
+  if constexpr (Halves == 0) {
     float2(*s_part)[BN] = (float2(*)[BN])lds;
     static_assert(2 * P::kStage >= WM * BN * 8, "a stage holds them");
 #pragma unroll
     for (int j = 0; j < P::NI; ++j) {
       const int n = P::n_of(j, l);
       const int64_t lab = (int64_t)info.label(n) - a.v0 - v0;
-      if (lab >= 0 && lab < kV) {
-#pragma unroll
-        for (int i = 0; i < P::MI; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (P::m_of(i, l) + 8 * (r >> 2) + (r & 3) == lab) a.at_label[n0 + n] = p.acc[i][j][r] * scale2;
-      }
-      if (left < kV) {
-#pragma unroll
-        for (int i = 0; i < P::MI; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (P::m_of(i, l) + 8 * (r >> 2) + (r & 3) >= left) p.acc[i][j][r] = -INFINITY;
-      }
+      if (lab >= 0 && lab < kV && has((int)lab)) a.at_label[n0 + n] = product_at(j, (int)lab) * scale2;
       float top = p.acc[0][j][0];
 #pragma unroll
       for (int i = 0; i < P::MI; ++i)
@@ -345,59 +356,57 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
   } else {
     constexpr int kRows = WN * 32;
     static_assert(P::kStage >= kRows * kV, "a stage holds a pass of e");
-#pragma unroll
-    for (int j = 0; j < P::NI; ++j) {
-      if (j) lds_barrier();
-      const int n = P::n_of(j, l), s = attn::wave_id() / WM * 32 + (l & 31);
-      const int64_t lab = (int64_t)info.label(n) - a.v0 - v0;
-      const float lse2 = info.lse2(n), c = info.coef(n) * mul;
-      // c exp2(s) = exp2(s + log2 c): the factor costs no instruction of its own
-      const float at = __builtin_amdgcn_logf(fabsf(c)) - lse2;
-      const uint32_t sign = c < 0.f ? 0x80008000u : 0u;
-#pragma unroll
-      for (int i = 0; i < P::MI; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int m = P::m_of(i, l) + 8 * q;
-          float v[4];
-#pragma unroll
-          for (int r = 0; r < 4; ++r)
-            v[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][4 * q + r], scale2, at));
-          u32x2 y;
-          y[0] = Elem<T>::pack(v[0], v[1]) ^ sign;
-          y[1] = Elem<T>::pack(v[2], v[3]) ^ sign;
-          Stage16<kV>::put(lds, s, m, y);
+    for (int half = 0; half < Halves; ++half) {
+      auto rounded = [&](float x, float y) {
+        uint32_t u = Elem<T>::pack(x, y);
+        if (half) {  // uniform
+          const auto back = Elem<T>::unpack(u);
+          u = Elem<T>::pack(x - back[0], y - back[1]);
         }
-      // the label's place, from the difference; places past the table
-      if (lab >= 0 && lab < kV) {
+        return u;
+      };
+#pragma unroll
+      for (int j = 0; j < P::NI; ++j) {
+        if (j || half) lds_barrier();
+        const int n = P::n_of(j, l), s = attn::wave_id() / WM * 32 + (l & 31);
+        const int64_t lab = (int64_t)info.label(n) - a.v0 - v0;
+        const float lse2 = info.lse2(n), c = info.coef(n) * mul;
+        // c exp2(s) = exp2(s + log2 c): the factor costs no instruction of its own
+        const float at = __builtin_amdgcn_logf(fabsf(c)) - lse2;
+        const uint32_t sign = c < 0.f ? 0x80008000u : 0u;
 #pragma unroll
         for (int i = 0; i < P::MI; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; ++r)
-            if (P::m_of(i, l) + 8 * (r >> 2) + (r & 3) == lab) {
-              const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][r], scale2, -lse2)) - 1.f;
-              Stage16<kV>::put1(lds, s, (int)lab, Elem<T>::pack(v * c, 0.f));
-            }
-      }
-      if (left < kV) {
+          for (int q = 0; q < 4; ++q) {
+            const int m = P::m_of(i, l) + 8 * q;
+            float v[4];
 #pragma unroll
-        for (int i = 0; i < P::MI; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int m = P::m_of(i, l) + 8 * (r >> 2) + (r & 3);
-            if (m >= left) Stage16<kV>::put1(lds, s, m, 0);
+            for (int r = 0; r < 4; ++r)
+              v[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][4 * q + r], scale2, at));
+            u32x2 y;
+            y[0] = rounded(v[0], v[1]) ^ sign;
+            y[1] = rounded(v[2], v[3]) ^ sign;
+            Stage16<kV>::put(lds, s, m, y);
           }
-      }
-      lds_barrier();
-      constexpr int kPieces = kV / 8;
+        // the label's place, from the difference
+        if (lab >= 0 && lab < kV && has((int)lab)) {
+          const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(product_at(j, (int)lab), scale2, -lse2)) - 1.f;
+          Stage16<kV>::put1(lds, s, (int)lab, rounded(v * c, 0.f));
+        }
+        lds_barrier();
+        constexpr int kPieces = kV / 8;
 #pragma unroll 4
-      for (int y = 0; y < kRows * kPieces / NT; ++y) {  // block by block
-        const int u = y * NT + tid, r = u / 8 % kRows, piece = u / (8 * kRows) * 8 + u % 8;
-        // past the caches, which hold the operands of the tiles beside this one
-        // (597 -> 565 us, and the product that reads e 503 -> 479)
-        __builtin_nontemporal_store(
-            Stage16<kV>::get(lds, r, piece),
-            (u32x4*)(a.e + 2 * blocked(n0 + (r / 32 * P::NI + j) * 32 + r % 32, v0 + 8 * piece, a.e_cols)));
+        for (int y = 0; y < kRows * kPieces / NT; ++y) {  // block by block
+          const int u = y * NT + tid, r = u / 8 % kRows, piece = u / (8 * kRows) * 8 + u % 8;
+          const u32x4 v = Stage16<kV>::get(lds, r, piece);
+          u32x4* to = (u32x4*)(a.e + half * a.e_half +
+                               2 * blocked(n0 + (r / 32 * P::NI + j) * 32 + r % 32, v0 + 8 * piece, a.e_cols));
+          // what outgrows the caches goes past them: they hold the operands of the
+          // tiles beside this one (597 -> 565 us, and the product that reads e 503
+          // -> 479); less is read from them soon
+          if (Halves == 1 && a.past) __builtin_nontemporal_store(v, to);
+          else *to = v;
+        }
       }
     }
   }
@@ -406,8 +415,9 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
 // One tile of scores. Columns of the product are table rows, its rows tokens:
 // a lane's registers hold one token's scores, so their maximum and sum need one
 // exchange between two lanes and one between waves.
-template <typename T, int BN, int WM, int WN, bool Back>
+template <typename T, int BN, int WM, int WN, int Halves>
 __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
+  constexpr bool Back = Halves > 0;
   constexpr int NT = WM * WN * kWave;
   using P = Tile<T, Rows<kV, NT>, BlockRows<BN, NT>, kV, BN, WM, WN>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
@@ -434,6 +444,7 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
     const int64_t n0 = (int64_t)tn * BN, v0 = (int64_t)tv * kV;
     const int32_t tile = tv;
     P p;
+    p.clear();
     p.template run<true, false, kAfter>(w, x, a.k, lds, id == (int32_t)blockIdx.x);
     if (id + (int32_t)gridDim.x < tiles) {  // the next tile's first loads, behind this one's scores
       order.at(in_order(id + gridDim.x, tiles), kGroup, &tn, &tv);
@@ -443,7 +454,7 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
       P::template ask<true, false>(w, x, a.k, lds);
     }
     const TokenInfo<BN> its{kMany ? (const float(*)[BN])info[turn] : nullptr, a.h, n0};
-    finish_scores<T, BN, WM, WN, Back>(a, p, second, n0, v0, tile, its, mul);
+    finish_scores<T, BN, WM, WN, Halves>(a, p, second, n0, v0, tile, its, mul);
     if (kMany) turn ^= 1;
   }
 }
@@ -456,7 +467,8 @@ struct SumArgs {
   int64_t rows;      // rows of the piece
   int32_t w_cols;
   const char* e;
-  int64_t e_cols;
+  int64_t e_cols, e_half;
+  int32_t halves;    // of e, see ScoreArgs
   Order order;       // of the output's tiles
   int32_t parts;     // of the sum
   int32_t steps;     // of 64, of a part (dx)
@@ -567,10 +579,13 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_grad_x(SumArgs a) {
   const int64_t n0 = (int64_t)tn * BN;
   const int64_t k0 = (int64_t)part * a.steps * kK, k1 = min(a.rows, k0 + (int64_t)a.steps * kK);
   P p;
-  Cols<kD, NT> w(a.w, a.w_stride, td * kD, a.w_cols, k0);
-  BlockRows<BN, NT> e(a.e, a.e_cols, n0, k0);
-  P::template ask<true, false>(w, e, k1 - k0, lds);
-  p.template run<true, false>(w, e, k1 - k0, lds);
+  p.clear();
+  for (int half = 0; half < a.halves; ++half) {
+    Cols<kD, NT> w(a.w, a.w_stride, td * kD, a.w_cols, k0);
+    BlockRows<BN, NT> e(a.e + half * a.e_half, a.e_cols, n0, k0);
+    P::template ask<true, false>(w, e, k1 - k0, lds);
+    p.template run<true, false>(w, e, k1 - k0, lds);
+  }
   put_sums<T, P, BN, WM>(p, lds, a, a.part + (int64_t)part * a.h.npad * a.h.dp, n0, a.h.npad, td * kD);
 }
 
@@ -588,10 +603,13 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_grad_w(SumArgs a) {
   const int64_t steps = cdiv(*a.h.n_live, kK), per = cdiv(steps, a.parts);
   const int64_t s0 = min(steps, part * per), s1 = min(steps, s0 + per);
   P p;
-  BlockCols<kD, NT> x(a.h.x, a.h.dp, td * kD, s0 * kK);
-  BlockCols<BV, NT> e(a.e, a.e_cols, (int64_t)tv * BV, s0 * kK);
-  P::template ask<false, false>(x, e, (s1 - s0) * kK, lds);
-  p.template run<false, false>(x, e, (s1 - s0) * kK, lds);
+  p.clear();
+  for (int half = 0; half < a.halves; ++half) {
+    BlockCols<kD, NT> x(a.h.x, a.h.dp, td * kD, s0 * kK);
+    BlockCols<BV, NT> e(a.e + half * a.e_half, a.e_cols, (int64_t)tv * BV, s0 * kK);
+    P::template ask<false, false>(x, e, (s1 - s0) * kK, lds);
+    p.template run<false, false>(x, e, (s1 - s0) * kK, lds);
+  }
   float* to = a.part ? a.part + (int64_t)part * a.out_rows * a.h.dp : nullptr;
   put_sums<T, P, BV, WM>(p, lds, a, to, (int64_t)tv * BV, a.out_rows, td * kD);
 }
@@ -722,7 +740,8 @@ struct TeacherArgs {
   // backward
   const float* logits_in;
   char* e;
-  int64_t e_cols, v0, piece_rows;
+  int64_t e_cols, e_half, v0, piece_rows;
+  int32_t halves;
 };
 
 constexpr int kRowsPerGroup = 4;  // tokens of a workgroup, a wave each
@@ -893,14 +912,16 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill_entries(Teach
     for (int k = 0; k < a.top; ++k) q += s_id[w][k] == t.id[u] ? s_q[w][k] : 0.f;
     const float z = a.logits_in[i * a.top + l + kWave * u];
     const float e = (__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -lse2)) - q) * c;
-    ((T*)a.e)[blocked(pos, v, a.e_cols)] = (T)e;
+    const int64_t at = blocked(pos, v, a.e_cols);
+    ((T*)a.e)[at] = (T)e;
+    if (a.halves > 1) ((T*)(a.e + a.e_half))[at] = (T)(e - (float)(T)e);
   }
 }
 
 // ---------------------------------------------------------------- host
 struct Sizes {
   int64_t n, rows, npad, vpad, piece, pack_rows, pack_bytes, e_bytes, dx_part, dw_part, tiles;
-  int32_t dim, dp, bn;
+  int32_t dim, dp, bn, halves;
 };
 
 int64_t most_parts(int64_t steps) { return std::min<int64_t>(kMostParts, std::max<int64_t>(1, steps / 4)); }
@@ -940,8 +961,10 @@ Sizes sizes_of(int64_t n, int64_t rows, int32_t dim) {
   s.vpad = (int64_t)align_up((size_t)rows, kV);
   s.tiles = s.vpad / kV;
   // e: all of it, or pieces of kPieceBytes, or of one tile's width
-  s.e_bytes = s.npad <= kPieceBytes / 2 / s.vpad ? s.npad * s.vpad * 2 : std::max(kPieceBytes, s.npad * kV * 2);
-  s.piece = std::min(s.vpad, std::max<int64_t>(kV, s.e_bytes / (s.npad * 2) / kV * kV));
+  s.halves = n <= kFew ? 2 : 1;
+  const int64_t e_rows = s.npad * s.halves;
+  s.e_bytes = e_rows <= kPieceBytes / 2 / s.vpad ? e_rows * s.vpad * 2 : std::max(kPieceBytes, e_rows * kV * 2);
+  s.piece = std::min(s.vpad, std::max<int64_t>(kV, s.e_bytes / (e_rows * 2) / kV * kV));
   s.pack_bytes = std::max(std::min(s.vpad * s.dp * 2, kPackBytes), (int64_t)kV * s.dp * 2);
   s.pack_rows = std::min(s.vpad, std::max<int64_t>(kV, s.pack_bytes / (s.dp * 2) / kV * kV));
   const int64_t dx = s.npad * s.dp * 4, dw = s.vpad * s.dp * 4;
@@ -1027,17 +1050,17 @@ int pack_tokens(PackArgs a, hipStream_t stream) {
   return FS_OK;
 }
 
-template <bool Back>
+template <int Halves>
 int launch_scores(const ScoreArgs& a, const Sizes& s, int32_t dtype, hipStream_t stream) {
   const int64_t grid = (int64_t)a.order.rows * a.order.cols;
   if (!grid_fits(grid, kMostThreads)) return FS_ERR_UNSUPPORTED;
   const dim3 g((unsigned)(s.bn == 256 ? std::min<int64_t>(grid, kCus) : grid)), b((s.bn == 256 ? kWM * kWN : 8) * kWave);
   if (dtype == FS_BF16) {
-    if (s.bn == 256) hipLaunchKernelGGL((k_scores<__bf16, 256, kWM, kWN, Back>), g, b, 0, stream, a);
-    else hipLaunchKernelGGL((k_scores<__bf16, 64, 8, 1, Back>), g, b, 0, stream, a);
+    if (s.bn == 256) hipLaunchKernelGGL((k_scores<__bf16, 256, kWM, kWN, Halves>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((k_scores<__bf16, 64, 8, 1, Halves>), g, b, 0, stream, a);
   } else {
-    if (s.bn == 256) hipLaunchKernelGGL((k_scores<_Float16, 256, kWM, kWN, Back>), g, b, 0, stream, a);
-    else hipLaunchKernelGGL((k_scores<_Float16, 64, 8, 1, Back>), g, b, 0, stream, a);
+    if (s.bn == 256) hipLaunchKernelGGL((k_scores<_Float16, 256, kWM, kWN, Halves>), g, b, 0, stream, a);
+    else hipLaunchKernelGGL((k_scores<_Float16, 64, 8, 1, Halves>), g, b, 0, stream, a);
   }
   FS_LAUNCH_CHECK();
   return FS_OK;
@@ -1109,7 +1132,7 @@ int forward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float
     a.scale2 = scale * kLog2e;
     a.part = o.part;
     a.at_label = o.at_label;
-    if ((rc = launch_scores<false>(a, s, dtype, stream))) return rc;
+    if ((rc = launch_scores<0>(a, s, dtype, stream))) return rc;
   }
   const LossArgs l{o.h, o.part, s.tiles, labels ? o.at_label : nullptr, loss, lse};
   if (s.n < 2048) hipLaunchKernelGGL(k_loss<4>, dim3((unsigned)cdiv(s.n, 4)), dim3(256), 0, stream, l);
@@ -1142,7 +1165,7 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
   int rc;
   const int64_t step = t.direct ? s.piece : std::min(s.piece, s.pack_rows);
   const int32_t token_tiles = (int32_t)cdiv(s.n, s.bn), col_tiles = (int32_t)cdiv(s.dim, kD);
-  const int32_t x_parts = parts_of((int64_t)token_tiles * col_tiles, cdiv(std::min(step, s.rows), kK),
+  const int32_t x_parts = parts_of((int64_t)token_tiles * col_tiles, cdiv(std::min(step, s.rows), kK) * s.halves,
                                    s.bn, s.npad * s.dp * 4, s.dx_part);
   for (int64_t v0 = 0; v0 < s.rows; v0 += step) {
     ScoreArgs a = {};
@@ -1151,15 +1174,20 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
     a.rows = std::min(step, s.rows - v0);
     a.e = o.e;
     a.e_cols = (int64_t)align_up((size_t)a.rows, kV);
+    a.e_half = 2 * s.npad * a.e_cols;
+    a.past = a.e_half > kCacheBytes;
     if ((rc = piece_of(t, s, v0, a.rows, o.pack, &a.w, &a.w_stride, &a.k, stream))) return rc;
     const int32_t table_tiles = (int32_t)cdiv(a.rows, kV);
     a.order = Order{token_tiles, table_tiles};
     a.scale2 = scale * kLog2e;
     if (s.n > 0) {
-      if ((rc = launch_scores<true>(a, s, dtype, stream))) return rc;
+      rc = s.halves == 2 ? launch_scores<2>(a, s, dtype, stream) : launch_scores<1>(a, s, dtype, stream);
+      if (rc) return rc;
       if (entries) {
         entries->e = a.e;
         entries->e_cols = a.e_cols;
+        entries->e_half = a.e_half;
+        entries->halves = s.halves;
         entries->v0 = v0;
         entries->piece_rows = a.rows;
         const dim3 grid((unsigned)cdiv(s.n, kRowsPerGroup)), block(kRowsPerGroup * kWave);
@@ -1176,6 +1204,8 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
     b.w_cols = a.k;
     b.e = a.e;
     b.e_cols = a.e_cols;
+    b.e_half = a.e_half;
+    b.halves = s.halves;
     if (g.dx && s.n > 0) {
       b.order = Order{token_tiles, col_tiles};
       b.parts = x_parts;
@@ -1193,7 +1223,7 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
       const int32_t bv = (int64_t)table_tiles * col_tiles < kCus ? 64 : kV;
       const int32_t row_tiles = (int32_t)cdiv(a.rows, bv);
       const int64_t tiles = (int64_t)row_tiles * col_tiles;
-      const int32_t parts = parts_of(tiles, cdiv(s.n, kK), bv, a.rows * s.dp * 4, s.dw_part);
+      const int32_t parts = parts_of(tiles, cdiv(s.n, kK) * s.halves, bv, a.rows * s.dp * 4, s.dw_part);
       b.order = Order{row_tiles, col_tiles};
       b.parts = parts;
       b.add = 0;

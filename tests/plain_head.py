@@ -124,7 +124,9 @@ def loss_gradients(x, w, lse, dloss, dtype, scale=1.0, pad=-1, labels=None, ids=
     if ids is not None:
         s = (teacher.double() * scale).abs().masked_fill(teacher == -math.inf, 0.0).amax(1, keepdim=True)
         off = off + c.abs() * target * (16 * s + 2 * 280) * U32
-    e_e = off * (1 + u(t)) + u(t) * e.abs()
+    # up to 256 tokens e is two numbers: what the rounding left is rounded once more
+    once = u(t) * u(t) if n <= 256 else u(t)
+    e_e = off * (1 + u(t)) + once * e.abs()
     if t == torch.float16:  # half a step of what is rounded times 2^13 .. 2^14 over the largest
         e_e = e_e + live[:, None] * 2.0 ** -38 * c.abs().max()
     xd, wd = torch.where(live[:, None], x.double(), 0.0), w.double()
