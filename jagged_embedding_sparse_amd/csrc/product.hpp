@@ -130,7 +130,7 @@ struct Rows {
 // k's apart: a tile of 64 k's, rows of R elements. Piece p of row r lies at
 // p ^ ((r & 3) << 2 | (r >> 2) & 3), of rows of 128 bytes at p ^ ((r & 2) << 1 |
 // (r >> 2) & 3): see attention.hpp.
-template <int R, int NT>
+template <int R, int NT, int Hold = 1>
 struct Cols {
   static constexpr int kElems = R * kK;
   static constexpr int kPieces = R / 8;
@@ -140,7 +140,7 @@ struct Cols {
   const char* base;  // of the next step's first row, at the tile's first column
   uint32_t at[kPer];
   uint32_t row_bytes;
-  int32_t cols;
+  int32_t cols, turn = 0;  // a step's tile is loaded Hold times
 
   static __device__ __forceinline__ int row_of(int x) { return x * kStepRows + (int)threadIdx.x / kPieces; }
   static __device__ __forceinline__ int piece_of(int x) {
@@ -163,7 +163,11 @@ struct Cols {
   __device__ __forceinline__ void load(uint32_t tile, int x) const {
     load_piece(base, at[x], tile + attn::wave_id() * (kWave * 16) + x * NT * 16);
   }
-  __device__ __forceinline__ void advance() { base = attn::uniform(base + (int64_t)kK * row_bytes); }
+  __device__ __forceinline__ void advance() {
+    if (Hold > 1 && ++turn < Hold) return;
+    turn = 0;
+    base = attn::uniform(base + (int64_t)kK * row_bytes);
+  }
   using Read = ReadCols<R>;
 };
 
@@ -202,23 +206,28 @@ struct BlockRows {
   using Read = ReadRows;
 };
 
-template <int R, int NT>
+// Hold: a step's tile is loaded so often. Parts: a block of columns is so many
+// blocks beside each other, of which a step takes one (the parts of a sum of
+// matrices, a step of each in turn).
+template <int R, int NT, int Hold = 1, int Parts = 1>
 struct BlockCols {
   static constexpr int kElems = R * kK;
   static constexpr int kPieces = R / 8, kPer = R * 8 / NT;
   static_assert(kPer >= 1 && R * 8 % NT == 0 && NT % kPieces == 0, "whole rows per step");
+  static_assert(Hold == 1 || Parts == 1, "one or the other");
   const char* base;
   uint32_t at[kPer];
   int64_t step;
+  int32_t turn = 0;
   // col0 and k0: multiples of 64; columns past `cols` are the tile's first block again
   __device__ __forceinline__ BlockCols(const char* p, int64_t cols, int64_t col0, int64_t k0) {
-    base = attn::uniform(p + 2 * blocked(k0, col0, cols));
-    step = cols * kK * 2;
+    base = attn::uniform(p + 2 * blocked(k0, col0 * Parts, cols * Parts));
+    step = cols * Parts * kK * 2;
 #pragma unroll
     for (int x = 0; x < kPer; ++x) {
       const int row = x * (NT / kPieces) + (int)threadIdx.x / kPieces;
       const int piece = ((int)threadIdx.x % kPieces) ^ attn::swz<kColsSwz<R>>(row);
-      const int block = col0 + 8 * piece < cols ? piece / 8 : 0;
+      const int block = col0 + 8 * piece < cols ? piece / 8 * Parts : 0;
       at[x] = block * (kBlock * 2) + row * (kK * 2) + 16 * (piece % 8);
     }
   }
@@ -226,13 +235,22 @@ struct BlockCols {
   __device__ __forceinline__ void load(uint32_t tile, int x) const {
     load_piece(base, at[x], tile + attn::wave_id() * (kWave * 16) + x * NT * 16);
   }
-  __device__ __forceinline__ void advance() { base = attn::uniform(base + step); }
+  __device__ __forceinline__ void advance() {
+    if (Hold > 1 && ++turn < Hold) return;
+    if (Parts > 1 && ++turn < Parts) {
+      base = attn::uniform(base + kBlock * 2);
+      return;
+    }
+    turn = 0;
+    base = attn::uniform(base + step - (Parts - 1) * (kBlock * 2));
+  }
   using Read = ReadCols<R>;
 };
 
+// (Turns: 64 k's are so many steps, with another part of one operand each.)
 // WM x WN waves, each of MI x NI blocks of 32 x 32. Register i of a lane's block
 // (mi, ni) is column m = m_of(mi) + 8 (i / 4) + i % 4 of row n = n_of(ni).
-template <typename T, typename A, typename B, int BM, int BN, int WM, int WN>
+template <typename T, typename A, typename B, int BM, int BN, int WM, int WN, int Turns = 1>
 struct Tile {
   static constexpr int kThreads = WM * WN * kWave;
   static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
@@ -290,7 +308,7 @@ struct Tile {
     const typename A::Read ra;
     const typename B::Read rb;
     const uint32_t lds0 = lds_address(lds);
-    const int steps = (int)cdiv(k, (int64_t)kK);
+    const int steps = (int)cdiv(k, (int64_t)kK) * Turns;
     if (steps <= 0) return;
     if (After == 0 || fresh) landed();
     else landed<After>();
@@ -341,9 +359,10 @@ struct Tile {
   }
   template <bool LimA, bool LimB>
   static __device__ __forceinline__ void limit(A& a, B& b, int64_t k, int step) {
-    if ((LimA || LimB) && (step + 1) * (int64_t)kK > k) {
-      if (LimA) a.limit((int)(k - step * (int64_t)kK));
-      if (LimB) b.limit((int)(k - step * (int64_t)kK));
+    const int64_t k0 = step / Turns * (int64_t)kK;
+    if ((LimA || LimB) && k0 + kK > k) {
+      if (LimA) a.limit((int)(k - k0));
+      if (LimB) b.limit((int)(k - k0));
     }
   }
   static __device__ __forceinline__ void load(const A& a, const B& b, uint32_t stage, int x) {

@@ -31,7 +31,7 @@ constexpr int kD = 256;                           // columns of a gradient's til
 constexpr int64_t kPieceBytes = (int64_t)1 << PB;  // e of one piece of the table
 constexpr int64_t kPackBytes = (int64_t)1 << 26;   // a piece of a table that has to be laid out
 constexpr int64_t kPartBytes = (int64_t)1 << 28;   // sums of a cut product
-constexpr int kMostParts = 64;
+constexpr int kMostParts = 256;
 constexpr int64_t kFew = 256;
 constexpr int64_t kCacheBytes = (int64_t)1 << 27;  // half of the last level
 
@@ -230,14 +230,18 @@ struct ScoreArgs {
   float2* part;      // forward: [tiles of the table][npad] maximum and sum, base 2
   float* at_label;   // forward: [npad] the label's score, base 2
   // backward: [npad][e_cols] 16 bits in blocks. Up to kFew tokens e is two numbers,
-  // rounded and what the rounding left, the second e_half bytes behind: few
-  // tokens' gradients have few terms to average a rounding over (64 tokens: dx off
-  // by 3.2e-4 of its size in one number, fp16, where its own rounding is 2.1e-4),
-  // and their time goes elsewhere.
+  // rounded and what the rounding left, in blocks beside each other: few tokens'
+  // gradients have few terms to average a rounding over (64 tokens: dx off by 3.2e-4
+  // of its size in one number, fp16, where its own rounding is 2.1e-4).
   char* e;
-  int64_t e_cols, e_half;
-  int32_t past;
+  int64_t e_cols;
+  int32_t past;      // e outgrows the caches
 };
+
+// element (token, row) of a half of e
+__device__ __forceinline__ int64_t place_of_e(int64_t n, int64_t v, int64_t cols, int half, int halves) {
+  return blocked(n, (v / kK * halves + half) * kK + v % kK, cols * halves);
+}
 
 // waves of a tile: 256 x 256 and 256 x 64
 #ifndef W_M
@@ -399,8 +403,8 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
         for (int y = 0; y < kRows * kPieces / NT; ++y) {  // block by block
           const int u = y * NT + tid, r = u / 8 % kRows, piece = u / (8 * kRows) * 8 + u % 8;
           const u32x4 v = Stage16<kV>::get(lds, r, piece);
-          u32x4* to = (u32x4*)(a.e + half * a.e_half +
-                               2 * blocked(n0 + (r / 32 * P::NI + j) * 32 + r % 32, v0 + 8 * piece, a.e_cols));
+          u32x4* to = (u32x4*)(a.e + 2 * place_of_e(n0 + (r / 32 * P::NI + j) * 32 + r % 32, v0 + 8 * piece,
+                                                    a.e_cols, half, Halves));
           // what outgrows the caches goes past them: they hold the operands of the
           // tiles beside this one (597 -> 565 us, and the product that reads e 503
           // -> 479); less is read from them soon
@@ -467,8 +471,7 @@ struct SumArgs {
   int64_t rows;      // rows of the piece
   int32_t w_cols;
   const char* e;
-  int64_t e_cols, e_half;
-  int32_t halves;    // of e, see ScoreArgs
+  int64_t e_cols;
   Order order;       // of the output's tiles
   int32_t parts;     // of the sum
   int32_t steps;     // of 64, of a part (dx)
@@ -561,57 +564,83 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
   }
 }
 
-// dx = e w over a part of the piece's rows, by tokens' places.
-template <typename T, int BN, int WM, int WN>
-__global__ void __launch_bounds__(WM * WN * kWave) k_grad_x(SumArgs a) {
-  constexpr int NT = WM * WN * kWave;
-  using P = Tile<T, Cols<kD, NT>, BlockRows<BN, NT>, kD, BN, WM, WN>;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
+// dx = e w over a part of the piece's rows, by tokens' places: workgroup `bid` of
+// the product's. lds: two stages.
+template <typename T, int BN, int WM, int WN, int Halves>
+struct GradX {
+  static constexpr int NT = WM * WN * kWave;
+  using W = Cols<kD, NT, Halves>;
+  using E = BlockRows<BN, NT>;
+  using P = Tile<T, W, E, kD, BN, WM, WN, Halves>;
   static_assert(4 * P::kStage >= WN * 32 * kD * 4, "the stages hold rows of sums");
-  const Order order{(int32_t)cdiv(*a.h.n_live, BN), a.order.cols};
-  const int32_t tiles = order.rows * order.cols;
-  if ((int64_t)blockIdx.x >= (int64_t)tiles * a.parts) return;
-  const int32_t id = in_order(blockIdx.x, tiles * a.parts);
-  int32_t tn, td;
-  // parts of one tile run apart, tiles of one part together
-  order.at(id % tiles, kGroup, &tn, &td);
-  const int32_t part = id / tiles;
-  const int64_t n0 = (int64_t)tn * BN;
-  const int64_t k0 = (int64_t)part * a.steps * kK, k1 = min(a.rows, k0 + (int64_t)a.steps * kK);
-  P p;
-  p.clear();
-  for (int half = 0; half < a.halves; ++half) {
-    Cols<kD, NT> w(a.w, a.w_stride, td * kD, a.w_cols, k0);
-    BlockRows<BN, NT> e(a.e + half * a.e_half, a.e_cols, n0, k0);
+  static __device__ __forceinline__ void run(const SumArgs& a, int32_t bid, uint16_t* lds) {
+    const Order order{(int32_t)cdiv(*a.h.n_live, BN), a.order.cols};
+    const int32_t tiles = order.rows * order.cols;
+    if ((int64_t)bid >= (int64_t)tiles * a.parts) return;
+    const int32_t id = in_order(bid, tiles * a.parts);
+    int32_t tn, td;
+    // parts of one tile run apart, tiles of one part together
+    order.at(id % tiles, kGroup, &tn, &td);
+    const int32_t part = id / tiles;
+    const int64_t n0 = (int64_t)tn * BN;
+    const int64_t k0 = (int64_t)part * a.steps * kK, k1 = min(a.rows, k0 + (int64_t)a.steps * kK);
+    P p;
+    p.clear();
+    W w(a.w, a.w_stride, td * kD, a.w_cols, k0);
+    E e(a.e, a.e_cols * Halves, n0, k0 * Halves);
     P::template ask<true, false>(w, e, k1 - k0, lds);
     p.template run<true, false>(w, e, k1 - k0, lds);
+    put_sums<T, P, BN, WM>(p, lds, a, a.part + (int64_t)part * a.h.npad * a.h.dp, n0, a.h.npad, td * kD);
   }
-  put_sums<T, P, BN, WM>(p, lds, a, a.part + (int64_t)part * a.h.npad * a.h.dp, n0, a.h.npad, td * kD);
-}
+};
 
 // dw = e^T x over a part of the tokens.
-template <typename T, int BV, int WM, int WN>
-__global__ void __launch_bounds__(WM * WN * kWave) k_grad_w(SumArgs a) {
-  constexpr int NT = WM * WN * kWave;
-  using P = Tile<T, BlockCols<kD, NT>, BlockCols<BV, NT>, kD, BV, WM, WN>;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
-  const int32_t tiles = a.order.rows * a.order.cols, id = in_order(blockIdx.x, gridDim.x);
-  int32_t tv, td;
-  a.order.at(id % tiles, kGroup, &tv, &td);
-  const int32_t part = id / tiles;
-  // rows of e and x are zeros from n_live to the next multiple of 64
-  const int64_t steps = cdiv(*a.h.n_live, kK), per = cdiv(steps, a.parts);
-  const int64_t s0 = min(steps, part * per), s1 = min(steps, s0 + per);
-  P p;
-  p.clear();
-  for (int half = 0; half < a.halves; ++half) {
-    BlockCols<kD, NT> x(a.h.x, a.h.dp, td * kD, s0 * kK);
-    BlockCols<BV, NT> e(a.e + half * a.e_half, a.e_cols, (int64_t)tv * BV, s0 * kK);
+template <typename T, int BV, int WM, int WN, int Halves>
+struct GradW {
+  static constexpr int NT = WM * WN * kWave;
+  using X = BlockCols<kD, NT, Halves>;
+  using E = BlockCols<BV, NT, 1, Halves>;
+  using P = Tile<T, X, E, kD, BV, WM, WN, Halves>;
+  static __device__ __forceinline__ void run(const SumArgs& a, int32_t bid, int32_t grid, uint16_t* lds) {
+    const int32_t tiles = a.order.rows * a.order.cols, id = in_order(bid, grid);
+    int32_t tv, td;
+    a.order.at(id % tiles, kGroup, &tv, &td);
+    const int32_t part = id / tiles;
+    // rows of e and x are zeros from n_live to the next multiple of 64
+    const int64_t steps = cdiv(*a.h.n_live, kK), per = cdiv(steps, a.parts);
+    const int64_t s0 = min(steps, part * per), s1 = min(steps, s0 + per);
+    P p;
+    p.clear();
+    X x(a.h.x, a.h.dp, td * kD, s0 * kK);
+    E e(a.e, a.e_cols, (int64_t)tv * BV, s0 * kK);
     P::template ask<false, false>(x, e, (s1 - s0) * kK, lds);
     p.template run<false, false>(x, e, (s1 - s0) * kK, lds);
+    float* to = a.part ? a.part + (int64_t)part * a.out_rows * a.h.dp : nullptr;
+    put_sums<T, P, BV, WM>(p, lds, a, to, (int64_t)tv * BV, a.out_rows, td * kD);
   }
-  float* to = a.part ? a.part + (int64_t)part * a.out_rows * a.h.dp : nullptr;
-  put_sums<T, P, BV, WM>(p, lds, a, to, (int64_t)tv * BV, a.out_rows, td * kD);
+};
+
+template <typename T, int BN, int WM, int WN, int Halves>
+__global__ void __launch_bounds__(WM * WN * kWave) k_grad_x(SumArgs a) {
+  using G = GradX<T, BN, WM, WN, Halves>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * G::P::kStage];
+  G::run(a, blockIdx.x, lds);
+}
+template <typename T, int BV, int WM, int WN, int Halves>
+__global__ void __launch_bounds__(WM * WN * kWave) k_grad_w(SumArgs a) {
+  using G = GradW<T, BV, WM, WN, Halves>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * G::P::kStage];
+  G::run(a, blockIdx.x, gridDim.x, lds);
+}
+// Both in one launch, dx's workgroups first, where neither fills the chip.
+template <typename T, int Halves>
+__global__ void __launch_bounds__(8 * kWave) k_grads(SumArgs x, SumArgs w, int32_t x_grid) {
+  using X = GradX<T, 64, 8, 1, Halves>;
+  using W = GradW<T, 64, 8, 1, Halves>;
+  static_assert(X::P::kStage == W::P::kStage, "one pair of stages");
+  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * X::P::kStage];
+  if ((int32_t)blockIdx.x < x_grid) X::run(x, blockIdx.x, lds);
+  else W::run(w, blockIdx.x - x_grid, gridDim.x - x_grid, lds);
 }
 
 // The parts of a sum, added in order and rounded once. Rows of pos < 0 are zeros.
@@ -740,7 +769,7 @@ struct TeacherArgs {
   // backward
   const float* logits_in;
   char* e;
-  int64_t e_cols, e_half, v0, piece_rows;
+  int64_t e_cols, v0, piece_rows;
   int32_t halves;
 };
 
@@ -912,9 +941,8 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill_entries(Teach
     for (int k = 0; k < a.top; ++k) q += s_id[w][k] == t.id[u] ? s_q[w][k] : 0.f;
     const float z = a.logits_in[i * a.top + l + kWave * u];
     const float e = (__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -lse2)) - q) * c;
-    const int64_t at = blocked(pos, v, a.e_cols);
-    ((T*)a.e)[at] = (T)e;
-    if (a.halves > 1) ((T*)(a.e + a.e_half))[at] = (T)(e - (float)(T)e);
+    ((T*)a.e)[place_of_e(pos, v, a.e_cols, 0, a.halves)] = (T)e;
+    if (a.halves > 1) ((T*)a.e)[place_of_e(pos, v, a.e_cols, 1, 2)] = (T)(e - (float)(T)e);
   }
 }
 
@@ -938,7 +966,7 @@ int32_t parts_of(int64_t tiles, int64_t steps, int32_t rows, int64_t bytes_each,
   const double step = rows == 64 ? 0.9 : 1.8;
   int32_t best = 1;
   double least = 1e300;
-  for (int64_t p = 1; p <= most; ++p) {
+  for (int64_t p = 1; p <= most; p += 1 + p / 8) {
     const double us = (double)cdiv(tiles * p, at_once) * ((double)cdiv(steps, p) * step + 6.0) +
                       (p > 1 ? 5.0 : 0.0) + 2e-6 * (double)(p * bytes_each) / 5.0;
     if (us < least) {
@@ -956,7 +984,7 @@ Sizes sizes_of(int64_t n, int64_t rows, int32_t dim) {
   s.dim = dim;
   s.dp = (int32_t)align_up((size_t)dim, kK);
   // Tiles of 64 tokens where those of 256 would be few or mostly empty
-  s.bn = n > 128 && cdiv(n, 256) * cdiv(rows, kV) >= 512 ? 256 : 64;
+  s.bn = n > kFew && cdiv(n, 256) * cdiv(rows, kV) >= 512 ? 256 : 64;
   s.npad = (int64_t)align_up((size_t)std::max<int64_t>(n, 1), n > 128 ? 256 : 64);
   s.vpad = (int64_t)align_up((size_t)rows, kV);
   s.tiles = s.vpad / kV;
@@ -1050,32 +1078,59 @@ int pack_tokens(PackArgs a, hipStream_t stream) {
   return FS_OK;
 }
 
+// Halves: 0 forward, else of e. Two go with tiles of 64 tokens.
+template <typename T, int Halves>
+void launch_scores(const ScoreArgs& a, const Sizes& s, int64_t tiles, hipStream_t stream) {
+  if constexpr (Halves < 2) {
+    if (s.bn == 256) {
+      hipLaunchKernelGGL((k_scores<T, 256, kWM, kWN, Halves>), dim3((unsigned)std::min<int64_t>(tiles, kCus)),
+                         dim3(kWM * kWN * kWave), 0, stream, a);
+      return;
+    }
+  }
+  hipLaunchKernelGGL((k_scores<T, 64, 8, 1, Halves>), dim3((unsigned)tiles), dim3(8 * kWave), 0, stream, a);
+}
 template <int Halves>
 int launch_scores(const ScoreArgs& a, const Sizes& s, int32_t dtype, hipStream_t stream) {
-  const int64_t grid = (int64_t)a.order.rows * a.order.cols;
-  if (!grid_fits(grid, kMostThreads)) return FS_ERR_UNSUPPORTED;
-  const dim3 g((unsigned)(s.bn == 256 ? std::min<int64_t>(grid, kCus) : grid)), b((s.bn == 256 ? kWM * kWN : 8) * kWave);
-  if (dtype == FS_BF16) {
-    if (s.bn == 256) hipLaunchKernelGGL((k_scores<__bf16, 256, kWM, kWN, Halves>), g, b, 0, stream, a);
-    else hipLaunchKernelGGL((k_scores<__bf16, 64, 8, 1, Halves>), g, b, 0, stream, a);
-  } else {
-    if (s.bn == 256) hipLaunchKernelGGL((k_scores<_Float16, 256, kWM, kWN, Halves>), g, b, 0, stream, a);
-    else hipLaunchKernelGGL((k_scores<_Float16, 64, 8, 1, Halves>), g, b, 0, stream, a);
-  }
+  const int64_t tiles = (int64_t)a.order.rows * a.order.cols;
+  if (!grid_fits(tiles, kMostThreads)) return FS_ERR_UNSUPPORTED;
+  if (dtype == FS_BF16) launch_scores<__bf16, Halves>(a, s, tiles, stream);
+  else launch_scores<_Float16, Halves>(a, s, tiles, stream);
   FS_LAUNCH_CHECK();
   return FS_OK;
 }
 
-template <typename T>
-void launch_grad_x(const SumArgs& a, const Sizes& s, dim3 g, hipStream_t stream) {
-  if (s.bn == 256) hipLaunchKernelGGL((k_grad_x<T, 256, kWM, kWN>), g, dim3(kWM * kWN * kWave), 0, stream, a);
-  else hipLaunchKernelGGL((k_grad_x<T, 64, 8, 1>), g, dim3(8 * kWave), 0, stream, a);
+// dx's and dw's products of a piece; a grid of 0 is left out.
+template <typename T, int Halves>
+void launch_grads(const SumArgs& x, int64_t x_grid, const SumArgs& w, int64_t w_grid, const Sizes& s,
+                  int32_t bv, hipStream_t stream) {
+  const dim3 many(kWM * kWN * kWave), few(8 * kWave);
+  // one launch where dx leaves room beside it (64 tokens, 32000 rows of 64: 14 + 7.5
+  // -> @@ us)
+  if (x_grid > 0 && w_grid > 0 && s.bn == 64 && bv == 64 && x_grid < 2 * kCus) {
+    hipLaunchKernelGGL((k_grads<T, Halves>), dim3((unsigned)(x_grid + w_grid)), few, 0, stream, x, w,
+                       (int32_t)x_grid);
+    return;
+  }
+  const dim3 gx((unsigned)x_grid), gw((unsigned)w_grid);
+  if (x_grid > 0) {
+    if constexpr (Halves == 1) {
+      if (s.bn == 256) hipLaunchKernelGGL((k_grad_x<T, 256, kWM, kWN, 1>), gx, many, 0, stream, x);
+      else hipLaunchKernelGGL((k_grad_x<T, 64, 8, 1, 1>), gx, few, 0, stream, x);
+    } else {
+      hipLaunchKernelGGL((k_grad_x<T, 64, 8, 1, Halves>), gx, few, 0, stream, x);
+    }
+  }
+  if (w_grid > 0) {
+    if (bv == 256) hipLaunchKernelGGL((k_grad_w<T, 256, kWM, kWN, Halves>), gw, many, 0, stream, w);
+    else hipLaunchKernelGGL((k_grad_w<T, 64, 8, 1, Halves>), gw, few, 0, stream, w);
+  }
 }
-
 template <typename T>
-void launch_grad_w(const SumArgs& a, int32_t bv, dim3 g, hipStream_t stream) {
-  if (bv == 256) hipLaunchKernelGGL((k_grad_w<T, 256, kWM, kWN>), g, dim3(kWM * kWN * kWave), 0, stream, a);
-  else hipLaunchKernelGGL((k_grad_w<T, 64, 8, 1>), g, dim3(8 * kWave), 0, stream, a);
+void launch_grads(const SumArgs& x, int64_t x_grid, const SumArgs& w, int64_t w_grid, const Sizes& s,
+                  int32_t bv, hipStream_t stream) {
+  if (s.halves == 1) launch_grads<T, 1>(x, x_grid, w, w_grid, s, bv, stream);
+  else launch_grads<T, 2>(x, x_grid, w, w_grid, s, bv, stream);
 }
 
 template <typename T>
@@ -1174,8 +1229,7 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
     a.rows = std::min(step, s.rows - v0);
     a.e = o.e;
     a.e_cols = (int64_t)align_up((size_t)a.rows, kV);
-    a.e_half = 2 * s.npad * a.e_cols;
-    a.past = a.e_half > kCacheBytes;
+    a.past = 2 * s.npad * a.e_cols > kCacheBytes;
     if ((rc = piece_of(t, s, v0, a.rows, o.pack, &a.w, &a.w_stride, &a.k, stream))) return rc;
     const int32_t table_tiles = (int32_t)cdiv(a.rows, kV);
     a.order = Order{token_tiles, table_tiles};
@@ -1186,7 +1240,6 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
       if (entries) {
         entries->e = a.e;
         entries->e_cols = a.e_cols;
-        entries->e_half = a.e_half;
         entries->halves = s.halves;
         entries->v0 = v0;
         entries->piece_rows = a.rows;
@@ -1204,43 +1257,37 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
     b.w_cols = a.k;
     b.e = a.e;
     b.e_cols = a.e_cols;
-    b.e_half = a.e_half;
-    b.halves = s.halves;
+    SumArgs c = b;
+    int64_t x_grid = 0, w_grid = 0;
     if (g.dx && s.n > 0) {
       b.order = Order{token_tiles, col_tiles};
       b.parts = x_parts;
       b.steps = (int32_t)cdiv(cdiv(a.rows, kK), x_parts);
       b.add = v0 > 0;
       b.part = o.dx_part;
-      const int64_t grid = (int64_t)token_tiles * col_tiles * x_parts;
-      if (!grid_fits(grid, kMostThreads)) return FS_ERR_UNSUPPORTED;
-      if (dtype == FS_BF16) launch_grad_x<__bf16>(b, s, dim3((unsigned)grid), stream);
-      else launch_grad_x<_Float16>(b, s, dim3((unsigned)grid), stream);
-      FS_LAUNCH_CHECK();
+      x_grid = (int64_t)token_tiles * col_tiles * x_parts;
     }
+    // tiles of 64 rows where those of 256 would leave CUs idle
+    const int32_t bv = (int64_t)table_tiles * col_tiles < kCus ? 64 : kV;
     if (g.dw) {
-      // tiles of 64 rows where those of 256 would leave CUs idle
-      const int32_t bv = (int64_t)table_tiles * col_tiles < kCus ? 64 : kV;
       const int32_t row_tiles = (int32_t)cdiv(a.rows, bv);
       const int64_t tiles = (int64_t)row_tiles * col_tiles;
-      const int32_t parts = parts_of(tiles, cdiv(s.n, kK) * s.halves, bv, a.rows * s.dp * 4, s.dw_part);
-      b.order = Order{row_tiles, col_tiles};
-      b.parts = parts;
-      b.add = 0;
-      b.part = parts > 1 ? o.dw_part : nullptr;
-      b.out = (char*)g.dw + v0 * g.dw_stride;
-      b.out_stride = g.dw_stride;
-      b.out_rows = a.rows;
-      b.out_type = g.dw_type;
-      if (!grid_fits(tiles * parts, kMostThreads)) return FS_ERR_UNSUPPORTED;
-      const dim3 grid((unsigned)(tiles * parts));
-      if (dtype == FS_BF16) launch_grad_w<__bf16>(b, bv, grid, stream);
-      else launch_grad_w<_Float16>(b, bv, grid, stream);
-      FS_LAUNCH_CHECK();
-      if (parts > 1) {
-        const JoinArgs j{o.dw_part, a.rows, parts, s.dp, s.dim, nullptr, a.rows, o.h.mul, b.out, g.dw_stride};
-        if ((rc = launch_join(j, g.dw_type, stream))) return rc;
-      }
+      c.order = Order{row_tiles, col_tiles};
+      c.parts = parts_of(tiles, cdiv(s.n, kK) * s.halves, bv, a.rows * s.dp * 4, s.dw_part);
+      c.part = c.parts > 1 ? o.dw_part : nullptr;
+      c.out = (char*)g.dw + v0 * g.dw_stride;
+      c.out_stride = g.dw_stride;
+      c.out_rows = a.rows;
+      c.out_type = g.dw_type;
+      w_grid = tiles * c.parts;
+    }
+    if (!grid_fits(x_grid + w_grid, kMostThreads)) return FS_ERR_UNSUPPORTED;
+    if (dtype == FS_BF16) launch_grads<__bf16>(b, x_grid, c, w_grid, s, bv, stream);
+    else launch_grads<_Float16>(b, x_grid, c, w_grid, s, bv, stream);
+    FS_LAUNCH_CHECK();
+    if (g.dw && c.parts > 1) {
+      const JoinArgs j{o.dw_part, a.rows, c.parts, s.dp, s.dim, nullptr, a.rows, o.h.mul, c.out, g.dw_stride};
+      if ((rc = launch_join(j, g.dw_type, stream))) return rc;
     }
   }
   if (g.dx && s.n > 0) {
