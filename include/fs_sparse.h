@@ -596,7 +596,8 @@ size_t fs_jagged_attention_backward_workspace_size(int64_t n_tok, int32_t n, int
 /*  dweight, dbias  device [dim] of param_dtype; NULL: not computed. With    */
 /*           n = 0 they are zeros.                                           */
 /*  eps      finite and not negative.                                        */
-/*  ws, ws_bytes  at least the workspace query's bytes, else FS_ERR_WORKSPACE. */
+/*  ws, ws_bytes  at least the workspace query's bytes, else FS_ERR_WORKSPACE; */
+/*           few rows need none (the query returns 0, ws may be NULL).        */
 /* Outputs must not alias inputs or each other. n < 2^31 - 1.                */
 int fs_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, int64_t n, int32_t dim,
                   const void* weight, const void* bias, int32_t param_dtype, float eps, void* out,

@@ -420,7 +420,12 @@ int rows_of(const void* p, int32_t type, int64_t stride, int32_t dim, NormRows* 
   return FS_OK;
 }
 
-constexpr int32_t kMaxParts = 1024;     // workgroups that sum dweight and dbias
+// Workgroups that sum dweight and dbias: as many as the chip holds at once, one of
+// 1024 threads a CU, four of 256, three where a lane has 16 elements (65537 x 1000
+// bf16: 768 workgroups 80 us, 1024 96, 512 85; fewer also mean fewer sums to add).
+template <int E, int L, int C>
+constexpr int32_t kParts = L > 256 ? 256 : C * E > 8 ? 768 : 1024;
+constexpr int32_t kMaxParts = 1024;
 
 // Lanes and pieces of a row by its width in pieces, calls launch.template go<E, L, C>().
 template <int E, typename F>
@@ -455,6 +460,20 @@ struct Forward {
   }
 };
 
+// Few rows are one workgroup's, whose sums need no second launch and no workspace:
+// threads it has, or 0.
+template <int E, int L, int C>
+constexpr int few_threads() { return L >= 256 ? 0 : C * E > 8 ? 512 : 1024; }
+struct Few {
+  int64_t n;
+  bool* all;
+  template <int E, int L, int C>
+  void go() const {
+    constexpr int T = few_threads<E, L, C>();
+    *all = *all && (T ? cdiv(n, std::max(T, 1) / L) <= 8 : n <= 1);
+  }
+};
+
 struct Backward {
   NormArgs& a;
   float* part;
@@ -463,10 +482,11 @@ struct Backward {
   template <int E, int L, int C>
   void go() const {
     int T = L > 256 ? L : 256;
-    int64_t blocks = std::min<int64_t>(cdiv(a.n, T / L), kMaxParts);
-    constexpr int Wide = C * E > 8 ? 512 : 1024;
-    if (L < 256 && cdiv(a.n, Wide / L) <= 8) {  // few rows: one workgroup, one launch
-      T = Wide;
+    int64_t blocks = std::min<int64_t>(cdiv(a.n, T / L), kParts<E, L, C>);
+    bool few = true;
+    Few{a.n, &few}.template go<E, L, C>();
+    if (few) {
+      if (few_threads<E, L, C>()) T = few_threads<E, L, C>();
       blocks = 1;
     }
     blocks = std::max<int64_t>(blocks, 1);
@@ -515,7 +535,11 @@ extern "C" int fs_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, i
 }
 
 extern "C" size_t fs_layer_norm_backward_workspace_size(int64_t n, int32_t dim) {
-  if (n < 0 || dim < 1) return 0;
+  if (n < 0 || dim < 1 || dim > FS_MAX_NORM_DIM) return 0;
+  bool few = true;
+  by_width<4>(dim, Few{n, &few});
+  by_width<8>(dim, Few{n, &few});
+  if (few) return 0;
   return sizeof(float) * 2 * (size_t)dim * (size_t)std::min<int64_t>(n, kMaxParts) + 256;
 }
 
@@ -539,7 +563,8 @@ extern "C" int fs_layer_norm_backward(const void* x, int32_t x_dtype, int64_t x_
   const int32_t e = elem_bytes(param_dtype);
   if ((n > 0 && (!mean || !rstd)) || (uintptr_t)weight % e || (uintptr_t)dweight % e || (uintptr_t)dbias % e)
     return FS_ERR_INVALID_ARG;
-  if (!ws || ws_bytes < fs_layer_norm_backward_workspace_size(n, dim)) return FS_ERR_WORKSPACE;
+  const size_t need = fs_layer_norm_backward_workspace_size(n, dim);
+  if (need > 0 && (!ws || ws_bytes < need)) return FS_ERR_WORKSPACE;
   if (n == 0 && !dweight && !dbias) return FS_OK;
   a.dx = to.p;
   a.dx_stride = to.stride;

@@ -764,8 +764,9 @@ struct TeacherArgs {
   // forward
   const char* w;
   int64_t w_stride;
-  float *loss, *logits;
-  const float* lse;
+  float *loss, *logits, *lse;
+  const float2* part;  // null: lse is there, else it is made of these tiles
+  int64_t tiles;
   // backward
   const float* logits_in;
   char* e;
@@ -853,7 +854,10 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
   const int32_t pos = a.h.pos[i];
   if (pos < 0) {
     for (int k = threadIdx.x; k < a.top; k += kRowsPerGroup * kWave) a.logits[i * a.top + k] = 0.f;
-    if (threadIdx.x == 0) a.loss[i] = 0.f;
+    if (threadIdx.x == 0) {
+      a.loss[i] = 0.f;
+      if (a.part) a.lse[i] = 0.f;
+    }
     return;
   }
   for (int k = threadIdx.x; k < a.top; k += kRowsPerGroup * kWave) {
@@ -895,10 +899,36 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
       if (l == 0 && k < a.top) s_z[k] = id[u] >= 0 ? z : 0.f;
     }
   }
+  __shared__ float2 s_part[kRowsPerGroup];
+  if (a.part) {
+    float top = -3e38f, sum = 0.f;
+    for (int64_t q = threadIdx.x; q < a.tiles; q += kRowsPerGroup * kWave) {
+      const float2 x = a.part[q * a.h.npad + pos];
+      const float m = fmaxf(x.x, top);
+      sum = sum * __builtin_amdgcn_exp2f(top - m) + x.y * __builtin_amdgcn_exp2f(x.x - m);
+      top = m;
+    }
+    float m = top;
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, kWave));
+    sum = wave_sum(sum * __builtin_amdgcn_exp2f(top - m));
+    if (l == 0) s_part[w] = make_float2(m, sum);
+  }
   __syncthreads();
   if (w) return;
   const Teacher t(a, i);
-  const float lse = a.lse[i];
+  float lse;
+  if (a.part) {
+    float m = s_part[0].x, sum = 0.f;
+#pragma unroll
+    for (int q = 1; q < kRowsPerGroup; ++q) m = fmaxf(m, s_part[q].x);
+#pragma unroll
+    for (int q = 0; q < kRowsPerGroup; ++q) sum += s_part[q].y * __builtin_amdgcn_exp2f(s_part[q].x - m);
+    lse = (m + __builtin_amdgcn_logf(sum)) * kLn2;
+    if (l == 0) a.lse[i] = lse;
+  } else {
+    lse = a.lse[i];
+  }
   float loss = 0.f;
 #pragma unroll
   for (int u = 0; u < kPerLane; ++u) {
@@ -1172,6 +1202,8 @@ int check(const void* x, int64_t* x_stride, int64_t n, const fs_table* table, fl
 }
 
 // lse (and the losses of labels) of the packed tokens
+constexpr int64_t kFewRows = 2048;
+
 int forward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float scale, bool labels,
             float* loss, float* lse, hipStream_t stream) {
   int rc;
@@ -1189,8 +1221,11 @@ int forward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float
     a.at_label = o.at_label;
     if ((rc = launch_scores<0>(a, s, dtype, stream))) return rc;
   }
+  // few tokens' tiles are joined where their entries are (a launch of 4 us less; of
+  // many tokens a token's tiles lie too far apart for that)
+  if (!labels && s.n < kFewRows) return FS_OK;
   const LossArgs l{o.h, o.part, s.tiles, labels ? o.at_label : nullptr, loss, lse};
-  if (s.n < 2048) hipLaunchKernelGGL(k_loss<4>, dim3((unsigned)cdiv(s.n, 4)), dim3(256), 0, stream, l);
+  if (s.n < kFewRows) hipLaunchKernelGGL(k_loss<4>, dim3((unsigned)cdiv(s.n, 4)), dim3(256), 0, stream, l);
   else hipLaunchKernelGGL(k_loss<16>, dim3((unsigned)cdiv(s.n, 16)), dim3(256), 0, stream, l);
   FS_LAUNCH_CHECK();
   return FS_OK;
@@ -1432,6 +1467,8 @@ extern "C" int fs_token_distill(const void* x, int64_t x_stride, int64_t n, cons
   a.loss = loss;
   a.logits = logits;
   a.lse = lse;
+  a.part = n < kFewRows ? o.part : nullptr;
+  a.tiles = s.tiles;
   const dim3 grid((unsigned)n), block(kRowsPerGroup * kWave);
   if (table->dtype == FS_BF16) hipLaunchKernelGGL(k_distill<__bf16>, grid, block, 0, stream, a);
   else hipLaunchKernelGGL(k_distill<_Float16>, grid, block, 0, stream, a);

@@ -775,6 +775,13 @@ def _out(t, shape, dtype, d):
     return t
 
 
+def _outs(pair, shape, dtype, d):
+    """Two such outputs, both fresh from one allocation."""
+    if pair[0] is None and pair[1] is None:
+        return torch.empty((2, *shape), dtype=dtype, device=d).unbind(0)
+    return _out(pair[0], shape, dtype, d), _out(pair[1], shape, dtype, d)
+
+
 def _space(nbytes, ws):
     """A call's workspace: the caller's, or a fresh one."""
     return _ws(nbytes, ws)
@@ -782,10 +789,12 @@ def _space(nbytes, ws):
 
 def _params(*tensors, dim):
     """The one type of a norm's parameters (fp32 where there are none)."""
-    types = {t.dtype for t in tensors if t is not None}
-    assert len(types) < 2, "a norm's weight and bias have one type"
-    assert all(t.shape == (dim,) for t in tensors if t is not None)
-    return types.pop() if types else torch.float32
+    dtype = None
+    for t in tensors:
+        if t is not None:
+            assert t.shape == (dim,) and dtype in (None, t.dtype), "a norm's parameters: [dim] of one type"
+            dtype = t.dtype
+    return dtype or torch.float32
 
 
 @_allocates
@@ -798,7 +807,7 @@ def fs_layer_norm(x, weight=None, bias=None, eps=1e-5, dtype=None, out=None, mea
     (n, dim), d = x.shape, _here(x, weight, bias, out, mean, rstd)
     param = _params(weight, bias, dim=dim)
     out = _out(out, (n, dim), dtype or (x.dtype if out is None else out.dtype), d)
-    mean, rstd = (_out(t, (n,), torch.float32, d) for t in (mean, rstd))
+    mean, rstd = _outs((mean, rstd), (n,), torch.float32, d)
     xptr, xstride = _own_rows_ptr(x)
     optr, ostride = _own_rows_ptr(out)
     _check("fs_layer_norm",
@@ -825,15 +834,18 @@ def fs_layer_norm_backward(x, mean, rstd, dout, weight=None, dx=None, dweight=No
     param = _params(weight, dweight, dbias, dim=dim)
     dx = _out(dx, (n, dim), x.dtype, d)
     if weight is not None:
-        dweight, dbias = (_out(t, (dim,), param, d) for t in (dweight, dbias))
-    ws = _space(layer_norm_backward_workspace_size(n, dim), ws)
+        dweight, dbias = _outs((dweight, dbias), (dim,), param, d)
+    need = layer_norm_backward_workspace_size(n, dim)
+    if need or ws is not None:
+        ws = _space(need, ws)
     xptr, xstride = _own_rows_ptr(x)
     optr, ostride = _own_rows_ptr(dout)
     gptr, gstride = _own_rows_ptr(dx)
     _check("fs_layer_norm_backward",
            _c_layer_norm_bwd(xptr, _dtype(x.dtype), xstride, n, dim, _ptr(mean), _ptr(rstd), optr,
                              _dtype(dout.dtype), ostride, _ptr(weight), _dtype(param), gptr, gstride,
-                             _ptr(dweight), _ptr(dbias), _ptr(ws), _nbytes(ws), _stream(stream)))
+                             _ptr(dweight), _ptr(dbias), _ptr(ws), 0 if ws is None else _nbytes(ws),
+                             _stream(stream)))
     return dx, dweight, dbias
 
 
@@ -893,7 +905,7 @@ def fs_token_loss(x, weight, labels, scale=1.0, padding_id=-1, loss=None, lse=No
     d = _here(x, weight, labels, loss, lse, err, ws)
     (xptr, xstride), n, tab = _scored(x, weight)
     assert labels.dtype == torch.int64 and labels.shape == (n,)
-    loss, lse = (_out(t, (n,), torch.float32, d) for t in (loss, lse))
+    loss, lse = _outs((loss, lse), (n,), torch.float32, d)
     ws = _space(token_loss_workspace_size(n, tab.rows, tab.dim), ws)
     _check("fs_token_loss",
            _c_token_loss(xptr, xstride, n, C.byref(tab), _ptr(labels), float(scale), int(padding_id),
@@ -935,7 +947,7 @@ def fs_token_distill(x, weight, ids, teacher, scale=1.0, padding_id=-1, loss=Non
     d = _here(x, weight, ids, teacher, loss, lse, logits, err, ws)
     (xptr, xstride), n, tab = _scored(x, weight)
     top = _targets(ids, teacher, n)
-    loss, lse = (_out(t, (n,), torch.float32, d) for t in (loss, lse))
+    loss, lse = _outs((loss, lse), (n,), torch.float32, d)
     logits = _out(logits, (n, top), torch.float32, d)
     ws = _space(token_loss_workspace_size(n, tab.rows, tab.dim), ws)
     _check("fs_token_distill",
