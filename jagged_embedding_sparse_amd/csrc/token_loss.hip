@@ -24,7 +24,6 @@ using namespace prod;
 
 constexpr float kLog2e = attn::kLog2e, kLn2 = attn::kLn2;
 constexpr int kV = 256;                           // table rows of a tile
-constexpr int kD = 256;                           // columns of a gradient's tile
 #ifndef PB
 #define PB 30
 #endif
@@ -483,13 +482,13 @@ struct SumArgs {
 };
 
 // A tile's sums, fp32, to [row][dp] floats or to an output of any type.
-template <typename T, typename P, int BN, int WM>
+template <typename P, int DM, int BN, int WM>
 __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, float* part, int64_t row0,
                                          int64_t rows, int32_t col0) {
   const int32_t cols = part ? a.h.dp : a.h.dim;
   if (part || a.out_type == FS_F32) {
     const float back = part ? 1.f : a.h.mul[1];
-    constexpr int kRows = P::kThreads / kWave / WM * 32, kPieces = kD / 4;
+    constexpr int kRows = P::kThreads / kWave / WM * 32, kPieces = DM / 4;
     float* f = (float*)lds;
 #pragma unroll
     for (int j = 0; j < P::NI; ++j) {
@@ -499,7 +498,7 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
       for (int i = 0; i < P::MI; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          Stage32<kD>::put(f, n, P::m_of(i) + 8 * q,
+          Stage32<DM>::put(f, n, P::m_of(i) + 8 * q,
                            f32x4{p.acc[i][j][4 * q] * back, p.acc[i][j][4 * q + 1] * back,
                                  p.acc[i][j][4 * q + 2] * back, p.acc[i][j][4 * q + 3] * back});
       __syncthreads();
@@ -509,7 +508,7 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
         const int64_t row = row0 + (s / 32 * P::NI + j) * 32 + s % 32;
         const int32_t col = col0 + 4 * piece;
         if (row >= rows || col >= cols) continue;
-        f32x4 v = Stage32<kD>::get(f, s, piece);
+        f32x4 v = Stage32<DM>::get(f, s, piece);
         if (part) {
           f32x4* to = (f32x4*)(part + row * a.h.dp + col);
           if (a.add) v += *to;
@@ -527,7 +526,7 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
     return;
   }
   const float back = a.h.mul[1];
-  constexpr int kPieces = kD / 8;
+  constexpr int kPieces = DM / 8;
 #pragma unroll
   for (int j = 0; j < P::NI; ++j)
 #pragma unroll
@@ -545,7 +544,7 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
           y[0] = Elem<_Float16>::pack(v[0], v[1]);
           y[1] = Elem<_Float16>::pack(v[2], v[3]);
         }
-        Stage16<kD>::put(lds, P::n_of(j), P::m_of(i) + 8 * q, y);
+        Stage16<DM>::put(lds, P::n_of(j), P::m_of(i) + 8 * q, y);
       }
   __syncthreads();
 #pragma unroll 4
@@ -554,7 +553,7 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
     const int64_t row = row0 + n;
     const int32_t col = col0 + 8 * piece;
     if (row >= rows || col >= cols) continue;
-    const u32x4 v = Stage16<kD>::get(lds, n, piece);
+    const u32x4 v = Stage16<DM>::get(lds, n, piece);
     uint16_t* to = (uint16_t*)(a.out + row * a.out_stride) + col;
     if (col + 8 <= cols) {
       *(u32x4_any*)to = v;
@@ -564,15 +563,23 @@ __device__ __forceinline__ void put_sums(P& p, uint16_t* lds, const SumArgs& a, 
   }
 }
 
+// Waves of a tile of DM columns and BN rows.
+template <int DM, int BN>
+struct Waves {
+  static constexpr int WM = BN == 256 ? 2 : DM / 32 < 4 ? 2 : DM == 128 ? 4 : 8;
+  static constexpr int WN = BN == 256 ? 4 : DM == 256 ? 1 : 2;
+  static constexpr int kThreads = WM * WN * kWave;
+};
+
 // dx = e w over a part of the piece's rows, by tokens' places: workgroup `bid` of
 // the product's. lds: two stages.
-template <typename T, int BN, int WM, int WN, int Halves>
-struct GradX {
-  static constexpr int NT = WM * WN * kWave;
-  using W = Cols<kD, NT, Halves>;
-  using E = BlockRows<BN, NT>;
-  using P = Tile<T, W, E, kD, BN, WM, WN, Halves>;
-  static_assert(4 * P::kStage >= WN * 32 * kD * 4, "the stages hold rows of sums");
+template <typename T, int DM, int BN, int Halves>
+struct GradX : Waves<DM, BN> {
+  using V = Waves<DM, BN>;
+  using W = Cols<DM, V::kThreads, Halves>;
+  using E = BlockRows<BN, V::kThreads>;
+  using P = Tile<T, W, E, DM, BN, V::WM, V::WN, Halves>;
+  static_assert(4 * P::kStage >= V::WN * 32 * DM * 4, "the stages hold rows of sums");
   static __device__ __forceinline__ void run(const SumArgs& a, int32_t bid, uint16_t* lds) {
     const Order order{(int32_t)cdiv(*a.h.n_live, BN), a.order.cols};
     const int32_t tiles = order.rows * order.cols;
@@ -586,21 +593,22 @@ struct GradX {
     const int64_t k0 = (int64_t)part * a.steps * kK, k1 = min(a.rows, k0 + (int64_t)a.steps * kK);
     P p;
     p.clear();
-    W w(a.w, a.w_stride, td * kD, a.w_cols, k0);
+    W w(a.w, a.w_stride, td * DM, a.w_cols, k0);
     E e(a.e, a.e_cols * Halves, n0, k0 * Halves);
     P::template ask<true, false>(w, e, k1 - k0, lds);
     p.template run<true, false>(w, e, k1 - k0, lds);
-    put_sums<T, P, BN, WM>(p, lds, a, a.part + (int64_t)part * a.h.npad * a.h.dp, n0, a.h.npad, td * kD);
+    put_sums<P, DM, BN, V::WM>(p, lds, a, a.part + (int64_t)part * a.h.npad * a.h.dp, n0, a.h.npad, td * DM);
   }
 };
 
 // dw = e^T x over a part of the tokens.
-template <typename T, int BV, int WM, int WN, int Halves>
-struct GradW {
-  static constexpr int NT = WM * WN * kWave;
-  using X = BlockCols<kD, NT, Halves>;
-  using E = BlockCols<BV, NT, 1, Halves>;
-  using P = Tile<T, X, E, kD, BV, WM, WN, Halves>;
+template <typename T, int DM, int BV, int Halves>
+struct GradW : Waves<DM, BV> {
+  using V = Waves<DM, BV>;
+  using X = BlockCols<DM, V::kThreads, Halves>;
+  using E = BlockCols<BV, V::kThreads, 1, Halves>;
+  using P = Tile<T, X, E, DM, BV, V::WM, V::WN, Halves>;
+  static_assert(4 * P::kStage >= V::WN * 32 * DM * 4 && 2 * P::kStage >= BV * DM, "the stages hold rows of sums");
   static __device__ __forceinline__ void run(const SumArgs& a, int32_t bid, int32_t grid, uint16_t* lds) {
     const int32_t tiles = a.order.rows * a.order.cols, id = in_order(bid, grid);
     int32_t tv, td;
@@ -611,32 +619,33 @@ struct GradW {
     const int64_t s0 = min(steps, part * per), s1 = min(steps, s0 + per);
     P p;
     p.clear();
-    X x(a.h.x, a.h.dp, td * kD, s0 * kK);
+    X x(a.h.x, a.h.dp, td * DM, s0 * kK);
     E e(a.e, a.e_cols, (int64_t)tv * BV, s0 * kK);
     P::template ask<false, false>(x, e, (s1 - s0) * kK, lds);
     p.template run<false, false>(x, e, (s1 - s0) * kK, lds);
     float* to = a.part ? a.part + (int64_t)part * a.out_rows * a.h.dp : nullptr;
-    put_sums<T, P, BV, WM>(p, lds, a, to, (int64_t)tv * BV, a.out_rows, td * kD);
+    put_sums<P, DM, BV, V::WM>(p, lds, a, to, (int64_t)tv * BV, a.out_rows, td * DM);
   }
 };
 
-template <typename T, int BN, int WM, int WN, int Halves>
-__global__ void __launch_bounds__(WM * WN * kWave) k_grad_x(SumArgs a) {
-  using G = GradX<T, BN, WM, WN, Halves>;
+template <typename T, int DM>
+__global__ void __launch_bounds__((Waves<DM, 256>::kThreads)) k_grad_x(SumArgs a) {
+  using G = GradX<T, DM, 256, 1>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * G::P::kStage];
   G::run(a, blockIdx.x, lds);
 }
-template <typename T, int BV, int WM, int WN, int Halves>
-__global__ void __launch_bounds__(WM * WN * kWave) k_grad_w(SumArgs a) {
-  using G = GradW<T, BV, WM, WN, Halves>;
+template <typename T, int DM, int BV>
+__global__ void __launch_bounds__((Waves<DM, BV>::kThreads)) k_grad_w(SumArgs a) {
+  using G = GradW<T, DM, BV, 1>;
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * G::P::kStage];
   G::run(a, blockIdx.x, gridDim.x, lds);
 }
-// Both in one launch, dx's workgroups first, where neither fills the chip.
-template <typename T, int Halves>
-__global__ void __launch_bounds__(8 * kWave) k_grads(SumArgs x, SumArgs w, int32_t x_grid) {
-  using X = GradX<T, 64, 8, 1, Halves>;
-  using W = GradW<T, 64, 8, 1, Halves>;
+// Few tokens: both in one launch, dx's x_grid workgroups first, so that neither
+// waits for the other to leave the chip half empty.
+template <typename T, int DM, int Halves>
+__global__ void __launch_bounds__((Waves<DM, 64>::kThreads)) k_grads(SumArgs x, SumArgs w, int32_t x_grid) {
+  using X = GradX<T, DM, 64, Halves>;
+  using W = GradW<T, DM, 64, Halves>;
   static_assert(X::P::kStage == W::P::kStage, "one pair of stages");
   __shared__ __attribute__((aligned(16))) uint16_t lds[2 * X::P::kStage];
   if ((int32_t)blockIdx.x < x_grid) X::run(x, blockIdx.x, lds);
@@ -979,7 +988,7 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill_entries(Teach
 // ---------------------------------------------------------------- host
 struct Sizes {
   int64_t n, rows, npad, vpad, piece, pack_rows, pack_bytes, e_bytes, dx_part, dw_part, tiles;
-  int32_t dim, dp, bn, halves;
+  int32_t dim, dp, bn, halves, dm;  // tiles of bn tokens, gradients' of dm columns
 };
 
 int64_t most_parts(int64_t steps) { return std::min<int64_t>(kMostParts, std::max<int64_t>(1, steps / 4)); }
@@ -988,12 +997,12 @@ int64_t most_parts(int64_t steps) { return std::min<int64_t>(kMostParts, std::ma
 // number for which its rounds of workgroups take the least time, with the sums that
 // every part writes and somebody reads. Measured: a step of 64 takes a workgroup 1.8
 // us in tiles of 256 x 256 (one to a CU) and 0.9 in tiles of 64 rows (two to a CU),
-// its start and end about 6, memory gives 5 bytes in a ps. 256 tiles of 256 steps:
-// in two parts 479 us, in one 453.
-int32_t parts_of(int64_t tiles, int64_t steps, int32_t rows, int64_t bytes_each, int64_t bytes) {
+// less as there are fewer columns to load; its start and end take about 6, memory
+// gives 5 bytes in a ps. 256 tiles of 256 steps: in two parts 479 us, in one 453.
+int32_t parts_of(int64_t tiles, int64_t steps, int32_t rows, int32_t cols, int64_t bytes_each, int64_t bytes) {
   const int64_t most = std::min(most_parts(steps), std::max<int64_t>(1, bytes / std::max<int64_t>(bytes_each, 1)));
-  const int64_t at_once = rows == 64 ? 2 * kCus : kCus;
-  const double step = rows == 64 ? 0.9 : 1.8;
+  const int64_t at_once = kCus * std::min<int64_t>(4, std::max<int64_t>(1, 640 / (rows + cols)));
+  const double step = 1.8 * (rows + cols) / 512.0 * (rows == 64 ? 1.4 : 1.0);
   int32_t best = 1;
   double least = 1e300;
   for (int64_t p = 1; p <= most; p += 1 + p / 8) {
@@ -1015,6 +1024,7 @@ Sizes sizes_of(int64_t n, int64_t rows, int32_t dim) {
   s.dp = (int32_t)align_up((size_t)dim, kK);
   // Tiles of 64 tokens where those of 256 would be few or mostly empty
   s.bn = n > kFew && cdiv(n, 256) * cdiv(rows, kV) >= 512 ? 256 : 64;
+  s.dm = dim <= 64 ? 64 : (dim <= 128 ? 128 : 256);
   s.npad = (int64_t)align_up((size_t)std::max<int64_t>(n, 1), n > 128 ? 256 : 64);
   s.vpad = (int64_t)align_up((size_t)rows, kV);
   s.tiles = s.vpad / kV;
@@ -1131,36 +1141,29 @@ int launch_scores(const ScoreArgs& a, const Sizes& s, int32_t dtype, hipStream_t
 }
 
 // dx's and dw's products of a piece; a grid of 0 is left out.
-template <typename T, int Halves>
+template <typename T, int DM>
 void launch_grads(const SumArgs& x, int64_t x_grid, const SumArgs& w, int64_t w_grid, const Sizes& s,
                   int32_t bv, hipStream_t stream) {
-  const dim3 many(kWM * kWN * kWave), few(8 * kWave);
-  // one launch where dx leaves room beside it (64 tokens, 32000 rows of 64: 14 + 7.5
-  // -> @@ us)
-  if (x_grid > 0 && w_grid > 0 && s.bn == 64 && bv == 64 && x_grid < 2 * kCus) {
-    hipLaunchKernelGGL((k_grads<T, Halves>), dim3((unsigned)(x_grid + w_grid)), few, 0, stream, x, w,
-                       (int32_t)x_grid);
+  const dim3 many(Waves<DM, 256>::kThreads), few(Waves<DM, 64>::kThreads);
+  if (s.bn == 64) {
+    const dim3 grid((unsigned)(x_grid + w_grid));
+    if (s.halves == 1) hipLaunchKernelGGL((k_grads<T, DM, 1>), grid, few, 0, stream, x, w, (int32_t)x_grid);
+    else hipLaunchKernelGGL((k_grads<T, DM, 2>), grid, few, 0, stream, x, w, (int32_t)x_grid);
     return;
   }
   const dim3 gx((unsigned)x_grid), gw((unsigned)w_grid);
-  if (x_grid > 0) {
-    if constexpr (Halves == 1) {
-      if (s.bn == 256) hipLaunchKernelGGL((k_grad_x<T, 256, kWM, kWN, 1>), gx, many, 0, stream, x);
-      else hipLaunchKernelGGL((k_grad_x<T, 64, 8, 1, 1>), gx, few, 0, stream, x);
-    } else {
-      hipLaunchKernelGGL((k_grad_x<T, 64, 8, 1, Halves>), gx, few, 0, stream, x);
-    }
-  }
+  if (x_grid > 0) hipLaunchKernelGGL((k_grad_x<T, DM>), gx, many, 0, stream, x);
   if (w_grid > 0) {
-    if (bv == 256) hipLaunchKernelGGL((k_grad_w<T, 256, kWM, kWN, Halves>), gw, many, 0, stream, w);
-    else hipLaunchKernelGGL((k_grad_w<T, 64, 8, 1, Halves>), gw, few, 0, stream, w);
+    if (bv == 256) hipLaunchKernelGGL((k_grad_w<T, DM, 256>), gw, many, 0, stream, w);
+    else hipLaunchKernelGGL((k_grad_w<T, DM, 64>), gw, few, 0, stream, w);
   }
 }
 template <typename T>
 void launch_grads(const SumArgs& x, int64_t x_grid, const SumArgs& w, int64_t w_grid, const Sizes& s,
                   int32_t bv, hipStream_t stream) {
-  if (s.halves == 1) launch_grads<T, 1>(x, x_grid, w, w_grid, s, bv, stream);
-  else launch_grads<T, 2>(x, x_grid, w, w_grid, s, bv, stream);
+  if (s.dm == 64) launch_grads<T, 64>(x, x_grid, w, w_grid, s, bv, stream);
+  else if (s.dm == 128) launch_grads<T, 128>(x, x_grid, w, w_grid, s, bv, stream);
+  else launch_grads<T, 256>(x, x_grid, w, w_grid, s, bv, stream);
 }
 
 template <typename T>
@@ -1254,9 +1257,9 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
              TeacherArgs* entries, hipStream_t stream) {
   int rc;
   const int64_t step = t.direct ? s.piece : std::min(s.piece, s.pack_rows);
-  const int32_t token_tiles = (int32_t)cdiv(s.n, s.bn), col_tiles = (int32_t)cdiv(s.dim, kD);
+  const int32_t token_tiles = (int32_t)cdiv(s.n, s.bn), col_tiles = (int32_t)cdiv(s.dim, s.dm);
   const int32_t x_parts = parts_of((int64_t)token_tiles * col_tiles, cdiv(std::min(step, s.rows), kK) * s.halves,
-                                   s.bn, s.npad * s.dp * 4, s.dx_part);
+                                   s.bn, s.dm, s.npad * s.dp * 4, s.dx_part);
   for (int64_t v0 = 0; v0 < s.rows; v0 += step) {
     ScoreArgs a = {};
     a.h = o.h;
@@ -1302,13 +1305,14 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
       b.part = o.dx_part;
       x_grid = (int64_t)token_tiles * col_tiles * x_parts;
     }
-    // tiles of 64 rows where those of 256 would leave CUs idle
-    const int32_t bv = (int64_t)table_tiles * col_tiles < kCus ? 64 : kV;
+    // tiles of 64 rows beside tiles of 64 tokens, and where those of 256 would leave
+    // CUs idle
+    const int32_t bv = s.bn == 64 || (int64_t)table_tiles * col_tiles < kCus ? 64 : kV;
     if (g.dw) {
       const int32_t row_tiles = (int32_t)cdiv(a.rows, bv);
       const int64_t tiles = (int64_t)row_tiles * col_tiles;
       c.order = Order{row_tiles, col_tiles};
-      c.parts = parts_of(tiles, cdiv(s.n, kK) * s.halves, bv, a.rows * s.dp * 4, s.dw_part);
+      c.parts = parts_of(tiles, cdiv(s.n, kK) * s.halves, bv, s.dm, a.rows * s.dp * 4, s.dw_part);
       c.part = c.parts > 1 ? o.dw_part : nullptr;
       c.out = (char*)g.dw + v0 * g.dw_stride;
       c.out_stride = g.dw_stride;
