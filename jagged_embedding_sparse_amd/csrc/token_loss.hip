@@ -59,13 +59,46 @@ __device__ __forceinline__ u32x4 row_piece(const char* row, int32_t col, int32_t
   return r;
 }
 
+// A teacher's entries, [n][top]. One takes part where its id is a row of the table
+// and not the padding, and its logit is not -inf.
+struct Entries {
+  const int64_t* ids;
+  const char* teacher;
+  int32_t type, top;
+  int64_t rows, pad;
+  __device__ __forceinline__ float logit(int64_t i) const {
+    if (type == FS_F32) return ((const float*)teacher)[i];
+    if (type == FS_BF16) return (float)((const __bf16*)teacher)[i];
+    return (float)((const _Float16*)teacher)[i];
+  }
+  __device__ __forceinline__ bool on(int64_t id, float t) const {
+    return id >= 0 && id < rows && id != pad && t != -INFINITY;
+  }
+  __device__ __forceinline__ bool bad(int64_t id) const { return (id < 0 || id >= rows) && id != pad; }
+  // whether token i has one, four at a time
+  __device__ __forceinline__ bool any(int64_t i) const {
+    for (int k = 0; k < top; k += 4) {
+      bool found = false;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int64_t at = i * top + min(k + u, top - 1);
+        found |= on(ids[at], logit(at));
+      }
+      if (found) return true;
+    }
+    return false;
+  }
+};
+
 // ---------------------------------------------------------------- packing
 struct PackArgs {
   Head h;
   const char* x;
   int64_t x_stride;
-  const int64_t* labels;  // or null: live says which tokens take part
-  const uint8_t* live;
+  const int64_t* labels;  // or null: live says which tokens take part,
+  const uint8_t* live;    // or, of tokens that stay, their entries
+  Entries entries;
+  int32_t stay;           // few tokens: each keeps its place, with a row of zeros where it takes no part
   int64_t rows, pad;
   const float *lse, *dloss;  // backward
   int32_t back;
@@ -77,9 +110,10 @@ struct PackArgs {
 };
 
 constexpr int kPackThreads = 256;
+static_assert(kFew <= kPackThreads, "tokens that stay: at most one a thread");
 
 __device__ __forceinline__ bool takes_part(const PackArgs& a, int64_t i, bool* bad) {
-  if (!a.labels) return a.live[i] != 0;
+  if (!a.labels) return a.stay ? a.entries.any(i) : a.live[i] != 0;
   const int64_t v = a.labels[i];
   const bool in = v >= 0 && v < a.rows;
   *bad = !in && v != a.pad;
@@ -114,27 +148,44 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
   __shared__ int32_t tmp[17], s_row[kPackThreads];
   __shared__ float s_max[kPackThreads / kWave];
   const int64_t i0 = (int64_t)blockIdx.x * a.per, i1 = min(a.h.n, i0 + a.per);
-  int32_t count = 0;
   bool bad = false;
-  for (int64_t i = threadIdx.x; i < i0; i += kAtOnce * kPackThreads) count += __popc(take_part(a, i, i0));
-  int32_t base;
-  block_excl_scan<int32_t>(count, tmp, &base);
+  int32_t base = (int32_t)i0;
+  if (!a.stay) {
+    int32_t count = 0;
+    for (int64_t i = threadIdx.x; i < i0; i += kAtOnce * kPackThreads) count += __popc(take_part(a, i, i0));
+    block_excl_scan<int32_t>(count, tmp, &base);
+  }
   const int32_t pieces = a.h.dp / 8;
   const bool whole = a.h.dim % 8 == 0;
   for (int64_t c = i0; c < i1; c += kPackThreads) {  // uniform
     const int64_t i = c + threadIdx.x;
     bad = false;
-    const bool on = i < i1 && takes_part(a, i, &bad);
+    bool on;
+    int32_t at = threadIdx.x, total = (int32_t)min((int64_t)kPackThreads, i1 - c);
+    if (a.stay && !a.labels) {  // the threads share the tokens' entries
+      s_row[threadIdx.x] = 0;
+      __syncthreads();
+      const int32_t top = a.entries.top;
+      for (int32_t u = threadIdx.x; u < total * top; u += kPackThreads) {
+        const int64_t id = a.entries.ids[c * top + u];
+        bad |= a.entries.bad(id);
+        if (a.entries.on(id, a.entries.logit(c * top + u))) s_row[u / top] = 1;
+      }
+      __syncthreads();
+      on = i < i1 && s_row[threadIdx.x];
+      __syncthreads();
+    } else {
+      on = i < i1 && takes_part(a, i, &bad);
+    }
     flag_err(a.err, bad, FS_EF_ID_RANGE);
-    int32_t total;
-    const int32_t at = block_excl_scan<int32_t>(on ? 1 : 0, tmp, &total);
+    if (!a.stay) at = block_excl_scan<int32_t>(on ? 1 : 0, tmp, &total);
     if (i < i1) a.h.pos[i] = on ? base + at : -1;
-    if (on) {
-      s_row[at] = (int32_t)(i - i0);
-      a.h.label[base + at] = a.labels ? (int32_t)a.labels[i] : -1;
+    if (a.stay ? i < i1 : on) {
+      s_row[at] = on ? (int32_t)(i - i0) : -1;
+      a.h.label[base + at] = a.labels && on ? (int32_t)a.labels[i] : -1;
       if (a.back) {
-        a.h.lse2[base + at] = a.lse[i] * kLog2e;
-        a.h.coef[base + at] = a.dloss[i] * a.scale;
+        a.h.lse2[base + at] = on ? a.lse[i] * kLog2e : 0.f;
+        a.h.coef[base + at] = on ? a.dloss[i] * a.scale : 0.f;
       }
     }
     __syncthreads();
@@ -142,19 +193,21 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
     for (int32_t u0 = 0; u0 < all; u0 += 4 * kPackThreads) {  // four pieces of a thread in flight
       u32x4 v[4];
       int32_t r[4], p[4];
+      bool on_row[4];
 #pragma unroll
       for (int y = 0; y < 4; ++y) {
         const int32_t u = min(u0 + y * kPackThreads + (int32_t)threadIdx.x, all - 1);
         r[y] = u / pieces;
         p[y] = u - r[y] * pieces;
-        const char* row = a.x + (i0 + s_row[r[y]]) * a.x_stride;
+        on_row[y] = s_row[r[y]] >= 0;
+        const char* row = a.x + (i0 + max(s_row[r[y]], 0)) * a.x_stride;
         if (whole) v[y] = *(const u32x4_any*)(row + 16 * (8 * p[y] < a.h.dim ? p[y] : 0));
         else v[y] = row_piece(row, 8 * p[y], a.h.dim);
       }
 #pragma unroll
       for (int y = 0; y < 4; ++y)
         *(u32x4*)(a.h.x + 2 * blocked(base + r[y], 8 * p[y], a.h.dp)) =
-            8 * p[y] < a.h.dim ? v[y] : u32x4{0, 0, 0, 0};
+            on_row[y] && 8 * p[y] < a.h.dim ? v[y] : u32x4{0, 0, 0, 0};
     }
     base += total;
     __syncthreads();
@@ -174,7 +227,11 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
     // that takes the largest coefficient to 2^13 .. 2^14, and the sums lose it again
     float top = 0.f;
     if (a.narrow) {
-      for (int64_t i = threadIdx.x; i < a.h.n; i += kAtOnce * kPackThreads) {
+      if (a.stay) {  // at most a token a thread
+        if (threadIdx.x < a.h.n && takes_part(a, threadIdx.x, &bad))
+          top = fabsf(a.dloss[threadIdx.x] * a.scale);
+      }
+      for (int64_t i = threadIdx.x; !a.stay && i < a.h.n; i += kAtOnce * kPackThreads) {
         float d[kAtOnce];
 #pragma unroll
         for (int u = 0; u < kAtOnce; ++u) d[u] = a.dloss[min(i + u * kPackThreads, a.h.n - 1)];
@@ -763,10 +820,7 @@ __global__ void __launch_bounds__(256) k_loss(LossArgs a) {
 // ---------------------------------------------------------------- distillation
 struct TeacherArgs {
   Head h;
-  const int64_t* ids;  // [n][top]
-  const char* teacher;
-  int32_t type, top;
-  int64_t rows, pad;
+  Entries in;
   float scale;
   uint8_t* live;
   int32_t* err;
@@ -785,25 +839,14 @@ struct TeacherArgs {
 
 constexpr int kRowsPerGroup = 4;  // tokens of a workgroup, a wave each
 
-__device__ __forceinline__ float teacher_at(const TeacherArgs& a, int64_t i) {
-  if (a.type == FS_F32) return ((const float*)a.teacher)[i];
-  if (a.type == FS_BF16) return (float)((const __bf16*)a.teacher)[i];
-  return (float)((const _Float16*)a.teacher)[i];
-}
-// An entry takes part where its id is a row of the table and not the padding,
-// and its logit is not -inf.
-__device__ __forceinline__ bool entry_on(const TeacherArgs& a, int64_t id, float t) {
-  return id >= 0 && id < a.rows && id != a.pad && t != -INFINITY;
-}
-
 __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_teacher_live(TeacherArgs a) {
   const int64_t i = (int64_t)blockIdx.x * kRowsPerGroup + threadIdx.x / kWave;
   if (i >= a.h.n) return;
   bool on = false, bad = false;
-  for (int k = lane(); k < a.top; k += kWave) {
-    const int64_t id = a.ids[i * a.top + k];
-    bad |= (id < 0 || id >= a.rows) && id != a.pad;
-    on |= entry_on(a, id, teacher_at(a, i * a.top + k));
+  for (int k = lane(); k < a.in.top; k += kWave) {
+    const int64_t id = a.in.ids[i * a.in.top + k];
+    bad |= a.in.bad(id);
+    on |= a.in.on(id, a.in.logit(i * a.in.top + k));
   }
   flag_err(a.err, bad, FS_EF_ID_RANGE);
   const bool any = __any(on);
@@ -826,10 +869,10 @@ struct Teacher {
       on[u] = false;
       id[u] = -1;
       t[u] = 0.f;
-      if (k < a.top) {
-        id[u] = a.ids[i * a.top + k];
-        const float x = teacher_at(a, i * a.top + k);
-        on[u] = entry_on(a, id[u], x);
+      if (k < a.in.top) {
+        id[u] = a.in.ids[i * a.in.top + k];
+        const float x = a.in.logit(i * a.in.top + k);
+        on[u] = a.in.on(id[u], x);
         t[u] = x * a.scale;
       }
       if (on[u]) top = fmaxf(top, t[u]);
@@ -862,26 +905,26 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
   const int64_t i = blockIdx.x;
   const int32_t pos = a.h.pos[i];
   if (pos < 0) {
-    for (int k = threadIdx.x; k < a.top; k += kRowsPerGroup * kWave) a.logits[i * a.top + k] = 0.f;
+    for (int k = threadIdx.x; k < a.in.top; k += kRowsPerGroup * kWave) a.logits[i * a.in.top + k] = 0.f;
     if (threadIdx.x == 0) {
       a.loss[i] = 0.f;
       if (a.part) a.lse[i] = 0.f;
     }
     return;
   }
-  for (int k = threadIdx.x; k < a.top; k += kRowsPerGroup * kWave) {
-    const int64_t id = a.ids[i * a.top + k];
-    s_id[k] = entry_on(a, id, teacher_at(a, i * a.top + k)) ? id : -1;
+  for (int k = threadIdx.x; k < a.in.top; k += kRowsPerGroup * kWave) {
+    const int64_t id = a.in.ids[i * a.in.top + k];
+    s_id[k] = a.in.on(id, a.in.logit(i * a.in.top + k)) ? id : -1;
   }
   __syncthreads();
   constexpr int kRows = 8;
-  for (int k0 = w; k0 < a.top; k0 += kRows * kRowsPerGroup) {  // uniform in a wave
+  for (int k0 = w; k0 < a.in.top; k0 += kRows * kRowsPerGroup) {  // uniform in a wave
     int64_t id[kRows];
     float sum[kRows];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
       const int k = k0 + u * kRowsPerGroup;
-      id[u] = k < a.top ? s_id[k] : -1;
+      id[u] = k < a.in.top ? s_id[k] : -1;
       sum[u] = 0.f;
     }
     for (int c = 8 * l; c < a.h.dim; c += 8 * kWave) {
@@ -905,7 +948,7 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
     for (int u = 0; u < kRows; ++u) {
       const float z = wave_sum(sum[u]) * a.scale;
       const int k = k0 + u * kRowsPerGroup;
-      if (l == 0 && k < a.top) s_z[k] = id[u] >= 0 ? z : 0.f;
+      if (l == 0 && k < a.in.top) s_z[k] = id[u] >= 0 ? z : 0.f;
     }
   }
   __shared__ float2 s_part[kRowsPerGroup];
@@ -942,9 +985,9 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
 #pragma unroll
   for (int u = 0; u < kPerLane; ++u) {
     const int k = l + kWave * u;
-    if (k < a.top) {
+    if (k < a.in.top) {
       const float z = s_z[k];
-      a.logits[i * a.top + k] = z;
+      a.logits[i * a.in.top + k] = z;
       if (t.on[u] && t.q[u] != 0.f) loss += t.q[u] * (t.logq[u] - z + lse);
     }
   }
@@ -977,8 +1020,8 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill_entries(Teach
     const int64_t v = t.id[u] - a.v0;
     if (!t.on[u] || v < 0 || v >= a.piece_rows) continue;
     float q = 0.f;
-    for (int k = 0; k < a.top; ++k) q += s_id[w][k] == t.id[u] ? s_q[w][k] : 0.f;
-    const float z = a.logits_in[i * a.top + l + kWave * u];
+    for (int k = 0; k < a.in.top; ++k) q += s_id[w][k] == t.id[u] ? s_q[w][k] : 0.f;
+    const float z = a.logits_in[i * a.in.top + l + kWave * u];
     const float e = (__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -lse2)) - q) * c;
     ((T*)a.e)[place_of_e(pos, v, a.e_cols, 0, a.halves)] = (T)e;
     if (a.halves > 1) ((T*)a.e)[place_of_e(pos, v, a.e_cols, 1, 2)] = (T)(e - (float)(T)e);
@@ -1353,6 +1396,7 @@ PackArgs pack_args(const Space& o, const Sizes& s, const void* x, int64_t x_stri
   p.pad = padding_id;
   p.scale = scale;
   p.pad_to = s.bn;
+  p.stay = s.n <= kFew;
   p.narrow = dtype == FS_F16;
   p.err = err;
   return p;
@@ -1366,23 +1410,22 @@ TeacherArgs teacher_args(const Space& o, const Sizes& s, const int64_t* ids, int
                          int32_t type, float scale, int64_t padding_id, int32_t* err) {
   TeacherArgs t = {};
   t.h = o.h;
-  t.ids = ids;
-  t.teacher = (const char*)teacher;
-  t.type = type;
-  t.top = top;
-  t.rows = s.rows;
-  t.pad = padding_id;
+  t.in = Entries{ids, (const char*)teacher, type, top, s.rows, padding_id};
   t.scale = scale;
   t.live = o.live;
   t.err = err;
   return t;
 }
 
-int teacher_live(const TeacherArgs& t, hipStream_t stream) {
+// Packs a distillation's tokens; those that stay need no launch for who takes part
+// (few tokens' calls are a launch of 4 us shorter).
+int pack_entries(const TeacherArgs& t, PackArgs p, hipStream_t stream) {
+  p.entries = t.in;
+  if (p.stay) return pack_tokens(p, stream);
   hipLaunchKernelGGL(k_teacher_live, dim3((unsigned)cdiv(t.h.n, kRowsPerGroup)), dim3(kRowsPerGroup * kWave), 0,
                      stream, t);
   FS_LAUNCH_CHECK();
-  return FS_OK;
+  return pack_tokens(p, stream);
 }
 
 }  // namespace
@@ -1462,8 +1505,7 @@ extern "C" int fs_token_distill(const void* x, int64_t x_stride, int64_t n, cons
   Space o;
   carve(aligned(ws), s, false, &o);
   TeacherArgs a = teacher_args(o, s, ids, top, teacher, teacher_dtype, scale, padding_id, err);
-  if ((rc = teacher_live(a, stream)) ||
-      (rc = pack_tokens(pack_args(o, s, x, x_stride, nullptr, padding_id, scale, table->dtype, err), stream)) ||
+  if ((rc = pack_entries(a, pack_args(o, s, x, x_stride, nullptr, padding_id, scale, table->dtype, err), stream)) ||
       (rc = forward(s, o, t, table->dtype, scale, false, loss, lse, stream)))
     return rc;
   a.w = t.w;
@@ -1502,11 +1544,10 @@ extern "C" int fs_token_distill_backward(const void* x, int64_t x_stride, int64_
   carve(aligned(ws), s, true, &o);
   TeacherArgs a = teacher_args(o, s, ids, top, teacher, teacher_dtype, scale, padding_id, err);
   a.logits_in = logits;
-  if (n > 0 && (rc = teacher_live(a, stream))) return rc;
   PackArgs p = pack_args(o, s, x, x_stride, nullptr, padding_id, scale, table->dtype, err);
   p.lse = lse;
   p.dloss = dloss;
   p.back = 1;
-  if ((rc = pack_tokens(p, stream))) return rc;
+  if ((rc = pack_entries(a, p, stream))) return rc;
   return backward(s, o, t, table->dtype, scale, g, &a, stream);
 }
