@@ -296,22 +296,18 @@ struct Tile {
   // Adds the product over `k` k's in steps of 64, behind ask(); in the last step the
   // operands are told how many are left where Lim says so. lds: 2 kStage elements.
   // The stages are free again when it returns, the second one before it begins.
-  // Since ask() the wave has issued `After` memory operations or more (of which
-  // none has to be waited for at the start: they complete in order), or none
-  // where `fresh`.
   //
   // Products, reads and loads are issued in this order and no other (left to
   // itself the compiler reads a chunk's operands right before its products and
   // waits for them there).
-  template <bool LimA, bool LimB, int After = 0>
-  __device__ __forceinline__ void run(A& a, B& b, int64_t k, uint16_t* lds, bool fresh = true) {
+  template <bool LimA, bool LimB>
+  __device__ __forceinline__ void run(A& a, B& b, int64_t k, uint16_t* lds) {
     const typename A::Read ra;
     const typename B::Read rb;
     const uint32_t lds0 = lds_address(lds);
     const int steps = (int)cdiv(k, (int64_t)kK) * Turns;
     if (steps <= 0) return;
-    if (After == 0 || fresh) landed();
-    else landed<After>();
+    landed();
     if (steps > 1) ask_step<LimA, LimB>(a, b, k, 1, lds0 + kStage * 2);
     Operands o[2];
 #pragma unroll
@@ -379,9 +375,8 @@ struct Tile {
   }
 
   // every wave's loads have landed and every wave's reads of LDS are done
-  template <int But = 0>  // all but the latest operations
   static __device__ __forceinline__ void landed() {
-    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"n"(But) : "memory");
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }

@@ -24,14 +24,13 @@ using namespace prod;
 
 constexpr float kLog2e = attn::kLog2e, kLn2 = attn::kLn2;
 constexpr int kV = 256;                           // table rows of a tile
-#ifndef PB
-#define PB 30
-#endif
-constexpr int64_t kPieceBytes = (int64_t)1 << PB;  // e of one piece of the table
+// e of one piece of the table: every piece adds to dx's fp32 sums in memory (16384 x
+// 131072 x 1024: pieces of 2^29 bytes 11.5 ms, 2^30 11.4, 2^27 13.3)
+constexpr int64_t kPieceBytes = (int64_t)1 << 30;
 constexpr int64_t kPackBytes = (int64_t)1 << 26;   // a piece of a table that has to be laid out
 constexpr int64_t kPartBytes = (int64_t)1 << 28;   // sums of a cut product
 constexpr int kMostParts = 256;
-constexpr int64_t kFew = 256;
+constexpr int64_t kFew = 256;                      // tokens, see ScoreArgs::e and PackArgs::stay
 constexpr int64_t kCacheBytes = (int64_t)1 << 27;  // half of the last level
 
 // What the kernels of one call share, in its workspace.
@@ -300,11 +299,7 @@ __device__ __forceinline__ int64_t place_of_e(int64_t n, int64_t v, int64_t cols
 }
 
 // waves of a tile: 256 x 256 and 256 x 64
-#ifndef W_M
-#define W_M 2
-#define W_N 4
-#endif
-constexpr int kWM = W_M, kWN = W_N;
+constexpr int kWM = 2, kWN = 4;
 constexpr int kMostThreads = 512;
 constexpr int kCus = 256;
 constexpr int kGroup = 8;  // token tiles that go by a table tile together
@@ -497,15 +492,13 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
   if constexpr (kMany) ask_info<BN, WM * WN, Back>(a.h, (int64_t)tn * BN, info[0]);
   const float mul = Back ? __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(a.h.mul[0]))) : 1.f;
   P::template ask<true, false>(w, x, a.k, lds);
-  // a thread's stores of e behind the next tile's loads
-  constexpr int kAfter = Back ? P::NI * WN * 32 * kV / 8 / NT : 0;
   int turn = 0;
   for (int32_t id = blockIdx.x; id < tiles; id += gridDim.x) {  // uniform
     const int64_t n0 = (int64_t)tn * BN, v0 = (int64_t)tv * kV;
     const int32_t tile = tv;
     P p;
     p.clear();
-    p.template run<true, false, kAfter>(w, x, a.k, lds, id == (int32_t)blockIdx.x);
+    p.template run<true, false>(w, x, a.k, lds);
     if (id + (int32_t)gridDim.x < tiles) {  // the next tile's first loads, behind this one's scores
       order.at(in_order(id + gridDim.x, tiles), kGroup, &tn, &tv);
       w = Rows<kV, NT>(a.w, a.w_stride, (int64_t)tv * kV, a.rows, 0);
@@ -1291,7 +1284,7 @@ int check_grads(Grads* g, int64_t n, int32_t dim) {
   if (!g->dx_stride) g->dx_stride = 2 * (int64_t)dim;
   if (!g->dw_stride) g->dw_stride = e * (int64_t)dim;
   if (g->dx_stride < 2 * (int64_t)dim || g->dx_stride % 2 || (uintptr_t)g->dx % 2 ||
-      g->dw_stride < e * (int64_t)dim || g->dw_stride % e || (uintptr_t)g->dw % e || (!g->dx && !g->dw))
+      g->dw_stride < e * (int64_t)dim || g->dw_stride % e || (uintptr_t)g->dw % e || (n > 0 && !g->dx && !g->dw))
     return FS_ERR_INVALID_ARG;
   return FS_OK;
 }
@@ -1477,6 +1470,7 @@ extern "C" int fs_token_loss_backward(const void* x, int64_t x_stride, int64_t n
   if (too_many(s)) return FS_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < fs_token_loss_backward_workspace_size(n, table->rows, table->dim))
     return FS_ERR_WORKSPACE;
+  if (n == 0 && !dweight) return FS_OK;
   Space o;
   carve(aligned(ws), s, true, &o);
   PackArgs p = pack_args(o, s, x, x_stride, labels, padding_id, scale, table->dtype, err);
@@ -1540,6 +1534,7 @@ extern "C" int fs_token_distill_backward(const void* x, int64_t x_stride, int64_
   if (too_many(s)) return FS_ERR_UNSUPPORTED;
   if (!ws || ws_bytes < fs_token_loss_backward_workspace_size(n, table->rows, table->dim))
     return FS_ERR_WORKSPACE;
+  if (n == 0 && !dweight) return FS_OK;
   Space o;
   carve(aligned(ws), s, true, &o);
   TeacherArgs a = teacher_args(o, s, ids, top, teacher, teacher_dtype, scale, padding_id, err);

@@ -159,6 +159,8 @@ def test_no_tokens(kind):
     assert got["loss"].shape == got["lse"].shape == (0,)
     dx, dw = backward(x.cuda(), w.cuda(), s, got, dloss)
     assert dx.shape == (0, 64) and dw.shape == (300, 64) and not dw.any()
+    dx, none = backward(x.cuda(), w.cuda(), s, got, dloss, dweight=False)
+    assert dx.shape == (0, 64) and none is None
 
 
 @pytest.mark.parametrize("kind", KINDS)
@@ -327,35 +329,42 @@ def test_two_streams_at_once(kind):
 
 @pytest.mark.parametrize("kind", KINDS)
 def test_more_pieces_than_one(kind):
-    """e of 9000 tokens and 40000 rows is more than one piece; held to 64-bit
-    products on the GPU, with the sums' bounds."""
-    n, rows, dim = 9000, 40_000, 64
+    """e of 9000 tokens and 70000 rows is more than one piece of 2^30 bytes; held to
+    64-bit products on the GPU, with the sums' bounds."""
+    n, rows, dim = 9000, 70_000, 64
     x, w, s, dloss = inputs(kind, n, rows, dim, masked=0.1)
     xd, wd = x.cuda(), w.cuda()
     got = forward(xd, wd, s)
     dx, dw = backward(xd, wd, s, got, dloss, dtype=F32)
     dw_want, dw_size = torch.zeros(rows, dim).cuda().double(), torch.zeros(rows, dim).cuda().double()
-    live, _, _ = H._targets(rows, **{k: v[:0] for k, v in s.items()})
-    for lo in range(0, n, 3000):
-        part = {k: v[lo:lo + 3000] for k, v in s.items()}
+    for lo in range(0, n, 1500):
+        part = {k: v[lo:lo + 1500] for k, v in s.items()}
         live, target, own = H._targets(rows, **part)
         live, target = live.cuda(), target.cuda()
-        a = torch.where(live[:, None], xd[lo:lo + 3000].double(), 0.0)
+        a = torch.where(live[:, None], xd[lo:lo + 1500].double(), 0.0)
         z = a @ wd.double().T
         lse = torch.logsumexp(z, 1)
         loss = torch.where(live, own.cuda() - (target * z).sum(1) + lse, 0.0)
-        assert (got["loss"][lo:lo + 3000] - loss).abs().max() < 1e-4
-        c = torch.where(live, dloss[lo:lo + 3000].cuda().double(), 0.0)[:, None]
-        e = c * (torch.exp(z - got["lse"][lo:lo + 3000, None].double()) - target)
+        assert (got["loss"][lo:lo + 1500] - loss).abs().max() < 1e-4
+        c = torch.where(live, dloss[lo:lo + 1500].cuda().double(), 0.0)[:, None]
+        e = c * (torch.exp(z - got["lse"][lo:lo + 1500, None].double()) - target)
         want, size = e @ wd.double(), e.abs() @ wd.double().abs()
         # half a step of e and of the result (bf16 has 8 bits, so a step is 2^-7 of
         # the value at most and half of it 2^-8), and what fp32 sums of many terms
         # of either sign leave
         bound = size * (2.0 ** -8 + 2.0 ** -13) + 2.0 ** -8 * want.abs() + 1e-30
-        assert ((dx[lo:lo + 3000].double() - want).abs() <= bound * 1.01).all()
+        assert ((dx[lo:lo + 1500].double() - want).abs() <= bound * 1.01).all()
         dw_want += e.T @ a
         dw_size += e.abs().T @ a.abs()
     assert ((dw.double() - dw_want).abs() <= dw_size * (2.0 ** -8 + 2.0 ** -13) + 1e-30).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("n,dim", [(20, 100), (300, 100)])
+def test_a_table_laid_out_in_pieces(kind, n, dim):
+    """Rows of 200 bytes are laid out in the workspace, 2^26 bytes of them a time."""
+    x, w, s, dloss = inputs(kind, n, 300_000, dim, top=3)
+    both(x, w, s, dloss)
 
 
 @pytest.mark.parametrize("kind", KINDS)
