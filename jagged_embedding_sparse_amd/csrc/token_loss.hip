@@ -320,18 +320,18 @@ __device__ __forceinline__ void ask_info(const Head& h, int64_t n0, float (*info
   }
 }
 
-// Where a tile's tokens' label, lse2 and coef are read: LDS, or memory where a
-// workgroup has one tile.
+// A tile's tokens' label, lse2 and coef: in LDS, or where a workgroup has one tile in
+// registers, a lane's NI tokens, read ahead of its product.
 template <int BN>
 struct TokenInfo {
   const float (*lds)[BN];
-  const Head& h;
-  int64_t n0;
-  __device__ __forceinline__ int32_t label(int n) const {
-    return BN == 256 ? __float_as_int(lds[0][n]) : h.label[n0 + n];
+  int32_t labels[2];
+  float lse2s[2], coefs[2];
+  __device__ __forceinline__ int32_t label(int n, int j) const {
+    return BN == 256 ? __float_as_int(lds[0][n]) : labels[j];
   }
-  __device__ __forceinline__ float lse2(int n) const { return BN == 256 ? lds[1][n] : h.lse2[n0 + n]; }
-  __device__ __forceinline__ float coef(int n) const { return BN == 256 ? lds[2][n] : h.coef[n0 + n]; }
+  __device__ __forceinline__ float lse2(int n, int j) const { return BN == 256 ? lds[1][n] : lse2s[j]; }
+  __device__ __forceinline__ float coef(int n, int j) const { return BN == 256 ? lds[2][n] : coefs[j]; }
 };
 
 // What a tile's scores leave behind, by way of the stage that the next tile's
@@ -380,7 +380,7 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
 #pragma unroll
     for (int j = 0; j < P::NI; ++j) {
       const int n = P::n_of(j, l);
-      const int64_t lab = (int64_t)info.label(n) - a.v0 - v0;
+      const int64_t lab = (int64_t)info.label(n, j) - a.v0 - v0;
       if (lab >= 0 && lab < kV && has((int)lab)) a.at_label[n0 + n] = product_at(j, (int)lab) * scale2;
       float top = p.acc[0][j][0];
 #pragma unroll
@@ -409,60 +409,76 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
       a.part[(int64_t)(a.v_tile0 + tv) * a.h.npad + n0 + n] = make_float2(top, sum);
     }
   } else {
-    constexpr int kRows = WN * 32;
-    static_assert(P::kStage >= kRows * kV, "a stage holds a pass of e");
-    for (int half = 0; half < Halves; ++half) {
-      auto rounded = [&](float x, float y) {
-        uint32_t u = Elem<T>::pack(x, y);
-        if (half) {  // uniform
-          const auto back = Elem<T>::unpack(u);
-          u = Elem<T>::pack(x - back[0], y - back[1]);
+    // Rows of e that pass through LDS at once: all of them and both halves where no
+    // next tile's loads are under way, else a block of 32 a wave.
+    constexpr bool kWhole = BN == 64;
+    constexpr int kRows = kWhole ? BN : WN * 32, kPieces = kV / 8;
+    static_assert((kWhole ? 2 * P::kStage : P::kStage) >= (kWhole ? Halves : 1) * kRows * kV, "LDS holds a pass of e");
+    uint16_t* const at0 = kWhole ? lds - P::kStage : lds;
+    auto store = [&](int half, int j) {
+#pragma unroll 4
+      for (int y = 0; y < kRows * kPieces / NT; ++y) {  // block by block
+        const int u = y * NT + tid, r = u / 8 % kRows, piece = u / (8 * kRows) * 8 + u % 8;
+        const int n = kWhole ? r : (r / 32 * P::NI + j) * 32 + r % 32;
+        const u32x4 v = Stage16<kV>::get(at0 + (kWhole ? half * kRows * kV : 0), r, piece);
+        u32x4* to = (u32x4*)(a.e + 2 * place_of_e(n0 + n, v0 + 8 * piece, a.e_cols, half, Halves));
+        // what outgrows the caches goes past them: they hold the operands of the
+        // tiles beside this one (597 -> 565 us, and the product that reads e 503
+        // -> 479); less is read from them soon
+        if (Halves == 1 && a.past) __builtin_nontemporal_store(v, to);
+        else *to = v;
+      }
+    };
+#pragma unroll
+    for (int j = 0; j < P::NI; ++j) {
+      if (j && !kWhole) lds_barrier();
+      const int n = P::n_of(j, l), s = kWhole ? n : attn::wave_id() / WM * 32 + (l & 31);
+      const int64_t lab = (int64_t)info.label(n, j) - a.v0 - v0;
+      const float lse2 = info.lse2(n, j), c = info.coef(n, j) * mul;
+      // c exp2(s) = exp2(s + log2 c): the factor costs no instruction of its own
+      const float at = __builtin_amdgcn_logf(fabsf(c)) - lse2;
+      const uint32_t sign = c < 0.f ? 0x80008000u : 0u;
+      // two values rounded, and what that leaves of them
+      auto rounded = [](float x, float y, uint32_t* u) {
+        u[0] = Elem<T>::pack(x, y);
+        if (Halves > 1) {
+          const auto back = Elem<T>::unpack(u[0]);
+          u[1] = Elem<T>::pack(x - back[0], y - back[1]);
         }
-        return u;
       };
 #pragma unroll
-      for (int j = 0; j < P::NI; ++j) {
-        if (j || half) lds_barrier();
-        const int n = P::n_of(j, l), s = attn::wave_id() / WM * 32 + (l & 31);
-        const int64_t lab = (int64_t)info.label(n) - a.v0 - v0;
-        const float lse2 = info.lse2(n), c = info.coef(n) * mul;
-        // c exp2(s) = exp2(s + log2 c): the factor costs no instruction of its own
-        const float at = __builtin_amdgcn_logf(fabsf(c)) - lse2;
-        const uint32_t sign = c < 0.f ? 0x80008000u : 0u;
+      for (int i = 0; i < P::MI; ++i)
 #pragma unroll
-        for (int i = 0; i < P::MI; ++i)
+        for (int q = 0; q < 4; ++q) {
+          const int m = P::m_of(i, l) + 8 * q;
+          float v[4];
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int m = P::m_of(i, l) + 8 * q;
-            float v[4];
+          for (int r = 0; r < 4; ++r)
+            v[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][4 * q + r], scale2, at));
+          uint32_t y0[2], y1[2];
+          rounded(v[0], v[1], y0);
+          rounded(v[2], v[3], y1);
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-              v[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(p.acc[i][j][4 * q + r], scale2, at));
-            u32x2 y;
-            y[0] = rounded(v[0], v[1]) ^ sign;
-            y[1] = rounded(v[2], v[3]) ^ sign;
-            Stage16<kV>::put(lds, s, m, y);
-          }
-        // the label's place, from the difference
-        if (lab >= 0 && lab < kV && has((int)lab)) {
-          const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(product_at(j, (int)lab), scale2, -lse2)) - 1.f;
-          Stage16<kV>::put1(lds, s, (int)lab, rounded(v * c, 0.f));
+          for (int half = 0; half < Halves; ++half)
+            Stage16<kV>::put(at0 + half * kRows * kV, s, m, u32x2{y0[half] ^ sign, y1[half] ^ sign});
         }
-        lds_barrier();
-        constexpr int kPieces = kV / 8;
-#pragma unroll 4
-        for (int y = 0; y < kRows * kPieces / NT; ++y) {  // block by block
-          const int u = y * NT + tid, r = u / 8 % kRows, piece = u / (8 * kRows) * 8 + u % 8;
-          const u32x4 v = Stage16<kV>::get(lds, r, piece);
-          u32x4* to = (u32x4*)(a.e + 2 * place_of_e(n0 + (r / 32 * P::NI + j) * 32 + r % 32, v0 + 8 * piece,
-                                                    a.e_cols, half, Halves));
-          // what outgrows the caches goes past them: they hold the operands of the
-          // tiles beside this one (597 -> 565 us, and the product that reads e 503
-          // -> 479); less is read from them soon
-          if (Halves == 1 && a.past) __builtin_nontemporal_store(v, to);
-          else *to = v;
-        }
+      // the label's place, from the difference
+      if (lab >= 0 && lab < kV && has((int)lab)) {
+        const float v = __builtin_amdgcn_exp2f(__builtin_fmaf(product_at(j, (int)lab), scale2, -lse2)) - 1.f;
+        uint32_t y[2];
+        rounded(v * c, 0.f, y);
+#pragma unroll
+        for (int half = 0; half < Halves; ++half) Stage16<kV>::put1(at0 + half * kRows * kV, s, (int)lab, y[half]);
       }
+      if (!kWhole) {
+        lds_barrier();
+        store(0, j);
+      }
+    }
+    if (kWhole) {
+      lds_barrier();
+#pragma unroll
+      for (int half = 0; half < Halves; ++half) store(half, 0);
     }
   }
 }
@@ -496,6 +512,17 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
   for (int32_t id = blockIdx.x; id < tiles; id += gridDim.x) {  // uniform
     const int64_t n0 = (int64_t)tn * BN, v0 = (int64_t)tv * kV;
     const int32_t tile = tv;
+    TokenInfo<BN> its;
+    if constexpr (kMany) {
+      its.lds = (const float(*)[BN])info[turn];
+    } else {
+#pragma unroll
+      for (int j = 0; j < P::NI; ++j) {
+        its.labels[j] = a.h.label[n0 + P::n_of(j)];
+        its.lse2s[j] = Back ? a.h.lse2[n0 + P::n_of(j)] : 0.f;
+        its.coefs[j] = Back ? a.h.coef[n0 + P::n_of(j)] : 0.f;
+      }
+    }
     P p;
     p.clear();
     p.template run<true, false>(w, x, a.k, lds);
@@ -506,7 +533,6 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
       if constexpr (kMany) ask_info<BN, WM * WN, Back>(a.h, (int64_t)tn * BN, info[turn ^ 1]);
       P::template ask<true, false>(w, x, a.k, lds);
     }
-    const TokenInfo<BN> its{kMany ? (const float(*)[BN])info[turn] : nullptr, a.h, n0};
     finish_scores<T, BN, WM, WN, Halves>(a, p, second, n0, v0, tile, its, mul);
     if (kMany) turn ^= 1;
   }
