@@ -1,6 +1,6 @@
-// Tile products of 16-bit matrices on the matrix cores: a workgroup of eight
-// waves computes out[n][m] = sum over k of A(m, k) B(n, k) for BM columns m and
-// BN rows n of the output, with fp32 sums in registers.
+// Tile products of 16-bit matrices on the matrix cores: a workgroup's waves compute
+// out[n][m] = sum over k of A(m, k) B(n, k) for BM columns m and BN rows n of the
+// output, with fp32 sums in registers.
 //
 // An operand lies in memory in one of two ways: Rows, its row m (or n) holding
 // the k's one after another, or Cols, its row k holding the m's. Either travels
@@ -14,6 +14,13 @@
 // of a step stands before its last chunk's products, which cover the first reads
 // of the next stage. Loads are asked for right behind the barrier, a whole step
 // before they are waited for.
+//
+// Measured (256 x 256, eight waves, K = 32768, 16384 x 1024 sums, bf16): 850 us, 1290
+// TFLOP/s, the matrix units busy 70% of the time at a clock that the card has brought
+// down from 2.4 to 1.65 GHz, so what bounds it is power. A library product of these
+// shapes reaches 960 to 1060, one of 8192^3 1380. Four waves of 128 x 128 instead of
+// eight of 128 x 64 do not fit the registers (737 against 613 us for 16384 x 16384 x
+// 1024); left to the compiler's order of reads and products, 470 against 458.
 #pragma once
 
 #include <type_traits>

@@ -30,7 +30,7 @@ constexpr int64_t kPieceBytes = (int64_t)1 << 30;
 constexpr int64_t kPackBytes = (int64_t)1 << 26;   // a piece of a table that has to be laid out
 constexpr int64_t kPartBytes = (int64_t)1 << 28;   // sums of a cut product
 constexpr int kMostParts = 256;
-constexpr int64_t kFew = 256;                      // tokens, see ScoreArgs::e and PackArgs::stay
+constexpr int64_t kFew = 256;                      // tokens, see ScoreArgs::e
 constexpr int64_t kCacheBytes = (int64_t)1 << 27;  // half of the last level
 
 // What the kernels of one call share, in its workspace.
@@ -109,7 +109,6 @@ struct PackArgs {
 };
 
 constexpr int kPackThreads = 256;
-static_assert(kFew <= kPackThreads, "tokens that stay: at most one a thread");
 
 __device__ __forceinline__ bool takes_part(const PackArgs& a, int64_t i, bool* bad) {
   if (!a.labels) return a.stay ? a.entries.any(i) : a.live[i] != 0;
@@ -140,12 +139,58 @@ __device__ __forceinline__ uint32_t take_part(const PackArgs& a, int64_t i, int6
   return left < kAtOnce ? on & ((1u << left) - 1) : on;
 }
 
+// What e is rounded times, and its inverse, by one workgroup. fp16's exponents end
+// where e's do not: there it is a power of two that takes the largest coefficient to
+// 2^13 .. 2^14, and the sums lose it again.
+__device__ void put_mul(const PackArgs& a) {
+  __shared__ float s_max[kPackThreads / kWave];
+  bool bad = false;
+  float top = 0.f;
+  if (a.narrow) {
+    if (a.stay) {  // few tokens a thread
+      for (int64_t i = threadIdx.x; i < a.h.n; i += kPackThreads)
+        if (takes_part(a, i, &bad)) top = fmaxf(top, fabsf(a.dloss[i] * a.scale));
+    }
+    for (int64_t i = threadIdx.x; !a.stay && i < a.h.n; i += kAtOnce * kPackThreads) {
+      float d[kAtOnce];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) d[u] = a.dloss[min(i + u * kPackThreads, a.h.n - 1)];
+      const uint32_t on = take_part(a, i, a.h.n);
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, on >> u & 1 ? fabsf(d[u] * a.scale) : 0.f);
+    }
+#pragma unroll
+    for (int d = kWave / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
+    if (lane() == 0) s_max[threadIdx.x / kWave] = top;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    float m = 1.f, back = 1.f;
+    if (a.narrow) {
+      for (int w = 0; w < kPackThreads / kWave; ++w) top = fmaxf(top, s_max[w]);
+      int ex = 0;
+      if (top > 0.f && top < INFINITY) frexpf(top, &ex);
+      // powers of two that fp32 has on both sides
+      const int s = min(max(14 - ex, -120), 120);
+      m = ldexpf(1.f, s);
+      back = ldexpf(1.f, -s);
+    }
+    a.h.mul[0] = m;
+    a.h.mul[1] = back;
+  }
+}
+
 // Each workgroup counts the tokens before its own that take part (labels are few
 // bytes beside the rows), so one launch does it without waiting for another
-// workgroup. The last workgroup writes the count and the zero rows behind it.
+// workgroup. The last of them writes the count and the zero rows behind it. 16384 x
+// 1024: 25 us, where copying the rows takes 13; the counting is the rest.
 __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
   __shared__ int32_t tmp[17], s_row[kPackThreads];
-  __shared__ float s_max[kPackThreads / kWave];
+  const int32_t groups = gridDim.x - a.back;
+  if ((int32_t)blockIdx.x == groups) {  // backward: one workgroup more
+    put_mul(a);
+    return;
+  }
   const int64_t i0 = (int64_t)blockIdx.x * a.per, i1 = min(a.h.n, i0 + a.per);
   bool bad = false;
   int32_t base = (int32_t)i0;
@@ -211,7 +256,7 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
     base += total;
     __syncthreads();
   }
-  if (blockIdx.x == gridDim.x - 1) {
+  if ((int32_t)blockIdx.x == groups - 1) {
     const int32_t end = (int32_t)cdiv(base, a.pad_to) * a.pad_to, rest = end - base;
     if (threadIdx.x == 0) *a.h.n_live = base;
     for (int32_t r = base + threadIdx.x; r < end; r += kPackThreads) {
@@ -220,43 +265,6 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
     }
     for (int32_t u = threadIdx.x; u < rest * pieces; u += kPackThreads)
       *(u32x4*)(a.h.x + 2 * blocked(base + u / pieces, 8 * (u % pieces), a.h.dp)) = u32x4{0, 0, 0, 0};
-  }
-  if (blockIdx.x == 0 && a.back) {
-    // fp16's exponents end where e's do not: e is rounded times a power of two
-    // that takes the largest coefficient to 2^13 .. 2^14, and the sums lose it again
-    float top = 0.f;
-    if (a.narrow) {
-      if (a.stay) {  // at most a token a thread
-        if (threadIdx.x < a.h.n && takes_part(a, threadIdx.x, &bad))
-          top = fabsf(a.dloss[threadIdx.x] * a.scale);
-      }
-      for (int64_t i = threadIdx.x; !a.stay && i < a.h.n; i += kAtOnce * kPackThreads) {
-        float d[kAtOnce];
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) d[u] = a.dloss[min(i + u * kPackThreads, a.h.n - 1)];
-        const uint32_t on = take_part(a, i, a.h.n);
-#pragma unroll
-        for (int u = 0; u < kAtOnce; ++u) top = fmaxf(top, on >> u & 1 ? fabsf(d[u] * a.scale) : 0.f);
-      }
-#pragma unroll
-      for (int d = kWave / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
-      if (lane() == 0) s_max[threadIdx.x / kWave] = top;
-      __syncthreads();
-    }
-    if (threadIdx.x == 0) {
-      float m = 1.f, back = 1.f;
-      if (a.narrow) {
-        for (int w = 0; w < kPackThreads / kWave; ++w) top = fmaxf(top, s_max[w]);
-        int ex = 0;
-        if (top > 0.f && top < INFINITY) frexpf(top, &ex);
-        // powers of two that fp32 has on both sides
-        const int s = min(max(14 - ex, -120), 120);
-        m = ldexpf(1.f, s);
-        back = ldexpf(1.f, -s);
-      }
-      a.h.mul[0] = m;
-      a.h.mul[1] = back;
-    }
   }
 }
 
@@ -483,9 +491,18 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
   }
 }
 
-// One tile of scores. Columns of the product are table rows, its rows tokens:
-// a lane's registers hold one token's scores, so their maximum and sum need one
-// exchange between two lanes and one between waves.
+// Tiles of scores. Columns of the product are table rows, its rows tokens: a lane's
+// registers hold one token's scores, so their maximum and sum need one exchange
+// between two lanes and one between waves. Workgroups of 256 tokens are as many as
+// CUs and take tiles in turn; the next tile's first loads are asked for before this
+// one's exponentials.
+// Bound by power where rows are long, as the products are: forward, 14746 tokens x
+// 100000 x 1024, 2.45 ms (1230 TFLOP/s, matrix units busy 64%). Backward, 16384 x
+// 32768 x 1024, 1.15 ms (955): of that a fifth is what follows the product, 140 us of
+// it the 1 GiB of e that it writes, 36 the exponentials. Tiles begun half a tile apart
+// on half of the CUs, so that fewer write at once: 1143 against 1134 us, not kept. With
+// rows of 64 (one step a tile) the exponentials bound it: 8778 x 104994 x 64 takes 300
+// us, the products alone 100.
 template <typename T, int BN, int WM, int WN, int Halves>
 __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
   constexpr bool Back = Halves > 0;
@@ -648,7 +665,8 @@ struct Waves {
 };
 
 // dx = e w over a part of the piece's rows, by tokens' places: workgroup `bid` of
-// the product's. lds: two stages.
+// the product's. lds: two stages. 16384 x 32768 x 1024: 860 us (1280 TFLOP/s, matrix
+// units busy 69%: power, see product.hpp), with the fp32 sums that it adds to.
 template <typename T, int DM, int BN, int Halves>
 struct GradX : Waves<DM, BN> {
   using V = Waves<DM, BN>;
@@ -677,7 +695,8 @@ struct GradX : Waves<DM, BN> {
   }
 };
 
-// dw = e^T x over a part of the tokens.
+// dw = e^T x over a part of the tokens. 16384 x 32768 x 1024: 847 us (1300 TFLOP/s,
+// matrix units busy 72%: power).
 template <typename T, int DM, int BV, int Halves>
 struct GradW : Waves<DM, BV> {
   using V = Waves<DM, BV>;
@@ -717,7 +736,9 @@ __global__ void __launch_bounds__((Waves<DM, BV>::kThreads)) k_grad_w(SumArgs a)
   G::run(a, blockIdx.x, gridDim.x, lds);
 }
 // Few tokens: both in one launch, dx's x_grid workgroups first, so that neither
-// waits for the other to leave the chip half empty.
+// waits for the other to leave the chip half empty. Bound by latency: a start, a few
+// steps and a way through LDS (64 tokens, 32000 rows of 64: 9 us; 499 tokens, 10007 of
+// 200: 15.5).
 template <typename T, int DM, int Halves>
 __global__ void __launch_bounds__((Waves<DM, 64>::kThreads)) k_grads(SumArgs x, SumArgs w, int32_t x_grid) {
   using X = GradX<T, DM, 64, Halves>;
@@ -795,7 +816,8 @@ struct LossArgs {
   float *loss, *lse;
 };
 
-// A token's tiles joined: R tokens a workgroup, 256 / R threads each.
+// A token's tiles joined: R tokens a workgroup, 256 / R threads each. 16384 tokens of
+// 391 tiles: 16 us, the 51 MB that the scores left in the caches at 3.2 TB/s.
 template <int R>
 __global__ void __launch_bounds__(256) k_loss(LossArgs a) {
   constexpr int Q = 256 / R;
@@ -915,7 +937,9 @@ struct Teacher {
 };
 
 // Scores of a token's entries, and its loss. A workgroup's waves take the entries
-// in turn, eight of their rows in flight, a row's elements shared by the lanes.
+// in turn, eight of their rows in flight, a row's elements shared by the lanes. 7800
+// tokens of 56 entries on average, rows of 2 KiB: 116 us, 0.9 GB from the caches at 7.7
+// TB/s, which is what bounds it.
 template <typename T>
 __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a) {
   __shared__ int64_t s_id[FS_MAX_TOP];
@@ -959,8 +983,8 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const auto p = Elem<T>::unpack(xv[e]), y = Elem<T>::unpack(wv[u][e]);
-          sum[u] += p[0] * y[0];
-          sum[u] += p[1] * y[1];
+          sum[u] = __builtin_fmaf(p[0], y[0], sum[u]);
+          sum[u] = __builtin_fmaf(p[1], y[1], sum[u]);
         }
     }
 #pragma unroll
@@ -1050,7 +1074,7 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill_entries(Teach
 // ---------------------------------------------------------------- host
 struct Sizes {
   int64_t n, rows, npad, vpad, piece, pack_rows, pack_bytes, e_bytes, dx_part, dw_part, tiles;
-  int32_t dim, dp, bn, halves, dm;  // tiles of bn tokens, gradients' of dm columns
+  int32_t dim, dp, bn, halves, stay, dm;  // tiles of bn tokens, gradients' of dm columns
 };
 
 int64_t most_parts(int64_t steps) { return std::min<int64_t>(kMostParts, std::max<int64_t>(1, steps / 4)); }
@@ -1093,6 +1117,10 @@ Sizes sizes_of(int64_t n, int64_t rows, int32_t dim) {
   // e: all of it, or pieces of kPieceBytes, or of one tile's width
   s.halves = n <= kFew ? 2 : 1;
   const int64_t e_rows = s.npad * s.halves;
+  // Tokens that take no part cost as much as others where all keep their places, so
+  // that is for what takes little time (499 tokens, 10007 rows of 200: two launches of
+  // together 10 us become one of 6)
+  s.stay = n <= kFew || (n <= 1024 && n * rows * dim <= ((int64_t)1 << 32));
   s.e_bytes = e_rows <= kPieceBytes / 2 / s.vpad ? e_rows * s.vpad * 2 : std::max(kPieceBytes, e_rows * kV * 2);
   s.piece = std::min(s.vpad, std::max<int64_t>(kV, s.e_bytes / (e_rows * 2) / kV * kV));
   s.pack_bytes = std::max(std::min(s.vpad * s.dp * 2, kPackBytes), (int64_t)kV * s.dp * 2);
@@ -1175,7 +1203,7 @@ int pack_tokens(PackArgs a, hipStream_t stream) {
   const int64_t per = std::max<int64_t>(16, cdiv(a.h.n, 1024));
   a.per = (int32_t)per;
   const int64_t blocks = std::max<int64_t>(1, cdiv(a.h.n, per));
-  hipLaunchKernelGGL(k_head_pack, dim3((unsigned)blocks), dim3(kPackThreads), 0, stream, a);
+  hipLaunchKernelGGL(k_head_pack, dim3((unsigned)(blocks + a.back)), dim3(kPackThreads), 0, stream, a);
   FS_LAUNCH_CHECK();
   return FS_OK;
 }
@@ -1415,7 +1443,7 @@ PackArgs pack_args(const Space& o, const Sizes& s, const void* x, int64_t x_stri
   p.pad = padding_id;
   p.scale = scale;
   p.pad_to = s.bn;
-  p.stay = s.n <= kFew;
+  p.stay = s.stay;
   p.narrow = dtype == FS_F16;
   p.err = err;
   return p;
