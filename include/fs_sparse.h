@@ -634,8 +634,9 @@ size_t fs_layer_norm_backward_workspace_size(int64_t n, int32_t dim);
 /* t_iv being 1 at the label, or the sum of the q_ik of entries with id v.   */
 /* Tokens that take no part have dx 0 and bring nothing to dweight. Scores,   */
 /* statistics and sums are fp32; e is rounded to x's type (half a step)      */
-/* before the products that sum it, and equal calls give equal bits. In fp16  */
-/* e is rounded times a power of two, which the sums lose again: a step ends  */
+/* before the products that sum it; up to 256 tokens e is two numbers of that */
+/* type, rounded and what that left. Equal calls give equal bits. In fp16 e  */
+/* is rounded times a power of two, which the sums lose again: a step ends   */
 /* only at 2^-37 of the largest |dloss scale|.                              */
 /*  x        device [n][dim] of the table's type, rows x_stride bytes apart   */
 /*           (0: dense).                                                     */

@@ -187,3 +187,50 @@ def test_another_stream():
     torch.cuda.current_stream().wait_stream(side)
     for x, y in zip((*got, *grads), (*want, *wantg)):
         assert torch.equal(x, y)
+
+
+def test_against_differences():
+    """The gradients against differences of the calls' own outputs: along v, whose
+    elements are 0 or 2^-6 in size (both ends exact in fp32), f(t) = sum dout out(x + t
+    v), and (4 D(1) - D(2)) / 3 of its central differences D.
+
+    What the outputs' rounding adds: B = sum |dout| times the forward's bound, at most
+    (4 B + B / 2) / 3. What the differences leave: with f = sum a_k t^k, 4 a_5 + 20 a_7
+    + .. A row's variance as a function of t has its zeros at |t| >= sigma / 2^-6 >= 64
+    where its sigma is 1 or more, so on |t| = 32 the root of it is at least sigma / 2 and
+    |f| <= M = sum |dout w| (|x - mean| + 2 32 2^-6) 2 / sigma; then |a_k| <= M 32^-k, 5 M
+    2^-25 in all."""
+    xs, w, b, dout = _inputs(37, 90)
+    xs = (xs * 256).round() / 256
+    assert xs.std(1).min() >= 1.05
+    g = torch.Generator().manual_seed(9)
+    v = torch.randint(-1, 2, xs.shape, generator=g) / 64.0
+    out, mean, rstd = L.fs_layer_norm(xs.cuda(), w.cuda(), b.cuda())
+    dx, dw, db = L.fs_layer_norm_backward(xs.cuda(), mean, rstd, dout.cuda(), w.cuda())
+
+    def total(x, w, b):
+        y, _, _ = L.fs_layer_norm(x.cuda(), w.cuda(), b.cuda())
+        return float((y.cpu().double() * dout.double()).sum())
+
+    def slope(f):
+        return (4 * (f(1) - f(-1)) / 2 - (f(2) - f(-2)) / 4) / 3
+
+    rounding = sum(float((H.norm(xs + t * v, w, b, 1e-5, F32)["out"][1] * dout.abs()).sum())
+                   for t in (-1, 1, -2, 2)) / 4 * 1.5
+    x64 = xs.double()
+    mid, sigma = x64.mean(1, keepdim=True), x64.std(1, correction=0, keepdim=True)
+    M = float(((dout * w).abs() * ((x64 - mid).abs() + 1) * 2 / sigma).sum())
+    ref = H.norm_backward(xs, mean.cpu(), rstd.cpu(), dout, w, F32, F32)
+    have = float((dx.cpu().double() * v).sum())
+    want = slope(lambda t: total(xs + t * v, w, b))
+    assert abs(have - want) <= rounding + 5 * M * 2 ** -25 + float((ref["dx"][1] * v.abs()).sum())
+    # linear in the parameters: w and b moved by v's first row, exact in fp32
+    w, b = (torch.round(t * 256) / 256 for t in (w, b))
+    dw, db = L.fs_layer_norm_backward(xs.cuda(), mean, rstd, dout.cuda(), w.cuda())[1:]
+    for grad, name, move in ((dw, "dweight", lambda t: total(xs, w + t * v[0], b)),
+                             (db, "dbias", lambda t: total(xs, w, b + t * v[0]))):
+        have = float((grad.cpu().double() * v[0]).sum())
+        rounding = sum(float((H.norm(xs, w + t * v[0], b + t * v[0], 1e-5, F32)["out"][1] * dout.abs()).sum())
+                       for t in (-1, 1, -2, 2)) / 4 * 1.5
+        # the forward's mean and rstd are rounded alike at every t: out's bound holds them
+        assert abs(have - slope(move)) <= rounding + float((ref[name][1] * v[0].abs()).sum())

@@ -82,6 +82,58 @@ def test_wide_tiles(kind, n, rows):
     both(x, w, s, dloss)
 
 
+def _masked_as_clean(kind, n, rows, dim, t):
+    """Both directions held to the plain forms, and the same bits again where the
+    masked tokens' rows, lse and dloss are NaN."""
+    x, w, s, dloss = inputs(kind, n, rows, dim, t, masked=0.4)
+    clean = both(x, w, s, dloss)
+    off = (s["labels"] if kind == "loss" else s["ids"].amax(1)) == -1
+    x[off], dloss[off] = math.nan, math.nan
+    got = forward(x.cuda(), w.cuda(), s)
+    for k in got:
+        assert torch.equal(got[k], clean[0][k]), k
+    got["lse"][off.cuda()] = math.nan
+    dx, dw = backward(x.cuda(), w.cuda(), s, got, dloss)
+    assert torch.equal(dx, clean[1]) and torch.equal(dw, clean[2])
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("n,rows,dim", [(1025, 700, 72), (2500, 300, 264)])
+def test_many_tokens_are_packed_together(kind, t, n, rows, dim):
+    _masked_as_clean(kind, n, rows, dim, t)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("dim", [64, 100, 128, 200, 320])
+def test_wide_tiles_of_every_width(kind, t, dim):
+    """256 tokens by 256 rows a tile, some rows of zeros in a tile's end."""
+    _masked_as_clean(kind, 1100, 27_000, dim, t)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("rows", [500, 27_000])
+def test_of_many_tokens_none_takes_part(kind, rows):
+    x, w, s, dloss = inputs(kind, 1100, rows, 64, masked=2.0)
+    x[:] = math.nan
+    got = forward(x.cuda(), w.cuda(), s)
+    for y in got.values():
+        assert not y.any()
+    dx, dw = backward(x.cuda(), w.cuda(), s, got, dloss)
+    assert not dx.any() and not dw.any()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_one_token_of_many_takes_part(kind):
+    x, w, s, dloss = inputs(kind, 1300, 400, 96, masked=0.0)
+    key = "labels" if kind == "loss" else "ids"
+    keep = s[key][1234].clone()
+    s[key][:] = -1
+    s[key][1234] = keep
+    both(x, w, s, dloss)
+
+
 @pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("scale", [-1.0, 0.0, 0.3, 4.0])
 def test_scales(kind, scale):
