@@ -209,11 +209,21 @@ __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
     if (a.stay && !a.labels) {  // the threads share the tokens' entries
       s_row[threadIdx.x] = 0;
       __syncthreads();
-      const int32_t top = a.entries.top;
-      for (int32_t u = threadIdx.x; u < total * top; u += kPackThreads) {
-        const int64_t id = a.entries.ids[c * top + u];
-        bad |= a.entries.bad(id);
-        if (a.entries.on(id, a.entries.logit(c * top + u))) s_row[u / top] = 1;
+      const int32_t top = a.entries.top, all = total * top;
+      for (int32_t u0 = threadIdx.x; u0 < all; u0 += 4 * kPackThreads) {  // four in flight
+        int64_t id[4];
+        float t[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const int64_t at = c * top + min(u0 + y * kPackThreads, all - 1);
+          id[y] = a.entries.ids[at];
+          t[y] = a.entries.logit(at);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {  // past the last one: it again
+          bad |= a.entries.bad(id[y]);
+          if (a.entries.on(id[y], t[y])) s_row[min(u0 + y * kPackThreads, all - 1) / top] = 1;
+        }
       }
       __syncthreads();
       on = i < i1 && s_row[threadIdx.x];
@@ -936,41 +946,53 @@ struct Teacher {
   }
 };
 
-// Scores of a token's entries, and its loss. A workgroup's waves take the entries
-// in turn, eight of their rows in flight, a row's elements shared by the lanes. 7800
-// tokens of 56 entries on average, rows of 2 KiB: 116 us, 0.9 GB from the caches at 7.7
-// TB/s, which is what bounds it.
-template <typename T>
+// What one wave wrote to LDS before what it reads behind
+__device__ __forceinline__ void wave_lds() {
+  __builtin_amdgcn_wave_barrier();
+  __threadfence_block();
+}
+
+// Scores of a token's entries, and its loss. W waves have a token: 4 where tokens are
+// few, which join its tiles as well, 1 where they are many. They take the entries in
+// turn; LP lanes share a row's elements, so narrow rows go several to an access, and
+// 8 accesses are in flight. Bound by the latency of a token's few dependent reads, so by
+// how many tokens are under way: 5135 tokens of 56 entries, rows of 32, 51 us with 4
+// waves of whole rows, 11 like this; 10813 x 5, rows of 440, 30 and 13; 8192 x 64, rows
+// of 1024, the whole call 569 and 520.
+template <typename T, int LP, int W>
 __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a) {
-  __shared__ int64_t s_id[FS_MAX_TOP];
-  __shared__ float s_z[FS_MAX_TOP];
-  const int w = attn::wave_id(), l = lane();
-  const int64_t i = blockIdx.x;
+  constexpr int kTokens = kRowsPerGroup / W, kRows = 8, kGroups = kWave / LP;
+  __shared__ int32_t s_id[kRowsPerGroup][FS_MAX_TOP];
+  __shared__ float s_z[kTokens][FS_MAX_TOP];
+  const int wave = attn::wave_id(), w = wave % W, l = lane();
+  const int64_t i = (int64_t)blockIdx.x * kTokens + wave / W;
+  if (W == 1 && i >= a.h.n) return;
+  float* const z_of = s_z[wave / W];
   const int32_t pos = a.h.pos[i];
-  if (pos < 0) {
-    for (int k = threadIdx.x; k < a.in.top; k += kRowsPerGroup * kWave) a.logits[i * a.in.top + k] = 0.f;
-    if (threadIdx.x == 0) {
+  const int32_t top = a.in.top;
+  if (pos < 0) {  // uniform where waves share a token
+    for (int k = w * kWave + l; k < top; k += W * kWave) a.logits[i * top + k] = 0.f;
+    if (w == 0 && l == 0) {
       a.loss[i] = 0.f;
-      if (a.part) a.lse[i] = 0.f;
+      if (W > 1) a.lse[i] = 0.f;
     }
     return;
   }
-  for (int k = threadIdx.x; k < a.in.top; k += kRowsPerGroup * kWave) {
-    const int64_t id = a.in.ids[i * a.in.top + k];
-    s_id[k] = a.in.on(id, a.in.logit(i * a.in.top + k)) ? id : -1;
-  }
-  __syncthreads();
-  constexpr int kRows = 8;
-  for (int k0 = w; k0 < a.in.top; k0 += kRows * kRowsPerGroup) {  // uniform in a wave
-    int64_t id[kRows];
+  const Teacher t(a, i);
+#pragma unroll
+  for (int u = 0; u < kPerLane; ++u) s_id[wave][l + kWave * u] = t.on[u] ? (int32_t)t.id[u] : -1;
+  wave_lds();
+  const int g = l / LP, c0 = 8 * (l % LP);
+  for (int k0 = w * kGroups; k0 < top; k0 += kRows * W * kGroups) {  // uniform in a wave
+    int32_t id[kRows];
     float sum[kRows];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const int k = k0 + u * kRowsPerGroup;
-      id[u] = k < a.in.top ? s_id[k] : -1;
+      const int k = k0 + u * W * kGroups + g;
+      id[u] = k < top ? s_id[wave][k] : -1;
       sum[u] = 0.f;
     }
-    for (int c = 8 * l; c < a.h.dim; c += 8 * kWave) {
+    for (int c = c0; c < a.h.dim; c += 8 * LP) {
       const u32x4 xv = *(const u32x4*)(a.h.x + 2 * blocked(pos, c, a.h.dp));
       u32x4 wv[kRows];
 #pragma unroll
@@ -989,48 +1011,49 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
     }
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
-      const float z = wave_sum(sum[u]) * a.scale;
-      const int k = k0 + u * kRowsPerGroup;
-      if (l == 0 && k < a.in.top) s_z[k] = id[u] >= 0 ? z : 0.f;
+      float z = sum[u];
+#pragma unroll
+      for (int d = LP / 2; d > 0; d >>= 1) z += __shfl_xor(z, d, kWave);
+      const int k = k0 + u * W * kGroups + g;
+      if (l % LP == 0 && k < top) z_of[k] = id[u] >= 0 ? z * a.scale : 0.f;
     }
   }
-  __shared__ float2 s_part[kRowsPerGroup];
-  if (a.part) {
-    float top = -3e38f, sum = 0.f;
-    for (int64_t q = threadIdx.x; q < a.tiles; q += kRowsPerGroup * kWave) {
+  float lse;
+  if constexpr (W > 1) {
+    __shared__ float2 s_part[W];
+    float top2 = -3e38f, sum = 0.f;
+    for (int64_t q = threadIdx.x; q < a.tiles; q += W * kWave) {
       const float2 x = a.part[q * a.h.npad + pos];
-      const float m = fmaxf(x.x, top);
-      sum = sum * __builtin_amdgcn_exp2f(top - m) + x.y * __builtin_amdgcn_exp2f(x.x - m);
-      top = m;
+      const float m = fmaxf(x.x, top2);
+      sum = sum * __builtin_amdgcn_exp2f(top2 - m) + x.y * __builtin_amdgcn_exp2f(x.x - m);
+      top2 = m;
     }
-    float m = top;
+    float m = top2;
 #pragma unroll
     for (int d = kWave / 2; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor(m, d, kWave));
-    sum = wave_sum(sum * __builtin_amdgcn_exp2f(top - m));
+    sum = wave_sum(sum * __builtin_amdgcn_exp2f(top2 - m));
     if (l == 0) s_part[w] = make_float2(m, sum);
-  }
-  __syncthreads();
-  if (w) return;
-  const Teacher t(a, i);
-  float lse;
-  if (a.part) {
-    float m = s_part[0].x, sum = 0.f;
+    __syncthreads();
+    if (w) return;
+    m = s_part[0].x;
+    sum = 0.f;
 #pragma unroll
-    for (int q = 1; q < kRowsPerGroup; ++q) m = fmaxf(m, s_part[q].x);
+    for (int q = 1; q < W; ++q) m = fmaxf(m, s_part[q].x);
 #pragma unroll
-    for (int q = 0; q < kRowsPerGroup; ++q) sum += s_part[q].y * __builtin_amdgcn_exp2f(s_part[q].x - m);
+    for (int q = 0; q < W; ++q) sum += s_part[q].y * __builtin_amdgcn_exp2f(s_part[q].x - m);
     lse = (m + __builtin_amdgcn_logf(sum)) * kLn2;
     if (l == 0) a.lse[i] = lse;
   } else {
+    wave_lds();
     lse = a.lse[i];
   }
   float loss = 0.f;
 #pragma unroll
   for (int u = 0; u < kPerLane; ++u) {
     const int k = l + kWave * u;
-    if (k < a.in.top) {
-      const float z = s_z[k];
-      a.logits[i * a.in.top + k] = z;
+    if (k < top) {
+      const float z = z_of[k];
+      a.logits[i * top + k] = z;
       if (t.on[u] && t.q[u] != 0.f) loss += t.q[u] * (t.logq[u] - z + lse);
     }
   }
@@ -1038,12 +1061,20 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
   if (l == 0) a.loss[i] = loss;
 }
 
+template <typename T, int W>
+void launch_distill(const TeacherArgs& a, hipStream_t stream) {
+  const dim3 grid((unsigned)cdiv(a.h.n, kRowsPerGroup / W)), block(kRowsPerGroup * kWave);
+  if (a.h.dim <= 64) hipLaunchKernelGGL((k_distill<T, 8, W>), grid, block, 0, stream, a);
+  else if (a.h.dim <= 128) hipLaunchKernelGGL((k_distill<T, 16, W>), grid, block, 0, stream, a);
+  else if (a.h.dim <= 256) hipLaunchKernelGGL((k_distill<T, 32, W>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((k_distill<T, 64, W>), grid, block, 0, stream, a);
+}
+
 // The entries' places of e in a piece: target off the softmax before the one
 // rounding. Entries of one id write the same value.
 template <typename T>
 __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill_entries(TeacherArgs a) {
-  __shared__ int64_t s_id[kRowsPerGroup][FS_MAX_TOP];
-  __shared__ float s_q[kRowsPerGroup][FS_MAX_TOP];
+  __shared__ uint2 s_own[kRowsPerGroup][FS_MAX_TOP];  // id and q
   const int w = threadIdx.x / kWave, l = lane();
   const int64_t i = (int64_t)blockIdx.x * kRowsPerGroup + w;
   if (i >= a.h.n) return;
@@ -1051,21 +1082,23 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill_entries(Teach
   if (pos < 0) return;
   const Teacher t(a, i);
 #pragma unroll
-  for (int u = 0; u < kPerLane; ++u) {
-    s_id[w][l + kWave * u] = t.on[u] ? t.id[u] : -1;
-    s_q[w][l + kWave * u] = t.q[u];
-  }
-  __builtin_amdgcn_wave_barrier();
-  __threadfence_block();
+  for (int u = 0; u < kPerLane; ++u)
+    s_own[w][l + kWave * u] = make_uint2(t.on[u] ? (uint32_t)t.id[u] : ~0u, __float_as_uint(t.q[u]));
+  wave_lds();
   const float c = a.h.coef[pos] * a.h.mul[0], lse2 = a.h.lse2[pos];
+  float q[kPerLane] = {};
+#pragma unroll 8
+  for (int k = 0; k < a.in.top; ++k) {  // the q of each id's entries, in order (84 x 124: 16 us one by one, 9)
+    const uint2 own = s_own[w][k];
+#pragma unroll
+    for (int u = 0; u < kPerLane; ++u) q[u] += own.x == (uint32_t)t.id[u] ? __uint_as_float(own.y) : 0.f;
+  }
 #pragma unroll
   for (int u = 0; u < kPerLane; ++u) {
     const int64_t v = t.id[u] - a.v0;
     if (!t.on[u] || v < 0 || v >= a.piece_rows) continue;
-    float q = 0.f;
-    for (int k = 0; k < a.in.top; ++k) q += s_id[w][k] == t.id[u] ? s_q[w][k] : 0.f;
     const float z = a.logits_in[i * a.in.top + l + kWave * u];
-    const float e = (__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -lse2)) - q) * c;
+    const float e = (__builtin_amdgcn_exp2f(__builtin_fmaf(z, kLog2e, -lse2)) - q[u]) * c;
     ((T*)a.e)[place_of_e(pos, v, a.e_cols, 0, a.halves)] = (T)e;
     if (a.halves > 1) ((T*)a.e)[place_of_e(pos, v, a.e_cols, 1, 2)] = (T)(e - (float)(T)e);
   }
@@ -1563,9 +1596,9 @@ extern "C" int fs_token_distill(const void* x, int64_t x_stride, int64_t n, cons
   a.lse = lse;
   a.part = n < kFewRows ? o.part : nullptr;
   a.tiles = s.tiles;
-  const dim3 grid((unsigned)n), block(kRowsPerGroup * kWave);
-  if (table->dtype == FS_BF16) hipLaunchKernelGGL(k_distill<__bf16>, grid, block, 0, stream, a);
-  else hipLaunchKernelGGL(k_distill<_Float16>, grid, block, 0, stream, a);
+  const bool few = n < kFewRows;
+  if (table->dtype == FS_BF16) few ? launch_distill<__bf16, 4>(a, stream) : launch_distill<__bf16, 1>(a, stream);
+  else few ? launch_distill<_Float16, 4>(a, stream) : launch_distill<_Float16, 1>(a, stream);
   FS_LAUNCH_CHECK();
   return FS_OK;
 }
