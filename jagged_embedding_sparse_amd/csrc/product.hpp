@@ -257,7 +257,8 @@ struct BlockCols {
 // (Turns: 64 k's are so many steps, with another part of one operand each.)
 // WM x WN waves, each of MI x NI blocks of 32 x 32. Register i of a lane's block
 // (mi, ni) is column m = m_of(mi) + 8 (i / 4) + i % 4 of row n = n_of(ni).
-template <typename T, typename A, typename B, int BM, int BN, int WM, int WN, int Turns = 1>
+// Stages: tiles of so many steps fit LDS, so the loads of all but one are in flight.
+template <typename T, typename A, typename B, int BM, int BN, int WM, int WN, int Turns = 1, int Stages = 2>
 struct Tile {
   static constexpr int kThreads = WM * WN * kWave;
   static constexpr int MI = BM / WM / 32, NI = BN / WN / 32;
@@ -294,15 +295,16 @@ struct Tile {
   }
 
   // Asks for the first 64 of `k` k's, from where a and b stand. The first stage
-  // must be free; run() may follow after other work that leaves it alone.
+  // must be free; run() may follow after other work that leaves it alone (with more
+  // than two stages that work has stored nothing: loads are counted, stores are not).
   template <bool LimA, bool LimB>
   static __device__ __forceinline__ void ask(A& a, B& b, int64_t k, uint16_t* lds) {
     if (k > 0) ask_step<LimA, LimB>(a, b, k, 0, lds_address(lds));
   }
 
   // Adds the product over `k` k's in steps of 64, behind ask(); in the last step the
-  // operands are told how many are left where Lim says so. lds: 2 kStage elements.
-  // The stages are free again when it returns, the second one before it begins.
+  // operands are told how many are left where Lim says so. lds: Stages kStage
+  // elements. They are free again when it returns, all but the first before it begins.
   //
   // Products, reads and loads are issued in this order and no other (left to
   // itself the compiler reads a chunk's operands right before its products and
@@ -314,17 +316,24 @@ struct Tile {
     const uint32_t lds0 = lds_address(lds);
     const int steps = (int)cdiv(k, (int64_t)kK) * Turns;
     if (steps <= 0) return;
-    landed();
-    if (steps > 1) ask_step<LimA, LimB>(a, b, k, 1, lds0 + kStage * 2);
+    if constexpr (Stages == 2) landed();
+#pragma unroll
+    for (int t = 1; t < Stages; ++t)
+      if (t < steps) ask_step<LimA, LimB>(a, b, k, t, lds0 + t * (kStage * 2));
+    if constexpr (Stages > 2) {
+      if (steps >= Stages) landed<(Stages - 1) * kLoads>();
+      else landed();
+    }
     Operands o[2];
 #pragma unroll
     for (int x = 0; x < kOperands; ++x) read(o[0], ra, rb, lds, 0, x);
     constexpr int kMost = kProducts > kOperands ? kProducts : kOperands;
-    // one step on stage `buf`; the other one holds the next step's tiles
+    // one step on stage `buf`; the one behind it holds the next step's tiles
     int buf = 0;
     auto step = [&](auto more) {
       const uint16_t* here = lds + buf * kStage;
-      const uint16_t* next = lds + (buf ^ 1) * kStage;
+      const int then = Stages == 2 ? buf ^ 1 : buf + 1 < Stages ? buf + 1 : 0;
+      const uint16_t* next = lds + then * kStage;
 #pragma unroll
       for (int kk = 0; kk < 3; ++kk)
 #pragma unroll
@@ -333,8 +342,9 @@ struct Tile {
           if (x < kProducts) multiply(o[kk & 1], x);
           __builtin_amdgcn_sched_barrier(0);
         }
-      // the last chunk's operands are here, so this stage may be written again
-      landed();
+      // the last chunk's operands are here, so this stage may be written again; of the
+      // loads, those of the next step are
+      landed<decltype(more)::value ? (Stages - 2) * kLoads : 0>();
 #pragma unroll
       for (int x = 0; x < kLoads || x < kMost; ++x) {
         if (x < kOperands) read(o[0], ra, rb, next, 0, x);  // behind the last step: of no use
@@ -346,11 +356,11 @@ struct Tile {
         a.advance();
         b.advance();
       }
-      buf ^= 1;
+      buf = then;
     };
     int t = 0;
-    for (; t + 2 < steps; ++t) {
-      limit<LimA, LimB>(a, b, k, t + 2);
+    for (; t + Stages < steps; ++t) {
+      limit<LimA, LimB>(a, b, k, t + Stages);
       step(std::true_type());
     }
     for (; t < steps; ++t) step(std::false_type());
@@ -381,9 +391,12 @@ struct Tile {
     b.advance();
   }
 
-  // every wave's loads have landed and every wave's reads of LDS are done
+  // every wave's loads but its last `Flying` have landed (loads land in order) and
+  // every wave's reads of LDS are done
+  template <int Flying = 0>
   static __device__ __forceinline__ void landed() {
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
+    static_assert(Flying < 64, "what the counter holds");
+    asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)" ::"i"(Flying) : "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
   }

@@ -513,12 +513,12 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
 // on half of the CUs, so that fewer write at once: 1143 against 1134 us, not kept. With
 // rows of 64 (one step a tile) the exponentials bound it: 8778 x 104994 x 64 takes 300
 // us, the products alone 100.
-template <typename T, int BN, int WM, int WN, int Halves>
+template <typename T, int BN, int WM, int WN, int Halves, int Stages>
 __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
   constexpr bool Back = Halves > 0;
   constexpr int NT = WM * WN * kWave;
-  using P = Tile<T, Rows<kV, NT>, BlockRows<BN, NT>, kV, BN, WM, WN>;
-  __shared__ __attribute__((aligned(16))) uint16_t lds[2 * P::kStage];
+  using P = Tile<T, Rows<kV, NT>, BlockRows<BN, NT>, kV, BN, WM, WN, 1, Stages>;
+  __shared__ __attribute__((aligned(16))) uint16_t lds[Stages * P::kStage];
   uint16_t* const second = lds + P::kStage;
   const int32_t live = *a.h.n_live;
   // tiles of tokens that take part, dealt to all XCDs alike
@@ -531,7 +531,12 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
   BlockRows<BN, NT> x(a.h.x, a.h.dp, (int64_t)tn * BN, 0);
   // tiles of 64 tokens are one to a workgroup, and LDS holds two such
   constexpr bool kMany = BN == 256;
-  __shared__ float info[kMany ? 2 : 1][kMany ? (Back ? 3 : 1) : 1][kMany ? BN : 1];
+  static_assert(Stages == 2 || !kMany, "a workgroup with more stages has one tile");
+  float(*info)[Back ? 3 : 1][BN] = nullptr;
+  if constexpr (kMany) {
+    __shared__ float two[2][Back ? 3 : 1][BN];
+    info = two;
+  }
   if constexpr (kMany) ask_info<BN, WM * WN, Back>(a.h, (int64_t)tn * BN, info[0]);
   const float mul = Back ? __uint_as_float(__builtin_amdgcn_readfirstlane(__float_as_uint(a.h.mul[0]))) : 1.f;
   P::template ask<true, false>(w, x, a.k, lds);
@@ -1246,12 +1251,17 @@ template <typename T, int Halves>
 void launch_scores(const ScoreArgs& a, const Sizes& s, int64_t tiles, hipStream_t stream) {
   if constexpr (Halves < 2) {
     if (s.bn == 256) {
-      hipLaunchKernelGGL((k_scores<T, 256, kWM, kWN, Halves>), dim3((unsigned)std::min<int64_t>(tiles, kCus)),
+      hipLaunchKernelGGL((k_scores<T, 256, kWM, kWN, Halves, 2>), dim3((unsigned)std::min<int64_t>(tiles, kCus)),
                          dim3(kWM * kWN * kWave), 0, stream, a);
       return;
     }
   }
-  hipLaunchKernelGGL((k_scores<T, 64, 8, 1, Halves>), dim3((unsigned)tiles), dim3(8 * kWave), 0, stream, a);
+  const dim3 grid((unsigned)tiles), block(8 * kWave);
+  // No more tiles than CUs: LDS of a whole CU, three steps' loads in flight instead of
+  // one (162 tokens, 1474 rows of 1472: 19.8 -> 16.7 us; 2 tokens, 48218 of 1176: 22.8 ->
+  // 19.9; rows of 512 and 192 gain nothing)
+  if (tiles <= kCus && a.k > 8 * kK) hipLaunchKernelGGL((k_scores<T, 64, 8, 1, Halves, 4>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((k_scores<T, 64, 8, 1, Halves, 2>), grid, block, 0, stream, a);
 }
 template <int Halves>
 int launch_scores(const ScoreArgs& a, const Sizes& s, int32_t dtype, hipStream_t stream) {

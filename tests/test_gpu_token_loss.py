@@ -135,6 +135,13 @@ def test_one_token_of_many_takes_part(kind):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("dim", [128, 200, 260, 384, 512, 513, 520, 576, 584, 640, 712, 2048])
+def test_few_tokens_of_long_rows(kind, dim):
+    """Few tiles, of 2 to 32 steps."""
+    both(*inputs(kind, 70, 900, dim))
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("scale", [-1.0, 0.0, 0.3, 4.0])
 def test_scales(kind, scale):
     x, w, s, dloss = inputs(kind, 90, 700, 64)
