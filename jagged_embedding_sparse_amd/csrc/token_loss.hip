@@ -300,6 +300,10 @@ struct ScoreArgs {
   int32_t v_tile0;   // forward: tiles of the pieces before
   Order order;
   float scale2;      // scale log2(e)
+  const char* x;     // forward of few tokens: their rows as they lie, with
+  int64_t x_stride;
+  const int64_t* labels;  // (null: none)
+  int64_t all_rows, pad;
   float2* part;      // forward: [tiles of the table][npad] maximum and sum, base 2
   float* at_label;   // forward: [npad] the label's score, base 2
   // backward: [npad][e_cols] 16 bits in blocks. Up to kFew tokens e is two numbers,
@@ -310,6 +314,11 @@ struct ScoreArgs {
   int64_t e_cols;
   int32_t past;      // e outgrows the caches
 };
+
+// a label's row, or -1 where its token takes no part
+__device__ __forceinline__ int32_t label_of(int64_t v, int64_t rows, int64_t pad) {
+  return v >= 0 && v < rows && v != pad ? (int32_t)v : -1;
+}
 
 // element (token, row) of a half of e
 __device__ __forceinline__ int64_t place_of_e(int64_t n, int64_t v, int64_t cols, int half, int halves) {
@@ -513,14 +522,19 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
 // on half of the CUs, so that fewer write at once: 1143 against 1134 us, not kept. With
 // rows of 64 (one step a tile) the exponentials bound it: 8778 x 104994 x 64 takes 300
 // us, the products alone 100.
-template <typename T, int BN, int WM, int WN, int Halves, int Stages>
+template <typename T, int BN, int WM, int WN, int Halves, int Stages, bool Direct>
 __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
   constexpr bool Back = Halves > 0;
   constexpr int NT = WM * WN * kWave;
-  using P = Tile<T, Rows<kV, NT>, BlockRows<BN, NT>, kV, BN, WM, WN, 1, Stages>;
+  using X = std::conditional_t<Direct, Rows<BN, NT>, BlockRows<BN, NT>>;
+  using P = Tile<T, Rows<kV, NT>, X, kV, BN, WM, WN, 1, Stages>;
+  auto tokens = [&](int32_t tn) {
+    if constexpr (Direct) return X(a.x, a.x_stride, (int64_t)tn * BN, a.h.n, 0);
+    else return X(a.h.x, a.h.dp, (int64_t)tn * BN, 0);
+  };
   __shared__ __attribute__((aligned(16))) uint16_t lds[Stages * P::kStage];
   uint16_t* const second = lds + P::kStage;
-  const int32_t live = *a.h.n_live;
+  const int32_t live = Direct ? (int32_t)a.h.n : *a.h.n_live;
   // tiles of tokens that take part, dealt to all XCDs alike
   const Order order{(int32_t)cdiv(live, BN), a.order.cols};
   const int32_t tiles = order.rows * order.cols;
@@ -528,7 +542,7 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
   int32_t tn, tv;
   order.at(in_order(blockIdx.x, tiles), kGroup, &tn, &tv);
   Rows<kV, NT> w(a.w, a.w_stride, (int64_t)tv * kV, a.rows, 0);
-  BlockRows<BN, NT> x(a.h.x, a.h.dp, (int64_t)tn * BN, 0);
+  X x = tokens(tn);
   // tiles of 64 tokens are one to a workgroup, and LDS holds two such
   constexpr bool kMany = BN == 256;
   static_assert(Stages == 2 || !kMany, "a workgroup with more stages has one tile");
@@ -550,9 +564,11 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
     } else {
 #pragma unroll
       for (int j = 0; j < P::NI; ++j) {
-        its.labels[j] = a.h.label[n0 + P::n_of(j)];
-        its.lse2s[j] = Back ? a.h.lse2[n0 + P::n_of(j)] : 0.f;
-        its.coefs[j] = Back ? a.h.coef[n0 + P::n_of(j)] : 0.f;
+        const int64_t n = n0 + P::n_of(j);
+        if constexpr (Direct) its.labels[j] = a.labels && n < a.h.n ? label_of(a.labels[n], a.all_rows, a.pad) : -1;
+        else its.labels[j] = a.h.label[n];
+        its.lse2s[j] = Back ? a.h.lse2[n] : 0.f;
+        its.coefs[j] = Back ? a.h.coef[n] : 0.f;
       }
     }
     P p;
@@ -561,7 +577,7 @@ __global__ void __launch_bounds__(WM * WN * kWave) k_scores(ScoreArgs a) {
     if (id + (int32_t)gridDim.x < tiles) {  // the next tile's first loads, behind this one's scores
       order.at(in_order(id + gridDim.x, tiles), kGroup, &tn, &tv);
       w = Rows<kV, NT>(a.w, a.w_stride, (int64_t)tv * kV, a.rows, 0);
-      x = BlockRows<BN, NT>(a.h.x, a.h.dp, (int64_t)tn * BN, 0);
+      x = tokens(tn);
       if constexpr (kMany) ask_info<BN, WM * WN, Back>(a.h, (int64_t)tn * BN, info[turn ^ 1]);
       P::template ask<true, false>(w, x, a.k, lds);
     }
@@ -829,6 +845,9 @@ struct LossArgs {
   int64_t tiles;
   const float* at_label;  // null: no loss here
   float *loss, *lse;
+  const int64_t* labels;  // of tokens that were read as they lie, or null
+  int64_t rows, pad;
+  int32_t* err;
 };
 
 // A token's tiles joined: R tokens a workgroup, 256 / R threads each. 16384 tokens of
@@ -839,7 +858,14 @@ __global__ void __launch_bounds__(256) k_loss(LossArgs a) {
   __shared__ float2 sh[Q][R];
   const int r = threadIdx.x % R, q = threadIdx.x / R;
   const int64_t i = (int64_t)blockIdx.x * R + r;
-  const int32_t pos = i < a.h.n ? a.h.pos[i] : -1;
+  int32_t pos = -1;
+  if (i < a.h.n && a.labels) {
+    const int64_t v = a.labels[i];
+    if (label_of(v, a.rows, a.pad) >= 0) pos = (int32_t)i;
+    flag_err(a.err, q == 0 && pos < 0 && v != a.pad, FS_EF_ID_RANGE);
+  } else if (i < a.h.n) {
+    pos = a.h.pos[i];
+  }
   float top = -3e38f, sum = 0.f;
   if (pos >= 0) {
     int64_t t = q;
@@ -883,6 +909,8 @@ struct TeacherArgs {
   // forward
   const char* w;
   int64_t w_stride;
+  const char* x;  // tokens as they lie, or null
+  int64_t x_stride;
   float *loss, *logits, *lse;
   const float2* part;  // null: lse is there, else it is made of these tiles
   int64_t tiles;
@@ -973,8 +1001,21 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
   const int64_t i = (int64_t)blockIdx.x * kTokens + wave / W;
   if (W == 1 && i >= a.h.n) return;
   float* const z_of = s_z[wave / W];
-  const int32_t pos = a.h.pos[i];
   const int32_t top = a.in.top;
+  const Teacher t(a, i);
+  int32_t pos;
+  if (a.x) {
+    bool on = false, bad = false;
+#pragma unroll
+    for (int u = 0; u < kPerLane; ++u) {
+      on |= t.on[u];
+      bad |= l + kWave * u < top && a.in.bad(t.id[u]);
+    }
+    flag_err(a.err, w == 0 && bad, FS_EF_ID_RANGE);
+    pos = __any(on) ? (int32_t)i : -1;
+  } else {
+    pos = a.h.pos[i];
+  }
   if (pos < 0) {  // uniform where waves share a token
     for (int k = w * kWave + l; k < top; k += W * kWave) a.logits[i * top + k] = 0.f;
     if (w == 0 && l == 0) {
@@ -983,7 +1024,6 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
     }
     return;
   }
-  const Teacher t(a, i);
 #pragma unroll
   for (int u = 0; u < kPerLane; ++u) s_id[wave][l + kWave * u] = t.on[u] ? (int32_t)t.id[u] : -1;
   wave_lds();
@@ -998,7 +1038,7 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a
       sum[u] = 0.f;
     }
     for (int c = c0; c < a.h.dim; c += 8 * LP) {
-      const u32x4 xv = *(const u32x4*)(a.h.x + 2 * blocked(pos, c, a.h.dp));
+      const u32x4 xv = *(const u32x4*)(a.x ? a.x + i * a.x_stride + 2 * c : a.h.x + 2 * blocked(pos, c, a.h.dp));
       u32x4 wv[kRows];
 #pragma unroll
       for (int u = 0; u < kRows; ++u) {
@@ -1251,7 +1291,7 @@ template <typename T, int Halves>
 void launch_scores(const ScoreArgs& a, const Sizes& s, int64_t tiles, hipStream_t stream) {
   if constexpr (Halves < 2) {
     if (s.bn == 256) {
-      hipLaunchKernelGGL((k_scores<T, 256, kWM, kWN, Halves, 2>), dim3((unsigned)std::min<int64_t>(tiles, kCus)),
+      hipLaunchKernelGGL((k_scores<T, 256, kWM, kWN, Halves, 2, false>), dim3((unsigned)std::min<int64_t>(tiles, kCus)),
                          dim3(kWM * kWN * kWave), 0, stream, a);
       return;
     }
@@ -1260,8 +1300,16 @@ void launch_scores(const ScoreArgs& a, const Sizes& s, int64_t tiles, hipStream_
   // No more tiles than CUs: LDS of a whole CU, three steps' loads in flight instead of
   // one (162 tokens, 1474 rows of 1472: 19.8 -> 16.7 us; 2 tokens, 48218 of 1176: 22.8 ->
   // 19.9; rows of 512 and 192 gain nothing)
-  if (tiles <= kCus && a.k > 8 * kK) hipLaunchKernelGGL((k_scores<T, 64, 8, 1, Halves, 4>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((k_scores<T, 64, 8, 1, Halves, 2>), grid, block, 0, stream, a);
+  const bool deep = tiles <= kCus && a.k > 8 * kK;
+  auto go = [&](auto direct) {
+    constexpr bool D = decltype(direct)::value;
+    if (deep) hipLaunchKernelGGL((k_scores<T, 64, 8, 1, Halves, 4, D>), grid, block, 0, stream, a);
+    else hipLaunchKernelGGL((k_scores<T, 64, 8, 1, Halves, 2, D>), grid, block, 0, stream, a);
+  };
+  if constexpr (Halves == 0) {
+    if (a.x) return go(std::true_type());
+  }
+  go(std::false_type());
 }
 template <int Halves>
 int launch_scores(const ScoreArgs& a, const Sizes& s, int32_t dtype, hipStream_t stream) {
@@ -1340,8 +1388,22 @@ int check(const void* x, int64_t* x_stride, int64_t n, const fs_table* table, fl
 // lse (and the losses of labels) of the packed tokens
 constexpr int64_t kFewRows = 2048;
 
-int forward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float scale, bool labels,
-            float* loss, float* lse, hipStream_t stream) {
+// Tokens of a forward call that the tiles can read as they lie.
+struct Tokens {
+  const char* x;  // null: packed
+  int64_t stride;
+};
+
+// Few tokens' rows of whole steps need no packing: what a token's row holds reaches no
+// other's score (17 tokens, 100000 rows of 256: 20.3 -> 17.5 us).
+Tokens as_they_lie(const void* x, int64_t stride, const Sizes& s) {
+  const bool can = s.stay && s.bn == 64 && s.dim % kK == 0 && loads_directly((const char*)x, stride, s.dim);
+  return can ? Tokens{(const char*)x, stride} : Tokens{};
+}
+
+int forward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float scale, const Tokens& x,
+            const int64_t* labels, int64_t padding_id, int32_t* err, float* loss, float* lse,
+            hipStream_t stream) {
   int rc;
   const int64_t step = t.direct ? s.vpad : s.pack_rows;
   for (int64_t v0 = 0; v0 < s.rows; v0 += step) {
@@ -1353,6 +1415,11 @@ int forward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float
     if ((rc = piece_of(t, s, v0, a.rows, o.pack, &a.w, &a.w_stride, &a.k, stream))) return rc;
     a.order = Order{(int32_t)cdiv(s.n, s.bn), (int32_t)cdiv(a.rows, kV)};
     a.scale2 = scale * kLog2e;
+    a.x = x.x;
+    a.x_stride = x.stride;
+    a.labels = labels;
+    a.all_rows = s.rows;
+    a.pad = padding_id;
     a.part = o.part;
     a.at_label = o.at_label;
     if ((rc = launch_scores<0>(a, s, dtype, stream))) return rc;
@@ -1360,7 +1427,8 @@ int forward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float
   // few tokens' tiles are joined where their entries are (a launch of 4 us less; of
   // many tokens a token's tiles lie too far apart for that)
   if (!labels && s.n < kFewRows) return FS_OK;
-  const LossArgs l{o.h, o.part, s.tiles, labels ? o.at_label : nullptr, loss, lse};
+  const LossArgs l{o.h, o.part, s.tiles, labels ? o.at_label : nullptr, loss, lse, x.x ? labels : nullptr,
+                   s.rows, padding_id, err};
   if (s.n < kFewRows) hipLaunchKernelGGL(k_loss<4>, dim3((unsigned)cdiv(s.n, 4)), dim3(256), 0, stream, l);
   else hipLaunchKernelGGL(k_loss<16>, dim3((unsigned)cdiv(s.n, 16)), dim3(256), 0, stream, l);
   FS_LAUNCH_CHECK();
@@ -1548,9 +1616,11 @@ extern "C" int fs_token_loss(const void* x, int64_t x_stride, int64_t n, const f
   if (n == 0) return FS_OK;
   Space o;
   carve(aligned(ws), s, false, &o);
-  if ((rc = pack_tokens(pack_args(o, s, x, x_stride, labels, padding_id, scale, table->dtype, err), stream)))
+  const Tokens lie = as_they_lie(x, x_stride, s);
+  if (!lie.x &&
+      (rc = pack_tokens(pack_args(o, s, x, x_stride, labels, padding_id, scale, table->dtype, err), stream)))
     return rc;
-  return forward(s, o, t, table->dtype, scale, true, loss, lse, stream);
+  return forward(s, o, t, table->dtype, scale, lie, labels, padding_id, err, loss, lse, stream);
 }
 
 extern "C" int fs_token_loss_backward(const void* x, int64_t x_stride, int64_t n, const fs_table* table,
@@ -1596,9 +1666,13 @@ extern "C" int fs_token_distill(const void* x, int64_t x_stride, int64_t n, cons
   Space o;
   carve(aligned(ws), s, false, &o);
   TeacherArgs a = teacher_args(o, s, ids, top, teacher, teacher_dtype, scale, padding_id, err);
-  if ((rc = pack_entries(a, pack_args(o, s, x, x_stride, nullptr, padding_id, scale, table->dtype, err), stream)) ||
-      (rc = forward(s, o, t, table->dtype, scale, false, loss, lse, stream)))
+  const Tokens lie = as_they_lie(x, x_stride, s);
+  if (!lie.x &&
+      (rc = pack_entries(a, pack_args(o, s, x, x_stride, nullptr, padding_id, scale, table->dtype, err), stream)))
     return rc;
+  if ((rc = forward(s, o, t, table->dtype, scale, lie, nullptr, padding_id, err, loss, lse, stream))) return rc;
+  a.x = lie.x;
+  a.x_stride = lie.stride;
   a.w = t.w;
   a.w_stride = t.stride;
   a.loss = loss;

@@ -142,6 +142,33 @@ def test_few_tokens_of_long_rows(kind, dim):
 
 
 @pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("n,dim", [(1, 64), (63, 128), (65, 64), (300, 192), (1024, 64), (40, 640)])
+def test_tokens_read_as_they_lie(kind, n, dim, t):
+    """Rows of whole steps, 16-byte aligned, apart; masked ones NaN, ids outside flagged."""
+    x, w, s, dloss = inputs(kind, n, 555, dim, t, masked=0.3 if n > 1 else 0.0)
+    key = "labels" if kind == "loss" else "ids"
+    if n > 4:
+        s[key][1] = 555
+        s[key][2] = -2
+    off = (s[key] if kind == "loss" else s[key].amax(1)) < 0
+    off |= (s[key] if kind == "loss" else s[key].amin(1)) >= 555
+    buf = torch.full((n, dim + 24), math.nan, dtype=t, device="cuda")
+    xd = buf[:, 8:8 + dim]
+    xd.copy_(x)
+    assert xd.data_ptr() % 16 == 0
+    both(x, w, s, dloss, xd=xd)
+    want = forward(xd, w.cuda(), s)
+    xd[off.cuda()] = math.nan
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = forward(xd, w.cuda(), s, err=err)
+    for k in got:
+        assert torch.equal(got[k], want[k]), k
+        assert not got[k][off.cuda()].any()
+    assert int(err) == (L.FS_EF_ID_RANGE if n > 4 else 0)
+
+
+@pytest.mark.parametrize("kind", KINDS)
 @pytest.mark.parametrize("scale", [-1.0, 0.0, 0.3, 4.0])
 def test_scales(kind, scale):
     x, w, s, dloss = inputs(kind, 90, 700, 64)
