@@ -430,32 +430,63 @@ int rows_of(const void* p, int32_t type, int64_t stride, int32_t dim, NormRows* 
 }
 
 // Workgroups that sum dweight and dbias: as many as the chip holds at once, one of
-// 1024 threads a CU, four of 256, three where a lane has 16 elements (65537 x 1000
-// bf16: 768 workgroups 80 us, 1024 96, 512 85; fewer also mean fewer sums to add).
+// 1024 threads a CU, two of 512, four of 256, three where a lane has 16 elements, one
+// of 512 where it has more than 8 (65537 x 1000 bf16: 768 workgroups 80 us, 1024 96,
+// 512 85; fewer also mean fewer sums to add).
 template <int E, int L, int C>
-constexpr int32_t kParts = L > 256 ? 256 : C * E > 8 ? 768 : 1024;
+constexpr int32_t kParts = L > 512 ? 256 : L > 256 ? (C * E > 8 ? 256 : 512) : C * E > 8 ? 768 : 1024;
 constexpr int32_t kMaxParts = 1024;
 
 // Lanes and pieces of a row by its width in pieces, calls launch.template go<E, L, C>().
-template <int E, typename F>
+// Wide rows: fewer lanes with more pieces each mean more rows under way in a CU, more
+// lanes more registers for each; the last piece of a narrower row is mostly idle. us
+// with 1024 lanes and with those taken: forward fp32 to bf16 16384 x 2560 82 and 47,
+// 16384 x 4096 95 and 76, 8192 x 5120 90 and 46, 4096 x 8192 59 and 46; bf16 8192 x 5120
+// 52 and 41, x 8192 60 and 55, x 12288 129 and 84. Backward fp32 16384 x 2560 148 and
+// 84, x 4096 159 and 138, 8192 x 5120 103 and 84; bf16 8192 x 12288 174 and 133; bf16
+// 8192 x 8192 86, with 512 105. The widest rows' backward sums do not fit the registers
+// of 1024 lanes and spill (4096 x 16384 bf16: 126 us, 3.2 TB/s).
+template <int E, bool Back, typename F>
 void by_width(int32_t dim, const F& launch) {
   const int32_t q = (int32_t)cdiv(dim, E);
-  if (q <= 8) launch.template go<E, 8, 1>();
-  else if (q <= 16) launch.template go<E, 16, 1>();
-  else if (q <= 32) launch.template go<E, 32, 1>();
-  else if (q <= 64) launch.template go<E, 64, 1>();
-  else if (q <= 128) launch.template go<E, 64, 2>();
-  else if (q <= 256) launch.template go<E, 256, 1>();
-  else if (q <= 512) launch.template go<E, 256, 2>();
-  else if (q <= 1024) launch.template go<E, 1024, 1>();
-  else if (q <= 2048) launch.template go<E, 1024, 2>();
-  else launch.template go<4, 1024, 4>();  // fp32 alone: 16 bits have half as many pieces
+  if (q <= 8) return launch.template go<E, 8, 1>();
+  if (q <= 16) return launch.template go<E, 16, 1>();
+  if (q <= 32) return launch.template go<E, 32, 1>();
+  if (q <= 64) return launch.template go<E, 64, 1>();
+  if (q <= 128) return launch.template go<E, 64, 2>();
+  if (q <= 256) return launch.template go<E, 256, 1>();
+  if (q <= 512) return launch.template go<E, 256, 2>();
+  if constexpr (Back) {
+    if constexpr (E == 4) {
+      if (q <= 1024) return launch.template go<E, 512, 2>();
+    } else {
+      if (q <= 1024) return launch.template go<E, 1024, 1>();
+    }
+  } else {
+    if (q <= 768) return launch.template go<E, 256, 3>();
+    if constexpr (E == 4) {
+      if (q <= 1024) return launch.template go<E, 256, 4>();
+    } else {
+      if (q <= 1024) return launch.template go<E, 512, 2>();
+    }
+  }
+  if (q <= 1536) return launch.template go<E, 512, 3>();
+  if constexpr (E == 4) {  // 16 bits have half as many pieces
+    if constexpr (Back) {
+      if (q <= 2048) return launch.template go<E, 1024, 2>();
+    } else {
+      if (q <= 2048) return launch.template go<E, 512, 4>();
+    }
+    launch.template go<E, 1024, 4>();
+  } else {
+    launch.template go<E, 1024, 2>();
+  }
 }
 
-template <typename F>
+template <bool Back, typename F>
 void by_type(const NormArgs& a, const F& launch) {
-  if (a.x.type == FS_F32) by_width<4>(a.dim, launch);
-  else by_width<8>(a.dim, launch);
+  if (a.x.type == FS_F32) by_width<4, Back>(a.dim, launch);
+  else by_width<8, Back>(a.dim, launch);
 }
 
 struct Forward {
@@ -538,7 +569,7 @@ extern "C" int fs_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, i
   a.param = param_dtype;
   a.inv_dim = 1.f / (float)dim;
   a.eps = eps;
-  by_type(a, Forward{a, stream});
+  by_type<false>(a, Forward{a, stream});
   FS_LAUNCH_CHECK();
   return FS_OK;
 }
@@ -546,8 +577,8 @@ extern "C" int fs_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, i
 extern "C" size_t fs_layer_norm_backward_workspace_size(int64_t n, int32_t dim) {
   if (n < 0 || dim < 1 || dim > FS_MAX_NORM_DIM) return 0;
   bool few = true;
-  by_width<4>(dim, Few{n, &few});
-  by_width<8>(dim, Few{n, &few});
+  by_width<4, true>(dim, Few{n, &few});
+  by_width<8, true>(dim, Few{n, &few});
   if (few) return 0;
   return sizeof(float) * 2 * (size_t)dim * (size_t)std::min<int64_t>(n, kMaxParts) + 256;
 }
@@ -591,7 +622,7 @@ extern "C" int fs_layer_norm_backward(const void* x, int32_t x_dtype, int64_t x_
   float* part = Carve(ws).take<float>(1);
   part = (float*)align_up((size_t)part, 256);
   int32_t parts = 1;
-  by_type(a, Backward{a, part, &parts, stream});
+  by_type<true>(a, Backward{a, part, &parts, stream});
   FS_LAUNCH_CHECK();
   if (parts > 1 && (dweight || dbias)) {
     hipLaunchKernelGGL(k_norm_params, dim3((unsigned)cdiv(2 * (int64_t)dim, kParamCols)), dim3(1024), 0,
