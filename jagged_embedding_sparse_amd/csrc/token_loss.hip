@@ -7,7 +7,8 @@
 //   back:     e_iv = dloss_i scale (exp(z_iv - lse_i) - target_iv),  dx = e w,  dw = e^T x
 //             target: 1 at the label; the sum of the q of the entries with id v
 //
-// Tokens that take part are first packed together (k_head_pack). The forward
+// Tokens that take part are first packed together (k_head_pack; the forward
+// pass reads few tokens as they lie). The forward
 // pass is one product whose tiles keep a maximum and a sum per token instead of
 // scores. The backward pass goes over the table in pieces: scores again, e in 16
 // bits, and the two products that sum it; what it holds of a piece is bounded
@@ -991,7 +992,7 @@ __device__ __forceinline__ void wave_lds() {
 // 8 accesses are in flight. Bound by the latency of a token's few dependent reads, so by
 // how many tokens are under way: 5135 tokens of 56 entries, rows of 32, 51 us with 4
 // waves of whole rows, 11 like this; 10813 x 5, rows of 440, 30 and 13; 8192 x 64, rows
-// of 1024, the whole call 569 and 520.
+// of 1024, 116 and 87.
 template <typename T, int LP, int W>
 __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_distill(TeacherArgs a) {
   constexpr int kTokens = kRowsPerGroup / W, kRows = 8, kGroups = kWave / LP;
