@@ -501,7 +501,10 @@ struct Forward {
 };
 
 // Few rows are one workgroup's, whose sums need no second launch and no workspace:
-// threads it has, or 0.
+// threads it has, or 0 where all of them share each row. There that is for up to 4 rows
+// (us of a call and, in a graph, of its kernels, with a second launch and without: 4 x
+// 1216 fp16 20 and 6.5, 14.5 and 6.8; 4 x 8152 20 and 14.3, 14.3 and 11.5; 8 x 8152 20
+// and 14.3, 16.6 and 16.9).
 template <int E, int L, int C>
 constexpr int few_threads() { return L >= 256 ? 0 : C * E > 8 ? 512 : 1024; }
 struct Few {
@@ -510,7 +513,7 @@ struct Few {
   template <int E, int L, int C>
   void go() const {
     constexpr int T = few_threads<E, L, C>();
-    *all = *all && (T ? cdiv(n, std::max(T, 1) / L) <= 8 : n <= 1);
+    *all = *all && (T ? cdiv(n, std::max(T, 1) / L) <= 8 : n <= 4);
   }
 };
 

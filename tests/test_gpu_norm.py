@@ -58,7 +58,7 @@ def test_wide_rows(dim, x):
 
 
 @pytest.mark.parametrize("dim", [2049, 3068, 3080, 4096, 5000, 6144, 6145, 8192, 12288, 12289])
-@pytest.mark.parametrize("n,x,out", [(1, F32, BF16), (21, F32, F32), (21, BF16, BF16), (700, F16, F16)])
+@pytest.mark.parametrize("n,x,out", [(1, F32, BF16), (4, BF16, F32), (5, F16, BF16), (21, F32, F32), (21, BF16, BF16), (700, F16, F16)])
 def test_wide_rows_of_every_share(n, dim, x, out):
     _both(n, dim, x, out, F32)
 
