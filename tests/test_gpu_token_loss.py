@@ -463,3 +463,28 @@ def test_a_capacity_s_workspace_serves_smaller_calls(kind):
     ws.fill_(255)  # NaN wherever a call reads what it has not written
     dx2, dw2 = backward(x.cuda(), w.cuda(), s, again, dloss, ws=ws)
     assert torch.equal(again["loss"], got["loss"]) and torch.equal(dx, dx2) and torch.equal(dw, dw2)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_a_table_past_32_bits(kind):
+    """4.5 GB of table and as much of its gradient: first, middle and last rows."""
+    rows, dim, n = 1_100_000, 2048, 5
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.empty(rows, dim, dtype=BF16, device="cuda").normal_(0, 2 / math.sqrt(dim), generator=g)
+    x = torch.randn(n, dim, generator=g, device="cuda").to(BF16)
+    at = torch.tensor([0, 1, rows // 2, rows - 2, rows - 1])
+    s = dict(labels=at) if kind == "loss" else dict(ids=at[:, None].clone(), teacher=torch.zeros(n, 1))
+    dloss = torch.full((n,), 0.25)
+    got = forward(x, w, s)
+    z = torch.cat([x.double() @ c.double().T for c in w.split(100_000)], 1).cpu()
+    lse = torch.logsumexp(z, 1)
+    # the plain forms' bounds: dim fp32 multiply-adds a score, the tiles' sums
+    e_z = (dim + 4) * P.U32 * float((x.double().abs() @ w[at].double().abs().T).max()) * 2
+    e_lse = e_z + 10 * P.U32 * (z.abs().amax(1) + lse) + (rows / 256 + 100) * P.U32
+    P.check(got["lse"], (lse, e_lse), "lse")
+    P.check(got["loss"], (lse - z[torch.arange(n), at], 2 * e_lse), "loss")
+    dx, dw = backward(x, w, s, got, dloss)
+    part = dict(labels=torch.arange(n)) if kind == "loss" else dict(ids=torch.arange(n)[:, None], teacher=s["teacher"])
+    ref = H.loss_gradients(x.cpu(), w[at].cpu(), got["lse"].cpu(), dloss, BF16, **part)
+    P.check(dw[at], ref["dweight"], "dweight")
+    assert dx.isfinite().all()
