@@ -617,7 +617,8 @@ size_t fs_layer_norm_backward_workspace_size(int64_t n, int32_t dim);
 /* a label or a teacher's top logits, without the tokens' logits. With       */
 /* z_iv = scale x_i . w_v over all rows v of the table,                      */
 /*   lse_i = log(sum_v exp z_iv)                                             */
-/* fs_token_loss: loss_i = lse_i - z_i,labels[i]; a token takes part where    */
+/* fs_token_loss: loss_i = lse_i - z_i,labels[i], never below 0 (near 0 its   */
+/* error is that of the scores beside the label's); a token takes part where */
 /* its label is not padding_id and inside [0, rows) (outside: FS_EF_ID_RANGE */
 /* is flagged).                                                             */
 /* fs_token_distill: entry k of token i takes part where ids[i][k] is not    */

@@ -306,7 +306,7 @@ struct ScoreArgs {
   const int64_t* labels;  // (null: none)
   int64_t all_rows, pad;
   float2* part;      // forward: [tiles of the table][npad] maximum and sum, base 2
-  float* at_label;   // forward: [npad] the label's score, base 2
+  float2* at_label;  // forward: [npad] the label's score, base 2, and what its rounding left
   // backward: [npad][e_cols] 16 bits in blocks. Up to kFew tokens e is two numbers,
   // rounded and what the rounding left, in blocks beside each other: few tokens'
   // gradients have few terms to average a rounding over (64 tokens: dx off by 3.2e-4
@@ -409,7 +409,10 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
     for (int j = 0; j < P::NI; ++j) {
       const int n = P::n_of(j, l);
       const int64_t lab = (int64_t)info.label(n, j) - a.v0 - v0;
-      if (lab >= 0 && lab < kV && has((int)lab)) a.at_label[n0 + n] = product_at(j, (int)lab) * scale2;
+      if (lab >= 0 && lab < kV && has((int)lab)) {
+        const float p_lab = product_at(j, (int)lab), z = p_lab * scale2, rest = __builtin_fmaf(p_lab, scale2, -z);
+        a.at_label[n0 + n] = make_float2(z, rest == rest ? rest : 0.f);  // none of an infinity
+      }
       float top = p.acc[0][j][0];
 #pragma unroll
       for (int i = 0; i < P::MI; ++i)
@@ -844,7 +847,7 @@ struct LossArgs {
   Head h;
   const float2* part;
   int64_t tiles;
-  const float* at_label;  // null: no loss here
+  const float2* at_label;  // null: no loss here
   float *loss, *lse;
   const int64_t* labels;  // of tokens that were read as they lie, or null
   int64_t rows, pad;
@@ -896,8 +899,19 @@ __global__ void __launch_bounds__(256) k_loss(LossArgs a) {
   for (int u = 0; u < Q; ++u) sum += sh[u][r].y * __builtin_amdgcn_exp2f(sh[u][r].x - m);
   const float log = __builtin_amdgcn_logf(sum);  // base 2
   a.lse[i] = pos >= 0 ? (m + log) * kLn2 : 0.f;
-  // the label's score is among those of the maximum, so a loss is not negative
-  if (a.at_label) a.loss[i] = pos >= 0 ? ((m - a.at_label[pos]) + log) * kLn2 : 0.f;
+  // The sum is that of the scores' distances from m, which is rounded: the label's own
+  // distance counts its rounding too, or a loss near 0 would be off by half a step of the
+  // score (8e-5 at scores of 1600). The label is one of the sum's terms, so what is left
+  // below 0 is rounding. NaN stays.
+  if (a.at_label) {
+    float loss = 0.f;
+    if (pos >= 0) {
+      const float2 z = a.at_label[pos];
+      loss = (((m - z.x) - z.y) + log) * kLn2;
+      loss = loss < 0.f ? 0.f : loss;
+    }
+    a.loss[i] = loss;
+  }
 }
 
 // ---------------------------------------------------------------- distillation
@@ -1216,7 +1230,7 @@ struct Space {
   uint8_t* live;
   char* pack;
   float2* part;      // forward
-  float* at_label;
+  float2* at_label;
   char* e;           // backward
   float *dx_part, *dw_part;
 };
@@ -1239,7 +1253,7 @@ size_t carve(void* ws, const Sizes& s, bool back, Space* o) {
     o->dw_part = c.take<float>((size_t)s.dw_part / 4);
   } else {
     o->part = c.take<float2>((size_t)(s.tiles * s.npad));
-    o->at_label = c.take<float>((size_t)s.npad);
+    o->at_label = c.take<float2>((size_t)s.npad);
   }
   h.n = s.n;
   h.npad = s.npad;
