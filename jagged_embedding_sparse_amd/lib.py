@@ -784,9 +784,8 @@ def _out_like(t, of, dtype):
 
 
 def _outs(pair, shape, dtype, d):
-    """Two such outputs, both fresh from one allocation."""
-    if pair[0] is None and pair[1] is None:
-        return torch.empty((2, *shape), dtype=dtype, device=d).unbind(0)
+    """Two such outputs, each of its own memory: views of one allocation would share a
+    version, and autograd would refuse to change one of them in place."""
     return _out(pair[0], shape, dtype, d), _out(pair[1], shape, dtype, d)
 
 
