@@ -664,9 +664,11 @@ size_t fs_layer_norm_backward_workspace_size(int64_t n, int32_t dim);
 /*           more) and the sums of cut products (2^28 bytes each, or one dx  */
 /*           in fp32 where that is more), all of them less where the sizes   */
 /*           need less.                                                     */
-/* A NaN or an infinity in a row of a token that takes part, in its dloss, or */
-/* in the table may reach every output of tokens that take part and all of    */
-/* dweight. scale is of any sign, below 2.3e38 in size. Outputs must not     */
+/* A NaN or an infinity in a row of a token that takes part, in its dloss, in  */
+/* the teacher's logits of its entries, or in the table may reach every output */
+/* of tokens that take part and all of dweight. Any finite logits will do, the */
+/* type's largest and lowest too, whatever they give times the scale.         */
+/* scale is of any sign, below 2.3e38 in size. Outputs must not              */
 /* alias inputs or each other. n < 2^24, n rows < 2^37 about (else            */
 /* FS_ERR_UNSUPPORTED), dim at most FS_MAX_TOKEN_DIM.                       */
 int fs_token_loss(const void* x, int64_t x_stride, int64_t n, const fs_table* table,

@@ -955,13 +955,16 @@ __global__ void __launch_bounds__(kRowsPerGroup * kWave) k_teacher_live(TeacherA
 constexpr int kPerLane = FS_MAX_TOP / kWave;
 
 // The teacher's distribution over a token's entries, one wave: q and log q of
-// entry lane + 64 u (0 where it takes no part).
+// entry lane + 64 u (0 where it takes no part). The scale goes to the distance from the
+// logit of the largest product, halves of both taken, so that neither a product nor a
+// distance of the type's largest and lowest values leaves fp32.
 struct Teacher {
   float q[kPerLane], logq[kPerLane];
   int64_t id[kPerLane];
   bool on[kPerLane];
   __device__ __forceinline__ Teacher(const TeacherArgs& a, int64_t i) {
     float t[kPerLane], top = -INFINITY, sum = 0.f;
+    const float sign = a.scale < 0.f ? -1.f : 1.f;
 #pragma unroll
     for (int u = 0; u < kPerLane; ++u) {
       const int k = lane() + kWave * u;
@@ -972,7 +975,7 @@ struct Teacher {
         id[u] = a.in.ids[i * a.in.top + k];
         const float x = a.in.logit(i * a.in.top + k);
         on[u] = a.in.on(id[u], x);
-        t[u] = x * a.scale;
+        t[u] = x * (0.5f * sign);
       }
       if (on[u]) top = fmaxf(top, t[u]);
     }
@@ -980,7 +983,7 @@ struct Teacher {
     for (int d = kWave / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor(top, d, kWave));
 #pragma unroll
     for (int u = 0; u < kPerLane; ++u) {
-      t[u] -= top;
+      t[u] = 2.f * ((t[u] - top) * (a.scale * sign));
       q[u] = on[u] ? expf(t[u]) : 0.f;
       sum += q[u];
     }

@@ -7,7 +7,7 @@ import torch
 
 import plain_head as H
 import plain_ops as P
-from test_gpu_token_loss import BF16, F16, forward, inputs
+from test_gpu_token_loss import BF16, F16, F32, backward, forward, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -40,3 +40,49 @@ def test_a_certain_token_s_loss(n, rows, k, t):
         bound += (rows / 256 + 116) * P.U32 + 8 * P.U32 * loss
     assert (got["loss"] >= 0).all(), got["loss"].min()
     P.check(got["loss"], (loss.cpu(), bound.cpu()), "loss")
+
+
+# ---------------------------------------------------------------- the teacher's ends
+
+
+def _ends(t):
+    """Rows of a teacher's logits and rows that have the same distribution."""
+    low, high, none = torch.finfo(t).min, torch.finfo(t).max, -math.inf
+    return [([low, low, low], [0.0, 0.0, 0.0]), ([high, high, high], [0.0, 0.0, 0.0]),
+            ([low, 1.0, 2.0], [-60000.0, 1.0, 2.0]), ([low, high, low], [-60000.0, 0.0, -60000.0]),
+            ([high, high, low], [0.0, 0.0, -60000.0]), ([low, none, low], [0.0, none, 0.0]),
+            ([low, none, none], [7.0, none, none])]
+
+
+@pytest.mark.parametrize("n", [7, 2100])
+@pytest.mark.parametrize("scale", [0.01, 0.5, 1.0, 2.0])
+@pytest.mark.parametrize("t", [F32, BF16, F16])
+def test_a_teacher_s_largest_and_lowest_logits(t, scale, n):
+    """Masks of the type's lowest value, alone too, and logits whose product with the scale
+    passes fp32: a softmax knows only differences, so rows of the same differences, or of ones
+    that fp32's exponential has no value for, give the same bits."""
+    x, w, _, dloss = inputs("distill", n, 150, 64)
+    g = torch.Generator().manual_seed(1)
+    ids = torch.randint(0, 150, (n, 3), generator=g)
+    ends = _ends(t)
+    a, b = (torch.tensor([ends[i % 7][j] for i in range(n)]).to(t) for j in (0, 1))
+    sa, sb = dict(ids=ids, teacher=a), dict(ids=ids, teacher=b)
+    got, want = (forward(x.cuda(), w.cuda(), s, scale=scale) for s in (sa, sb))
+    for k in got:
+        assert got[k].isfinite().all() and torch.equal(got[k], want[k]), k
+    for y, z in zip(*(backward(x.cuda(), w.cuda(), s, want, dloss, scale=scale) for s in (sa, sb))):
+        assert y.isfinite().all() and torch.equal(y, z)
+    ref = H.losses(x, w, scale, **sb)
+    for k, y in want.items():
+        P.check(y, ref[k], k)
+
+
+@pytest.mark.parametrize("t", [F32, BF16, F16])
+def test_a_negative_scale_s_lowest_logit_is_certain(t):
+    x, w, _, dloss = inputs("distill", 40, 150, 64)
+    ids = torch.randint(0, 150, (40, 3), generator=torch.Generator().manual_seed(1))
+    low = torch.tensor([[torch.finfo(t).min, 1.0, torch.finfo(t).max]]).repeat(40, 1).to(t)
+    sure = torch.tensor([[-60000.0, 1.0, 60000.0]]).repeat(40, 1).to(t)
+    got, want = (forward(x.cuda(), w.cuda(), dict(ids=ids, teacher=y), scale=-2.0) for y in (low, sure))
+    for k in got:
+        assert got[k].isfinite().all() and torch.equal(got[k], want[k]), k
