@@ -205,6 +205,16 @@ struct NormArgs {
   float inv_dim, eps;
 };
 
+// A sum over a row by its length, rounded once: the product with 1 / dim, and what that
+// leaves of the sum by 1 / dim once more. The product alone may be off by a step, and a row
+// of one number c would keep what is left of c - mean times rstd (0.02 for 1000 columns of
+// 1000 with an eps of 1e-5). 4096 x 16384 bf16 backward: 127 us with the product alone, 128
+// like this, 133 with a division; forward and rows that fit the registers within 1% of it.
+__device__ __forceinline__ float by_dim(float sum, const NormArgs& a) {
+  const float q = sum * a.inv_dim, left = __builtin_fmaf(-q, (float)a.dim, sum);
+  return left == left ? __builtin_fmaf(left, a.inv_dim, q) : q;  // none of an infinity
+}
+
 // 32768 x 1024 fp32 to bf16: 33 us on one set of rows, part of them in the caches, 40
 // on changing ones, where copying the bytes takes 41.
 template <int E, int L, int C>
@@ -238,7 +248,7 @@ __global__ void __launch_bounds__(L > 256 ? L : 256) k_norm(NormArgs a) {
 #pragma unroll
       for (int e = 0; e < E; ++e) sum[0] += s.mine(c, e) ? v[c][e] : 0.f;
     row_sums<L>(sum, tmp, 0);
-    const float mean = sum[0] * a.inv_dim;
+    const float mean = by_dim(sum[0], a);
     float sq[1] = {0.f};
 #pragma unroll
     for (int c = 0; c < C; ++c)
@@ -248,7 +258,7 @@ __global__ void __launch_bounds__(L > 256 ? L : 256) k_norm(NormArgs a) {
         sq[0] += s.mine(c, e) ? v[c][e] * v[c][e] : 0.f;
       }
     row_sums<L>(sq, tmp, 1);
-    const float rstd = 1.f / sqrtf(sq[0] * a.inv_dim + a.eps);
+    const float rstd = 1.f / sqrtf(by_dim(sq[0], a) + a.eps);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -350,7 +360,7 @@ __global__ void __launch_bounds__(L > 256 ? L : C * E > 8 ? 512 : 1024) k_norm_b
       }
     row_sums<L>(sum, tmp, turn);
     turn ^= 1;
-    const float sg = sum[0] * a.inv_dim, sgh = sum[1] * a.inv_dim;
+    const float sg = by_dim(sum[0], a), sgh = by_dim(sum[1], a);
 #pragma unroll
     for (int c = 0; c < C; ++c)
 #pragma unroll
