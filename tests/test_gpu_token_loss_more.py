@@ -5,9 +5,10 @@ import math
 import pytest
 import torch
 
+import head_differences as D
 import plain_head as H
 import plain_ops as P
-from test_gpu_token_loss import BF16, F16, F32, backward, forward, inputs
+from test_gpu_token_loss import BF16, F16, F32, KINDS, backward, forward, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +87,25 @@ def test_a_negative_scale_s_lowest_logit_is_certain(t):
     got, want = (forward(x.cuda(), w.cuda(), dict(ids=ids, teacher=y), scale=-2.0) for y in (low, sure))
     for k in got:
         assert got[k].isfinite().all() and torch.equal(got[k], want[k]), k
+
+
+# ---------------------------------------------------------------- differences
+
+
+@pytest.mark.parametrize("side", ["x", "w"])
+@pytest.mark.parametrize("kind", KINDS)
+def test_gradients_against_differences(kind, side):
+    """The calls' gradients against differences of the calls' own losses; test_head_differences
+    has which wrong gradients these bounds refuse."""
+    x, w, s, dloss = D.inputs(kind)
+    got = forward(x.cuda(), w.cuda(), s)
+    dx, dw = backward(x.cuda(), w.cuda(), s, got, dloss, dtype=F32)
+    lse = got["lse"].cpu()
+    ref = H.loss_gradients(x, w, lse, dloss, F32, **s)
+
+    def losses(a, b):
+        return forward(a.cuda(), b.cuda(), s)["loss"].cpu().double(), H.losses(a, b, **s)["loss"][1]
+
+    grad, name = (dx, "dx") if side == "x" else (dw, "dweight")
+    apart, most = D.off(x, w, s, dloss, side, grad, ref[name][1], D.direction(ref[name][0]), losses)
+    assert apart <= most, (apart, most)
