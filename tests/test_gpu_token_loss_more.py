@@ -1,4 +1,6 @@
-"""Losses of tokens against a vocabulary's table at their ends."""
+"""Losses of tokens against a vocabulary's table at their ends: sharp distributions, the
+teacher's largest and lowest logits, infinities and NaN, gradients against differences, every
+kernel of the large products, many tokens, tables past 32 bits."""
 
 import math
 
@@ -8,7 +10,7 @@ import torch
 import head_differences as D
 import plain_head as H
 import plain_ops as P
-from test_gpu_token_loss import BF16, F16, F32, KINDS, backward, forward, inputs
+from test_gpu_token_loss import BF16, F16, F32, KINDS, backward, both, forward, inputs
 
 pytestmark = pytest.mark.gpu
 
@@ -89,6 +91,51 @@ def test_a_negative_scale_s_lowest_logit_is_certain(t):
         assert got[k].isfinite().all() and torch.equal(got[k], want[k]), k
 
 
+# ---------------------------------------------------------------- infinities and NaN
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("n,dim", [(70, 64), (70, 72), (1100, 72)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_what_a_token_that_takes_part_holds_stays_in_its_loss(kind, n, dim, what):
+    x, w, s, dloss = inputs(kind, n, 600, dim, masked=0.3)
+    on = ((s["labels"] if kind == "loss" else s["ids"].amax(1)) >= 0)
+    clean = forward(x.cuda(), w.cuda(), s)
+    bad = int(on.nonzero()[n // 4])
+    x[bad, 5] = what
+    got = forward(x.cuda(), w.cuda(), s)
+    keep = torch.arange(n) != bad
+    for k in got:
+        assert torch.equal(got[k].cpu()[keep], clean[k].cpu()[keep]), k
+    assert not got["loss"][bad].isfinite() and not got["lse"][bad].isfinite()
+    dx, _ = backward(x.cuda(), w.cuda(), s, got, dloss)
+    assert not dx[bad].isfinite().any() and not dx.cpu()[~on].any()
+
+
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+@pytest.mark.parametrize("n,rows", [(70, 600), (1100, 600), (300, 66_000)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_what_the_table_holds_reaches_tokens_that_take_part(kind, n, rows, what):
+    x, w, s, dloss = inputs(kind, n, rows, 64, masked=0.3)
+    on = ((s["labels"] if kind == "loss" else s["ids"].amax(1)) >= 0)
+    w[rows // 3] = what
+    got = forward(x.cuda(), w.cuda(), s)
+    dx, _ = backward(x.cuda(), w.cuda(), s, got, dloss)
+    for y in (got["loss"], got["lse"]):
+        assert not y.cpu()[on].isfinite().any() and not y.cpu()[~on].any()
+    assert not dx.cpu()[~on].any()
+
+
+@pytest.mark.parametrize("n", [40, 300])
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("kind", KINDS)
+def test_losses_gradients_of_either_sign_and_zero(kind, t, n):
+    x, w, s, dloss = inputs(kind, n, 500, 72, t)
+    dloss *= (torch.arange(n) % 3 - 1).float()
+    got, dx, _ = both(x, w, s, dloss)
+    assert not dx[1::3].any()
+
+
 # ---------------------------------------------------------------- differences
 
 
@@ -109,3 +156,85 @@ def test_gradients_against_differences(kind, side):
     grad, name = (dx, "dx") if side == "x" else (dw, "dweight")
     apart, most = D.off(x, w, s, dloss, side, grad, ref[name][1], D.direction(ref[name][0]), losses)
     assert apart <= most, (apart, most)
+
+
+# ---------------------------------------------------------------- every kernel
+
+
+def _held(x, w, s, dloss, dtype=None, scale=1.0):
+    """Both directions against the plain forms, computed in 64 bits on the GPU."""
+    live = (s["labels"] if "labels" in s else s["ids"].amax(1)) >= 0
+    x = x.clone()
+    x[~live] = math.nan
+    xd, wd = x.cuda(), w.cuda()
+    got = forward(xd, wd, s, scale=scale)
+    dx, dw = backward(xd, wd, s, got, dloss, dtype=dtype, scale=scale)
+    with torch.device("cuda"):
+        sd = {k: v.cuda() for k, v in s.items()}
+        ref = H.losses(xd, wd, scale, **sd)
+        ref.update(H.loss_gradients(xd, wd, got["lse"], dloss.cuda(), dtype or x.dtype, scale, **sd))
+        ref = {k: tuple(y.cpu() for y in v) for k, v in ref.items()}
+    for name, y in dict(got, dx=dx, dweight=dw).items():
+        P.check(y, ref[name], name)
+
+
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("dim", [40, 64, 128, 136, 200, 256, 264, 328])
+@pytest.mark.parametrize("kind", KINDS)
+def test_gradients_of_the_table_in_the_widest_tiles(kind, dim, t):
+    """256 tiles of 256 table rows and more: the table's gradient is made in tiles as wide."""
+    _held(*inputs(kind, 300, 66_000, dim, t, seed=dim))
+
+
+@pytest.mark.parametrize("kind,t,dim", [("loss", BF16, 200), ("distill", F16, 264), ("distill", BF16, 128),
+                                        ("loss", F16, 100)])
+def test_more_pieces_than_one_of_wider_rows(kind, t, dim):
+    _held(*inputs(kind, 9000, 70_000, dim, t, masked=0.1, seed=dim))
+
+
+@pytest.mark.parametrize("n,rows,dim", [(40_001, 300, 72), (300_001, 50, 8)])
+@pytest.mark.parametrize("t", [BF16, F16])
+@pytest.mark.parametrize("kind", KINDS)
+def test_many_tokens(kind, t, n, rows, dim):
+    """A workgroup packs more tokens than it has threads."""
+    _held(*inputs(kind, n, rows, dim, t, top=3, masked=0.4))
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_row_of_a_table_past_32_bits(kind):
+    """4.5 GB of table and as much of its gradient: dx, which reads the table past them, and
+    every row of the table's gradient."""
+    rows, dim, n, step = 1_100_000, 2048, 5, 50_000
+    g = torch.Generator(device="cuda").manual_seed(1)
+    w = torch.empty(rows, dim, dtype=BF16, device="cuda").normal_(0, 2 / math.sqrt(dim), generator=g)
+    x = torch.randn(n, dim, generator=g, device="cuda").to(BF16)
+    at = torch.tensor([0, 1, rows // 2, rows - 2, rows - 1])
+    s = dict(labels=at) if kind == "loss" else dict(ids=at[:, None].clone(), teacher=torch.zeros(n, 1))
+    dloss = torch.full((n,), 0.25)
+    dx = torch.full((n, dim), math.nan, dtype=BF16, device="cuda")
+    dw = torch.full((rows, dim), math.nan, dtype=BF16, device="cuda")
+    got = forward(x, w, s)
+    backward(x, w, s, got, dloss, dx=dx, dweight=dw)
+    with torch.device("cuda"):
+        total, size, lse = torch.zeros(n, dim, dtype=torch.float64), 0, got["lse"]
+        for lo in range(0, rows, step):
+            # the rows' own part of the plain form: labels and entries outside it take part in
+            # the tokens' softmax as the given lse, and bring no target
+            part, own = w[lo:lo + step], (at >= lo) & (at < lo + step)
+            wd = part.double()
+            z, e_z = H._scores(x, part, 1.0, torch.ones(n, dtype=torch.bool))
+            p = torch.exp(z - lse.double()[:, None])
+            target = torch.zeros_like(p)
+            target[own.nonzero()[:, 0].cuda(), (at[own] - lo).cuda()] = 1
+            e = 0.25 * (p - target)
+            off = 0.25 * (p * (2 * e_z + 6 * P.U32 * (z.abs() + lse.abs()[:, None] + 42) + 4 * P.U32)
+                          + (4 + 560) * P.U32 * (p + target))
+            e_e = off * (1 + P.u(BF16)) + P.u(BF16) ** 2 * e.abs()  # two numbers of bf16
+            have, want = dw[lo:lo + step], e.T @ x.double()
+            bound = (e_e.T @ x.double().abs() + 45 * P.U32 * (e.abs().T @ x.double().abs())) * (1 + P.u(BF16))
+            bound += P.u(BF16) * want.abs() + P.tiny(BF16)
+            assert ((have.double() - want).abs() <= bound).all(), lo
+            total += e @ wd
+            size = size + e_e @ wd.abs() + (rows + 40) * P.U32 * (e.abs() @ wd.abs())
+        size = size * (1 + P.u(BF16)) + P.u(BF16) * total.abs() + P.tiny(BF16)
+    P.check(dx, (total.cpu(), size.cpu()), "dx")
