@@ -200,13 +200,99 @@ def test_many_tokens(kind, t, n, rows, dim):
     _held(*inputs(kind, n, rows, dim, t, top=3, masked=0.4))
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256, 264])
+@pytest.mark.parametrize("top", [1, 9, 64, 65, 200, 256])
+def test_many_tokens_entries(top, dim):
+    """A wave to a token and its entries, rows of every share of a wave."""
+    _held(*inputs("distill", 2100, 400, dim, top=top, seed=top))
+
+
+@pytest.mark.parametrize("n", [9, 5000])
+@pytest.mark.parametrize("rows", [1, 2])
 @pytest.mark.parametrize("kind", KINDS)
-def test_every_row_of_a_table_past_32_bits(kind):
-    """4.5 GB of table and as much of its gradient: dx, which reads the table past them, and
-    every row of the table's gradient."""
-    rows, dim, n, step = 1_100_000, 2048, 5, 50_000
+def test_tables_of_one_and_two_rows(kind, n, rows):
+    x, w, s, dloss = inputs(kind, n, rows, 72)
+    _held(x, w, s, dloss)
+    if rows == 1 and kind == "loss":  # the one row is certain (entries of one id have an entropy)
+        got = forward(x.cuda(), w.cuda(), s)
+        assert got["loss"].abs().max() <= 4 * P.U32 * (1 + got["lse"].abs().max())
+
+
+@pytest.mark.parametrize("n", [40, 1100])
+@pytest.mark.parametrize("kind", KINDS)
+def test_ids_that_32_bits_would_make_good(kind, n):
+    x, w, s, dloss = inputs(kind, n, 300, 64, masked=0.0)
+    key = "labels" if kind == "loss" else "ids"
+    for i, v in enumerate(((1 << 32) + 3, -(1 << 32) + 3, (1 << 63) - 1, -(1 << 63), 1 << 31)):
+        s[key][3 * i] = v
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = forward(x.cuda(), w.cuda(), s, err=err)
+    assert int(err) != 0
+    dx, _ = backward(x.cuda(), w.cuda(), s, got, dloss)
+    assert not got["loss"][:15:3].any() and not got["lse"][:15:3].any() and not dx[:15:3].any()
+    both(x, w, s, dloss)
+
+
+@pytest.mark.parametrize("n,rows,dim", [(3, 300, 65536), (3, 300, 65535), (300, 70, 65536)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_the_widest_rows(kind, n, rows, dim):
+    _held(*inputs(kind, n, rows, dim, masked=0.0))
+
+
+# ---------------------------------------------------------------- past 32 bits
+
+
+def _in_parts(x, w, s, dloss, step):
+    """_held by parts of the tokens, for tokens and a table that are on the GPU."""
+    n, t = x.shape[0], x.dtype
+    got = forward(x, w, s)
+    dx, dw = backward(x, w, s, got, dloss, dtype=F32)
+    total, most = 0, 0
+    with torch.device("cuda"):
+        for lo in range(0, n, step):
+            part = {k: v[lo:lo + step] for k, v in s.items()}
+            ref = H.losses(x[lo:lo + step], w, **part)
+            for name, y in got.items():
+                off = (y[lo:lo + step].double() - ref[name][0]).abs()
+                assert (off <= ref[name][1]).all(), (name, lo)
+            ref = H.loss_gradients(x[lo:lo + step], w, got["lse"][lo:lo + step], dloss[lo:lo + step], t, **part)
+            assert ((dx[lo:lo + step].double() - ref["dx"][0]).abs() <= ref["dx"][1]).all(), lo
+            total, most = total + ref["dweight"][0], most + ref["dweight"][1]
+        assert ((dw.double() - total).abs() <= most).all()
+
+
+def _on_gpu(kind, n, rows, dim, t=BF16):
+    g = torch.Generator(device="cuda").manual_seed(2)
+    w = torch.empty(rows, dim, dtype=t, device="cuda").normal_(0, 2 / math.sqrt(dim), generator=g)
+    x = torch.empty(n, dim, dtype=t, device="cuda").normal_(generator=g)
+    ids = torch.randint(-rows // 4, rows, (n, 1 if kind == "loss" else 2), generator=g, device="cuda").clamp_min_(-1)
+    s = dict(labels=ids[:, 0].contiguous()) if kind == "loss" else \
+        dict(ids=ids, teacher=torch.empty(n, 2, device="cuda").normal_(generator=g))
+    return x, w, s, torch.rand(n, generator=g, device="cuda") / n
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_tokens_past_32_bits(kind):
+    """4.5 GB of tokens, and as much of their gradient."""
+    _in_parts(*_on_gpu(kind, 1_100_000, 50, 2048), 100_000)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+def test_the_most_tokens(kind):
+    x, w, s, dloss = _on_gpu(kind, (1 << 24) - 256, 20, 8)
+    _in_parts(x, w, s, dloss, 1 << 21)
+
+
+@pytest.mark.parametrize("rows,dim,step", [(1_100_000, 2048, 50_000), ((1 << 31) - 1024, 8, 1 << 24)])
+@pytest.mark.parametrize("kind", KINDS)
+def test_every_row_of_a_table_past_32_bits(kind, rows, dim, step):
+    """4.5 and 34 GB of table and as much of its gradient, the second of nearly as many rows as
+    a call takes: dx, which reads the table past 32 bits, and every row of the table's gradient."""
+    n = 5
     g = torch.Generator(device="cuda").manual_seed(1)
-    w = torch.empty(rows, dim, dtype=BF16, device="cuda").normal_(0, 2 / math.sqrt(dim), generator=g)
+    w = torch.empty(rows, dim, dtype=BF16, device="cuda")
+    for lo in range(0, rows, 1 << 27):
+        w[lo:lo + (1 << 27)].normal_(0, 2 / math.sqrt(dim), generator=g)
     x = torch.randn(n, dim, generator=g, device="cuda").to(BF16)
     at = torch.tensor([0, 1, rows // 2, rows - 2, rows - 1])
     s = dict(labels=at) if kind == "loss" else dict(ids=at[:, None].clone(), teacher=torch.zeros(n, 1))
@@ -215,14 +301,23 @@ def test_every_row_of_a_table_past_32_bits(kind):
     dw = torch.full((rows, dim), math.nan, dtype=BF16, device="cuda")
     got = forward(x, w, s)
     backward(x, w, s, got, dloss, dx=dx, dweight=dw)
+    # e's terms of dx are added up within a part of a piece of the table, then by part and piece
+    terms = min(rows, 1 << 22) + 1000
+
+    def over_rows(a, b):  # a @ b, whose long sums a product of few rows makes one by one
+        return torch.stack([(r[:, None] * b).sum(0) for r in a])
+
     with torch.device("cuda"):
-        total, size, lse = torch.zeros(n, dim, dtype=torch.float64), 0, got["lse"]
+        live = torch.ones(n, dtype=torch.bool)
+        total, size, sums, lse, most = torch.zeros(n, dim, dtype=torch.float64), 0, [], got["lse"], 0
         for lo in range(0, rows, step):
             # the rows' own part of the plain form: labels and entries outside it take part in
             # the tokens' softmax as the given lse, and bring no target
             part, own = w[lo:lo + step], (at >= lo) & (at < lo + step)
             wd = part.double()
-            z, e_z = H._scores(x, part, 1.0, torch.ones(n, dtype=torch.bool))
+            z, e_z = H._scores(x, part, 1.0, live)
+            sums.append(torch.logsumexp(z, 1))
+            most = torch.maximum(z.abs().amax(1), torch.as_tensor(most))
             p = torch.exp(z - lse.double()[:, None])
             target = torch.zeros_like(p)
             target[own.nonzero()[:, 0].cuda(), (at[own] - lo).cuda()] = 1
@@ -234,7 +329,14 @@ def test_every_row_of_a_table_past_32_bits(kind):
             bound = (e_e.T @ x.double().abs() + 45 * P.U32 * (e.abs().T @ x.double().abs())) * (1 + P.u(BF16))
             bound += P.u(BF16) * want.abs() + P.tiny(BF16)
             assert ((have.double() - want).abs() <= bound).all(), lo
-            total += e @ wd
-            size = size + e_e @ wd.abs() + (rows + 40) * P.U32 * (e.abs() @ wd.abs())
+            total += over_rows(e, wd)
+            size = size + over_rows(e_e + terms * P.U32 * e.abs(), wd.abs())
         size = size * (1 + P.u(BF16)) + P.u(BF16) * total.abs() + P.tiny(BF16)
+        ref = torch.logsumexp(torch.stack(sums), 0)
+        z = (x.double() * w[at.cuda()].double()).sum(1)
+        e_z = (dim + 4) * P.U32 * float(x.double().abs().sum(1).max()) * float(w[:1 << 20].abs().max())
+        # the tiles' sums: 256 scores, and as many tiles as a thread of 64 takes
+        e_lse = e_z + 10 * P.U32 * (most + ref.abs()) + (rows / 256 / 64 + 100) * P.U32
+    P.check(got["lse"], (ref.cpu(), e_lse.cpu()), "lse")
+    P.check(got["loss"], ((ref - z).cpu(), 2 * e_lse.cpu()), "loss")
     P.check(dx, (total.cpu(), size.cpu()), "dx")
