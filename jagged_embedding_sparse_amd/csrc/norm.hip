@@ -202,16 +202,18 @@ struct NormArgs {
   float* part;               // backward: [workgroups][2][dim], or null: one workgroup writes
   char *dweight, *dbias;
   int32_t dim, param;        // type of weight, bias and their gradients
-  float inv_dim, eps;
+  float inv_dim, count, eps;  // count: dim
 };
 
 // A sum over a row by its length, rounded once: the product with 1 / dim, and what that
 // leaves of the sum by 1 / dim once more. The product alone may be off by a step, and a row
 // of one number c would keep what is left of c - mean times rstd (0.02 for 1000 columns of
-// 1000 with an eps of 1e-5). 4096 x 16384 bf16 backward: 127 us with the product alone, 128
-// like this, 133 with a division; forward and rows that fit the registers within 1% of it.
+// 1000 with an eps of 1e-5). 4096 x 16384 bf16 backward: 126.6 us with the product alone, 127.3
+// like this, 133 with a division; 32768 x 1024 fp32 to bf16 forward 42 and 43 to 44, others
+// within 1%. The length comes with the call: made here it would take a register of rows that
+// have none left (4096 x 9000, fp32 with a bf16 dout, backward 161 and 175 us).
 __device__ __forceinline__ float by_dim(float sum, const NormArgs& a) {
-  const float q = sum * a.inv_dim, left = __builtin_fmaf(-q, (float)a.dim, sum);
+  const float q = sum * a.inv_dim, left = __builtin_fmaf(-q, a.count, sum);
   return left == left ? __builtin_fmaf(left, a.inv_dim, q) : q;  // none of an infinity
 }
 
@@ -454,8 +456,9 @@ constexpr int32_t kMaxParts = 1024;
 // 16384 x 4096 95 and 76, 8192 x 5120 90 and 46, 4096 x 8192 59 and 46; bf16 8192 x 5120
 // 52 and 41, x 8192 60 and 55, x 12288 129 and 84. Backward fp32 16384 x 2560 148 and
 // 84, x 4096 159 and 138, 8192 x 5120 103 and 84; bf16 8192 x 12288 174 and 133; bf16
-// 8192 x 8192 86, with 512 105. The widest rows' backward sums do not fit the registers
-// of 1024 lanes and spill (4096 x 16384 bf16: 126 us, 3.2 TB/s).
+// 8192 x 8192 86, with 512 105. The widest rows' backward sums (16 bits above 12288 columns,
+// fp32 above 8192) do not fit the registers of 1024 lanes and spill: 4096 x 16384 bf16 127 us,
+// 3.2 TB/s, fp32 235, 3.4; 4096 x 9000 fp32 173, 2.6.
 template <int E, bool Back, typename F>
 void by_width(int32_t dim, const F& launch) {
   const int32_t q = (int32_t)cdiv(dim, E);
@@ -581,6 +584,7 @@ extern "C" int fs_layer_norm(const void* x, int32_t x_dtype, int64_t x_stride, i
   a.dim = dim;
   a.param = param_dtype;
   a.inv_dim = 1.f / (float)dim;
+  a.count = (float)dim;
   a.eps = eps;
   by_type<false>(a, Forward{a, stream});
   FS_LAUNCH_CHECK();
@@ -630,6 +634,7 @@ extern "C" int fs_layer_norm_backward(const void* x, int32_t x_dtype, int64_t x_
   a.dim = dim;
   a.param = param_dtype;
   a.inv_dim = 1.f / (float)dim;
+  a.count = (float)dim;
   a.x.type = x_dtype;
   a.out.type = dout_dtype;
   float* part = Carve(ws).take<float>(1);
