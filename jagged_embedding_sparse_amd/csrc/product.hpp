@@ -15,10 +15,10 @@
 // of the next stage. Loads are asked for right behind the barrier, a whole step
 // before they are waited for.
 //
-// Measured (256 x 256, eight waves, K = 32768, 16384 x 1024 sums, bf16): 850 us, 1290
-// TFLOP/s, the matrix units busy 70% of the time at a clock that the card has brought
-// down from 2.4 to 1.65 GHz, so what bounds it is power. A library product of these
-// shapes reaches 960 to 1060, one of 8192^3 1380. Four waves of 128 x 128 instead of
+// Measured (256 x 256, eight waves, K = 32768, 16384 x 1024 sums, bf16): 845 to 884 us by
+// card, 1245 to 1300 TFLOP/s, the matrix units busy 70% of the time at a clock that the card has
+// brought down from 2.4 to 1.7 GHz, so what bounds it is power. A library product of these
+// shapes reaches 960 to 1070, one of 8192^3 1380 to 1410. Four waves of 128 x 128 instead of
 // eight of 128 x 64 do not fit the registers (737 against 613 us for 16384 x 16384 x
 // 1024); left to the compiler's order of reads and products, 470 against 458.
 #pragma once
@@ -70,8 +70,8 @@ __device__ __forceinline__ void load_words(const void* base, uint32_t at, uint32
       : "memory");
 }
 
-// A operand reads of a tile in LDS: rows r0 .. r0 + 31 (a multiple of 32), k's
-// 16 kk + 8 g .. of a tile of rows of 64 k's;
+// A operand reads of a tile in LDS: rows r0 .. r0 + 31 (r0 a multiple of 32), k's
+// 16 kk + 8 g .. of a tile of rows of 64 k's,
 struct ReadRows {
   int rows_at;
   __device__ __forceinline__ ReadRows() { rows_at = attn::piece<kK>(lane() & 31, lane() >> 5); }
@@ -130,7 +130,6 @@ struct Rows {
     load_piece(base, at[x], tile + attn::wave_id() * (kWave * 16) + x * NT * 16);
   }
   __device__ __forceinline__ void advance() { base = attn::uniform(base + kK * 2); }
-  // rows r0 .. r0 + 31 (a multiple of 32), k's 16 kk ..
   using Read = ReadRows;
 };
 

@@ -32,6 +32,13 @@ constexpr int64_t kPackBytes = (int64_t)1 << 26;   // a piece of a table that ha
 constexpr int64_t kPartBytes = (int64_t)1 << 28;   // sums of a cut product
 constexpr int kMostParts = 256;
 constexpr int64_t kFew = 256;                      // tokens, see ScoreArgs::e
+constexpr int64_t kStayMost = 1024;                // tokens that may keep their places
+// Tokens whose tiles are joined by many threads each, a distillation's where its entries are
+// (a launch of 4 us less). Calls with that and without, us: distillation of 2100 tokens, 4000
+// rows of 512, 46 and 39, 4096 64 and 48, 8192 100 and 68; of 1500 34 and 30, so 1025 would do
+// as well. Cross entropy 8192 x 4000 x 512 59 and 56, 1500 24 and 22.
+constexpr int64_t kFewRows = 2048;
+static_assert(kFewRows > kStayMost, "tokens that keep their places have no list of them for k_loss");
 constexpr int64_t kCacheBytes = (int64_t)1 << 27;  // half of the last level
 
 // What the kernels of one call share, in its workspace.
@@ -184,7 +191,9 @@ __device__ void put_mul(const PackArgs& a) {
 // Each workgroup counts the tokens before its own that take part (labels are few
 // bytes beside the rows), so one launch does it without waiting for another
 // workgroup. The last of them writes the count and the zero rows behind it. 16384 x
-// 1024: 25 us, where copying the rows takes 13; the counting is the rest.
+// 1024: 25 us, where copying the rows takes 13; the counting is the rest. There are at most
+// 1024 workgroups, so it grows with the tokens: rows of 64, 2^17 tokens 57 us, 2^20 520 and
+// 2^23 4.1 ms, more than the forward scores of 300 table rows (2^20: 250).
 __global__ void __launch_bounds__(kPackThreads) k_head_pack(PackArgs a) {
   __shared__ int32_t tmp[17], s_row[kPackThreads];
   const int32_t groups = gridDim.x - a.back;
@@ -520,8 +529,9 @@ __device__ __forceinline__ void finish_scores(const ScoreArgs& a, P& p, uint16_t
 // CUs and take tiles in turn; the next tile's first loads are asked for before this
 // one's exponentials.
 // Bound by power where rows are long, as the products are: forward, 14746 tokens x
-// 100000 x 1024, 2.45 ms (1230 TFLOP/s, matrix units busy 64%). Backward, 16384 x
-// 32768 x 1024, 1.15 ms (955): of that a fifth is what follows the product, 140 us of
+// 100000 x 1024, 2.42 to 2.55 ms by card (1185 to 1250 TFLOP/s, matrix units busy 64%).
+// Backward, 16384 x 32768 x 1024, 1.12 to 1.17 ms (940 to 980; 49%, 1.88 GHz): of that a fifth
+// is what follows the product and does not overlap it, 140 us of
 // it the 1 GiB of e that it writes, 36 the exponentials. Tiles begun half a tile apart
 // on half of the CUs, so that fewer write at once: 1143 against 1134 us, not kept. With
 // rows of 64 (one step a tile) the exponentials bound it: 8778 x 104994 x 64 takes 300
@@ -700,8 +710,8 @@ struct Waves {
 };
 
 // dx = e w over a part of the piece's rows, by tokens' places: workgroup `bid` of
-// the product's. lds: two stages. 16384 x 32768 x 1024: 860 us (1280 TFLOP/s, matrix
-// units busy 69%: power, see product.hpp), with the fp32 sums that it adds to.
+// the product's. lds: two stages. 16384 x 32768 x 1024: 854 to 884 us by card (1245 to 1290
+// TFLOP/s, matrix units busy 69%: power, see product.hpp), with the fp32 sums that it adds to.
 template <typename T, int DM, int BN, int Halves>
 struct GradX : Waves<DM, BN> {
   using V = Waves<DM, BN>;
@@ -730,8 +740,8 @@ struct GradX : Waves<DM, BN> {
   }
 };
 
-// dw = e^T x over a part of the tokens. 16384 x 32768 x 1024: 847 us (1300 TFLOP/s,
-// matrix units busy 72%: power).
+// dw = e^T x over a part of the tokens. 16384 x 32768 x 1024: 845 to 877 us by card (1255 to
+// 1300 TFLOP/s, matrix units busy 72%: power).
 template <typename T, int DM, int BV, int Halves>
 struct GradW : Waves<DM, BV> {
   using V = Waves<DM, BV>;
@@ -1204,7 +1214,12 @@ Sizes sizes_of(int64_t n, int64_t rows, int32_t dim) {
   s.rows = rows;
   s.dim = dim;
   s.dp = (int32_t)align_up((size_t)dim, kK);
-  // Tiles of 64 tokens where those of 256 would be few or mostly empty
+  // Tiles of 64 tokens where those of 256 would be few or mostly empty: of 512 tiles and
+  // more those of 256 win forward (4096 tokens, 8192 rows of 256: 35 us against 41; 2048, 32000
+  // of 512: 81 and 99) and both ways of the largest (263 and 273), below them those of 64
+  // mostly backward (512, 32000 of 256: 69 and 73; 1024, 32000 of 256: 104 and 108; of 1024
+  // columns 260 and 238). Long rows' forward alone would have those of 256 from 128 tiles on
+  // (1024, 32000 of 1024: 94 and 76 us).
   s.bn = n > kFew && cdiv(n, 256) * cdiv(rows, kV) >= 512 ? 256 : 64;
   s.dm = dim <= 64 ? 64 : (dim <= 128 ? 128 : 256);
   s.npad = (int64_t)align_up((size_t)std::max<int64_t>(n, 1), n > 128 ? 256 : 64);
@@ -1214,9 +1229,12 @@ Sizes sizes_of(int64_t n, int64_t rows, int32_t dim) {
   s.halves = n <= kFew ? 2 : 1;
   const int64_t e_rows = s.npad * s.halves;
   // Tokens that take no part cost as much as others where all keep their places, so
-  // that is for what takes little time (499 tokens, 10007 rows of 200: two launches of
-  // together 10 us become one of 6)
-  s.stay = n <= kFew || (n <= 1024 && n * rows * dim <= ((int64_t)1 << 32));
+  // that is for what takes little time. us of a call's kernels, places kept and not, all
+  // tokens taking part and half of them: forward 1000 tokens, 8000 rows of 256, 14 and 20, 14
+  // and 17; 32000 of 128 27 and 32, 27 and 22; 32000 of 512 54 and 58, 52 and 36. Backward of a
+  // distillation, 499 tokens, 10007 of 200, 43 and 47, 40 and 38; 1000, 32000 of 128 83 and 88,
+  // 76 and 60; 32000 of 512 160 and 163, 150 and 98.
+  s.stay = n <= kFew || (n <= kStayMost && n * rows * dim <= ((int64_t)1 << 32));
   s.e_bytes = e_rows <= kPieceBytes / 2 / s.vpad ? e_rows * s.vpad * 2 : std::max(kPieceBytes, e_rows * kV * 2);
   s.piece = std::min(s.vpad, std::max<int64_t>(kV, s.e_bytes / (e_rows * 2) / kV * kV));
   s.pack_bytes = std::max(std::min(s.vpad * s.dp * 2, kPackBytes), (int64_t)kV * s.dp * 2);
@@ -1403,9 +1421,6 @@ int check(const void* x, int64_t* x_stride, int64_t n, const fs_table* table, fl
   return FS_OK;
 }
 
-// lse (and the losses of labels) of the packed tokens
-constexpr int64_t kFewRows = 2048;
-
 // Tokens of a forward call that the tiles can read as they lie.
 struct Tokens {
   const char* x;  // null: packed
@@ -1419,6 +1434,7 @@ Tokens as_they_lie(const void* x, int64_t stride, const Sizes& s) {
   return can ? Tokens{(const char*)x, stride} : Tokens{};
 }
 
+// Scores of all tiles, then lse and the losses of labels.
 int forward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, float scale, const Tokens& x,
             const int64_t* labels, int64_t padding_id, int32_t* err, float* loss, float* lse,
             hipStream_t stream) {
@@ -1525,7 +1541,10 @@ int backward(const Sizes& s, const Space& o, const Table& t, int32_t dtype, floa
       x_grid = (int64_t)token_tiles * col_tiles * x_parts;
     }
     // tiles of 64 rows beside tiles of 64 tokens, and where those of 256 would leave
-    // CUs idle
+    // CUs idle (us of the call with 64 and 256: 4096 tokens, 8192 rows of 256, 121 and 125,
+    // 32768 of 512 522 and 470; 16384 tokens, 16384 of 1024 1677 and 1508. Many tokens' tiles of
+    // 256 are cut into parts and win below that too: 16384, 8192 of 1024 866 and 814, of
+    // 256 364 and 350)
     const int32_t bv = s.bn == 64 || (int64_t)table_tiles * col_tiles < kCus ? 64 : kV;
     if (g.dw) {
       const int32_t row_tiles = (int32_t)cdiv(a.rows, bv);

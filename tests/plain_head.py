@@ -8,8 +8,9 @@ import torch
 
 from plain_ops import U32, tiny, u
 
-# A row's sum in the kernels: at most 16 values of a lane, 6 exchanges inside a
-# wave, at most 16 waves, and the division by dim.
+# A row's sum in the kernels: a lane's values, 6 exchanges inside a wave, a row's waves, and
+# the division by dim. Values and waves are 32 together at most: 16 and 16 (1024 lanes of two
+# pieces of 8 or four of 4), 24 and 8 (512 lanes of three pieces of 8).
 NORM_STEPS = 16 + 6 + 16 + 2
 
 
